@@ -385,6 +385,150 @@ muon_status muon_get_bucket_stats(const muon_plan_t* plan, int64_t b, muon_bucke
  * MUON_ERR_CUDA. */
 muon_status muon_get_input_norms(const muon_plan_t* plan, float* out, int64_t n, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Before the step: the loss whose gradient it takes, and the gradient's clipping.
+ * These entry points have no counterpart on the pages (their only mention of a
+ * gradient norm is "Muon Optimizer + FSDP", section 内存控制方案 item 4, among the
+ * scalars kept in fp32); the formulas are stated at each of them.  They take no plan, only
+ * launch kernels on `stream` (capturable in a CUDA graph; the captured pointers
+ * and scalars are replayed) and accept pointers aligned to one element; rows and
+ * matrices that start on 16-byte boundaries move fastest.  Workspaces are the
+ * caller's (16-byte aligned, contents irrelevant before and after) and are free
+ * for other work on the same stream after the call.
+ * ------------------------------------------------------------------------- */
+
+/* One gradient tensor: `count` blocks of `elems` consecutive elements,
+ * `stride_elems` apart (0 means elems).  A plain tensor is {g, out, numel, 1, 0}.
+ * out: where its clipped values go, NULL or g itself for in place.  It has the
+ * layout of g, in out_dtype, and overlaps no other tensor's g or out. */
+typedef struct {
+  void* g;
+  void* out;
+  int64_t elems;
+  int64_t count;
+  int64_t stride_elems;
+  int32_t dtype;      /* MUON_DTYPE_* of g */
+  int32_t out_dtype;  /* MUON_DTYPE_* of out (in place: equal to dtype) */
+} muon_grad;
+
+/* what muon_clip_grad_norm does when the norm is not finite */
+#define MUON_NONFINITE_KEEP 0 /* factor 1: gradients keep their values, so that muon_step's
+                                 skip_nonfinite sees the matrices concerned */
+#define MUON_NONFINITE_ZERO 1 /* factor 0: every gradient is set to zero */
+
+/* Workspace of the two calls below for these n tensors (bytes).  Host work. */
+muon_status muon_clip_workspace_bytes(const muon_grad* grads, int64_t n, size_t* bytes);
+
+/* N = sqrt(sum over all tensors and elements of g^2), into *norm (device, fp32).
+ * Squares are summed in fp32 over a few dozen elements and the sums carried with
+ * their rounding errors, in a fixed order; blocks whose squares leave fp32's range
+ * are summed again in 64 bits, so N is right for every finite input whose N is a
+ * finite fp32 number.  Nothing is written but *norm.  n = 0 gives 0. */
+muon_status muon_grad_norm(const muon_grad* grads, int64_t n, float* norm, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* Clipping by the global norm: c = min(1, max_norm / (N + eps)), out = c g, each
+ * element rounded once.  result (device, 2 fp32): N and c.  c is decided on the
+ * device; in place with c = 1 nothing is written.  max_norm >= 0 (inf: never
+ * clips), eps >= 0; a sum N + eps of zero gives c = 1.
+ * nonfinite: MUON_NONFINITE_*. */
+muon_status muon_clip_grad_norm(const muon_grad* grads, int64_t n, float max_norm, float eps,
+                                int32_t nonfinite, float* result, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/* The logits of `tokens` positions and the token taken at each. */
+typedef struct {
+  const void* logits;      /* [tokens][vocab], rows row_stride elements apart */
+  const int64_t* targets;  /* [tokens], each in [0, vocab) where the mask is not 0 */
+  const uint8_t* mask;     /* [tokens], 0: the position takes no part; NULL: all do */
+  int64_t tokens;
+  int64_t vocab;           /* 1 .. 2^30 */
+  int64_t row_stride;      /* >= vocab; 0 means vocab */
+  int32_t dtype;           /* MUON_DTYPE_* of the logits and their gradient */
+  float temperature;       /* logits are divided by it; finite, > 0 */
+} muon_token_batch;
+
+/* logp[t] = z[t, y_t] - log sum_j exp(z[t, j]), z = logits / temperature (fp32,
+ * device).  A position whose mask is 0 has logp 0 and its logits and target are not
+ * read.  An unmasked target outside [0, vocab) gives NaN (here, and in the losses
+ * and the row of the gradient below).  Logits of -inf are tokens that cannot be
+ * taken. */
+muon_status muon_token_logprobs(const muon_token_batch* batch, float* logp, void* stream);
+
+/* Workspace of muon_policy_loss and muon_preference_loss (bytes).  Host work. */
+muon_status muon_loss_workspace_bytes(int64_t tokens, int64_t n_seqs, size_t* bytes);
+
+/* weights w_t of the policy loss (m_t: 1 where the mask is not 0) */
+#define MUON_REDUCE_TOKEN_MEAN 0    /* m_t / max(1, sum m) */
+#define MUON_REDUCE_SEQUENCE_MEAN 1 /* m_t / (n_seqs max(1, n_q)), n_q the sequence's sum of m;
+                                       0 for positions in no sequence */
+#define MUON_REDUCE_SUM 2           /* m_t */
+
+typedef struct {
+  float clip_low;       /* the ratio is held in [1 - clip_low, 1 + clip_high]; */
+  float clip_high;      /* 0 <= clip_low <= 1, clip_high >= 0 (inf: no upper limit) */
+  float kl_beta;        /* weight of the KL term; 0: none */
+  float grad_scale;     /* factor of the gradient (not of the loss) */
+  int32_t reduction;    /* MUON_REDUCE_* */
+  int32_t reserved[3];
+} muon_policy_config;
+
+/* (0.2, 0.2, 0, 1, MUON_REDUCE_TOKEN_MEAN). */
+void muon_policy_config_default(muon_policy_config* cfg);
+
+/* The clipped policy loss and its gradient with respect to the logits:
+ *   r = exp(logp - old_logp),  s = min(r A, clip(r, 1 - clip_low, 1 + clip_high) A),
+ *   k = exp(ref_logp - logp) - (ref_logp - logp) - 1,
+ *   L = sum_t w_t (-s + kl_beta k),
+ *   dL/dlogp = w (-A r where the unclipped product is the minimum, else 0,
+ *                 + kl_beta (1 - exp(ref_logp - logp))),
+ *   grad[t, j] = grad_scale dL/dlogp_t / temperature (1[j = y_t] - softmax(z_t)_j).
+ *   old_logp, advantages: [tokens] fp32, read where the mask is not 0.
+ *   ref_logp: the same; NULL only with kl_beta = 0, and not read then.
+ *   seq_offsets: [n_seqs + 1] device offsets into the positions, ascending; needed
+ *     by MUON_REDUCE_SEQUENCE_MEAN only (else may be NULL).
+ *   stats: 4 fp32 (device): L, sum w (-s), sum w k, sum w [clipped].
+ *   logp: [tokens] fp32 (device), or NULL.
+ *   grad: [tokens][vocab] in the logits' type, rows grad_stride elements apart
+ *     (0 means vocab), written whole (masked rows are zero); may be the logits
+ *     themselves (same stride).  NULL: the loss only. */
+muon_status muon_policy_loss(const muon_token_batch* batch, const muon_policy_config* cfg,
+                             const float* old_logp, const float* ref_logp, const float* advantages,
+                             const int64_t* seq_offsets, int64_t n_seqs, float* stats, float* logp,
+                             void* grad, int64_t grad_stride, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+typedef struct {
+  float beta;               /* > 0 */
+  float label_smoothing;    /* e in [0, 1] */
+  float grad_scale;         /* factor of the gradient (not of the loss) */
+  int32_t length_normalize; /* 1: S is the mean over the sequence's unmasked positions */
+  int32_t reserved[4];
+} muon_preference_config;
+
+/* (0.1, 0, 1, 0). */
+void muon_preference_config_default(muon_preference_config* cfg);
+
+/* The preference loss over n_pairs pairs of sequences, and its gradient with
+ * respect to the logits.  Sequence q holds the positions seq_offsets[q] ..
+ * seq_offsets[q + 1]; the preferred answer of pair i is sequence i, the other one
+ * sequence n_pairs + i.
+ *   S_q = sum of logp over the sequence's unmasked positions (0 if there are none),
+ *   h_i = beta ((S_i - R_i) - (S_{P+i} - R_{P+i})),
+ *   L = (1/P) sum_i (-(1 - e) log sigmoid(h_i) - e log sigmoid(-h_i)),
+ *   grad[t, j] = grad_scale dL/dlogp_t / temperature (1[j = y_t] - softmax(z_t)_j).
+ *   ref_logp: [2 n_pairs] fp32, R (formed like S, by the reference policy).
+ *   seq_offsets: [2 n_pairs + 1] device, ascending from 0; positions in no sequence
+ *     take no part in the loss.
+ *   loss: 1 fp32; margins: [n_pairs] fp32, h; seq_logp: [2 n_pairs] fp32, S
+ *     (device); margins and seq_logp may be NULL.
+ *   grad, grad_stride: as in muon_policy_loss.  n_pairs = 0 gives loss 0. */
+muon_status muon_preference_loss(const muon_token_batch* batch, const muon_preference_config* cfg,
+                                 const float* ref_logp, const int64_t* seq_offsets, int64_t n_pairs,
+                                 float* loss, float* margins, float* seq_logp, void* grad,
+                                 int64_t grad_stride, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
 /* Text of the last error reported by an entry point on the calling thread
  * (empty string if none).  Valid until that thread's next call. */
 const char* muon_last_error(void);

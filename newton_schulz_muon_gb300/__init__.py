@@ -40,6 +40,11 @@ MUON_NS_KERNEL_GEMM = 1
 MUON_NS_METHOD_STANDARD = 0
 MUON_NS_METHOD_GRAM = 1
 MUON_MAX_NS_STEPS = 16
+MUON_NONFINITE_KEEP = 0
+MUON_NONFINITE_ZERO = 1
+MUON_REDUCE_TOKEN_MEAN = 0
+MUON_REDUCE_SEQUENCE_MEAN = 1
+MUON_REDUCE_SUM = 2
 
 
 class muon_shape(ctypes.Structure):
@@ -80,6 +85,26 @@ class muon_stats(ctypes.Structure):
                 ("h2d_bytes", c_int64), ("d2h_bytes", c_int64), ("n_buckets", c_int64)]
 
 
+class muon_grad(ctypes.Structure):
+    _fields_ = [("g", c_void_p), ("out", c_void_p), ("elems", c_int64), ("count", c_int64),
+                ("stride_elems", c_int64), ("dtype", c_int32), ("out_dtype", c_int32)]
+
+
+class muon_token_batch(ctypes.Structure):
+    _fields_ = [("logits", c_void_p), ("targets", c_void_p), ("mask", c_void_p), ("tokens", c_int64),
+                ("vocab", c_int64), ("row_stride", c_int64), ("dtype", c_int32), ("temperature", c_float)]
+
+
+class muon_policy_config(ctypes.Structure):
+    _fields_ = [("clip_low", c_float), ("clip_high", c_float), ("kl_beta", c_float), ("grad_scale", c_float),
+                ("reduction", c_int32), ("reserved", c_int32 * 3)]
+
+
+class muon_preference_config(ctypes.Structure):
+    _fields_ = [("beta", c_float), ("label_smoothing", c_float), ("grad_scale", c_float),
+                ("length_normalize", c_int32), ("reserved", c_int32 * 4)]
+
+
 def _load(path: str = LIB_PATH) -> ctypes.CDLL:
     if not os.path.exists(path):
         raise ImportError(f"{os.path.basename(path)} not found at {path}; run __graft_entry__.build() "
@@ -113,6 +138,17 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
         "muon_inject_copy_failure": (c_int32, [P, c_int64]),
         "muon_get_bucket_stats": (c_int32, [P, c_int64, POINTER(muon_bucket_stats)]),
         "muon_get_input_norms": (c_int32, [P, POINTER(c_float), c_int64, P]),
+        "muon_clip_workspace_bytes": (c_int32, [P, c_int64, POINTER(c_size_t)]),
+        "muon_grad_norm": (c_int32, [P, c_int64, P, P, c_size_t, P]),
+        "muon_clip_grad_norm": (c_int32, [P, c_int64, c_float, c_float, c_int32, P, P, c_size_t, P]),
+        "muon_token_logprobs": (c_int32, [POINTER(muon_token_batch), P, P]),
+        "muon_loss_workspace_bytes": (c_int32, [c_int64, c_int64, POINTER(c_size_t)]),
+        "muon_policy_config_default": (None, [POINTER(muon_policy_config)]),
+        "muon_policy_loss": (c_int32, [POINTER(muon_token_batch), POINTER(muon_policy_config), P, P, P, P, c_int64,
+                                       P, P, P, c_int64, P, c_size_t, P]),
+        "muon_preference_config_default": (None, [POINTER(muon_preference_config)]),
+        "muon_preference_loss": (c_int32, [POINTER(muon_token_batch), POINTER(muon_preference_config), P, P, c_int64,
+                                           P, P, P, P, c_int64, P, c_size_t, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -354,3 +390,275 @@ def allocate_workspace(plan: Plan, device=None):
     ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device or "cuda")
     muon_plan_bind_workspace(plan, ws)
     return ws
+
+
+# ---------------------------------------------------------------------------
+# losses on token log-probabilities, and clipping by the global gradient norm
+# ---------------------------------------------------------------------------
+def _on_stream(stream):
+    """(context for the tensors a call allocates, cudaStream_t) of a call on `stream`: the
+    allocator hands their memory out again in the order of the stream that uses it."""
+    import contextlib
+    import torch
+    if stream is None:
+        return contextlib.nullcontext(), torch.cuda.current_stream().cuda_stream
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)))
+    return torch.cuda.stream(stream), stream.cuda_stream
+
+
+def _dtype_code(dtype) -> int:
+    import torch
+    code = {torch.float32: MUON_DTYPE_F32, torch.bfloat16: MUON_DTYPE_BF16}.get(dtype)
+    if code is None:
+        raise TypeError(f"expected a float32 or bfloat16 tensor, got {dtype}")
+    return code
+
+
+def _blocks(t):
+    """(elements, count, stride) of a tensor whose memory is `count` equal blocks a stride
+    apart, each dense in some order of its dimensions; ValueError otherwise."""
+    if t.is_contiguous():
+        return t.numel(), 1, 0
+    if t.numel() == 0:
+        return 0, 0, 0
+    elems, outer = 1, None
+    for stride, size in sorted(d for d in zip(t.stride(), t.shape) if d[1] != 1):
+        if outer is None and stride == elems:
+            elems *= size
+        elif outer is None and stride > elems:
+            outer = (size, stride)
+        elif outer is not None and stride == outer[0] * outer[1]:
+            outer = (outer[0] * size, outer[1])
+        else:
+            raise ValueError(f"gradient of shape {tuple(t.shape)} and strides {t.stride()} is not equal dense blocks "
+                             "a stride apart")
+    return (elems, 1, 0) if outer is None else (elems, outer[0], outer[1])
+
+
+class GradSet:
+    """Gradient tensors (and where their clipped values go) as the library takes them.  A
+    program whose gradients stay in place makes one and passes it to every call."""
+
+    def __init__(self, grads, out=None):
+        grads = list(grads)
+        self.tensors = grads
+        self.out = grads if out is None else list(out)
+        if len(self.out) != len(grads):
+            raise ValueError(f"{len(grads)} gradients, but {len(self.out)} outputs")
+        n = len(grads)
+        self.array = (muon_grad * max(n, 1))()
+        for i, (g, o) in enumerate(zip(grads, self.out)):
+            if not g.is_cuda or not o.is_cuda:
+                raise ValueError(f"gradient {i}: not a CUDA tensor")
+            elems, count, stride = _blocks(g)
+            if o is not g and (o.shape != g.shape or (o.stride() != g.stride() and g.numel() > 1)):
+                raise ValueError(f"gradient {i}: out has another shape or layout")
+            code = _dtype_code(g.dtype)
+            self.array[i] = (g.data_ptr(), o.data_ptr(), elems, count, stride, code,
+                             code if o is g else _dtype_code(o.dtype))
+
+    def __len__(self):
+        return len(self.tensors)
+
+
+def muon_clip_workspace_bytes(grads) -> int:
+    grads = grads if isinstance(grads, GradSet) else GradSet(grads)
+    v = c_size_t()
+    _check(_lib().muon_clip_workspace_bytes(grads.array, len(grads), byref(v)), "muon_clip_workspace_bytes")
+    return v.value
+
+
+def _vector(t, n, dtype, what, optional=False):
+    """Device pointer of a contiguous CUDA tensor of n elements of `dtype`; 0 for None."""
+    if t is None:
+        if optional:
+            return 0
+        raise ValueError(f"{what} is needed")
+    if t.dtype != dtype or t.numel() != n or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous CUDA tensor of {n} {dtype} values, got shape "
+                         f"{tuple(t.shape)}, strides {t.stride()}, {t.dtype} on {t.device}")
+    return t.data_ptr()
+
+
+def _space(workspace, nbytes):
+    import torch
+    if workspace is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace: expected a contiguous CUDA tensor")
+    return workspace
+
+
+def muon_grad_norm(grads, norm=None, workspace=None, stream=None):
+    """The global L2 norm of the gradients (a list of tensors or a GradSet), as a
+    one-element fp32 device tensor."""
+    import torch
+    grads = grads if isinstance(grads, GradSet) else GradSet(grads)
+    nbytes = muon_clip_workspace_bytes(grads)
+    context, handle = _on_stream(stream)
+    with context:
+        workspace = _space(workspace, nbytes)
+        if norm is None:
+            norm = torch.empty(1, dtype=torch.float32, device="cuda")
+    _check(_lib().muon_grad_norm(grads.array, len(grads), _vector(norm, 1, torch.float32, "norm"),
+                                 workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle),
+           "muon_grad_norm")
+    return norm
+
+
+def muon_clip_grad_norm(grads, max_norm: float, out=None, eps: float = 1e-6,
+                        nonfinite: int = MUON_NONFINITE_KEEP, result=None, workspace=None, stream=None):
+    """Scales the gradients (a list of tensors or a GradSet) by min(1, max_norm / (norm + eps)),
+    in place or into `out` (a list of tensors of the same layouts, bf16 or fp32).  Returns
+    a two-element fp32 device tensor: the norm and the factor."""
+    import torch
+    if not isinstance(grads, GradSet):
+        grads = GradSet(grads, out)
+    elif out is not None:
+        raise ValueError("a GradSet has its outputs already")
+    nbytes = muon_clip_workspace_bytes(grads)
+    context, handle = _on_stream(stream)
+    with context:
+        workspace = _space(workspace, nbytes)
+        if result is None:
+            result = torch.empty(2, dtype=torch.float32, device="cuda")
+    _check(_lib().muon_clip_grad_norm(grads.array, len(grads), float(max_norm), float(eps), int(nonfinite),
+                                      _vector(result, 2, torch.float32, "result"), workspace.data_ptr(),
+                                      workspace.numel() * workspace.element_size(), handle),
+           "muon_clip_grad_norm")
+    return result
+
+
+def _token_batch(logits, targets, mask, temperature):
+    import torch
+    if logits.dim() != 2 or not logits.is_cuda:
+        raise ValueError(f"logits: expected a CUDA matrix [tokens, vocab], got shape {tuple(logits.shape)} on "
+                         f"{logits.device}")
+    tokens, vocab = logits.shape
+    stride = logits.stride(0)
+    if (vocab > 1 and logits.stride(1) != 1) or (tokens > 1 and stride < vocab):
+        raise ValueError(f"logits: rows must be contiguous and not overlap, got strides {logits.stride()}")
+    if mask is not None and mask.dtype not in (torch.bool, torch.uint8):
+        raise ValueError(f"mask: expected bool or uint8, got {mask.dtype}")
+    return muon_token_batch(logits.data_ptr(), _vector(targets, tokens, torch.int64, "targets"),
+                            None if mask is None else _vector(mask, tokens, mask.dtype, "mask"), tokens, vocab,
+                            stride if tokens > 1 else vocab, _dtype_code(logits.dtype), temperature)
+
+
+def _grad_like(logits, grad, with_grad, batch):
+    """(gradient tensor or None, row stride): by default with the logits' row stride, so
+    that both start on the same boundaries, unless that would waste memory."""
+    import torch
+    if grad is None:
+        if not with_grad:
+            return None, 0
+        tokens, vocab = logits.shape
+        stride = batch.row_stride if batch.row_stride <= vocab + vocab // 8 else vocab
+        return torch.empty_strided((tokens, vocab), (stride, 1), dtype=logits.dtype, device=logits.device), stride
+    if grad.shape != logits.shape or grad.dtype != logits.dtype or not grad.is_cuda:
+        raise ValueError(f"grad: expected a CUDA tensor like the logits, got shape {tuple(grad.shape)}, {grad.dtype}")
+    tokens, vocab = grad.shape
+    if (vocab > 1 and grad.stride(1) != 1) or (tokens > 1 and grad.stride(0) < vocab):
+        raise ValueError(f"grad: rows must be contiguous and not overlap, got strides {grad.stride()}")
+    return grad, grad.stride(0) if tokens > 1 else (batch.row_stride if grad is logits else vocab)
+
+
+def muon_token_logprobs(logits, targets, mask=None, temperature: float = 1.0, logp=None, stream=None):
+    """log softmax(logits / temperature) at each position's target, fp32; 0 where the mask
+    is False.  logits: [tokens, vocab], targets: [tokens] int64, mask: [tokens] bool."""
+    import torch
+    batch = _token_batch(logits, targets, mask, temperature)
+    context, handle = _on_stream(stream)
+    if logp is None:
+        with context:
+            logp = torch.empty(batch.tokens, dtype=torch.float32, device=logits.device)
+    _check(_lib().muon_token_logprobs(byref(batch), _vector(logp, batch.tokens, torch.float32, "logp"), handle),
+           "muon_token_logprobs")
+    return logp
+
+
+def muon_loss_workspace_bytes(tokens: int, n_seqs: int) -> int:
+    v = c_size_t()
+    _check(_lib().muon_loss_workspace_bytes(int(tokens), int(n_seqs), byref(v)), "muon_loss_workspace_bytes")
+    return v.value
+
+
+def _default_config(cls, default, overrides):
+    cfg = cls()
+    default(byref(cfg))
+    for k, v in overrides.items():
+        if not hasattr(cfg, k):
+            raise AttributeError(f"{cls.__name__} has no field {k!r}")
+        setattr(cfg, k, v)
+    return cfg
+
+
+def muon_policy_config_default(**overrides) -> muon_policy_config:
+    return _default_config(muon_policy_config, _lib().muon_policy_config_default, overrides)
+
+
+def muon_preference_config_default(**overrides) -> muon_preference_config:
+    return _default_config(muon_preference_config, _lib().muon_preference_config_default, overrides)
+
+
+def muon_policy_loss(logits, targets, old_logp, advantages, mask=None, ref_logp=None, seq_offsets=None,
+                     temperature: float = 1.0, config: Optional[muon_policy_config] = None, grad=None, logp=None,
+                     stats=None, with_grad: bool = True, workspace=None, stream=None):
+    """The clipped policy loss with a KL term, and its gradient with respect to the logits.
+
+    Returns (stats, logp, grad): stats holds the loss, the policy term, the KL term and the
+    clipped share (fp32, on the device); grad is None with with_grad=False.  seq_offsets:
+    [n_seqs + 1] int64, for the sequence mean.  grad may be the logits themselves."""
+    import torch
+    batch = _token_batch(logits, targets, mask, temperature)
+    tokens = batch.tokens
+    n_seqs = 0 if seq_offsets is None else max(seq_offsets.numel() - 1, 0)
+    nbytes = muon_loss_workspace_bytes(tokens, n_seqs)
+    context, handle = _on_stream(stream)
+    with context:
+        workspace = _space(workspace, nbytes)
+        grad, grad_stride = _grad_like(logits, grad, with_grad, batch)
+        if logp is None:
+            logp = torch.empty(tokens, dtype=torch.float32, device=logits.device)
+        if stats is None:
+            stats = torch.empty(4, dtype=torch.float32, device=logits.device)
+    f32 = torch.float32
+    _check(_lib().muon_policy_loss(
+        byref(batch), byref(config) if config is not None else None, _vector(old_logp, tokens, f32, "old_logp"),
+        _vector(ref_logp, tokens, f32, "ref_logp", True), _vector(advantages, tokens, f32, "advantages"),
+        0 if seq_offsets is None else _vector(seq_offsets, n_seqs + 1, torch.int64, "seq_offsets"), n_seqs,
+        _vector(stats, 4, f32, "stats"), _vector(logp, tokens, f32, "logp"), 0 if grad is None else grad.data_ptr(),
+        grad_stride, workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle),
+        "muon_policy_loss")
+    return stats, logp, grad
+
+
+def muon_preference_loss(logits, targets, seq_offsets, ref_logp, mask=None, temperature: float = 1.0,
+                         config: Optional[muon_preference_config] = None, grad=None, loss=None, margins=None,
+                         seq_logp=None, with_grad: bool = True, workspace=None, stream=None):
+    """The preference loss over pairs of sequences, and its gradient with respect to the logits.
+
+    seq_offsets: [2 P + 1] int64: the P preferred answers, then the P others.  ref_logp:
+    [2 P] fp32, the reference policy's sums.  Returns (loss, margins, seq_logp, grad)."""
+    import torch
+    batch = _token_batch(logits, targets, mask, temperature)
+    n_seqs = seq_offsets.numel() - 1
+    if n_seqs < 0 or n_seqs % 2:
+        raise ValueError(f"seq_offsets: expected 2 P + 1 offsets, got {seq_offsets.numel()}")
+    nbytes = muon_loss_workspace_bytes(batch.tokens, n_seqs)
+    context, handle = _on_stream(stream)
+    f32, device = torch.float32, logits.device
+    with context:
+        workspace = _space(workspace, nbytes)
+        grad, grad_stride = _grad_like(logits, grad, with_grad, batch)
+        loss = torch.empty(1, dtype=f32, device=device) if loss is None else loss
+        margins = torch.empty(n_seqs // 2, dtype=f32, device=device) if margins is None else margins
+        seq_logp = torch.empty(n_seqs, dtype=f32, device=device) if seq_logp is None else seq_logp
+    _check(_lib().muon_preference_loss(
+        byref(batch), byref(config) if config is not None else None, _vector(ref_logp, n_seqs, f32, "ref_logp"),
+        _vector(seq_offsets, n_seqs + 1, torch.int64, "seq_offsets"), n_seqs // 2, _vector(loss, 1, f32, "loss"),
+        _vector(margins, n_seqs // 2, f32, "margins"), _vector(seq_logp, n_seqs, f32, "seq_logp"),
+        0 if grad is None else grad.data_ptr(), grad_stride, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), handle), "muon_preference_loss")
+    return loss, margins, seq_logp, grad

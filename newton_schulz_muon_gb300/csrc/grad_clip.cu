@@ -1,0 +1,518 @@
+// Global gradient norm over many tensors, and clipping by it.
+//
+//   N = sqrt(sum g^2),  c = min(1, max_norm / (N + eps)),  out = c g
+//
+// Two passes, bound by HBM: every element is read once for N; where something has to
+// be written it is read again (in the reverse order, so that what the first pass left
+// in L2 is met first), scaled and written.  The tensor table travels as a kernel
+// parameter, so a call copies nothing to the device and waits for nothing on the host.
+//
+// The unit of work is a chunk of kChunk elements of one tensor, taken by one warp: a
+// set of a thousand small tensors spreads over the GPU like one large tensor does.
+// A warp's chunks are warp, warp + warps, ...: every partial sum has a fixed place and
+// order, so that a call gives the same bits each time.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <cmath>
+
+#include "device.cuh"
+#include "kernels.h"
+#include "epilogue.cuh"
+#include "launch.cuh"
+#include "momentum.cuh"
+#include "muon.h"
+
+namespace muon {
+namespace {
+
+constexpr int kChunk = 2048;       // elements of one warp's unit of work: 8 octets a lane
+constexpr int kClipThreads = 256;
+constexpr int kClipWarps = kClipThreads / 32;
+constexpr int kClipCtasPerSm = 4;
+constexpr int kClipMaxCtas = 1024; // partial sums of one launch
+
+struct ClipSeg {
+  const void* g;
+  void* out;
+  int64_t elems, stride;
+  int32_t chunk0;          // first chunk of the tensor in its launch
+  int32_t chunks_per_mat;  // chunks of one of its blocks
+  int32_t g_bf16, out_bf16;
+};
+
+// A launch takes up to Cap tensors.  64 keeps the parameters of the usual call at
+// 3 KB; 640 (30 KB, of the 32,764 bytes a kernel may have) serves sets of many tensors.
+template <int Cap>
+struct ClipArgs {
+  ClipSeg seg[Cap];
+  int32_t n_segs, n_chunks;
+  double* partials;        // of the whole call
+  int32_t partial0;        // this launch's first partial sum (norm)
+  int32_t n_partials;      // all of them (clip)
+  float max_norm, eps;
+  int32_t nonfinite;
+  float* result;
+};
+
+// A block's chunk: its address, length and the elements before the first 16-byte boundary.
+struct Chunk {
+  const ClipSeg* seg;
+  int64_t at;     // element offset of the block from seg->g and seg->out
+  int64_t begin;  // elements [begin, end) of the block
+  int64_t end;
+  int head;       // the block's elements before its first aligned octet
+};
+
+template <int Cap>
+__device__ __forceinline__ Chunk find_chunk(const ClipArgs<Cap>& a, int c, int& cur) {
+  const int next = cur + 1 < a.n_segs ? a.seg[cur + 1].chunk0 : a.n_chunks;
+  if (c < a.seg[cur].chunk0 || c >= next) {
+    int lo = 0, hi = a.n_segs - 1;
+    while (lo < hi) {  // last tensor with chunk0 <= c
+      const int mid = (lo + hi + 1) >> 1;
+      if (a.seg[mid].chunk0 <= c) lo = mid; else hi = mid - 1;
+    }
+    cur = lo;
+  }
+  const ClipSeg& s = a.seg[cur];
+  const int local = c - s.chunk0;
+  const int mat = local / s.chunks_per_mat;
+  const int64_t j = local - mat * s.chunks_per_mat;
+  Chunk k;
+  k.seg = &s;
+  k.at = mat * s.stride;
+  const int es = s.g_bf16 ? 2 : 4;
+  const uint64_t addr = reinterpret_cast<uint64_t>(s.g) + (uint64_t)k.at * es;
+  k.head = (int)(((16 - (addr & 15)) & 15) / es);
+  if (k.head > s.elems) k.head = (int)s.elems;
+  // chunk 0 takes the head too, so that the others start on a boundary
+  k.begin = j == 0 ? 0 : min(s.elems, k.head + j * kChunk);
+  k.end = min(s.elems, k.head + (j + 1) * kChunk);
+  return k;
+}
+
+__device__ __forceinline__ void unpack8(const uint4& w, float (&v)[8]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(u[i] << 16);
+    v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+  }
+}
+
+// Sum of squares of a lane's part of a chunk in fp32, and the OR of its bits without signs.
+struct Part {
+  float s;
+  uint32_t bits;
+};
+
+__device__ __forceinline__ void add_octet_bf16(const uint4& w, float& s0, float& s1, uint32_t& bits) {
+  float v[8];
+  unpack8(w, v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    s0 = __fmaf_rn(v[2 * i], v[2 * i], s0);
+    s1 = __fmaf_rn(v[2 * i + 1], v[2 * i + 1], s1);
+  }
+  bits |= (w.x | w.y | w.z | w.w) & 0x7FFF7FFFu;
+}
+
+__device__ __forceinline__ void add_quad_f32(const float4& w, float& s0, float& s1, uint32_t& bits) {
+  s0 = __fmaf_rn(w.x, w.x, s0);
+  s1 = __fmaf_rn(w.y, w.y, s1);
+  s0 = __fmaf_rn(w.z, w.z, s0);
+  s1 = __fmaf_rn(w.w, w.w, s1);
+  bits |= (__float_as_uint(w.x) | __float_as_uint(w.y) | __float_as_uint(w.z) | __float_as_uint(w.w)) & 0x7FFFFFFFu;
+}
+
+__device__ __forceinline__ float load_elem(const void* p, int64_t i, int bf16) {
+  return bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[i]) : reinterpret_cast<const float*>(p)[i];
+}
+
+__device__ __forceinline__ Part chunk_squares(const Chunk& k, int lane) {
+  float s0 = 0.f, s1 = 0.f;
+  uint32_t bits = 0;
+  const int64_t vec0 = k.begin == 0 ? k.head : k.begin;  // aligned
+  const int n8 = (int)((k.end - vec0) >> 3);
+  const int bf16 = k.seg->g_bf16;
+  if (bf16) {
+    const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(k.seg->g) + k.at + vec0);
+    if (n8 == kChunk / 8) {
+      uint4 w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = p[i * 32 + lane];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) add_octet_bf16(w[i], s0, s1, bits);
+    } else {
+      for (int i = lane; i < n8; i += 32) add_octet_bf16(p[i], s0, s1, bits);
+    }
+  } else {
+    const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(k.seg->g) + k.at + vec0);
+    if (n8 == kChunk / 8) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float4 w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = p[h * 256 + i * 32 + lane];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) add_quad_f32(w[i], s0, s1, bits);
+      }
+    } else {
+      for (int i = lane; i < 2 * n8; i += 32) add_quad_f32(p[i], s0, s1, bits);
+    }
+  }
+  // the elements before the first boundary and after the last whole octet, < 8 each
+  const int64_t tail = vec0 + 8ll * n8;
+  int64_t i = -1;
+  if (lane < 8) {
+    if (k.begin == 0 && lane < k.head) i = lane;
+  } else if (lane < 16 && tail + (lane - 8) < k.end) {
+    i = tail + (lane - 8);
+  }
+  if (i >= 0) {
+    const float x = load_elem(k.seg->g, k.at + i, bf16);
+    s0 = __fmaf_rn(x, x, s0);
+    bits |= __float_as_uint(x) & 0x7FFFFFFFu;
+  }
+  return Part{s0 + s1, bits};
+}
+
+// The same in 64 bits, for a chunk whose squares fp32 cannot hold.
+__device__ __noinline__ double chunk_squares_wide(const Chunk& k, int lane) {
+  double s = 0.0;
+  for (int64_t i = k.begin + lane; i < k.end; i += 32) {
+    const double x = (double)load_elem(k.seg->g, k.at + i, k.seg->g_bf16);
+    s = fma(x, x, s);
+  }
+  return s;
+}
+
+// A lane adds at most 2 * kChunk / 32 + 1 squares in fp32 (relative error below 130
+// units of 2^-24 at the very worst, a few in practice), then carries the sum of its
+// chunks as an unevaluated pair.  A chunk whose lane sums leave [2^-116, 2^90], where
+// squares overflow or lose bits to underflow, is summed again in 64 bits; an all-zero
+// one is not.
+template <int Cap>
+__global__ void __launch_bounds__(kClipThreads) clip_norm_kernel(const __grid_constant__ ClipArgs<Cap> a) {
+  __shared__ double red[kClipWarps];
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int warps = gridDim.x * kClipWarps;
+  float hi = 0.f, lo = 0.f;
+  double wide = 0.0;
+  int cur = 0;
+  for (int c = blockIdx.x * kClipWarps + warp; c < a.n_chunks; c += warps) {
+    const Chunk k = find_chunk(a, c, cur);
+    const Part p = chunk_squares(k, lane);
+    const bool fits = p.s <= 0x1p90f && (p.s >= 0x1p-116f || p.bits == 0);
+    if (__all_sync(0xFFFFFFFFu, fits)) {
+      float s, e;
+      two_sum(hi, p.s, s, e);
+      hi = s;
+      lo += e;
+    } else {
+      wide += chunk_squares_wide(k, lane);
+    }
+  }
+  double sum = (double)hi + (double)lo + wide;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  if (lane == 0) red[warp] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double t = red[0];
+#pragma unroll
+    for (int w = 1; w < kClipWarps; ++w) t += red[w];
+    a.partials[a.partial0 + blockIdx.x] = t;
+  }
+}
+
+// The call's sum of squares, in the same order in every CTA.
+__device__ __forceinline__ double total_of(const double* partials, int n) {
+  __shared__ double red[kClipWarps];
+  double t = 0.0;
+  for (int i = threadIdx.x; i < n; i += kClipThreads) t += __ldcg(partials + i);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = t;
+  __syncthreads();
+  t = red[0];
+#pragma unroll
+  for (int w = 1; w < kClipWarps; ++w) t += red[w];
+  return t;
+}
+
+__global__ void __launch_bounds__(kClipThreads) norm_result_kernel(const double* partials, int n, float* norm) {
+  griddep_wait();
+  const double t = total_of(partials, n);
+  if (threadIdx.x == 0) *norm = (float)sqrt(t);
+}
+
+__device__ __forceinline__ void scale8(const float (&v)[8], float c, float (&r)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = c * v[i];
+}
+
+__device__ __forceinline__ void store8(void* out, int64_t i, int bf16, const float (&r)[8]) {
+  if (bf16) {
+    *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(out) + i) =
+        make_uint4(pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3]), pack_bf16x2(r[4], r[5]), pack_bf16x2(r[6], r[7]));
+  } else {
+    float4* p = reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + i);
+    p[0] = make_float4(r[0], r[1], r[2], r[3]);
+    p[1] = make_float4(r[4], r[5], r[6], r[7]);
+  }
+}
+
+__device__ __forceinline__ void load8(const void* g, int64_t i, int bf16, float (&v)[8]) {
+  if (bf16) {
+    unpack8(__ldcs(reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(g) + i)), v);
+  } else {
+    const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(g) + i);
+    const float4 x = __ldcs(p), y = __ldcs(p + 1);
+    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+    v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+  }
+}
+
+__device__ __forceinline__ void scale_elem(const Chunk& k, int64_t i, float c, bool zero) {
+  const float r = zero ? 0.f : c * load_elem(k.seg->g, k.at + i, k.seg->g_bf16);
+  if (k.seg->out_bf16) reinterpret_cast<__nv_bfloat16*>(k.seg->out)[k.at + i] = __float2bfloat16_rn(r);
+  else reinterpret_cast<float*>(k.seg->out)[k.at + i] = r;
+}
+
+template <int Cap>
+__global__ void __launch_bounds__(kClipThreads) clip_scale_kernel(const __grid_constant__ ClipArgs<Cap> a) {
+  griddep_wait();
+  const double sumsq = total_of(a.partials, a.n_partials);
+  const double norm = sqrt(sumsq);
+  float c = 1.f;
+  if (!isfinite(sumsq)) {
+    c = a.nonfinite == MUON_NONFINITE_ZERO ? 0.f : 1.f;
+  } else {
+    const double den = norm + (double)a.eps;
+    if (den > (double)a.max_norm) c = (float)((double)a.max_norm / den);
+  }
+  const bool zero = !isfinite(sumsq) && c == 0.f;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    a.result[0] = (float)norm;
+    a.result[1] = c;
+  }
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int warps = gridDim.x * kClipWarps;
+  int cur = a.n_segs - 1;
+  for (int r = blockIdx.x * kClipWarps + warp; r < a.n_chunks; r += warps) {
+    const Chunk k = find_chunk(a, a.n_chunks - 1 - r, cur);
+    const ClipSeg& s = *k.seg;
+    if (c == 1.f && s.out == s.g) continue;
+    const int64_t vec0 = k.begin == 0 ? k.head : k.begin;
+    const int os = s.out_bf16 ? 2 : 4;
+    if (((reinterpret_cast<uint64_t>(s.out) + (uint64_t)(k.at + vec0) * os) & 15) != 0) {
+      // out is not aligned where g is: element by element
+      for (int64_t i = k.begin + lane; i < k.end; i += 32) scale_elem(k, i, c, zero);
+      continue;
+    }
+    const int n8 = (int)((k.end - vec0) >> 3);
+    for (int i = lane; i < n8; i += 32) {
+      float v[8], w[8];
+      load8(s.g, k.at + vec0 + 8ll * i, s.g_bf16, v);
+      scale8(v, c, w);
+      if (zero) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = 0.f;
+      }
+      store8(s.out, k.at + vec0 + 8ll * i, s.out_bf16, w);
+    }
+    const int64_t tail = vec0 + 8ll * n8;
+    if (lane < 8) {
+      if (k.begin == 0 && lane < k.head) scale_elem(k, lane, c, zero);
+    } else if (lane < 16 && tail + (lane - 8) < k.end) {
+      scale_elem(k, tail + (lane - 8), c, zero);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+constexpr int kCapSmall = 64, kCapLarge = 640;
+
+int64_t elem_size(int32_t dtype) { return dtype == MUON_DTYPE_BF16 ? 2 : 4; }
+
+int64_t chunks_per_mat(const muon_grad& t) { return (t.elems + kChunk - 1) / kChunk; }
+
+const char* check_grad(const muon_grad& t) {
+  if (t.elems < 0 || t.count < 0) return "gradient: elems and count must be >= 0";
+  if (t.elems > (1ll << 40) || t.count > (1ll << 31) - 1) return "gradient: too many elements";
+  if (t.stride_elems != 0 && (t.stride_elems < t.elems || t.stride_elems > (1ll << 40)))
+    return "gradient: stride_elems must be 0 or at least elems";
+  if (t.dtype != MUON_DTYPE_F32 && t.dtype != MUON_DTYPE_BF16) return "gradient: unknown dtype";
+  if (t.elems == 0 || t.count == 0) return nullptr;
+  if ((double)chunks_per_mat(t) * (double)t.count > 2e9) return "gradient: too many elements";
+  if (!t.g) return "gradient pointer is NULL";
+  if (reinterpret_cast<uint64_t>(t.g) % elem_size(t.dtype)) return "gradient pointer is not aligned to its type";
+  return nullptr;
+}
+
+const char* check_out(const muon_grad& t) {
+  if (t.elems == 0 || t.count == 0) return nullptr;
+  if (!t.out || t.out == t.g) {
+    if (t.out_dtype != t.dtype) return "gradient in place: out_dtype must be dtype";
+    return nullptr;
+  }
+  if (t.out_dtype != MUON_DTYPE_F32 && t.out_dtype != MUON_DTYPE_BF16) return "gradient: unknown out_dtype";
+  if (reinterpret_cast<uint64_t>(t.out) % elem_size(t.out_dtype)) return "out pointer is not aligned to its type";
+  return nullptr;
+}
+
+// Launches of at most Cap tensors and 2^31 chunks cover the call's tensors in order.
+// The callback fills and launches one; `i` is left at the first tensor not taken.
+template <int Cap>
+void fill_args(const muon_grad* grads, int64_t n, int64_t& i, ClipArgs<Cap>& a) {
+  int64_t chunks = 0;
+  a.n_segs = 0;
+  for (; i < n && a.n_segs < Cap; ++i) {
+    const muon_grad& t = grads[i];
+    if (t.elems == 0 || t.count == 0) continue;
+    const int64_t cpm = chunks_per_mat(t), all = cpm * t.count;
+    if (chunks + all > 2000000000ll) break;
+    ClipSeg& s = a.seg[a.n_segs++];
+    s.g = t.g;
+    s.out = t.out ? t.out : t.g;
+    s.elems = t.elems;
+    s.stride = t.stride_elems ? t.stride_elems : t.elems;
+    s.chunk0 = (int32_t)chunks;
+    s.chunks_per_mat = (int32_t)cpm;
+    s.g_bf16 = t.dtype == MUON_DTYPE_BF16;
+    s.out_bf16 = t.out && t.out != t.g ? t.out_dtype == MUON_DTYPE_BF16 : s.g_bf16;
+    chunks += all;
+  }
+  a.n_chunks = (int32_t)chunks;
+}
+
+int grid_for(int32_t n_chunks, int sms) {
+  int64_t ctas = ((int64_t)n_chunks + kClipWarps - 1) / kClipWarps;
+  const int64_t most = sms * kClipCtasPerSm < kClipMaxCtas ? sms * kClipCtasPerSm : kClipMaxCtas;
+  return (int)(ctas < 1 ? 1 : ctas > most ? most : ctas);
+}
+
+int32_t cuda_error(cudaError_t e) { return set_error(MUON_ERR_CUDA, cudaGetErrorString(e)); }
+
+// Launches (of Cap tensors at most) that a set needs: tensors and chunks bound them.
+int64_t launches_for(const muon_grad* grads, int64_t n) {
+  int64_t launches = 0, segs = 0, chunks = 0;
+  for (int64_t i = 0; i < n; ++i) {
+    const int64_t all = grads[i].elems > 0 ? chunks_per_mat(grads[i]) * grads[i].count : 0;
+    if (all == 0) continue;
+    if (launches == 0 || segs == kCapSmall || chunks + all > 2000000000ll) {
+      ++launches;
+      segs = chunks = 0;
+    }
+    ++segs;
+    chunks += all;
+  }
+  return launches;
+}
+
+template <int Cap>
+int32_t run_clip(const muon_grad* grads, int64_t n, bool clip, float max_norm, float eps, int32_t nonfinite,
+                 float* result, double* partials, int sms, cudaStream_t s) {
+  ClipArgs<Cap> a;
+  a.partials = partials;
+  a.n_partials = 0;
+  a.max_norm = max_norm;
+  a.eps = eps;
+  a.nonfinite = nonfinite;
+  a.result = result;
+  int64_t i = 0;
+  cudaError_t e;
+  int launches = 0;
+  while (i < n) {
+    fill_args(grads, n, i, a);
+    if (a.n_chunks == 0) continue;
+    const int grid = grid_for(a.n_chunks, sms);
+    a.partial0 = a.n_partials;
+    a.n_partials += grid;
+    e = launch(clip_norm_kernel<Cap>, grid, kClipThreads, 0, s, 1, false, a);
+    if (e != cudaSuccess) return cuda_error(e);
+    ++launches;
+  }
+  if (!clip) {
+    e = launch(norm_result_kernel, 1, kClipThreads, 0, s, 1, launches > 0, (const double*)partials, (int)a.n_partials,
+               result);
+    return e == cudaSuccess ? MUON_OK : cuda_error(e);
+  }
+  if (launches <= 1) {  // the table is filled already (or empty: the result alone)
+    if (launches == 0) a.n_segs = a.n_chunks = 0;
+    e = launch(clip_scale_kernel<Cap>, grid_for(a.n_chunks, sms), kClipThreads, 0, s, 1, launches > 0, a);
+    return e == cudaSuccess ? MUON_OK : cuda_error(e);
+  }
+  for (i = 0; i < n;) {
+    fill_args(grads, n, i, a);
+    if (a.n_chunks == 0) continue;
+    e = launch(clip_scale_kernel<Cap>, grid_for(a.n_chunks, sms), kClipThreads, 0, s, 1, false, a);
+    if (e != cudaSuccess) return cuda_error(e);
+  }
+  return MUON_OK;
+}
+
+int32_t clip_entry(const muon_grad* grads, int64_t n, bool clip, float max_norm, float eps, int32_t nonfinite,
+                   float* result, void* workspace, size_t workspace_bytes, void* stream) {
+  if (n < 0 || (n > 0 && !grads)) return set_error(MUON_ERR_INVALID, "gradient array is NULL or its length negative");
+  if (!result || reinterpret_cast<uint64_t>(result) % 4) return set_error(MUON_ERR_INVALID, "result is NULL or not aligned");
+  for (int64_t i = 0; i < n; ++i) {
+    const char* bad = check_grad(grads[i]);
+    if (!bad && clip) bad = check_out(grads[i]);
+    if (bad) return set_error(MUON_ERR_INVALID, bad);
+  }
+  if (clip) {
+    if (!(max_norm >= 0.f)) return set_error(MUON_ERR_INVALID, "max_norm must be >= 0");
+    if (!(eps >= 0.f) || std::isinf(eps)) return set_error(MUON_ERR_INVALID, "eps must be finite and >= 0");
+    if (nonfinite != MUON_NONFINITE_KEEP && nonfinite != MUON_NONFINITE_ZERO)
+      return set_error(MUON_ERR_INVALID, "unknown nonfinite policy");
+  }
+  size_t need = 0;
+  const int32_t st = muon_clip_workspace_bytes(grads, n, &need);
+  if (st != MUON_OK) return st;
+  if (!workspace || workspace_bytes < need) return set_error(MUON_ERR_NO_WORKSPACE, "workspace is NULL or too small");
+  if (reinterpret_cast<uint64_t>(workspace) % 16) return set_error(MUON_ERR_INVALID, "workspace must be 16-byte aligned");
+  cudaError_t e;
+  const int sms = device_sms(&e);
+  if (e != cudaSuccess) return cuda_error(e);
+  if (sms == 0) return set_error(MUON_ERR_UNSUPPORTED, "libmuon is built for sm_103a");
+  double* partials = static_cast<double*>(workspace);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return n <= kCapSmall
+             ? run_clip<kCapSmall>(grads, n, clip, max_norm, eps, nonfinite, result, partials, sms, s)
+             : run_clip<kCapLarge>(grads, n, clip, max_norm, eps, nonfinite, result, partials, sms, s);
+}
+
+}  // namespace
+}  // namespace muon
+
+using namespace muon;
+
+extern "C" {
+
+muon_status muon_clip_workspace_bytes(const muon_grad* grads, int64_t n, size_t* bytes) {
+  if (!bytes || n < 0 || (n > 0 && !grads)) return set_error(MUON_ERR_INVALID, "NULL argument or negative length");
+  for (int64_t i = 0; i < n; ++i)
+    if (const char* bad = check_grad(grads[i])) return set_error(MUON_ERR_INVALID, bad);
+  const int64_t launches = launches_for(grads, n);
+  *bytes = (size_t)(launches < 1 ? 1 : launches) * kClipMaxCtas * sizeof(double);
+  return MUON_OK;
+}
+
+muon_status muon_grad_norm(const muon_grad* grads, int64_t n, float* norm, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  return clip_entry(grads, n, false, 0.f, 0.f, 0, norm, workspace, workspace_bytes, stream);
+}
+
+muon_status muon_clip_grad_norm(const muon_grad* grads, int64_t n, float max_norm, float eps, int32_t nonfinite,
+                                float* result, void* workspace, size_t workspace_bytes, void* stream) {
+  return clip_entry(grads, n, true, max_norm, eps, nonfinite, result, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,175 @@
+"""The loss and clipping entry points: defaults, workspace sizes and refusals (no kernel runs)."""
+import ctypes
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def nsm():
+    import newton_schulz_muon_gb300.build as b
+    b.build()
+    import newton_schulz_muon_gb300 as m
+    return m
+
+
+def test_defaults(nsm):
+    p = nsm.muon_policy_config_default()
+    assert (p.clip_low, p.clip_high, p.kl_beta, p.grad_scale) == pytest.approx((0.2, 0.2, 0.0, 1.0))
+    assert p.reduction == nsm.MUON_REDUCE_TOKEN_MEAN
+    q = nsm.muon_preference_config_default(label_smoothing=0.1)
+    assert (q.beta, q.label_smoothing, q.grad_scale, q.length_normalize) == pytest.approx((0.1, 0.1, 1.0, 0))
+    with pytest.raises(AttributeError):
+        nsm.muon_policy_config_default(nothing=1)
+
+
+def test_workspace_bytes(nsm):
+    assert nsm.muon_loss_workspace_bytes(0, 0) >= 16
+    assert nsm.muon_loss_workspace_bytes(1000, 8) > nsm.muon_loss_workspace_bytes(10, 8)
+    for bad in ((-1, 0), (0, -1), (1 << 31, 0)):
+        with pytest.raises(nsm.MuonError) as e:
+            nsm.muon_loss_workspace_bytes(*bad)
+        assert e.value.status == nsm.MUON_ERR_INVALID
+
+
+def _grads(nsm, **over):
+    base = dict(g=1 << 20, out=1 << 20, elems=100, count=1, stride_elems=0, dtype=0, out_dtype=0)
+    base.update(over)
+    arr = (nsm.muon_grad * 1)()
+    arr[0] = tuple(base[k] for k in ("g", "out", "elems", "count", "stride_elems", "dtype", "out_dtype"))
+    return arr
+
+
+@pytest.mark.parametrize("over", [
+    dict(elems=-1), dict(count=-1), dict(stride_elems=99, count=2), dict(dtype=2), dict(out_dtype=1), dict(g=0),
+    dict(g=(1 << 20) + 2), dict(out=(1 << 21) + 1), dict(elems=1 << 41), dict(out=1 << 21, out_dtype=7)])
+def test_clip_refuses_bad_tensors(nsm, over):
+    st = nsm.lib.muon_clip_grad_norm(_grads(nsm, **over), 1, 1.0, 1e-6, 0, 1 << 22, 1 << 23, 1 << 20, None)
+    assert st == nsm.MUON_ERR_INVALID
+
+
+def test_clip_refuses_bad_arguments(nsm):
+    call = nsm.lib.muon_clip_grad_norm
+    g = _grads(nsm)
+    inv, ws = nsm.MUON_ERR_INVALID, 1 << 23
+    assert call(None, 1, 1.0, 1e-6, 0, 1 << 22, ws, 1 << 20, None) == inv
+    assert call(g, -1, 1.0, 1e-6, 0, 1 << 22, ws, 1 << 20, None) == inv
+    assert call(g, 1, -1.0, 1e-6, 0, 1 << 22, ws, 1 << 20, None) == inv
+    assert call(g, 1, float("nan"), 1e-6, 0, 1 << 22, ws, 1 << 20, None) == inv
+    assert call(g, 1, 1.0, -1e-6, 0, 1 << 22, ws, 1 << 20, None) == inv
+    assert call(g, 1, 1.0, float("inf"), 0, 1 << 22, ws, 1 << 20, None) == inv
+    assert call(g, 1, 1.0, 1e-6, 2, 1 << 22, ws, 1 << 20, None) == inv
+    assert call(g, 1, 1.0, 1e-6, 0, None, ws, 1 << 20, None) == inv
+    assert call(g, 1, 1.0, 1e-6, 0, 1 << 22, ws + 8, 1 << 20, None) == inv
+    assert call(g, 1, 1.0, 1e-6, 0, 1 << 22, None, 1 << 20, None) == nsm.MUON_ERR_NO_WORKSPACE
+    assert call(g, 1, 1.0, 1e-6, 0, 1 << 22, ws, 8, None) == nsm.MUON_ERR_NO_WORKSPACE
+    size = ctypes.c_size_t()
+    assert nsm.lib.muon_clip_workspace_bytes(g, 1, None) == inv
+    assert nsm.lib.muon_clip_workspace_bytes(None, 0, ctypes.byref(size)) == nsm.MUON_OK and size.value > 0
+
+
+def _batch(nsm, **over):
+    base = dict(logits=1 << 20, targets=1 << 21, mask=0, tokens=4, vocab=10, row_stride=0, dtype=0, temperature=1.0)
+    base.update(over)
+    return nsm.muon_token_batch(*[base[k] for k in ("logits", "targets", "mask", "tokens", "vocab", "row_stride",
+                                                    "dtype", "temperature")])
+
+
+def _policy(nsm, batch=None, cfg=None, old=1 << 22, ref=0, adv=1 << 22, offsets=0, n_seqs=0, stats=1 << 22, logp=0,
+            grad=1 << 23, grad_stride=0, ws=1 << 24, nbytes=1 << 20):
+    b = batch or _batch(nsm)
+    return nsm.lib.muon_policy_loss(ctypes.byref(b), None if cfg is None else ctypes.byref(cfg), old, ref, adv,
+                                    offsets, n_seqs, stats, logp, grad, grad_stride, ws, nbytes, None)
+
+
+BAD_BATCHES = [dict(tokens=-1), dict(tokens=1 << 31), dict(vocab=0), dict(vocab=(1 << 30) + 1), dict(row_stride=9),
+               dict(dtype=2), dict(temperature=0.0), dict(temperature=-1.0), dict(temperature=float("nan")),
+               dict(temperature=float("inf")), dict(logits=0), dict(targets=0), dict(logits=(1 << 20) + 2),
+               dict(targets=(1 << 21) + 4)]
+
+
+@pytest.mark.parametrize("over", BAD_BATCHES)
+def test_bad_batches_are_refused(nsm, over):
+    b = _batch(nsm, **over)
+    assert nsm.lib.muon_token_logprobs(ctypes.byref(b), 1 << 22, None) == nsm.MUON_ERR_INVALID
+    assert _policy(nsm, b) == nsm.MUON_ERR_INVALID
+    assert nsm.lib.muon_preference_loss(ctypes.byref(b), None, 1 << 22, 1 << 22, 1, 1 << 22, 0, 0, 0, 0, 1 << 24,
+                                        1 << 20, None) == nsm.MUON_ERR_INVALID
+
+
+def test_null_batch_and_outputs_are_refused(nsm):
+    assert nsm.lib.muon_token_logprobs(None, 1 << 22, None) == nsm.MUON_ERR_INVALID
+    b = _batch(nsm)
+    assert nsm.lib.muon_token_logprobs(ctypes.byref(b), None, None) == nsm.MUON_ERR_INVALID
+    assert nsm.lib.muon_token_logprobs(ctypes.byref(b), (1 << 22) + 2, None) == nsm.MUON_ERR_INVALID
+    assert nsm.lib.muon_token_logprobs(ctypes.byref(_batch(nsm, tokens=0)), None, None) == nsm.MUON_OK
+
+
+@pytest.mark.parametrize("cfg", [dict(clip_low=-0.1), dict(clip_low=1.1), dict(clip_high=-0.1),
+                                 dict(kl_beta=float("nan")), dict(grad_scale=float("inf")), dict(reduction=3),
+                                 dict(reduction=-1), dict(kl_beta=0.1), dict(reduction=1)])
+def test_bad_policy_configurations_are_refused(nsm, cfg):
+    # the last two: a KL term without ref_logp, a sequence mean without sequences
+    assert _policy(nsm, cfg=nsm.muon_policy_config_default(**cfg)) == nsm.MUON_ERR_INVALID
+
+
+@pytest.mark.parametrize("kw", [dict(old=0), dict(adv=0), dict(stats=0), dict(old=(1 << 22) + 2), dict(grad_stride=9),
+                                dict(grad=(1 << 23) + 2), dict(n_seqs=-1), dict(logp=(1 << 22) + 1),
+                                dict(grad=1 << 20, grad_stride=16), dict(ws=(1 << 24) + 4)])
+def test_bad_policy_arguments_are_refused(nsm, kw):
+    assert _policy(nsm, **kw) == nsm.MUON_ERR_INVALID
+
+
+def test_small_workspaces_are_refused(nsm):
+    assert _policy(nsm, ws=0) == nsm.MUON_ERR_NO_WORKSPACE
+    assert _policy(nsm, nbytes=nsm.muon_loss_workspace_bytes(4, 0) - 1) == nsm.MUON_ERR_NO_WORKSPACE
+
+
+@pytest.mark.parametrize("cfg", [dict(beta=0.0), dict(beta=float("inf")), dict(label_smoothing=-0.1),
+                                 dict(label_smoothing=1.1), dict(grad_scale=float("nan")), dict(length_normalize=2)])
+def test_bad_preference_configurations_are_refused(nsm, cfg):
+    b = _batch(nsm)
+    c = nsm.muon_preference_config_default(**cfg)
+    assert nsm.lib.muon_preference_loss(ctypes.byref(b), ctypes.byref(c), 1 << 22, 1 << 22, 1, 1 << 22, 0, 0, 0, 0,
+                                        1 << 24, 1 << 20, None) == nsm.MUON_ERR_INVALID
+
+
+@pytest.mark.parametrize("ref,offsets,pairs,loss", [(0, 1 << 22, 1, 1 << 22), (1 << 22, 0, 1, 1 << 22),
+                                                    (1 << 22, 1 << 22, -1, 1 << 22), (1 << 22, 1 << 22, 1, 0),
+                                                    (1 << 22, (1 << 22) + 4, 1, 1 << 22)])
+def test_bad_preference_arguments_are_refused(nsm, ref, offsets, pairs, loss):
+    b = _batch(nsm)
+    assert nsm.lib.muon_preference_loss(ctypes.byref(b), None, ref, offsets, pairs, loss, 0, 0, 0, 0, 1 << 24,
+                                        1 << 20, None) == nsm.MUON_ERR_INVALID
+
+
+def test_python_checks_need_no_gpu(nsm):
+    torch = pytest.importorskip("torch")
+    x = torch.zeros(4, 10)
+    with pytest.raises(ValueError):
+        nsm.muon_token_logprobs(x, torch.zeros(4, dtype=torch.int64))     # not on a GPU
+    with pytest.raises(ValueError):
+        nsm.GradSet([x])
+    with pytest.raises(ValueError):
+        nsm.GradSet([], [x])
+
+
+@pytest.mark.parametrize("make,want", [
+    (lambda t: t.empty(6, 8, 4), (192, 1, 0)),
+    (lambda t: t.empty(6, 8, 4).permute(1, 2, 0), (192, 1, 0)),
+    (lambda t: t.empty(6, 8, 4)[:, 2:5], (12, 6, 32)),
+    (lambda t: t.empty(3, 4, 10)[:, :, :8], (8, 12, 10)),
+    (lambda t: t.empty(5, 0, 2), (0, 1, 0)),
+    (lambda t: t.empty(()), (1, 1, 0)),
+    (lambda t: t.empty(20)[::2], (1, 10, 2)),
+])
+def test_gradient_layouts(nsm, make, want):
+    torch = pytest.importorskip("torch")
+    assert nsm._blocks(make(torch)) == want
+
+
+@pytest.mark.parametrize("make", [lambda t: t.empty(5, 1).expand(5, 4), lambda t: t.empty(4, 4)[::2, ::2],
+                                  lambda t: t.empty(10).as_strided((3, 4), (2, 1))])
+def test_overlapping_or_scattered_gradients_are_refused(nsm, make):
+    torch = pytest.importorskip("torch")
+    with pytest.raises(ValueError):
+        nsm._blocks(make(torch))
