@@ -445,7 +445,7 @@ typedef struct {
   int64_t vocab;           /* 1 .. 2^30 */
   int64_t row_stride;      /* >= vocab; 0 means vocab */
   int32_t dtype;           /* MUON_DTYPE_* of the logits and their gradient */
-  float temperature;       /* logits are divided by it; finite, > 0 */
+  float temperature;       /* logits are divided by it; 1e-20 .. 1e20 */
 } muon_token_batch;
 
 /* logp[t] = z[t, y_t] - log sum_j exp(z[t, j]), z = logits / temperature (fp32,

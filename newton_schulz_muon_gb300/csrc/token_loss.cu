@@ -8,9 +8,14 @@
 // the sums over whole sequences first, so its forward and backward passes are launches
 // of their own with a small one between them.
 //
-// Exponentials are taken in base 2 with c = log2(e) / temperature: a row's sum is
-// s = sum_j 2^(c z_j - f) with the frame f = fl(c m), m = max_j z_j, and every later use
-// takes the same f, so that its rounding cancels.
+// The sum over a row leaves the target out: with m the largest of the other logits,
+//   S = sum_{j != y} e^(z_j - m),   x = z_y - m,
+//   logp = -log1p(S e^-x) where x >= 0, else x - log(S + e^x),
+// which keeps logp's digits (and those of 1 - p_y) where the target is nearly certain.
+// Exponentials are taken in base 2, 2^(c (z - m)) with c = log2(e) / temperature in two
+// floats: the difference is formed first, so that the largest term is exactly 1 and
+// logits at the type's limits do not overflow, and a rounded c alone would shift every
+// row's sum the same way.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -27,8 +32,6 @@
 namespace muon {
 namespace {
 
-constexpr float kLn2 = 0.693147180559945309f;
-
 // What a row kernel does with each row.
 enum RowMode : int32_t {
   kLogp = 0,     // log-probabilities
@@ -41,10 +44,10 @@ struct RowArgs {
   const int64_t* targets;
   const uint8_t* mask;
   int64_t tokens, vocab, stride, grad_stride;
-  float c;               // log2(e) / temperature
+  float c_hi, c_lo;      // log2(e) / temperature = c_hi + c_lo, c_lo > 0
   float inv_temp;
   float* logp;           // or null
-  float2* frame;         // kForward: (m, s) of each row
+  float2* frame;         // kForward: (m, sum over the whole row) of each row
   float* slope;          // kForward: cleared for rows of no sequence
   // kPolicy
   const float* old_logp;
@@ -54,7 +57,12 @@ struct RowArgs {
   const float* weight;    // sequence mean: [tokens]
   float low, high, beta, grad_scale;
   void* grad;             // or null
-  float4* terms;          // [tokens]: w (-s + beta k), w (-s), w k, w [clipped]
+  double* partials;       // 4 for each cluster: its rows' sums of w (-s + beta k), w (-s), w k, w [clipped]
+  unsigned* ticket;       // zeroed by the kernel before
+  float* stats;
+  // shape of the launch
+  int32_t cluster;        // CTAs a row
+  int32_t stage_vecs;     // 16-byte units of one ring stage
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -75,6 +83,22 @@ struct Vec<float> {
   static __device__ __forceinline__ uint4 pack(const float (&v)[4]) {
     return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
   }
+  static constexpr uint32_t kLowest = 0xFF800000u;  // -inf in every element of a word
+  static __device__ __forceinline__ void drop(uint4& w, int e) {
+    w.x = e == 0 ? kLowest : w.x;
+    w.y = e == 1 ? kLowest : w.y;
+    w.z = e == 2 ? kLowest : w.z;
+    w.w = e == 3 ? kLowest : w.w;
+  }
+  template <int G>
+  static __device__ __forceinline__ float max(const uint4 (&w)[G]) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+      m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(w[g].x), __uint_as_float(w[g].y)),
+                         fmaxf(__uint_as_float(w[g].z), __uint_as_float(w[g].w))));
+    return m;
+  }
   static __device__ __forceinline__ float load(const float* p) { return *p; }
   static __device__ __forceinline__ void store(float* p, float v) { *p = v; }
 };
@@ -93,84 +117,170 @@ struct Vec<__nv_bfloat16> {
     return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                       pack_bf16x2(v[6], v[7]));
   }
+  static constexpr uint32_t kLowest = 0xFF80FF80u;
+  static __device__ __forceinline__ void drop(uint4& w, int e) {
+    const uint32_t keep = (e & 1) ? 0x0000FFFFu : 0xFFFF0000u, low = kLowest & ~keep;
+    w.x = (e >> 1) == 0 ? (w.x & keep) | low : w.x;
+    w.y = (e >> 1) == 1 ? (w.y & keep) | low : w.y;
+    w.z = (e >> 1) == 2 ? (w.z & keep) | low : w.z;
+    w.w = (e >> 1) == 3 ? (w.w & keep) | low : w.w;
+  }
+  template <int G>
+  static __device__ __forceinline__ float max(const uint4 (&w)[G]) {
+    __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162*>(&w[0].x);
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const uint32_t u[4] = {w[g].x, w[g].y, w[g].z, w[g].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162*>(&u[i]));
+    }
+    return fmaxf(__low2float(m), __high2float(m));
+  }
   static __device__ __forceinline__ float load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
   static __device__ __forceinline__ void store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 };
 
-// A partial sum of exponentials: s = sum_j 2^(c z_j - fl(c m)), m the largest z so far
-// (-inf: nothing yet, or only logits of -inf).  c m leaves fp32's range for logits near
-// the type's limits (a mask of its lowest value); the numbers there are so far apart that
-// only those equal to m count, one each.
+// Two floats at a time (one issue slot).
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 make_f2(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 split(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
+// 2^(c (z - m)) of one value and of two.  c_lo > 0, so that a difference of -inf stays one.
+struct Expo {
+  float m, c_hi, c_lo;  // m finite or +inf
+  __device__ __forceinline__ float one(float z) const {
+    const float d = z - m;
+    return ex2(__fmaf_rn(d, c_hi, d * c_lo));
+  }
+  __device__ __forceinline__ float2 two(float z0, float z1) const {
+    const F2 d = add2(make_f2(z0, z1), make_f2(-m, -m));
+    const float2 u = split(fma2(d, make_f2(c_hi, c_hi), mul2(d, make_f2(c_lo, c_lo))));
+    return make_float2(ex2(u.x), ex2(u.y));
+  }
+};
+
+// With no finite logit but the target's, any finite m gives the right zeros.
+__device__ __forceinline__ Expo exponent(const RowArgs& a, float m) {
+  return Expo{m == -INFINITY ? 0.f : m, a.c_hi, a.c_lo};
+}
+
+// A partial sum of exponentials: s = sum_j 2^(c (z_j - m)), m the largest z so far
+// (-inf: nothing yet, or only logits of -inf).
 struct Sum {
   float m, s;
 };
 
-__device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
-
 // Factor that takes a sum from the frame of m to that of the larger `to`.
-__device__ __forceinline__ float reframe(float m, float to, float c) {
+__device__ __forceinline__ float reframe(const RowArgs& a, float m, float to) {
   if (m == to) return 1.f;  // both -inf among them
-  const float f = to * c;
-  return f == -INFINITY ? 0.f : ex2(m * c - f);  // a NaN stays one
+  return exponent(a, to).one(m);  // a NaN stays one
 }
 
-__device__ __forceinline__ Sum merge(const Sum& a, const Sum& b, float c) {
+__device__ __forceinline__ Sum merge(const RowArgs& a, const Sum& x, const Sum& y) {
   Sum r;
-  r.m = fmaxf(a.m, b.m);
-  r.s = a.s * reframe(a.m, r.m, c) + b.s * reframe(b.m, r.m, c);
+  r.m = fmaxf(x.m, y.m);
+  r.s = x.s * reframe(a, x.m, r.m) + y.s * reframe(a, y.m, r.m);
   return r;
 }
 
-// 2^(c z - f) in the frame of m whose f = c m is out of range.
-__device__ __forceinline__ float far_term(float z, float m) {
-  if (z != z || z == INFINITY) return NAN;
-  return z == m && z != -INFINITY ? 1.f : 0.f;
+// Merges the lanes' sums: the largest m first, then one factor a lane.
+__device__ __forceinline__ Sum warp_merge(const RowArgs& a, const Sum& t) {
+  Sum r;
+  r.m = t.m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) r.m = fmaxf(r.m, __shfl_xor_sync(0xFFFFFFFFu, r.m, o));
+  r.s = t.s * reframe(a, t.m, r.m);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) r.s += __shfl_xor_sync(0xFFFFFFFFu, r.s, o);
+  return r;
 }
 
-template <int N>
-__device__ __forceinline__ void add_values(Sum& t, const float (&v)[N], float c) {
-  float m = v[0];
-#pragma unroll
-  for (int i = 1; i < N; ++i) m = fmaxf(m, v[i]);
+// G 16-byte units of a row.
+template <typename T, int G>
+__device__ __forceinline__ void add_units(const RowArgs& a, Sum& t, const uint4 (&w)[G]) {
+  constexpr int N = Vec<T>::N;
+  const float m = Vec<T>::max(w);
   if (!(m <= t.m)) {
-    t.s *= t.s == 0.f ? 1.f : reframe(t.m, m, c);
+    t.s *= reframe(a, t.m, m);
     t.m = m;
   }
-  const float f = t.m * c;
-  if (finite(f)) {
+  const Expo x = exponent(a, t.m);
+  F2 s0 = make_f2(t.s, 0.f), s1 = make_f2(0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < N; ++i) t.s += ex2(__fmaf_rn(v[i], c, -f));
-  } else {
+  for (int g = 0; g < G; ++g) {
+    float v[N];
+    Vec<T>::unpack(w[g], v);
 #pragma unroll
-    for (int i = 0; i < N; ++i) t.s += far_term(v[i], t.m);
+    for (int i = 0; i < N; i += 4) {
+      const float2 e0 = x.two(v[i], v[i + 1]), e1 = x.two(v[i + 2], v[i + 3]);
+      s0 = add2(s0, make_f2(e0.x, e0.y));
+      s1 = add2(s1, make_f2(e1.x, e1.y));
+    }
   }
+  const float2 r = split(add2(s0, s1));
+  t.s = r.x + r.y;
 }
 
-// log2 of the target's probability; also the exponent's form in pass 2.
-__device__ __forceinline__ float log2_prob(float z, const Sum& t, float c) {
-  const float f = t.m * c;
-  const float d = finite(f) ? __fmaf_rn(z, c, -f) : log2f(far_term(z, t.m));
-  return d - log2f(t.s);
-}
-
-__device__ __forceinline__ float term(float z, float c, float m, float f, bool near) {
-  return near ? ex2(__fmaf_rn(z, c, -f)) : far_term(z, m);
-}
-
-__device__ __forceinline__ Sum warp_merge(Sum t, float c) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    Sum b;
-    b.m = __shfl_xor_sync(0xFFFFFFFFu, t.m, o);
-    b.s = __shfl_xor_sync(0xFFFFFFFFu, t.s, o);
-    t = merge(t, b, c);
+__device__ __forceinline__ void add_value(const RowArgs& a, Sum& t, float v) {
+  if (!(v <= t.m)) {
+    t.s *= reframe(a, t.m, v);
+    t.m = v;
   }
-  return t;
+  t.s += exponent(a, t.m).one(v);
 }
 
-// A position's scalars, read before its logits are.
+// A row's log-probability, and the sum over the whole row in the frame of m.
+struct Prob {
+  float logp, s;
+};
+
+__device__ __forceinline__ Prob row_prob(const RowArgs& a, const Sum& t, float zy) {
+  const float x = (zy - t.m) * a.inv_temp;
+  const float e = expf(x);
+  Prob p;
+  p.s = t.s + e;
+  p.logp = x >= 0.f ? 0.f - log1pf(t.s * expf(-x)) : x - logf(p.s);
+  if (zy == INFINITY) p.logp = NAN;
+  return p;
+}
+
+// The gradient's elements: factor 2^(c (z_j - m)), and at_y at the target.
+struct Factor {
+  float m, factor, at_y;
+};
+
+__device__ __forceinline__ Factor row_factor(const RowArgs& a, float m, float s, float logp, float slope) {
+  const float f = slope * a.grad_scale * a.inv_temp;
+  return Factor{m, f == 0.f ? 0.f : -f / s, -f * expm1f(logp)};
+}
+
+// A position's scalars.
 struct Position {
-  int64_t y;
   float old_logp, ref, adv, w;
 };
 
@@ -207,116 +317,498 @@ __device__ __forceinline__ Outcome policy_terms(const RowArgs& a, const Position
   return o;
 }
 
-constexpr int kRowThreads = 512;
-constexpr int kRowWarps = kRowThreads / 32;
+// ---------------------------------------------------------------------------
+// rows
+// ---------------------------------------------------------------------------
+// The 16-byte units that lie whole in a row, and the elements around them.
+struct Row {
+  int64_t head;  // elements before the first unit
+  int64_t units;
+  int64_t tail;  // first element after the last unit
+};
 
-// One CTA a row, the row read twice (the second time from L2).
-template <typename T, int kMode>
-__global__ void __launch_bounds__(kRowThreads) row_kernel(const __grid_constant__ RowArgs a) {
+template <typename T>
+__device__ __forceinline__ Row row_of(const T* z, int64_t vocab) {
+  Row r;
+  r.head = min(vocab, (int64_t)(((16 - (reinterpret_cast<uint64_t>(z) & 15)) & 15) / sizeof(T)));
+  r.units = (vocab - r.head) / Vec<T>::N;
+  r.tail = r.head + r.units * Vec<T>::N;
+  return r;
+}
+
+// The element of a row that lane `lane` of its edge warp looks after, or -1: lanes 0-7
+// those before the first unit, 8-15 those after the last.
+__device__ __forceinline__ int64_t edge_of(const Row& r, int64_t vocab, int lane) {
+  if (lane < 8) return lane < r.head ? lane : -1;
+  return lane < 16 && r.tail + lane - 8 < vocab ? r.tail + lane - 8 : -1;
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 scaled_unit(const uint4& w, const Expo& x, float factor) {
   constexpr int N = Vec<T>::N;
-  __shared__ Sum red[kRowWarps];
-  __shared__ float2 back;  // dL/dz factor of the row, and the target's value
-  const int tid = threadIdx.x;
+  float v[N];
+  Vec<T>::unpack(w, v);
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    const float2 e = x.two(v[i], v[i + 1]);
+    const float2 r = split(mul2(make_f2(e.x, e.y), make_f2(factor, factor)));
+    v[i] = r.x;
+    v[i + 1] = r.y;
+  }
+  return Vec<T>::pack(v);
+}
+
+template <typename T>
+__device__ __forceinline__ void put(uint4& w, int e, float v) {
+  float u[Vec<T>::N];
+  Vec<T>::unpack(w, u);
+#pragma unroll
+  for (int i = 0; i < Vec<T>::N; ++i) u[i] = i == e ? v : u[i];
+  w = Vec<T>::pack(u);
+}
+
+// A unit of the gradient: one store where the gradient's row is aligned as the logits'
+// row is, else its elements one by one.
+template <typename T>
+__device__ __forceinline__ void store_unit(T* g, const uint4& w, bool whole) {
+  if (whole) {
+    *reinterpret_cast<uint4*>(g) = w;
+  } else {
+    float v[Vec<T>::N];
+    Vec<T>::unpack(w, v);  // exact both ways
+#pragma unroll
+    for (int i = 0; i < Vec<T>::N; ++i) Vec<T>::store(g + i, v[i]);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ bool aligned_unit(const T* g) {
+  return (reinterpret_cast<uint64_t>(g) & 15) == 0;
+}
+
+constexpr int kMaxRowThreads = 512;
+constexpr int kMaxRowWarps = kMaxRowThreads / 32;
+constexpr int kMaxCluster = 8;
+constexpr int kBatch = 256;  // rows whose scalars a CTA holds at a time
+constexpr int kGroup = 4;    // 16-byte units a thread takes at a time
+
+// Shared memory beside the ring.
+struct RowShared {
+  Sum slot[2][kMaxCluster][kMaxRowWarps];  // partial sums of a row, from every warp of the cluster
+  Factor factor[2];
+  int32_t row[kBatch];      // live rows from the front, masked rows from the back (offset in the batch)
+  int32_t unit[kBatch];     // the target's unit in this CTA's part; -1: elsewhere
+  int32_t elem[kBatch];     // its element in the unit; or, with unit = -2, the edge lane that has it
+  float zy[kBatch];
+  float old_logp[kBatch], ref[kBatch], adv[kBatch], w[kBatch];
+  int32_t live[kBatch / 32];
+  int32_t last;
+};
+
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// Barriers 1 and 2 (by the row's parity): warp 0 has written a row's factor.
+__device__ __forceinline__ void factor_sync(int par, uint32_t count) {
+  if (par) asm volatile("bar.sync 2, %0;" ::"r"(count) : "memory");
+  else asm volatile("bar.sync 1, %0;" ::"r"(count) : "memory");
+}
+__device__ __forceinline__ void factor_arrive(int par, uint32_t count) {
+  if (par) asm volatile("bar.arrive 2, %0;" ::"r"(count) : "memory");
+  else asm volatile("bar.arrive 1, %0;" ::"r"(count) : "memory");
+}
+
+__device__ __forceinline__ void store_remote(Sum* p, uint32_t rank, const Sum& v) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(mapa_shared(p, rank)), "f"(v.m), "f"(v.s) : "memory");
+}
+
+// Sums of rows' terms, carried with their rounding errors.
+struct Terms {
+  float hi[4] = {0.f, 0.f, 0.f, 0.f}, lo[4] = {0.f, 0.f, 0.f, 0.f};
+  __device__ __forceinline__ void add(const float4& t) {
+    const float v[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float sum, err;
+      two_sum(hi[k], v[k], sum, err);
+      hi[k] = sum;
+      lo[k] += fabsf(sum) < INFINITY ? err : 0.f;
+    }
+  }
+};
+
+// Thread 0's sums into the partials; the last of `n` to come adds all of them, in their order.
+__device__ __forceinline__ void finish_stats(const RowArgs& a, const Terms& acc, int64_t part, int64_t n, int32_t* last) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) a.partials[4 * part + k] = (double)acc.hi[k] + (double)acc.lo[k];
+    __threadfence();
+    *last = atomicAdd(a.ticket, 1u) == (unsigned)n - 1;
+  }
+  __syncthreads();
+  if (*last && warp < 4) {
+    __threadfence();
+    double sum = 0.0;
+    for (int64_t k = lane; k < n; k += 32) sum += __ldcg(a.partials + 4 * k + warp);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    if (lane == 0) a.stats[warp] = (float)sum;
+  }
+}
+
+// A cluster of 1 to 8 CTAs takes one row at a time and keeps it in shared memory between
+// the sum and the gradient, so that every logit is read from HBM once.  Each thread copies
+// its own 16-byte units into a ring of kStages rows (cp.async) and is the only one to read
+// them, so that only the sums cross threads: every warp writes its partial sum to all CTAs
+// of the cluster and warp 0 of each forms the row's result.  While a row's sums travel, the
+// other warps write the gradient of the row before; its stage then takes the row
+// kStages - 1 further on.
+template <typename T, int kMode, int kStages>
+__global__ void __launch_bounds__(kMaxRowThreads) row_kernel(const __grid_constant__ RowArgs a) {
+  constexpr int N = Vec<T>::N;
+  extern __shared__ __align__(16) uint4 ring[];
+  RowShared& sh = *reinterpret_cast<RowShared*>(ring + (size_t)kStages * a.stage_vecs);
+  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = nt >> 5;
+  const int ncta = a.cluster;
+  const int rank = ncta > 1 ? (int)cluster_ctarank() : 0;
+  const int64_t cid = blockIdx.x / ncta, n_clusters = gridDim.x / ncta;
+  const bool has_grad = kMode == kPolicy && a.grad != nullptr;
+  const bool edge_warp = rank == 0 && warp == 1;
+  const T* const logits = reinterpret_cast<const T*>(a.logits);
+  T* const grads = reinterpret_cast<T*>(a.grad);
+  Terms acc;  // of warp 0
+
+  griddep_launch_dependents();
+  bool waited = false;
+  const int64_t my_rows = a.tokens > cid ? (a.tokens - cid + n_clusters - 1) / n_clusters : 0;
+  for (int64_t first = 0; first < my_rows; first += kBatch) {
+    const int rows = (int)min((int64_t)kBatch, my_rows - first);
+    const int64_t t0 = cid + first * n_clusters;  // row r of the batch is t0 + r n_clusters
+    // live rows in order from the front of sh.row, the others from its back
+    for (int r = tid; r < kBatch; r += nt) {
+      const bool live = r < rows && (a.mask == nullptr || a.mask[t0 + r * n_clusters] != 0);
+      const unsigned bits = __ballot_sync(0xFFFFFFFFu, live);
+      if (lane == 0) sh.live[r >> 5] = (int32_t)bits;
+    }
+    __syncthreads();
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < kBatch / 32; ++k) n += __popc((unsigned)sh.live[k]);
+    for (int r = tid; r < rows; r += nt) {
+      int before = __popc((unsigned)sh.live[r >> 5] & ((1u << (r & 31)) - 1));
+      for (int k = 0; k < (r >> 5); ++k) before += __popc((unsigned)sh.live[k]);
+      const bool live = ((unsigned)sh.live[r >> 5] >> (r & 31)) & 1;
+      sh.row[live ? before : rows - 1 - (r - before)] = r;
+    }
+    __syncthreads();
+
+    auto part_of = [&](const Row& row, int64_t& v0) {  // this CTA's units of a row
+      const int64_t per = (row.units + ncta - 1) / ncta;
+      v0 = rank * per;
+      return (int)max((int64_t)0, min(per, row.units - v0));
+    };
+    // Starts the copy of live row i; the edge warp's lanes get their elements of it.
+    auto issue = [&](int i) {
+      float e = -INFINITY;
+      if (i < n) {
+        const T* z = logits + (t0 + sh.row[i] * n_clusters) * a.stride;
+        const Row row = row_of(z, a.vocab);
+        int64_t v0;
+        const int cnt = part_of(row, v0);
+        const uint4* src = reinterpret_cast<const uint4*>(z + row.head) + v0;
+        uint4* dst = ring + (size_t)(i % kStages) * a.stage_vecs;
+        for (int l = tid; l < cnt; l += nt) cp_async_16(dst + l, src + l);
+        if (edge_warp) {
+          const int64_t at = edge_of(row, a.vocab, lane);
+          if (at >= 0) e = Vec<T>::load(z + at);
+        }
+      }
+      cp_async_commit();
+      return e;
+    };
+    float edge[kStages];  // of rows i - 1, i, i + 1, ...
+    edge[0] = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) edge[i + 1] = issue(i);
+
+    // the scalars of the batch's live rows
+    for (int i = tid; i < n; i += nt) {
+      const int64_t t = t0 + sh.row[i] * n_clusters;
+      const T* z = logits + t * a.stride;
+      const int64_t y = a.targets[t];
+      const bool in = y >= 0 && y < a.vocab;
+      sh.zy[i] = in ? Vec<T>::load(z + y) : NAN;
+      const Row row = row_of(z, a.vocab);
+      int64_t v0;
+      const int cnt = part_of(row, v0);
+      int32_t unit = -1, elem = 0;
+      if (in && y >= row.head && y < row.tail) {
+        const int64_t u = (y - row.head) / N - v0;
+        if (u >= 0 && u < cnt) unit = (int32_t)u;
+        elem = (int32_t)((y - row.head) % N);
+      } else if (in) {
+        unit = -2;
+        elem = (int32_t)(y < row.head ? y : 8 + y - row.tail);
+      }
+      sh.unit[i] = unit;
+      sh.elem[i] = elem;
+      if (kMode == kPolicy) {
+        sh.old_logp[i] = a.old_logp[t];
+        sh.ref[i] = a.ref_logp ? a.ref_logp[t] : 0.f;
+        sh.adv[i] = a.adv[t];
+      }
+    }
+    if (!waited) {
+      griddep_wait();
+      waited = true;
+    }
+    if (kMode == kPolicy)
+      for (int i = tid; i < n; i += nt) sh.w[i] = a.weight ? __ldcg(a.weight + t0 + sh.row[i] * n_clusters) : __ldcg(a.inv_count);
+    // masked rows
+    for (int i = n; i < rows; ++i) {
+      const int64_t t = t0 + sh.row[i] * n_clusters;
+      if (rank == 0 && tid == 0) {
+        if (a.logp) a.logp[t] = 0.f;
+        if (kMode == kForward) a.slope[t] = 0.f;
+      }
+      if (!has_grad) continue;
+      T* g = grads + t * a.grad_stride;
+      const Row row = row_of(g, a.vocab);
+      int64_t v0;
+      const int cnt = part_of(row, v0);
+      uint4* dst = reinterpret_cast<uint4*>(g + row.head) + v0;
+      for (int l = tid; l < cnt; l += nt) dst[l] = make_uint4(0, 0, 0, 0);
+      if (edge_warp) {
+        const int64_t e = edge_of(row, a.vocab, lane);
+        if (e >= 0) Vec<T>::store(g + e, 0.f);
+      }
+    }
+    __syncthreads();
+
+    for (int i = 0; i <= n; ++i) {
+      const int par = i & 1;
+      if (i < n) {
+        // the row's sum without its target: this thread's part, then the warp's
+        cp_async_wait<kStages - 2>();
+        const T* z = logits + (t0 + sh.row[i] * n_clusters) * a.stride;
+        const Row row = row_of(z, a.vocab);
+        int64_t v0;
+        const int cnt = part_of(row, v0);
+        const uint4* src = ring + (size_t)(i % kStages) * a.stage_vecs;
+        const int unit = sh.unit[i], elem = sh.elem[i];
+        Sum t{-INFINITY, 0.f};
+        for (int l = tid; l < cnt; l += kGroup * nt) {
+          uint4 w[kGroup];
+#pragma unroll
+          for (int g = 0; g < kGroup; ++g) {
+            const int j = l + g * nt;
+            w[g] = j < cnt ? src[j] : make_uint4(Vec<T>::kLowest, Vec<T>::kLowest, Vec<T>::kLowest, Vec<T>::kLowest);
+            if (j == unit) Vec<T>::drop(w[g], elem);
+          }
+          add_units<T>(a, t, w);
+        }
+        if (edge_warp && !(unit == -2 && elem == lane)) add_value(a, t, edge[1]);
+        t = warp_merge(a, t);
+        if (i > 0 && warp != 0) cluster_wait();  // row i - 1's sums are everywhere: its slots' twins are free
+        if (lane < ncta) store_remote(&sh.slot[par][rank][warp], lane, t);
+        __syncwarp();
+        cluster_arrive();
+      } else if (i > 0 && warp != 0) {
+        cluster_wait();
+      }
+      if (i > 0 && has_grad) {
+        // the gradient of the row before
+        const int64_t t = t0 + sh.row[i - 1] * n_clusters;
+        const Row row = row_of(logits + t * a.stride, a.vocab);
+        int64_t v0;
+        const int cnt = part_of(row, v0);
+        const uint4* src = ring + (size_t)((i - 1) % kStages) * a.stage_vecs;
+        T* g = grads + t * a.grad_stride;
+        T* dst = g + row.head + v0 * N;
+        const bool whole = aligned_unit(g + row.head);
+        const int unit = sh.unit[i - 1], elem = sh.elem[i - 1];
+        if (warp != 0) factor_sync(par ^ 1, nt);  // warp 0 has put the factor there
+        const Factor f = sh.factor[par ^ 1];
+        const Expo x = exponent(a, f.m);
+        for (int l = tid; l < cnt; l += nt) {
+          uint4 w = scaled_unit<T>(src[l], x, f.factor);
+          if (l == unit) put<T>(w, elem, f.at_y);
+          store_unit(dst + (int64_t)l * N, w, whole);
+        }
+        if (edge_warp) {
+          const int64_t e = edge_of(row, a.vocab, lane);
+          if (e >= 0) Vec<T>::store(g + e, unit == -2 && elem == lane ? f.at_y : f.factor * x.one(edge[0]));
+        }
+      }
+      if (i < n) {
+        if (warp == 0) {
+          __syncwarp();
+          cluster_wait();
+          // the row's sum: every warp of every CTA, in the same order in each
+          Sum t{-INFINITY, 0.f};
+          for (int k = lane; k < ncta * warps; k += 32) t = merge(a, t, sh.slot[par][k / warps][k % warps]);
+          t = warp_merge(a, t);
+          const Prob p = row_prob(a, t, sh.zy[i]);
+          const int64_t pos = t0 + sh.row[i] * n_clusters;
+          const bool writer = rank == 0 && lane == 0;
+          if (writer && a.logp) a.logp[pos] = p.logp;
+          if (kMode == kForward && writer) {
+            a.frame[pos] = make_float2(t.m, p.s);
+            a.slope[pos] = 0.f;
+          }
+          if (kMode == kPolicy) {
+            const Position at{sh.old_logp[i], sh.ref[i], sh.adv[i], sh.w[i]};
+            const Outcome o = policy_terms(a, at, p.logp);
+            if (has_grad && lane == 0) sh.factor[par] = row_factor(a, t.m, p.s, p.logp, o.slope);
+            acc.add(o.terms);
+          }
+          if (has_grad) {
+            __syncwarp();
+            factor_arrive(par, nt);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k + 1 < kStages; ++k) edge[k] = edge[k + 1];
+        edge[kStages - 1] = issue(i + kStages - 1);
+      }
+    }
+    // the batch's scalars are free, and so are its slots in every CTA of the cluster
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+  }
+  if (!waited) griddep_wait();
+  if (kMode == kPolicy && rank == 0) finish_stats(a, acc, cid, n_clusters, &sh.last);
+}
+
+// Rows too long for a cluster's shared memory: one CTA a row, which it reads twice where
+// it writes the gradient.
+template <typename T, int kMode>
+__global__ void __launch_bounds__(kMaxRowThreads) wide_row_kernel(const __grid_constant__ RowArgs a) {
+  constexpr int N = Vec<T>::N, nt = kMaxRowThreads;
+  __shared__ Sum red[kMaxRowWarps];
+  __shared__ int32_t last;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  Terms acc;
+  griddep_launch_dependents();
   griddep_wait();
   for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
     const T* z = reinterpret_cast<const T*>(a.logits) + t * a.stride;
     T* g = reinterpret_cast<T*>(a.grad) + t * a.grad_stride;
-    const bool live = a.mask == nullptr || a.mask[t] != 0;
-    const uint64_t mis = reinterpret_cast<uint64_t>(z) & 15;
-    const int64_t head = min(a.vocab, (int64_t)(((16 - mis) & 15) / sizeof(T)));
-    const int64_t nv = (a.vocab - head) / N;
-    const int64_t tail = head + nv * N;
-    const uint4* zv = reinterpret_cast<const uint4*>(z + head);
-    if (!live) {
-      if (tid == 0) {
-        if (a.logp) a.logp[t] = 0.f;
-        if (kMode == kForward) a.slope[t] = 0.f;
-        if (kMode == kPolicy) a.terms[t] = make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-      if (kMode == kPolicy && a.grad)
-        for (int64_t j = tid; j < a.vocab; j += kRowThreads) Vec<T>::store(g + j, 0.f);
+    const bool has_grad = kMode == kPolicy && a.grad != nullptr;
+    if (a.mask != nullptr && a.mask[t] == 0) {
+      if (tid == 0 && a.logp) a.logp[t] = 0.f;
+      if (kMode == kForward && tid == 0) a.slope[t] = 0.f;
+      if (has_grad)
+        for (int64_t j = tid; j < a.vocab; j += nt) Vec<T>::store(g + j, 0.f);
       continue;
     }
-    Sum part{-INFINITY, 0.f};
-    for (int64_t i = tid; i < nv; i += kRowThreads) {
-      float v[N];
-      Vec<T>::unpack(zv[i], v);
-      add_values<N>(part, v, a.c);
-    }
-    const int64_t edge = tid < 16 ? (tid < head ? tid : -1) : (tid < 32 && tail + tid - 16 < a.vocab ? tail + tid - 16 : -1);
-    if (edge >= 0) {
-      float v[1] = {Vec<T>::load(z + edge)};
-      add_values<1>(part, v, a.c);
-    }
-    part = warp_merge(part, a.c);
-    if ((tid & 31) == 0) red[tid >> 5] = part;
-    __syncthreads();
-    Sum all = red[0];
+    const Row row = row_of(z, a.vocab);
+    const uint4* src = reinterpret_cast<const uint4*>(z + row.head);
+    const int64_t y = a.targets[t];
+    const bool in = y >= 0 && y < a.vocab;
+    const float zy = in ? Vec<T>::load(z + y) : NAN;
+    const int64_t unit = in && y >= row.head && y < row.tail ? (y - row.head) / N : -1;
+    const int elem = (int)((y - row.head) % N);
+    const int64_t edge = tid < 16 ? edge_of(row, a.vocab, tid) : -1;
+    const float zedge = edge >= 0 ? Vec<T>::load(z + edge) : -INFINITY;
+    Sum s{-INFINITY, 0.f};
+    for (int64_t l = tid; l < row.units; l += kGroup * nt) {
+      uint4 w[kGroup];
 #pragma unroll
-    for (int w = 1; w < kRowWarps; ++w) all = merge(all, red[w], a.c);
+      for (int k = 0; k < kGroup; ++k) {
+        const int64_t u = l + k * nt;
+        w[k] = u < row.units ? src[u] : make_uint4(Vec<T>::kLowest, Vec<T>::kLowest, Vec<T>::kLowest, Vec<T>::kLowest);
+        if (u == unit) Vec<T>::drop(w[k], elem);
+      }
+      add_units<T>(a, s, w);
+    }
+    if (edge >= 0 && edge != y) add_value(a, s, zedge);
+    s = warp_merge(a, s);
+    if (lane == 0) red[warp] = s;
+    __syncthreads();
+    s = warp_merge(a, lane < kMaxRowWarps ? red[lane] : Sum{-INFINITY, 0.f});
+    const Prob p = row_prob(a, s, zy);
     if (tid == 0) {
-      const int64_t y = a.targets[t];
-      const bool fits = y >= 0 && y < a.vocab;
-      const float zy = fits ? Vec<T>::load(z + y) : NAN;
-      const float logp = kLn2 * log2_prob(zy, all, a.c);
-      if (a.logp) a.logp[t] = logp;
+      if (a.logp) a.logp[t] = p.logp;
       if (kMode == kForward) {
-        a.frame[t] = make_float2(all.m, all.s);
+        a.frame[t] = make_float2(s.m, p.s);
         a.slope[t] = 0.f;
       }
-      if (kMode == kPolicy) {
-        Position p;
-        p.y = y;
-        p.old_logp = a.old_logp[t];
-        p.ref = a.ref_logp ? a.ref_logp[t] : 0.f;
-        p.adv = a.adv[t];
-        p.w = a.weight ? a.weight[t] : *a.inv_count;
-        const Outcome o = policy_terms(a, p, logp);
-        a.terms[t] = o.terms;
-        const float f = o.slope * a.grad_scale * a.inv_temp;
-        back = make_float2(-f / all.s, -f * expm1f(logp));
+    }
+    if (kMode == kPolicy) {
+      const Position at{a.old_logp[t], a.ref_logp ? a.ref_logp[t] : 0.f, a.adv[t],
+                        a.weight ? __ldcg(a.weight + t) : __ldcg(a.inv_count)};
+      const Outcome o = policy_terms(a, at, p.logp);
+      acc.add(o.terms);
+      if (has_grad) {
+        const Factor f = row_factor(a, s.m, p.s, p.logp, o.slope);
+        const Expo x = exponent(a, f.m);
+        const bool whole = aligned_unit(g + row.head);
+        for (int64_t l = tid; l < row.units; l += nt) {
+          uint4 w = scaled_unit<T>(src[l], x, f.factor);
+          if (l == unit) put<T>(w, elem, f.at_y);
+          store_unit(g + row.head + l * N, w, whole);
+        }
+        if (edge >= 0) Vec<T>::store(g + edge, edge == y ? f.at_y : f.factor * x.one(zedge));
       }
     }
-    __syncthreads();
-    if (kMode == kPolicy && a.grad) {
-      const float2 b = back;
-      const int64_t y = a.targets[t];
-      const float f = all.m * a.c;
-      const bool near = finite(f);
-      for (int64_t j = tid; j < a.vocab; j += kRowThreads) {
-        const float e = term(Vec<T>::load(z + j), a.c, all.m, f, near);
-        Vec<T>::store(g + j, j == y ? b.y : b.x * e);
-      }
-      __syncthreads();  // `back` and `red` are free for the next row
-    }
+    __syncthreads();  // red is free
   }
+  if (kMode == kPolicy) finish_stats(a, acc, blockIdx.x, gridDim.x, &last);
 }
 
-// The gradient of rows whose slope, frame and sum are known: one CTA a row.
+// The gradient of rows whose slope, frame and sum are known, a piece of kPiece units a
+// CTA; the last rows first, whose logits the forward pass left in L2.
+constexpr int kPieceThreads = 256;
+constexpr int kPiece = kPieceThreads * kGroup;
+
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads) backward_kernel(const __grid_constant__ RowArgs a) {
+__global__ void __launch_bounds__(kPieceThreads) backward_kernel(const __grid_constant__ RowArgs a, int pieces) {
+  constexpr int N = Vec<T>::N;
   griddep_wait();
   const int tid = threadIdx.x;
-  for (int64_t r = blockIdx.x; r < a.tokens; r += gridDim.x) {
-    const int64_t t = a.tokens - 1 - r;
+  for (int64_t r = blockIdx.x; r < a.tokens * pieces; r += gridDim.x) {
+    const int64_t t = a.tokens - 1 - r / pieces;
+    const int piece = (int)(r % pieces);
     const T* z = reinterpret_cast<const T*>(a.logits) + t * a.stride;
     T* g = reinterpret_cast<T*>(a.grad) + t * a.grad_stride;
     const bool live = a.mask == nullptr || a.mask[t] != 0;
-    const float f = live ? a.slope[t] * a.grad_scale * a.inv_temp : 0.f;
-    if (f == 0.f) {
-      for (int64_t j = tid; j < a.vocab; j += kRowThreads) Vec<T>::store(g + j, 0.f);
+    const float slope = live ? __ldcg(a.slope + t) : 0.f;
+    if (slope == 0.f) {
+      const Row row = row_of(g, a.vocab);
+      uint4* dst = reinterpret_cast<uint4*>(g + row.head);
+      for (int64_t l = (int64_t)piece * kPiece + tid; l < min((int64_t)(piece + 1) * kPiece, row.units); l += kPieceThreads)
+        dst[l] = make_uint4(0, 0, 0, 0);
+      const int64_t e = piece == 0 && tid < 16 ? edge_of(row, a.vocab, tid) : -1;
+      if (e >= 0) Vec<T>::store(g + e, 0.f);
       continue;
     }
-    const float2 fs = a.frame[t];
+    const Row row = row_of(z, a.vocab);
+    const int64_t v0 = (int64_t)piece * kPiece + tid;
+    const uint4* src = reinterpret_cast<const uint4*>(z + row.head);
+    uint4 w[kGroup];
+#pragma unroll
+    for (int k = 0; k < kGroup; ++k)
+      if (v0 + k * kPieceThreads < row.units) w[k] = src[v0 + k * kPieceThreads];
+    const float2 ms = __ldcg(a.frame + t);
     const int64_t y = a.targets[t];
-    const float at_y = -f * expm1f(a.logp[t]);
-    const float factor = -f / fs.y;
-    const float frame = fs.x * a.c;
-    const bool near = finite(frame);
-    for (int64_t j = tid; j < a.vocab; j += kRowThreads) {
-      const float e = term(Vec<T>::load(z + j), a.c, fs.x, frame, near);
-      Vec<T>::store(g + j, j == y ? at_y : factor * e);
+    const Factor f = row_factor(a, ms.x, ms.y, __ldcg(a.logp + t), slope);
+    const Expo x = exponent(a, f.m);
+    const bool whole = aligned_unit(g + row.head);
+    const int64_t unit = y >= row.head && y < row.tail ? (y - row.head) / N : -1;
+#pragma unroll
+    for (int k = 0; k < kGroup; ++k) {
+      const int64_t u = v0 + k * kPieceThreads;
+      if (u >= row.units) continue;
+      uint4 o = scaled_unit<T>(w[k], x, f.factor);
+      if (u == unit) put<T>(o, (int)((y - row.head) % N), f.at_y);
+      store_unit(g + row.head + u * N, o, whole);
     }
+    const int64_t e = piece == 0 && tid < 16 ? edge_of(row, a.vocab, tid) : -1;
+    if (e >= 0) Vec<T>::store(g + e, e == y ? f.at_y : f.factor * x.one(Vec<T>::load(z + e)));
   }
 }
 
@@ -364,7 +856,9 @@ __device__ __forceinline__ int64_t live_count(const uint8_t* mask, int64_t a, in
 
 // Weight of every position under the token mean (or the sum: 1).
 __global__ void __launch_bounds__(kSmallThreads) count_kernel(const uint8_t* mask, int64_t tokens, int mean,
-                                                              float* inv_count) {
+                                                              float* inv_count, unsigned* ticket) {
+  griddep_launch_dependents();
+  if (threadIdx.x == 0) *ticket = 0;
   float w = 1.f;
   if (mean) {
     const int64_t n = live_count(mask, 0, tokens);
@@ -376,9 +870,12 @@ __global__ void __launch_bounds__(kSmallThreads) count_kernel(const uint8_t* mas
 // Sequence mean: one CTA a sequence writes the weights of its positions; CTA n_seqs
 // clears those before the first and after the last.
 __global__ void __launch_bounds__(kSmallThreads) weight_kernel(const uint8_t* mask, int64_t tokens,
-                                                               const int64_t* offsets, int64_t n_seqs, float* weight) {
+                                                               const int64_t* offsets, int64_t n_seqs, float* weight,
+                                                               unsigned* ticket) {
+  griddep_launch_dependents();
   const int64_t q = blockIdx.x;
   if (q == n_seqs) {
+    if (threadIdx.x == 0) *ticket = 0;
     const int64_t a = clamp_offset(offsets[0], 0, tokens), b = clamp_offset(offsets[n_seqs], a, tokens);
     for (int64_t t = threadIdx.x; t < a; t += kSmallThreads) weight[t] = 0.f;
     for (int64_t t = b + threadIdx.x; t < tokens; t += kSmallThreads) weight[t] = 0.f;
@@ -389,28 +886,6 @@ __global__ void __launch_bounds__(kSmallThreads) weight_kernel(const uint8_t* ma
   const float w = 1.f / ((float)n_seqs * (float)(n < 1 ? 1 : n));
   for (int64_t t = a + threadIdx.x; t < b; t += kSmallThreads)
     weight[t] = mask == nullptr || mask[t] != 0 ? w : 0.f;
-}
-
-// stats = sum of the positions' terms.
-__global__ void __launch_bounds__(kSmallThreads) stats_kernel(const float4* terms, int64_t tokens, float* stats) {
-  griddep_wait();
-  float h[4] = {0.f, 0.f, 0.f, 0.f}, l[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int64_t t = threadIdx.x; t < tokens; t += kSmallThreads) {
-    const float4 x = terms[t];
-    const float v[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float s, e;
-      two_sum(h[i], v[i], s, e);
-      h[i] = s;
-      l[i] += isfinite(s) ? e : 0.f;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const double s = block_sum((double)h[i] + (double)l[i]);
-    if (threadIdx.x == 0) stats[i] = (float)s;
-  }
 }
 
 struct PairArgs {
@@ -441,9 +916,9 @@ __global__ void __launch_bounds__(kSmallThreads) pair_kernel(const __grid_consta
     float h = 0.f, l = 0.f;
     for (int64_t t = lo[k] + threadIdx.x; t < hi[k]; t += kSmallThreads) {
       float s, e;
-      two_sum(h, a.logp[t], s, e);  // 0 where masked
+      two_sum(h, __ldcg(a.logp + t), s, e);  // 0 where masked
       h = s;
-      l += isfinite(s) ? e : 0.f;
+      l += fabsf(s) < INFINITY ? e : 0.f;
     }
     double sum = block_sum((double)h + (double)l);
     const int64_t n = a.mean ? live_count(a.mask, lo[k], hi[k]) : 1;
@@ -490,7 +965,7 @@ int32_t check_batch(const muon_token_batch* b) {
   if (b->row_stride != 0 && (b->row_stride < b->vocab || b->row_stride > (1ll << 40)))
     return invalid("row_stride must be 0 or at least vocab");
   if (b->dtype != MUON_DTYPE_F32 && b->dtype != MUON_DTYPE_BF16) return invalid("unknown logits dtype");
-  if (!(b->temperature > 0.f) || std::isinf(b->temperature)) return invalid("temperature must be finite and > 0");
+  if (!(b->temperature >= 1e-20f && b->temperature <= 1e20f)) return invalid("temperature must be in [1e-20, 1e20]");
   if (b->tokens == 0) return MUON_OK;
   if (!b->logits || !b->targets) return invalid("logits or targets is NULL");
   if (!aligned(b->logits, b->dtype == MUON_DTYPE_BF16 ? 2 : 4) || !aligned(b->targets, 8))
@@ -532,36 +1007,133 @@ RowArgs row_args(const muon_token_batch* b) {
   a.vocab = b->vocab;
   a.stride = b->row_stride ? b->row_stride : b->vocab;
   a.grad_stride = a.vocab;
-  a.c = (float)(1.4426950408889634 / (double)b->temperature);
+  const double c = 1.4426950408889634 / (double)b->temperature;
+  a.c_hi = std::nextafterf((float)c, 0.f);
+  if ((double)a.c_hi >= c) a.c_hi = std::nextafterf(a.c_hi, 0.f);
+  a.c_lo = (float)(c - (double)a.c_hi);
   a.inv_temp = (float)(1.0 / (double)b->temperature);
   a.grad_scale = 1.f;
   return a;
 }
 
+constexpr int kMaxParts = 2048;            // partial sums of the policy loss
+constexpr size_t kSmemPerSm = 227 * 1024;  // what one CTA may have
+
+// Shape of a row kernel's launch.  cluster = 0: rows too long for shared memory.
+struct RowShape {
+  int cluster, stages, threads;
+  size_t smem;
+};
+
+size_t row_smem(int64_t units, int cluster, int stages) {
+  return (size_t)stages * (size_t)((units + cluster - 1) / cluster) * 16 + sizeof(RowShared);
+}
+
+RowShape row_shape(int64_t vocab, int32_t dtype, int64_t tokens, int sms) {
+  const int64_t per_unit = dtype == MUON_DTYPE_BF16 ? 8 : 4;
+  const int64_t units = vocab / per_unit < 1 ? 1 : vocab / per_unit;
+  RowShape s;
+  s.stages = 3;
+  s.cluster = 1;
+  while (s.cluster < kMaxCluster && row_smem(units, s.cluster, 3) > kSmemPerSm) s.cluster *= 2;
+  // few rows: more CTAs for each, while each still has some 4 KB of it
+  while (s.cluster < kMaxCluster && tokens * s.cluster * 2 <= sms && units / s.cluster >= 512) s.cluster *= 2;
+  s.smem = row_smem(units, s.cluster, s.stages);
+  if (s.smem > kSmemPerSm) {
+    s.stages = 2;
+    s.smem = row_smem(units, s.cluster, s.stages);
+  }
+  if (s.smem > kSmemPerSm) s.cluster = 0;
+  const int64_t per_cta = (units + (s.cluster ? s.cluster : 1) - 1) / (s.cluster ? s.cluster : 1);
+  const int64_t want = (per_cta + 7) / 8;  // about 8 units a thread
+  s.threads = (int)(want <= 128 ? 128 : want >= kMaxRowThreads ? kMaxRowThreads : (want + 31) / 32 * 32);
+  return s;
+}
+
+// Clusters of this kernel that the device holds at once.
+template <typename K>
+cudaError_t resident_clusters(K kernel, const RowShape& s, int* n) {
+  struct Known {
+    const void* kernel;
+    int device, cluster, threads;
+    size_t smem;
+    int n;
+  };
+  static thread_local Known known[16];
+  static thread_local int next = 0;
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  for (const Known& k : known)
+    if (k.kernel == (const void*)kernel && k.device == device && k.cluster == s.cluster && k.threads == s.threads &&
+        k.smem == s.smem) {
+      *n = k.n;
+      return cudaSuccess;
+    }
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemPerSm);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)s.cluster);
+  cfg.blockDim = dim3((unsigned)s.threads);
+  cfg.dynamicSmemBytes = s.smem;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)s.cluster;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaOccupancyMaxActiveClusters(n, kernel, &cfg);
+  if (e != cudaSuccess) return e;
+  if (*n < 1) *n = 1;
+  known[next] = Known{(const void*)kernel, device, s.cluster, s.threads, s.smem, *n};
+  next = (next + 1) % 16;
+  return cudaSuccess;
+}
+
+template <typename T, int kMode>
+cudaError_t launch_rows_as(RowArgs a, int32_t dtype, int sms, bool dependent, cudaStream_t s) {
+  const RowShape shape = row_shape(a.vocab, dtype, a.tokens, sms);
+  const int64_t rows = a.tokens < 1 ? 1 : a.tokens;
+  if (shape.cluster == 0) {
+    const int grid = (int)(rows < 4ll * sms ? rows : 4ll * sms < kMaxParts ? 4ll * sms : kMaxParts);
+    return launch(wide_row_kernel<T, kMode>, grid, kMaxRowThreads, 0, s, 1, dependent, a);
+  }
+  a.cluster = shape.cluster;
+  a.stage_vecs = (int32_t)((shape.smem - sizeof(RowShared)) / 16 / shape.stages);
+  auto kernel = shape.stages == 3 ? row_kernel<T, kMode, 3> : row_kernel<T, kMode, 2>;
+  int n = 0;
+  const cudaError_t e = resident_clusters(kernel, shape, &n);
+  if (e != cudaSuccess) return e;
+  if (n > kMaxParts) n = kMaxParts;
+  if (n > rows) n = (int)rows;
+  return launch(kernel, n * shape.cluster, shape.threads, shape.smem, s, shape.cluster, dependent, a);
+}
+
 template <int kMode>
 cudaError_t launch_rows(const RowArgs& a, int32_t dtype, int sms, bool dependent, cudaStream_t s) {
-  if (a.tokens == 0) return cudaSuccess;
-  const int grid = (int)(a.tokens < 4ll * sms ? a.tokens : 4ll * sms);
-  return dtype == MUON_DTYPE_BF16
-             ? launch(row_kernel<__nv_bfloat16, kMode>, grid, kRowThreads, 0, s, 1, dependent, a)
-             : launch(row_kernel<float, kMode>, grid, kRowThreads, 0, s, 1, dependent, a);
+  return dtype == MUON_DTYPE_BF16 ? launch_rows_as<__nv_bfloat16, kMode>(a, dtype, sms, dependent, s)
+                                  : launch_rows_as<float, kMode>(a, dtype, sms, dependent, s);
 }
 
 cudaError_t launch_backward(const RowArgs& a, int32_t dtype, int sms, cudaStream_t s) {
   if (a.tokens == 0) return cudaSuccess;
-  const int grid = (int)(a.tokens < 4ll * sms ? a.tokens : 4ll * sms);
-  return dtype == MUON_DTYPE_BF16 ? launch(backward_kernel<__nv_bfloat16>, grid, kRowThreads, 0, s, 1, true, a)
-                                  : launch(backward_kernel<float>, grid, kRowThreads, 0, s, 1, true, a);
+  const int64_t units = a.vocab / (dtype == MUON_DTYPE_BF16 ? 8 : 4);
+  const int pieces = (int)((units < 1 ? 1 : units) + kPiece - 1) / kPiece;
+  const int64_t all = a.tokens * pieces;
+  const int grid = (int)(all < 8ll * sms ? all : 8ll * sms);
+  return dtype == MUON_DTYPE_BF16 ? launch(backward_kernel<__nv_bfloat16>, grid, kPieceThreads, 0, s, 1, true, a, pieces)
+                                  : launch(backward_kernel<float>, grid, kPieceThreads, 0, s, 1, true, a, pieces);
 }
 
-// Workspace of the losses: per position 16 bytes (terms; or frame, slope and logp),
-// 4 more for a weight, and 4 for each sequence.
+// Workspace of the losses.
 size_t round16(size_t v) { return (v + 15) / 16 * 16; }
 
 struct LossSpace {
-  float4* terms;
+  float* inv_count;
+  unsigned* ticket;
+  double* partials;
   float2* frame;
-  float *slope, *logp, *weight, *inv_count, *pair_loss;
+  float *slope, *logp, *weight, *pair_loss;
   size_t bytes;
 };
 
@@ -569,14 +1141,19 @@ LossSpace loss_space(void* ws, int64_t tokens, int64_t n_seqs) {
   uint8_t* p = static_cast<uint8_t*>(ws);
   LossSpace s;
   size_t off = 0;
-  s.inv_count = reinterpret_cast<float*>(p + off); off += 16;
-  s.terms = reinterpret_cast<float4*>(p + off);
-  s.frame = reinterpret_cast<float2*>(p + off);
-  s.slope = reinterpret_cast<float*>(p + off + 8 * (size_t)tokens);
-  s.logp = reinterpret_cast<float*>(p + off + 12 * (size_t)tokens);
-  off += 16 * (size_t)tokens;
-  s.weight = reinterpret_cast<float*>(p + off); off += round16(4 * (size_t)tokens);
-  s.pair_loss = reinterpret_cast<float*>(p + off); off += round16(4 * (size_t)n_seqs);
+  auto take = [&](size_t bytes) {
+    uint8_t* at = p + off;
+    off += round16(bytes);
+    return static_cast<void*>(at);
+  };
+  s.inv_count = static_cast<float*>(take(4));
+  s.ticket = static_cast<unsigned*>(take(4));
+  s.partials = static_cast<double*>(take((size_t)kMaxParts * 4 * sizeof(double)));
+  s.frame = static_cast<float2*>(take(8 * (size_t)tokens));
+  s.slope = static_cast<float*>(take(4 * (size_t)tokens));
+  s.logp = static_cast<float*>(take(4 * (size_t)tokens));
+  s.weight = static_cast<float*>(take(4 * (size_t)tokens));
+  s.pair_loss = static_cast<float*>(take(4 * (size_t)n_seqs));
   s.bytes = off;
   return s;
 }
@@ -654,10 +1231,10 @@ muon_status muon_policy_loss(const muon_token_batch* batch, const muon_policy_co
   cudaError_t e;
   if (by_seq)
     e = launch(weight_kernel, (int)n_seqs + 1, kSmallThreads, 0, s, 1, false, batch->mask, (int64_t)batch->tokens,
-               seq_offsets, (int64_t)n_seqs, ws.weight);
+               seq_offsets, (int64_t)n_seqs, ws.weight, ws.ticket);
   else
     e = launch(count_kernel, 1, kSmallThreads, 0, s, 1, false, batch->mask, (int64_t)batch->tokens,
-               (int)(c.reduction == MUON_REDUCE_TOKEN_MEAN), ws.inv_count);
+               (int)(c.reduction == MUON_REDUCE_TOKEN_MEAN), ws.inv_count, ws.ticket);
   if (e != cudaSuccess) return cuda_error(e);
   RowArgs a = row_args(batch);
   a.logp = logp;
@@ -672,9 +1249,10 @@ muon_status muon_policy_loss(const muon_token_batch* batch, const muon_policy_co
   a.grad_scale = c.grad_scale;
   a.grad = grad;
   if (grad_stride) a.grad_stride = grad_stride;
-  a.terms = ws.terms;
-  if ((e = launch_rows<kPolicy>(a, batch->dtype, sms, true, s)) != cudaSuccess) return cuda_error(e);
-  e = launch(stats_kernel, 1, kSmallThreads, 0, s, 1, true, (const float4*)ws.terms, (int64_t)batch->tokens, stats);
+  a.partials = ws.partials;
+  a.ticket = ws.ticket;
+  a.stats = stats;
+  e = launch_rows<kPolicy>(a, batch->dtype, sms, true, s);
   return e == cudaSuccess ? MUON_OK : cuda_error(e);
 }
 
@@ -709,8 +1287,9 @@ muon_status muon_preference_loss(const muon_token_batch* batch, const muon_prefe
   a.grad_scale = c.grad_scale;
   a.grad = grad;
   if (grad_stride) a.grad_stride = grad_stride;
-  cudaError_t e = launch_rows<kForward>(a, batch->dtype, sms, false, s);
-  if (e != cudaSuccess) return cuda_error(e);
+  cudaError_t e;
+  if (batch->tokens > 0 && (e = launch_rows<kForward>(a, batch->dtype, sms, false, s)) != cudaSuccess)
+    return cuda_error(e);
   if (n_pairs > 0) {
     PairArgs p;
     p.mask = batch->mask;
