@@ -61,7 +61,7 @@ struct RowArgs {
   unsigned* ticket;       // zeroed by the kernel before
   float* stats;
   // shape of the launch
-  int32_t cluster;        // CTAs a row
+  int32_t log_cluster;    // 2^log_cluster CTAs a row
   int32_t stage_vecs;     // 16-byte units of one ring stage
 };
 
@@ -322,23 +322,23 @@ __device__ __forceinline__ Outcome policy_terms(const RowArgs& a, const Position
 // ---------------------------------------------------------------------------
 // The 16-byte units that lie whole in a row, and the elements around them.
 struct Row {
-  int64_t head;  // elements before the first unit
-  int64_t units;
-  int64_t tail;  // first element after the last unit
+  int head;  // elements before the first unit
+  int units;
+  int tail;  // first element after the last unit
 };
 
 template <typename T>
 __device__ __forceinline__ Row row_of(const T* z, int64_t vocab) {
   Row r;
-  r.head = min(vocab, (int64_t)(((16 - (reinterpret_cast<uint64_t>(z) & 15)) & 15) / sizeof(T)));
-  r.units = (vocab - r.head) / Vec<T>::N;
+  r.head = min((int)vocab, (int)((-reinterpret_cast<uint64_t>(z) & 15) / sizeof(T)));
+  r.units = (int)(vocab - r.head) / Vec<T>::N;
   r.tail = r.head + r.units * Vec<T>::N;
   return r;
 }
 
 // The element of a row that lane `lane` of its edge warp looks after, or -1: lanes 0-7
 // those before the first unit, 8-15 those after the last.
-__device__ __forceinline__ int64_t edge_of(const Row& r, int64_t vocab, int lane) {
+__device__ __forceinline__ int edge_of(const Row& r, int64_t vocab, int lane) {
   if (lane < 8) return lane < r.head ? lane : -1;
   return lane < 16 && r.tail + lane - 8 < vocab ? r.tail + lane - 8 : -1;
 }
@@ -356,15 +356,6 @@ __device__ __forceinline__ uint4 scaled_unit(const uint4& w, const Expo& x, floa
     v[i + 1] = r.y;
   }
   return Vec<T>::pack(v);
-}
-
-template <typename T>
-__device__ __forceinline__ void put(uint4& w, int e, float v) {
-  float u[Vec<T>::N];
-  Vec<T>::unpack(w, u);
-#pragma unroll
-  for (int i = 0; i < Vec<T>::N; ++i) u[i] = i == e ? v : u[i];
-  w = Vec<T>::pack(u);
 }
 
 // A unit of the gradient: one store where the gradient's row is aligned as the logits'
@@ -386,30 +377,28 @@ __device__ __forceinline__ bool aligned_unit(const T* g) {
   return (reinterpret_cast<uint64_t>(g) & 15) == 0;
 }
 
-constexpr int kMaxRowThreads = 512;
-constexpr int kMaxRowWarps = kMaxRowThreads / 32;
+constexpr int kMaxRowThreads = 512;                   // that hold a row's units
+constexpr int kMaxRowWarps = kMaxRowThreads / 32 + 1;  // and the finishing warp
 constexpr int kMaxCluster = 8;
 constexpr int kBatch = 256;  // rows whose scalars a CTA holds at a time
+constexpr int kSlots = 4;    // rows whose partial sums may be on their way
 constexpr int kGroup = 4;    // 16-byte units a thread takes at a time
 
 // Shared memory beside the ring.
 struct RowShared {
-  Sum slot[2][kMaxCluster][kMaxRowWarps];  // partial sums of a row, from every warp of the cluster
-  Factor factor[2];
+  uint64_t full[kSlots];                        // a slot has every partial sum of its row
+  Sum slot[kSlots][kMaxCluster][kMaxRowWarps];  // partial sums of a row, from every warp of the cluster
+  Factor factor[kSlots];                        // by the row's slot
   int32_t row[kBatch];      // live rows from the front, masked rows from the back (offset in the batch)
   int32_t unit[kBatch];     // the target's unit in this CTA's part; -1: elsewhere
-  int32_t elem[kBatch];     // its element in the unit; or, with unit = -2, the edge lane that has it
+  int32_t elem[kBatch];     // its element there + 16 times the thread that has it; with unit = -2 the edge lane
   float zy[kBatch];
   float old_logp[kBatch], ref[kBatch], adv[kBatch], w[kBatch];
-  int32_t live[kBatch / 32];
+  uint32_t live[kBatch / 32];
   int32_t last;
 };
 
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-// Barriers 1 and 2 (by the row's parity): warp 0 has written a row's factor.
+// Barriers 1 and 2 (by the row's parity): the finishing warp has written a row's factor.
 __device__ __forceinline__ void factor_sync(int par, uint32_t count) {
   if (par) asm volatile("bar.sync 2, %0;" ::"r"(count) : "memory");
   else asm volatile("bar.sync 1, %0;" ::"r"(count) : "memory");
@@ -419,8 +408,18 @@ __device__ __forceinline__ void factor_arrive(int par, uint32_t count) {
   else asm volatile("bar.arrive 1, %0;" ::"r"(count) : "memory");
 }
 
-__device__ __forceinline__ void store_remote(Sum* p, uint32_t rank, const Sum& v) {
-  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(mapa_shared(p, rank)), "f"(v.m), "f"(v.s) : "memory");
+// Writes a partial sum to a slot of CTA `rank` of the cluster and counts it there.  The
+// asynchronous store belongs to cluster launches; a CTA alone writes its own memory.
+__device__ __forceinline__ void send(Sum* slot, uint64_t* full, int ncta, uint32_t rank, const Sum& v) {
+  if (ncta == 1) {
+    *slot = v;
+    mbar_arrive(full);
+    return;
+  }
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(
+                   mapa_shared(slot, rank)),
+               "r"(__float_as_uint(v.m)), "r"(__float_as_uint(v.s)), "r"(mapa_shared(full, rank))
+               : "memory");
 }
 
 // Sums of rows' terms, carried with their rounding errors.
@@ -438,10 +437,10 @@ struct Terms {
   }
 };
 
-// Thread 0's sums into the partials; the last of `n` to come adds all of them, in their order.
+// The last warp's sums into the partials; the last of `n` to come adds all of them, in their order.
 __device__ __forceinline__ void finish_stats(const RowArgs& a, const Terms& acc, int64_t part, int64_t n, int32_t* last) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == blockDim.x - 32) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) a.partials[4 * part + k] = (double)acc.hi[k] + (double)acc.lo[k];
     __threadfence();
@@ -462,67 +461,80 @@ __device__ __forceinline__ void finish_stats(const RowArgs& a, const Terms& acc,
 // the sum and the gradient, so that every logit is read from HBM once.  Each thread copies
 // its own 16-byte units into a ring of kStages rows (cp.async) and is the only one to read
 // them, so that only the sums cross threads: every warp writes its partial sum to all CTAs
-// of the cluster and warp 0 of each forms the row's result.  While a row's sums travel, the
-// other warps write the gradient of the row before; its stage then takes the row
-// kStages - 1 further on.
+// of the cluster, and a warp of each CTA that holds no units forms the row's result from
+// them.  While it does, the others write the gradient of the row before, whose stage then
+// takes the row kStages - 1 further on, and sum the next row.
+//
+// The sums travel as asynchronous stores that count on a barrier of the receiver, so that no
+// store of a gradient is waited for.  A warp sends row i after it has had the result of row
+// i - 2 from its own CTA's finishing warp; that took the sums of row i - 2 from every CTA,
+// which were sent after the results of row i - 4 there: slot i - 4 = i mod kSlots has been
+// read in every CTA.
 template <typename T, int kMode, int kStages>
-__global__ void __launch_bounds__(kMaxRowThreads) row_kernel(const __grid_constant__ RowArgs a) {
+__global__ void __launch_bounds__(kMaxRowThreads + 32) row_kernel(const __grid_constant__ RowArgs a) {
   constexpr int N = Vec<T>::N;
   extern __shared__ __align__(16) uint4 ring[];
   RowShared& sh = *reinterpret_cast<RowShared*>(ring + (size_t)kStages * a.stage_vecs);
-  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = nt >> 5;
-  const int ncta = a.cluster;
+  const int tid = threadIdx.x, all = blockDim.x, nt = all - 32, lane = tid & 31, warp = tid >> 5, warps = all >> 5;
+  const int ncta = 1 << a.log_cluster;
   const int rank = ncta > 1 ? (int)cluster_ctarank() : 0;
-  const int64_t cid = blockIdx.x / ncta, n_clusters = gridDim.x / ncta;
+  const int64_t cid = blockIdx.x >> a.log_cluster, n_clusters = gridDim.x >> a.log_cluster;
   const bool has_grad = kMode == kPolicy && a.grad != nullptr;
-  const bool edge_warp = rank == 0 && warp == 1;
+  const bool finisher = warp == warps - 1;
   const T* const logits = reinterpret_cast<const T*>(a.logits);
   T* const grads = reinterpret_cast<T*>(a.grad);
-  Terms acc;  // of warp 0
+  Terms acc;  // of the finishing warp
+
+  auto part_of = [&](const Row& row, int& v0) {  // this CTA's units of a row
+    const int per = (row.units + ncta - 1) >> a.log_cluster;
+    v0 = rank * per;
+    return max(0, min(per, row.units - v0));
+  };
 
   griddep_launch_dependents();
-  bool waited = false;
+  bool waited = false, arrived = true;
+  int64_t done = 0;  // rows summed in earlier batches
+  // a cluster's sums are counted in bytes, one CTA's (no cluster launch) in arrivals
+  if (tid < kSlots) mbar_init(&sh.full[tid], ncta > 1 ? 1 : warps);
+  fence_mbarrier_init();
+  cluster_sync();
   const int64_t my_rows = a.tokens > cid ? (a.tokens - cid + n_clusters - 1) / n_clusters : 0;
   for (int64_t first = 0; first < my_rows; first += kBatch) {
     const int rows = (int)min((int64_t)kBatch, my_rows - first);
     const int64_t t0 = cid + first * n_clusters;  // row r of the batch is t0 + r n_clusters
     // live rows in order from the front of sh.row, the others from its back
-    for (int r = tid; r < kBatch; r += nt) {
+    for (int r = tid; r < (kBatch + all - 1) / all * all; r += all) {
       const bool live = r < rows && (a.mask == nullptr || a.mask[t0 + r * n_clusters] != 0);
       const unsigned bits = __ballot_sync(0xFFFFFFFFu, live);
-      if (lane == 0) sh.live[r >> 5] = (int32_t)bits;
+      if (lane == 0 && r < kBatch) sh.live[r >> 5] = bits;
     }
     __syncthreads();
     int n = 0;
 #pragma unroll
-    for (int k = 0; k < kBatch / 32; ++k) n += __popc((unsigned)sh.live[k]);
-    for (int r = tid; r < rows; r += nt) {
-      int before = __popc((unsigned)sh.live[r >> 5] & ((1u << (r & 31)) - 1));
-      for (int k = 0; k < (r >> 5); ++k) before += __popc((unsigned)sh.live[k]);
-      const bool live = ((unsigned)sh.live[r >> 5] >> (r & 31)) & 1;
+    for (int k = 0; k < kBatch / 32; ++k) n += __popc(sh.live[k]);
+    for (int r = tid; r < rows; r += all) {
+      int before = __popc(sh.live[r >> 5] & ((1u << (r & 31)) - 1));
+      for (int k = 0; k < (r >> 5); ++k) before += __popc(sh.live[k]);
+      const bool live = (sh.live[r >> 5] >> (r & 31)) & 1;
       sh.row[live ? before : rows - 1 - (r - before)] = r;
     }
     __syncthreads();
 
-    auto part_of = [&](const Row& row, int64_t& v0) {  // this CTA's units of a row
-      const int64_t per = (row.units + ncta - 1) / ncta;
-      v0 = rank * per;
-      return (int)max((int64_t)0, min(per, row.units - v0));
-    };
-    // Starts the copy of live row i; the edge warp's lanes get their elements of it.
-    auto issue = [&](int i) {
+    // Starts the copy of live row i; the finishing warp's lanes get their elements of it.
+    auto issue = [&](int i, int stage) {
       float e = -INFINITY;
       if (i < n) {
         const T* z = logits + (t0 + sh.row[i] * n_clusters) * a.stride;
         const Row row = row_of(z, a.vocab);
-        int64_t v0;
-        const int cnt = part_of(row, v0);
-        const uint4* src = reinterpret_cast<const uint4*>(z + row.head) + v0;
-        uint4* dst = ring + (size_t)(i % kStages) * a.stage_vecs;
-        for (int l = tid; l < cnt; l += nt) cp_async_16(dst + l, src + l);
-        if (edge_warp) {
-          const int64_t at = edge_of(row, a.vocab, lane);
+        if (finisher) {
+          const int at = rank == 0 ? edge_of(row, a.vocab, lane) : -1;
           if (at >= 0) e = Vec<T>::load(z + at);
+        } else {
+          int v0;
+          const int cnt = part_of(row, v0);
+          const uint4* src = reinterpret_cast<const uint4*>(z + row.head) + v0;
+          uint4* dst = ring + (size_t)stage * a.stage_vecs;
+          for (int l = tid; l < cnt; l += nt) cp_async_16(dst + l, src + l);
         }
       }
       cp_async_commit();
@@ -531,26 +543,28 @@ __global__ void __launch_bounds__(kMaxRowThreads) row_kernel(const __grid_consta
     float edge[kStages];  // of rows i - 1, i, i + 1, ...
     edge[0] = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) edge[i + 1] = issue(i);
+    for (int i = 0; i < kStages - 1; ++i) edge[i + 1] = issue(i, i);
 
     // the scalars of the batch's live rows
-    for (int i = tid; i < n; i += nt) {
+    for (int i = tid; i < n; i += all) {
       const int64_t t = t0 + sh.row[i] * n_clusters;
       const T* z = logits + t * a.stride;
       const int64_t y = a.targets[t];
       const bool in = y >= 0 && y < a.vocab;
       sh.zy[i] = in ? Vec<T>::load(z + y) : NAN;
       const Row row = row_of(z, a.vocab);
-      int64_t v0;
+      int v0;
       const int cnt = part_of(row, v0);
-      int32_t unit = -1, elem = 0;
+      int unit = -1, elem = 0;
       if (in && y >= row.head && y < row.tail) {
-        const int64_t u = (y - row.head) / N - v0;
-        if (u >= 0 && u < cnt) unit = (int32_t)u;
-        elem = (int32_t)((y - row.head) % N);
+        const int u = ((int)y - row.head) / N - v0;
+        if (u >= 0 && u < cnt) {
+          unit = u;
+          elem = ((int)y - row.head) % N + 16 * (u % nt);
+        }
       } else if (in) {
         unit = -2;
-        elem = (int32_t)(y < row.head ? y : 8 + y - row.tail);
+        elem = (int)(y < row.head ? y : 8 + y - row.tail);
       }
       sh.unit[i] = unit;
       sh.elem[i] = elem;
@@ -565,7 +579,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) row_kernel(const __grid_consta
       waited = true;
     }
     if (kMode == kPolicy)
-      for (int i = tid; i < n; i += nt) sh.w[i] = a.weight ? __ldcg(a.weight + t0 + sh.row[i] * n_clusters) : __ldcg(a.inv_count);
+      for (int i = tid; i < n; i += all) sh.w[i] = a.weight ? __ldcg(a.weight + t0 + sh.row[i] * n_clusters) : __ldcg(a.inv_count);
     // masked rows
     for (int i = n; i < rows; ++i) {
       const int64_t t = t0 + sh.row[i] * n_clusters;
@@ -576,128 +590,146 @@ __global__ void __launch_bounds__(kMaxRowThreads) row_kernel(const __grid_consta
       if (!has_grad) continue;
       T* g = grads + t * a.grad_stride;
       const Row row = row_of(g, a.vocab);
-      int64_t v0;
-      const int cnt = part_of(row, v0);
-      uint4* dst = reinterpret_cast<uint4*>(g + row.head) + v0;
-      for (int l = tid; l < cnt; l += nt) dst[l] = make_uint4(0, 0, 0, 0);
-      if (edge_warp) {
-        const int64_t e = edge_of(row, a.vocab, lane);
+      if (finisher) {
+        const int e = rank == 0 ? edge_of(row, a.vocab, lane) : -1;
         if (e >= 0) Vec<T>::store(g + e, 0.f);
+      } else {
+        int v0;
+        const int cnt = part_of(row, v0);
+        uint4* dst = reinterpret_cast<uint4*>(g + row.head) + v0;
+        for (int l = tid; l < cnt; l += nt) dst[l] = make_uint4(0, 0, 0, 0);
       }
     }
     __syncthreads();
 
-    for (int i = 0; i <= n; ++i) {
-      const int par = i & 1;
-      if (i < n) {
-        // the row's sum without its target: this thread's part, then the warp's
-        cp_async_wait<kStages - 2>();
-        const T* z = logits + (t0 + sh.row[i] * n_clusters) * a.stride;
-        const Row row = row_of(z, a.vocab);
-        int64_t v0;
-        const int cnt = part_of(row, v0);
-        const uint4* src = ring + (size_t)(i % kStages) * a.stage_vecs;
-        const int unit = sh.unit[i], elem = sh.elem[i];
+    if (finisher) {
+      for (int i = 0; i < n; ++i) {
+        const int par = i & 1;
+        const int64_t pos = t0 + sh.row[i] * n_clusters;
+        // the row's elements outside whole units are this warp's part of the sum
+        const bool at_edge = sh.unit[i] == -2 && sh.elem[i] == lane;
         Sum t{-INFINITY, 0.f};
-        for (int l = tid; l < cnt; l += kGroup * nt) {
-          uint4 w[kGroup];
-#pragma unroll
-          for (int g = 0; g < kGroup; ++g) {
-            const int j = l + g * nt;
-            w[g] = j < cnt ? src[j] : make_uint4(Vec<T>::kLowest, Vec<T>::kLowest, Vec<T>::kLowest, Vec<T>::kLowest);
-            if (j == unit) Vec<T>::drop(w[g], elem);
-          }
-          add_units<T>(a, t, w);
-        }
-        if (edge_warp && !(unit == -2 && elem == lane)) add_value(a, t, edge[1]);
+        if (!at_edge) add_value(a, t, edge[1]);
         t = warp_merge(a, t);
-        if (i > 0 && warp != 0) cluster_wait();  // row i - 1's sums are everywhere: its slots' twins are free
-        if (lane < ncta) store_remote(&sh.slot[par][rank][warp], lane, t);
+        const int slot = (int)((done + i) % kSlots);
+        if (ncta > 1 && lane == 0) mbar_arrive_expect_tx(&sh.full[slot], ncta * warps * (uint32_t)sizeof(Sum));
+        if (lane < ncta) send(&sh.slot[slot][rank][warp], &sh.full[slot], ncta, lane, t);
         __syncwarp();
-        cluster_arrive();
-      } else if (i > 0 && warp != 0) {
-        cluster_wait();
-      }
-      if (i > 0 && has_grad) {
-        // the gradient of the row before
-        const int64_t t = t0 + sh.row[i - 1] * n_clusters;
-        const Row row = row_of(logits + t * a.stride, a.vocab);
-        int64_t v0;
-        const int cnt = part_of(row, v0);
-        const uint4* src = ring + (size_t)((i - 1) % kStages) * a.stage_vecs;
-        T* g = grads + t * a.grad_stride;
-        T* dst = g + row.head + v0 * N;
-        const bool whole = aligned_unit(g + row.head);
-        const int unit = sh.unit[i - 1], elem = sh.elem[i - 1];
-        if (warp != 0) factor_sync(par ^ 1, nt);  // warp 0 has put the factor there
-        const Factor f = sh.factor[par ^ 1];
-        const Expo x = exponent(a, f.m);
-        for (int l = tid; l < cnt; l += nt) {
-          uint4 w = scaled_unit<T>(src[l], x, f.factor);
-          if (l == unit) put<T>(w, elem, f.at_y);
-          store_unit(dst + (int64_t)l * N, w, whole);
+        arrived = arrived && mbar_wait(&sh.full[slot], (uint32_t)((done + i) / kSlots) & 1, nullptr, nullptr);
+        arrived = __all_sync(0xFFFFFFFFu, arrived);
+        // every warp of every CTA, in the same order in each
+        t = Sum{-INFINITY, 0.f};
+        for (int k = lane; k < ncta * kMaxRowWarps; k += 32)
+          if (k % kMaxRowWarps < warps) t = merge(a, t, sh.slot[slot][k / kMaxRowWarps][k % kMaxRowWarps]);
+        t = warp_merge(a, t);
+        if (!arrived) t.s = NAN;  // a wait ran out: the results say so
+        const Prob p = row_prob(a, t, sh.zy[i]);
+        const bool writer = rank == 0 && lane == 0;
+        if (writer && a.logp) a.logp[pos] = p.logp;
+        if (kMode == kForward && writer) {
+          a.frame[pos] = make_float2(t.m, p.s);
+          a.slope[pos] = 0.f;
         }
-        if (edge_warp) {
-          const int64_t e = edge_of(row, a.vocab, lane);
-          if (e >= 0) Vec<T>::store(g + e, unit == -2 && elem == lane ? f.at_y : f.factor * x.one(edge[0]));
-        }
-      }
-      if (i < n) {
-        if (warp == 0) {
-          __syncwarp();
-          cluster_wait();
-          // the row's sum: every warp of every CTA, in the same order in each
-          Sum t{-INFINITY, 0.f};
-          for (int k = lane; k < ncta * warps; k += 32) t = merge(a, t, sh.slot[par][k / warps][k % warps]);
-          t = warp_merge(a, t);
-          const Prob p = row_prob(a, t, sh.zy[i]);
-          const int64_t pos = t0 + sh.row[i] * n_clusters;
-          const bool writer = rank == 0 && lane == 0;
-          if (writer && a.logp) a.logp[pos] = p.logp;
-          if (kMode == kForward && writer) {
-            a.frame[pos] = make_float2(t.m, p.s);
-            a.slope[pos] = 0.f;
-          }
-          if (kMode == kPolicy) {
-            const Position at{sh.old_logp[i], sh.ref[i], sh.adv[i], sh.w[i]};
-            const Outcome o = policy_terms(a, at, p.logp);
-            if (has_grad && lane == 0) sh.factor[par] = row_factor(a, t.m, p.s, p.logp, o.slope);
-            acc.add(o.terms);
-          }
+        if (kMode == kPolicy) {
+          const Position at{sh.old_logp[i], sh.ref[i], sh.adv[i], sh.w[i]};
+          const Outcome o = policy_terms(a, at, p.logp);
+          acc.add(o.terms);
           if (has_grad) {
+            const Factor f = row_factor(a, t.m, p.s, p.logp, o.slope);
+            if (lane == 0) sh.factor[slot] = f;
+            T* g = grads + pos * a.grad_stride;
+            const int e = rank == 0 ? edge_of(row_of(logits + pos * a.stride, a.vocab), a.vocab, lane) : -1;
             __syncwarp();
-            factor_arrive(par, nt);
+            factor_arrive(par, all);
+            if (e >= 0) Vec<T>::store(g + e, at_edge ? f.at_y : f.factor * exponent(a, f.m).one(edge[1]));
           }
         }
+        if (!has_grad) factor_arrive(par, all);  // the other warps keep the row's distance all the same
 #pragma unroll
         for (int k = 0; k + 1 < kStages; ++k) edge[k] = edge[k + 1];
-        edge[kStages - 1] = issue(i + kStages - 1);
+        edge[kStages - 1] = issue(i + kStages - 1, 0);
+      }
+    } else {
+      int stage = 0, before = kStages - 1;  // of rows i and i - 1
+      for (int i = 0; i <= n; ++i) {
+        if (i < n) {
+          // the row's sum without its target: this thread's part, then the warp's
+          cp_async_wait<kStages - 2>();
+          const Row row = row_of(logits + (t0 + sh.row[i] * n_clusters) * a.stride, a.vocab);
+          int v0;
+          const int cnt = part_of(row, v0);
+          uint4* src = ring + (size_t)stage * a.stage_vecs;
+          const int unit = sh.unit[i], elem = sh.elem[i];
+          if (unit >= 0 && elem >> 4 == tid) {  // the target leaves the sum
+            uint4 w = src[unit];
+            Vec<T>::drop(w, elem & 15);
+            src[unit] = w;
+          }
+          Sum t{-INFINITY, 0.f};
+          for (int l = tid; l < cnt; l += kGroup * nt) {
+            uint4 w[kGroup];
+#pragma unroll
+            for (int g = 0; g < kGroup; ++g) {
+              const int j = l + g * nt;
+              w[g] = j < cnt ? src[j] : make_uint4(Vec<T>::kLowest, Vec<T>::kLowest, Vec<T>::kLowest, Vec<T>::kLowest);
+            }
+            add_units<T>(a, t, w);
+          }
+          t = warp_merge(a, t);
+          const int slot = (int)((done + i) % kSlots);
+          if (lane < ncta) send(&sh.slot[slot][rank][warp], &sh.full[slot], ncta, lane, t);
+        }
+        if (i > 0 && !has_grad) factor_sync((i - 1) & 1, all);
+        if (i > 0 && has_grad) {
+          // the gradient of the row before
+          const int64_t t = t0 + sh.row[i - 1] * n_clusters;
+          const Row row = row_of(logits + t * a.stride, a.vocab);
+          int v0;
+          const int cnt = part_of(row, v0);
+          const uint4* src = ring + (size_t)before * a.stage_vecs;
+          T* g = grads + t * a.grad_stride + row.head;
+          const bool whole = aligned_unit(g);
+          g += (int64_t)v0 * N;
+          factor_sync((i - 1) & 1, all);
+          const Factor f = sh.factor[(done + i - 1) % kSlots];
+          const Expo x = exponent(a, f.m);
+          for (int l = tid; l < cnt; l += nt) store_unit(g + (int64_t)l * N, scaled_unit<T>(src[l], x, f.factor), whole);
+          const int unit = sh.unit[i - 1], elem = sh.elem[i - 1];
+          if (unit >= 0 && elem >> 4 == tid) Vec<T>::store(g + (int64_t)unit * N + (elem & 15), f.at_y);
+        }
+        if (i < n) issue(i + kStages - 1, before);
+        before = stage;
+        stage = stage + 1 == kStages ? 0 : stage + 1;
       }
     }
     // the batch's scalars are free, and so are its slots in every CTA of the cluster
+    done += n;
     __syncwarp();
-    cluster_arrive();
-    cluster_wait();
+    cluster_sync();
   }
   if (!waited) griddep_wait();
   if (kMode == kPolicy && rank == 0) finish_stats(a, acc, cid, n_clusters, &sh.last);
 }
 
-// Rows too long for a cluster's shared memory: one CTA a row, which it reads twice where
-// it writes the gradient.
+// Rows straight from memory, one CTA a row: where nothing is written back a row need not
+// stay on chip, and many CTAs an SM hide a row's end behind others' loads.  A different warp
+// forms each row's result while the others go on to the next.  With a gradient (rows too
+// long for a cluster's shared memory) the row is read a second time.
 template <typename T, int kMode>
-__global__ void __launch_bounds__(kMaxRowThreads) wide_row_kernel(const __grid_constant__ RowArgs a) {
-  constexpr int N = Vec<T>::N, nt = kMaxRowThreads;
-  __shared__ Sum red[kMaxRowWarps];
+__global__ void __launch_bounds__(kMaxRowThreads) stream_kernel(const __grid_constant__ RowArgs a) {
+  constexpr int N = Vec<T>::N;
+  __shared__ Sum red[2][kMaxRowThreads / 32];
+  __shared__ Factor factor;
   __shared__ int32_t last;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  Terms acc;
+  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = nt >> 5;
+  const bool has_grad = kMode == kPolicy && a.grad != nullptr;
+  Terms acc;  // of the last warp
+  int turn = 0;
   griddep_launch_dependents();
   griddep_wait();
   for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
     const T* z = reinterpret_cast<const T*>(a.logits) + t * a.stride;
     T* g = reinterpret_cast<T*>(a.grad) + t * a.grad_stride;
-    const bool has_grad = kMode == kPolicy && a.grad != nullptr;
     if (a.mask != nullptr && a.mask[t] == 0) {
       if (tid == 0 && a.logp) a.logp[t] = 0.f;
       if (kMode == kForward && tid == 0) a.slope[t] = 0.f;
@@ -705,57 +737,65 @@ __global__ void __launch_bounds__(kMaxRowThreads) wide_row_kernel(const __grid_c
         for (int64_t j = tid; j < a.vocab; j += nt) Vec<T>::store(g + j, 0.f);
       continue;
     }
-    const Row row = row_of(z, a.vocab);
-    const uint4* src = reinterpret_cast<const uint4*>(z + row.head);
     const int64_t y = a.targets[t];
     const bool in = y >= 0 && y < a.vocab;
-    const float zy = in ? Vec<T>::load(z + y) : NAN;
-    const int64_t unit = in && y >= row.head && y < row.tail ? (y - row.head) / N : -1;
-    const int elem = (int)((y - row.head) % N);
-    const int64_t edge = tid < 16 ? edge_of(row, a.vocab, tid) : -1;
-    const float zedge = edge >= 0 ? Vec<T>::load(z + edge) : -INFINITY;
+    const Row row = row_of(z, a.vocab);
+    const uint4* src = reinterpret_cast<const uint4*>(z + row.head);
+    const int unit = in && y >= row.head && y < row.tail ? ((int)y - row.head) / N : -1;
+    const int elem = ((int)y - row.head) % N;
+    // the unit is the target_k-th of the kGroup that its thread takes from target_l on
+    const int target_l = unit >= 0 && unit % nt == tid ? unit - unit / nt % kGroup * nt : -1;
+    const int target_k = unit / nt % kGroup;
+    const int edge = tid < 16 ? edge_of(row, a.vocab, tid) : -1;
     Sum s{-INFINITY, 0.f};
-    for (int64_t l = tid; l < row.units; l += kGroup * nt) {
+    for (int l = tid; l < row.units; l += kGroup * nt) {
       uint4 w[kGroup];
 #pragma unroll
       for (int k = 0; k < kGroup; ++k) {
-        const int64_t u = l + k * nt;
-        w[k] = u < row.units ? src[u] : make_uint4(Vec<T>::kLowest, Vec<T>::kLowest, Vec<T>::kLowest, Vec<T>::kLowest);
-        if (u == unit) Vec<T>::drop(w[k], elem);
+        const int u = l + k * nt;
+        w[k] = u < row.units ? __ldg(src + u) : make_uint4(Vec<T>::kLowest, Vec<T>::kLowest, Vec<T>::kLowest, Vec<T>::kLowest);
+      }
+      if (l == target_l) {  // the target leaves the sum
+#pragma unroll
+        for (int k = 0; k < kGroup; ++k)
+          if (k == target_k) Vec<T>::drop(w[k], elem);
       }
       add_units<T>(a, s, w);
     }
+    const float zedge = edge >= 0 ? Vec<T>::load(z + edge) : -INFINITY;
     if (edge >= 0 && edge != y) add_value(a, s, zedge);
     s = warp_merge(a, s);
-    if (lane == 0) red[warp] = s;
+    if (lane == 0) red[turn & 1][warp] = s;
     __syncthreads();
-    s = warp_merge(a, lane < kMaxRowWarps ? red[lane] : Sum{-INFINITY, 0.f});
-    const Prob p = row_prob(a, s, zy);
-    if (tid == 0) {
-      if (a.logp) a.logp[t] = p.logp;
-      if (kMode == kForward) {
-        a.frame[t] = make_float2(s.m, p.s);
-        a.slope[t] = 0.f;
-      }
-    }
-    if (kMode == kPolicy) {
-      const Position at{a.old_logp[t], a.ref_logp ? a.ref_logp[t] : 0.f, a.adv[t],
-                        a.weight ? __ldcg(a.weight + t) : __ldcg(a.inv_count)};
-      const Outcome o = policy_terms(a, at, p.logp);
-      acc.add(o.terms);
-      if (has_grad) {
-        const Factor f = row_factor(a, s.m, p.s, p.logp, o.slope);
-        const Expo x = exponent(a, f.m);
-        const bool whole = aligned_unit(g + row.head);
-        for (int64_t l = tid; l < row.units; l += nt) {
-          uint4 w = scaled_unit<T>(src[l], x, f.factor);
-          if (l == unit) put<T>(w, elem, f.at_y);
-          store_unit(g + row.head + l * N, w, whole);
+    if (warp == (kMode == kPolicy ? warps - 1 : turn % warps)) {
+      s = warp_merge(a, lane < warps ? red[turn & 1][lane] : Sum{-INFINITY, 0.f});
+      const Prob p = row_prob(a, s, in ? Vec<T>::load(z + y) : NAN);
+      if (lane == 0) {
+        if (a.logp) a.logp[t] = p.logp;
+        if (kMode == kForward) {
+          a.frame[t] = make_float2(s.m, p.s);
+          a.slope[t] = 0.f;
         }
-        if (edge >= 0) Vec<T>::store(g + edge, edge == y ? f.at_y : f.factor * x.one(zedge));
+      }
+      if (kMode == kPolicy) {
+        const Position at{a.old_logp[t], a.ref_logp ? a.ref_logp[t] : 0.f, a.adv[t],
+                          a.weight ? __ldcg(a.weight + t) : __ldcg(a.inv_count)};
+        const Outcome o = policy_terms(a, at, p.logp);
+        acc.add(o.terms);
+        if (lane == 0) factor = row_factor(a, s.m, p.s, p.logp, o.slope);
       }
     }
-    __syncthreads();  // red is free
+    ++turn;
+    if (!has_grad) continue;  // red's other half takes the next row
+    __syncthreads();
+    const Factor f = factor;
+    const Expo x = exponent(a, f.m);
+    const bool whole = aligned_unit(g + row.head);
+    for (int l = tid; l < row.units; l += nt)
+      store_unit(g + row.head + (int64_t)l * N, scaled_unit<T>(src[l], x, f.factor), whole);
+    if (unit >= 0 && unit % nt == tid) Vec<T>::store(g + y, f.at_y);
+    if (edge >= 0) Vec<T>::store(g + edge, edge == y ? f.at_y : f.factor * x.one(zedge));
+    __syncthreads();  // factor is free
   }
   if (kMode == kPolicy) finish_stats(a, acc, blockIdx.x, gridDim.x, &last);
 }
@@ -780,14 +820,14 @@ __global__ void __launch_bounds__(kPieceThreads) backward_kernel(const __grid_co
     if (slope == 0.f) {
       const Row row = row_of(g, a.vocab);
       uint4* dst = reinterpret_cast<uint4*>(g + row.head);
-      for (int64_t l = (int64_t)piece * kPiece + tid; l < min((int64_t)(piece + 1) * kPiece, row.units); l += kPieceThreads)
+      for (int l = piece * kPiece + tid; l < min((piece + 1) * kPiece, row.units); l += kPieceThreads)
         dst[l] = make_uint4(0, 0, 0, 0);
-      const int64_t e = piece == 0 && tid < 16 ? edge_of(row, a.vocab, tid) : -1;
+      const int e = piece == 0 && tid < 16 ? edge_of(row, a.vocab, tid) : -1;
       if (e >= 0) Vec<T>::store(g + e, 0.f);
       continue;
     }
     const Row row = row_of(z, a.vocab);
-    const int64_t v0 = (int64_t)piece * kPiece + tid;
+    const int v0 = piece * kPiece + tid;
     const uint4* src = reinterpret_cast<const uint4*>(z + row.head);
     uint4 w[kGroup];
 #pragma unroll
@@ -798,16 +838,15 @@ __global__ void __launch_bounds__(kPieceThreads) backward_kernel(const __grid_co
     const Factor f = row_factor(a, ms.x, ms.y, __ldcg(a.logp + t), slope);
     const Expo x = exponent(a, f.m);
     const bool whole = aligned_unit(g + row.head);
-    const int64_t unit = y >= row.head && y < row.tail ? (y - row.head) / N : -1;
+    const int unit = y >= row.head && y < row.tail ? ((int)y - row.head) / N : -1;
 #pragma unroll
     for (int k = 0; k < kGroup; ++k) {
-      const int64_t u = v0 + k * kPieceThreads;
+      const int u = v0 + k * kPieceThreads;
       if (u >= row.units) continue;
-      uint4 o = scaled_unit<T>(w[k], x, f.factor);
-      if (u == unit) put<T>(o, (int)((y - row.head) % N), f.at_y);
-      store_unit(g + row.head + u * N, o, whole);
+      store_unit(g + row.head + (int64_t)u * N, scaled_unit<T>(w[k], x, f.factor), whole);
     }
-    const int64_t e = piece == 0 && tid < 16 ? edge_of(row, a.vocab, tid) : -1;
+    if (unit >= v0 && unit < v0 + kPiece && (unit - v0) % kPieceThreads == 0) Vec<T>::store(g + y, f.at_y);
+    const int e = piece == 0 && tid < 16 ? edge_of(row, a.vocab, tid) : -1;
     if (e >= 0) Vec<T>::store(g + e, e == y ? f.at_y : f.factor * x.one(Vec<T>::load(z + e)));
   }
 }
@@ -1029,13 +1068,14 @@ size_t row_smem(int64_t units, int cluster, int stages) {
   return (size_t)stages * (size_t)((units + cluster - 1) / cluster) * 16 + sizeof(RowShared);
 }
 
-RowShape row_shape(int64_t vocab, int32_t dtype, int64_t tokens, int sms) {
+RowShape row_shape(int64_t vocab, int32_t dtype, int64_t tokens, int sms, bool resident) {
   const int64_t per_unit = dtype == MUON_DTYPE_BF16 ? 8 : 4;
   const int64_t units = vocab / per_unit < 1 ? 1 : vocab / per_unit;
   RowShape s;
   s.stages = 3;
   s.cluster = 1;
-  while (s.cluster < kMaxCluster && row_smem(units, s.cluster, 3) > kSmemPerSm) s.cluster *= 2;
+  if (resident)
+    while (s.cluster < kMaxCluster && row_smem(units, s.cluster, 3) > kSmemPerSm) s.cluster *= 2;
   // few rows: more CTAs for each, while each still has some 4 KB of it
   while (s.cluster < kMaxCluster && tokens * s.cluster * 2 <= sms && units / s.cluster >= 512) s.cluster *= 2;
   s.smem = row_smem(units, s.cluster, s.stages);
@@ -1043,7 +1083,7 @@ RowShape row_shape(int64_t vocab, int32_t dtype, int64_t tokens, int sms) {
     s.stages = 2;
     s.smem = row_smem(units, s.cluster, s.stages);
   }
-  if (s.smem > kSmemPerSm) s.cluster = 0;
+  if (s.smem > kSmemPerSm || (!resident && s.cluster == 1)) s.cluster = 0;
   const int64_t per_cta = (units + (s.cluster ? s.cluster : 1) - 1) / (s.cluster ? s.cluster : 1);
   const int64_t want = (per_cta + 7) / 8;  // about 8 units a thread
   s.threads = (int)(want <= 128 ? 128 : want >= kMaxRowThreads ? kMaxRowThreads : (want + 31) / 32 * 32);
@@ -1074,7 +1114,7 @@ cudaError_t resident_clusters(K kernel, const RowShape& s, int* n) {
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)s.cluster);
-  cfg.blockDim = dim3((unsigned)s.threads);
+  cfg.blockDim = dim3((unsigned)s.threads + 32);
   cfg.dynamicSmemBytes = s.smem;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -1092,13 +1132,13 @@ cudaError_t resident_clusters(K kernel, const RowShape& s, int* n) {
 
 template <typename T, int kMode>
 cudaError_t launch_rows_as(RowArgs a, int32_t dtype, int sms, bool dependent, cudaStream_t s) {
-  const RowShape shape = row_shape(a.vocab, dtype, a.tokens, sms);
+  const RowShape shape = row_shape(a.vocab, dtype, a.tokens, sms, kMode == kPolicy && a.grad != nullptr);
   const int64_t rows = a.tokens < 1 ? 1 : a.tokens;
   if (shape.cluster == 0) {
-    const int grid = (int)(rows < 4ll * sms ? rows : 4ll * sms < kMaxParts ? 4ll * sms : kMaxParts);
-    return launch(wide_row_kernel<T, kMode>, grid, kMaxRowThreads, 0, s, 1, dependent, a);
+    const int64_t most = (int64_t)sms * (2048 / shape.threads) < kMaxParts ? (int64_t)sms * (2048 / shape.threads) : kMaxParts;
+    return launch(stream_kernel<T, kMode>, (int)(rows < most ? rows : most), shape.threads, 0, s, 1, dependent, a);
   }
-  a.cluster = shape.cluster;
+  for (a.log_cluster = 0; (1 << a.log_cluster) < shape.cluster;) ++a.log_cluster;
   a.stage_vecs = (int32_t)((shape.smem - sizeof(RowShared)) / 16 / shape.stages);
   auto kernel = shape.stages == 3 ? row_kernel<T, kMode, 3> : row_kernel<T, kMode, 2>;
   int n = 0;
@@ -1106,7 +1146,7 @@ cudaError_t launch_rows_as(RowArgs a, int32_t dtype, int sms, bool dependent, cu
   if (e != cudaSuccess) return e;
   if (n > kMaxParts) n = kMaxParts;
   if (n > rows) n = (int)rows;
-  return launch(kernel, n * shape.cluster, shape.threads, shape.smem, s, shape.cluster, dependent, a);
+  return launch(kernel, n * shape.cluster, shape.threads + 32, shape.smem, s, shape.cluster, dependent, a);
 }
 
 template <int kMode>
