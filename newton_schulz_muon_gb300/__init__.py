@@ -9,6 +9,8 @@ missing library raises ImportError there.
 """
 from __future__ import annotations
 
+import array
+import contextlib
 import ctypes
 import os
 from ctypes import POINTER, byref, c_char_p, c_float, c_int32, c_int64, c_size_t, c_void_p
@@ -395,21 +397,29 @@ def allocate_workspace(plan: Plan, device=None):
 # ---------------------------------------------------------------------------
 # losses on token log-probabilities, and clipping by the global gradient norm
 # ---------------------------------------------------------------------------
-def _on_stream(stream):
+_NO_CONTEXT = contextlib.nullcontext()
+
+
+def _on_stream(stream, device: int):
     """(context for the tensors a call allocates, cudaStream_t) of a call on `stream`: the
     allocator hands their memory out again in the order of the stream that uses it."""
-    import contextlib
     import torch
     if stream is None:
-        return contextlib.nullcontext(), torch.cuda.current_stream().cuda_stream
+        # current_stream(device).cuda_stream without the Stream object
+        return _NO_CONTEXT, torch._C._cuda_getCurrentRawStream(device)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)))
     return torch.cuda.stream(stream), stream.cuda_stream
 
 
+_DTYPE_CODES: dict = {}
+
+
 def _dtype_code(dtype) -> int:
-    import torch
-    code = {torch.float32: MUON_DTYPE_F32, torch.bfloat16: MUON_DTYPE_BF16}.get(dtype)
+    if not _DTYPE_CODES:
+        import torch
+        _DTYPE_CODES.update({torch.float32: MUON_DTYPE_F32, torch.bfloat16: MUON_DTYPE_BF16})
+    code = _DTYPE_CODES.get(dtype)
     if code is None:
         raise TypeError(f"expected a float32 or bfloat16 tensor, got {dtype}")
     return code
@@ -441,25 +451,45 @@ class GradSet:
     program whose gradients stay in place makes one and passes it to every call."""
 
     def __init__(self, grads, out=None):
+        import torch
         grads = list(grads)
-        self.tensors = grads
-        self.out = grads if out is None else list(out)
-        if len(self.out) != len(grads):
-            raise ValueError(f"{len(grads)} gradients, but {len(self.out)} outputs")
+        out = grads if out is None else list(out)
         n = len(grads)
-        self.array = (muon_grad * max(n, 1))()
-        for i, (g, o) in enumerate(zip(grads, self.out)):
-            if not g.is_cuda or not o.is_cuda:
-                raise ValueError(f"gradient {i}: not a CUDA tensor")
-            elems, count, stride = _blocks(g)
-            if o is not g and (o.shape != g.shape or (o.stride() != g.stride() and g.numel() > 1)):
-                raise ValueError(f"gradient {i}: out has another shape or layout")
-            code = _dtype_code(g.dtype)
-            self.array[i] = (g.data_ptr(), o.data_ptr(), elems, count, stride, code,
-                             code if o is g else _dtype_code(o.dtype))
+        if len(out) != n:
+            raise ValueError(f"{n} gradients, but {len(out)} outputs")
+        self.tensors, self.out = grads, out
+        # muon_grad entries, filled field by field (six 8-byte words each): a set may have
+        # thousands of tensors
+        words = array.array("q", bytes(ctypes.sizeof(muon_grad) * max(n, 1)))
+        tensor = torch.Tensor
+        codes = [_dtype_code(g.dtype) for g in grads]
+        out_codes = codes if out is grads else [_dtype_code(o.dtype) for o in out]
+        if not all(g.is_cuda for g in grads) or not (out is grads or all(o.is_cuda for o in out)):
+            raise ValueError("gradients and outputs must be CUDA tensors")
+        words[0::6] = _words(map(tensor.data_ptr, grads), n)
+        words[1::6] = words[0::6] if out is grads else _words(map(tensor.data_ptr, out), n)
+        words[5::6] = _words([c | o << 32 for c, o in zip(codes, out_codes)], n)
+        if all(map(tensor.is_contiguous, grads)):
+            words[2::6] = _words(map(tensor.numel, grads), n)
+            words[3::6] = _words([1] * n, n)
+        else:
+            for i, g in enumerate(grads):
+                words[6 * i + 2], words[6 * i + 3], words[6 * i + 4] = _blocks(g)
+        if out is not grads:
+            for i, (g, o) in enumerate(zip(grads, out)):
+                if o.shape != g.shape or (o.stride() != g.stride() and not (o.is_contiguous() and g.is_contiguous())):
+                    raise ValueError(f"gradient {i}: out has another shape or layout")
+        self._words = words
+        self.array = c_void_p(words.buffer_info()[0])
+        self.device = grads[0].get_device() if n else torch.cuda.current_device()
 
     def __len__(self):
         return len(self.tensors)
+
+
+def _words(values, n):
+    w = array.array("q", values)
+    return w if n else array.array("q", [0])
 
 
 def muon_clip_workspace_bytes(grads) -> int:
@@ -469,25 +499,23 @@ def muon_clip_workspace_bytes(grads) -> int:
     return v.value
 
 
-def _vector(t, n, dtype, what, optional=False):
-    """Device pointer of a contiguous CUDA tensor of n elements of `dtype`; 0 for None."""
-    if t is None:
-        if optional:
-            return 0
-        raise ValueError(f"{what} is needed")
-    if t.dtype != dtype or t.numel() != n or not t.is_cuda or not t.is_contiguous():
+def _vector(t, n, dtype, what):
+    """Device pointer of a contiguous CUDA tensor of n elements of `dtype`."""
+    if t.dtype is not dtype or t.numel() != n or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{what}: expected a contiguous CUDA tensor of {n} {dtype} values, got shape "
                          f"{tuple(t.shape)}, strides {t.stride()}, {t.dtype} on {t.device}")
     return t.data_ptr()
 
 
-def _space(workspace, nbytes):
+def _space(workspace, nbytes, device):
+    """(tensor to keep, pointer, bytes) of a workspace."""
     import torch
     if workspace is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return workspace, workspace.data_ptr(), nbytes
     if not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace: expected a contiguous CUDA tensor")
-    return workspace
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def muon_grad_norm(grads, norm=None, workspace=None, stream=None):
@@ -495,14 +523,14 @@ def muon_grad_norm(grads, norm=None, workspace=None, stream=None):
     one-element fp32 device tensor."""
     import torch
     grads = grads if isinstance(grads, GradSet) else GradSet(grads)
+    device = grads.device
     nbytes = muon_clip_workspace_bytes(grads)
-    context, handle = _on_stream(stream)
+    context, handle = _on_stream(stream, device)
     with context:
-        workspace = _space(workspace, nbytes)
+        keep, ws, nbytes = _space(workspace, nbytes, device)
         if norm is None:
-            norm = torch.empty(1, dtype=torch.float32, device="cuda")
-    _check(_lib().muon_grad_norm(grads.array, len(grads), _vector(norm, 1, torch.float32, "norm"),
-                                 workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle),
+            norm = torch.empty(1, dtype=torch.float32, device=device)
+    _check(_lib().muon_grad_norm(grads.array, len(grads), _vector(norm, 1, torch.float32, "norm"), ws, nbytes, handle),
            "muon_grad_norm")
     return norm
 
@@ -517,63 +545,70 @@ def muon_clip_grad_norm(grads, max_norm: float, out=None, eps: float = 1e-6,
         grads = GradSet(grads, out)
     elif out is not None:
         raise ValueError("a GradSet has its outputs already")
+    device = grads.device
     nbytes = muon_clip_workspace_bytes(grads)
-    context, handle = _on_stream(stream)
+    context, handle = _on_stream(stream, device)
     with context:
-        workspace = _space(workspace, nbytes)
+        keep, ws, nbytes = _space(workspace, nbytes, device)
         if result is None:
-            result = torch.empty(2, dtype=torch.float32, device="cuda")
-    _check(_lib().muon_clip_grad_norm(grads.array, len(grads), float(max_norm), float(eps), int(nonfinite),
-                                      _vector(result, 2, torch.float32, "result"), workspace.data_ptr(),
-                                      workspace.numel() * workspace.element_size(), handle),
+            result = torch.empty(2, dtype=torch.float32, device=device)
+    _check(_lib().muon_clip_grad_norm(grads.array, len(grads), max_norm, eps, nonfinite,
+                                      _vector(result, 2, torch.float32, "result"), ws, nbytes, handle),
            "muon_clip_grad_norm")
     return result
 
 
+def _rows(t, what):
+    """Row stride of a matrix whose rows are contiguous and do not overlap."""
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{what}: expected a CUDA matrix [tokens, vocab], got shape {tuple(t.shape)} on {t.device}")
+    tokens, vocab = t.shape
+    stride, inner = t.stride()
+    if (vocab > 1 and inner != 1) or (tokens > 1 and stride < vocab):
+        raise ValueError(f"{what}: rows must be contiguous and not overlap, got strides {t.stride()}")
+    return tokens, vocab, stride if tokens > 1 else vocab
+
+
 def _token_batch(logits, targets, mask, temperature):
+    """(muon_token_batch, tokens, vocab, row stride)"""
     import torch
-    if logits.dim() != 2 or not logits.is_cuda:
-        raise ValueError(f"logits: expected a CUDA matrix [tokens, vocab], got shape {tuple(logits.shape)} on "
-                         f"{logits.device}")
-    tokens, vocab = logits.shape
-    stride = logits.stride(0)
-    if (vocab > 1 and logits.stride(1) != 1) or (tokens > 1 and stride < vocab):
-        raise ValueError(f"logits: rows must be contiguous and not overlap, got strides {logits.stride()}")
-    if mask is not None and mask.dtype not in (torch.bool, torch.uint8):
-        raise ValueError(f"mask: expected bool or uint8, got {mask.dtype}")
-    return muon_token_batch(logits.data_ptr(), _vector(targets, tokens, torch.int64, "targets"),
-                            None if mask is None else _vector(mask, tokens, mask.dtype, "mask"), tokens, vocab,
-                            stride if tokens > 1 else vocab, _dtype_code(logits.dtype), temperature)
+    tokens, vocab, stride = _rows(logits, "logits")
+    masked = None
+    if mask is not None:
+        if mask.dtype is not torch.bool and mask.dtype is not torch.uint8:
+            raise ValueError(f"mask: expected bool or uint8, got {mask.dtype}")
+        masked = _vector(mask, tokens, mask.dtype, "mask")
+    return muon_token_batch(logits.data_ptr(), _vector(targets, tokens, torch.int64, "targets"), masked, tokens, vocab,
+                            stride, _dtype_code(logits.dtype), temperature), tokens, vocab, stride
 
 
-def _grad_like(logits, grad, with_grad, batch):
-    """(gradient tensor or None, row stride): by default with the logits' row stride, so
-    that both start on the same boundaries, unless that would waste memory."""
+def _grad_rows(logits, grad, with_grad, tokens, vocab, stride):
+    """(gradient tensor or None, its pointer, its row stride): by default with the logits'
+    row stride, so that both start on the same boundaries, unless that would waste memory."""
     import torch
     if grad is None:
         if not with_grad:
-            return None, 0
-        tokens, vocab = logits.shape
-        stride = batch.row_stride if batch.row_stride <= vocab + vocab // 8 else vocab
-        return torch.empty_strided((tokens, vocab), (stride, 1), dtype=logits.dtype, device=logits.device), stride
-    if grad.shape != logits.shape or grad.dtype != logits.dtype or not grad.is_cuda:
-        raise ValueError(f"grad: expected a CUDA tensor like the logits, got shape {tuple(grad.shape)}, {grad.dtype}")
-    tokens, vocab = grad.shape
-    if (vocab > 1 and grad.stride(1) != 1) or (tokens > 1 and grad.stride(0) < vocab):
-        raise ValueError(f"grad: rows must be contiguous and not overlap, got strides {grad.stride()}")
-    return grad, grad.stride(0) if tokens > 1 else (batch.row_stride if grad is logits else vocab)
+            return None, None, 0
+        if stride > vocab + vocab // 8:
+            stride = vocab
+        grad = torch.empty_strided((tokens, vocab), (stride, 1), dtype=logits.dtype, device=logits.device)
+        return grad, grad.data_ptr(), stride
+    if grad.shape != logits.shape or grad.dtype is not logits.dtype:
+        raise ValueError(f"grad: expected a tensor like the logits, got shape {tuple(grad.shape)}, {grad.dtype}")
+    return grad, grad.data_ptr(), _rows(grad, "grad")[2]
 
 
 def muon_token_logprobs(logits, targets, mask=None, temperature: float = 1.0, logp=None, stream=None):
     """log softmax(logits / temperature) at each position's target, fp32; 0 where the mask
     is False.  logits: [tokens, vocab], targets: [tokens] int64, mask: [tokens] bool."""
     import torch
-    batch = _token_batch(logits, targets, mask, temperature)
-    context, handle = _on_stream(stream)
+    batch, tokens, _, _ = _token_batch(logits, targets, mask, temperature)
+    device = logits.get_device()
+    context, handle = _on_stream(stream, device)
     if logp is None:
         with context:
-            logp = torch.empty(batch.tokens, dtype=torch.float32, device=logits.device)
-    _check(_lib().muon_token_logprobs(byref(batch), _vector(logp, batch.tokens, torch.float32, "logp"), handle),
+            logp = torch.empty(tokens, dtype=torch.float32, device=device)
+    _check(_lib().muon_token_logprobs(byref(batch), _vector(logp, tokens, torch.float32, "logp"), handle),
            "muon_token_logprobs")
     return logp
 
@@ -611,26 +646,26 @@ def muon_policy_loss(logits, targets, old_logp, advantages, mask=None, ref_logp=
     clipped share (fp32, on the device); grad is None with with_grad=False.  seq_offsets:
     [n_seqs + 1] int64, for the sequence mean.  grad may be the logits themselves."""
     import torch
-    batch = _token_batch(logits, targets, mask, temperature)
-    tokens = batch.tokens
-    n_seqs = 0 if seq_offsets is None else max(seq_offsets.numel() - 1, 0)
-    nbytes = muon_loss_workspace_bytes(tokens, n_seqs)
-    context, handle = _on_stream(stream)
-    with context:
-        workspace = _space(workspace, nbytes)
-        grad, grad_stride = _grad_like(logits, grad, with_grad, batch)
-        if logp is None:
-            logp = torch.empty(tokens, dtype=torch.float32, device=logits.device)
-        if stats is None:
-            stats = torch.empty(4, dtype=torch.float32, device=logits.device)
     f32 = torch.float32
+    batch, tokens, vocab, stride = _token_batch(logits, targets, mask, temperature)
+    device = logits.get_device()
+    n_seqs, offsets = 0, None
+    if seq_offsets is not None:
+        n_seqs = max(seq_offsets.numel() - 1, 0)
+        offsets = _vector(seq_offsets, n_seqs + 1, torch.int64, "seq_offsets")
+    context, handle = _on_stream(stream, device)
+    with context:
+        keep, ws, nbytes = _space(workspace, muon_loss_workspace_bytes(tokens, n_seqs), device)
+        grad, grad_ptr, grad_stride = _grad_rows(logits, grad, with_grad, tokens, vocab, stride)
+        if logp is None:
+            logp = torch.empty(tokens, dtype=f32, device=device)
+        if stats is None:
+            stats = torch.empty(4, dtype=f32, device=device)
     _check(_lib().muon_policy_loss(
         byref(batch), byref(config) if config is not None else None, _vector(old_logp, tokens, f32, "old_logp"),
-        _vector(ref_logp, tokens, f32, "ref_logp", True), _vector(advantages, tokens, f32, "advantages"),
-        0 if seq_offsets is None else _vector(seq_offsets, n_seqs + 1, torch.int64, "seq_offsets"), n_seqs,
-        _vector(stats, 4, f32, "stats"), _vector(logp, tokens, f32, "logp"), 0 if grad is None else grad.data_ptr(),
-        grad_stride, workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle),
-        "muon_policy_loss")
+        None if ref_logp is None else _vector(ref_logp, tokens, f32, "ref_logp"),
+        _vector(advantages, tokens, f32, "advantages"), offsets, n_seqs, _vector(stats, 4, f32, "stats"),
+        _vector(logp, tokens, f32, "logp"), grad_ptr, grad_stride, ws, nbytes, handle), "muon_policy_loss")
     return stats, logp, grad
 
 
@@ -642,23 +677,25 @@ def muon_preference_loss(logits, targets, seq_offsets, ref_logp, mask=None, temp
     seq_offsets: [2 P + 1] int64: the P preferred answers, then the P others.  ref_logp:
     [2 P] fp32, the reference policy's sums.  Returns (loss, margins, seq_logp, grad)."""
     import torch
-    batch = _token_batch(logits, targets, mask, temperature)
+    f32 = torch.float32
+    batch, tokens, vocab, stride = _token_batch(logits, targets, mask, temperature)
+    device = logits.get_device()
     n_seqs = seq_offsets.numel() - 1
     if n_seqs < 0 or n_seqs % 2:
         raise ValueError(f"seq_offsets: expected 2 P + 1 offsets, got {seq_offsets.numel()}")
-    nbytes = muon_loss_workspace_bytes(batch.tokens, n_seqs)
-    context, handle = _on_stream(stream)
-    f32, device = torch.float32, logits.device
+    context, handle = _on_stream(stream, device)
     with context:
-        workspace = _space(workspace, nbytes)
-        grad, grad_stride = _grad_like(logits, grad, with_grad, batch)
-        loss = torch.empty(1, dtype=f32, device=device) if loss is None else loss
-        margins = torch.empty(n_seqs // 2, dtype=f32, device=device) if margins is None else margins
-        seq_logp = torch.empty(n_seqs, dtype=f32, device=device) if seq_logp is None else seq_logp
+        keep, ws, nbytes = _space(workspace, muon_loss_workspace_bytes(tokens, n_seqs), device)
+        grad, grad_ptr, grad_stride = _grad_rows(logits, grad, with_grad, tokens, vocab, stride)
+        if loss is None:
+            loss = torch.empty(1, dtype=f32, device=device)
+        if margins is None:
+            margins = torch.empty(n_seqs // 2, dtype=f32, device=device)
+        if seq_logp is None:
+            seq_logp = torch.empty(n_seqs, dtype=f32, device=device)
     _check(_lib().muon_preference_loss(
         byref(batch), byref(config) if config is not None else None, _vector(ref_logp, n_seqs, f32, "ref_logp"),
         _vector(seq_offsets, n_seqs + 1, torch.int64, "seq_offsets"), n_seqs // 2, _vector(loss, 1, f32, "loss"),
-        _vector(margins, n_seqs // 2, f32, "margins"), _vector(seq_logp, n_seqs, f32, "seq_logp"),
-        0 if grad is None else grad.data_ptr(), grad_stride, workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), handle), "muon_preference_loss")
+        _vector(margins, n_seqs // 2, f32, "margins"), _vector(seq_logp, n_seqs, f32, "seq_logp"), grad_ptr,
+        grad_stride, ws, nbytes, handle), "muon_preference_loss")
     return loss, margins, seq_logp, grad

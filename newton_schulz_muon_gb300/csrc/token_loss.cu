@@ -384,6 +384,12 @@ constexpr int kBatch = 256;  // rows whose scalars a CTA holds at a time
 constexpr int kSlots = 4;    // rows whose partial sums may be on their way
 constexpr int kGroup = 4;    // 16-byte units a thread takes at a time
 
+// A CTA's sums of its rows' terms, and whether it is the last to have them.
+struct StatsShared {
+  double sum[4];
+  int32_t last;
+};
+
 // Shared memory beside the ring.
 struct RowShared {
   uint64_t full[kSlots];                        // a slot has every partial sum of its row
@@ -395,7 +401,7 @@ struct RowShared {
   float zy[kBatch];
   float old_logp[kBatch], ref[kBatch], adv[kBatch], w[kBatch];
   uint32_t live[kBatch / 32];
-  int32_t last;
+  StatsShared stats;
 };
 
 // Barriers 1 and 2 (by the row's parity): the finishing warp has written a row's factor.
@@ -435,19 +441,25 @@ struct Terms {
       lo[k] += fabsf(sum) < INFINITY ? err : 0.f;
     }
   }
+  __device__ __forceinline__ void get(double* sum) const {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) sum[k] = (double)hi[k] + (double)lo[k];
+  }
 };
 
-// The last warp's sums into the partials; the last of `n` to come adds all of them, in their order.
-__device__ __forceinline__ void finish_stats(const RowArgs& a, const Terms& acc, int64_t part, int64_t n, int32_t* last) {
+// The CTA's sums into the partials; the last of `n` CTAs to come adds all of them, in
+// their order.
+__device__ __forceinline__ void finish_stats(const RowArgs& a, StatsShared& sh, int64_t part, int64_t n) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (threadIdx.x == blockDim.x - 32) {
+  __syncthreads();
+  if (threadIdx.x == 0) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) a.partials[4 * part + k] = (double)acc.hi[k] + (double)acc.lo[k];
+    for (int k = 0; k < 4; ++k) a.partials[4 * part + k] = sh.sum[k];
     __threadfence();
-    *last = atomicAdd(a.ticket, 1u) == (unsigned)n - 1;
+    sh.last = atomicAdd(a.ticket, 1u) == (unsigned)n - 1;
   }
   __syncthreads();
-  if (*last && warp < 4) {
+  if (sh.last && warp < 4) {
     __threadfence();
     double sum = 0.0;
     for (int64_t k = lane; k < n; k += 32) sum += __ldcg(a.partials + 4 * k + warp);
@@ -708,7 +720,134 @@ __global__ void __launch_bounds__(kMaxRowThreads + 32) row_kernel(const __grid_c
     cluster_sync();
   }
   if (!waited) griddep_wait();
-  if (kMode == kPolicy && rank == 0) finish_stats(a, acc, cid, n_clusters, &sh.last);
+  if (kMode == kForward && blockIdx.x == 0 && tid == 0) *a.ticket = 0;
+  if (kMode == kPolicy && rank == 0) {
+    if (finisher && lane == 0) acc.get(sh.stats.sum);
+    finish_stats(a, sh.stats, cid, n_clusters);
+  }
+}
+
+// Rows of at most 32 kUnits 16-byte units (and the elements around them): one warp holds a
+// row in registers, and nothing is shared between warps.  The row's largest logit is known
+// before the first exponential.
+constexpr int kWarpRowThreads = 256;
+constexpr int kWarpRowWarps = kWarpRowThreads / 32;
+
+template <typename T, int kMode, int kUnits>
+__global__ void __launch_bounds__(kWarpRowThreads, kUnits > 4 ? 2 : 3) warp_row_kernel(const __grid_constant__ RowArgs a) {
+  constexpr int N = Vec<T>::N;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool has_grad = kMode == kPolicy && a.grad != nullptr;
+  const int64_t warps = (int64_t)gridDim.x * kWarpRowWarps;
+  Terms acc;
+  griddep_launch_dependents();
+  griddep_wait();
+  for (int64_t t = (int64_t)blockIdx.x * kWarpRowWarps + warp; t < a.tokens; t += warps) {
+    const T* z = reinterpret_cast<const T*>(a.logits) + t * a.stride;
+    T* g = reinterpret_cast<T*>(a.grad) + t * a.grad_stride;
+    if (a.mask != nullptr && a.mask[t] == 0) {
+      if (lane == 0 && a.logp) a.logp[t] = 0.f;
+      if (kMode == kForward && lane == 0) a.slope[t] = 0.f;
+      if (has_grad) {
+        const Row row = row_of(g, a.vocab);
+        uint4* dst = reinterpret_cast<uint4*>(g + row.head);
+        for (int u = lane; u < row.units; u += 32) dst[u] = make_uint4(0, 0, 0, 0);
+        const int e = edge_of(row, a.vocab, lane);
+        if (e >= 0) Vec<T>::store(g + e, 0.f);
+      }
+      continue;
+    }
+    const Row row = row_of(z, a.vocab);
+    const uint4* src = reinterpret_cast<const uint4*>(z + row.head);
+    uint4 w[kUnits];
+#pragma unroll
+    for (int k = 0; k < kUnits; ++k)
+      w[k] = k * 32 + lane < row.units ? src[k * 32 + lane]
+                                       : make_uint4(Vec<T>::kLowest, Vec<T>::kLowest, Vec<T>::kLowest, Vec<T>::kLowest);
+    const int edge = edge_of(row, a.vocab, lane);
+    const float zedge = edge >= 0 ? Vec<T>::load(z + edge) : -INFINITY;
+    const int64_t y = a.targets[t];
+    const bool in = y >= 0 && y < a.vocab;
+    const float zy = in ? Vec<T>::load(z + y) : NAN;
+    Position at{0.f, 0.f, 0.f, 0.f};
+    if (kMode == kPolicy) {
+      at.old_logp = a.old_logp[t];
+      if (a.ref_logp) at.ref = a.ref_logp[t];
+      at.adv = a.adv[t];
+      at.w = a.weight ? __ldcg(a.weight + t) : __ldcg(a.inv_count);
+    }
+    const int unit = in && y >= row.head && y < row.tail ? ((int)y - row.head) / N : -1;
+    const int owned = unit >= 0 && (unit & 31) == lane ? unit >> 5 : -1;
+    const int elem = ((int)y - row.head) % N;
+#pragma unroll
+    for (int k = 0; k < kUnits; ++k) {
+      int mine = owned;
+      asm volatile("" : "+r"(mine));  // one test a register, not an indexed array
+      if (mine == k) Vec<T>::drop(w[k], elem);  // the target leaves the sum
+    }
+    const bool at_edge = edge >= 0 && edge == y;
+    const float others = at_edge ? -INFINITY : zedge;
+    Sum s;
+    s.m = fmaxf(Vec<T>::max(w), others);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s.m = fmaxf(s.m, __shfl_xor_sync(0xFFFFFFFFu, s.m, o));
+    const Expo x = exponent(a, s.m);
+    F2 s0 = make_f2(x.one(others), 0.f), s1 = make_f2(0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kUnits; ++k) {
+      float v[N];
+      Vec<T>::unpack(w[k], v);
+#pragma unroll
+      for (int i = 0; i < N; i += 4) {
+        const float2 e0 = x.two(v[i], v[i + 1]), e1 = x.two(v[i + 2], v[i + 3]);
+        s0 = add2(s0, make_f2(e0.x, e0.y));
+        s1 = add2(s1, make_f2(e1.x, e1.y));
+      }
+    }
+    const float2 r = split(add2(s0, s1));
+    s.s = warp_sum(r.x + r.y);
+    const Prob p = row_prob(a, s, zy);
+    if (lane == 0) {
+      if (a.logp) a.logp[t] = p.logp;
+      if (kMode == kForward) {
+        a.frame[t] = make_float2(s.m, p.s);
+        a.slope[t] = 0.f;
+      }
+    }
+    if (kMode == kPolicy) {
+      const Outcome o = policy_terms(a, at, p.logp);
+      acc.add(o.terms);
+      if (has_grad) {
+        const Factor f = row_factor(a, s.m, p.s, p.logp, o.slope);
+        const bool whole = aligned_unit(g + row.head);
+        T* dst = g + row.head + lane * N;
+        if (kUnits * N > 64) {  // up to 64 exponentials stay in registers from the sum; more are taken again
+#pragma unroll
+          for (int k = 0; k < kUnits; ++k)
+            asm volatile("" : "+r"(w[k].x), "+r"(w[k].y), "+r"(w[k].z), "+r"(w[k].w));
+        }
+#pragma unroll
+        for (int k = 0; k < kUnits; ++k)
+          if (k * 32 + lane < row.units) store_unit(dst + k * 32 * N, scaled_unit<T>(w[k], x, f.factor), whole);
+        if (owned >= 0) Vec<T>::store(g + y, f.at_y);
+        if (edge >= 0) Vec<T>::store(g + edge, at_edge ? f.at_y : f.factor * x.one(zedge));
+      }
+    }
+  }
+  if (kMode == kForward && blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
+  if (kMode == kPolicy) {
+    __shared__ double part[kWarpRowWarps][4];
+    __shared__ StatsShared stats;
+    if (lane == 0) acc.get(part[warp]);
+    __syncthreads();
+    if (threadIdx.x < 4) {
+      double sum = part[0][threadIdx.x];
+#pragma unroll
+      for (int k = 1; k < kWarpRowWarps; ++k) sum += part[k][threadIdx.x];
+      stats.sum[threadIdx.x] = sum;
+    }
+    finish_stats(a, stats, blockIdx.x, gridDim.x);
+  }
 }
 
 // Rows straight from memory, one CTA a row: where nothing is written back a row need not
@@ -720,7 +859,6 @@ __global__ void __launch_bounds__(kMaxRowThreads) stream_kernel(const __grid_con
   constexpr int N = Vec<T>::N;
   __shared__ Sum red[2][kMaxRowThreads / 32];
   __shared__ Factor factor;
-  __shared__ int32_t last;
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = nt >> 5;
   const bool has_grad = kMode == kPolicy && a.grad != nullptr;
   Terms acc;  // of the last warp
@@ -797,7 +935,12 @@ __global__ void __launch_bounds__(kMaxRowThreads) stream_kernel(const __grid_con
     if (edge >= 0) Vec<T>::store(g + edge, edge == y ? f.at_y : f.factor * x.one(zedge));
     __syncthreads();  // factor is free
   }
-  if (kMode == kPolicy) finish_stats(a, acc, blockIdx.x, gridDim.x, &last);
+  if (kMode == kForward && blockIdx.x == 0 && tid == 0) *a.ticket = 0;
+  if (kMode == kPolicy) {
+    __shared__ StatsShared stats;
+    if (warp == warps - 1 && lane == 0) acc.get(stats.sum);
+    finish_stats(a, stats, blockIdx.x, gridDim.x);
+  }
 }
 
 // The gradient of rows whose slope, frame and sum are known, a piece of kPiece units a
@@ -939,10 +1082,15 @@ struct PairArgs {
   float* seq_logp;  // or null
   float* pair_loss; // [n_pairs]
   float* slope;     // [tokens], or null
+  float* loss;
+  unsigned* ticket; // zeroed by the kernel before
 };
 
-// One CTA a pair: both sums, the margin, and the slope of each of its positions.
+// One CTA a pair: both sums, the margin, and the slope of each of its positions.  The last
+// CTA to come forms the mean over the pairs, in their order.
 __global__ void __launch_bounds__(kSmallThreads) pair_kernel(const __grid_constant__ PairArgs a) {
+  __shared__ int32_t last;
+  griddep_launch_dependents();
   griddep_wait();
   const int64_t i = blockIdx.x;
   double gain[2];
@@ -972,6 +1120,8 @@ __global__ void __launch_bounds__(kSmallThreads) pair_kernel(const __grid_consta
   if (threadIdx.x == 0) {
     if (a.margins) a.margins[i] = h;
     a.pair_loss[i] = (1.f - a.smooth) * (soft - fminf(h, 0.f)) + a.smooth * (soft + fmaxf(h, 0.f));
+    __threadfence();
+    last = atomicAdd(a.ticket, 1u) == (unsigned)a.n_pairs - 1;
   }
   if (a.slope) {
     const float up = 1.f / (1.f + expf(-h)), down = 1.f / (1.f + expf(h));
@@ -979,14 +1129,13 @@ __global__ void __launch_bounds__(kSmallThreads) pair_kernel(const __grid_consta
     for (int k = 0; k < 2; ++k)
       for (int64_t t = lo[k] + threadIdx.x; t < hi[k]; t += kSmallThreads) a.slope[t] = (k == 0 ? d : -d) * per[k];
   }
-}
-
-__global__ void __launch_bounds__(kSmallThreads) pair_mean_kernel(const float* pair_loss, int64_t n, float* loss) {
-  griddep_wait();
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
   double t = 0.0;
-  for (int64_t i = threadIdx.x; i < n; i += kSmallThreads) t += (double)pair_loss[i];
+  for (int64_t k = threadIdx.x; k < a.n_pairs; k += kSmallThreads) t += (double)__ldcg(a.pair_loss + k);
   t = block_sum(t);
-  if (threadIdx.x == 0) *loss = n > 0 ? (float)(t / (double)n) : 0.f;
+  if (threadIdx.x == 0) *a.loss = (float)(t / (double)a.n_pairs);
 }
 
 // ---------------------------------------------------------------------------
@@ -1058,9 +1207,10 @@ RowArgs row_args(const muon_token_batch* b) {
 constexpr int kMaxParts = 2048;            // partial sums of the policy loss
 constexpr size_t kSmemPerSm = 227 * 1024;  // what one CTA may have
 
-// Shape of a row kernel's launch.  cluster = 0: rows too long for shared memory.
+// Shape of a row kernel's launch.  warp_units > 0: a warp a row; else cluster = 0: straight
+// from memory, one CTA a row.
 struct RowShape {
-  int cluster, stages, threads;
+  int warp_units, cluster, stages, threads;
   size_t smem;
 };
 
@@ -1071,21 +1221,31 @@ size_t row_smem(int64_t units, int cluster, int stages) {
 RowShape row_shape(int64_t vocab, int32_t dtype, int64_t tokens, int sms, bool resident) {
   const int64_t per_unit = dtype == MUON_DTYPE_BF16 ? 8 : 4;
   const int64_t units = vocab / per_unit < 1 ? 1 : vocab / per_unit;
-  RowShape s;
+  RowShape s = {};
+  // few rows: more CTAs for each, while each still has some 8 KB of it
+  int split = 1;
+  while (split < kMaxCluster && tokens * split * 2 <= sms && units / split >= 1024) split *= 2;
+  if (units <= 512 && split == 1) {
+    s.warp_units = units <= 128 ? 4 : units <= 256 ? 8 : 16;
+    return s;
+  }
   s.stages = 3;
   s.cluster = 1;
   if (resident)
     while (s.cluster < kMaxCluster && row_smem(units, s.cluster, 3) > kSmemPerSm) s.cluster *= 2;
-  // few rows: more CTAs for each, while each still has some 4 KB of it
-  while (s.cluster < kMaxCluster && tokens * s.cluster * 2 <= sms && units / s.cluster >= 512) s.cluster *= 2;
+  if (split > s.cluster) s.cluster = split;
   s.smem = row_smem(units, s.cluster, s.stages);
   if (s.smem > kSmemPerSm) {
     s.stages = 2;
     s.smem = row_smem(units, s.cluster, s.stages);
   }
   if (s.smem > kSmemPerSm || (!resident && s.cluster == 1)) s.cluster = 0;
-  const int64_t per_cta = (units + (s.cluster ? s.cluster : 1) - 1) / (s.cluster ? s.cluster : 1);
-  const int64_t want = (per_cta + 7) / 8;  // about 8 units a thread
+  if (s.cluster == 0) {
+    s.threads = units <= 8192 ? 64 : 256;
+    if (resident) s.threads = 512;
+    return s;
+  }
+  const int64_t want = ((units + s.cluster - 1) / s.cluster + 7) / 8;  // about 8 units a thread
   s.threads = (int)(want <= 128 ? 128 : want >= kMaxRowThreads ? kMaxRowThreads : (want + 31) / 32 * 32);
   return s;
 }
@@ -1134,6 +1294,12 @@ template <typename T, int kMode>
 cudaError_t launch_rows_as(RowArgs a, int32_t dtype, int sms, bool dependent, cudaStream_t s) {
   const RowShape shape = row_shape(a.vocab, dtype, a.tokens, sms, kMode == kPolicy && a.grad != nullptr);
   const int64_t rows = a.tokens < 1 ? 1 : a.tokens;
+  if (shape.warp_units > 0) {
+    auto kernel = shape.warp_units == 4 ? warp_row_kernel<T, kMode, 4>
+                  : shape.warp_units == 8 ? warp_row_kernel<T, kMode, 8> : warp_row_kernel<T, kMode, 16>;
+    const int64_t ctas = (rows + kWarpRowWarps - 1) / kWarpRowWarps, most = (shape.warp_units > 4 ? 2 : 3) * (int64_t)sms;
+    return launch(kernel, (int)(ctas < most ? ctas : most), kWarpRowThreads, 0, s, 1, dependent, a);
+  }
   if (shape.cluster == 0) {
     const int64_t most = (int64_t)sms * (2048 / shape.threads) < kMaxParts ? (int64_t)sms * (2048 / shape.threads) : kMaxParts;
     return launch(stream_kernel<T, kMode>, (int)(rows < most ? rows : most), shape.threads, 0, s, 1, dependent, a);
@@ -1324,12 +1490,15 @@ muon_status muon_preference_loss(const muon_token_batch* batch, const muon_prefe
   a.logp = ws.logp;
   a.frame = ws.frame;
   a.slope = ws.slope;
+  a.ticket = ws.ticket;
   a.grad_scale = c.grad_scale;
   a.grad = grad;
   if (grad_stride) a.grad_stride = grad_stride;
   cudaError_t e;
-  if (batch->tokens > 0 && (e = launch_rows<kForward>(a, batch->dtype, sms, false, s)) != cudaSuccess)
-    return cuda_error(e);
+  // clears the pair kernel's ticket too
+  e = batch->tokens > 0 ? launch_rows<kForward>(a, batch->dtype, sms, false, s)
+                        : cudaMemsetAsync(ws.ticket, 0, sizeof(unsigned), s);
+  if (e != cudaSuccess) return cuda_error(e);
   if (n_pairs > 0) {
     PairArgs p;
     p.mask = batch->mask;
@@ -1344,12 +1513,13 @@ muon_status muon_preference_loss(const muon_token_batch* batch, const muon_prefe
     p.margins = margins;
     p.seq_logp = seq_logp;
     p.pair_loss = ws.pair_loss;
-    p.slope = ws.slope;
+    p.slope = grad ? ws.slope : nullptr;
+    p.loss = loss;
+    p.ticket = ws.ticket;
     if ((e = launch(pair_kernel, (int)n_pairs, kSmallThreads, 0, s, 1, batch->tokens > 0, p)) != cudaSuccess)
       return cuda_error(e);
   }
-  e = launch(pair_mean_kernel, 1, kSmallThreads, 0, s, 1, false, (const float*)ws.pair_loss, (int64_t)n_pairs, loss);
-  if (e != cudaSuccess) return cuda_error(e);
+  if (n_pairs == 0 && (e = cudaMemsetAsync(loss, 0, sizeof(float), s)) != cudaSuccess) return cuda_error(e);
   if (grad && (e = launch_backward(a, batch->dtype, sms, s)) != cudaSuccess) return cuda_error(e);
   return MUON_OK;
 }
