@@ -507,15 +507,30 @@ def _vector(t, n, dtype, what):
     return t.data_ptr()
 
 
-def _space(workspace, nbytes, device):
-    """(tensor to keep, pointer, bytes) of a workspace."""
+def _space(workspace, nbytes, device, sizes, given):
+    """(outputs, workspace pointer, bytes).  The fp32 outputs that are not given, of these
+    sizes, and the workspace that is not come from one allocation."""
     import torch
+    need = 0
+    for size, t in zip(sizes, given):
+        if t is None:
+            need += size
+    at = (need + 3) // 4 * 4  # the workspace follows on a 16-byte boundary
     if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        return workspace, workspace.data_ptr(), nbytes
-    if not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("workspace: expected a contiguous CUDA tensor")
-    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        buffer = torch.empty(at + (nbytes + 3) // 4, dtype=torch.float32, device=device)
+        ptr = buffer.data_ptr() + 4 * at
+    else:
+        if not workspace.is_cuda or not workspace.is_contiguous():
+            raise ValueError("workspace: expected a contiguous CUDA tensor")
+        buffer = torch.empty(need, dtype=torch.float32, device=device) if need else workspace
+        ptr, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    outputs, at = [buffer], 0  # the buffer stays alive while the call is enqueued
+    for size, t in zip(sizes, given):
+        if t is None:
+            t = buffer[at:at + size]
+            at += size
+        outputs.append(t)
+    return outputs, ptr, nbytes
 
 
 def muon_grad_norm(grads, norm=None, workspace=None, stream=None):
@@ -527,9 +542,7 @@ def muon_grad_norm(grads, norm=None, workspace=None, stream=None):
     nbytes = muon_clip_workspace_bytes(grads)
     context, handle = _on_stream(stream, device)
     with context:
-        keep, ws, nbytes = _space(workspace, nbytes, device)
-        if norm is None:
-            norm = torch.empty(1, dtype=torch.float32, device=device)
+        (_keep, norm), ws, nbytes = _space(workspace, nbytes, device, (1,), (norm,))
     _check(_lib().muon_grad_norm(grads.array, len(grads), _vector(norm, 1, torch.float32, "norm"), ws, nbytes, handle),
            "muon_grad_norm")
     return norm
@@ -549,9 +562,7 @@ def muon_clip_grad_norm(grads, max_norm: float, out=None, eps: float = 1e-6,
     nbytes = muon_clip_workspace_bytes(grads)
     context, handle = _on_stream(stream, device)
     with context:
-        keep, ws, nbytes = _space(workspace, nbytes, device)
-        if result is None:
-            result = torch.empty(2, dtype=torch.float32, device=device)
+        (_keep, result), ws, nbytes = _space(workspace, nbytes, device, (2,), (result,))
     _check(_lib().muon_clip_grad_norm(grads.array, len(grads), max_norm, eps, nonfinite,
                                       _vector(result, 2, torch.float32, "result"), ws, nbytes, handle),
            "muon_clip_grad_norm")
@@ -655,12 +666,9 @@ def muon_policy_loss(logits, targets, old_logp, advantages, mask=None, ref_logp=
         offsets = _vector(seq_offsets, n_seqs + 1, torch.int64, "seq_offsets")
     context, handle = _on_stream(stream, device)
     with context:
-        keep, ws, nbytes = _space(workspace, muon_loss_workspace_bytes(tokens, n_seqs), device)
+        (_keep, stats, logp), ws, nbytes = _space(workspace, muon_loss_workspace_bytes(tokens, n_seqs), device,
+                                                  (4, tokens), (stats, logp))
         grad, grad_ptr, grad_stride = _grad_rows(logits, grad, with_grad, tokens, vocab, stride)
-        if logp is None:
-            logp = torch.empty(tokens, dtype=f32, device=device)
-        if stats is None:
-            stats = torch.empty(4, dtype=f32, device=device)
     _check(_lib().muon_policy_loss(
         byref(batch), byref(config) if config is not None else None, _vector(old_logp, tokens, f32, "old_logp"),
         None if ref_logp is None else _vector(ref_logp, tokens, f32, "ref_logp"),
@@ -685,14 +693,10 @@ def muon_preference_loss(logits, targets, seq_offsets, ref_logp, mask=None, temp
         raise ValueError(f"seq_offsets: expected 2 P + 1 offsets, got {seq_offsets.numel()}")
     context, handle = _on_stream(stream, device)
     with context:
-        keep, ws, nbytes = _space(workspace, muon_loss_workspace_bytes(tokens, n_seqs), device)
+        (_keep, loss, margins, seq_logp), ws, nbytes = _space(
+            workspace, muon_loss_workspace_bytes(tokens, n_seqs), device, (1, n_seqs // 2, n_seqs),
+            (loss, margins, seq_logp))
         grad, grad_ptr, grad_stride = _grad_rows(logits, grad, with_grad, tokens, vocab, stride)
-        if loss is None:
-            loss = torch.empty(1, dtype=f32, device=device)
-        if margins is None:
-            margins = torch.empty(n_seqs // 2, dtype=f32, device=device)
-        if seq_logp is None:
-            seq_logp = torch.empty(n_seqs, dtype=f32, device=device)
     _check(_lib().muon_preference_loss(
         byref(batch), byref(config) if config is not None else None, _vector(ref_logp, n_seqs, f32, "ref_logp"),
         _vector(seq_offsets, n_seqs + 1, torch.int64, "seq_offsets"), n_seqs // 2, _vector(loss, 1, f32, "loss"),

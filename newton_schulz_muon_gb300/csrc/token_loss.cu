@@ -12,10 +12,14 @@
 //   S = sum_{j != y} e^(z_j - m),   x = z_y - m,
 //   logp = -log1p(S e^-x) where x >= 0, else x - log(S + e^x),
 // which keeps logp's digits (and those of 1 - p_y) where the target is nearly certain.
-// Exponentials are taken in base 2, 2^(c (z - m)) with c = log2(e) / temperature in two
-// floats: the difference is formed first, so that the largest term is exactly 1 and
-// logits at the type's limits do not overflow, and a rounded c alone would shift every
-// row's sum the same way.
+// Exponentials are taken in base 2, 2^(c (z - m)) with c = log2(e) / temperature: the
+// difference is formed first, so that the largest term is exactly 1 and logits at the
+// type's limits do not overflow.  A rounded c would shift every row's sum the same way,
+// which the sum over a sequence adds up.  fp32 logits, which HBM delivers more slowly
+// than the SMs can take them, use c as two floats; for bf16 logits, where every
+// instruction counts, the eight elements of a 16-byte unit take the two floats next to c
+// in the proportion that gives c in the mean (4096 x 131072 policy loss: 0.400 ms with
+// two floats, 0.370 ms this way).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -43,8 +47,11 @@ struct RowArgs {
   const void* logits;
   const int64_t* targets;
   const uint8_t* mask;
+  const int32_t* order;   // live rows, then masked ones; null: by the mask as they come
+  const int32_t* n_live;
   int64_t tokens, vocab, stride, grad_stride;
   float c_hi, c_lo;      // log2(e) / temperature = c_hi + c_lo, c_lo > 0
+  float2 c_mix[4];       // the floats next to it, for the four pairs of a unit of bf16
   float inv_temp;
   float* logp;           // or null
   float2* frame;         // kForward: (m, sum over the whole row) of each row
@@ -84,11 +91,8 @@ struct Vec<float> {
     return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
   }
   static constexpr uint32_t kLowest = 0xFF800000u;  // -inf in every element of a word
-  static __device__ __forceinline__ void drop(uint4& w, int e) {
-    w.x = e == 0 ? kLowest : w.x;
-    w.y = e == 1 ? kLowest : w.y;
-    w.z = e == 2 ? kLowest : w.z;
-    w.w = e == 3 ? kLowest : w.w;
+  static __device__ __forceinline__ uint4 mask_of(int e) {  // the bits of element e
+    return make_uint4(e == 0 ? ~0u : 0u, e == 1 ? ~0u : 0u, e == 2 ? ~0u : 0u, e == 3 ? ~0u : 0u);
   }
   template <int G>
   static __device__ __forceinline__ float max(const uint4 (&w)[G]) {
@@ -118,12 +122,9 @@ struct Vec<__nv_bfloat16> {
                       pack_bf16x2(v[6], v[7]));
   }
   static constexpr uint32_t kLowest = 0xFF80FF80u;
-  static __device__ __forceinline__ void drop(uint4& w, int e) {
-    const uint32_t keep = (e & 1) ? 0x0000FFFFu : 0xFFFF0000u, low = kLowest & ~keep;
-    w.x = (e >> 1) == 0 ? (w.x & keep) | low : w.x;
-    w.y = (e >> 1) == 1 ? (w.y & keep) | low : w.y;
-    w.z = (e >> 1) == 2 ? (w.z & keep) | low : w.z;
-    w.w = (e >> 1) == 3 ? (w.w & keep) | low : w.w;
+  static __device__ __forceinline__ uint4 mask_of(int e) {
+    const uint32_t m = (e & 1) ? 0xFFFF0000u : 0x0000FFFFu;
+    return make_uint4((e >> 1) == 0 ? m : 0u, (e >> 1) == 1 ? m : 0u, (e >> 1) == 2 ? m : 0u, (e >> 1) == 3 ? m : 0u);
   }
   template <int G>
   static __device__ __forceinline__ float max(const uint4 (&w)[G]) {
@@ -139,6 +140,15 @@ struct Vec<__nv_bfloat16> {
   static __device__ __forceinline__ float load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
   static __device__ __forceinline__ void store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 };
+
+// Replaces the masked bits of a unit by those of -inf.
+template <typename T>
+__device__ __forceinline__ void drop(uint4& w, const uint4& m) {
+  w.x = (w.x & ~m.x) | (Vec<T>::kLowest & m.x);
+  w.y = (w.y & ~m.y) | (Vec<T>::kLowest & m.y);
+  w.z = (w.z & ~m.z) | (Vec<T>::kLowest & m.z);
+  w.w = (w.w & ~m.w) | (Vec<T>::kLowest & m.w);
+}
 
 // Two floats at a time (one issue slot).
 struct F2 {
@@ -170,24 +180,34 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
   return r;
 }
 
-// 2^(c (z - m)) of one value and of two.  c_lo > 0, so that a difference of -inf stays one.
+// 2^(c (z - m)) of one value, and of elements 2 i and 2 i + 1 of a unit.  c_lo > 0, so that
+// a difference of -inf stays one.
+template <typename T>
 struct Expo {
   float m, c_hi, c_lo;  // m finite or +inf
+  F2 mix[4];
+  __device__ __forceinline__ Expo(const RowArgs& a, float largest) : c_hi(a.c_hi), c_lo(a.c_lo) {
+    frame(largest);
+    if (sizeof(T) == 2) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        mix[i] = make_f2(a.c_mix[i].x, a.c_mix[i].y);
+        asm volatile("" : "+l"(mix[i].v));  // in registers: packed products take no other operands
+      }
+    }
+  }
+  // With no finite logit but the target's, any finite m gives the right zeros.
+  __device__ __forceinline__ void frame(float largest) { m = largest == -INFINITY ? 0.f : largest; }
   __device__ __forceinline__ float one(float z) const {
     const float d = z - m;
     return ex2(__fmaf_rn(d, c_hi, d * c_lo));
   }
-  __device__ __forceinline__ float2 two(float z0, float z1) const {
-    const F2 d = add2(make_f2(z0, z1), make_f2(-m, -m));
-    const float2 u = split(fma2(d, make_f2(c_hi, c_hi), mul2(d, make_f2(c_lo, c_lo))));
+  __device__ __forceinline__ float2 two(const float* v, int i) const {
+    const F2 d = add2(make_f2(v[2 * i], v[2 * i + 1]), make_f2(-m, -m));
+    const float2 u = split(sizeof(T) == 2 ? mul2(d, mix[i]) : fma2(d, make_f2(c_hi, c_hi), mul2(d, make_f2(c_lo, c_lo))));
     return make_float2(ex2(u.x), ex2(u.y));
   }
 };
-
-// With no finite logit but the target's, any finite m gives the right zeros.
-__device__ __forceinline__ Expo exponent(const RowArgs& a, float m) {
-  return Expo{m == -INFINITY ? 0.f : m, a.c_hi, a.c_lo};
-}
 
 // A partial sum of exponentials: s = sum_j 2^(c (z_j - m)), m the largest z so far
 // (-inf: nothing yet, or only logits of -inf).
@@ -198,7 +218,8 @@ struct Sum {
 // Factor that takes a sum from the frame of m to that of the larger `to`.
 __device__ __forceinline__ float reframe(const RowArgs& a, float m, float to) {
   if (m == to) return 1.f;  // both -inf among them
-  return exponent(a, to).one(m);  // a NaN stays one
+  const float d = m - to;   // a NaN stays one; `to` is not -inf
+  return ex2(__fmaf_rn(d, a.c_hi, d * a.c_lo));
 }
 
 __device__ __forceinline__ Sum merge(const RowArgs& a, const Sum& x, const Sum& y) {
@@ -222,22 +243,22 @@ __device__ __forceinline__ Sum warp_merge(const RowArgs& a, const Sum& t) {
 
 // G 16-byte units of a row.
 template <typename T, int G>
-__device__ __forceinline__ void add_units(const RowArgs& a, Sum& t, const uint4 (&w)[G]) {
+__device__ __forceinline__ void add_units(const RowArgs& a, Expo<T>& x, Sum& t, const uint4 (&w)[G]) {
   constexpr int N = Vec<T>::N;
   const float m = Vec<T>::max(w);
   if (!(m <= t.m)) {
     t.s *= reframe(a, t.m, m);
     t.m = m;
+    x.frame(m);
   }
-  const Expo x = exponent(a, t.m);
   F2 s0 = make_f2(t.s, 0.f), s1 = make_f2(0.f, 0.f);
 #pragma unroll
   for (int g = 0; g < G; ++g) {
     float v[N];
     Vec<T>::unpack(w[g], v);
 #pragma unroll
-    for (int i = 0; i < N; i += 4) {
-      const float2 e0 = x.two(v[i], v[i + 1]), e1 = x.two(v[i + 2], v[i + 3]);
+    for (int i = 0; i < N / 2; i += 2) {
+      const float2 e0 = x.two(v, i), e1 = x.two(v, i + 1);
       s0 = add2(s0, make_f2(e0.x, e0.y));
       s1 = add2(s1, make_f2(e1.x, e1.y));
     }
@@ -251,7 +272,7 @@ __device__ __forceinline__ void add_value(const RowArgs& a, Sum& t, float v) {
     t.s *= reframe(a, t.m, v);
     t.m = v;
   }
-  t.s += exponent(a, t.m).one(v);
+  if (v != -INFINITY) t.s += reframe(a, v, t.m);
 }
 
 // A row's log-probability, and the sum over the whole row in the frame of m.
@@ -344,16 +365,16 @@ __device__ __forceinline__ int edge_of(const Row& r, int64_t vocab, int lane) {
 }
 
 template <typename T>
-__device__ __forceinline__ uint4 scaled_unit(const uint4& w, const Expo& x, float factor) {
+__device__ __forceinline__ uint4 scaled_unit(const uint4& w, const Expo<T>& x, float factor) {
   constexpr int N = Vec<T>::N;
   float v[N];
   Vec<T>::unpack(w, v);
 #pragma unroll
-  for (int i = 0; i < N; i += 2) {
-    const float2 e = x.two(v[i], v[i + 1]);
+  for (int i = 0; i < N / 2; ++i) {
+    const float2 e = x.two(v, i);
     const float2 r = split(mul2(make_f2(e.x, e.y), make_f2(factor, factor)));
-    v[i] = r.x;
-    v[i + 1] = r.y;
+    v[2 * i] = r.x;
+    v[2 * i + 1] = r.y;
   }
   return Vec<T>::pack(v);
 }
@@ -395,7 +416,7 @@ struct RowShared {
   uint64_t full[kSlots];                        // a slot has every partial sum of its row
   Sum slot[kSlots][kMaxCluster][kMaxRowWarps];  // partial sums of a row, from every warp of the cluster
   Factor factor[kSlots];                        // by the row's slot
-  int32_t row[kBatch];      // live rows from the front, masked rows from the back (offset in the batch)
+  int32_t row[kBatch];      // live rows from the front, masked rows from the back
   int32_t unit[kBatch];     // the target's unit in this CTA's part; -1: elsewhere
   int32_t elem[kBatch];     // its element there + 16 times the thread that has it; with unit = -2 the edge lane
   float zy[kBatch];
@@ -510,13 +531,20 @@ __global__ void __launch_bounds__(kMaxRowThreads + 32) row_kernel(const __grid_c
   if (tid < kSlots) mbar_init(&sh.full[tid], ncta > 1 ? 1 : warps);
   fence_mbarrier_init();
   cluster_sync();
+  int64_t n_live = 0;
+  if (a.order) {
+    griddep_wait();
+    waited = true;
+    n_live = __ldcg(a.n_live);
+  }
   const int64_t my_rows = a.tokens > cid ? (a.tokens - cid + n_clusters - 1) / n_clusters : 0;
   for (int64_t first = 0; first < my_rows; first += kBatch) {
     const int rows = (int)min((int64_t)kBatch, my_rows - first);
-    const int64_t t0 = cid + first * n_clusters;  // row r of the batch is t0 + r n_clusters
+    const int64_t p0 = cid + first * n_clusters;  // the batch's rows are p0, p0 + n_clusters, ... of the order
     // live rows in order from the front of sh.row, the others from its back
     for (int r = tid; r < (kBatch + all - 1) / all * all; r += all) {
-      const bool live = r < rows && (a.mask == nullptr || a.mask[t0 + r * n_clusters] != 0);
+      const int64_t p = p0 + r * n_clusters;
+      const bool live = r < rows && (a.order ? p < n_live : a.mask == nullptr || a.mask[p] != 0);
       const unsigned bits = __ballot_sync(0xFFFFFFFFu, live);
       if (lane == 0 && r < kBatch) sh.live[r >> 5] = bits;
     }
@@ -525,10 +553,11 @@ __global__ void __launch_bounds__(kMaxRowThreads + 32) row_kernel(const __grid_c
 #pragma unroll
     for (int k = 0; k < kBatch / 32; ++k) n += __popc(sh.live[k]);
     for (int r = tid; r < rows; r += all) {
+      const int64_t p = p0 + r * n_clusters;
       int before = __popc(sh.live[r >> 5] & ((1u << (r & 31)) - 1));
       for (int k = 0; k < (r >> 5); ++k) before += __popc(sh.live[k]);
       const bool live = (sh.live[r >> 5] >> (r & 31)) & 1;
-      sh.row[live ? before : rows - 1 - (r - before)] = r;
+      sh.row[live ? before : rows - 1 - (r - before)] = a.order ? __ldcg(a.order + p) : (int32_t)p;
     }
     __syncthreads();
 
@@ -536,7 +565,7 @@ __global__ void __launch_bounds__(kMaxRowThreads + 32) row_kernel(const __grid_c
     auto issue = [&](int i, int stage) {
       float e = -INFINITY;
       if (i < n) {
-        const T* z = logits + (t0 + sh.row[i] * n_clusters) * a.stride;
+        const T* z = logits + sh.row[i] * a.stride;
         const Row row = row_of(z, a.vocab);
         if (finisher) {
           const int at = rank == 0 ? edge_of(row, a.vocab, lane) : -1;
@@ -559,7 +588,7 @@ __global__ void __launch_bounds__(kMaxRowThreads + 32) row_kernel(const __grid_c
 
     // the scalars of the batch's live rows
     for (int i = tid; i < n; i += all) {
-      const int64_t t = t0 + sh.row[i] * n_clusters;
+      const int64_t t = sh.row[i];
       const T* z = logits + t * a.stride;
       const int64_t y = a.targets[t];
       const bool in = y >= 0 && y < a.vocab;
@@ -591,10 +620,10 @@ __global__ void __launch_bounds__(kMaxRowThreads + 32) row_kernel(const __grid_c
       waited = true;
     }
     if (kMode == kPolicy)
-      for (int i = tid; i < n; i += all) sh.w[i] = a.weight ? __ldcg(a.weight + t0 + sh.row[i] * n_clusters) : __ldcg(a.inv_count);
+      for (int i = tid; i < n; i += all) sh.w[i] = a.weight ? __ldcg(a.weight + sh.row[i]) : __ldcg(a.inv_count);
     // masked rows
     for (int i = n; i < rows; ++i) {
-      const int64_t t = t0 + sh.row[i] * n_clusters;
+      const int64_t t = sh.row[i];
       if (rank == 0 && tid == 0) {
         if (a.logp) a.logp[t] = 0.f;
         if (kMode == kForward) a.slope[t] = 0.f;
@@ -617,7 +646,7 @@ __global__ void __launch_bounds__(kMaxRowThreads + 32) row_kernel(const __grid_c
     if (finisher) {
       for (int i = 0; i < n; ++i) {
         const int par = i & 1;
-        const int64_t pos = t0 + sh.row[i] * n_clusters;
+        const int64_t pos = sh.row[i];
         // the row's elements outside whole units are this warp's part of the sum
         const bool at_edge = sh.unit[i] == -2 && sh.elem[i] == lane;
         Sum t{-INFINITY, 0.f};
@@ -653,7 +682,7 @@ __global__ void __launch_bounds__(kMaxRowThreads + 32) row_kernel(const __grid_c
             const int e = rank == 0 ? edge_of(row_of(logits + pos * a.stride, a.vocab), a.vocab, lane) : -1;
             __syncwarp();
             factor_arrive(par, all);
-            if (e >= 0) Vec<T>::store(g + e, at_edge ? f.at_y : f.factor * exponent(a, f.m).one(edge[1]));
+            if (e >= 0) Vec<T>::store(g + e, at_edge ? f.at_y : f.factor * Expo<T>(a, f.m).one(edge[1]));
           }
         }
         if (!has_grad) factor_arrive(par, all);  // the other warps keep the row's distance all the same
@@ -663,29 +692,33 @@ __global__ void __launch_bounds__(kMaxRowThreads + 32) row_kernel(const __grid_c
       }
     } else {
       int stage = 0, before = kStages - 1;  // of rows i and i - 1
+      Expo<T> x(a, 0.f);
       for (int i = 0; i <= n; ++i) {
         if (i < n) {
           // the row's sum without its target: this thread's part, then the warp's
           cp_async_wait<kStages - 2>();
-          const Row row = row_of(logits + (t0 + sh.row[i] * n_clusters) * a.stride, a.vocab);
+          const Row row = row_of(logits + sh.row[i] * a.stride, a.vocab);
           int v0;
           const int cnt = part_of(row, v0);
           uint4* src = ring + (size_t)stage * a.stage_vecs;
           const int unit = sh.unit[i], elem = sh.elem[i];
           if (unit >= 0 && elem >> 4 == tid) {  // the target leaves the sum
             uint4 w = src[unit];
-            Vec<T>::drop(w, elem & 15);
+            drop<T>(w, Vec<T>::mask_of(elem & 15));
             src[unit] = w;
           }
           Sum t{-INFINITY, 0.f};
-          for (int l = tid; l < cnt; l += kGroup * nt) {
+          x.frame(t.m);
+          int l = tid;
+          for (; l + (kGroup - 1) * nt < cnt; l += kGroup * nt) {
             uint4 w[kGroup];
 #pragma unroll
-            for (int g = 0; g < kGroup; ++g) {
-              const int j = l + g * nt;
-              w[g] = j < cnt ? src[j] : make_uint4(Vec<T>::kLowest, Vec<T>::kLowest, Vec<T>::kLowest, Vec<T>::kLowest);
-            }
-            add_units<T>(a, t, w);
+            for (int g = 0; g < kGroup; ++g) w[g] = src[l + g * nt];
+            add_units<T>(a, x, t, w);
+          }
+          for (; l < cnt; l += nt) {
+            const uint4 w[1] = {src[l]};
+            add_units<T>(a, x, t, w);
           }
           t = warp_merge(a, t);
           const int slot = (int)((done + i) % kSlots);
@@ -694,7 +727,7 @@ __global__ void __launch_bounds__(kMaxRowThreads + 32) row_kernel(const __grid_c
         if (i > 0 && !has_grad) factor_sync((i - 1) & 1, all);
         if (i > 0 && has_grad) {
           // the gradient of the row before
-          const int64_t t = t0 + sh.row[i - 1] * n_clusters;
+          const int64_t t = sh.row[i - 1];
           const Row row = row_of(logits + t * a.stride, a.vocab);
           int v0;
           const int cnt = part_of(row, v0);
@@ -704,8 +737,19 @@ __global__ void __launch_bounds__(kMaxRowThreads + 32) row_kernel(const __grid_c
           g += (int64_t)v0 * N;
           factor_sync((i - 1) & 1, all);
           const Factor f = sh.factor[(done + i - 1) % kSlots];
-          const Expo x = exponent(a, f.m);
-          for (int l = tid; l < cnt; l += nt) store_unit(g + (int64_t)l * N, scaled_unit<T>(src[l], x, f.factor), whole);
+          x.frame(f.m);
+          int l = tid;
+          if (whole) {
+            for (; l + (kGroup - 1) * nt < cnt; l += kGroup * nt) {
+              uint4 w[kGroup];
+#pragma unroll
+              for (int k = 0; k < kGroup; ++k) w[k] = src[l + k * nt];
+#pragma unroll
+              for (int k = 0; k < kGroup; ++k)
+                store_unit(g + (int64_t)(l + k * nt) * N, scaled_unit<T>(w[k], x, f.factor), true);
+            }
+          }
+          for (; l < cnt; l += nt) store_unit(g + (int64_t)l * N, scaled_unit<T>(src[l], x, f.factor), whole);
           const int unit = sh.unit[i - 1], elem = sh.elem[i - 1];
           if (unit >= 0 && elem >> 4 == tid) Vec<T>::store(g + (int64_t)unit * N + (elem & 15), f.at_y);
         }
@@ -742,10 +786,20 @@ __global__ void __launch_bounds__(kWarpRowThreads, kUnits > 4 ? 2 : 3) warp_row_
   Terms acc;
   griddep_launch_dependents();
   griddep_wait();
-  for (int64_t t = (int64_t)blockIdx.x * kWarpRowWarps + warp; t < a.tokens; t += warps) {
+  const int64_t first = (int64_t)blockIdx.x * kWarpRowWarps + warp;
+  bool next_live = first < a.tokens && (a.mask == nullptr || a.mask[first] != 0);
+  int64_t next_y = first < a.tokens ? a.targets[first] : 0;
+  for (int64_t t = first; t < a.tokens; t += warps) {
+    // the next row's mask and target are on their way while this row is worked on
+    const bool live = next_live;
+    const int64_t y = next_y;
+    if (t + warps < a.tokens) {
+      next_live = a.mask == nullptr || a.mask[t + warps] != 0;
+      next_y = a.targets[t + warps];
+    }
     const T* z = reinterpret_cast<const T*>(a.logits) + t * a.stride;
     T* g = reinterpret_cast<T*>(a.grad) + t * a.grad_stride;
-    if (a.mask != nullptr && a.mask[t] == 0) {
+    if (!live) {
       if (lane == 0 && a.logp) a.logp[t] = 0.f;
       if (kMode == kForward && lane == 0) a.slope[t] = 0.f;
       if (has_grad) {
@@ -766,7 +820,6 @@ __global__ void __launch_bounds__(kWarpRowThreads, kUnits > 4 ? 2 : 3) warp_row_
                                        : make_uint4(Vec<T>::kLowest, Vec<T>::kLowest, Vec<T>::kLowest, Vec<T>::kLowest);
     const int edge = edge_of(row, a.vocab, lane);
     const float zedge = edge >= 0 ? Vec<T>::load(z + edge) : -INFINITY;
-    const int64_t y = a.targets[t];
     const bool in = y >= 0 && y < a.vocab;
     const float zy = in ? Vec<T>::load(z + y) : NAN;
     Position at{0.f, 0.f, 0.f, 0.f};
@@ -778,12 +831,12 @@ __global__ void __launch_bounds__(kWarpRowThreads, kUnits > 4 ? 2 : 3) warp_row_
     }
     const int unit = in && y >= row.head && y < row.tail ? ((int)y - row.head) / N : -1;
     const int owned = unit >= 0 && (unit & 31) == lane ? unit >> 5 : -1;
-    const int elem = ((int)y - row.head) % N;
+    const uint4 bits = Vec<T>::mask_of(((int)y - row.head) % N);
 #pragma unroll
     for (int k = 0; k < kUnits; ++k) {
       int mine = owned;
       asm volatile("" : "+r"(mine));  // one test a register, not an indexed array
-      if (mine == k) Vec<T>::drop(w[k], elem);  // the target leaves the sum
+      if (mine == k) drop<T>(w[k], bits);  // the target leaves the sum
     }
     const bool at_edge = edge >= 0 && edge == y;
     const float others = at_edge ? -INFINITY : zedge;
@@ -791,15 +844,15 @@ __global__ void __launch_bounds__(kWarpRowThreads, kUnits > 4 ? 2 : 3) warp_row_
     s.m = fmaxf(Vec<T>::max(w), others);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s.m = fmaxf(s.m, __shfl_xor_sync(0xFFFFFFFFu, s.m, o));
-    const Expo x = exponent(a, s.m);
+    const Expo<T> x(a, s.m);
     F2 s0 = make_f2(x.one(others), 0.f), s1 = make_f2(0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < kUnits; ++k) {
       float v[N];
       Vec<T>::unpack(w[k], v);
 #pragma unroll
-      for (int i = 0; i < N; i += 4) {
-        const float2 e0 = x.two(v[i], v[i + 1]), e1 = x.two(v[i + 2], v[i + 3]);
+      for (int i = 0; i < N / 2; i += 2) {
+        const float2 e0 = x.two(v, i), e1 = x.two(v, i + 1);
         s0 = add2(s0, make_f2(e0.x, e0.y));
         s1 = add2(s1, make_f2(e1.x, e1.y));
       }
@@ -819,7 +872,11 @@ __global__ void __launch_bounds__(kWarpRowThreads, kUnits > 4 ? 2 : 3) warp_row_
       acc.add(o.terms);
       if (has_grad) {
         const Factor f = row_factor(a, s.m, p.s, p.logp, o.slope);
-        const bool whole = aligned_unit(g + row.head);
+        if (!aligned_unit(g + row.head)) {  // (then g is not z) element by element
+          for (int j = lane; j < a.vocab; j += 32)
+            Vec<T>::store(g + j, j == y ? f.at_y : f.factor * x.one(Vec<T>::load(z + j)));
+          continue;
+        }
         T* dst = g + row.head + lane * N;
         if (kUnits * N > 64) {  // up to 64 exponentials stay in registers from the sum; more are taken again
 #pragma unroll
@@ -828,7 +885,7 @@ __global__ void __launch_bounds__(kWarpRowThreads, kUnits > 4 ? 2 : 3) warp_row_
         }
 #pragma unroll
         for (int k = 0; k < kUnits; ++k)
-          if (k * 32 + lane < row.units) store_unit(dst + k * 32 * N, scaled_unit<T>(w[k], x, f.factor), whole);
+          if (k * 32 + lane < row.units) store_unit(dst + k * 32 * N, scaled_unit<T>(w[k], x, f.factor), true);
         if (owned >= 0) Vec<T>::store(g + y, f.at_y);
         if (edge >= 0) Vec<T>::store(g + edge, at_edge ? f.at_y : f.factor * x.one(zedge));
       }
@@ -886,6 +943,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) stream_kernel(const __grid_con
     const int target_k = unit / nt % kGroup;
     const int edge = tid < 16 ? edge_of(row, a.vocab, tid) : -1;
     Sum s{-INFINITY, 0.f};
+    Expo<T> x(a, s.m);
     for (int l = tid; l < row.units; l += kGroup * nt) {
       uint4 w[kGroup];
 #pragma unroll
@@ -896,9 +954,9 @@ __global__ void __launch_bounds__(kMaxRowThreads) stream_kernel(const __grid_con
       if (l == target_l) {  // the target leaves the sum
 #pragma unroll
         for (int k = 0; k < kGroup; ++k)
-          if (k == target_k) Vec<T>::drop(w[k], elem);
+          if (k == target_k) drop<T>(w[k], Vec<T>::mask_of(elem));
       }
-      add_units<T>(a, s, w);
+      add_units<T>(a, x, s, w);
     }
     const float zedge = edge >= 0 ? Vec<T>::load(z + edge) : -INFINITY;
     if (edge >= 0 && edge != y) add_value(a, s, zedge);
@@ -927,7 +985,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) stream_kernel(const __grid_con
     if (!has_grad) continue;  // red's other half takes the next row
     __syncthreads();
     const Factor f = factor;
-    const Expo x = exponent(a, f.m);
+    x.frame(f.m);
     const bool whole = aligned_unit(g + row.head);
     for (int l = tid; l < row.units; l += nt)
       store_unit(g + row.head + (int64_t)l * N, scaled_unit<T>(src[l], x, f.factor), whole);
@@ -979,7 +1037,7 @@ __global__ void __launch_bounds__(kPieceThreads) backward_kernel(const __grid_co
     const float2 ms = __ldcg(a.frame + t);
     const int64_t y = a.targets[t];
     const Factor f = row_factor(a, ms.x, ms.y, __ldcg(a.logp + t), slope);
-    const Expo x = exponent(a, f.m);
+    const Expo<T> x(a, f.m);
     const bool whole = aligned_unit(g + row.head);
     const int unit = y >= row.head && y < row.tail ? ((int)y - row.head) / N : -1;
 #pragma unroll
@@ -1036,27 +1094,71 @@ __device__ __forceinline__ int64_t live_count(const uint8_t* mask, int64_t a, in
   return block_sum(n);
 }
 
-// Weight of every position under the token mean (or the sum: 1).
+// Lists the live positions, then (from the back) the masked ones, so that every cluster of
+// the row kernel gets as many of each; returns the number of live ones.
+__device__ __forceinline__ int64_t build_order(const uint8_t* mask, int64_t tokens, int32_t* order, int32_t* n_live) {
+  __shared__ int totals[kSmallThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t live = 0;
+  for (int64_t base = 0; base < tokens; base += 8 * kSmallThreads) {
+    const int64_t t = base + 8 * threadIdx.x;
+    unsigned bits = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (t + j < tokens && mask[t + j] != 0) bits |= 1u << j;
+    const int own = __popc(bits);
+    int upto = own;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    if (lane == 31) totals[warp] = upto;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kSmallThreads / 32; ++w) {
+      before += w < warp ? totals[w] : 0;
+      all += totals[w];
+    }
+    int64_t front = live + before + upto - own, back = tokens - 1 - (t - front);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (t + j >= tokens) break;
+      order[(bits >> j) & 1 ? front++ : back--] = (int32_t)(t + j);
+    }
+    live += all;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) *n_live = (int32_t)live;
+  return live;
+}
+
+// Weight of every position under the token mean (or the sum: 1); the order if it is asked for.
 __global__ void __launch_bounds__(kSmallThreads) count_kernel(const uint8_t* mask, int64_t tokens, int mean,
-                                                              float* inv_count, unsigned* ticket) {
+                                                              float* inv_count, unsigned* ticket, int32_t* order,
+                                                              int32_t* n_live) {
   griddep_launch_dependents();
   if (threadIdx.x == 0) *ticket = 0;
   float w = 1.f;
+  int64_t n = -1;
+  if (order) n = build_order(mask, tokens, order, n_live);
   if (mean) {
-    const int64_t n = live_count(mask, 0, tokens);
+    if (n < 0) n = live_count(mask, 0, tokens);
     w = 1.f / (float)(n < 1 ? 1 : n);
   }
   if (threadIdx.x == 0) *inv_count = w;
 }
 
 // Sequence mean: one CTA a sequence writes the weights of its positions; CTA n_seqs
-// clears those before the first and after the last.
+// clears those before the first and after the last, and does what concerns all.
 __global__ void __launch_bounds__(kSmallThreads) weight_kernel(const uint8_t* mask, int64_t tokens,
                                                                const int64_t* offsets, int64_t n_seqs, float* weight,
-                                                               unsigned* ticket) {
+                                                               unsigned* ticket, int32_t* order, int32_t* n_live) {
   griddep_launch_dependents();
   const int64_t q = blockIdx.x;
   if (q == n_seqs) {
+    if (order) build_order(mask, tokens, order, n_live);
     if (threadIdx.x == 0) *ticket = 0;
     const int64_t a = clamp_offset(offsets[0], 0, tokens), b = clamp_offset(offsets[n_seqs], a, tokens);
     for (int64_t t = threadIdx.x; t < a; t += kSmallThreads) weight[t] = 0.f;
@@ -1199,6 +1301,11 @@ RowArgs row_args(const muon_token_batch* b) {
   a.c_hi = std::nextafterf((float)c, 0.f);
   if ((double)a.c_hi >= c) a.c_hi = std::nextafterf(a.c_hi, 0.f);
   a.c_lo = (float)(c - (double)a.c_hi);
+  // c = down + (up - down) k / 8 within a sixteenth of their distance
+  const float near = (float)c, down = (double)near <= c ? near : std::nextafterf(near, 0.f);
+  const float up = std::nextafterf(down, INFINITY);
+  const int k = (int)std::lround(8.0 * (c - (double)down) / ((double)up - (double)down));
+  for (int i = 0; i < 4; ++i) a.c_mix[i] = make_float2(2 * i < k ? up : down, 2 * i + 1 < k ? up : down);
   a.inv_temp = (float)(1.0 / (double)b->temperature);
   a.grad_scale = 1.f;
   return a;
@@ -1301,7 +1408,8 @@ cudaError_t launch_rows_as(RowArgs a, int32_t dtype, int sms, bool dependent, cu
     return launch(kernel, (int)(ctas < most ? ctas : most), kWarpRowThreads, 0, s, 1, dependent, a);
   }
   if (shape.cluster == 0) {
-    const int64_t most = (int64_t)sms * (2048 / shape.threads) < kMaxParts ? (int64_t)sms * (2048 / shape.threads) : kMaxParts;
+    // without partial sums to keep, a CTA for each row balances masked ones by itself
+    const int64_t most = kMode == kPolicy ? kMaxParts : rows;
     return launch(stream_kernel<T, kMode>, (int)(rows < most ? rows : most), shape.threads, 0, s, 1, dependent, a);
   }
   for (a.log_cluster = 0; (1 << a.log_cluster) < shape.cluster;) ++a.log_cluster;
@@ -1337,6 +1445,7 @@ size_t round16(size_t v) { return (v + 15) / 16 * 16; }
 struct LossSpace {
   float* inv_count;
   unsigned* ticket;
+  int32_t *n_live, *order;
   double* partials;
   float2* frame;
   float *slope, *logp, *weight, *pair_loss;
@@ -1354,6 +1463,8 @@ LossSpace loss_space(void* ws, int64_t tokens, int64_t n_seqs) {
   };
   s.inv_count = static_cast<float*>(take(4));
   s.ticket = static_cast<unsigned*>(take(4));
+  s.n_live = static_cast<int32_t*>(take(4));
+  s.order = static_cast<int32_t*>(take(4 * (size_t)tokens));
   s.partials = static_cast<double*>(take((size_t)kMaxParts * 4 * sizeof(double)));
   s.frame = static_cast<float2*>(take(8 * (size_t)tokens));
   s.slope = static_cast<float*>(take(4 * (size_t)tokens));
@@ -1435,14 +1546,21 @@ muon_status muon_policy_loss(const muon_token_batch* batch, const muon_policy_co
   if ((st = find_device(&sms)) != MUON_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
+  // Clusters that take several rows each get as many masked ones each; with few rows, or a
+  // warp a row, the list would only be waited for (4096 x 131072, a fifth masked at random:
+  // 0.365 ms without it, 0.352 ms with it; 20011 x 4099: 0.075 and 0.086 ms).
+  const RowShape shape = row_shape(batch->vocab, batch->dtype, batch->tokens, sms, grad != nullptr);
+  int32_t* order = batch->mask && shape.cluster > 0 && batch->tokens * shape.cluster >= 4ll * sms ? ws.order : nullptr;
   if (by_seq)
     e = launch(weight_kernel, (int)n_seqs + 1, kSmallThreads, 0, s, 1, false, batch->mask, (int64_t)batch->tokens,
-               seq_offsets, (int64_t)n_seqs, ws.weight, ws.ticket);
+               seq_offsets, (int64_t)n_seqs, ws.weight, ws.ticket, order, ws.n_live);
   else
     e = launch(count_kernel, 1, kSmallThreads, 0, s, 1, false, batch->mask, (int64_t)batch->tokens,
-               (int)(c.reduction == MUON_REDUCE_TOKEN_MEAN), ws.inv_count, ws.ticket);
+               (int)(c.reduction == MUON_REDUCE_TOKEN_MEAN), ws.inv_count, ws.ticket, order, ws.n_live);
   if (e != cudaSuccess) return cuda_error(e);
   RowArgs a = row_args(batch);
+  a.order = order;
+  a.n_live = ws.n_live;
   a.logp = logp;
   a.old_logp = old_logp;
   a.ref_logp = c.kl_beta != 0.f ? ref_logp : nullptr;
