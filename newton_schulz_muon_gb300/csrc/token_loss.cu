@@ -229,12 +229,16 @@ __device__ __forceinline__ Sum merge(const RowArgs& a, const Sum& x, const Sum& 
   return r;
 }
 
+__device__ __forceinline__ float warp_max(float v) {  // of the numbers among them, like fmaxf
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
 // Merges the lanes' sums: the largest m first, then one factor a lane.
 __device__ __forceinline__ Sum warp_merge(const RowArgs& a, const Sum& t) {
   Sum r;
-  r.m = t.m;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) r.m = fmaxf(r.m, __shfl_xor_sync(0xFFFFFFFFu, r.m, o));
+  r.m = warp_max(t.m);
   r.s = t.s * reframe(a, t.m, r.m);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) r.s += __shfl_xor_sync(0xFFFFFFFFu, r.s, o);
@@ -398,10 +402,9 @@ __device__ __forceinline__ bool aligned_unit(const T* g) {
   return (reinterpret_cast<uint64_t>(g) & 15) == 0;
 }
 
-constexpr int kMaxRowThreads = 512;                   // that hold a row's units
-constexpr int kMaxRowWarps = kMaxRowThreads / 32 + 1;  // and the finishing warp
+constexpr int kMaxRowThreads = 512;  // that hold units of a row, beside the finishing warp
 constexpr int kMaxCluster = 8;
-constexpr int kBatch = 256;  // rows whose scalars a CTA holds at a time
+constexpr int kInfo = 32;    // rows whose places and scalars a CTA holds at a time
 constexpr int kSlots = 4;    // rows whose partial sums may be on their way
 constexpr int kGroup = 4;    // 16-byte units a thread takes at a time
 
@@ -411,18 +414,22 @@ struct StatsShared {
   int32_t last;
 };
 
-// Shared memory beside the ring.
+// Shared memory beside the ring of rows: the partial sums of kSlots rows follow it, from
+// every warp of the cluster.
 struct RowShared {
-  uint64_t full[kSlots];                        // a slot has every partial sum of its row
-  Sum slot[kSlots][kMaxCluster][kMaxRowWarps];  // partial sums of a row, from every warp of the cluster
-  Factor factor[kSlots];                        // by the row's slot
-  int32_t row[kBatch];      // live rows from the front, masked rows from the back
-  int32_t unit[kBatch];     // the target's unit in this CTA's part; -1: elsewhere
-  int32_t elem[kBatch];     // its element there + 16 times the thread that has it; with unit = -2 the edge lane
-  float zy[kBatch];
-  float old_logp[kBatch], ref[kBatch], adv[kBatch], w[kBatch];
-  uint32_t live[kBatch / 32];
+  uint64_t full[kSlots];   // a slot has every partial sum of its row
   StatsShared stats;
+  Factor factor[kSlots];   // by the row's slot
+  // live rows by index modulo kInfo
+  const uint4* src[kInfo]; // this CTA's units of the logits
+  void* dst[kInfo];        // the gradient's elements there
+  int32_t units[kInfo];    // how many; negative (~units): the gradient is not aligned there
+  int32_t row[kInfo];
+  int32_t unit[kInfo];     // the target's unit in this CTA's part; -1: elsewhere
+  int32_t elem[kInfo];     // its element there + 16 times the thread that has it; with unit = -2 the edge lane
+  float zy[kInfo];
+  float old_logp[kInfo], ref[kInfo], adv[kInfo], w[kInfo];
+  uint32_t live;
 };
 
 // Barriers 1 and 2 (by the row's parity): the finishing warp has written a row's factor.
@@ -516,6 +523,8 @@ __global__ void __launch_bounds__(kMaxRowThreads + 32) row_kernel(const __grid_c
   const bool finisher = warp == warps - 1;
   const T* const logits = reinterpret_cast<const T*>(a.logits);
   T* const grads = reinterpret_cast<T*>(a.grad);
+  const int64_t my_rows = a.tokens > cid ? (a.tokens - cid + n_clusters - 1) / n_clusters : 0;
+  Sum* const slots = reinterpret_cast<Sum*>(&sh + 1);  // [kSlots][ncta][warps]
   Terms acc;  // of the finishing warp
 
   auto part_of = [&](const Row& row, int& v0) {  // this CTA's units of a row
@@ -525,250 +534,300 @@ __global__ void __launch_bounds__(kMaxRowThreads + 32) row_kernel(const __grid_c
   };
 
   griddep_launch_dependents();
-  bool waited = false, arrived = true;
-  int64_t done = 0;  // rows summed in earlier batches
   // a cluster's sums are counted in bytes, one CTA's (no cluster launch) in arrivals
   if (tid < kSlots) mbar_init(&sh.full[tid], ncta > 1 ? 1 : warps);
   fence_mbarrier_init();
   cluster_sync();
-  int64_t n_live = 0;
-  if (a.order) {
-    griddep_wait();
-    waited = true;
-    n_live = __ldcg(a.n_live);
-  }
-  const int64_t my_rows = a.tokens > cid ? (a.tokens - cid + n_clusters - 1) / n_clusters : 0;
-  for (int64_t first = 0; first < my_rows; first += kBatch) {
-    const int rows = (int)min((int64_t)kBatch, my_rows - first);
-    const int64_t p0 = cid + first * n_clusters;  // the batch's rows are p0, p0 + n_clusters, ... of the order
-    // live rows in order from the front of sh.row, the others from its back
-    for (int r = tid; r < (kBatch + all - 1) / all * all; r += all) {
-      const int64_t p = p0 + r * n_clusters;
-      const bool live = r < rows && (a.order ? p < n_live : a.mask == nullptr || a.mask[p] != 0);
-      const unsigned bits = __ballot_sync(0xFFFFFFFFu, live);
-      if (lane == 0 && r < kBatch) sh.live[r >> 5] = bits;
-    }
-    __syncthreads();
-    int n = 0;
-#pragma unroll
-    for (int k = 0; k < kBatch / 32; ++k) n += __popc(sh.live[k]);
-    for (int r = tid; r < rows; r += all) {
-      const int64_t p = p0 + r * n_clusters;
-      int before = __popc(sh.live[r >> 5] & ((1u << (r & 31)) - 1));
-      for (int k = 0; k < (r >> 5); ++k) before += __popc(sh.live[k]);
-      const bool live = (sh.live[r >> 5] >> (r & 31)) & 1;
-      sh.row[live ? before : rows - 1 - (r - before)] = a.order ? __ldcg(a.order + p) : (int32_t)p;
-    }
-    __syncthreads();
 
-    // Starts the copy of live row i; the finishing warp's lanes get their elements of it.
-    auto issue = [&](int i, int stage) {
-      float e = -INFINITY;
-      if (i < n) {
-        const T* z = logits + sh.row[i] * a.stride;
-        const Row row = row_of(z, a.vocab);
-        if (finisher) {
-          const int at = rank == 0 ? edge_of(row, a.vocab, lane) : -1;
-          if (at >= 0) e = Vec<T>::load(z + at);
-        } else {
-          int v0;
-          const int cnt = part_of(row, v0);
-          const uint4* src = reinterpret_cast<const uint4*>(z + row.head) + v0;
-          uint4* dst = ring + (size_t)stage * a.stage_vecs;
-          for (int l = tid; l < cnt; l += nt) cp_async_16(dst + l, src + l);
-        }
-      }
-      cp_async_commit();
-      return e;
-    };
-    float edge[kStages];  // of rows i - 1, i, i + 1, ...
-    edge[0] = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) edge[i + 1] = issue(i, i);
-
-    // the scalars of the batch's live rows
-    for (int i = tid; i < n; i += all) {
-      const int64_t t = sh.row[i];
-      const T* z = logits + t * a.stride;
-      const int64_t y = a.targets[t];
-      const bool in = y >= 0 && y < a.vocab;
-      sh.zy[i] = in ? Vec<T>::load(z + y) : NAN;
-      const Row row = row_of(z, a.vocab);
-      int v0;
-      const int cnt = part_of(row, v0);
-      int unit = -1, elem = 0;
-      if (in && y >= row.head && y < row.tail) {
-        const int u = ((int)y - row.head) / N - v0;
-        if (u >= 0 && u < cnt) {
-          unit = u;
-          elem = ((int)y - row.head) % N + 16 * (u % nt);
-        }
-      } else if (in) {
-        unit = -2;
-        elem = (int)(y < row.head ? y : 8 + y - row.tail);
-      }
-      sh.unit[i] = unit;
-      sh.elem[i] = elem;
-      if (kMode == kPolicy) {
-        sh.old_logp[i] = a.old_logp[t];
-        sh.ref[i] = a.ref_logp ? a.ref_logp[t] : 0.f;
-        sh.adv[i] = a.adv[t];
-      }
-    }
-    if (!waited) {
+  // The cluster's n live rows.  With the list of all live rows (or no mask) they are its
+  // entries cid, cid + n_clusters, ...; without it there are at most kInfo rows, live ones
+  // and then the others in sh.row.
+  int n;
+  int64_t n_live = a.tokens;
+  const bool listed = a.order != nullptr || a.mask == nullptr;
+  auto row_at = [&](int64_t i) {
+    const int64_t p = cid + i * n_clusters;
+    return a.order ? __ldcg(a.order + p) : (int32_t)p;
+  };
+  if (listed) {
+    if (a.order) {
       griddep_wait();
-      waited = true;
+      n_live = __ldcg(a.n_live);
     }
-    if (kMode == kPolicy)
-      for (int i = tid; i < n; i += all) sh.w[i] = a.weight ? __ldcg(a.weight + sh.row[i]) : __ldcg(a.inv_count);
-    // masked rows
-    for (int i = n; i < rows; ++i) {
-      const int64_t t = sh.row[i];
-      if (rank == 0 && tid == 0) {
-        if (a.logp) a.logp[t] = 0.f;
-        if (kMode == kForward) a.slope[t] = 0.f;
-      }
-      if (!has_grad) continue;
-      T* g = grads + t * a.grad_stride;
-      const Row row = row_of(g, a.vocab);
-      if (finisher) {
-        const int e = rank == 0 ? edge_of(row, a.vocab, lane) : -1;
-        if (e >= 0) Vec<T>::store(g + e, 0.f);
-      } else {
-        int v0;
-        const int cnt = part_of(row, v0);
-        uint4* dst = reinterpret_cast<uint4*>(g + row.head) + v0;
-        for (int l = tid; l < cnt; l += nt) dst[l] = make_uint4(0, 0, 0, 0);
-      }
+    n = (int)(n_live > cid ? (n_live - cid + n_clusters - 1) / n_clusters : 0);
+    if (tid < kInfo && tid < n) sh.row[tid] = row_at(tid);
+  } else {
+    if (warp == 0) {
+      const bool live = tid < my_rows && a.mask[cid + tid * n_clusters] != 0;
+      const unsigned bits = __ballot_sync(0xFFFFFFFFu, live);
+      const int before = __popc(bits & ((1u << lane) - 1));
+      if (tid < my_rows) sh.row[live ? before : (int)my_rows - 1 - (tid - before)] = (int32_t)(cid + tid * n_clusters);
+      if (lane == 0) sh.live = bits;
     }
     __syncthreads();
+    n = __popc(sh.live);
+  }
+  auto put_place = [&](int i, int64_t t) {
+    const T* z = logits + t * a.stride;
+    T* g = grads + t * a.grad_stride;
+    const Row row = row_of(z, a.vocab);
+    int v0;
+    const int cnt = part_of(row, v0);
+    const int64_t first = row.head + (int64_t)v0 * N;
+    const int k = i % kInfo;
+    sh.row[k] = (int32_t)t;
+    sh.src[k] = reinterpret_cast<const uint4*>(z + first);
+    sh.dst[k] = g + first;
+    sh.units[k] = !has_grad || aligned_unit(g + first) ? cnt : ~cnt;
+  };
+  if (warp == 0) {
+    __syncwarp();
+    if (lane < n) put_place(lane, sh.row[lane]);
+  }
+  __syncthreads();
 
-    if (finisher) {
-      for (int i = 0; i < n; ++i) {
-        const int par = i & 1;
-        const int64_t pos = sh.row[i];
-        // the row's elements outside whole units are this warp's part of the sum
-        const bool at_edge = sh.unit[i] == -2 && sh.elem[i] == lane;
-        Sum t{-INFINITY, 0.f};
-        if (!at_edge) add_value(a, t, edge[1]);
-        t = warp_merge(a, t);
-        const int slot = (int)((done + i) % kSlots);
-        if (ncta > 1 && lane == 0) mbar_arrive_expect_tx(&sh.full[slot], ncta * warps * (uint32_t)sizeof(Sum));
-        if (lane < ncta) send(&sh.slot[slot][rank][warp], &sh.full[slot], ncta, lane, t);
-        __syncwarp();
-        arrived = arrived && mbar_wait(&sh.full[slot], (uint32_t)((done + i) / kSlots) & 1, nullptr, nullptr);
-        arrived = __all_sync(0xFFFFFFFFu, arrived);
-        // every warp of every CTA, in the same order in each
-        t = Sum{-INFINITY, 0.f};
-        for (int k = lane; k < ncta * kMaxRowWarps; k += 32)
-          if (k % kMaxRowWarps < warps) t = merge(a, t, sh.slot[slot][k / kMaxRowWarps][k % kMaxRowWarps]);
-        t = warp_merge(a, t);
-        if (!arrived) t.s = NAN;  // a wait ran out: the results say so
-        const Prob p = row_prob(a, t, sh.zy[i]);
-        const bool writer = rank == 0 && lane == 0;
-        if (writer && a.logp) a.logp[pos] = p.logp;
-        if (kMode == kForward && writer) {
-          a.frame[pos] = make_float2(t.m, p.s);
-          a.slope[pos] = 0.f;
-        }
-        if (kMode == kPolicy) {
-          const Position at{sh.old_logp[i], sh.ref[i], sh.adv[i], sh.w[i]};
-          const Outcome o = policy_terms(a, at, p.logp);
-          acc.add(o.terms);
-          if (has_grad) {
-            const Factor f = row_factor(a, t.m, p.s, p.logp, o.slope);
-            if (lane == 0) sh.factor[slot] = f;
-            T* g = grads + pos * a.grad_stride;
-            const int e = rank == 0 ? edge_of(row_of(logits + pos * a.stride, a.vocab), a.vocab, lane) : -1;
-            __syncwarp();
-            factor_arrive(par, all);
-            if (e >= 0) Vec<T>::store(g + e, at_edge ? f.at_y : f.factor * Expo<T>(a, f.m).one(edge[1]));
-          }
-        }
-        if (!has_grad) factor_arrive(par, all);  // the other warps keep the row's distance all the same
-#pragma unroll
-        for (int k = 0; k + 1 < kStages; ++k) edge[k] = edge[k + 1];
-        edge[kStages - 1] = issue(i + kStages - 1, 0);
+  // Starts the copy of live row i; the finishing warp's lanes get their elements of it.
+  auto issue = [&](int i, int stage) {
+    float e = -INFINITY;
+    if (i < n) {
+      const int k = i % kInfo;
+      if (finisher) {
+        const T* z = logits + sh.row[k] * a.stride;
+        const int at = rank == 0 ? edge_of(row_of(z, a.vocab), a.vocab, lane) : -1;
+        if (at >= 0) e = Vec<T>::load(z + at);
+      } else {
+        const int cnt = max(sh.units[k], ~sh.units[k]);
+        const uint4* src = sh.src[k];
+        uint4* dst = ring + (size_t)stage * a.stage_vecs;
+        for (int l = tid; l < cnt; l += nt) cp_async_16(dst + l, src + l);
       }
-    } else {
-      int stage = 0, before = kStages - 1;  // of rows i and i - 1
-      Expo<T> x(a, 0.f);
-      for (int i = 0; i <= n; ++i) {
-        if (i < n) {
-          // the row's sum without its target: this thread's part, then the warp's
-          cp_async_wait<kStages - 2>();
-          const Row row = row_of(logits + sh.row[i] * a.stride, a.vocab);
-          int v0;
-          const int cnt = part_of(row, v0);
-          uint4* src = ring + (size_t)stage * a.stage_vecs;
-          const int unit = sh.unit[i], elem = sh.elem[i];
-          if (unit >= 0 && elem >> 4 == tid) {  // the target leaves the sum
-            uint4 w = src[unit];
-            drop<T>(w, Vec<T>::mask_of(elem & 15));
-            src[unit] = w;
-          }
-          Sum t{-INFINITY, 0.f};
-          x.frame(t.m);
-          int l = tid;
+    }
+    cp_async_commit();
+    return e;
+  };
+  float edge[kStages];  // of rows i - 1, i, i + 1, ...
+  edge[0] = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) edge[i + 1] = issue(i, i);
+
+  // A row's scalars, in three steps whose loads depend on one another.
+  struct Info {
+    int32_t row;
+    int64_t y;
+    float zy, old_logp, ref, adv, w;
+  };
+  auto load_scalars = [&](Info& f) {
+    f.y = a.targets[f.row];
+    if (kMode == kPolicy) {
+      f.old_logp = a.old_logp[f.row];
+      f.ref = a.ref_logp ? a.ref_logp[f.row] : 0.f;
+      f.adv = a.adv[f.row];
+    }
+  };
+  auto load_target = [&](Info& f) {
+    f.zy = f.y >= 0 && f.y < a.vocab ? Vec<T>::load(logits + f.row * a.stride + f.y) : NAN;
+  };
+  auto load_weight = [&](Info& f) {
+    if (kMode == kPolicy) f.w = a.weight ? __ldcg(a.weight + f.row) : __ldcg(a.inv_count);
+  };
+  auto put_scalars = [&](int i, const Info& f) {
+    const int k = i % kInfo;
+    const Row row = row_of(logits + f.row * a.stride, a.vocab);
+    int v0;
+    const int cnt = part_of(row, v0);
+    int unit = -1, elem = 0;
+    if (f.y >= row.head && f.y < row.tail) {
+      const int u = ((int)f.y - row.head) / N - v0;
+      if (u >= 0 && u < cnt) {
+        unit = u;
+        elem = ((int)f.y - row.head) % N + 16 * (u % nt);
+      }
+    } else if (f.y >= 0 && f.y < a.vocab) {
+      unit = -2;
+      elem = (int)(f.y < row.head ? f.y : 8 + f.y - row.tail);
+    }
+    sh.unit[k] = unit;
+    sh.elem[k] = elem;
+    sh.zy[k] = f.zy;
+    if (kMode == kPolicy) {
+      sh.old_logp[k] = f.old_logp;
+      sh.ref[k] = f.ref;
+      sh.adv[k] = f.adv;
+      sh.w[k] = f.w;
+    }
+  };
+  Info info = {};
+  const bool mine = tid < kInfo && tid < n;
+  if (mine) {
+    info.row = sh.row[tid];
+    load_scalars(info);
+    load_target(info);
+  }
+  griddep_wait();
+  if (mine) {
+    load_weight(info);
+    put_scalars(tid, info);
+  }
+  __syncthreads();
+
+  bool arrived = true;
+  if (finisher) {
+    for (int i = 0; i < n; ++i) {
+      const int par = i & 1, k = i % kInfo, slot = i % kSlots;
+      const int64_t pos = sh.row[k];
+      // the row's elements outside whole units are this warp's part of the sum
+      const bool at_edge = sh.unit[k] == -2 && sh.elem[k] == lane;
+      Sum t{-INFINITY, 0.f};
+      if (!at_edge) add_value(a, t, edge[1]);
+      t = warp_merge(a, t);
+      if (ncta > 1 && lane == 0) mbar_arrive_expect_tx(&sh.full[slot], ncta * warps * (uint32_t)sizeof(Sum));
+      if (lane < ncta) send(slots + (slot * ncta + rank) * warps + warp, &sh.full[slot], ncta, lane, t);
+      // The 16 rows after this row's 16, a step a row, into the half that held the 16 before:
+      // their gradients have been written once the sums of the row two before this are here.
+      const int step = i & (kInfo / 2 - 1), base = i - step + kInfo / 2;
+      if (base >= kInfo && base < n) {
+        const bool in = lane < kInfo / 2 && base + lane < n;
+        if (step == 0 && in) info.row = row_at(base + lane);
+        if (step == 1 && in) load_scalars(info);
+        if (step == 2 && in) load_target(info);
+        if (step == 3 && in) load_weight(info);
+        if (step == 4 && in) {
+          put_place(base + lane, info.row);
+          put_scalars(base + lane, info);
+        }
+      }
+      __syncwarp();
+      arrived = arrived && mbar_wait(&sh.full[slot], (uint32_t)(i / kSlots) & 1, nullptr, nullptr);
+      arrived = __all_sync(0xFFFFFFFFu, arrived);
+      // every warp of every CTA, in the same order in each
+      t = Sum{-INFINITY, 0.f};
+      for (int j = lane; j < ncta * warps; j += 32) t = merge(a, t, slots[slot * ncta * warps + j]);
+      t = warp_merge(a, t);
+      if (!arrived) t.s = NAN;  // a wait ran out: the results say so
+      const Prob p = row_prob(a, t, sh.zy[k]);
+      const bool writer = rank == 0 && lane == 0;
+      if (writer && a.logp) a.logp[pos] = p.logp;
+      if (kMode == kForward && writer) {
+        a.frame[pos] = make_float2(t.m, p.s);
+        a.slope[pos] = 0.f;
+      }
+      if (kMode == kPolicy) {
+        const Position at{sh.old_logp[k], sh.ref[k], sh.adv[k], sh.w[k]};
+        const Outcome o = policy_terms(a, at, p.logp);
+        acc.add(o.terms);
+        if (has_grad) {
+          const Factor f = row_factor(a, t.m, p.s, p.logp, o.slope);
+          if (lane == 0) sh.factor[slot] = f;
+          T* g = grads + pos * a.grad_stride;
+          const int e = rank == 0 ? edge_of(row_of(logits + pos * a.stride, a.vocab), a.vocab, lane) : -1;
+          __syncwarp();
+          factor_arrive(par, all);
+          if (e >= 0) Vec<T>::store(g + e, at_edge ? f.at_y : f.factor * Expo<T>(a, f.m).one(edge[1]));
+        }
+      }
+      if (!has_grad) factor_arrive(par, all);  // the other warps keep the row's distance all the same
+#pragma unroll
+      for (int j = 0; j + 1 < kStages; ++j) edge[j] = edge[j + 1];
+      edge[kStages - 1] = issue(i + kStages - 1, 0);
+    }
+  } else {
+    int stage = 0, before = kStages - 1;  // of rows i and i - 1
+    Expo<T> x(a, 0.f);
+    for (int i = 0; i <= n; ++i) {
+      if (i < n) {
+        // the row's sum without its target: this thread's part, then the warp's
+        cp_async_wait<kStages - 2>();
+        const int k = i % kInfo, slot = i % kSlots;
+        const int cnt = max(sh.units[k], ~sh.units[k]);
+        uint4* src = ring + (size_t)stage * a.stage_vecs;
+        const int unit = sh.unit[k], elem = sh.elem[k];
+        if (unit >= 0 && elem >> 4 == tid) {  // the target leaves the sum
+          uint4 w = src[unit];
+          drop<T>(w, Vec<T>::mask_of(elem & 15));
+          src[unit] = w;
+        }
+        Sum t{-INFINITY, 0.f};
+        x.frame(t.m);
+        int l = tid;
+        for (; l + (kGroup - 1) * nt < cnt; l += kGroup * nt) {
+          uint4 w[kGroup];
+#pragma unroll
+          for (int g = 0; g < kGroup; ++g) w[g] = src[l + g * nt];
+          add_units<T>(a, x, t, w);
+        }
+        if (l + (kGroup - 2) * nt < cnt) {  // all but one of a group
+          uint4 w[kGroup];
+#pragma unroll
+          for (int g = 0; g < kGroup - 1; ++g) w[g] = src[l + g * nt];
+          w[kGroup - 1] = make_uint4(Vec<T>::kLowest, Vec<T>::kLowest, Vec<T>::kLowest, Vec<T>::kLowest);
+          add_units<T>(a, x, t, w);
+          l = cnt;
+        }
+        for (; l < cnt; l += nt) {
+          const uint4 w[1] = {src[l]};
+          add_units<T>(a, x, t, w);
+        }
+        t = warp_merge(a, t);
+        if (lane < ncta) send(slots + (slot * ncta + rank) * warps + warp, &sh.full[slot], ncta, lane, t);
+      }
+      if (i > 0 && !has_grad) factor_sync((i - 1) & 1, all);
+      if (i > 0 && has_grad) {
+        // the gradient of the row before
+        const int k = (i - 1) % kInfo;
+        const bool whole = sh.units[k] >= 0;
+        const int cnt = max(sh.units[k], ~sh.units[k]);
+        const uint4* src = ring + (size_t)before * a.stage_vecs;
+        T* g = static_cast<T*>(sh.dst[k]);
+        factor_sync((i - 1) & 1, all);
+        const Factor f = sh.factor[(i - 1) % kSlots];
+        x.frame(f.m);
+        int l = tid;
+        if (whole) {
           for (; l + (kGroup - 1) * nt < cnt; l += kGroup * nt) {
             uint4 w[kGroup];
 #pragma unroll
-            for (int g = 0; g < kGroup; ++g) w[g] = src[l + g * nt];
-            add_units<T>(a, x, t, w);
-          }
-          for (; l < cnt; l += nt) {
-            const uint4 w[1] = {src[l]};
-            add_units<T>(a, x, t, w);
-          }
-          t = warp_merge(a, t);
-          const int slot = (int)((done + i) % kSlots);
-          if (lane < ncta) send(&sh.slot[slot][rank][warp], &sh.full[slot], ncta, lane, t);
-        }
-        if (i > 0 && !has_grad) factor_sync((i - 1) & 1, all);
-        if (i > 0 && has_grad) {
-          // the gradient of the row before
-          const int64_t t = sh.row[i - 1];
-          const Row row = row_of(logits + t * a.stride, a.vocab);
-          int v0;
-          const int cnt = part_of(row, v0);
-          const uint4* src = ring + (size_t)before * a.stage_vecs;
-          T* g = grads + t * a.grad_stride + row.head;
-          const bool whole = aligned_unit(g);
-          g += (int64_t)v0 * N;
-          factor_sync((i - 1) & 1, all);
-          const Factor f = sh.factor[(done + i - 1) % kSlots];
-          x.frame(f.m);
-          int l = tid;
-          if (whole) {
-            for (; l + (kGroup - 1) * nt < cnt; l += kGroup * nt) {
-              uint4 w[kGroup];
+            for (int j = 0; j < kGroup; ++j) w[j] = src[l + j * nt];
 #pragma unroll
-              for (int k = 0; k < kGroup; ++k) w[k] = src[l + k * nt];
-#pragma unroll
-              for (int k = 0; k < kGroup; ++k)
-                store_unit(g + (int64_t)(l + k * nt) * N, scaled_unit<T>(w[k], x, f.factor), true);
-            }
+            for (int j = 0; j < kGroup; ++j)
+              store_unit(g + (int64_t)(l + j * nt) * N, scaled_unit<T>(w[j], x, f.factor), true);
           }
-          for (; l < cnt; l += nt) store_unit(g + (int64_t)l * N, scaled_unit<T>(src[l], x, f.factor), whole);
-          const int unit = sh.unit[i - 1], elem = sh.elem[i - 1];
-          if (unit >= 0 && elem >> 4 == tid) Vec<T>::store(g + (int64_t)unit * N + (elem & 15), f.at_y);
         }
-        if (i < n) issue(i + kStages - 1, before);
-        before = stage;
-        stage = stage + 1 == kStages ? 0 : stage + 1;
+        for (; l < cnt; l += nt) store_unit(g + (int64_t)l * N, scaled_unit<T>(src[l], x, f.factor), whole);
+        const int unit = sh.unit[k], elem = sh.elem[k];
+        if (unit >= 0 && elem >> 4 == tid) Vec<T>::store(g + (int64_t)unit * N + (elem & 15), f.at_y);
       }
+      if (i < n) issue(i + kStages - 1, before);
+      before = stage;
+      stage = stage + 1 == kStages ? 0 : stage + 1;
     }
-    // the batch's scalars are free, and so are its slots in every CTA of the cluster
-    done += n;
-    __syncwarp();
-    cluster_sync();
   }
-  if (!waited) griddep_wait();
+
+  // masked rows
+  for (int64_t i = n; i < my_rows; ++i) {
+    const int64_t t = listed ? row_at(i) : sh.row[i];
+    if (rank == 0 && tid == 0) {
+      if (a.logp) a.logp[t] = 0.f;
+      if (kMode == kForward) a.slope[t] = 0.f;
+    }
+    if (!has_grad) continue;
+    T* g = grads + t * a.grad_stride;
+    const Row row = row_of(g, a.vocab);
+    if (finisher) {
+      const int e = rank == 0 ? edge_of(row, a.vocab, lane) : -1;
+      if (e >= 0) Vec<T>::store(g + e, 0.f);
+    } else {
+      int v0;
+      const int cnt = part_of(row, v0);
+      uint4* dst = reinterpret_cast<uint4*>(g + row.head) + v0;
+      for (int l = tid; l < cnt; l += nt) dst[l] = make_uint4(0, 0, 0, 0);
+    }
+  }
   if (kMode == kForward && blockIdx.x == 0 && tid == 0) *a.ticket = 0;
   if (kMode == kPolicy && rank == 0) {
     if (finisher && lane == 0) acc.get(sh.stats.sum);
     finish_stats(a, sh.stats, cid, n_clusters);
   }
+  cluster_sync();  // no CTA of the cluster ends before the others have all it sent
 }
 
 // Rows of at most 32 kUnits 16-byte units (and the elements around them): one warp holds a
@@ -841,9 +900,7 @@ __global__ void __launch_bounds__(kWarpRowThreads, kUnits > 4 ? 2 : 3) warp_row_
     const bool at_edge = edge >= 0 && edge == y;
     const float others = at_edge ? -INFINITY : zedge;
     Sum s;
-    s.m = fmaxf(Vec<T>::max(w), others);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s.m = fmaxf(s.m, __shfl_xor_sync(0xFFFFFFFFu, s.m, o));
+    s.m = warp_max(fmaxf(Vec<T>::max(w), others));
     const Expo<T> x(a, s.m);
     F2 s0 = make_f2(x.one(others), 0.f), s1 = make_f2(0.f, 0.f);
 #pragma unroll
@@ -1055,7 +1112,7 @@ __global__ void __launch_bounds__(kPieceThreads) backward_kernel(const __grid_co
 // ---------------------------------------------------------------------------
 // small kernels
 // ---------------------------------------------------------------------------
-constexpr int kSmallThreads = 512;
+constexpr int kSmallThreads = 1024;
 
 __device__ __forceinline__ int64_t clamp_offset(int64_t v, int64_t lo, int64_t hi) {
   return v < lo ? lo : v > hi ? hi : v;
@@ -1097,15 +1154,24 @@ __device__ __forceinline__ int64_t live_count(const uint8_t* mask, int64_t a, in
 // Lists the live positions, then (from the back) the masked ones, so that every cluster of
 // the row kernel gets as many of each; returns the number of live ones.
 __device__ __forceinline__ int64_t build_order(const uint8_t* mask, int64_t tokens, int32_t* order, int32_t* n_live) {
+  constexpr int kEach = 16;
   __shared__ int totals[kSmallThreads / 32];
+  const bool whole = (reinterpret_cast<uint64_t>(mask) & 15) == 0;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t live = 0;
-  for (int64_t base = 0; base < tokens; base += 8 * kSmallThreads) {
-    const int64_t t = base + 8 * threadIdx.x;
+  for (int64_t base = 0; base < tokens; base += kEach * kSmallThreads) {
+    const int64_t t = base + kEach * threadIdx.x;
     unsigned bits = 0;
+    if (whole && t + kEach <= tokens) {
+      const uint4 w = *reinterpret_cast<const uint4*>(mask + t);
+      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (t + j < tokens && mask[t + j] != 0) bits |= 1u << j;
+      for (int j = 0; j < kEach; ++j) bits |= ((u[j >> 2] >> (8 * (j & 3))) & 255u) != 0 ? 1u << j : 0u;
+    } else {
+#pragma unroll
+      for (int j = 0; j < kEach; ++j)
+        if (t + j < tokens && mask[t + j] != 0) bits |= 1u << j;
+    }
     const int own = __popc(bits);
     int upto = own;
 #pragma unroll
@@ -1123,7 +1189,7 @@ __device__ __forceinline__ int64_t build_order(const uint8_t* mask, int64_t toke
     }
     int64_t front = live + before + upto - own, back = tokens - 1 - (t - front);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < kEach; ++j) {
       if (t + j >= tokens) break;
       order[(bits >> j) & 1 ? front++ : back--] = (int32_t)(t + j);
     }
@@ -1321,8 +1387,14 @@ struct RowShape {
   size_t smem;
 };
 
+int row_threads(int64_t units, int cluster) {  // that hold units: about 8 each
+  const int64_t want = ((units + cluster - 1) / cluster + 7) / 8;
+  return (int)(want <= 128 ? 128 : want >= kMaxRowThreads ? kMaxRowThreads : (want + 31) / 32 * 32);
+}
+
 size_t row_smem(int64_t units, int cluster, int stages) {
-  return (size_t)stages * (size_t)((units + cluster - 1) / cluster) * 16 + sizeof(RowShared);
+  const size_t sums = (size_t)kSlots * cluster * (row_threads(units, cluster) / 32 + 1) * sizeof(Sum);
+  return (size_t)stages * (size_t)((units + cluster - 1) / cluster) * 16 + sizeof(RowShared) + sums;
 }
 
 RowShape row_shape(int64_t vocab, int32_t dtype, int64_t tokens, int sms, bool resident) {
@@ -1336,24 +1408,30 @@ RowShape row_shape(int64_t vocab, int32_t dtype, int64_t tokens, int sms, bool r
     s.warp_units = units <= 128 ? 4 : units <= 256 ? 8 : 16;
     return s;
   }
-  s.stages = 3;
-  s.cluster = 1;
-  if (resident)
-    while (s.cluster < kMaxCluster && row_smem(units, s.cluster, 3) > kSmemPerSm) s.cluster *= 2;
-  if (split > s.cluster) s.cluster = split;
-  s.smem = row_smem(units, s.cluster, s.stages);
-  if (s.smem > kSmemPerSm) {
-    s.stages = 2;
-    s.smem = row_smem(units, s.cluster, s.stages);
-  }
-  if (s.smem > kSmemPerSm || (!resident && s.cluster == 1)) s.cluster = 0;
+  // The fewest CTAs a row that hold three rows (or, four CTAs of two rows where two CTAs fit
+  // an SM; clusters of eight leave SMs idle, so four CTAs of two rows come before them).
+  // bf16 rows, GB/s of compulsory traffic: 100000 logits 5420 (4 CTAs, 2 rows, two an SM),
+  // 4670 (4, 3), 5035 (2, 2); 131072 5980 (4, 3), 4400 (8, 3); 200064 4890 (4, 2), 3990 (8, 3).
+  struct Choice {
+    int cluster, stages;
+    size_t most;
+  };
+  static const Choice choices[] = {{1, 3, kSmemPerSm}, {2, 3, kSmemPerSm}, {4, 2, kSmemPerSm / 2 - 1024},
+                                   {4, 3, kSmemPerSm}, {4, 2, kSmemPerSm}, {8, 3, kSmemPerSm}, {8, 2, kSmemPerSm}};
+  if (split > 1 || resident)
+    for (const Choice& c : choices) {
+      if (c.cluster < split || row_smem(units, c.cluster, c.stages) > c.most) continue;
+      s.cluster = c.cluster;
+      s.stages = c.stages;
+      s.smem = row_smem(units, c.cluster, c.stages);
+      break;
+    }
   if (s.cluster == 0) {
     s.threads = units <= 8192 ? 64 : 256;
     if (resident) s.threads = 512;
     return s;
   }
-  const int64_t want = ((units + s.cluster - 1) / s.cluster + 7) / 8;  // about 8 units a thread
-  s.threads = (int)(want <= 128 ? 128 : want >= kMaxRowThreads ? kMaxRowThreads : (want + 31) / 32 * 32);
+  s.threads = row_threads(units, s.cluster);
   return s;
 }
 
@@ -1413,11 +1491,14 @@ cudaError_t launch_rows_as(RowArgs a, int32_t dtype, int sms, bool dependent, cu
     return launch(stream_kernel<T, kMode>, (int)(rows < most ? rows : most), shape.threads, 0, s, 1, dependent, a);
   }
   for (a.log_cluster = 0; (1 << a.log_cluster) < shape.cluster;) ++a.log_cluster;
-  a.stage_vecs = (int32_t)((shape.smem - sizeof(RowShared)) / 16 / shape.stages);
+  const int64_t units = a.vocab / Vec<T>::N < 1 ? 1 : a.vocab / Vec<T>::N;
+  a.stage_vecs = (int32_t)((units + shape.cluster - 1) / shape.cluster);
   auto kernel = shape.stages == 3 ? row_kernel<T, kMode, 3> : row_kernel<T, kMode, 2>;
   int n = 0;
   const cudaError_t e = resident_clusters(kernel, shape, &n);
   if (e != cudaSuccess) return e;
+  // without the list a cluster holds all its rows' scalars at once
+  if (a.mask && !a.order && (rows + kInfo - 1) / kInfo > n) n = (int)((rows + kInfo - 1) / kInfo);
   if (n > kMaxParts) n = kMaxParts;
   if (n > rows) n = (int)rows;
   return launch(kernel, n * shape.cluster, shape.threads + 32, shape.smem, s, shape.cluster, dependent, a);
