@@ -448,7 +448,8 @@ def _blocks(t):
 
 class GradSet:
     """Gradient tensors (and where their clipped values go) as the library takes them.  A
-    program whose gradients stay in place makes one and passes it to every call."""
+    program whose gradients stay in place makes one and passes it to every call.  An output
+    has its gradient's shape and strides, or as many elements where both are contiguous."""
 
     def __init__(self, grads, out=None):
         import torch
@@ -462,29 +463,45 @@ class GradSet:
         # thousands of tensors
         words = array.array("q", bytes(ctypes.sizeof(muon_grad) * max(n, 1)))
         tensor = torch.Tensor
-        codes = [_dtype_code(g.dtype) for g in grads]
-        out_codes = codes if out is grads else [_dtype_code(o.dtype) for o in out]
-        if not all(g.is_cuda for g in grads) or not (out is grads or all(o.is_cuda for o in out)):
-            raise ValueError("gradients and outputs must be CUDA tensors")
+        codes, devices, dense = _describe(grads)
         words[0::6] = _words(map(tensor.data_ptr, grads), n)
-        words[1::6] = words[0::6] if out is grads else _words(map(tensor.data_ptr, out), n)
-        words[5::6] = _words([c | o << 32 for c, o in zip(codes, out_codes)], n)
-        if all(map(tensor.is_contiguous, grads)):
+        if dense:
             words[2::6] = _words(map(tensor.numel, grads), n)
             words[3::6] = _words([1] * n, n)
         else:
             for i, g in enumerate(grads):
                 words[6 * i + 2], words[6 * i + 3], words[6 * i + 4] = _blocks(g)
-        if out is not grads:
-            for i, (g, o) in enumerate(zip(grads, out)):
-                if o.shape != g.shape or (o.stride() != g.stride() and not (o.is_contiguous() and g.is_contiguous())):
-                    raise ValueError(f"gradient {i}: out has another shape or layout")
+        if out is grads:
+            words[1::6] = words[0::6]
+            words[5::6] = _words([c | c << 32 for c in codes], n)
+        else:
+            out_codes, out_devices, out_dense = _describe(out)
+            devices |= out_devices
+            words[1::6] = _words(map(tensor.data_ptr, out), n)
+            words[5::6] = _words([c | o << 32 for c, o in zip(codes, out_codes)], n)
+            if not dense or not out_dense or words[2::6] != _words(map(tensor.numel, out), n):
+                for i, (g, o) in enumerate(zip(grads, out)):
+                    if o.shape != g.shape or (o.stride() != g.stride() and not (o.is_contiguous() and g.is_contiguous())):
+                        raise ValueError(f"gradient {i}: out has another layout")
+        if -1 in devices or len(devices) > 1:
+            raise ValueError("gradients and outputs must be CUDA tensors of one device")
         self._words = words
         self.array = c_void_p(words.buffer_info()[0])
-        self.device = grads[0].get_device() if n else torch.cuda.current_device()
+        self.device = devices.pop() if n else torch.cuda.current_device()
 
     def __len__(self):
         return len(self.tensors)
+
+
+def _describe(tensors):
+    """(dtype codes, devices (-1: the CPU), whether all are contiguous), with few steps a tensor."""
+    import torch
+    if not _DTYPE_CODES:
+        _dtype_code(torch.float32)
+    codes = list(map(_DTYPE_CODES.get, [t.dtype for t in tensors]))
+    if None in codes:
+        _dtype_code(tensors[codes.index(None)].dtype)  # raises
+    return codes, set(map(torch.Tensor.get_device, tensors)), all(map(torch.Tensor.is_contiguous, tensors))
 
 
 def _words(values, n):

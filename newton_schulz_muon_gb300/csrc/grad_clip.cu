@@ -33,40 +33,61 @@ constexpr int kClipWarps = kClipThreads / 32;
 constexpr int kClipCtasPerSm = 4;
 constexpr int kClipMaxCtas = 1024; // partial sums of one launch
 
-struct ClipSeg {
+// A plain tensor, and one of several blocks a stride apart.
+struct PlainSeg {
   const void* g;
   void* out;
-  int64_t elems, stride;
-  int32_t chunk0;          // first chunk of the tensor in its launch
-  int32_t chunks_per_mat;  // chunks of one of its blocks
-  int32_t g_bf16, out_bf16;
+  int64_t elems;
+  int32_t chunk0;   // first chunk of the tensor in its launch
+  int32_t bf16;     // bit 0: g, bit 1: out
+  __device__ __forceinline__ int64_t block(int&) const { return 0; }
+};
+struct BlockSeg {
+  const void* g;
+  void* out;
+  int64_t elems;
+  int32_t chunk0;
+  int32_t bf16;
+  int64_t stride;
+  int32_t chunks_per_block;
+  int32_t pad_;
+  // element offset of the block that chunk `local` of the tensor lies in; `local` becomes the chunk in it
+  __device__ __forceinline__ int64_t block(int& local) const {
+    const int b = local / chunks_per_block;
+    local -= b * chunks_per_block;
+    return b * stride;
+  }
 };
 
-// A launch takes up to Cap tensors.  64 keeps the parameters of the usual call at
-// 3 KB; 640 (30 KB, of the 32,764 bytes a kernel may have) serves sets of many tensors.
-template <int Cap>
+// A launch takes up to kCap tensors.  The small tables keep the parameters of the usual
+// call at 2 or 3 KB; the large ones fill the 32,764 bytes that a kernel may have.
+template <typename S, int kCap>
 struct ClipArgs {
-  ClipSeg seg[Cap];
+  using Seg = S;
+  static constexpr int kMost = kCap;
+  S seg[kCap];
   int32_t n_segs, n_chunks;
   double* partials;        // of the whole call
   int32_t partial0;        // this launch's first partial sum (norm)
   int32_t n_partials;      // all of them (clip)
   float max_norm, eps;
   int32_t nonfinite;
+  int32_t in_place;        // every tensor of this launch is
   float* result;
 };
 
-// A block's chunk: its address, length and the elements before the first 16-byte boundary.
+// A chunk: its tensor, and the part of a block that it is.
 struct Chunk {
-  const ClipSeg* seg;
-  int64_t at;     // element offset of the block from seg->g and seg->out
+  const void* g;  // of the block
+  void* out;
+  bool g_bf16, out_bf16;
   int64_t begin;  // elements [begin, end) of the block
   int64_t end;
   int head;       // the block's elements before its first aligned octet
 };
 
-template <int Cap>
-__device__ __forceinline__ Chunk find_chunk(const ClipArgs<Cap>& a, int c, int& cur) {
+template <typename A>
+__device__ __forceinline__ Chunk find_chunk(const A& a, int c, int& cur) {
   const int next = cur + 1 < a.n_segs ? a.seg[cur + 1].chunk0 : a.n_chunks;
   if (c < a.seg[cur].chunk0 || c >= next) {
     int lo = 0, hi = a.n_segs - 1;
@@ -76,20 +97,20 @@ __device__ __forceinline__ Chunk find_chunk(const ClipArgs<Cap>& a, int c, int& 
     }
     cur = lo;
   }
-  const ClipSeg& s = a.seg[cur];
-  const int local = c - s.chunk0;
-  const int mat = local / s.chunks_per_mat;
-  const int64_t j = local - mat * s.chunks_per_mat;
+  const typename A::Seg& s = a.seg[cur];
+  int local = c - s.chunk0;
+  const int64_t at = s.block(local);
   Chunk k;
-  k.seg = &s;
-  k.at = mat * s.stride;
-  const int es = s.g_bf16 ? 2 : 4;
-  const uint64_t addr = reinterpret_cast<uint64_t>(s.g) + (uint64_t)k.at * es;
-  k.head = (int)(((16 - (addr & 15)) & 15) / es);
+  k.g_bf16 = s.bf16 & 1;
+  k.out_bf16 = s.bf16 & 2;
+  const int shift = k.g_bf16 ? 1 : 2;
+  k.g = static_cast<const uint8_t*>(s.g) + (at << shift);
+  k.out = static_cast<uint8_t*>(s.out) + (at << (k.out_bf16 ? 1 : 2));
+  k.head = (int)((-reinterpret_cast<uint64_t>(k.g) & ((8u << shift) - 1)) >> shift);  // to 16 (bf16) or 32 bytes
   if (k.head > s.elems) k.head = (int)s.elems;
   // chunk 0 takes the head too, so that the others start on a boundary
-  k.begin = j == 0 ? 0 : min(s.elems, k.head + j * kChunk);
-  k.end = min(s.elems, k.head + (j + 1) * kChunk);
+  k.begin = local == 0 ? 0 : min(s.elems, k.head + (int64_t)local * kChunk);
+  k.end = min(s.elems, k.head + (int64_t)(local + 1) * kChunk);
   return k;
 }
 
@@ -134,11 +155,10 @@ __device__ __forceinline__ float load_elem(const void* p, int64_t i, int bf16) {
 __device__ __forceinline__ Part chunk_squares(const Chunk& k, int lane) {
   float s0 = 0.f, s1 = 0.f;
   uint32_t bits = 0;
-  const int64_t vec0 = k.begin == 0 ? k.head : k.begin;  // aligned
+  const int64_t vec0 = k.begin == 0 ? k.head : k.begin;  // on an octet's boundary
   const int n8 = (int)((k.end - vec0) >> 3);
-  const int bf16 = k.seg->g_bf16;
-  if (bf16) {
-    const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(k.seg->g) + k.at + vec0);
+  if (k.g_bf16) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(k.g) + vec0);
     if (n8 == kChunk / 8) {
       uint4 w[8];
 #pragma unroll
@@ -149,7 +169,7 @@ __device__ __forceinline__ Part chunk_squares(const Chunk& k, int lane) {
       for (int i = lane; i < n8; i += 32) add_octet_bf16(p[i], s0, s1, bits);
     }
   } else {
-    const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(k.seg->g) + k.at + vec0);
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(k.g) + vec0);
     if (n8 == kChunk / 8) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -172,7 +192,7 @@ __device__ __forceinline__ Part chunk_squares(const Chunk& k, int lane) {
     i = tail + (lane - 8);
   }
   if (i >= 0) {
-    const float x = load_elem(k.seg->g, k.at + i, bf16);
+    const float x = load_elem(k.g, i, k.g_bf16);
     s0 = __fmaf_rn(x, x, s0);
     bits |= __float_as_uint(x) & 0x7FFFFFFFu;
   }
@@ -183,7 +203,7 @@ __device__ __forceinline__ Part chunk_squares(const Chunk& k, int lane) {
 __device__ __noinline__ double chunk_squares_wide(const Chunk& k, int lane) {
   double s = 0.0;
   for (int64_t i = k.begin + lane; i < k.end; i += 32) {
-    const double x = (double)load_elem(k.seg->g, k.at + i, k.seg->g_bf16);
+    const double x = (double)load_elem(k.g, i, k.g_bf16);
     s = fma(x, x, s);
   }
   return s;
@@ -194,8 +214,8 @@ __device__ __noinline__ double chunk_squares_wide(const Chunk& k, int lane) {
 // chunks as an unevaluated pair.  A chunk whose lane sums leave [2^-116, 2^90], where
 // squares overflow or lose bits to underflow, is summed again in 64 bits; an all-zero
 // one is not.
-template <int Cap>
-__global__ void __launch_bounds__(kClipThreads) clip_norm_kernel(const __grid_constant__ ClipArgs<Cap> a) {
+template <typename A>
+__global__ void __launch_bounds__(kClipThreads) clip_norm_kernel(const __grid_constant__ A a) {
   __shared__ double red[kClipWarps];
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -216,10 +236,19 @@ __global__ void __launch_bounds__(kClipThreads) clip_norm_kernel(const __grid_co
       wide += chunk_squares_wide(k, lane);
     }
   }
-  double sum = (double)hi + (double)lo + wide;
+  // 64-bit additions are two a clock and SM: the pairs are merged in fp32
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-  if (lane == 0) red[warp] = sum;
+  for (int o = 16; o > 0; o >>= 1) {
+    float s, e;
+    two_sum(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o), s, e);
+    hi = s;
+    lo += e + __shfl_xor_sync(0xFFFFFFFFu, lo, o);
+  }
+  if (__any_sync(0xFFFFFFFFu, wide != 0.0)) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) wide += __shfl_xor_sync(0xFFFFFFFFu, wide, o);
+  }
+  if (lane == 0) red[warp] = (double)hi + (double)lo + wide;
   __syncthreads();
   if (threadIdx.x == 0) {
     double t = red[0];
@@ -229,19 +258,19 @@ __global__ void __launch_bounds__(kClipThreads) clip_norm_kernel(const __grid_co
   }
 }
 
-// The call's sum of squares, in the same order in every CTA.
+// The call's sum of squares, in the same order in every CTA; by one warp of it, since
+// 64-bit additions are two a clock and SM.
 __device__ __forceinline__ double total_of(const double* partials, int n) {
-  __shared__ double red[kClipWarps];
-  double t = 0.0;
-  for (int i = threadIdx.x; i < n; i += kClipThreads) t += __ldcg(partials + i);
+  __shared__ double total;
+  if (threadIdx.x < 32) {
+    double t = 0.0;
+    for (int i = threadIdx.x; i < n; i += 32) t += __ldcg(partials + i);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = t;
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+    if (threadIdx.x == 0) total = t;
+  }
   __syncthreads();
-  t = red[0];
-#pragma unroll
-  for (int w = 1; w < kClipWarps; ++w) t += red[w];
-  return t;
+  return total;
 }
 
 __global__ void __launch_bounds__(kClipThreads) norm_result_kernel(const double* partials, int n, float* norm) {
@@ -250,41 +279,88 @@ __global__ void __launch_bounds__(kClipThreads) norm_result_kernel(const double*
   if (threadIdx.x == 0) *norm = (float)sqrt(t);
 }
 
-__device__ __forceinline__ void scale8(const float (&v)[8], float c, float (&r)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) r[i] = c * v[i];
-}
+__device__ __forceinline__ float scaled(float x, float c, bool zero) { return zero ? 0.f : c * x; }
 
-__device__ __forceinline__ void store8(void* out, int64_t i, int bf16, const float (&r)[8]) {
-  if (bf16) {
-    *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(out) + i) =
-        make_uint4(pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3]), pack_bf16x2(r[4], r[5]), pack_bf16x2(r[6], r[7]));
+template <bool kBf16>
+struct Octet;  // eight elements as loaded
+template <>
+struct Octet<true> {
+  uint4 w;
+  __device__ __forceinline__ void load(const void* g, int64_t i) {
+    w = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(g) + i));
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const { unpack8(w, v); }
+};
+template <>
+struct Octet<false> {
+  float w[8];
+  __device__ __forceinline__ void load(const void* g, int64_t i) {  // 32-byte aligned
+    asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(w[0]), "=f"(w[1]), "=f"(w[2]), "=f"(w[3]), "=f"(w[4]), "=f"(w[5]), "=f"(w[6]), "=f"(w[7])
+                 : "l"(static_cast<const float*>(g) + i)
+                 : "memory");
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = w[e];
+  }
+};
+
+// fp32 octets leave as whole 32-byte sectors where they are aligned to them (404 MB from
+// 202 MB of bf16: 138 us in halves).
+template <bool kBf16>
+__device__ __forceinline__ void store8(void* out, int64_t i, const float (&r)[8], bool sectors) {
+  if (kBf16) {
+    __stcs(reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + i),
+           make_uint4(pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3]), pack_bf16x2(r[4], r[5]), pack_bf16x2(r[6], r[7])));
+  } else if (sectors) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(static_cast<float*>(out) + i),
+                 "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7])
+                 : "memory");
   } else {
-    float4* p = reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + i);
-    p[0] = make_float4(r[0], r[1], r[2], r[3]);
-    p[1] = make_float4(r[4], r[5], r[6], r[7]);
+    float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + i);
+    __stcs(p, make_float4(r[0], r[1], r[2], r[3]));
+    __stcs(p + 1, make_float4(r[4], r[5], r[6], r[7]));
   }
 }
 
-__device__ __forceinline__ void load8(const void* g, int64_t i, int bf16, float (&v)[8]) {
-  if (bf16) {
-    unpack8(__ldcs(reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(g) + i)), v);
-  } else {
-    const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(g) + i);
-    const float4 x = __ldcs(p), y = __ldcs(p + 1);
-    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-    v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+template <bool kIn, bool kOut>
+__device__ __forceinline__ void scale_octets(const Chunk& k, int64_t vec0, int n8, float c, bool zero, int lane) {
+  constexpr int kEach = 4;  // octets of a lane on their way at a time
+  const bool sectors = ((reinterpret_cast<uint64_t>(k.out) + 4 * (uint64_t)vec0) & 31) == 0;
+  int i = lane;
+  for (; i + 32 * (kEach - 1) < n8; i += 32 * kEach) {
+    Octet<kIn> w[kEach];
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) w[j].load(k.g, vec0 + 8ll * (i + 32 * j));
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      float v[8];
+      w[j].get(v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = scaled(v[e], c, zero);
+      store8<kOut>(k.out, vec0 + 8ll * (i + 32 * j), v, sectors);
+    }
+  }
+  for (; i < n8; i += 32) {
+    Octet<kIn> w;
+    float v[8];
+    w.load(k.g, vec0 + 8ll * i);
+    w.get(v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = scaled(v[e], c, zero);
+    store8<kOut>(k.out, vec0 + 8ll * i, v, sectors);
   }
 }
 
 __device__ __forceinline__ void scale_elem(const Chunk& k, int64_t i, float c, bool zero) {
-  const float r = zero ? 0.f : c * load_elem(k.seg->g, k.at + i, k.seg->g_bf16);
-  if (k.seg->out_bf16) reinterpret_cast<__nv_bfloat16*>(k.seg->out)[k.at + i] = __float2bfloat16_rn(r);
-  else reinterpret_cast<float*>(k.seg->out)[k.at + i] = r;
+  const float r = scaled(load_elem(k.g, i, k.g_bf16), c, zero);
+  if (k.out_bf16) static_cast<__nv_bfloat16*>(k.out)[i] = __float2bfloat16_rn(r);
+  else static_cast<float*>(k.out)[i] = r;
 }
 
-template <int Cap>
-__global__ void __launch_bounds__(kClipThreads) clip_scale_kernel(const __grid_constant__ ClipArgs<Cap> a) {
+template <typename A>
+__global__ void __launch_bounds__(kClipThreads) clip_scale_kernel(const __grid_constant__ A a) {
   griddep_wait();
   const double sumsq = total_of(a.partials, a.n_partials);
   const double norm = sqrt(sumsq);
@@ -300,30 +376,26 @@ __global__ void __launch_bounds__(kClipThreads) clip_scale_kernel(const __grid_c
     a.result[0] = (float)norm;
     a.result[1] = c;
   }
+  if (c == 1.f && a.in_place) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int warps = gridDim.x * kClipWarps;
   int cur = a.n_segs - 1;
   for (int r = blockIdx.x * kClipWarps + warp; r < a.n_chunks; r += warps) {
     const Chunk k = find_chunk(a, a.n_chunks - 1 - r, cur);
-    const ClipSeg& s = *k.seg;
-    if (c == 1.f && s.out == s.g) continue;
+    if (c == 1.f && k.out == k.g) continue;
     const int64_t vec0 = k.begin == 0 ? k.head : k.begin;
-    const int os = s.out_bf16 ? 2 : 4;
-    if (((reinterpret_cast<uint64_t>(s.out) + (uint64_t)(k.at + vec0) * os) & 15) != 0) {
+    if (((reinterpret_cast<uint64_t>(k.out) + ((uint64_t)vec0 << (k.out_bf16 ? 1 : 2))) & 15) != 0) {
       // out is not aligned where g is: element by element
       for (int64_t i = k.begin + lane; i < k.end; i += 32) scale_elem(k, i, c, zero);
       continue;
     }
     const int n8 = (int)((k.end - vec0) >> 3);
-    for (int i = lane; i < n8; i += 32) {
-      float v[8], w[8];
-      load8(s.g, k.at + vec0 + 8ll * i, s.g_bf16, v);
-      scale8(v, c, w);
-      if (zero) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = 0.f;
-      }
-      store8(s.out, k.at + vec0 + 8ll * i, s.out_bf16, w);
+    if (k.g_bf16) {
+      if (k.out_bf16) scale_octets<true, true>(k, vec0, n8, c, zero, lane);
+      else scale_octets<true, false>(k, vec0, n8, c, zero, lane);
+    } else {
+      if (k.out_bf16) scale_octets<false, true>(k, vec0, n8, c, zero, lane);
+      else scale_octets<false, false>(k, vec0, n8, c, zero, lane);
     }
     const int64_t tail = vec0 + 8ll * n8;
     if (lane < 8) {
@@ -337,11 +409,17 @@ __global__ void __launch_bounds__(kClipThreads) clip_scale_kernel(const __grid_c
 // ---------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------
-constexpr int kCapSmall = 64, kCapLarge = 640;
+using PlainSmall = ClipArgs<PlainSeg, 64>;
+using PlainLarge = ClipArgs<PlainSeg, 1000>;
+using BlockSmall = ClipArgs<BlockSeg, 64>;
+using BlockLarge = ClipArgs<BlockSeg, 640>;
+static_assert(sizeof(PlainLarge) <= 32764 && sizeof(BlockLarge) <= 32764, "kernel parameters");
 
 int64_t elem_size(int32_t dtype) { return dtype == MUON_DTYPE_BF16 ? 2 : 4; }
 
-int64_t chunks_per_mat(const muon_grad& t) { return (t.elems + kChunk - 1) / kChunk; }
+int64_t chunks_per_block(const muon_grad& t) { return (t.elems + kChunk - 1) / kChunk; }
+
+constexpr int64_t kMostChunks = 2000000000ll;  // of a launch
 
 const char* check_grad(const muon_grad& t) {
   if (t.elems < 0 || t.count < 0) return "gradient: elems and count must be >= 0";
@@ -350,7 +428,7 @@ const char* check_grad(const muon_grad& t) {
     return "gradient: stride_elems must be 0 or at least elems";
   if (t.dtype != MUON_DTYPE_F32 && t.dtype != MUON_DTYPE_BF16) return "gradient: unknown dtype";
   if (t.elems == 0 || t.count == 0) return nullptr;
-  if ((double)chunks_per_mat(t) * (double)t.count > 2e9) return "gradient: too many elements";
+  if ((double)chunks_per_block(t) * (double)t.count > (double)kMostChunks) return "gradient: too many elements";
   if (!t.g) return "gradient pointer is NULL";
   if (reinterpret_cast<uint64_t>(t.g) % elem_size(t.dtype)) return "gradient pointer is not aligned to its type";
   return nullptr;
@@ -367,26 +445,33 @@ const char* check_out(const muon_grad& t) {
   return nullptr;
 }
 
-// Launches of at most Cap tensors and 2^31 chunks cover the call's tensors in order.
-// The callback fills and launches one; `i` is left at the first tensor not taken.
-template <int Cap>
-void fill_args(const muon_grad* grads, int64_t n, int64_t& i, ClipArgs<Cap>& a) {
+void put_stride(PlainSeg&, const muon_grad&) {}
+void put_stride(BlockSeg& s, const muon_grad& t) {
+  s.stride = t.stride_elems ? t.stride_elems : t.elems;
+  s.chunks_per_block = (int32_t)chunks_per_block(t);
+}
+
+// Launches of at most kMost tensors and 2e9 chunks cover the call's tensors in order: fills
+// one from tensor `i` on, and leaves `i` at the first that it did not take.
+template <typename A>
+void fill_args(const muon_grad* grads, int64_t n, int64_t& i, A& a) {
   int64_t chunks = 0;
   a.n_segs = 0;
-  for (; i < n && a.n_segs < Cap; ++i) {
+  a.in_place = 1;
+  for (; i < n && a.n_segs < A::kMost; ++i) {
     const muon_grad& t = grads[i];
     if (t.elems == 0 || t.count == 0) continue;
-    const int64_t cpm = chunks_per_mat(t), all = cpm * t.count;
-    if (chunks + all > 2000000000ll) break;
-    ClipSeg& s = a.seg[a.n_segs++];
+    const int64_t all = chunks_per_block(t) * t.count;
+    if (chunks + all > kMostChunks) break;
+    typename A::Seg& s = a.seg[a.n_segs++];
+    const bool in_place = !t.out || t.out == t.g;
     s.g = t.g;
-    s.out = t.out ? t.out : t.g;
+    s.out = in_place ? t.g : t.out;
     s.elems = t.elems;
-    s.stride = t.stride_elems ? t.stride_elems : t.elems;
     s.chunk0 = (int32_t)chunks;
-    s.chunks_per_mat = (int32_t)cpm;
-    s.g_bf16 = t.dtype == MUON_DTYPE_BF16;
-    s.out_bf16 = t.out && t.out != t.g ? t.out_dtype == MUON_DTYPE_BF16 : s.g_bf16;
+    s.bf16 = (t.dtype == MUON_DTYPE_BF16 ? 1 : 0) | ((in_place ? t.dtype : t.out_dtype) == MUON_DTYPE_BF16 ? 2 : 0);
+    put_stride(s, t);
+    if (!in_place) a.in_place = 0;
     chunks += all;
   }
   a.n_chunks = (int32_t)chunks;
@@ -400,13 +485,13 @@ int grid_for(int32_t n_chunks, int sms) {
 
 int32_t cuda_error(cudaError_t e) { return set_error(MUON_ERR_CUDA, cudaGetErrorString(e)); }
 
-// Launches (of Cap tensors at most) that a set needs: tensors and chunks bound them.
+// An upper bound of the launches that a set needs: by the smallest tables.
 int64_t launches_for(const muon_grad* grads, int64_t n) {
   int64_t launches = 0, segs = 0, chunks = 0;
   for (int64_t i = 0; i < n; ++i) {
-    const int64_t all = grads[i].elems > 0 ? chunks_per_mat(grads[i]) * grads[i].count : 0;
+    const int64_t all = grads[i].elems > 0 ? chunks_per_block(grads[i]) * grads[i].count : 0;
     if (all == 0) continue;
-    if (launches == 0 || segs == kCapSmall || chunks + all > 2000000000ll) {
+    if (launches == 0 || segs == PlainSmall::kMost || chunks + all > kMostChunks) {
       ++launches;
       segs = chunks = 0;
     }
@@ -416,10 +501,10 @@ int64_t launches_for(const muon_grad* grads, int64_t n) {
   return launches;
 }
 
-template <int Cap>
+template <typename A>
 int32_t run_clip(const muon_grad* grads, int64_t n, bool clip, float max_norm, float eps, int32_t nonfinite,
                  float* result, double* partials, int sms, cudaStream_t s) {
-  ClipArgs<Cap> a;
+  A a;
   a.partials = partials;
   a.n_partials = 0;
   a.max_norm = max_norm;
@@ -435,7 +520,7 @@ int32_t run_clip(const muon_grad* grads, int64_t n, bool clip, float max_norm, f
     const int grid = grid_for(a.n_chunks, sms);
     a.partial0 = a.n_partials;
     a.n_partials += grid;
-    e = launch(clip_norm_kernel<Cap>, grid, kClipThreads, 0, s, 1, false, a);
+    e = launch(clip_norm_kernel<A>, grid, kClipThreads, 0, s, 1, false, a);
     if (e != cudaSuccess) return cuda_error(e);
     ++launches;
   }
@@ -445,14 +530,14 @@ int32_t run_clip(const muon_grad* grads, int64_t n, bool clip, float max_norm, f
     return e == cudaSuccess ? MUON_OK : cuda_error(e);
   }
   if (launches <= 1) {  // the table is filled already (or empty: the result alone)
-    if (launches == 0) a.n_segs = a.n_chunks = 0;
-    e = launch(clip_scale_kernel<Cap>, grid_for(a.n_chunks, sms), kClipThreads, 0, s, 1, launches > 0, a);
+    if (launches == 0) a.n_segs = a.n_chunks = a.in_place = 0;
+    e = launch(clip_scale_kernel<A>, grid_for(a.n_chunks, sms), kClipThreads, 0, s, 1, launches > 0, a);
     return e == cudaSuccess ? MUON_OK : cuda_error(e);
   }
   for (i = 0; i < n;) {
     fill_args(grads, n, i, a);
     if (a.n_chunks == 0) continue;
-    e = launch(clip_scale_kernel<Cap>, grid_for(a.n_chunks, sms), kClipThreads, 0, s, 1, false, a);
+    e = launch(clip_scale_kernel<A>, grid_for(a.n_chunks, sms), kClipThreads, 0, s, 1, false, a);
     if (e != cudaSuccess) return cuda_error(e);
   }
   return MUON_OK;
@@ -484,9 +569,11 @@ int32_t clip_entry(const muon_grad* grads, int64_t n, bool clip, float max_norm,
   if (sms == 0) return set_error(MUON_ERR_UNSUPPORTED, "libmuon is built for sm_103a");
   double* partials = static_cast<double*>(workspace);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return n <= kCapSmall
-             ? run_clip<kCapSmall>(grads, n, clip, max_norm, eps, nonfinite, result, partials, sms, s)
-             : run_clip<kCapLarge>(grads, n, clip, max_norm, eps, nonfinite, result, partials, sms, s);
+  bool plain = true;
+  for (int64_t i = 0; i < n; ++i) plain = plain && grads[i].count <= 1;
+  auto run = plain ? (n <= PlainSmall::kMost ? run_clip<PlainSmall> : run_clip<PlainLarge>)
+                   : (n <= BlockSmall::kMost ? run_clip<BlockSmall> : run_clip<BlockLarge>);
+  return run(grads, n, clip, max_norm, eps, nonfinite, result, partials, sms, s);
 }
 
 }  // namespace

@@ -1118,8 +1118,9 @@ __device__ __forceinline__ int64_t clamp_offset(int64_t v, int64_t lo, int64_t h
   return v < lo ? lo : v > hi ? hi : v;
 }
 
+template <int kThreads>
 __device__ __forceinline__ int64_t block_sum(int64_t v) {
-  __shared__ int64_t red[kSmallThreads / 32];
+  __shared__ int64_t red[kThreads / 32];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   __syncthreads();
@@ -1127,28 +1128,51 @@ __device__ __forceinline__ int64_t block_sum(int64_t v) {
   __syncthreads();
   v = 0;
 #pragma unroll
-  for (int w = 0; w < kSmallThreads / 32; ++w) v += red[w];
+  for (int w = 0; w < kThreads / 32; ++w) v += red[w];
   return v;
 }
 
-__device__ __forceinline__ double block_sum(double v) {
-  __shared__ double red[kSmallThreads / 32];
+// A sum and the rounding errors that it left.
+struct Pair {
+  float s = 0.f, err = 0.f;
+  __device__ __forceinline__ void add(float v) {
+    float t, e;
+    two_sum(s, v, t, e);
+    s = t;
+    err += fabsf(t) < INFINITY ? e : 0.f;
+  }
+  __device__ __forceinline__ void add(const Pair& v) {
+    add(v.s);
+    err += v.err;
+  }
+};
+
+// In fp32 pairs: 64-bit additions are two a clock and SM.
+template <int kThreads>
+__device__ __forceinline__ double block_sum(Pair v) {
+  __shared__ Pair red[kThreads / 32];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  for (int o = 16; o > 0; o >>= 1) {
+    Pair u;
+    u.s = __shfl_xor_sync(0xFFFFFFFFu, v.s, o);
+    u.err = __shfl_xor_sync(0xFFFFFFFFu, v.err, o);
+    v.add(u);
+  }
   __syncthreads();
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = 0;
+  v = red[0];
 #pragma unroll
-  for (int w = 0; w < kSmallThreads / 32; ++w) v += red[w];
-  return v;
+  for (int w = 1; w < kThreads / 32; ++w) v.add(red[w]);
+  return (double)v.s + (double)v.err;
 }
 
+template <int kThreads>
 __device__ __forceinline__ int64_t live_count(const uint8_t* mask, int64_t a, int64_t b) {
   if (mask == nullptr) return b > a ? b - a : 0;
   int64_t n = 0;
-  for (int64_t t = a + threadIdx.x; t < b; t += kSmallThreads) n += mask[t] != 0;
-  return block_sum(n);
+  for (int64_t t = a + threadIdx.x; t < b; t += kThreads) n += mask[t] != 0;
+  return block_sum<kThreads>(n);
 }
 
 // Lists the live positions, then (from the back) the masked ones, so that every cluster of
@@ -1210,7 +1234,7 @@ __global__ void __launch_bounds__(kSmallThreads) count_kernel(const uint8_t* mas
   int64_t n = -1;
   if (order) n = build_order(mask, tokens, order, n_live);
   if (mean) {
-    if (n < 0) n = live_count(mask, 0, tokens);
+    if (n < 0) n = live_count<kSmallThreads>(mask, 0, tokens);
     w = 1.f / (float)(n < 1 ? 1 : n);
   }
   if (threadIdx.x == 0) *inv_count = w;
@@ -1232,11 +1256,13 @@ __global__ void __launch_bounds__(kSmallThreads) weight_kernel(const uint8_t* ma
     return;
   }
   const int64_t a = clamp_offset(offsets[q], 0, tokens), b = clamp_offset(offsets[q + 1], a, tokens);
-  const int64_t n = live_count(mask, a, b);
+  const int64_t n = live_count<kSmallThreads>(mask, a, b);
   const float w = 1.f / ((float)n_seqs * (float)(n < 1 ? 1 : n));
   for (int64_t t = a + threadIdx.x; t < b; t += kSmallThreads)
     weight[t] = mask == nullptr || mask[t] != 0 ? w : 0.f;
 }
+
+constexpr int kPairThreads = 256;
 
 struct PairArgs {
   const uint8_t* mask;
@@ -1256,7 +1282,7 @@ struct PairArgs {
 
 // One CTA a pair: both sums, the margin, and the slope of each of its positions.  The last
 // CTA to come forms the mean over the pairs, in their order.
-__global__ void __launch_bounds__(kSmallThreads) pair_kernel(const __grid_constant__ PairArgs a) {
+__global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constant__ PairArgs a) {
   __shared__ int32_t last;
   griddep_launch_dependents();
   griddep_wait();
@@ -1268,15 +1294,10 @@ __global__ void __launch_bounds__(kSmallThreads) pair_kernel(const __grid_consta
     const int64_t q = k == 0 ? i : a.n_pairs + i;
     lo[k] = clamp_offset(a.offsets[q], 0, a.tokens);
     hi[k] = clamp_offset(a.offsets[q + 1], lo[k], a.tokens);
-    float h = 0.f, l = 0.f;
-    for (int64_t t = lo[k] + threadIdx.x; t < hi[k]; t += kSmallThreads) {
-      float s, e;
-      two_sum(h, __ldcg(a.logp + t), s, e);  // 0 where masked
-      h = s;
-      l += fabsf(s) < INFINITY ? e : 0.f;
-    }
-    double sum = block_sum((double)h + (double)l);
-    const int64_t n = a.mean ? live_count(a.mask, lo[k], hi[k]) : 1;
+    Pair part;
+    for (int64_t t = lo[k] + threadIdx.x; t < hi[k]; t += kPairThreads) part.add(__ldcg(a.logp + t));  // 0 where masked
+    double sum = block_sum<kPairThreads>(part);
+    const int64_t n = a.mean ? live_count<kPairThreads>(a.mask, lo[k], hi[k]) : 1;
     per[k] = 1.f / (float)(n < 1 ? 1 : n);
     if (a.mean) sum /= (double)(n < 1 ? 1 : n);
     if (threadIdx.x == 0 && a.seq_logp) a.seq_logp[q] = (float)sum;
@@ -1295,14 +1316,14 @@ __global__ void __launch_bounds__(kSmallThreads) pair_kernel(const __grid_consta
     const float up = 1.f / (1.f + expf(-h)), down = 1.f / (1.f + expf(h));
     const float d = a.beta / (float)a.n_pairs * (a.smooth * up - (1.f - a.smooth) * down);
     for (int k = 0; k < 2; ++k)
-      for (int64_t t = lo[k] + threadIdx.x; t < hi[k]; t += kSmallThreads) a.slope[t] = (k == 0 ? d : -d) * per[k];
+      for (int64_t t = lo[k] + threadIdx.x; t < hi[k]; t += kPairThreads) a.slope[t] = (k == 0 ? d : -d) * per[k];
   }
   __syncthreads();
   if (!last) return;
   __threadfence();
-  double t = 0.0;
-  for (int64_t k = threadIdx.x; k < a.n_pairs; k += kSmallThreads) t += (double)__ldcg(a.pair_loss + k);
-  t = block_sum(t);
+  Pair part;
+  for (int64_t k = threadIdx.x; k < a.n_pairs; k += kPairThreads) part.add(__ldcg(a.pair_loss + k));
+  const double t = block_sum<kPairThreads>(part);
   if (threadIdx.x == 0) *a.loss = (float)(t / (double)a.n_pairs);
 }
 
@@ -1715,7 +1736,7 @@ muon_status muon_preference_loss(const muon_token_batch* batch, const muon_prefe
     p.slope = grad ? ws.slope : nullptr;
     p.loss = loss;
     p.ticket = ws.ticket;
-    if ((e = launch(pair_kernel, (int)n_pairs, kSmallThreads, 0, s, 1, batch->tokens > 0, p)) != cudaSuccess)
+    if ((e = launch(pair_kernel, (int)n_pairs, kPairThreads, 0, s, 1, batch->tokens > 0, p)) != cudaSuccess)
       return cuda_error(e);
   }
   if (n_pairs == 0 && (e = cudaMemsetAsync(loss, 0, sizeof(float), s)) != cudaSuccess) return cuda_error(e);
