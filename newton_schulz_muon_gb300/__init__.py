@@ -13,6 +13,7 @@ import array
 import contextlib
 import ctypes
 import os
+import threading
 from ctypes import POINTER, byref, c_char_p, c_float, c_int32, c_int64, c_size_t, c_void_p
 from typing import Optional, Sequence
 
@@ -524,30 +525,28 @@ def _vector(t, n, dtype, what):
     return t.data_ptr()
 
 
-def _space(workspace, nbytes, device, sizes, given):
-    """(outputs, workspace pointer, bytes).  The fp32 outputs that are not given, of these
-    sizes, and the workspace that is not come from one allocation."""
+_SPACES = threading.local()  # .held: {(device, stream): workspace}
+
+
+def _space(workspace, nbytes, device: int, handle: int):
+    """(pointer, bytes) of a call's workspace: the caller's, or one that this thread holds for
+    the stream, whose calls follow one another.  A call that is being captured, whose graph
+    may run beside them, gets one of its own from the capture's memory."""
     import torch
-    need = 0
-    for size, t in zip(sizes, given):
-        if t is None:
-            need += size
-    at = (need + 3) // 4 * 4  # the workspace follows on a 16-byte boundary
-    if workspace is None:
-        buffer = torch.empty(at + (nbytes + 3) // 4, dtype=torch.float32, device=device)
-        ptr = buffer.data_ptr() + 4 * at
-    else:
+    if workspace is not None:
         if not workspace.is_cuda or not workspace.is_contiguous():
             raise ValueError("workspace: expected a contiguous CUDA tensor")
-        buffer = torch.empty(need, dtype=torch.float32, device=device) if need else workspace
-        ptr, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    outputs, at = [buffer], 0  # the buffer stays alive while the call is enqueued
-    for size, t in zip(sizes, given):
-        if t is None:
-            t = buffer[at:at + size]
-            at += size
-        outputs.append(t)
-    return outputs, ptr, nbytes
+        return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if torch.cuda.is_current_stream_capturing():
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return workspace, workspace.data_ptr(), nbytes
+    held = _SPACES.__dict__.setdefault("held", {})
+    got = held.get((device, handle))
+    if got is None or got[2] < nbytes:
+        size = max(nbytes, 1 << 17)
+        workspace = torch.empty(size, dtype=torch.uint8, device=device)
+        got = held[device, handle] = (workspace, workspace.data_ptr(), size)
+    return got
 
 
 def muon_grad_norm(grads, norm=None, workspace=None, stream=None):
@@ -559,7 +558,9 @@ def muon_grad_norm(grads, norm=None, workspace=None, stream=None):
     nbytes = muon_clip_workspace_bytes(grads)
     context, handle = _on_stream(stream, device)
     with context:
-        (_keep, norm), ws, nbytes = _space(workspace, nbytes, device, (1,), (norm,))
+        _keep, ws, nbytes = _space(workspace, nbytes, device, handle)
+        if norm is None:
+            norm = torch.empty(1, dtype=torch.float32, device=device)
     _check(_lib().muon_grad_norm(grads.array, len(grads), _vector(norm, 1, torch.float32, "norm"), ws, nbytes, handle),
            "muon_grad_norm")
     return norm
@@ -579,7 +580,9 @@ def muon_clip_grad_norm(grads, max_norm: float, out=None, eps: float = 1e-6,
     nbytes = muon_clip_workspace_bytes(grads)
     context, handle = _on_stream(stream, device)
     with context:
-        (_keep, result), ws, nbytes = _space(workspace, nbytes, device, (2,), (result,))
+        _keep, ws, nbytes = _space(workspace, nbytes, device, handle)
+        if result is None:
+            result = torch.empty(2, dtype=torch.float32, device=device)
     _check(_lib().muon_clip_grad_norm(grads.array, len(grads), max_norm, eps, nonfinite,
                                       _vector(result, 2, torch.float32, "result"), ws, nbytes, handle),
            "muon_clip_grad_norm")
@@ -683,8 +686,11 @@ def muon_policy_loss(logits, targets, old_logp, advantages, mask=None, ref_logp=
         offsets = _vector(seq_offsets, n_seqs + 1, torch.int64, "seq_offsets")
     context, handle = _on_stream(stream, device)
     with context:
-        (_keep, stats, logp), ws, nbytes = _space(workspace, muon_loss_workspace_bytes(tokens, n_seqs), device,
-                                                  (4, tokens), (stats, logp))
+        _keep, ws, nbytes = _space(workspace, muon_loss_workspace_bytes(tokens, n_seqs), device, handle)
+        if stats is None:
+            stats = torch.empty(4, dtype=f32, device=device)
+        if logp is None:
+            logp = torch.empty(tokens, dtype=f32, device=device)
         grad, grad_ptr, grad_stride = _grad_rows(logits, grad, with_grad, tokens, vocab, stride)
     _check(_lib().muon_policy_loss(
         byref(batch), byref(config) if config is not None else None, _vector(old_logp, tokens, f32, "old_logp"),
@@ -710,9 +716,16 @@ def muon_preference_loss(logits, targets, seq_offsets, ref_logp, mask=None, temp
         raise ValueError(f"seq_offsets: expected 2 P + 1 offsets, got {seq_offsets.numel()}")
     context, handle = _on_stream(stream, device)
     with context:
-        (_keep, loss, margins, seq_logp), ws, nbytes = _space(
-            workspace, muon_loss_workspace_bytes(tokens, n_seqs), device, (1, n_seqs // 2, n_seqs),
-            (loss, margins, seq_logp))
+        _keep, ws, nbytes = _space(workspace, muon_loss_workspace_bytes(tokens, n_seqs), device, handle)
+        if loss is None and margins is None and seq_logp is None:  # one allocation for the three
+            loss, margins, seq_logp = torch.empty(1 + 3 * (n_seqs // 2), dtype=f32, device=device).split_with_sizes(
+                (1, n_seqs // 2, n_seqs))
+        if loss is None:
+            loss = torch.empty(1, dtype=f32, device=device)
+        if margins is None:
+            margins = torch.empty(n_seqs // 2, dtype=f32, device=device)
+        if seq_logp is None:
+            seq_logp = torch.empty(n_seqs, dtype=f32, device=device)
         grad, grad_ptr, grad_stride = _grad_rows(logits, grad, with_grad, tokens, vocab, stride)
     _check(_lib().muon_preference_loss(
         byref(batch), byref(config) if config is not None else None, _vector(ref_logp, n_seqs, f32, "ref_logp"),

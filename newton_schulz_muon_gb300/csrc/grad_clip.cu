@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kClipThreads) clip_scale_kernel(const __grid_c
 // host
 // ---------------------------------------------------------------------------
 using PlainSmall = ClipArgs<PlainSeg, 64>;
-using PlainLarge = ClipArgs<PlainSeg, 1000>;
+using PlainLarge = ClipArgs<PlainSeg, 1020>;
 using BlockSmall = ClipArgs<BlockSeg, 64>;
 using BlockLarge = ClipArgs<BlockSeg, 640>;
 static_assert(sizeof(PlainLarge) <= 32764 && sizeof(BlockLarge) <= 32764, "kernel parameters");

@@ -1132,7 +1132,7 @@ __device__ __forceinline__ int64_t block_sum(int64_t v) {
   return v;
 }
 
-// A sum and the rounding errors that it left.
+// A sum and the rounding errors that it left (64-bit additions are two a clock and SM).
 struct Pair {
   float s = 0.f, err = 0.f;
   __device__ __forceinline__ void add(float v) {
@@ -1146,26 +1146,6 @@ struct Pair {
     err += v.err;
   }
 };
-
-// In fp32 pairs: 64-bit additions are two a clock and SM.
-template <int kThreads>
-__device__ __forceinline__ double block_sum(Pair v) {
-  __shared__ Pair red[kThreads / 32];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    Pair u;
-    u.s = __shfl_xor_sync(0xFFFFFFFFu, v.s, o);
-    u.err = __shfl_xor_sync(0xFFFFFFFFu, v.err, o);
-    v.add(u);
-  }
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = red[0];
-#pragma unroll
-  for (int w = 1; w < kThreads / 32; ++w) v.add(red[w]);
-  return (double)v.s + (double)v.err;
-}
 
 template <int kThreads>
 __device__ __forceinline__ int64_t live_count(const uint8_t* mask, int64_t a, int64_t b) {
@@ -1262,7 +1242,7 @@ __global__ void __launch_bounds__(kSmallThreads) weight_kernel(const uint8_t* ma
     weight[t] = mask == nullptr || mask[t] != 0 ? w : 0.f;
 }
 
-constexpr int kPairThreads = 256;
+constexpr int kPairThreads = 512;
 
 struct PairArgs {
   const uint8_t* mask;
@@ -1280,51 +1260,92 @@ struct PairArgs {
   unsigned* ticket; // zeroed by the kernel before
 };
 
-// One CTA a pair: both sums, the margin, and the slope of each of its positions.  The last
+// One CTA a pair: half of it sums each sequence, one thread forms the margin (in 64 bits:
+// a difference of long sums), and each half writes the slopes of its positions.  The last
 // CTA to come forms the mean over the pairs, in their order.
 __global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constant__ PairArgs a) {
+  constexpr int kHalf = kPairThreads / 2, kWarps = kPairThreads / 32;
+  __shared__ Pair sums[kWarps];
+  __shared__ int live[kWarps];
+  __shared__ float slope[2];
   __shared__ int32_t last;
   griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, half = threadIdx.x / kHalf, at = threadIdx.x % kHalf;
+  const int64_t i = blockIdx.x, q = half == 0 ? i : a.n_pairs + i;
+  const int64_t lo = clamp_offset(a.offsets[q], 0, a.tokens), hi = clamp_offset(a.offsets[q + 1], lo, a.tokens);
+  const float ref[2] = {a.ref[i], a.ref[a.n_pairs + i]};
+  Pair part;
+  int n = 0;
+  if (a.mean)
+    for (int64_t t = lo + at; t < hi; t += kHalf) n += a.mask == nullptr || a.mask[t] != 0;
   griddep_wait();
-  const int64_t i = blockIdx.x;
-  double gain[2];
-  int64_t lo[2], hi[2];
-  float per[2];
-  for (int k = 0; k < 2; ++k) {
-    const int64_t q = k == 0 ? i : a.n_pairs + i;
-    lo[k] = clamp_offset(a.offsets[q], 0, a.tokens);
-    hi[k] = clamp_offset(a.offsets[q + 1], lo[k], a.tokens);
-    Pair part;
-    for (int64_t t = lo[k] + threadIdx.x; t < hi[k]; t += kPairThreads) part.add(__ldcg(a.logp + t));  // 0 where masked
-    double sum = block_sum<kPairThreads>(part);
-    const int64_t n = a.mean ? live_count<kPairThreads>(a.mask, lo[k], hi[k]) : 1;
-    per[k] = 1.f / (float)(n < 1 ? 1 : n);
-    if (a.mean) sum /= (double)(n < 1 ? 1 : n);
-    if (threadIdx.x == 0 && a.seq_logp) a.seq_logp[q] = (float)sum;
-    gain[k] = sum - (double)a.ref[q];
+#pragma unroll 4
+  for (int64_t t = lo + at; t < hi; t += kHalf) part.add(__ldcg(a.logp + t));  // 0 where masked
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    Pair u;
+    u.s = __shfl_xor_sync(0xFFFFFFFFu, part.s, o);
+    u.err = __shfl_xor_sync(0xFFFFFFFFu, part.err, o);
+    part.add(u);
+    n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
   }
-  const float h = (float)((double)a.beta * (gain[0] - gain[1]));
-  // log sigmoid(h) = min(h, 0) - log(1 + exp(-|h|))
-  const float soft = log1pf(expf(-fabsf(h)));
+  if (lane == 0) {
+    sums[warp] = part;
+    live[warp] = n;
+  }
+  __syncthreads();
   if (threadIdx.x == 0) {
+    double gain[2];
+    float per[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      Pair s = sums[k * kWarps / 2];
+      int count = live[k * kWarps / 2];
+#pragma unroll
+      for (int w = 1; w < kWarps / 2; ++w) {
+        s.add(sums[k * kWarps / 2 + w]);
+        count += live[k * kWarps / 2 + w];
+      }
+      double sum = (double)s.s + (double)s.err;
+      per[k] = a.mean ? 1.f / (float)max(count, 1) : 1.f;
+      if (a.mean) sum /= (double)max(count, 1);
+      if (a.seq_logp) a.seq_logp[k == 0 ? i : a.n_pairs + i] = (float)sum;
+      gain[k] = sum - (double)ref[k];
+    }
+    const float h = (float)((double)a.beta * (gain[0] - gain[1]));
     if (a.margins) a.margins[i] = h;
+    // log sigmoid(h) = min(h, 0) - log(1 + exp(-|h|))
+    const float soft = log1pf(expf(-fabsf(h)));
     a.pair_loss[i] = (1.f - a.smooth) * (soft - fminf(h, 0.f)) + a.smooth * (soft + fmaxf(h, 0.f));
+    const float up = 1.f / (1.f + expf(-h)), down = 1.f / (1.f + expf(h));
+    const float d = a.beta / (float)a.n_pairs * (a.smooth * up - (1.f - a.smooth) * down);
+    slope[0] = d * per[0];
+    slope[1] = -d * per[1];
     __threadfence();
     last = atomicAdd(a.ticket, 1u) == (unsigned)a.n_pairs - 1;
   }
-  if (a.slope) {
-    const float up = 1.f / (1.f + expf(-h)), down = 1.f / (1.f + expf(h));
-    const float d = a.beta / (float)a.n_pairs * (a.smooth * up - (1.f - a.smooth) * down);
-    for (int k = 0; k < 2; ++k)
-      for (int64_t t = lo[k] + threadIdx.x; t < hi[k]; t += kPairThreads) a.slope[t] = (k == 0 ? d : -d) * per[k];
-  }
   __syncthreads();
+  if (a.slope)
+    for (int64_t t = lo + at; t < hi; t += kHalf) a.slope[t] = slope[half];
   if (!last) return;
   __threadfence();
-  Pair part;
+  part = Pair();
   for (int64_t k = threadIdx.x; k < a.n_pairs; k += kPairThreads) part.add(__ldcg(a.pair_loss + k));
-  const double t = block_sum<kPairThreads>(part);
-  if (threadIdx.x == 0) *a.loss = (float)(t / (double)a.n_pairs);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    Pair u;
+    u.s = __shfl_xor_sync(0xFFFFFFFFu, part.s, o);
+    u.err = __shfl_xor_sync(0xFFFFFFFFu, part.err, o);
+    part.add(u);
+  }
+  if (lane == 0) sums[warp] = part;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    part = sums[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) part.add(sums[w]);
+    *a.loss = (float)(((double)part.s + (double)part.err) / (double)a.n_pairs);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -1448,7 +1469,9 @@ RowShape row_shape(int64_t vocab, int32_t dtype, int64_t tokens, int sms, bool r
       break;
     }
   if (s.cluster == 0) {
+    // many rows: small CTAs, whose ends overlap; few: enough threads to fill the SMs
     s.threads = units <= 8192 ? 64 : 256;
+    while (s.threads < kMaxRowThreads && tokens * s.threads <= 512ll * sms && units >= 8 * s.threads) s.threads *= 2;
     if (resident) s.threads = 512;
     return s;
   }
