@@ -844,7 +844,7 @@ __global__ void __launch_bounds__(kWarpRowThreads, kUnits > 4 ? 2 : 3) warp_row_
   const int64_t warps = (int64_t)gridDim.x * kWarpRowWarps;
   Terms acc;
   griddep_launch_dependents();
-  griddep_wait();
+  bool waited = false;
   const int64_t first = (int64_t)blockIdx.x * kWarpRowWarps + warp;
   bool next_live = first < a.tokens && (a.mask == nullptr || a.mask[first] != 0);
   int64_t next_y = first < a.tokens ? a.targets[first] : 0;
@@ -855,6 +855,10 @@ __global__ void __launch_bounds__(kWarpRowThreads, kUnits > 4 ? 2 : 3) warp_row_
     if (t + warps < a.tokens) {
       next_live = a.mask == nullptr || a.mask[t + warps] != 0;
       next_y = a.targets[t + warps];
+    }
+    if (!waited && !live) {
+      griddep_wait();
+      waited = true;
     }
     const T* z = reinterpret_cast<const T*>(a.logits) + t * a.stride;
     T* g = reinterpret_cast<T*>(a.grad) + t * a.grad_stride;
@@ -886,6 +890,12 @@ __global__ void __launch_bounds__(kWarpRowThreads, kUnits > 4 ? 2 : 3) warp_row_
       at.old_logp = a.old_logp[t];
       if (a.ref_logp) at.ref = a.ref_logp[t];
       at.adv = a.adv[t];
+    }
+    if (!waited) {  // the first row's loads are under way
+      griddep_wait();
+      waited = true;
+    }
+    if (kMode == kPolicy) {
       at.w = a.weight ? __ldcg(a.weight + t) : __ldcg(a.inv_count);
     }
     const int unit = in && y >= row.head && y < row.tail ? ((int)y - row.head) / N : -1;
@@ -948,6 +958,7 @@ __global__ void __launch_bounds__(kWarpRowThreads, kUnits > 4 ? 2 : 3) warp_row_
       }
     }
   }
+  if (!waited) griddep_wait();
   if (kMode == kForward && blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
   if (kMode == kPolicy) {
     __shared__ double part[kWarpRowWarps][4];
@@ -1151,7 +1162,17 @@ template <int kThreads>
 __device__ __forceinline__ int64_t live_count(const uint8_t* mask, int64_t a, int64_t b) {
   if (mask == nullptr) return b > a ? b - a : 0;
   int64_t n = 0;
-  for (int64_t t = a + threadIdx.x; t < b; t += kThreads) n += mask[t] != 0;
+  // 16 positions at a time between the first and the last 16-byte boundary
+  const int64_t a16 = min(b, a + (int64_t)(-reinterpret_cast<uint64_t>(mask + a) & 15));
+  const int64_t units = b > a16 ? (b - a16) / 16 : 0;
+  const uint4* p = reinterpret_cast<const uint4*>(mask + a16);
+  for (int64_t u = threadIdx.x; u < units; u += kThreads) {
+    const uint4 w = p[u];
+    // a byte that is not 0 becomes 0xff, so that every one counts 8 bits
+    n += (__popc(__vcmpne4(w.x, 0)) + __popc(__vcmpne4(w.y, 0)) + __popc(__vcmpne4(w.z, 0)) + __popc(__vcmpne4(w.w, 0))) / 8;
+  }
+  for (int64_t t = a + threadIdx.x; t < a16; t += kThreads) n += mask[t] != 0;
+  for (int64_t t = a16 + 16 * units + threadIdx.x; t < b; t += kThreads) n += mask[t] != 0;
   return block_sum<kThreads>(n);
 }
 
