@@ -4,7 +4,8 @@
 //
 // Two passes, bound by HBM: every element is read once for N; where something has to
 // be written it is read again (in the reverse order, so that what the first pass left
-// in L2 is met first), scaled and written.  The tensor table travels as a kernel
+// in L2 is met first: its last kKeptBytes, read with the normal policy while all before
+// them are marked to be evicted first), scaled and written.  The tensor table travels as a kernel
 // parameter, so a call copies nothing to the device and waits for nothing on the host.
 //
 // The unit of work is a chunk of kChunk elements of one tensor, taken by one warp: a
@@ -32,6 +33,7 @@ constexpr int kClipThreads = 256;
 constexpr int kClipWarps = kClipThreads / 32;
 constexpr int kClipCtasPerSm = 4;
 constexpr int kClipMaxCtas = 1024; // partial sums of one launch
+constexpr int64_t kKeptBytes = 80ll << 20;
 
 // A plain tensor, and one of several blocks a stride apart.
 struct PlainSeg {
@@ -73,6 +75,7 @@ struct ClipArgs {
   float max_norm, eps;
   int32_t nonfinite;
   int32_t in_place;        // every tensor of this launch is
+  int32_t kept;            // the chunks from here on are left in L2
   float* result;
 };
 
@@ -140,19 +143,29 @@ __device__ __forceinline__ void add_octet_bf16(const uint4& w, float& s0, float&
   bits |= (w.x | w.y | w.z | w.w) & 0x7FFF7FFFu;
 }
 
-__device__ __forceinline__ void add_quad_f32(const float4& w, float& s0, float& s1, uint32_t& bits) {
-  s0 = __fmaf_rn(w.x, w.x, s0);
-  s1 = __fmaf_rn(w.y, w.y, s1);
-  s0 = __fmaf_rn(w.z, w.z, s0);
-  s1 = __fmaf_rn(w.w, w.w, s1);
-  bits |= (__float_as_uint(w.x) | __float_as_uint(w.y) | __float_as_uint(w.z) | __float_as_uint(w.w)) & 0x7FFFFFFFu;
+__device__ __forceinline__ void add_quad_f32(const uint4& w, float& s0, float& s1, uint32_t& bits) {
+  const float x = __uint_as_float(w.x), y = __uint_as_float(w.y), z = __uint_as_float(w.z), u = __uint_as_float(w.w);
+  s0 = __fmaf_rn(x, x, s0);
+  s1 = __fmaf_rn(y, y, s1);
+  s0 = __fmaf_rn(z, z, s0);
+  s1 = __fmaf_rn(u, u, s1);
+  bits |= (w.x | w.y | w.z | w.w) & 0x7FFFFFFFu;
 }
 
 __device__ __forceinline__ float load_elem(const void* p, int64_t i, int bf16) {
   return bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[i]) : reinterpret_cast<const float*>(p)[i];
 }
 
-__device__ __forceinline__ Part chunk_squares(const Chunk& k, int lane) {
+__device__ __forceinline__ uint4 load16(const void* p, uint64_t policy) {
+  uint4 w;
+  asm volatile("ld.global.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
+               : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+               : "l"(p), "l"(policy)
+               : "memory");
+  return w;
+}
+
+__device__ __forceinline__ Part chunk_squares(const Chunk& k, int lane, uint64_t policy) {
   float s0 = 0.f, s1 = 0.f;
   uint32_t bits = 0;
   const int64_t vec0 = k.begin == 0 ? k.head : k.begin;  // on an octet's boundary
@@ -162,20 +175,20 @@ __device__ __forceinline__ Part chunk_squares(const Chunk& k, int lane) {
     if (n8 == kChunk / 8) {
       uint4 w[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = p[i * 32 + lane];
+      for (int i = 0; i < 8; ++i) w[i] = load16(p + i * 32 + lane, policy);
 #pragma unroll
       for (int i = 0; i < 8; ++i) add_octet_bf16(w[i], s0, s1, bits);
     } else {
       for (int i = lane; i < n8; i += 32) add_octet_bf16(p[i], s0, s1, bits);
     }
   } else {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(k.g) + vec0);
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(k.g) + vec0);
     if (n8 == kChunk / 8) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        float4 w[8];
+        uint4 w[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = p[h * 256 + i * 32 + lane];
+        for (int i = 0; i < 8; ++i) w[i] = load16(p + h * 256 + i * 32 + lane, policy);
 #pragma unroll
         for (int i = 0; i < 8; ++i) add_quad_f32(w[i], s0, s1, bits);
       }
@@ -220,12 +233,15 @@ __global__ void __launch_bounds__(kClipThreads) clip_norm_kernel(const __grid_co
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int warps = gridDim.x * kClipWarps;
+  uint64_t first, normal;  // L2 policies
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(first));
+  asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(normal));
   float hi = 0.f, lo = 0.f;
   double wide = 0.0;
   int cur = 0;
   for (int c = blockIdx.x * kClipWarps + warp; c < a.n_chunks; c += warps) {
     const Chunk k = find_chunk(a, c, cur);
-    const Part p = chunk_squares(k, lane);
+    const Part p = chunk_squares(k, lane, c < a.kept ? first : normal);
     const bool fits = p.s <= 0x1p90f && (p.s >= 0x1p-116f || p.bits == 0);
     if (__all_sync(0xFFFFFFFFu, fits)) {
       float s, e;
@@ -295,7 +311,7 @@ template <>
 struct Octet<false> {
   float w[8];
   __device__ __forceinline__ void load(const void* g, int64_t i) {  // 32-byte aligned
-    asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+    asm volatile("ld.global.L2::evict_first.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=f"(w[0]), "=f"(w[1]), "=f"(w[2]), "=f"(w[3]), "=f"(w[4]), "=f"(w[5]), "=f"(w[6]), "=f"(w[7])
                  : "l"(static_cast<const float*>(g) + i)
                  : "memory");
@@ -314,7 +330,7 @@ __device__ __forceinline__ void store8(void* out, int64_t i, const float (&r)[8]
     __stcs(reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + i),
            make_uint4(pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3]), pack_bf16x2(r[4], r[5]), pack_bf16x2(r[6], r[7])));
   } else if (sectors) {
-    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(static_cast<float*>(out) + i),
+    asm volatile("st.global.L2::evict_first.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(static_cast<float*>(out) + i),
                  "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7])
                  : "memory");
   } else {
@@ -475,6 +491,16 @@ void fill_args(const muon_grad* grads, int64_t n, int64_t& i, A& a) {
     chunks += all;
   }
   a.n_chunks = (int32_t)chunks;
+  a.kept = 0;
+  int64_t room = kKeptBytes / kChunk;  // bytes an element times chunks
+  for (int k = a.n_segs - 1; k >= 0; --k) {
+    const int64_t size = (a.seg[k].bf16 & 1) ? 2 : 4, mine = (k + 1 < a.n_segs ? a.seg[k + 1].chunk0 : chunks) - a.seg[k].chunk0;
+    if (mine * size > room) {
+      a.kept = (int32_t)(a.seg[k].chunk0 + mine - room / size);
+      break;
+    }
+    room -= mine * size;
+  }
 }
 
 int grid_for(int32_t n_chunks, int sms) {
