@@ -150,6 +150,27 @@ __device__ __forceinline__ void drop(uint4& w, const uint4& m) {
   w.w = (w.w & ~m.w) | (Vec<T>::kLowest & m.w);
 }
 
+// 16-byte accesses with an L2 policy.
+__device__ __forceinline__ uint64_t l2_policy(bool evict_first) {
+  uint64_t first, normal;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(first));
+  asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(normal));
+  return evict_first ? first : normal;
+}
+__device__ __forceinline__ uint4 load16(const uint4* p, uint64_t policy) {
+  uint4 w;
+  asm volatile("ld.global.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
+               : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+               : "l"(p), "l"(policy)
+               : "memory");
+  return w;
+}
+__device__ __forceinline__ void store16(uint4* p, const uint4& w, uint64_t policy) {
+  asm volatile("st.global.L2::cache_hint.v4.u32 [%0], {%1, %2, %3, %4}, %5;" ::"l"(p), "r"(w.x), "r"(w.y), "r"(w.z),
+               "r"(w.w), "l"(policy)
+               : "memory");
+}
+
 // Two floats at a time (one issue slot).
 struct F2 {
   uint64_t v;
@@ -407,6 +428,7 @@ constexpr int kMaxCluster = 8;
 constexpr int kInfo = 32;    // rows whose places and scalars a CTA holds at a time
 constexpr int kSlots = 4;    // rows whose partial sums may be on their way
 constexpr int kGroup = 4;    // 16-byte units a thread takes at a time
+constexpr int64_t kKeptBytes = 80ll << 20;  // of logits that L2 holds from the forward pass to the backward pass
 
 // A CTA's sums of its rows' terms, and whether it is the last to have them.
 struct StatsShared {
@@ -1012,12 +1034,14 @@ __global__ void __launch_bounds__(kMaxRowThreads) stream_kernel(const __grid_con
     const int edge = tid < 16 ? edge_of(row, a.vocab, tid) : -1;
     Sum s{-INFINITY, 0.f};
     Expo<T> x(a, s.m);
+    // the backward pass begins with the last rows: L2 keeps them rather than those before
+    const uint64_t policy = l2_policy(kMode == kForward && (a.tokens - t) * a.vocab * (int)sizeof(T) > kKeptBytes);
     for (int l = tid; l < row.units; l += kGroup * nt) {
       uint4 w[kGroup];
 #pragma unroll
       for (int k = 0; k < kGroup; ++k) {
         const int u = l + k * nt;
-        w[k] = u < row.units ? __ldg(src + u) : make_uint4(Vec<T>::kLowest, Vec<T>::kLowest, Vec<T>::kLowest, Vec<T>::kLowest);
+        w[k] = u < row.units ? (kMode == kForward ? load16(src + u, policy) : __ldg(src + u)) : make_uint4(Vec<T>::kLowest, Vec<T>::kLowest, Vec<T>::kLowest, Vec<T>::kLowest);
       }
       if (l == target_l) {  // the target leaves the sum
 #pragma unroll
@@ -1070,54 +1094,69 @@ __global__ void __launch_bounds__(kMaxRowThreads) stream_kernel(const __grid_con
 }
 
 // The gradient of rows whose slope, frame and sum are known, a piece of kPiece units a
-// CTA; the last rows first, whose logits the forward pass left in L2.
+// CTA; the last rows first, whose logits the forward pass left in L2 (a gradient too large
+// for L2 does not displace them: 1024 x 65536 fp32, forward and backward 125 us with the
+// default policies, 117 us so).
 constexpr int kPieceThreads = 256;
 constexpr int kPiece = kPieceThreads * kGroup;
 
 template <typename T>
 __global__ void __launch_bounds__(kPieceThreads) backward_kernel(const __grid_constant__ RowArgs a, int pieces) {
   constexpr int N = Vec<T>::N;
-  griddep_wait();
   const int tid = threadIdx.x;
+  const uint64_t policy = l2_policy(a.tokens * a.vocab * (int)sizeof(T) > kKeptBytes);
+  bool waited = false;
   for (int64_t r = blockIdx.x; r < a.tokens * pieces; r += gridDim.x) {
     const int64_t t = a.tokens - 1 - r / pieces;
     const int piece = (int)(r % pieces);
     const T* z = reinterpret_cast<const T*>(a.logits) + t * a.stride;
     T* g = reinterpret_cast<T*>(a.grad) + t * a.grad_stride;
     const bool live = a.mask == nullptr || a.mask[t] != 0;
-    const float slope = live ? __ldcg(a.slope + t) : 0.f;
-    if (slope == 0.f) {
-      const Row row = row_of(g, a.vocab);
-      uint4* dst = reinterpret_cast<uint4*>(g + row.head);
-      for (int l = piece * kPiece + tid; l < min((piece + 1) * kPiece, row.units); l += kPieceThreads)
-        dst[l] = make_uint4(0, 0, 0, 0);
-      const int e = piece == 0 && tid < 16 ? edge_of(row, a.vocab, tid) : -1;
-      if (e >= 0) Vec<T>::store(g + e, 0.f);
-      continue;
-    }
+    // the logits are on their way while the row's scalars are read (and, at first, while
+    // the pair kernel runs)
     const Row row = row_of(z, a.vocab);
     const int v0 = piece * kPiece + tid;
     const uint4* src = reinterpret_cast<const uint4*>(z + row.head);
     uint4 w[kGroup];
+    if (live) {
 #pragma unroll
-    for (int k = 0; k < kGroup; ++k)
-      if (v0 + k * kPieceThreads < row.units) w[k] = src[v0 + k * kPieceThreads];
+      for (int k = 0; k < kGroup; ++k)
+        if (v0 + k * kPieceThreads < row.units) w[k] = src[v0 + k * kPieceThreads];
+    }
+    if (!waited) {
+      griddep_wait();
+      waited = true;
+    }
+    const float slope = live ? __ldcg(a.slope + t) : 0.f;
+    if (slope == 0.f) {
+      const Row out = row_of(g, a.vocab);
+      uint4* dst = reinterpret_cast<uint4*>(g + out.head);
+      for (int l = v0; l < min((piece + 1) * kPiece, out.units); l += kPieceThreads)
+        store16(dst + l, make_uint4(0, 0, 0, 0), policy);
+      const int e = piece == 0 && tid < 16 ? edge_of(out, a.vocab, tid) : -1;
+      if (e >= 0) Vec<T>::store(g + e, 0.f);
+      continue;
+    }
     const float2 ms = __ldcg(a.frame + t);
     const int64_t y = a.targets[t];
     const Factor f = row_factor(a, ms.x, ms.y, __ldcg(a.logp + t), slope);
     const Expo<T> x(a, f.m);
     const bool whole = aligned_unit(g + row.head);
-    const int unit = y >= row.head && y < row.tail ? ((int)y - row.head) / N : -1;
 #pragma unroll
     for (int k = 0; k < kGroup; ++k) {
       const int u = v0 + k * kPieceThreads;
       if (u >= row.units) continue;
-      store_unit(g + row.head + (int64_t)u * N, scaled_unit<T>(w[k], x, f.factor), whole);
+      T* dst = g + row.head + (int64_t)u * N;
+      const uint4 o = scaled_unit<T>(w[k], x, f.factor);
+      if (whole) store16(reinterpret_cast<uint4*>(dst), o, policy);
+      else store_unit(dst, o, false);
     }
+    const int unit = y >= row.head && y < row.tail ? ((int)y - row.head) / N : -1;
     if (unit >= v0 && unit < v0 + kPiece && (unit - v0) % kPieceThreads == 0) Vec<T>::store(g + y, f.at_y);
     const int e = piece == 0 && tid < 16 ? edge_of(row, a.vocab, tid) : -1;
     if (e >= 0) Vec<T>::store(g + e, e == y ? f.at_y : f.factor * x.one(Vec<T>::load(z + e)));
   }
+  if (!waited) griddep_wait();
 }
 
 // ---------------------------------------------------------------------------
@@ -1441,6 +1480,7 @@ RowArgs row_args(const muon_token_batch* b) {
 }
 
 constexpr int kMaxParts = 2048;            // partial sums of the policy loss
+constexpr int64_t kMostCtas = 2000000000;
 constexpr size_t kSmemPerSm = 227 * 1024;  // what one CTA may have
 
 // Shape of a row kernel's launch.  warp_units > 0: a warp a row; else cluster = 0: straight
@@ -1575,12 +1615,14 @@ cudaError_t launch_rows(const RowArgs& a, int32_t dtype, int sms, bool dependent
                                   : launch_rows_as<float, kMode>(a, dtype, sms, dependent, s);
 }
 
-cudaError_t launch_backward(const RowArgs& a, int32_t dtype, int sms, cudaStream_t s) {
+cudaError_t launch_backward(const RowArgs& a, int32_t dtype, cudaStream_t s) {
   if (a.tokens == 0) return cudaSuccess;
   const int64_t units = a.vocab / (dtype == MUON_DTYPE_BF16 ? 8 : 4);
   const int pieces = (int)((units < 1 ? 1 : units) + kPiece - 1) / kPiece;
   const int64_t all = a.tokens * pieces;
-  const int grid = (int)(all < 8ll * sms ? all : 8ll * sms);
+  // a CTA for each piece: 8192 x 131072 with a quarter masked, both passes, 0.912 ms with 8
+  // CTAs an SM that take pieces in turn, 0.791 ms so
+  const int grid = (int)(all < kMostCtas ? all : kMostCtas);
   return dtype == MUON_DTYPE_BF16 ? launch(backward_kernel<__nv_bfloat16>, grid, kPieceThreads, 0, s, 1, true, a, pieces)
                                   : launch(backward_kernel<float>, grid, kPieceThreads, 0, s, 1, true, a, pieces);
 }
@@ -1784,7 +1826,7 @@ muon_status muon_preference_loss(const muon_token_batch* batch, const muon_prefe
       return cuda_error(e);
   }
   if (n_pairs == 0 && (e = cudaMemsetAsync(loss, 0, sizeof(float), s)) != cudaSuccess) return cuda_error(e);
-  if (grad && (e = launch_backward(a, batch->dtype, sms, s)) != cudaSuccess) return cuda_error(e);
+  if (grad && (e = launch_backward(a, batch->dtype, s)) != cudaSuccess) return cuda_error(e);
   return MUON_OK;
 }
 
