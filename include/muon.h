@@ -444,8 +444,9 @@ typedef struct {
   int64_t tokens;
   int64_t vocab;           /* 1 .. 2^30 */
   int64_t row_stride;      /* >= vocab; 0 means vocab */
+  double temperature;      /* logits are divided by it; 1e-20 .. 1e20 */
   int32_t dtype;           /* MUON_DTYPE_* of the logits and their gradient */
-  float temperature;       /* logits are divided by it; 1e-20 .. 1e20 */
+  int32_t reserved;
 } muon_token_batch;
 
 /* logp[t] = z[t, y_t] - log sum_j exp(z[t, j]), z = logits / temperature (fp32,

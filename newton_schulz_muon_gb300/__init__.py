@@ -95,7 +95,8 @@ class muon_grad(ctypes.Structure):
 
 class muon_token_batch(ctypes.Structure):
     _fields_ = [("logits", c_void_p), ("targets", c_void_p), ("mask", c_void_p), ("tokens", c_int64),
-                ("vocab", c_int64), ("row_stride", c_int64), ("dtype", c_int32), ("temperature", c_float)]
+                ("vocab", c_int64), ("row_stride", c_int64), ("temperature", ctypes.c_double), ("dtype", c_int32),
+                ("reserved", c_int32)]
 
 
 class muon_policy_config(ctypes.Structure):
@@ -610,7 +611,7 @@ def _token_batch(logits, targets, mask, temperature):
             raise ValueError(f"mask: expected bool or uint8, got {mask.dtype}")
         masked = _vector(mask, tokens, mask.dtype, "mask")
     return muon_token_batch(logits.data_ptr(), _vector(targets, tokens, torch.int64, "targets"), masked, tokens, vocab,
-                            stride, _dtype_code(logits.dtype), temperature), tokens, vocab, stride
+                            stride, temperature, _dtype_code(logits.dtype)), tokens, vocab, stride
 
 
 def _grad_rows(logits, grad, with_grad, tokens, vocab, stride):

@@ -52,7 +52,8 @@ struct RowArgs {
   int64_t tokens, vocab, stride, grad_stride;
   float c_hi, c_lo;      // log2(e) / temperature = c_hi + c_lo, c_lo > 0
   float2 c_mix[4];       // the floats next to it, for the four pairs of a unit of bf16
-  float inv_temp;
+  float inv_temp;        // 1 / temperature, and
+  float inv_hi, inv_lo;  // in two floats, inv_lo > 0
   float* logp;           // or null
   float2* frame;         // kForward: (m, sum over the whole row) of each row
   float* slope;          // kForward: cleared for rows of no sequence
@@ -306,7 +307,8 @@ struct Prob {
 };
 
 __device__ __forceinline__ Prob row_prob(const RowArgs& a, const Sum& t, float zy) {
-  const float x = (zy - t.m) * a.inv_temp;
+  const float d = zy - t.m;
+  const float x = __fmaf_rn(d, a.inv_hi, d * a.inv_lo);
   const float e = expf(x);
   Prob p;
   p.s = t.s + e;
@@ -1423,7 +1425,7 @@ int32_t check_batch(const muon_token_batch* b) {
   if (b->row_stride != 0 && (b->row_stride < b->vocab || b->row_stride > (1ll << 40)))
     return invalid("row_stride must be 0 or at least vocab");
   if (b->dtype != MUON_DTYPE_F32 && b->dtype != MUON_DTYPE_BF16) return invalid("unknown logits dtype");
-  if (!(b->temperature >= 1e-20f && b->temperature <= 1e20f)) return invalid("temperature must be in [1e-20, 1e20]");
+  if (!(b->temperature >= 1e-20 && b->temperature <= 1e20)) return invalid("temperature must be in [1e-20, 1e20]");
   if (b->tokens == 0) return MUON_OK;
   if (!b->logits || !b->targets) return invalid("logits or targets is NULL");
   if (!aligned(b->logits, b->dtype == MUON_DTYPE_BF16 ? 2 : 4) || !aligned(b->targets, 8))
@@ -1456,6 +1458,13 @@ int32_t find_device(int* sms) {
   return MUON_OK;
 }
 
+// v = hi + lo with lo > 0 (v > 0).
+void split_down(double v, float* hi, float* lo) {
+  *hi = std::nextafterf((float)v, 0.f);
+  if ((double)*hi >= v) *hi = std::nextafterf(*hi, 0.f);
+  *lo = (float)(v - (double)*hi);
+}
+
 RowArgs row_args(const muon_token_batch* b) {
   RowArgs a = {};
   a.logits = b->logits;
@@ -1465,16 +1474,15 @@ RowArgs row_args(const muon_token_batch* b) {
   a.vocab = b->vocab;
   a.stride = b->row_stride ? b->row_stride : b->vocab;
   a.grad_stride = a.vocab;
-  const double c = 1.4426950408889634 / (double)b->temperature;
-  a.c_hi = std::nextafterf((float)c, 0.f);
-  if ((double)a.c_hi >= c) a.c_hi = std::nextafterf(a.c_hi, 0.f);
-  a.c_lo = (float)(c - (double)a.c_hi);
+  const double c = 1.4426950408889634 / b->temperature;
+  split_down(c, &a.c_hi, &a.c_lo);
+  split_down(1.0 / b->temperature, &a.inv_hi, &a.inv_lo);
   // c = down + (up - down) k / 8 within a sixteenth of their distance
   const float near = (float)c, down = (double)near <= c ? near : std::nextafterf(near, 0.f);
   const float up = std::nextafterf(down, INFINITY);
   const int k = (int)std::lround(8.0 * (c - (double)down) / ((double)up - (double)down));
   for (int i = 0; i < 4; ++i) a.c_mix[i] = make_float2(2 * i < k ? up : down, 2 * i + 1 < k ? up : down);
-  a.inv_temp = (float)(1.0 / (double)b->temperature);
+  a.inv_temp = (float)(1.0 / b->temperature);
   a.grad_scale = 1.f;
   return a;
 }

@@ -71,7 +71,7 @@ def _batch(nsm, **over):
     base = dict(logits=1 << 20, targets=1 << 21, mask=0, tokens=4, vocab=10, row_stride=0, dtype=0, temperature=1.0)
     base.update(over)
     return nsm.muon_token_batch(*[base[k] for k in ("logits", "targets", "mask", "tokens", "vocab", "row_stride",
-                                                    "dtype", "temperature")])
+                                                    "temperature", "dtype")])
 
 
 def _policy(nsm, batch=None, cfg=None, old=1 << 22, ref=0, adv=1 << 22, offsets=0, n_seqs=0, stats=1 << 22, logp=0,
