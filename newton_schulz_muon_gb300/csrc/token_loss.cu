@@ -317,14 +317,16 @@ __device__ __forceinline__ Prob row_prob(const RowArgs& a, const Sum& t, float z
   return p;
 }
 
-// The gradient's elements: factor 2^(c (z_j - m)), and at_y at the target.
+// The gradient's elements: factor 2^(c (z_j - m)), and at_y at the target.  Both are zero
+// for a row that does not move the loss: its elements are then, whatever its logits.
 struct Factor {
   float m, factor, at_y;
+  __device__ __forceinline__ bool none() const { return factor == 0.f && at_y == 0.f; }
 };
 
 __device__ __forceinline__ Factor row_factor(const RowArgs& a, float m, float s, float logp, float slope) {
   const float f = slope * a.grad_scale * a.inv_temp;
-  return Factor{m, f == 0.f ? 0.f : -f / s, -f * expm1f(logp)};
+  return f == 0.f ? Factor{m, 0.f, 0.f} : Factor{m, -f / s, -f * expm1f(logp)};
 }
 
 // A position's scalars.
@@ -746,7 +748,7 @@ __global__ void __launch_bounds__(kMaxRowThreads + 32) row_kernel(const __grid_c
           const int e = rank == 0 ? edge_of(row_of(logits + pos * a.stride, a.vocab), a.vocab, lane) : -1;
           __syncwarp();
           factor_arrive(par, all);
-          if (e >= 0) Vec<T>::store(g + e, at_edge ? f.at_y : f.factor * Expo<T>(a, f.m).one(edge[1]));
+          if (e >= 0) Vec<T>::store(g + e, f.none() ? 0.f : at_edge ? f.at_y : f.factor * Expo<T>(a, f.m).one(edge[1]));
         }
       }
       if (!has_grad) factor_arrive(par, all);  // the other warps keep the row's distance all the same
@@ -806,6 +808,9 @@ __global__ void __launch_bounds__(kMaxRowThreads + 32) row_kernel(const __grid_c
         const Factor f = sh.factor[(i - 1) % kSlots];
         x.frame(f.m);
         int l = tid;
+        if (f.none()) {
+          for (; l < cnt; l += nt) store_unit(g + (int64_t)l * N, make_uint4(0, 0, 0, 0), whole);
+        }
         if (whole) {
           for (; l + (kGroup - 1) * nt < cnt; l += kGroup * nt) {
             uint4 w[kGroup];
@@ -963,9 +968,9 @@ __global__ void __launch_bounds__(kWarpRowThreads, kUnits > 4 ? 2 : 3) warp_row_
       acc.add(o.terms);
       if (has_grad) {
         const Factor f = row_factor(a, s.m, p.s, p.logp, o.slope);
-        if (!aligned_unit(g + row.head)) {  // (then g is not z) element by element
+        if (f.none() || !aligned_unit(g + row.head)) {  // zeros; or (then g is not z) element by element
           for (int j = lane; j < a.vocab; j += 32)
-            Vec<T>::store(g + j, j == y ? f.at_y : f.factor * x.one(Vec<T>::load(z + j)));
+            Vec<T>::store(g + j, f.none() ? 0.f : j == y ? f.at_y : f.factor * x.one(Vec<T>::load(z + j)));
           continue;
         }
         T* dst = g + row.head + lane * N;
@@ -1082,9 +1087,9 @@ __global__ void __launch_bounds__(kMaxRowThreads) stream_kernel(const __grid_con
     x.frame(f.m);
     const bool whole = aligned_unit(g + row.head);
     for (int l = tid; l < row.units; l += nt)
-      store_unit(g + row.head + (int64_t)l * N, scaled_unit<T>(src[l], x, f.factor), whole);
+      store_unit(g + row.head + (int64_t)l * N, f.none() ? make_uint4(0, 0, 0, 0) : scaled_unit<T>(src[l], x, f.factor), whole);
     if (unit >= 0 && unit % nt == tid) Vec<T>::store(g + y, f.at_y);
-    if (edge >= 0) Vec<T>::store(g + edge, edge == y ? f.at_y : f.factor * x.one(zedge));
+    if (edge >= 0) Vec<T>::store(g + edge, f.none() ? 0.f : edge == y ? f.at_y : f.factor * x.one(zedge));
     __syncthreads();  // factor is free
   }
   if (kMode == kForward && blockIdx.x == 0 && tid == 0) *a.ticket = 0;

@@ -202,6 +202,26 @@ def test_gaps_around_the_sequences_have_no_weight(m):
     assert (grad[:4] == 0).all() and (grad[22:] == 0).all()
 
 
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("v", [200, 5003, 131072, 500009])
+def test_rows_that_move_nothing_have_zero_gradients(m, dtype, v):
+    """Positions of no sequence take no part, whatever their logits; a clipped position's row is zero."""
+    import torch
+    b = Batch(8, v, dtype, pad=1, drop=None)
+    b.logits[:2] = math.nan
+    b.logits[7, 1:] = math.inf
+    one = torch.ones(8, device="cuda")
+    off = torch.tensor([2, 4, 7], device="cuda")
+    cfg = m.muon_policy_config_default(reduction=m.MUON_REDUCE_SEQUENCE_MEAN)
+    for args in (dict(), dict(grad=torch.empty(8, v, device="cuda", dtype=b.logits.dtype))):
+        stats, _, grad = m.muon_policy_loss(b.logits, b.y, one * -50, one, seq_offsets=off, config=cfg, **args)
+        assert stats.tolist() == pytest.approx([-1.2, -1.2, 0.0, 1.0], rel=1e-6)     # every ratio is above the limit
+        assert (grad == 0).all()
+        out = m.muon_preference_loss(b.logits, b.y, off, one[:2], **args)
+        assert torch.isfinite(out[0]).all() and torch.isfinite(out[3]).all()
+        assert (out[3][:2] == 0).all() and (out[3][7] == 0).all() and (out[3][2:7] != 0).any(1).all()
+
+
 def test_offsets_out_of_range_stay_inside(m):
     # offsets beyond the batch are cut to it: nothing outside the buffers is touched
     b = Batch(12, 100, drop=None)
