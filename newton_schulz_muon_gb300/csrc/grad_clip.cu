@@ -8,6 +8,11 @@
 // them are marked to be evicted first), scaled and written.  The tensor table travels as a kernel
 // parameter, so a call copies nothing to the device and waits for nothing on the host.
 //
+// Measured: the norm of a 36-layer model's 7.3 GB of bf16 gradients 1.02 ms (7.1 TB/s; in
+// place below the limit that is the whole call); one layer's 202 MB of bf16 gradients into
+// fp32 0.135 ms: 0.035 ms for the norm, 0.100 ms for 606 MB of the second pass (6.1 TB/s);
+// 1003 tensors of up to 40000 elements, 141 MB, 0.042 ms.
+//
 // The unit of work is a chunk of kChunk elements of one tensor, taken by one warp: a
 // set of a thousand small tensors spreads over the GPU like one large tensor does.
 // A warp's chunks are warp, warp + warps, ...: every partial sum has a fixed place and
@@ -323,7 +328,7 @@ struct Octet<false> {
 };
 
 // fp32 octets leave as whole 32-byte sectors where they are aligned to them (404 MB from
-// 202 MB of bf16: 138 us in halves).
+// 202 MB of bf16: 138 us in halves, 105 us so).
 template <bool kBf16>
 __device__ __forceinline__ void store8(void* out, int64_t i, const float (&r)[8], bool sectors) {
   if (kBf16) {

@@ -18,8 +18,8 @@
 // which the sum over a sequence adds up.  fp32 logits, which HBM delivers more slowly
 // than the SMs can take them, use c as two floats; for bf16 logits, where every
 // instruction counts, the eight elements of a 16-byte unit take the two floats next to c
-// in the proportion that gives c in the mean (4096 x 131072 policy loss: 0.400 ms with
-// two floats, 0.370 ms this way).
+// in the proportion that gives c in the mean (4096 x 131072 policy loss, when this was
+// chosen: 0.400 ms with two floats, 0.370 ms with one; HBM's time is 0.316 ms).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -542,6 +542,15 @@ __device__ __forceinline__ void finish_stats(const RowArgs& a, StatsShared& sh, 
 // i - 2 from its own CTA's finishing warp; that took the sums of row i - 2 from every CTA,
 // which were sent after the results of row i - 4 there: slot i - 4 = i mod kSlots has been
 // read in every CTA.
+//
+// Bound by HBM, and nearly as much by the SM's issue slots (55% taken on 608 x 131072 bf16
+// rows: 14.5 instructions a logit, 9 of them the two exponentials, their unpacking and
+// packing; the rest a row's fixed cost over 8 units a thread), which is why the warps read
+// a row's places from shared memory and test nothing inside their loops.  4096 x 131072
+// bf16, a fifth masked: 0.307 ms, 6.3 TB/s of compulsory traffic (the same with the row
+// read twice from memory: 0.50 ms; with a cluster barrier a row instead of the asynchronous
+// stores: 0.42 ms; with 384 or 640 threads: 0.33 and 0.34 ms).  6250 x 32000 fp32: 0.245 ms,
+// 5.9 TB/s.
 template <typename T, int kMode, int kStages>
 __global__ void __launch_bounds__(kMaxRowThreads + 32) row_kernel(const __grid_constant__ RowArgs a) {
   constexpr int N = Vec<T>::N;
@@ -867,7 +876,9 @@ __global__ void __launch_bounds__(kMaxRowThreads + 32) row_kernel(const __grid_c
 
 // Rows of at most 32 kUnits 16-byte units (and the elements around them): one warp holds a
 // row in registers, and nothing is shared between warps.  The row's largest logit is known
-// before the first exponential.
+// before the first exponential.  Bound by the latency of a row's loads (16 warps an SM, 122
+// registers) and by issue (53%): 20011 x 4099 bf16, a tenth masked, 0.061 ms, 5.1 TB/s of
+// compulsory traffic; with a CTA a row (row_kernel) 0.093 ms.
 constexpr int kWarpRowThreads = 256;
 constexpr int kWarpRowWarps = kWarpRowThreads / 32;
 
@@ -1013,7 +1024,9 @@ __global__ void __launch_bounds__(kWarpRowThreads, kUnits > 4 ? 2 : 3) warp_row_
 // Rows straight from memory, one CTA a row: where nothing is written back a row need not
 // stay on chip, and many CTAs an SM hide a row's end behind others' loads.  A different warp
 // forms each row's result while the others go on to the next.  With a gradient (rows too
-// long for a cluster's shared memory) the row is read a second time.
+// long for a cluster's shared memory) the row is read a second time.  Bound by HBM: 16411 x
+// 131072 bf16, a tenth masked, 0.567 ms, 6.8 TB/s (persistent CTAs with rows dealt out in
+// turn: 0.63 ms, since masked rows leave some idle; row_kernel: 1.1 ms).
 template <typename T, int kMode>
 __global__ void __launch_bounds__(kMaxRowThreads) stream_kernel(const __grid_constant__ RowArgs a) {
   constexpr int N = Vec<T>::N;
@@ -1109,7 +1122,8 @@ __global__ void __launch_bounds__(kMaxRowThreads) stream_kernel(const __grid_con
 // The gradient of rows whose slope, frame and sum are known, a piece of kPiece units a
 // CTA; the last rows first, whose logits the forward pass left in L2 (a gradient too large
 // for L2 does not displace them: 1024 x 65536 fp32, forward and backward 125 us with the
-// default policies, 117 us so).
+// default policies, 117 us so).  Bound by HBM: with its forward pass 8192 x 131072 bf16, a
+// quarter masked, in 0.79 ms, 6.8 TB/s of the three passes' traffic.
 constexpr int kPieceThreads = 256;
 constexpr int kPiece = kPieceThreads * kGroup;
 
@@ -1335,7 +1349,8 @@ struct PairArgs {
 
 // One CTA a pair: half of it sums each sequence, one thread forms the margin (in 64 bits:
 // a difference of long sums), and each half writes the slopes of its positions.  The last
-// CTA to come forms the mean over the pairs, in their order.
+// CTA to come forms the mean over the pairs, in their order.  Bound by latency (6 us for
+// sequences of 50 positions).
 __global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constant__ PairArgs a) {
   constexpr int kHalf = kPairThreads / 2, kWarps = kPairThreads / 32;
   __shared__ Pair sums[kWarps];
