@@ -547,10 +547,10 @@ __device__ __forceinline__ void finish_stats(const RowArgs& a, StatsShared& sh, 
 // rows: 14.5 instructions a logit, 9 of them the two exponentials, their unpacking and
 // packing; the rest a row's fixed cost over 8 units a thread), which is why the warps read
 // a row's places from shared memory and test nothing inside their loops.  4096 x 131072
-// bf16, a fifth masked: 0.307 ms, 6.3 TB/s of compulsory traffic (the same with the row
-// read twice from memory: 0.50 ms; with a cluster barrier a row instead of the asynchronous
-// stores: 0.42 ms; with 384 or 640 threads: 0.33 and 0.34 ms).  6250 x 32000 fp32: 0.245 ms,
-// 5.9 TB/s.
+// bf16, a fifth masked: 0.309 ms, 6.3 TB/s of compulsory traffic (with the row read twice
+// from memory, stream_kernel: 0.483 ms; with 384 or 256 threads: 0.320 and 0.337 ms; when
+// asynchronous stores took the place of a cluster barrier a row, 0.416 ms became 0.365 ms).
+// 6250 x 32000 fp32: 0.245 ms, 5.9 TB/s.
 template <typename T, int kMode, int kStages>
 __global__ void __launch_bounds__(kMaxRowThreads + 32) row_kernel(const __grid_constant__ RowArgs a) {
   constexpr int N = Vec<T>::N;
@@ -878,7 +878,7 @@ __global__ void __launch_bounds__(kMaxRowThreads + 32) row_kernel(const __grid_c
 // row in registers, and nothing is shared between warps.  The row's largest logit is known
 // before the first exponential.  Bound by the latency of a row's loads (16 warps an SM, 122
 // registers) and by issue (53%): 20011 x 4099 bf16, a tenth masked, 0.061 ms, 5.1 TB/s of
-// compulsory traffic; with a CTA a row (row_kernel) 0.093 ms.
+// compulsory traffic; with a CTA a row (row_kernel) 0.094 ms.
 constexpr int kWarpRowThreads = 256;
 constexpr int kWarpRowWarps = kWarpRowThreads / 32;
 
@@ -1026,7 +1026,7 @@ __global__ void __launch_bounds__(kWarpRowThreads, kUnits > 4 ? 2 : 3) warp_row_
 // forms each row's result while the others go on to the next.  With a gradient (rows too
 // long for a cluster's shared memory) the row is read a second time.  Bound by HBM: 16411 x
 // 131072 bf16, a tenth masked, 0.567 ms, 6.8 TB/s (persistent CTAs with rows dealt out in
-// turn: 0.63 ms, since masked rows leave some idle; row_kernel: 1.1 ms).
+// turn: 0.614 ms, since masked rows leave some idle; row_kernel: 0.807 ms).
 template <typename T, int kMode>
 __global__ void __launch_bounds__(kMaxRowThreads) stream_kernel(const __grid_constant__ RowArgs a) {
   constexpr int N = Vec<T>::N;
@@ -1534,6 +1534,16 @@ size_t row_smem(int64_t units, int cluster, int stages) {
   return (size_t)stages * (size_t)((units + cluster - 1) / cluster) * 16 + sizeof(RowShared) + sums;
 }
 
+// Threads that hold units, of all CTAs that an SM has room for; 0: a CTA does not fit.
+int resident_threads(int64_t units, int cluster, int stages) {
+  const size_t smem = row_smem(units, cluster, stages);
+  if (smem > kSmemPerSm) return 0;
+  const int threads = row_threads(units, cluster), all = threads + 32;
+  const int by_smem = (int)((kSmemPerSm + 1024) / (smem + 1024));
+  const int by_regs = 65536 / (all * (stages == 3 ? 80 : 64));
+  return threads * (by_smem < by_regs ? by_smem : by_regs);
+}
+
 RowShape row_shape(int64_t vocab, int32_t dtype, int64_t tokens, int sms, bool resident) {
   const int64_t per_unit = dtype == MUON_DTYPE_BF16 ? 8 : 4;
   const int64_t units = vocab / per_unit < 1 ? 1 : vocab / per_unit;
@@ -1545,24 +1555,35 @@ RowShape row_shape(int64_t vocab, int32_t dtype, int64_t tokens, int sms, bool r
     s.warp_units = units <= 128 ? 4 : units <= 256 ? 8 : 16;
     return s;
   }
-  // The fewest CTAs a row that hold three rows (or, four CTAs of two rows where two CTAs fit
-  // an SM; clusters of eight leave SMs idle, so four CTAs of two rows come before them).
-  // bf16 rows, GB/s of compulsory traffic: 100000 logits 5420 (4 CTAs, 2 rows, two an SM),
-  // 4670 (4, 3), 5035 (2, 2); 131072 5980 (4, 3), 4400 (8, 3); 200064 4890 (4, 2), 3990 (8, 3).
-  struct Choice {
-    int cluster, stages;
-    size_t most;
+  const auto take = [&](int cluster, int stages) {
+    s.cluster = cluster;
+    s.stages = stages;
+    s.smem = row_smem(units, cluster, stages);
   };
-  static const Choice choices[] = {{1, 3, kSmemPerSm}, {2, 3, kSmemPerSm}, {4, 2, kSmemPerSm / 2 - 1024},
-                                   {4, 3, kSmemPerSm}, {4, 2, kSmemPerSm}, {8, 3, kSmemPerSm}, {8, 2, kSmemPerSm}};
-  if (split > 1 || resident)
-    for (const Choice& c : choices) {
-      if (c.cluster < split || row_smem(units, c.cluster, c.stages) > c.most) continue;
-      s.cluster = c.cluster;
-      s.stages = c.stages;
-      s.smem = row_smem(units, c.cluster, c.stages);
-      break;
-    }
+  if (split > 1) {
+    for (int c = split; c <= kMaxCluster && s.cluster == 0; c *= 2)
+      for (int stages = 3; stages >= 2 && s.cluster == 0; --stages)
+        if (resident_threads(units, c, stages) > 0) take(c, stages);
+  } else if (resident) {
+    // Three rows of the ring keep HBM busy with some 480 threads an SM that hold units (448
+    // where a CTA has the whole row: bf16 28000 logits 5790 GB/s of compulsory traffic, two
+    // CTAs and rows 5460; but 110000 logits 5050 with four CTAs and three rows, 5490 with
+    // eight and two), two rows with some 850; clusters of eight fill the SMs badly unless
+    // several of their CTAs share one.  GB/s, CTAs a row / rows: bf16 50000 logits 4/2 5540,
+    // 2/3 5050, 8/2 5120; 65536 2/3 6170, 4/2 5870; 100000 8/2 5590, 4/2 5250, 4/3 4790;
+    // 131072 4/3 5960, 4/2 4610; 200064 8/2 5290, 4/2 4870; fp32 20000 4/3 6100, 2/3 5130;
+    // 131072 8/3 5530, 8/2 4480.
+    for (int c = 1; c <= 4 && s.cluster == 0; c *= 2)
+      if (resident_threads(units, c, 3) >= (c == 1 ? 448 : 480)) take(c, 3);
+    int best = 0, best_cluster = 0;
+    for (int c = 1; c <= kMaxCluster; c *= 2)
+      if (resident_threads(units, c, 2) > best) {
+        best = resident_threads(units, c, 2);
+        best_cluster = c;
+      }
+    if (s.cluster == 0 && best < 832 && resident_threads(units, kMaxCluster, 3) >= 512) take(kMaxCluster, 3);
+    if (s.cluster == 0 && best > 0) take(best_cluster, 2);
+  }
   if (s.cluster == 0) {
     // many rows: small CTAs, whose ends overlap; few: enough threads to fill the SMs
     s.threads = units <= 8192 ? 64 : 256;
