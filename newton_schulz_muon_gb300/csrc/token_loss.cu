@@ -19,7 +19,7 @@
 // than the SMs can take them, use c as two floats; for bf16 logits, where every
 // instruction counts, the eight elements of a 16-byte unit take the two floats next to c
 // in the proportion that gives c in the mean (4096 x 131072 policy loss, when this was
-// chosen: 0.400 ms with two floats, 0.370 ms with one; HBM's time is 0.316 ms).
+// chosen: 0.400 ms with two floats, 0.370 ms with one; HBM's time is 0.285 ms).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -877,8 +877,9 @@ __global__ void __launch_bounds__(kMaxRowThreads + 32) row_kernel(const __grid_c
 // Rows of at most 32 kUnits 16-byte units (and the elements around them): one warp holds a
 // row in registers, and nothing is shared between warps.  The row's largest logit is known
 // before the first exponential.  Bound by the latency of a row's loads (16 warps an SM, 122
-// registers) and by issue (53%): 20011 x 4099 bf16, a tenth masked, 0.061 ms, 5.1 TB/s of
-// compulsory traffic; with a CTA a row (row_kernel) 0.094 ms.
+// registers) and by issue (53%): 20011 x 4099 bf16, a tenth masked, 0.062 ms, 5.0 TB/s of
+// compulsory traffic; with a CTA a row (row_kernel) 0.094 ms; with the next row copied to
+// shared memory meanwhile 0.073 ms (rows of 1024 to 4000 logits 0 to 12% slower so, too).
 constexpr int kWarpRowThreads = 256;
 constexpr int kWarpRowWarps = kWarpRowThreads / 32;
 
