@@ -448,6 +448,14 @@ def _blocks(t):
     return (elems, 1, 0) if outer is None else (elems, outer[0], outer[1])
 
 
+def _same_layout(g, o):
+    """Whether o's elements lie as g's do: its shape and strides (where they matter), or both
+    contiguous with as many elements."""
+    if g.is_contiguous() and o.is_contiguous():
+        return g.numel() == o.numel()
+    return g.shape == o.shape and all(a == b or n == 1 for a, b, n in zip(g.stride(), o.stride(), g.shape))
+
+
 class GradSet:
     """Gradient tensors (and where their clipped values go) as the library takes them.  A
     program whose gradients stay in place makes one and passes it to every call.  An output
@@ -483,7 +491,7 @@ class GradSet:
             words[5::6] = _words([c | o << 32 for c, o in zip(codes, out_codes)], n)
             if not dense or not out_dense or words[2::6] != _words(map(tensor.numel, out), n):
                 for i, (g, o) in enumerate(zip(grads, out)):
-                    if o.shape != g.shape or (o.stride() != g.stride() and not (o.is_contiguous() and g.is_contiguous())):
+                    if not _same_layout(g, o):
                         raise ValueError(f"gradient {i}: out has another layout")
         if -1 in devices or len(devices) > 1:
             raise ValueError("gradients and outputs must be CUDA tensors of one device")

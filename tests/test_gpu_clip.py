@@ -125,6 +125,25 @@ def test_strided_and_permuted_layouts(m):
     _check(torch, m, [one], 0.1, [torch.empty(12, 7, device="cuda").t()])
 
 
+def test_output_layouts_beside_a_strided_gradient(m):
+    import torch
+    # what counts as an output's layout does not depend on the set's other tensors
+    flat = torch.randn(6, device="cuda")
+    wide = torch.randn(4, 5, device="cuda")
+    whole = torch.empty(2, 3, device="cuda")
+    out = torch.empty(4, 5, device="cuda")[:, :3]
+    result = m.muon_clip_grad_norm([flat, wide[:, :3]], 0.5, out=[whole, out])
+    factor = result[1].item()
+    assert torch.equal(whole.flatten(), flat * factor) and torch.equal(out, wide[:, :3] * factor)
+    one = torch.empty(1, 7, 5, device="cuda").as_strided((1, 7, 3), (99, 5, 1))   # a stride that nothing uses
+    src = torch.randn(1, 7, 5, device="cuda")[:, :, :3]
+    factor = m.muon_clip_grad_norm([src], 0.5, out=[one])[1].item()
+    assert torch.equal(one, src * factor)
+    for wrong in (torch.empty(4, 6, device="cuda")[:, :3], torch.empty(4, 3, device="cuda"), torch.empty(6, 5, device="cuda")[:, :2]):
+        with pytest.raises(ValueError, match="layout"):
+            m.muon_clip_grad_norm([wide[:, :3]], 0.5, out=[wrong])
+
+
 @pytest.mark.parametrize("scale", [1e-38, 1e-30, 1e-22, 1e-17, 1e15, 1e19, 1e25, 1e33])
 @pytest.mark.parametrize("n", [5, 70001])
 def test_full_range(m, scale, n):
