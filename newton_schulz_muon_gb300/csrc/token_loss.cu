@@ -1569,11 +1569,12 @@ RowShape row_shape(int64_t vocab, int32_t dtype, int64_t tokens, int sms, bool r
     // Three rows of the ring keep HBM busy with some 480 threads an SM that hold units (448
     // where a CTA has the whole row: bf16 28000 logits 5790 GB/s of compulsory traffic, two
     // CTAs and rows 5460; but 110000 logits 5050 with four CTAs and three rows, 5490 with
-    // eight and two), two rows with some 850; clusters of eight fill the SMs badly unless
-    // several of their CTAs share one.  GB/s, CTAs a row / rows: bf16 50000 logits 4/2 5540,
-    // 2/3 5050, 8/2 5120; 65536 2/3 6170, 4/2 5870; 100000 8/2 5590, 4/2 5250, 4/3 4790;
-    // 131072 4/3 5960, 4/2 4610; 200064 8/2 5290, 4/2 4870; 240000 8/3 4530, 8/2 3590; fp32 20000
-    // 4/3 6100, 2/3 5130; 120000 8/3 4940, 8/2 3980; 131072 8/3 5530, 8/2 4480.
+    // eight and two), two rows with more; clusters of eight fill the SMs badly unless several
+    // of their CTAs share one.  GB/s, CTAs a row / rows: bf16 50000 logits 4/2 5540, 2/3 5050,
+    // 8/2 5120; 65536 2/3 6170, 4/2 5870; 90000 8/2 5420, 8/3 5190; 100000 8/2 5590, 4/2 5250,
+    // 4/3 4790; 131072 4/3 5960, 4/2 4610; 200064 8/2 5290, 4/2 4870; 240000 8/3 4530, 8/2
+    // 3590; fp32 20000 4/3 6100, 2/3 5130; 48000 8/2 6250, 8/3 6400; 120000 8/3 4940, 8/2
+    // 3980; 131072 8/3 5530, 8/2 4480.
     for (int c = 1; c <= 4 && s.cluster == 0; c *= 2)
       if (resident_threads(units, c, 3) >= (c == 1 ? 448 : 480)) take(c, 3);
     int best = 0, best_cluster = 0;
@@ -1582,7 +1583,7 @@ RowShape row_shape(int64_t vocab, int32_t dtype, int64_t tokens, int sms, bool r
         best = resident_threads(units, c, 2);
         best_cluster = c;
       }
-    if (s.cluster == 0 && best < 832 && resident_threads(units, kMaxCluster, 3) >= 480) take(kMaxCluster, 3);
+    if (s.cluster == 0 && best < 576 && resident_threads(units, kMaxCluster, 3) >= 480) take(kMaxCluster, 3);
     if (s.cluster == 0 && best > 0) take(best_cluster, 2);
   }
   if (s.cluster == 0) {

@@ -80,6 +80,19 @@ def test_policy_rows(m, n, v, dtype, mask):
     _policy(m, n, v, dtype, mask)
 
 
+# one row's CTAs and the rows of their ring: 2/2, 8/2 with several CTAs an SM, 4/3, 8/3
+MORE_SHAPES = [(3001, 20001, "bfloat16"), (2000, 54005, "bfloat16"), (3000, 45001, "bfloat16"), (2001, 90007, "bfloat16"),
+               (1000, 200064, "bfloat16"), (900, 240001, "bfloat16"), (500, 320003, "bfloat16"),
+               (3000, 11001, "float32"), (2500, 25003, "float32"), (1500, 50001, "float32"), (1000, 100001, "float32"),
+               (700, 120003, "float32"), (500, 151936, "float32")]
+
+
+@pytest.mark.parametrize("n,v,dtype", MORE_SHAPES)
+@pytest.mark.parametrize("mask", ["all", "random"])
+def test_policy_rows_of_more_launch_shapes(m, n, v, dtype, mask):
+    _policy(m, n, v, dtype, mask, pad=1)
+
+
 @pytest.mark.parametrize("n", [1, 2, 31, 152, 153, 600, 1217, 2431, 2433, 5000])
 @pytest.mark.parametrize("mask", ["all", "front", "back", "blocks"])
 @pytest.mark.parametrize("v,dtype", [(9001, "bfloat16"), (600, "float32"), (33003, "float32")])
