@@ -508,7 +508,7 @@ struct Terms {
 };
 
 // The CTA's sums into the partials; the last of `n` CTAs to come adds all of them, in
-// their order.
+// their order (a warp a sum; a CTA may have fewer warps than there are sums).
 __device__ __forceinline__ void finish_stats(const RowArgs& a, StatsShared& sh, int64_t part, int64_t n) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   __syncthreads();
@@ -519,13 +519,14 @@ __device__ __forceinline__ void finish_stats(const RowArgs& a, StatsShared& sh, 
     sh.last = atomicAdd(a.ticket, 1u) == (unsigned)n - 1;
   }
   __syncthreads();
-  if (sh.last && warp < 4) {
-    __threadfence();
+  if (!sh.last) return;
+  __threadfence();
+  for (int j = warp; j < 4; j += blockDim.x >> 5) {
     double sum = 0.0;
-    for (int64_t k = lane; k < n; k += 32) sum += __ldcg(a.partials + 4 * k + warp);
+    for (int64_t k = lane; k < n; k += 32) sum += __ldcg(a.partials + 4 * k + j);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    if (lane == 0) a.stats[warp] = (float)sum;
+    if (lane == 0) a.stats[j] = (float)sum;
   }
 }
 

@@ -193,3 +193,54 @@ def test_two_threads_on_one_stream(m):
     for f in seen:
         assert len(seen[f]) == 200
         assert all(torch.equal(a, b) for got in seen[f] for a, b in zip(want[f], got))
+
+
+# rows, logits, type: without a gradient rows come from memory with 64, 128, 256 and 512
+# threads (both sides of each step), through a cluster where they are few, or a warp a row
+LOSS_ONLY = [(5000, 9001, "bfloat16"), (1217, 20001, "float32"), (1216, 20001, "float32"), (609, 20001, "bfloat16"),
+             (608, 20001, "bfloat16"), (304, 33003, "float32"), (2500, 131072, "bfloat16"), (400, 131072, "bfloat16"),
+             (304, 131072, "float32"), (31, 33003, "float32"), (5, 131072, "bfloat16"), (20000, 1000, "bfloat16"),
+             (1, 50001, "float32")]
+
+
+@pytest.mark.parametrize("n,v,dtype", LOSS_ONLY)
+@pytest.mark.parametrize("mask", ["none", "blocks"])
+def test_policy_without_a_gradient_writes_every_output(m, n, v, dtype, mask):
+    """The statistics and log-probabilities of a loss-only call, into tensors that hold NaN before it."""
+    import torch
+    z, y, live, gen = _inputs(n, v, dtype, mask, 2, seed=n + v)
+    logp = _reference(z, y, live, 0.9)
+    delta = 0.3 * torch.randn(n, generator=gen, device="cuda", dtype=torch.float64)
+    for lim in (math.log(0.8), math.log(1.2)):
+        delta = torch.where((delta - lim).abs() < 2e-3, delta + 5e-3, delta)
+    old, adv = (logp - delta).float(), torch.randn(n, generator=gen, device="cuda")
+    ref = (logp + 0.3).float()
+    cfg = m.muon_policy_config_default(kl_beta=0.1)
+    stats, got = (torch.full((k,), math.nan, device="cuda") for k in (4, n))
+    out = m.muon_policy_loss(z, y, old, adv, mask=live, ref_logp=ref, temperature=0.9, config=cfg, with_grad=False,
+                             stats=stats, logp=got)
+    assert out[0] is stats and out[1] is got and out[2] is None
+    w = torch.ones(n, dtype=torch.float64, device="cuda") if live is None else live.double()
+    w /= w.sum().clamp(min=1)
+    r = (logp - old.double()).exp()
+    plain, held = r * adv, r.clamp(float(torch.tensor(1 - 0.2)), float(torch.tensor(1.2))) * adv
+    d = ref.double() - logp
+    s, k = torch.minimum(plain, held), torch.expm1(d) - d
+    want = torch.stack([(w * (0.1 * k - s)).sum(), -(w * s).sum(), (w * k).sum(), (w * (held < plain)).sum()])
+    size = (w * (plain.abs() + 0.1 * (1 + d.exp()))).sum() + 2
+    assert ((got.double() - logp).abs() <= LP_ABS + LP_REL * logp.abs()).all()
+    assert ((stats.double() - want).abs() <= 2e-5 * size).all(), (stats.tolist(), want.tolist())
+
+
+@pytest.mark.parametrize("n,v,dtype", LOSS_ONLY)
+def test_preference_without_a_gradient_writes_every_output(m, n, v, dtype):
+    import torch
+    z, y, live, _ = _inputs(n, v, dtype, "blocks", 2, seed=n)
+    off = torch.tensor([0, n // 3, n // 2, n // 2, n], device="cuda")
+    refs = torch.zeros(4, device="cuda")
+    want = m.muon_preference_loss(z, y, off, refs, mask=live)
+    outs = [torch.full((k,), math.nan, device="cuda") for k in (1, 2, 4)]
+    got = m.muon_preference_loss(z, y, off, refs, mask=live, with_grad=False, loss=outs[0], margins=outs[1],
+                                 seq_logp=outs[2])
+    assert got[3] is None and all(torch.equal(a, b) for a, b in zip(want[:3], got[:3]))
+    assert all(torch.isfinite(t).all() for t in got[:3])
