@@ -516,7 +516,8 @@ void muon_preference_config_default(muon_preference_config* cfg);
  * sequence n_pairs + i.
  *   S_q = sum of logp over the sequence's unmasked positions (0 if there are none),
  *   h_i = beta ((S_i - R_i) - (S_{P+i} - R_{P+i})),
- *   L = (1/P) sum_i (-(1 - e) log sigmoid(h_i) - e log sigmoid(-h_i)),
+ *   L = (1/P) sum_i (-(1 - e) log sigmoid(h_i) - e log sigmoid(-h_i)), a term whose
+ *     factor (1 - e or e) is 0 being 0 where its logarithm is infinite too,
  *   grad[t, j] = grad_scale dL/dlogp_t / temperature (1[j = y_t] - softmax(z_t)_j).
  *   ref_logp: [2 n_pairs] fp32, R (formed like S, by the reference policy).
  *   seq_offsets: [2 n_pairs + 1] device, ascending from 0; positions in no sequence

@@ -1406,7 +1406,11 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constan
     if (a.margins) a.margins[i] = h;
     // log sigmoid(h) = min(h, 0) - log(1 + exp(-|h|))
     const float soft = log1pf(expf(-fabsf(h)));
-    a.pair_loss[i] = (1.f - a.smooth) * (soft - fminf(h, 0.f)) + a.smooth * (soft + fmaxf(h, 0.f));
+    // an infinite margin (an answer with a token that cannot be taken) has a term of infinity,
+    // which counts for nothing where its weight is zero
+    const float won = a.smooth < 1.f ? (1.f - a.smooth) * (soft - fminf(h, 0.f)) : 0.f;
+    const float lost = a.smooth > 0.f ? a.smooth * (soft + fmaxf(h, 0.f)) : 0.f;
+    a.pair_loss[i] = won + lost;
     const float up = 1.f / (1.f + expf(-h)), down = 1.f / (1.f + expf(h));
     const float d = a.beta / (float)a.n_pairs * (a.smooth * up - (1.f - a.smooth) * down);
     slope[0] = d * per[0];

@@ -105,7 +105,8 @@ def preference_loss(logits, targets, offsets, ref, *, mask=None, temperature=1.0
     gain = sums - np.asarray(ref, np.float64)
     margins = beta * (gain[:pairs] - gain[pairs:])
     log_sig = lambda h: -np.logaddexp(0.0, -h)  # noqa: E731
-    loss = np.mean(-(1 - smooth) * log_sig(margins) - smooth * log_sig(-margins)) if pairs else 0.0
+    term = lambda weight, h: weight * log_sig(h) if weight else np.zeros(pairs)  # noqa: E731  (0, not 0 * inf)
+    loss = -np.mean(term(1 - smooth, margins) + term(smooth, -margins)) if pairs else 0.0
     slope = np.zeros(n)
     for i in range(pairs):
         sig = np.exp(log_sig(margins[i]))

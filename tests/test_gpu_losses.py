@@ -549,3 +549,34 @@ def test_refusals(m):
         m.muon_policy_loss(z, y, f, f, workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))
     assert e.value.status == m.MUON_ERR_NO_WORKSPACE
     assert m.muon_token_logprobs(z, y)[0].item() == pytest.approx(-math.log(30), rel=1e-6)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("v", [200, 5003, 131072])
+@pytest.mark.parametrize("mean", [False, True])
+@pytest.mark.parametrize("smooth", [0.0, 0.25, 1.0])
+@pytest.mark.parametrize("answer", ["preferred", "other"])
+def test_preference_of_impossible_answers(m, dtype, v, mean, smooth, answer):
+    """An answer with a token that cannot be taken: margin +-inf, a loss that is infinite only
+    where its weight is not 0, and finite gradients."""
+    b = Batch(9, v, dtype, pad=1, drop=None)
+    offsets = np.array([0, 2, 4, 7, 9], np.int64)     # pair 0: rows 0-1 over 4-6, pair 1: rows 2-3 over 7-8
+    row = 3 if answer == "preferred" else 7
+    b.logits[row, int(b.targets[row])] = -math.inf
+    b.z = _f64(b.logits)
+    with np.errstate(divide="ignore"):
+        b.logp = losses.token_logprobs(b.z, b.targets)
+    ref = b.rng.normal(-5, 1, 4).astype(np.float32)
+    want = losses.preference_loss(b.z, b.targets, offsets, ref, beta=0.5, smooth=smooth, mean=mean, logp=b.logp)
+    cfg = m.muon_preference_config_default(beta=0.5, label_smoothing=smooth, length_normalize=int(mean))
+    loss, margins, sums, grad = m.muon_preference_loss(b.logits, b.y, _dev(offsets), _dev(ref), config=cfg)
+    sign = -1 if answer == "preferred" else 1
+    assert margins[1].item() == sign * math.inf and sums[1 if answer == "preferred" else 3].item() == -math.inf
+    # rows 0-1 and 4-6: at most LP_ABS + LP_REL |logp| each
+    off = 0.5 * sum(LP_ABS + LP_REL * abs(b.logp[t]) for t in (0, 1, 4, 5, 6)) + 2 ** -22 * (1 + abs(want["margins"][0]))
+    assert abs(margins[0].item() - want["margins"][0]) <= off
+    if smooth == (0.0 if answer == "other" else 1.0):
+        assert abs(loss.item() - want["loss"]) <= off + 2e-6 * (1 + want["loss"])
+    else:
+        assert loss.item() == math.inf == want["loss"]
+    b.check_grad(grad, want["slope"], np.abs(want["slope"]) * (2 + 1e4 * 0.25 * off) + 1e-12)

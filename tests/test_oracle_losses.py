@@ -102,3 +102,21 @@ def test_clip_factor():
     assert losses.clip_factor(5.0, 1.0, 0.0) == pytest.approx(0.2)
     assert losses.clip_factor(5.0, 5.0, 0.0) == 1.0 and losses.clip_factor(0.0, 0.0, 0.0) == 1.0
     assert losses.clip_factor(np.inf, 1.0, 0.0) == 1.0 and losses.clip_factor(np.nan, 1.0, 0.0, True) == 0.0
+
+
+@pytest.mark.parametrize("smooth", [0.0, 0.25, 1.0])
+def test_preference_of_impossible_answers(smooth):
+    """A margin of +-inf: a term of weight 0 is 0, another is its limit."""
+    logp, offsets, ref = np.array([-1.0, -np.inf, -2.0, -3.0]), [0, 1, 2, 3, 4], np.zeros(4)
+    # pair 0: an ordinary answer over an ordinary one (h = 0.1), pair 1: an impossible one over an ordinary one
+    out = losses.preference_loss(None, np.zeros(4, int), offsets, ref, logp=logp, smooth=smooth)
+    one = (1 - smooth) * np.log1p(np.exp(-0.1)) + smooth * np.log1p(np.exp(0.1))
+    assert out["margins"].tolist() == [pytest.approx(0.1), -np.inf]
+    assert out["loss"] == (pytest.approx(one / 2) if smooth == 1.0 else np.inf)
+    # pair 1 turned round
+    turned = losses.preference_loss(None, np.zeros(4, int), offsets, ref, logp=logp[[0, 3, 2, 1]], smooth=smooth)
+    assert turned["margins"].tolist() == [pytest.approx(0.1), np.inf]
+    assert turned["loss"] == (pytest.approx(one / 2) if smooth == 0.0 else np.inf)
+    # d loss / d margin = smooth sigmoid(h) - (1 - smooth) sigmoid(-h)
+    assert out["slope"][[1, 3]] == pytest.approx([-0.05 * (1 - smooth), 0.05 * (1 - smooth)])
+    assert turned["slope"][[1, 3]] == pytest.approx([0.05 * smooth, -0.05 * smooth])
