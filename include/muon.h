@@ -392,7 +392,9 @@ muon_status muon_get_input_norms(const muon_plan_t* plan, float* out, int64_t n,
  * scalars kept in fp32); the formulas are stated at each of them.  They take no plan, only
  * launch kernels on `stream` (capturable in a CUDA graph; the captured pointers
  * and scalars are replayed) and accept pointers aligned to one element; rows and
- * matrices that start on 16-byte boundaries move fastest.  Workspaces are the
+ * matrices that start on 16-byte boundaries move fastest.  The stream and every
+ * pointer belong to the current device (the Python binding makes its tensors' device
+ * the current one for the call).  Workspaces are the
  * caller's (16-byte aligned, contents irrelevant before and after) and are free
  * for other work on the same stream after the call.
  * ------------------------------------------------------------------------- */

@@ -403,14 +403,16 @@ _NO_CONTEXT = contextlib.nullcontext()
 
 
 def _on_stream(stream, device: int):
-    """(context for the tensors a call allocates, cudaStream_t) of a call on `stream`: the
-    allocator hands their memory out again in the order of the stream that uses it."""
+    """(context of a call on `stream`, cudaStream_t).  In the context the tensors' device is the
+    current one, on which the library launches, and the allocator hands the memory of the
+    tensors that the call allocates out again in the order of the stream that uses it."""
     import torch
     if stream is None:
+        context = _NO_CONTEXT if device == torch.cuda.current_device() else torch.cuda.device(device)
         # current_stream(device).cuda_stream without the Stream object
-        return _NO_CONTEXT, torch._C._cuda_getCurrentRawStream(device)
+        return context, torch._C._cuda_getCurrentRawStream(device)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)))
+        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=device)
     return torch.cuda.stream(stream), stream.cuda_stream
 
 
@@ -570,8 +572,8 @@ def muon_grad_norm(grads, norm=None, workspace=None, stream=None):
         _keep, ws, nbytes = _space(workspace, nbytes, device, handle)
         if norm is None:
             norm = torch.empty(1, dtype=torch.float32, device=device)
-    _check(_lib().muon_grad_norm(grads.array, len(grads), _vector(norm, 1, torch.float32, "norm"), ws, nbytes, handle),
-           "muon_grad_norm")
+        _check(_lib().muon_grad_norm(grads.array, len(grads), _vector(norm, 1, torch.float32, "norm"), ws, nbytes,
+                                     handle), "muon_grad_norm")
     return norm
 
 
@@ -592,9 +594,9 @@ def muon_clip_grad_norm(grads, max_norm: float, out=None, eps: float = 1e-6,
         _keep, ws, nbytes = _space(workspace, nbytes, device, handle)
         if result is None:
             result = torch.empty(2, dtype=torch.float32, device=device)
-    _check(_lib().muon_clip_grad_norm(grads.array, len(grads), max_norm, eps, nonfinite,
-                                      _vector(result, 2, torch.float32, "result"), ws, nbytes, handle),
-           "muon_clip_grad_norm")
+        _check(_lib().muon_clip_grad_norm(grads.array, len(grads), max_norm, eps, nonfinite,
+                                          _vector(result, 2, torch.float32, "result"), ws, nbytes, handle),
+               "muon_clip_grad_norm")
     return result
 
 
@@ -645,11 +647,11 @@ def muon_token_logprobs(logits, targets, mask=None, temperature: float = 1.0, lo
     batch, tokens, _, _ = _token_batch(logits, targets, mask, temperature)
     device = logits.get_device()
     context, handle = _on_stream(stream, device)
-    if logp is None:
-        with context:
+    with context:
+        if logp is None:
             logp = torch.empty(tokens, dtype=torch.float32, device=device)
-    _check(_lib().muon_token_logprobs(byref(batch), _vector(logp, tokens, torch.float32, "logp"), handle),
-           "muon_token_logprobs")
+        _check(_lib().muon_token_logprobs(byref(batch), _vector(logp, tokens, torch.float32, "logp"), handle),
+               "muon_token_logprobs")
     return logp
 
 
@@ -701,11 +703,11 @@ def muon_policy_loss(logits, targets, old_logp, advantages, mask=None, ref_logp=
         if logp is None:
             logp = torch.empty(tokens, dtype=f32, device=device)
         grad, grad_ptr, grad_stride = _grad_rows(logits, grad, with_grad, tokens, vocab, stride)
-    _check(_lib().muon_policy_loss(
-        byref(batch), byref(config) if config is not None else None, _vector(old_logp, tokens, f32, "old_logp"),
-        None if ref_logp is None else _vector(ref_logp, tokens, f32, "ref_logp"),
-        _vector(advantages, tokens, f32, "advantages"), offsets, n_seqs, _vector(stats, 4, f32, "stats"),
-        _vector(logp, tokens, f32, "logp"), grad_ptr, grad_stride, ws, nbytes, handle), "muon_policy_loss")
+        _check(_lib().muon_policy_loss(
+            byref(batch), byref(config) if config is not None else None, _vector(old_logp, tokens, f32, "old_logp"),
+            None if ref_logp is None else _vector(ref_logp, tokens, f32, "ref_logp"),
+            _vector(advantages, tokens, f32, "advantages"), offsets, n_seqs, _vector(stats, 4, f32, "stats"),
+            _vector(logp, tokens, f32, "logp"), grad_ptr, grad_stride, ws, nbytes, handle), "muon_policy_loss")
     return stats, logp, grad
 
 
@@ -736,9 +738,9 @@ def muon_preference_loss(logits, targets, seq_offsets, ref_logp, mask=None, temp
         if seq_logp is None:
             seq_logp = torch.empty(n_seqs, dtype=f32, device=device)
         grad, grad_ptr, grad_stride = _grad_rows(logits, grad, with_grad, tokens, vocab, stride)
-    _check(_lib().muon_preference_loss(
-        byref(batch), byref(config) if config is not None else None, _vector(ref_logp, n_seqs, f32, "ref_logp"),
-        _vector(seq_offsets, n_seqs + 1, torch.int64, "seq_offsets"), n_seqs // 2, _vector(loss, 1, f32, "loss"),
-        _vector(margins, n_seqs // 2, f32, "margins"), _vector(seq_logp, n_seqs, f32, "seq_logp"), grad_ptr,
-        grad_stride, ws, nbytes, handle), "muon_preference_loss")
+        _check(_lib().muon_preference_loss(
+            byref(batch), byref(config) if config is not None else None, _vector(ref_logp, n_seqs, f32, "ref_logp"),
+            _vector(seq_offsets, n_seqs + 1, torch.int64, "seq_offsets"), n_seqs // 2, _vector(loss, 1, f32, "loss"),
+            _vector(margins, n_seqs // 2, f32, "margins"), _vector(seq_logp, n_seqs, f32, "seq_logp"), grad_ptr,
+            grad_stride, ws, nbytes, handle), "muon_preference_loss")
     return loss, margins, seq_logp, grad

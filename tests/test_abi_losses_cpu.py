@@ -173,3 +173,112 @@ def test_overlapping_or_scattered_gradients_are_refused(nsm, make):
     torch = pytest.importorskip("torch")
     with pytest.raises(ValueError):
         nsm._blocks(make(torch))
+
+
+class _TwoDevices:
+    """Two devices of a GPU machine, on the CPU: tensors carry the index that they would have,
+    and library calls note the device that was current."""
+
+    def __init__(self, nsm, torch, patch):
+        self.torch, self.current, self.calls, self.made, self.index = torch, 0, [], [], {}
+        owner, empty, strided = self, torch.empty, torch.empty_strided
+
+        def home(make):
+            def made(*size, device=None, **kw):
+                owner.made.append(owner.current if device is None else int(getattr(device, "index", device)))
+                return owner.put(make(*size, **kw), owner.made[-1])
+            return made
+
+        class device:
+            def __init__(self, index):
+                self.index = index
+
+            def __enter__(self):
+                self.before, owner.current = owner.current, self.index
+
+            def __exit__(self, *_):
+                owner.current = self.before
+
+        class Stream:
+            def __init__(self, index):
+                self.cuda_stream, self.device_index, self.device = 0x77, index, type("D", (), {"index": index})
+
+        class library:
+            def __getattr__(self, name):
+                if name.endswith("_bytes"):
+                    return lambda *a: 0
+                return lambda *a: owner.calls.append((name, owner.current)) or 0
+
+        patch.setattr(nsm, "_lib", lambda: library())
+        patch.setattr(nsm, "_SPACES", type("S", (), {})())
+        patch.setattr(torch.Tensor, "get_device", lambda t: owner.of(t), raising=False)
+        patch.setattr(torch.Tensor, "is_cuda", property(lambda t: owner.of(t) >= 0), raising=False)
+        patch.setattr(torch.Tensor, "device", property(lambda t: type("D", (), {"index": owner.of(t)})), raising=False)
+        patch.setattr(torch, "empty", home(empty))
+        patch.setattr(torch, "empty_strided", home(strided))
+        patch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 0, raising=False)
+        patch.setattr(torch.cuda, "current_device", lambda: owner.current)
+        patch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+        patch.setattr(torch.cuda, "device", device)
+        patch.setattr(torch.cuda, "Stream", Stream)
+        patch.setattr(torch.cuda, "ExternalStream", lambda ptr, device=None: Stream(owner.current if device is None else device))
+        patch.setattr(torch.cuda, "stream", lambda s: device(s.device_index))
+        self.stream, self.keep = Stream, []
+
+    def put(self, t, device):
+        self.index[t.untyped_storage().data_ptr()] = device
+        self.keep.append(t)
+        return t
+
+    def of(self, t):
+        return self.index.get(t.untyped_storage().data_ptr(), -1)   # a view's is its base's
+
+    def batch(self, device, tokens=4, vocab=10):
+        t = self.torch
+        return (self.put(t.zeros(tokens, vocab), device), self.put(t.zeros(tokens, dtype=t.int64), device),
+                self.put(t.zeros(tokens), device), self.put(t.tensor([0, 2, 4]), device), self.put(t.zeros(2), device))
+
+
+def _calls(nsm, fake, device):
+    """name -> (call, the tensors it takes by name), all on `device`"""
+    t, put = fake.torch, fake.put
+    z, y, f, off, two = fake.batch(device)
+    mask, grad = put(t.ones(4, dtype=t.bool), device), put(t.zeros(4, 10), device)
+    ws = put(t.zeros(1 << 16, dtype=t.uint8), device)
+    one, four = put(t.zeros(1), device), put(t.zeros(4), device)
+    return {
+        "logprobs": (lambda **kw: nsm.muon_token_logprobs(**{**dict(logits=z, targets=y, mask=mask, logp=f), **kw}),
+                     dict(targets=y, mask=mask, logp=f)),
+        "policy": (lambda **kw: nsm.muon_policy_loss(**{**dict(
+            logits=z, targets=y, old_logp=f, advantages=f, mask=mask, ref_logp=f, seq_offsets=off, grad=grad, logp=f,
+            stats=four, workspace=ws), **kw}),
+            dict(targets=y, old_logp=f, advantages=f, mask=mask, ref_logp=f, seq_offsets=off, grad=grad, logp=f,
+                 stats=four, workspace=ws)),
+        "preference": (lambda **kw: nsm.muon_preference_loss(**{**dict(
+            logits=z, targets=y, seq_offsets=off, ref_logp=two, mask=mask, grad=grad, loss=one, margins=one,
+            seq_logp=two, workspace=ws), **kw}),
+            dict(targets=y, seq_offsets=off, ref_logp=two, mask=mask, grad=grad, loss=one, margins=one, seq_logp=two,
+                 workspace=ws)),
+        "norm": (lambda **kw: nsm.muon_grad_norm(**{**dict(grads=[z], norm=one, workspace=ws), **kw}),
+                 dict(norm=one, workspace=ws)),
+        "clip": (lambda **kw: nsm.muon_clip_grad_norm(**{**dict(grads=[z], max_norm=1.0, result=two, workspace=ws), **kw}),
+                 dict(result=two, workspace=ws)),
+    }
+
+
+CALLS = ["logprobs", "policy", "preference", "norm", "clip"]
+
+
+@pytest.mark.parametrize("which", CALLS)
+@pytest.mark.parametrize("stream", [None, "object", "handle"])
+@pytest.mark.parametrize("device", [0, 1])
+def test_calls_launch_on_their_tensors_device(nsm, monkeypatch, which, stream, device):
+    """What a call allocates and launches belongs to the tensors' device, whichever is current."""
+    fake = _TwoDevices(nsm, pytest.importorskip("torch"), monkeypatch)
+    call, named = _calls(nsm, fake, device)[which]
+    with_stream = {} if stream is None else dict(stream=fake.stream(device) if stream == "object" else 0x77)
+    call(**with_stream)
+    call(**with_stream, **{k: None for k in named if k in ("logp", "stats", "grad", "loss", "margins", "seq_logp",
+                                                           "norm", "result", "workspace")})
+    assert [d for _, d in fake.calls] == [device] * len(fake.calls) and fake.calls
+    assert fake.made and set(fake.made) == {device} and fake.current == 0
