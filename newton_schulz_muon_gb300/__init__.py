@@ -413,6 +413,8 @@ def _on_stream(stream, device: int):
         return context, torch._C._cuda_getCurrentRawStream(device)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=device)
+    elif stream.device.index != device:
+        raise ValueError(f"stream: expected one of cuda:{device}, got one of {stream.device}")
     return torch.cuda.stream(stream), stream.cuda_stream
 
 
@@ -528,10 +530,10 @@ def muon_clip_workspace_bytes(grads) -> int:
     return v.value
 
 
-def _vector(t, n, dtype, what):
-    """Device pointer of a contiguous CUDA tensor of n elements of `dtype`."""
-    if t.dtype is not dtype or t.numel() != n or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{what}: expected a contiguous CUDA tensor of {n} {dtype} values, got shape "
+def _vector(t, n, dtype, what, device):
+    """Device pointer of a contiguous tensor of n elements of `dtype` on CUDA device `device`."""
+    if t.dtype is not dtype or t.numel() != n or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous tensor of {n} {dtype} values on cuda:{device}, got shape "
                          f"{tuple(t.shape)}, strides {t.stride()}, {t.dtype} on {t.device}")
     return t.data_ptr()
 
@@ -545,8 +547,8 @@ def _space(workspace, nbytes, device: int, handle: int):
     may run beside them, gets one of its own from the capture's memory."""
     import torch
     if workspace is not None:
-        if not workspace.is_cuda or not workspace.is_contiguous():
-            raise ValueError("workspace: expected a contiguous CUDA tensor")
+        if workspace.get_device() != device or not workspace.is_contiguous():
+            raise ValueError(f"workspace: expected a contiguous tensor on cuda:{device}, got {workspace.device}")
         return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
     if torch.cuda.is_current_stream_capturing():
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
@@ -572,8 +574,8 @@ def muon_grad_norm(grads, norm=None, workspace=None, stream=None):
         _keep, ws, nbytes = _space(workspace, nbytes, device, handle)
         if norm is None:
             norm = torch.empty(1, dtype=torch.float32, device=device)
-        _check(_lib().muon_grad_norm(grads.array, len(grads), _vector(norm, 1, torch.float32, "norm"), ws, nbytes,
-                                     handle), "muon_grad_norm")
+        _check(_lib().muon_grad_norm(grads.array, len(grads), _vector(norm, 1, torch.float32, "norm", device), ws,
+                                     nbytes, handle), "muon_grad_norm")
     return norm
 
 
@@ -595,13 +597,13 @@ def muon_clip_grad_norm(grads, max_norm: float, out=None, eps: float = 1e-6,
         if result is None:
             result = torch.empty(2, dtype=torch.float32, device=device)
         _check(_lib().muon_clip_grad_norm(grads.array, len(grads), max_norm, eps, nonfinite,
-                                          _vector(result, 2, torch.float32, "result"), ws, nbytes, handle),
+                                          _vector(result, 2, torch.float32, "result", device), ws, nbytes, handle),
                "muon_clip_grad_norm")
     return result
 
 
 def _rows(t, what):
-    """Row stride of a matrix whose rows are contiguous and do not overlap."""
+    """(rows, columns, row stride) of a matrix whose rows are contiguous and do not overlap."""
     if t.dim() != 2 or not t.is_cuda:
         raise ValueError(f"{what}: expected a CUDA matrix [tokens, vocab], got shape {tuple(t.shape)} on {t.device}")
     tokens, vocab = t.shape
@@ -612,16 +614,17 @@ def _rows(t, what):
 
 
 def _token_batch(logits, targets, mask, temperature):
-    """(muon_token_batch, tokens, vocab, row stride)"""
+    """(muon_token_batch, tokens, vocab, row stride, device)"""
     import torch
     tokens, vocab, stride = _rows(logits, "logits")
+    device = logits.get_device()
     masked = None
     if mask is not None:
         if mask.dtype is not torch.bool and mask.dtype is not torch.uint8:
             raise ValueError(f"mask: expected bool or uint8, got {mask.dtype}")
-        masked = _vector(mask, tokens, mask.dtype, "mask")
-    return muon_token_batch(logits.data_ptr(), _vector(targets, tokens, torch.int64, "targets"), masked, tokens, vocab,
-                            stride, temperature, _dtype_code(logits.dtype)), tokens, vocab, stride
+        masked = _vector(mask, tokens, mask.dtype, "mask", device)
+    return muon_token_batch(logits.data_ptr(), _vector(targets, tokens, torch.int64, "targets", device), masked, tokens,
+                            vocab, stride, temperature, _dtype_code(logits.dtype)), tokens, vocab, stride, device
 
 
 def _grad_rows(logits, grad, with_grad, tokens, vocab, stride):
@@ -635,8 +638,9 @@ def _grad_rows(logits, grad, with_grad, tokens, vocab, stride):
             stride = vocab
         grad = torch.empty_strided((tokens, vocab), (stride, 1), dtype=logits.dtype, device=logits.device)
         return grad, grad.data_ptr(), stride
-    if grad.shape != logits.shape or grad.dtype is not logits.dtype:
-        raise ValueError(f"grad: expected a tensor like the logits, got shape {tuple(grad.shape)}, {grad.dtype}")
+    if grad.shape != logits.shape or grad.dtype is not logits.dtype or grad.get_device() != logits.get_device():
+        raise ValueError(f"grad: expected a tensor like the logits, got shape {tuple(grad.shape)}, {grad.dtype} "
+                         f"on {grad.device}")
     return grad, grad.data_ptr(), _rows(grad, "grad")[2]
 
 
@@ -644,13 +648,12 @@ def muon_token_logprobs(logits, targets, mask=None, temperature: float = 1.0, lo
     """log softmax(logits / temperature) at each position's target, fp32; 0 where the mask
     is False.  logits: [tokens, vocab], targets: [tokens] int64, mask: [tokens] bool."""
     import torch
-    batch, tokens, _, _ = _token_batch(logits, targets, mask, temperature)
-    device = logits.get_device()
+    batch, tokens, _, _, device = _token_batch(logits, targets, mask, temperature)
     context, handle = _on_stream(stream, device)
     with context:
         if logp is None:
             logp = torch.empty(tokens, dtype=torch.float32, device=device)
-        _check(_lib().muon_token_logprobs(byref(batch), _vector(logp, tokens, torch.float32, "logp"), handle),
+        _check(_lib().muon_token_logprobs(byref(batch), _vector(logp, tokens, torch.float32, "logp", device), handle),
                "muon_token_logprobs")
     return logp
 
@@ -689,12 +692,11 @@ def muon_policy_loss(logits, targets, old_logp, advantages, mask=None, ref_logp=
     [n_seqs + 1] int64, for the sequence mean.  grad may be the logits themselves."""
     import torch
     f32 = torch.float32
-    batch, tokens, vocab, stride = _token_batch(logits, targets, mask, temperature)
-    device = logits.get_device()
+    batch, tokens, vocab, stride, device = _token_batch(logits, targets, mask, temperature)
     n_seqs, offsets = 0, None
     if seq_offsets is not None:
         n_seqs = max(seq_offsets.numel() - 1, 0)
-        offsets = _vector(seq_offsets, n_seqs + 1, torch.int64, "seq_offsets")
+        offsets = _vector(seq_offsets, n_seqs + 1, torch.int64, "seq_offsets", device)
     context, handle = _on_stream(stream, device)
     with context:
         _keep, ws, nbytes = _space(workspace, muon_loss_workspace_bytes(tokens, n_seqs), device, handle)
@@ -704,10 +706,12 @@ def muon_policy_loss(logits, targets, old_logp, advantages, mask=None, ref_logp=
             logp = torch.empty(tokens, dtype=f32, device=device)
         grad, grad_ptr, grad_stride = _grad_rows(logits, grad, with_grad, tokens, vocab, stride)
         _check(_lib().muon_policy_loss(
-            byref(batch), byref(config) if config is not None else None, _vector(old_logp, tokens, f32, "old_logp"),
-            None if ref_logp is None else _vector(ref_logp, tokens, f32, "ref_logp"),
-            _vector(advantages, tokens, f32, "advantages"), offsets, n_seqs, _vector(stats, 4, f32, "stats"),
-            _vector(logp, tokens, f32, "logp"), grad_ptr, grad_stride, ws, nbytes, handle), "muon_policy_loss")
+            byref(batch), byref(config) if config is not None else None,
+            _vector(old_logp, tokens, f32, "old_logp", device),
+            None if ref_logp is None else _vector(ref_logp, tokens, f32, "ref_logp", device),
+            _vector(advantages, tokens, f32, "advantages", device), offsets, n_seqs,
+            _vector(stats, 4, f32, "stats", device), _vector(logp, tokens, f32, "logp", device), grad_ptr, grad_stride,
+            ws, nbytes, handle), "muon_policy_loss")
     return stats, logp, grad
 
 
@@ -720,8 +724,7 @@ def muon_preference_loss(logits, targets, seq_offsets, ref_logp, mask=None, temp
     [2 P] fp32, the reference policy's sums.  Returns (loss, margins, seq_logp, grad)."""
     import torch
     f32 = torch.float32
-    batch, tokens, vocab, stride = _token_batch(logits, targets, mask, temperature)
-    device = logits.get_device()
+    batch, tokens, vocab, stride, device = _token_batch(logits, targets, mask, temperature)
     n_seqs = seq_offsets.numel() - 1
     if n_seqs < 0 or n_seqs % 2:
         raise ValueError(f"seq_offsets: expected 2 P + 1 offsets, got {seq_offsets.numel()}")
@@ -739,8 +742,10 @@ def muon_preference_loss(logits, targets, seq_offsets, ref_logp, mask=None, temp
             seq_logp = torch.empty(n_seqs, dtype=f32, device=device)
         grad, grad_ptr, grad_stride = _grad_rows(logits, grad, with_grad, tokens, vocab, stride)
         _check(_lib().muon_preference_loss(
-            byref(batch), byref(config) if config is not None else None, _vector(ref_logp, n_seqs, f32, "ref_logp"),
-            _vector(seq_offsets, n_seqs + 1, torch.int64, "seq_offsets"), n_seqs // 2, _vector(loss, 1, f32, "loss"),
-            _vector(margins, n_seqs // 2, f32, "margins"), _vector(seq_logp, n_seqs, f32, "seq_logp"), grad_ptr,
-            grad_stride, ws, nbytes, handle), "muon_preference_loss")
+            byref(batch), byref(config) if config is not None else None,
+            _vector(ref_logp, n_seqs, f32, "ref_logp", device),
+            _vector(seq_offsets, n_seqs + 1, torch.int64, "seq_offsets", device), n_seqs // 2,
+            _vector(loss, 1, f32, "loss", device), _vector(margins, n_seqs // 2, f32, "margins", device),
+            _vector(seq_logp, n_seqs, f32, "seq_logp", device), grad_ptr, grad_stride, ws, nbytes, handle),
+            "muon_preference_loss")
     return loss, margins, seq_logp, grad

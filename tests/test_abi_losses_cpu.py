@@ -282,3 +282,16 @@ def test_calls_launch_on_their_tensors_device(nsm, monkeypatch, which, stream, d
                                                            "norm", "result", "workspace")})
     assert [d for _, d in fake.calls] == [device] * len(fake.calls) and fake.calls
     assert fake.made and set(fake.made) == {device} and fake.current == 0
+
+
+@pytest.mark.parametrize("which", CALLS)
+def test_tensors_of_another_device_are_refused(nsm, monkeypatch, which):
+    fake = _TwoDevices(nsm, pytest.importorskip("torch"), monkeypatch)
+    call, named = _calls(nsm, fake, 0)[which]
+    for name, t in named.items():
+        elsewhere = fake.put(t.clone(), 1)
+        with pytest.raises(ValueError, match=name):
+            call(**{name: elsewhere})
+    with pytest.raises(ValueError, match="stream"):
+        call(stream=fake.stream(1))
+    assert fake.calls == []
