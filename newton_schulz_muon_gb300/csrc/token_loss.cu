@@ -508,8 +508,10 @@ struct Terms {
 };
 
 // The CTA's sums into the partials; the last of `n` CTAs to come adds all of them, in
-// their order (a warp a sum; a CTA may have fewer warps than there are sums).
+// their order: kEach sums a warp, side by side (4 / kEach warps at least).
+template <int kEach>
 __device__ __forceinline__ void finish_stats(const RowArgs& a, StatsShared& sh, int64_t part, int64_t n) {
+  constexpr int kWarps = 4 / kEach;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -519,14 +521,19 @@ __device__ __forceinline__ void finish_stats(const RowArgs& a, StatsShared& sh, 
     sh.last = atomicAdd(a.ticket, 1u) == (unsigned)n - 1;
   }
   __syncthreads();
-  if (!sh.last) return;
-  __threadfence();
-  for (int j = warp; j < 4; j += blockDim.x >> 5) {
-    double sum = 0.0;
-    for (int64_t k = lane; k < n; k += 32) sum += __ldcg(a.partials + 4 * k + j);
+  if (sh.last && warp < kWarps) {
+    __threadfence();
+    double sum[kEach] = {};
+    for (int64_t k = lane; k < n; k += 32) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    if (lane == 0) a.stats[j] = (float)sum;
+      for (int j = 0; j < kEach; ++j) sum[j] += __ldcg(a.partials + 4 * k + warp + kWarps * j);
+    }
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum[j] += __shfl_xor_sync(0xFFFFFFFFu, sum[j], o);
+      if (lane == 0) a.stats[warp + kWarps * j] = (float)sum[j];
+    }
   }
 }
 
@@ -870,7 +877,7 @@ __global__ void __launch_bounds__(kMaxRowThreads + 32) row_kernel(const __grid_c
   if (kMode == kForward && blockIdx.x == 0 && tid == 0) *a.ticket = 0;
   if (kMode == kPolicy && rank == 0) {
     if (finisher && lane == 0) acc.get(sh.stats.sum);
-    finish_stats(a, sh.stats, cid, n_clusters);
+    finish_stats<1>(a, sh.stats, cid, n_clusters);
   }
   cluster_sync();  // no CTA of the cluster ends before the others have all it sent
 }
@@ -1019,7 +1026,7 @@ __global__ void __launch_bounds__(kWarpRowThreads, kUnits > 4 ? 2 : 3) warp_row_
       for (int k = 1; k < kWarpRowWarps; ++k) sum += part[k][threadIdx.x];
       stats.sum[threadIdx.x] = sum;
     }
-    finish_stats(a, stats, blockIdx.x, gridDim.x);
+    finish_stats<1>(a, stats, blockIdx.x, gridDim.x);
   }
 }
 
@@ -1117,7 +1124,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) stream_kernel(const __grid_con
   if (kMode == kPolicy) {
     __shared__ StatsShared stats;
     if (warp == warps - 1 && lane == 0) acc.get(stats.sum);
-    finish_stats(a, stats, blockIdx.x, gridDim.x);
+    finish_stats<2>(a, stats, blockIdx.x, gridDim.x);  // a CTA may have two warps
   }
 }
 
