@@ -430,7 +430,7 @@ muon_status muon_grad_norm(const muon_grad* grads, int64_t n, float* norm, void*
                            size_t workspace_bytes, void* stream);
 
 /* Clipping by the global norm: c = min(1, max_norm / (N + eps)), out = c g, each
- * element rounded once.  result (device, 2 fp32): N and c.  c is decided on the
+ * product rounded to fp32 and then to out's type.  result (device, 2 fp32): N and c.  c is decided on the
  * device; in place with c = 1 nothing is written.  max_norm >= 0 (inf: never
  * clips), eps >= 0; a sum N + eps of zero gives c = 1.
  * nonfinite: MUON_NONFINITE_*. */

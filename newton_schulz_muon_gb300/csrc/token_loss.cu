@@ -308,7 +308,8 @@ struct Prob {
 
 // ex2.approx is low by 4.9e-8 in the mean over [-16, 0), measured against 64 bits (its
 // terms of exactly 1 are not): a sequence's sum of log-probabilities adds that up, so the
-// sum makes up for it.
+// sum makes up for it.  Where many logits equal the largest, whose terms are exactly 1, the
+// correction is the error: 4.9e-8 in log S, under half a unit of any |logp| >= 1.
 constexpr float kExpLow = 4.9e-8f;
 
 __device__ __forceinline__ Prob row_prob(const RowArgs& a, const Sum& t, float zy) {
@@ -1547,7 +1548,9 @@ size_t row_smem(int64_t units, int cluster, int stages) {
   return (size_t)stages * (size_t)((units + cluster - 1) / cluster) * 16 + sizeof(RowShared) + sums;
 }
 
-// Threads that hold units, of all CTAs that an SM has room for; 0: a CTA does not fit.
+// Threads that hold units, of all CTAs that an SM has room for; 0: a CTA does not fit.  80 and
+// 64 registers are those of the bf16 forms in the units that they are given out in (74 and 56
+// used); fp32 rows use 56 with three rows too and may fit more often than this says.
 int resident_threads(int64_t units, int cluster, int stages) {
   const size_t smem = row_smem(units, cluster, stages);
   if (smem > kSmemPerSm) return 0;
@@ -1660,7 +1663,8 @@ cudaError_t launch_rows_as(RowArgs a, int32_t dtype, int sms, bool dependent, cu
     return launch(kernel, (int)(ctas < most ? ctas : most), kWarpRowThreads, 0, s, 1, dependent, a);
   }
   if (shape.cluster == 0) {
-    // without partial sums to keep, a CTA for each row balances masked ones by itself
+    // without partial sums to keep, a CTA for each row balances masked ones by itself; the policy
+    // loss has room for those of kMaxParts CTAs, which take rows in turn
     const int64_t most = kMode == kPolicy ? kMaxParts : rows;
     return launch(stream_kernel<T, kMode>, (int)(rows < most ? rows : most), shape.threads, 0, s, 1, dependent, a);
   }
@@ -1805,7 +1809,9 @@ muon_status muon_policy_loss(const muon_token_batch* batch, const muon_policy_co
   cudaError_t e;
   // Clusters that take several rows each get as many masked ones each; with few rows, or a
   // warp a row, the list would only be waited for (4096 x 131072, a fifth masked at random:
-  // 0.365 ms without it, 0.352 ms with it; 20011 x 4099: 0.075 and 0.086 ms).
+  // 0.365 ms without it, 0.352 ms with it; 20011 x 4099: 0.075 and 0.086 ms).  Few rows: fewer
+  // CTAs than four an SM.  That counts no CTAs that share an SM, so where several do (50001
+  // fp32 logits: four) a list is made from one row a cluster on, and waited for.
   const RowShape shape = row_shape(batch->vocab, batch->dtype, batch->tokens, sms, grad != nullptr);
   int32_t* order = batch->mask && shape.cluster > 0 && batch->tokens * shape.cluster >= 4ll * sms ? ws.order : nullptr;
   if (by_seq)
