@@ -458,6 +458,47 @@ typedef struct {
  * taken. */
 muon_status muon_token_logprobs(const muon_token_batch* batch, float* logp, void* stream);
 
+/* A token for each row of logits, drawn with a given uniform number: p = softmax(logits /
+ * temperature), the first token j with sum_{i <= j} p_i > uniforms[t] sum_i p_i.
+ *   batch: its targets are not read.
+ *   uniforms: [tokens] fp32 in [0, 1) (below, or NaN: as 0; above: the last token that can
+ *     be taken).
+ *   tokens: [tokens]; logp: [tokens] fp32, log p of the token (device).
+ * A row whose mask is 0 gets token -1 and logp 0 and its logits are not read; one without
+ * probabilities (a logit of NaN or +inf, or none but -inf) token -1 and logp NaN.  Sums and
+ * the search for the token are in 64 bits over terms of fp32. */
+muon_status muon_sample_tokens(const muon_token_batch* batch, const float* uniforms, int64_t* tokens,
+                               float* logp, void* stream);
+
+/* Verifies drafted tokens against the target's probabilities, so that what is emitted is
+ * distributed as if sampled from the target.  Sequence s holds the drafts draft_offsets[s]
+ * .. draft_offsets[s + 1], n of them (0: its token is sampled), and n + 1 rows of the target
+ * from row draft_offsets[s] + s on: row i holds the logits at draft i, row n those after the
+ * last one.  p = softmax(target / temperature) and q = softmax(draft / its temperature) at row i:
+ *   draft x is taken while accept_uniforms[i] q(x) < p(x);
+ *   the token after the a taken ones is drawn with sample_uniforms[s], as in
+ *   muon_sample_tokens, from max(p - q, 0) at row a where a < n (from p where that is zero
+ *   throughout), else from p at row n.
+ *   target: [n_drafts + n_seqs][vocab]; its targets are not read.
+ *   draft: [n_drafts][vocab], of the target's vocab and dtype; its targets are the drafts.
+ *     One outside [0, vocab) is not taken.  logits NULL: drafts that were certain, q = 1 there
+ *     and 0 elsewhere.  Neither batch takes a mask.
+ *   draft_logp: [n_drafts] fp32, log q(x) as sampling the drafts gave it; NULL: from the
+ *     draft model's logits, which are then read for every draft up to the first refused one.
+ *   draft_offsets: [n_seqs + 1] device, ascending from 0 to n_drafts.
+ *   accept_uniforms: [n_drafts], sample_uniforms: [n_seqs], fp32 in [0, 1).
+ *   tokens: [n_drafts + n_seqs], laid out as the target's rows: the taken drafts, the drawn
+ *     token, then -1.
+ *   counts: [n_seqs], how many drafts were taken.
+ *   logp: [n_drafts + n_seqs] fp32, log p of the tokens, 0 where they are -1 (the old_logp
+ *     of muon_policy_loss, whose mask is tokens >= 0).
+ * Rows without probabilities refuse their draft, and the token drawn there is -1, its logp
+ * NaN.  No workspace. */
+muon_status muon_verify_drafts(const muon_token_batch* target, const muon_token_batch* draft,
+                               const float* draft_logp, const int64_t* draft_offsets, int64_t n_seqs,
+                               const float* accept_uniforms, const float* sample_uniforms,
+                               int64_t* tokens, int64_t* counts, float* logp, void* stream);
+
 /* Workspace of muon_policy_loss and muon_preference_loss (bytes).  Host work. */
 muon_status muon_loss_workspace_bytes(int64_t tokens, int64_t n_seqs, size_t* bytes);
 

@@ -146,6 +146,9 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
         "muon_grad_norm": (c_int32, [P, c_int64, P, P, c_size_t, P]),
         "muon_clip_grad_norm": (c_int32, [P, c_int64, c_float, c_float, c_int32, P, P, c_size_t, P]),
         "muon_token_logprobs": (c_int32, [POINTER(muon_token_batch), P, P]),
+        "muon_sample_tokens": (c_int32, [POINTER(muon_token_batch), P, P, P, P]),
+        "muon_verify_drafts": (c_int32, [POINTER(muon_token_batch), POINTER(muon_token_batch), P, P, c_int64, P, P,
+                                         P, P, P, P]),
         "muon_loss_workspace_bytes": (c_int32, [c_int64, c_int64, POINTER(c_size_t)]),
         "muon_policy_config_default": (None, [POINTER(muon_policy_config)]),
         "muon_policy_loss": (c_int32, [POINTER(muon_token_batch), POINTER(muon_policy_config), P, P, P, P, c_int64,
@@ -613,6 +616,13 @@ def _rows(t, what):
     return tokens, vocab, stride if tokens > 1 else vocab
 
 
+def _mask_type(mask):
+    import torch
+    if mask.dtype is not torch.bool and mask.dtype is not torch.uint8:
+        raise ValueError(f"mask: expected bool or uint8, got {mask.dtype}")
+    return mask.dtype
+
+
 def _token_batch(logits, targets, mask, temperature):
     """(muon_token_batch, tokens, vocab, row stride, device)"""
     import torch
@@ -620,11 +630,20 @@ def _token_batch(logits, targets, mask, temperature):
     device = logits.get_device()
     masked = None
     if mask is not None:
-        if mask.dtype is not torch.bool and mask.dtype is not torch.uint8:
-            raise ValueError(f"mask: expected bool or uint8, got {mask.dtype}")
-        masked = _vector(mask, tokens, mask.dtype, "mask", device)
+        masked = _vector(mask, tokens, _mask_type(mask), "mask", device)
     return muon_token_batch(logits.data_ptr(), _vector(targets, tokens, torch.int64, "targets", device), masked, tokens,
                             vocab, stride, temperature, _dtype_code(logits.dtype)), tokens, vocab, stride, device
+
+
+def _row_batch(logits, mask, temperature, what="logits"):
+    """(muon_token_batch without targets, rows, device)"""
+    rows, vocab, stride = _rows(logits, what)
+    device = logits.get_device()
+    masked = None
+    if mask is not None:
+        masked = _vector(mask, rows, _mask_type(mask), "mask", device)
+    return muon_token_batch(logits.data_ptr(), None, masked, rows, vocab, stride, temperature,
+                            _dtype_code(logits.dtype)), rows, device
 
 
 def _grad_rows(logits, grad, with_grad, tokens, vocab, stride):
@@ -656,6 +675,73 @@ def muon_token_logprobs(logits, targets, mask=None, temperature: float = 1.0, lo
         _check(_lib().muon_token_logprobs(byref(batch), _vector(logp, tokens, torch.float32, "logp", device), handle),
                "muon_token_logprobs")
     return logp
+
+
+def muon_sample_tokens(logits, uniforms, mask=None, temperature: float = 1.0, tokens=None, logp=None, stream=None):
+    """A token for each row of logits [rows, vocab], drawn from softmax(logits / temperature)
+    with a given uniform number: the first whose cumulated probability exceeds it.  uniforms:
+    [rows] fp32 in [0, 1), mask: [rows] bool.  Returns (tokens int64, their log-probabilities
+    fp32); -1 and 0 where the mask is False, -1 and NaN in a row without probabilities."""
+    import torch
+    batch, rows, device = _row_batch(logits, mask, temperature)
+    context, handle = _on_stream(stream, device)
+    with context:
+        if tokens is None:
+            tokens = torch.empty(rows, dtype=torch.int64, device=device)
+        if logp is None:
+            logp = torch.empty(rows, dtype=torch.float32, device=device)
+        _check(_lib().muon_sample_tokens(byref(batch), _vector(uniforms, rows, torch.float32, "uniforms", device),
+                                         _vector(tokens, rows, torch.int64, "tokens", device),
+                                         _vector(logp, rows, torch.float32, "logp", device), handle),
+               "muon_sample_tokens")
+    return tokens, logp
+
+
+def muon_verify_drafts(logits, drafts, draft_offsets, accept_uniforms, sample_uniforms, draft_logits=None,
+                       draft_logp=None, temperature: float = 1.0, draft_temperature: Optional[float] = None,
+                       tokens=None, counts=None, logp=None, stream=None):
+    """Verifies the drafted tokens of several sequences against the target's probabilities.
+
+    logits: [N + S, vocab], for each sequence a row for each of its drafts and one after them;
+    drafts: [N] int64; draft_offsets: [S + 1] int64, ascending from 0 to N; accept_uniforms
+    [N] and sample_uniforms [S]: fp32 in [0, 1).  draft_logits: [N, vocab], what the drafts
+    were sampled from (None: they were certain), and draft_logp: [N] fp32, their
+    log-probabilities under it where they are known.  draft_temperature: by default the
+    target's.  Returns (tokens [N + S]: taken drafts, one drawn token, then -1; counts [S] of
+    the drafts taken; logp [N + S] of the tokens under the target)."""
+    import torch
+    f32, i64 = torch.float32, torch.int64
+    target, rows, device = _row_batch(logits, None, temperature)
+    n_seqs = draft_offsets.numel() - 1
+    if n_seqs < 0:
+        raise ValueError("draft_offsets: expected S + 1 offsets, got none")
+    n = rows - n_seqs
+    if draft_temperature is None:
+        draft_temperature = temperature
+    if draft_logits is None:
+        draft = muon_token_batch(None, None, None, n, target.vocab, 0, draft_temperature, target.dtype)
+    else:
+        draft, got, draft_device = _row_batch(draft_logits, None, draft_temperature, "draft_logits")
+        if got != n or draft.vocab != target.vocab or draft.dtype != target.dtype or draft_device != device:
+            raise ValueError(f"draft_logits: expected [{n}, {target.vocab}] {logits.dtype} values on cuda:{device}, got "
+                             f"shape {tuple(draft_logits.shape)}, {draft_logits.dtype} on {draft_logits.device}")
+    draft.targets = _vector(drafts, n, i64, "drafts", device)
+    context, handle = _on_stream(stream, device)
+    with context:
+        if tokens is None:
+            tokens = torch.empty(rows, dtype=i64, device=device)
+        if counts is None:
+            counts = torch.empty(n_seqs, dtype=i64, device=device)
+        if logp is None:
+            logp = torch.empty(rows, dtype=f32, device=device)
+        _check(_lib().muon_verify_drafts(
+            byref(target), byref(draft), None if draft_logp is None else _vector(draft_logp, n, f32, "draft_logp", device),
+            _vector(draft_offsets, n_seqs + 1, i64, "draft_offsets", device), n_seqs,
+            _vector(accept_uniforms, n, f32, "accept_uniforms", device),
+            _vector(sample_uniforms, n_seqs, f32, "sample_uniforms", device), _vector(tokens, rows, i64, "tokens", device),
+            _vector(counts, n_seqs, i64, "counts", device), _vector(logp, rows, f32, "logp", device), handle),
+            "muon_verify_drafts")
+    return tokens, counts, logp
 
 
 def muon_loss_workspace_bytes(tokens: int, n_seqs: int) -> int:

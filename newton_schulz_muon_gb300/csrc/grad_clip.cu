@@ -517,8 +517,6 @@ int grid_for(int32_t n_chunks, int sms) {
   return (int)(ctas < 1 ? 1 : ctas > most ? most : ctas);
 }
 
-int32_t cuda_error(cudaError_t e) { return set_error(MUON_ERR_CUDA, cudaGetErrorString(e)); }
-
 // An upper bound of the launches that a set needs: by the smallest tables.
 int64_t launches_for(const muon_grad* grads, int64_t n) {
   int64_t launches = 0, segs = 0, chunks = 0;

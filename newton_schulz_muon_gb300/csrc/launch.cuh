@@ -1,12 +1,16 @@
-// Host-side helpers of the entry points that take no plan: the device they run on,
-// and launches with a cluster size or with programmatic dependence on the kernel
+// Host-side helpers of the entry points that take no plan: their refusals, the device they
+// run on, and launches with a cluster size or with programmatic dependence on the kernel
 // before them in the stream.
 #pragma once
 
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <cmath>
 #include <utility>
+
+#include "kernels.h"
+#include "muon.h"
 
 namespace muon {
 namespace {
@@ -26,6 +30,32 @@ inline int device_sms(cudaError_t* err) {
   const int found = major == 10 && minor == 3 ? sms : -1;
   if (dev < 64) cached[dev] = found;
   return found > 0 ? found : 0;
+}
+
+inline int32_t invalid(const char* msg) { return set_error(MUON_ERR_INVALID, msg); }
+inline int32_t cuda_error(cudaError_t e) { return set_error(MUON_ERR_CUDA, cudaGetErrorString(e)); }
+
+inline bool aligned(const void* p, size_t a) { return reinterpret_cast<uint64_t>(p) % a == 0; }
+
+inline int32_t check_workspace(const void* ws, size_t bytes, size_t need) {
+  if (!ws || bytes < need) return set_error(MUON_ERR_NO_WORKSPACE, "workspace is NULL or too small");
+  if (!aligned(ws, 16)) return invalid("workspace must be 16-byte aligned");
+  return MUON_OK;
+}
+
+inline int32_t find_device(int* sms) {
+  cudaError_t e;
+  *sms = device_sms(&e);
+  if (e != cudaSuccess) return cuda_error(e);
+  if (*sms == 0) return set_error(MUON_ERR_UNSUPPORTED, "libmuon is built for sm_103a");
+  return MUON_OK;
+}
+
+// v = hi + lo with lo > 0 (v > 0).
+inline void split_down(double v, float* hi, float* lo) {
+  *hi = std::nextafterf((float)v, 0.f);
+  if ((double)*hi >= v) *hi = std::nextafterf(*hi, 0.f);
+  *lo = (float)(v - (double)*hi);
 }
 
 // dependent = true: the kernel may start while the kernel before it in the stream

@@ -1,0 +1,722 @@
+// Tokens sampled from logits, and drafted tokens verified against the target's
+// probabilities, from given uniform numbers.
+//
+//   p = softmax(target logits / temperature), q the draft model's probabilities likewise
+//   a draft x is taken while u q(x) < p(x);
+//   the token after the a taken ones comes from max(p - q, 0) at row a where a draft was
+//   refused there, else from p: the first token whose cumulated weight exceeds
+//   u' (the sum of all weights).
+//
+// A row is cut into strips of consecutive 16-byte units, one warp a strip, and each strip's
+// sum of exponentials is kept (in the frame of its own largest logit).  The sums give the
+// row's normaliser, and by them the strip that holds the sampled token is found: only that
+// strip is read again, so that a row is read once.  A refused draft's row is read twice,
+// since the difference of the probabilities needs both rows' normalisers first.
+//
+// Sums over a strip are fp32 (1024 bf16 or 512 fp32 logits, 32 or 16 a lane and then the
+// lanes'), sums over strips and the search for the token are in 64 bits: a token's share of
+// [0, 1) begins within a few 1e-8 of where it should.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <cmath>
+
+#include "device.cuh"
+#include "kernels.h"
+#include "launch.cuh"
+#include "muon.h"
+#include "rows.cuh"
+
+namespace muon {
+namespace {
+
+constexpr int kLoads = 4;                  // 16-byte units a lane takes at a time
+constexpr int kStripStep = 32 * kLoads;    // units that a warp takes at a time
+constexpr int kMaxRound = 8;               // rows of a sequence in one round
+constexpr int kMaxTable = 512;             // strips of a CTA and round, of each kind
+constexpr int kMaxCluster = 8;
+constexpr int kMaxSampleThreads = 1024;
+
+// Logits are divided by the temperature: exponents in base 2 are c = c_hi + c_lo times
+// theirs, c_lo > 0 (so that -inf stays -inf).
+struct Scale {
+  float c_hi, c_lo, inv_hi, inv_lo;
+};
+
+struct SampleArgs {
+  const void* target;
+  const void* draft;         // null: drafts that were certain
+  const uint8_t* mask;       // rows of a sampling call that take part; or null
+  const int64_t* drafts;
+  const float* draft_logp;   // or null
+  const int64_t* offsets;    // [n_seqs + 1]
+  const float* accept_u;
+  const float* sample_u;
+  int64_t* tokens;
+  int64_t* counts;
+  float* logp;
+  int64_t target_stride, draft_stride;
+  int64_t n_drafts;
+  Scale target_scale, draft_scale;
+  int32_t vocab;
+  int32_t cluster;           // CTAs a sequence
+  int32_t strip_units;       // a multiple of kStripStep
+  int32_t strips;            // of a CTA
+  int32_t round;             // rows of a sequence taken side by side
+};
+
+// A sum of exponentials in the frame of m, the largest logit (-inf: none).
+struct StripSum {
+  float m, s;
+};
+struct RowSum {
+  double s;
+  float m;
+};
+
+struct SampleShared {
+  RowSum slice[2][2 * kMaxRound];  // this CTA's part of each row, read by the cluster's other CTAs
+  RowSum total[2][2 * kMaxRound];
+  double weights;                  // this CTA's part of the weights a token is drawn from
+};
+
+__device__ __forceinline__ float factor(const Scale& c, float m, float to) {
+  if (m == to) return 1.f;
+  const float d = m - to;
+  return ex2(__fmaf_rn(d, c.c_hi, d * c.c_lo));
+}
+__device__ __forceinline__ float frame_of(float m) { return m == -INFINITY ? 0.f : m; }
+
+__device__ __forceinline__ double warp_sum64(double v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+__device__ __forceinline__ double warp_scan64(double v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double w = __shfl_up_sync(0xFFFFFFFFu, v, o);
+    if (lane >= o) v += w;
+  }
+  return v;
+}
+
+// A row in 16-byte units: unit u holds the elements u N - shift .. + N - 1, those outside
+// the row being -inf.
+template <typename T>
+struct RowUnits {
+  const T* z;
+  int32_t vocab, shift, units;
+  __device__ __forceinline__ RowUnits(const void* base, int64_t row, int64_t stride, int32_t v)
+      : z(reinterpret_cast<const T*>(base) + row * stride), vocab(v) {
+    shift = (int)(reinterpret_cast<uint64_t>(z) & 15) / (int)sizeof(T);
+    units = (shift + vocab + Vec<T>::N - 1) / Vec<T>::N;
+  }
+  __device__ __forceinline__ int first(int u) const { return u * Vec<T>::N - shift; }
+};
+
+// The 16 bytes of elements e .. e + N - 1 of a row, -inf outside it; one load where they lie
+// in the row and on a 16-byte boundary.
+template <typename T>
+__device__ __forceinline__ uint4 load_elems(const T* z, int32_t vocab, int e) {
+  constexpr int N = Vec<T>::N;
+  const T* p = z + e;
+  if (e >= 0 && e + N <= vocab && (reinterpret_cast<uint64_t>(p) & 15) == 0)
+    return __ldg(reinterpret_cast<const uint4*>(p));
+  float v[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = e + i >= 0 && e + i < vocab ? Vec<T>::load(p + i) : -INFINITY;
+  return Vec<T>::pack(v);
+}
+
+// 2^(c (z - m)) of a unit's elements.
+template <typename T>
+__device__ __forceinline__ void exps(const Scale& c, float m, const uint4& w, float (&e)[Vec<T>::N]) {
+  float v[Vec<T>::N];
+  Vec<T>::unpack(w, v);
+#pragma unroll
+  for (int i = 0; i < Vec<T>::N; i += 2) {
+    const F2 d = add2(make_f2(v[i], v[i + 1]), make_f2(-m, -m));
+    const float2 u = split(fma2(d, make_f2(c.c_hi, c.c_hi), mul2(d, make_f2(c.c_lo, c.c_lo))));
+    e[i] = ex2(u.x);
+    e[i + 1] = ex2(u.y);
+  }
+}
+
+// The sum of exponentials over the units [u0, u1) of a row; the same in every lane.
+template <typename T>
+__device__ __forceinline__ StripSum strip_sum(const RowUnits<T>& row, const Scale& c, int u0, int u1, int lane) {
+  constexpr uint32_t low = Vec<T>::kLowest;
+  StripSum t{-INFINITY, 0.f};
+  for (int u = u0; u < u1; u += kStripStep) {
+    uint4 w[kLoads];
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) {
+      const int at = u + k * 32 + lane;
+      w[k] = at < u1 ? load_elems<T>(row.z, row.vocab, row.first(at)) : make_uint4(low, low, low, low);
+    }
+    const float m = fmaxf(t.m, warp_max(Vec<T>::max(w)));
+    F2 s0 = make_f2(0.f, 0.f), s1 = make_f2(0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) {
+      float e[Vec<T>::N];
+      exps<T>(c, frame_of(m), w[k], e);
+#pragma unroll
+      for (int i = 0; i < Vec<T>::N; i += 4) {
+        s0 = add2(s0, make_f2(e[i], e[i + 1]));
+        s1 = add2(s1, make_f2(e[i + 2], e[i + 3]));
+      }
+    }
+    const float2 r = split(add2(s0, s1));
+    t.s = t.s * factor(c, t.m, m) + warp_sum(r.x + r.y);
+    t.m = m;
+  }
+  return t;
+}
+
+// The probabilities of both models at a refused draft.
+struct Refused {
+  float mp, ip, mq, iq;  // frames, and reciprocals of the sums
+};
+
+// max(p - q, 0) of unit u of the target's row.
+template <typename T>
+__device__ __forceinline__ void left_over(const SampleArgs& a, const Refused& f, const RowUnits<T>& p, const T* zq,
+                                          int u, float (&r)[Vec<T>::N]) {
+  float q[Vec<T>::N];
+  exps<T>(a.target_scale, f.mp, load_elems<T>(p.z, p.vocab, p.first(u)), r);
+  exps<T>(a.draft_scale, f.mq, load_elems<T>(zq, p.vocab, p.first(u)), q);
+#pragma unroll
+  for (int i = 0; i < Vec<T>::N; ++i) r[i] = fmaxf(r[i] * f.ip - q[i] * f.iq, 0.f);
+}
+
+// The first element of the units [u0, u1) at which the cumulated weight exceeds t (a token
+// of weight 0 never does), or the last of positive weight, or -1.  weights(u, w): those of
+// unit u.
+template <typename T, typename F>
+__device__ __forceinline__ int pick_element(const RowUnits<T>& row, int u0, int u1, double t, int lane, F weights) {
+  constexpr int N = Vec<T>::N;
+  double before = 0.;
+  int last = -1;
+  for (int u = u0; u < u1; u += 32) {
+    float w[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = 0.f;
+    if (u + lane < u1) weights(u + lane, w);
+    double s = 0.;
+    int positive = -1;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      s += (double)w[i];
+      if (w[i] > 0.f) positive = i;
+    }
+    const double upto = before + warp_scan64(s, lane);
+    const unsigned over = __ballot_sync(0xFFFFFFFFu, positive >= 0 && upto > t);
+    const unsigned any = __ballot_sync(0xFFFFFFFFu, positive >= 0);
+    if (over) {
+      const int l = __ffs(over) - 1;
+      int found = positive;
+      double c = upto;
+#pragma unroll
+      for (int i = N - 1; i >= 0; --i) {  // c: the weights up to element i
+        if (w[i] > 0.f && c > t) found = i;
+        c -= (double)w[i];
+      }
+      return __shfl_sync(0xFFFFFFFFu, row.first(u + lane) + found, l);
+    }
+    if (any) last = __shfl_sync(0xFFFFFFFFu, row.first(u + lane) + positive, 31 - __clz(any));
+    before = __shfl_sync(0xFFFFFFFFu, upto, 31);
+  }
+  return last;
+}
+
+// log p of a token of the strip [u0, u1): the strip is summed again without the token, so
+// that a nearly certain token keeps its digits.  rest: each lane's part of the sum over the
+// other strips, in the row's frame m.
+template <typename T>
+__device__ __forceinline__ float token_logp(const RowUnits<T>& row, const Scale& c, float m, double rest, int u0, int u1,
+                                            int token, int lane) {
+  constexpr int N = Vec<T>::N;
+  for (int u = u0 + lane; u < u1; u += 32) {
+    float e[N];
+    exps<T>(c, m, load_elems<T>(row.z, row.vocab, row.first(u)), e);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (row.first(u) + i != token) rest += (double)e[i];
+  }
+  float s = (float)warp_sum64(rest);
+  const float d = Vec<T>::load(row.z + token) - m;
+  const float x = __fmaf_rn(d, c.inv_hi, d * c.inv_lo);
+  // x <= 0; at the row's largest logit, log1p keeps the digits of a nearly certain token
+  s = __fmaf_rn(x == 0.f ? s : s - 1.f, kExpLow, s);
+  return x == 0.f ? 0.f - log1pf(s) : x - logf(s + expf(x));
+}
+
+__device__ __forceinline__ RowSum load_peer(const RowSum* p, int rank, int own) {
+  if (rank == own) return *p;
+  const uint32_t at = mapa_shared(p, (uint32_t)rank);
+  RowSum r;
+  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(r.s) : "r"(at) : "memory");
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(r.m) : "r"(at + 8) : "memory");
+  return r;
+}
+
+__device__ __forceinline__ bool usable(const RowSum& t) { return t.s > 0. && t.s < (double)INFINITY; }
+
+// A cluster of CTAs a sequence (or, without drafts, a row).  Its rows are taken `round` at a
+// time until a draft is refused.
+template <typename T, bool kDrafts>
+__global__ void __launch_bounds__(kMaxSampleThreads) sample_kernel(const __grid_constant__ SampleArgs a) {
+  constexpr int N = Vec<T>::N;
+  extern __shared__ StripSum tables[];  // [2][target and draft][round][strips]
+  __shared__ SampleShared sh;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int rank = a.cluster > 1 ? (int)cluster_ctarank() : 0;
+  const int64_t seq = blockIdx.x / a.cluster;
+  int64_t lo = 0, n = 0;
+  if (kDrafts) {
+    // offsets out of order or range: nothing outside the arrays is touched
+    lo = min(max(a.offsets[seq], (int64_t)0), a.n_drafts);
+    n = min(max(a.offsets[seq + 1], lo), a.n_drafts) - lo;
+  } else if (a.mask != nullptr && a.mask[seq] == 0) {
+    if (rank == 0 && threadIdx.x == 0) {
+      a.tokens[seq] = -1;
+      a.logp[seq] = 0.f;
+    }
+    return;
+  }
+  const int64_t row0 = lo + seq;  // the sequence's first row
+  const bool both = kDrafts && a.draft != nullptr && a.draft_logp == nullptr;  // rows of both models a round
+  const int set = a.round * a.strips;
+  const int strip0 = rank * a.strips;
+  auto exchange = [&] {
+    if (a.cluster > 1) cluster_sync();
+    else __syncthreads();
+  };
+  auto units_of = [&](const RowUnits<T>& row, int k, int& u0, int& u1) {  // of this CTA's strip k
+    u0 = (int)min((int64_t)(strip0 + k) * a.strip_units, (int64_t)row.units);
+    u1 = min(u0 + a.strip_units, row.units);
+  };
+  // sums a row's slices: warp-wide, the same in every lane
+  auto merge = [&](const RowSum* slice, const Scale& c) {
+    RowSum t{0., -INFINITY};
+    if (lane < a.cluster) t = load_peer(slice, lane, rank);
+    RowSum r;
+    r.m = warp_max(t.m);
+    r.s = warp_sum64(t.s * (double)factor(c, t.m, r.m));
+    return r;
+  };
+  auto slice_sum = [&](const StripSum* table, const Scale& c) {
+    float m = -INFINITY;
+    for (int k = lane; k < a.strips; k += 32) m = fmaxf(m, table[k].m);
+    RowSum r;
+    r.m = warp_max(m);
+    r.s = 0.;
+    for (int k = lane; k < a.strips; k += 32) r.s += (double)table[k].s * (double)factor(c, table[k].m, r.m);
+    r.s = warp_sum64(r.s);
+    return r;
+  };
+  // each lane's part of a row's sum without the strip k0 of this CTA
+  auto other_strips = [&](const StripSum* table, const RowSum* slice, int k0, float m, const Scale& c) {
+    double s = 0.;
+    for (int k = lane; k < a.strips; k += 32)
+      if (k != k0) s += (double)table[k].s * (double)factor(c, table[k].m, m);
+    if (lane < a.cluster && lane != rank) {
+      const RowSum t = load_peer(slice, lane, rank);
+      s += t.s * (double)factor(c, t.m, m);
+    }
+    return s;
+  };
+
+  int parity = 0, at = 0;  // at: the last row's place in its round
+  int64_t base = 0, taken = 0;
+  bool refused = false;
+  StripSum* table = tables;
+  for (;; base += a.round, parity ^= 1) {
+    const int rows = (int)min((int64_t)a.round, n + 1 - base);
+    table = tables + (size_t)parity * 2 * set;
+    // the drafts' scalars are on their way while the rows are read
+    int64_t y = -1;
+    float u = 0.f, zy = -INFINITY, logq = 0.f;
+    const bool draft_lane = kDrafts && lane < rows && base + lane < n;
+    if (draft_lane) {
+      const int64_t d = lo + base + lane;
+      y = a.drafts[d];
+      u = a.accept_u[d];
+      if (y < 0 || y >= a.vocab) y = -1;
+      if (y >= 0) {
+        zy = Vec<T>::load(reinterpret_cast<const T*>(a.target) + (row0 + base + lane) * a.target_stride + y);
+        if (both) logq = Vec<T>::load(reinterpret_cast<const T*>(a.draft) + d * a.draft_stride + y);
+        else if (a.draft_logp != nullptr) logq = a.draft_logp[d];
+      }
+    }
+    const int drafted = both ? (int)min((int64_t)rows, n - base) : 0;
+    for (int job = warp; job < (rows + drafted) * a.strips; job += warps) {
+      const int r = job / a.strips, k = job - r * a.strips;
+      const bool q = r >= rows;
+      const RowUnits<T> row(q ? a.draft : a.target, q ? lo + base + r - rows : row0 + base + r,
+                            q ? a.draft_stride : a.target_stride, a.vocab);
+      int u0, u1;
+      units_of(row, k, u0, u1);
+      const StripSum t = strip_sum<T>(row, q ? a.draft_scale : a.target_scale, u0, u1, lane);
+      if (lane == 0) table[(q ? set + (r - rows) * a.strips : r * a.strips) + k] = t;
+    }
+    __syncthreads();
+    for (int r = warp; r < rows + drafted; r += warps) {
+      const bool q = r >= rows;
+      const RowSum t = slice_sum(table + (q ? set + (r - rows) * a.strips : r * a.strips),
+                                 q ? a.draft_scale : a.target_scale);
+      if (lane == 0) sh.slice[parity][q ? kMaxRound + r - rows : r] = t;
+    }
+    exchange();
+    for (int r = warp; r < rows + drafted; r += warps) {
+      const bool q = r >= rows;
+      const int slot = q ? kMaxRound + r - rows : r;
+      const RowSum t = merge(&sh.slice[parity][slot], q ? a.draft_scale : a.target_scale);
+      if (lane == 0) sh.total[parity][slot] = t;
+    }
+    __syncthreads();
+    at = rows - 1;
+    if (!kDrafts) break;
+    // every warp of every CTA decides alike
+    bool ok = true;
+    if (draft_lane) {
+      const RowSum p = sh.total[parity][lane];
+      const Scale& c = a.target_scale;
+      const float d = zy - p.m;
+      const float logp = __fmaf_rn(d, c.inv_hi, d * c.inv_lo) - logf((float)p.s);
+      bool fine = usable(p) && y >= 0;
+      if (both) {
+        const RowSum q = sh.total[parity][kMaxRound + lane];
+        const float e = logq - q.m;
+        logq = __fmaf_rn(e, a.draft_scale.inv_hi, e * a.draft_scale.inv_lo) - logf((float)q.s);
+        fine = fine && usable(q);
+      }
+      ok = fine && u < expf(logp - logq);
+    }
+    const unsigned bad = __ballot_sync(0xFFFFFFFFu, !ok);
+    refused = bad != 0;
+    if (refused) at = __ffs(bad) - 1;
+    // rows of this round whose drafts were taken
+    const int good = (int)min(refused ? (int64_t)at : (int64_t)rows, n - base);
+    for (int r = 0; r < good; ++r) {
+      const int64_t t = __shfl_sync(0xFFFFFFFFu, y, r);
+      if ((base + r) % warps != warp) continue;
+      const RowUnits<T> row(a.target, row0 + base + r, a.target_stride, a.vocab);
+      const int k = ((int)t + row.shift) / N / a.strip_units - strip0;
+      if (k < 0 || k >= a.strips) continue;  // another CTA's strip
+      int u0, u1;
+      units_of(row, k, u0, u1);
+      const float m = sh.total[parity][r].m;
+      const double rest = other_strips(table + r * a.strips, &sh.slice[parity][r], k, m, a.target_scale);
+      const float lp = token_logp<T>(row, a.target_scale, m, rest, u0, u1, (int)t, lane);
+      if (lane == 0) {
+        a.tokens[row0 + base + r] = t;
+        a.logp[row0 + base + r] = lp;
+      }
+    }
+    taken = base + good;
+    if (refused || base + rows == n + 1) break;
+  }
+
+  // the token after the drafts that were taken, from row `taken`
+  const RowUnits<T> row(a.target, row0 + taken, a.target_stride, a.vocab);
+  const RowSum p = sh.total[parity][at];
+  const StripSum* own = table + at * a.strips;
+  const Scale& c = a.target_scale;
+  bool fine = usable(p);
+  // weights of the strips: kPlain p in its frame; kWithout p without the refused draft;
+  // kLeft max(p - q, 0)
+  enum { kPlain, kWithout, kLeft };
+  int kind = kPlain;
+  int64_t without = -1;
+  Refused f{};
+  const T* zq = nullptr;
+  StripSum* left = table + set + at * a.strips;  // of the draft model's row, then of the difference
+  int without_strip = -1;
+  float without_sum = 0.f;
+  if (kDrafts && refused && fine) {
+    const int64_t d = lo + taken;
+    if (a.draft == nullptr) {
+      kind = kWithout;
+      without = a.drafts[d];
+      if (without >= 0 && without < a.vocab) {
+        const int k = ((int)without + row.shift) / N / a.strip_units - strip0;
+        if (k >= 0 && k < a.strips) {  // every warp sums the strip alike
+          int u0, u1;
+          units_of(row, k, u0, u1);
+          double s = 0.;
+          for (int u = u0 + lane; u < u1; u += 32) {
+            float e[N];
+            exps<T>(c, p.m, load_elems<T>(row.z, row.vocab, row.first(u)), e);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+              if (row.first(u) + i != without) s += (double)e[i];
+          }
+          without_strip = k;
+          without_sum = (float)warp_sum64(s);
+        }
+      }
+    } else {
+      kind = kLeft;
+      const RowUnits<T> draft(a.draft, d, a.draft_stride, a.vocab);
+      zq = draft.z;
+      RowSum q;
+      if (both) {
+        q = sh.total[parity][kMaxRound + at];
+      } else {
+        for (int k = warp; k < a.strips; k += warps) {
+          int u0, u1;
+          units_of(draft, k, u0, u1);
+          const StripSum t = strip_sum<T>(draft, a.draft_scale, u0, u1, lane);
+          if (lane == 0) left[k] = t;
+        }
+        __syncthreads();
+        if (warp == 0) {
+          const RowSum t = slice_sum(left, a.draft_scale);
+          if (lane == 0) sh.slice[parity][kMaxRound] = t;
+        }
+        exchange();
+        q = merge(&sh.slice[parity][kMaxRound], a.draft_scale);
+      }
+      fine = usable(q);
+      f = Refused{p.m, (float)(1. / p.s), q.m, (float)(1. / q.s)};
+      if (fine) {
+        for (int k = warp; k < a.strips; k += warps) {
+          int u0, u1;
+          units_of(row, k, u0, u1);
+          float s = 0.f;
+          for (int u = u0 + lane; u < u1; u += 32) {
+            float r[N];
+            left_over<T>(a, f, row, zq, u, r);
+#pragma unroll
+            for (int i = 0; i < N; ++i) s += r[i];
+          }
+          s = warp_sum(s);
+          if (lane == 0) left[k] = StripSum{0.f, s};
+        }
+        __syncthreads();
+      }
+    }
+  }
+
+  int64_t token = -1;
+  bool mine = rank == 0;  // this CTA writes the token
+  float lp = NAN;
+  if (fine) {
+    auto weight = [&](int k) {
+      if (kind == kLeft) return (double)left[k].s;
+      if (kind == kWithout && k == without_strip) return (double)without_sum;
+      return (double)own[k].s * (double)factor(c, own[k].m, p.m);
+    };
+    double v = 0., upto = 0., sum = 0.;
+    for (;;) {
+      // each CTA's share of the weights, and their running sum
+      double slice = 0.;
+      for (int k = lane; k < a.strips; k += 32) slice += weight(k);
+      slice = warp_sum64(slice);
+      if (a.cluster > 1) {
+        if (threadIdx.x == 0) sh.weights = slice;
+        cluster_sync();
+        v = 0.;
+        if (lane < a.cluster) {
+          if (lane == rank) v = slice;
+          else asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(mapa_shared(&sh.weights, (uint32_t)lane)) : "memory");
+        }
+        cluster_sync();  // sh.weights is free
+      } else {
+        v = lane == 0 ? slice : 0.;
+      }
+      upto = warp_scan64(v, lane);
+      sum = __shfl_sync(0xFFFFFFFFu, upto, 31);
+      if (sum > 0. || kind == kPlain) break;
+      kind = kPlain;  // the two models agree: the refusal was one of rounding
+    }
+    const float su = fmaxf(a.sample_u[seq], 0.f);
+    const double t = su < 1.f ? (double)su * sum : (double)INFINITY;  // 1 and above: the last token
+    const unsigned over = __ballot_sync(0xFFFFFFFFu, v > 0. && upto > t);
+    const unsigned any = __ballot_sync(0xFFFFFFFFu, v > 0.);
+    const int owner = over ? __ffs(over) - 1 : 31 - __clz(any);
+    mine = rank == owner;
+    if (mine && warp == 0) {
+      double before = __shfl_sync(0xFFFFFFFFu, upto - v, owner);
+      int strip = -1;
+      for (int k0 = 0; k0 < a.strips; k0 += 32) {
+        const double w = k0 + lane < a.strips ? weight(k0 + lane) : 0.;
+        const double end = before + warp_scan64(w, lane);
+        const unsigned above = __ballot_sync(0xFFFFFFFFu, w > 0. && end > t);
+        const unsigned some = __ballot_sync(0xFFFFFFFFu, w > 0.);
+        if (above) {
+          const int l = __ffs(above) - 1;
+          strip = k0 + l;
+          before = __shfl_sync(0xFFFFFFFFu, end - w, l);
+          break;
+        }
+        if (some) strip = k0 + 31 - __clz(some);
+        before = __shfl_sync(0xFFFFFFFFu, end, 31);
+      }
+      int u0, u1;
+      units_of(row, strip, u0, u1);
+      token = pick_element<T>(row, u0, u1, t - before, lane, [&](int u, float(&w)[N]) {
+        if (kind == kLeft) {
+          left_over<T>(a, f, row, zq, u, w);
+          return;
+        }
+        exps<T>(c, p.m, load_elems<T>(row.z, row.vocab, row.first(u)), w);
+        if (kind == kWithout) {
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            if (row.first(u) + i == without) w[i] = 0.f;
+        }
+      });
+      if (token >= 0)
+        lp = token_logp<T>(row, c, p.m, other_strips(own, &sh.slice[parity][at], strip, p.m, c), u0, u1, (int)token, lane);
+    }
+  }
+  if (mine && threadIdx.x == 0) {
+    a.tokens[row0 + taken] = token;
+    a.logp[row0 + taken] = lp;
+  }
+  if (kDrafts && rank == 0) {
+    if (threadIdx.x == 0) a.counts[seq] = taken;
+    for (int64_t r = taken + 1 + threadIdx.x; r <= n; r += blockDim.x) {
+      a.tokens[row0 + r] = -1;
+      a.logp[row0 + r] = 0.f;
+    }
+  }
+  if (a.cluster > 1) cluster_sync();  // no CTA leaves while another may read its sums
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+Scale scale_of(double temperature) {
+  Scale c;
+  split_down(1.4426950408889634 / temperature, &c.c_hi, &c.c_lo);
+  split_down(1.0 / temperature, &c.inv_hi, &c.inv_lo);
+  return c;
+}
+
+int32_t check_rows(const muon_token_batch* b) {
+  if (b->tokens < 0 || b->tokens > (1ll << 31) - 1) return invalid("tokens must be in [0, 2^31)");
+  if (b->vocab < 1 || b->vocab > (1ll << 30)) return invalid("vocab must be in [1, 2^30]");
+  if (b->row_stride != 0 && (b->row_stride < b->vocab || b->row_stride > (1ll << 40)))
+    return invalid("row_stride must be 0 or at least vocab");
+  if (b->dtype != MUON_DTYPE_F32 && b->dtype != MUON_DTYPE_BF16) return invalid("unknown logits dtype");
+  if (!(b->temperature >= 1e-20 && b->temperature <= 1e20)) return invalid("temperature must be in [1e-20, 1e20]");
+  if (!aligned(b->logits, b->dtype == MUON_DTYPE_BF16 ? 2 : 4)) return invalid("logits are not aligned to their type");
+  return MUON_OK;
+}
+
+// The launch's shape: CTAs a sequence, rows a round, strips and threads.
+int shape_of(SampleArgs& a, int64_t n_seqs, int64_t rows, int32_t dtype, int sms, size_t* smem) {
+  const int64_t per = dtype == MUON_DTYPE_BF16 ? 8 : 4;
+  const int64_t units = (2 * (per - 1) + a.vocab) / per;
+  const int64_t steps = (units + kStripStep - 1) / kStripStep;  // strips if there is room for them
+  int64_t cluster = 1;
+  while (cluster < kMaxCluster && n_seqs * cluster * 2 <= 4 * sms && steps > 2 * cluster) cluster *= 2;
+  const int64_t most = (rows + n_seqs - 1) / n_seqs;  // rows of a sequence, in the mean
+  a.cluster = (int32_t)cluster;
+  a.round = n_seqs * cluster <= sms ? (int32_t)(most < kMaxRound ? most : kMaxRound) : 1;
+  const int64_t table = kMaxTable / a.round;
+  const int64_t mult = (steps + cluster * table - 1) / (cluster * table);
+  a.strip_units = (int32_t)(mult * kStripStep);
+  const int64_t strips = (steps + mult - 1) / mult;
+  a.strips = (int32_t)((strips + cluster - 1) / cluster);
+  *smem = (size_t)4 * a.round * a.strips * sizeof(StripSum);
+  const int64_t jobs = (int64_t)a.round * a.strips;
+  const int64_t most_warps = n_seqs * cluster <= sms ? 32 : 8;
+  return (int)(32 * (jobs < most_warps ? jobs : most_warps));
+}
+
+template <typename T>
+cudaError_t launch_sample(const SampleArgs& a, bool drafts, int64_t n_seqs, int threads, size_t smem, cudaStream_t s) {
+  return launch(drafts ? sample_kernel<T, true> : sample_kernel<T, false>, (int)(n_seqs * a.cluster), threads, smem, s,
+                a.cluster, false, a);
+}
+
+int32_t run_sample(SampleArgs& a, bool drafts, int64_t n_seqs, int64_t rows, int32_t dtype, void* stream) {
+  int sms;
+  const int32_t st = find_device(&sms);
+  if (st != MUON_OK) return st;
+  size_t smem;
+  const int threads = shape_of(a, n_seqs, rows, dtype, sms, &smem);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = dtype == MUON_DTYPE_BF16 ? launch_sample<__nv_bfloat16>(a, drafts, n_seqs, threads, smem, s)
+                                                 : launch_sample<float>(a, drafts, n_seqs, threads, smem, s);
+  return e == cudaSuccess ? MUON_OK : cuda_error(e);
+}
+
+}  // namespace
+}  // namespace muon
+
+using namespace muon;
+
+extern "C" {
+
+muon_status muon_sample_tokens(const muon_token_batch* batch, const float* uniforms, int64_t* tokens, float* logp,
+                               void* stream) {
+  if (!batch) return invalid("batch is NULL");
+  const int32_t st = check_rows(batch);
+  if (st != MUON_OK) return st;
+  if (batch->tokens == 0) return MUON_OK;
+  if (!batch->logits) return invalid("logits is NULL");
+  if (!uniforms || !tokens || !logp) return invalid("uniforms, tokens or logp is NULL");
+  if (!aligned(uniforms, 4) || !aligned(tokens, 8) || !aligned(logp, 4))
+    return invalid("uniforms, tokens or logp is not aligned to its type");
+  SampleArgs a = {};
+  a.target = batch->logits;
+  a.target_stride = batch->row_stride ? batch->row_stride : batch->vocab;
+  a.mask = batch->mask;
+  a.sample_u = uniforms;
+  a.tokens = tokens;
+  a.logp = logp;
+  a.target_scale = a.draft_scale = scale_of(batch->temperature);
+  a.vocab = (int32_t)batch->vocab;
+  return run_sample(a, false, batch->tokens, batch->tokens, batch->dtype, stream);
+}
+
+muon_status muon_verify_drafts(const muon_token_batch* target, const muon_token_batch* draft, const float* draft_logp,
+                               const int64_t* draft_offsets, int64_t n_seqs, const float* accept_uniforms,
+                               const float* sample_uniforms, int64_t* tokens, int64_t* counts, float* logp,
+                               void* stream) {
+  if (!target || !draft) return invalid("target or draft is NULL");
+  int32_t st = check_rows(target);
+  if (st == MUON_OK) st = check_rows(draft);
+  if (st != MUON_OK) return st;
+  if (n_seqs < 0 || n_seqs > (1ll << 31) - 1) return invalid("n_seqs must be in [0, 2^31)");
+  if (target->tokens != draft->tokens + n_seqs)
+    return invalid("the target has a row for each draft and one more for each sequence");
+  if (draft->vocab != target->vocab || draft->dtype != target->dtype)
+    return invalid("target and draft must have one vocabulary and one dtype");
+  if (target->mask || draft->mask) return invalid("target and draft take no mask");
+  if (draft_logp && !draft->logits) return invalid("draft_logp without the draft model's logits");
+  if (n_seqs == 0) return MUON_OK;
+  if (!target->logits || !draft_offsets || !sample_uniforms || !tokens || !counts || !logp)
+    return invalid("logits, draft_offsets, sample_uniforms, tokens, counts or logp is NULL");
+  if (draft->tokens > 0 && (!draft->targets || !accept_uniforms)) return invalid("drafts or accept_uniforms is NULL");
+  if (!aligned(draft->targets, 8) || !aligned(draft_offsets, 8) || !aligned(tokens, 8) || !aligned(counts, 8) ||
+      !aligned(draft_logp, 4) || !aligned(accept_uniforms, 4) || !aligned(sample_uniforms, 4) || !aligned(logp, 4))
+    return invalid("an array is not aligned to its type");
+  SampleArgs a = {};
+  a.target = target->logits;
+  a.target_stride = target->row_stride ? target->row_stride : target->vocab;
+  a.draft = draft->logits;
+  a.draft_stride = draft->row_stride ? draft->row_stride : draft->vocab;
+  a.drafts = draft->targets;
+  a.draft_logp = draft_logp;
+  a.offsets = draft_offsets;
+  a.accept_u = accept_uniforms;
+  a.sample_u = sample_uniforms;
+  a.tokens = tokens;
+  a.counts = counts;
+  a.logp = logp;
+  a.n_drafts = draft->tokens;
+  a.target_scale = scale_of(target->temperature);
+  a.draft_scale = scale_of(draft->temperature);
+  a.vocab = (int32_t)target->vocab;
+  return run_sample(a, true, n_seqs, target->tokens, target->dtype, stream);
+}
+
+}  // extern "C"
