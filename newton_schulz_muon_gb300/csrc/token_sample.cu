@@ -180,7 +180,7 @@ struct Refused {
   float mp, ip, mq, iq;  // frames, and reciprocals of the sums
 };
 
-// max(p - q, 0) of unit u of the target's row.
+// max(p - q, 0) of unit u of the target's row; each product rounded, so that equal rows leave 0.
 template <typename T>
 __device__ __forceinline__ void left_over(const SampleArgs& a, const Refused& f, const RowUnits<T>& p, const T* zq,
                                           int u, float (&r)[Vec<T>::N]) {
@@ -188,7 +188,7 @@ __device__ __forceinline__ void left_over(const SampleArgs& a, const Refused& f,
   exps<T>(a.target_scale, f.mp, load_elems<T>(p.z, p.vocab, p.first(u)), r);
   exps<T>(a.draft_scale, f.mq, load_elems<T>(zq, p.vocab, p.first(u)), q);
 #pragma unroll
-  for (int i = 0; i < Vec<T>::N; ++i) r[i] = fmaxf(r[i] * f.ip - q[i] * f.iq, 0.f);
+  for (int i = 0; i < Vec<T>::N; ++i) r[i] = fmaxf(__fmul_rn(r[i], f.ip) - __fmul_rn(q[i], f.iq), 0.f);
 }
 
 // The first element of the units [u0, u1) at which the cumulated weight exceeds t (a token
