@@ -574,6 +574,50 @@ muon_status muon_preference_loss(const muon_token_batch* batch, const muon_prefe
                                  int64_t grad_stride, void* workspace, size_t workspace_bytes,
                                  void* stream);
 
+/* An activation matrix x [rows][cols] kept in 8 bits from the forward pass to the backward
+ * pass.  data: rows * P signed bytes q, P = cols rounded up to a multiple of 32, the rows P
+ * bytes apart, then rows * P / 32 bytes b, one for each block of 32 consecutive columns of a
+ * row (16-byte aligned; padding columns hold 0).  A value stands for q 2^(b - 133), and 2^(b -
+ * 133) is the smallest power of two, 2^-126 at least, for which the block's largest magnitude
+ * rounds to 127 steps or fewer: a value is off by at most half a step, which is 2^-7 of the
+ * block's largest magnitude or less.  Rounding is to even; magnitudes above 127.5 2^121 are cut
+ * to 127 2^121.  b = 255: the block held an infinity or a NaN, and reads back as NaN.  Every value
+ * is a bf16 number. */
+typedef struct {
+  void* data;
+  int64_t rows;  /* 0 .. 2^31 - 1 */
+  int64_t cols;  /* 1 .. 2^30 */
+} muon_checkpoint;
+
+/* Size of a checkpoint's data.  Host work. */
+muon_status muon_checkpoint_bytes(int64_t rows, int64_t cols, size_t* bytes);
+
+/* checkpoint <- x; x: dtype (MUON_DTYPE_*), rows x_stride elements apart (0 means cols). */
+muon_status muon_checkpoint_save(const void* x, int64_t x_stride, int32_t dtype,
+                                 const muon_checkpoint* checkpoint, void* stream);
+
+/* x <- the checkpoint's values (exact in either dtype). */
+muon_status muon_checkpoint_load(const muon_checkpoint* checkpoint, void* x, int64_t x_stride,
+                                 int32_t dtype, void* stream);
+
+/* A gated activation and the checkpoints of its inputs, in one pass over them:
+ *   h = gate s up, s = 1 / (1 + exp(-gate)).
+ * gate, up and h have the checkpoints' shape and one dtype, each its own row stride (0 means
+ * cols); gate and up may be the two halves of one matrix, and h may be gate or up (same stride). */
+muon_status muon_swiglu_forward(const void* gate, int64_t gate_stride, const void* up, int64_t up_stride,
+                                int32_t dtype, void* h, int64_t h_stride,
+                                const muon_checkpoint* gate_checkpoint,
+                                const muon_checkpoint* up_checkpoint, void* stream);
+
+/* Its backward pass from the checkpoints:
+ *   dgate = dh up s (1 + gate (1 - s)),  dup = dh gate s,
+ * and, where h is not NULL, h = gate s up again (for the weight gradient of the product that
+ * took h).  The outputs are three matrices, one of which may be dh (same stride). */
+muon_status muon_swiglu_backward(const void* dh, int64_t dh_stride, int32_t dtype,
+                                 const muon_checkpoint* gate_checkpoint,
+                                 const muon_checkpoint* up_checkpoint, void* dgate, int64_t dgate_stride,
+                                 void* dup, int64_t dup_stride, void* h, int64_t h_stride, void* stream);
+
 /* Text of the last error reported by an entry point on the calling thread
  * (empty string if none).  Valid until that thread's next call. */
 const char* muon_last_error(void);

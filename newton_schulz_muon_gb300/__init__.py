@@ -109,6 +109,10 @@ class muon_preference_config(ctypes.Structure):
                 ("length_normalize", c_int32), ("reserved", c_int32 * 4)]
 
 
+class muon_checkpoint(ctypes.Structure):
+    _fields_ = [("data", c_void_p), ("rows", c_int64), ("cols", c_int64)]
+
+
 def _load(path: str = LIB_PATH) -> ctypes.CDLL:
     if not os.path.exists(path):
         raise ImportError(f"{os.path.basename(path)} not found at {path}; run __graft_entry__.build() "
@@ -149,6 +153,13 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
         "muon_sample_tokens": (c_int32, [POINTER(muon_token_batch), P, P, P, P]),
         "muon_verify_drafts": (c_int32, [POINTER(muon_token_batch), POINTER(muon_token_batch), P, P, c_int64, P, P,
                                          P, P, P, P]),
+        "muon_checkpoint_bytes": (c_int32, [c_int64, c_int64, POINTER(c_size_t)]),
+        "muon_checkpoint_save": (c_int32, [P, c_int64, c_int32, POINTER(muon_checkpoint), P]),
+        "muon_checkpoint_load": (c_int32, [POINTER(muon_checkpoint), P, c_int64, c_int32, P]),
+        "muon_swiglu_forward": (c_int32, [P, c_int64, P, c_int64, c_int32, P, c_int64, POINTER(muon_checkpoint),
+                                          POINTER(muon_checkpoint), P]),
+        "muon_swiglu_backward": (c_int32, [P, c_int64, c_int32, POINTER(muon_checkpoint), POINTER(muon_checkpoint), P,
+                                           c_int64, P, c_int64, P, c_int64, P]),
         "muon_loss_workspace_bytes": (c_int32, [c_int64, c_int64, POINTER(c_size_t)]),
         "muon_policy_config_default": (None, [POINTER(muon_policy_config)]),
         "muon_policy_loss": (c_int32, [POINTER(muon_token_batch), POINTER(muon_policy_config), P, P, P, P, c_int64,
@@ -835,3 +846,130 @@ def muon_preference_loss(logits, targets, seq_offsets, ref_logp, mask=None, temp
             _vector(seq_logp, n_seqs, f32, "seq_logp", device), grad_ptr, grad_stride, ws, nbytes, handle),
             "muon_preference_loss")
     return loss, margins, seq_logp, grad
+
+
+# ---------------------------------------------------------------------------
+# activation checkpoints in 8 bits
+# ---------------------------------------------------------------------------
+def muon_checkpoint_bytes(rows: int, cols: int) -> int:
+    v = c_size_t()
+    _check(_lib().muon_checkpoint_bytes(int(rows), int(cols), byref(v)), "muon_checkpoint_bytes")
+    return v.value
+
+
+class Checkpoint:
+    """An activation matrix [rows, cols] in 8 bits (include/muon.h, muon_checkpoint).  data: a
+    contiguous CUDA uint8 tensor of muon_checkpoint_bytes bytes that starts on a 16-byte
+    boundary; by default a new one on `device` (the current one)."""
+
+    def __init__(self, rows: int, cols: int, data=None, device=None):
+        import torch
+        nbytes = muon_checkpoint_bytes(rows, cols)
+        if data is None:
+            data = torch.empty(nbytes, dtype=torch.uint8, device="cuda" if device is None else device)
+        if data.dtype is not torch.uint8 or data.numel() != nbytes or not data.is_cuda or not data.is_contiguous():
+            raise ValueError(f"data: expected a contiguous CUDA tensor of {nbytes} uint8 values, got shape "
+                             f"{tuple(data.shape)}, strides {data.stride()}, {data.dtype} on {data.device}")
+        self.rows, self.cols, self.data, self.device = rows, cols, data, data.get_device()
+        self.struct = muon_checkpoint(data.data_ptr(), rows, cols)
+
+    @property
+    def shape(self):
+        return self.rows, self.cols
+
+
+def _saved(checkpoint, rows, cols, device, what="checkpoint"):
+    """A given checkpoint of this shape and device, or a new one."""
+    if checkpoint is None:
+        return Checkpoint(rows, cols, device=device)
+    if checkpoint.shape != (rows, cols) or checkpoint.device != device:
+        raise ValueError(f"{what}: expected one of [{rows}, {cols}] on cuda:{device}, got one of "
+                         f"{list(checkpoint.shape)} on cuda:{checkpoint.device}")
+    return checkpoint
+
+
+def _matrix(t, rows, cols, dtype, device, what):
+    """(pointer, row stride) of a matrix whose rows are contiguous and do not overlap."""
+    if t.dtype is not dtype or t.shape != (rows, cols) or t.get_device() != device:
+        raise ValueError(f"{what}: expected [{rows}, {cols}] {dtype} values on cuda:{device}, got shape {tuple(t.shape)}, "
+                         f"{t.dtype} on {t.device}")
+    stride, inner = t.stride()
+    if (cols > 1 and inner != 1) or (rows > 1 and stride < cols):
+        raise ValueError(f"{what}: rows must be contiguous and not overlap, got strides {t.stride()}")
+    return t.data_ptr(), stride if rows > 1 else cols
+
+
+def muon_checkpoint_save(x, checkpoint=None, stream=None):
+    """Keeps x [rows, cols] (bf16 or fp32) in 8 bits: int8 values and one power of two for each
+    block of 32 columns of a row.  Returns the Checkpoint."""
+    rows, cols, stride = _rows(x, "x")
+    device, dtype = x.get_device(), _dtype_code(x.dtype)
+    context, handle = _on_stream(stream, device)
+    with context:
+        checkpoint = _saved(checkpoint, rows, cols, device)
+        _check(_lib().muon_checkpoint_save(x.data_ptr(), stride, dtype, byref(checkpoint.struct), handle),
+               "muon_checkpoint_save")
+    return checkpoint
+
+
+def muon_checkpoint_load(checkpoint, out=None, dtype=None, stream=None):
+    """The values of a checkpoint, in `out` or a new matrix of `dtype` (bf16 by default, which
+    holds them exactly)."""
+    import torch
+    rows, cols = checkpoint.shape
+    device = checkpoint.device
+    context, handle = _on_stream(stream, device)
+    with context:
+        if out is None:
+            out = torch.empty(rows, cols, dtype=dtype or torch.bfloat16, device=device)
+        elif dtype is not None and out.dtype is not dtype:
+            raise ValueError(f"out: expected {dtype}, got {out.dtype}")
+        code = _dtype_code(out.dtype)
+        _check(_lib().muon_checkpoint_load(byref(checkpoint.struct), *_matrix(out, rows, cols, out.dtype, device, "out"),
+                                           code, handle), "muon_checkpoint_load")
+    return out
+
+
+def muon_swiglu_forward(gate, up, h=None, gate_checkpoint=None, up_checkpoint=None, stream=None):
+    """h = gate sigmoid(gate) up, and the 8-bit checkpoints of gate and up [rows, cols] (which
+    may be halves of one matrix).  Returns (h, gate's Checkpoint, up's Checkpoint)."""
+    import torch
+    rows, cols, stride = _rows(gate, "gate")
+    device, dtype = gate.get_device(), gate.dtype
+    code = _dtype_code(dtype)
+    context, handle = _on_stream(stream, device)
+    with context:
+        if h is None:
+            h = torch.empty(rows, cols, dtype=dtype, device=device)
+        gate_checkpoint = _saved(gate_checkpoint, rows, cols, device, "gate_checkpoint")
+        up_checkpoint = _saved(up_checkpoint, rows, cols, device, "up_checkpoint")
+        _check(_lib().muon_swiglu_forward(gate.data_ptr(), stride, *_matrix(up, rows, cols, dtype, device, "up"), code,
+                                          *_matrix(h, rows, cols, dtype, device, "h"), byref(gate_checkpoint.struct),
+                                          byref(up_checkpoint.struct), handle), "muon_swiglu_forward")
+    return h, gate_checkpoint, up_checkpoint
+
+
+def muon_swiglu_backward(dh, gate_checkpoint, up_checkpoint, dgate=None, dup=None, h=None, with_h: bool = False,
+                         stream=None):
+    """The gradients of muon_swiglu_forward's inputs from h's [rows, cols] and the
+    checkpoints.  Returns (dgate, dup, h): h is computed again with with_h=True (or a given
+    h), else None.  One of the outputs may be dh itself."""
+    import torch
+    rows, cols, stride = _rows(dh, "dh")
+    device, dtype = dh.get_device(), dh.dtype
+    code = _dtype_code(dtype)
+    _saved(gate_checkpoint, rows, cols, device, "gate_checkpoint")
+    _saved(up_checkpoint, rows, cols, device, "up_checkpoint")
+    context, handle = _on_stream(stream, device)
+    with context:
+        if dgate is None:
+            dgate = torch.empty(rows, cols, dtype=dtype, device=device)
+        if dup is None:
+            dup = torch.empty(rows, cols, dtype=dtype, device=device)
+        if h is None and with_h:
+            h = torch.empty(rows, cols, dtype=dtype, device=device)
+        _check(_lib().muon_swiglu_backward(
+            dh.data_ptr(), stride, code, byref(gate_checkpoint.struct), byref(up_checkpoint.struct),
+            *_matrix(dgate, rows, cols, dtype, device, "dgate"), *_matrix(dup, rows, cols, dtype, device, "dup"),
+            *((None, 0) if h is None else _matrix(h, rows, cols, dtype, device, "h")), handle), "muon_swiglu_backward")
+    return dgate, dup, h

@@ -25,7 +25,7 @@ LIBMUON_DEBUG = os.path.join(PKG, "libmuon_debug.so")
 LIBSYNTH = os.path.join(ROOT, "synth", "libmuonsynth.so")
 
 MUON_SOURCES = ["runtime.cu", "elementwise.cu", "ns_gemm.cu", "ns_small.cu", "ns_gram.cu", "noalloc.cu",
-                "schedule.cu", "grad_clip.cu", "token_loss.cu", "token_sample.cu"]
+                "schedule.cu", "grad_clip.cu", "token_loss.cu", "token_sample.cu", "checkpoint.cu"]
 
 
 def _nvcc() -> str:
