@@ -579,9 +579,9 @@ muon_status muon_preference_loss(const muon_token_batch* batch, const muon_prefe
  * bytes apart, then rows * P / 32 bytes b, one for each block of 32 consecutive columns of a
  * row (16-byte aligned; padding columns hold 0).  A value stands for q 2^(b - 133), and 2^(b -
  * 133) is the smallest power of two, 2^-126 at least, for which the block's largest magnitude
- * rounds to 127 steps or fewer: a value is off by at most half a step, which is 2^-7 of the
- * block's largest magnitude or less.  Rounding is to even; magnitudes above 127.5 2^121 are cut
- * to 127 2^121.  b = 255: the block held an infinity or a NaN, and reads back as NaN.  Every value
+ * rounds to 127 steps or fewer: a value is off by at most half a step, 1/127.5 of the
+ * block's largest magnitude (or 2^-127).  Rounding is to even; magnitudes above 127.5 2^121 are
+ * cut to 127 2^121.  b = 255: the block held an infinity or a NaN, and reads back as NaN.  Every value
  * is a bf16 number. */
 typedef struct {
   void* data;

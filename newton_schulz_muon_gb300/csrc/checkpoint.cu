@@ -123,12 +123,10 @@ __device__ __forceinline__ void values_of(const SavedUnit<N>& s, float (&v)[N]) 
   for (int i = 0; i < N; ++i) v[i] = (float)(int8_t)(s.q[i / 4] >> (8 * (i % 4))) * step;
 }
 
-// 1 / (1 + e^-g) and 1 minus that.  e^-g is held below 1e38, so that the product does not
-// become 0 times infinity.
+// 1 / (1 + e^-g) and 1 minus that, e^-g / (1 + e^-g).
 __device__ __forceinline__ float2 sigmoid(float g) {
-  const float e = fminf(expf(-g), 1e38f);
-  const float s = __frcp_rn(1.f + e);
-  return make_float2(s, e * s);
+  const float e = expf(-g), s = __frcp_rn(1.f + e);
+  return make_float2(s, e == INFINITY ? 1.f : e * s);
 }
 
 enum Pass { kSave, kLoad, kGatedForward, kGatedBackward };

@@ -4,8 +4,8 @@
 //   b = 255      an infinity or NaN in the block: every value of it reads back as NaN
 //   b = 7 .. 254 2^(b - 133) is the smallest power of two (no smaller than 2^-126) for which
 //                the block's largest magnitude rounds to 127 steps or fewer
-// A value is thus off by half a step at most, 2^-7 of the block's largest magnitude or
-// less; only magnitudes above 127.5 2^121 are cut to 127 2^121.  Steps are powers of two so
+// A value is thus off by half a step at most, which is 2^-127 or up to 1/127.5 of the block's largest
+// magnitude; only magnitudes above 127.5 2^121 are cut to 127 2^121.  Steps are powers of two so
 // that a value, of 7 significant bits, is a bf16 number: products on the tensor cores take
 // it as it is.
 #pragma once

@@ -1,0 +1,221 @@
+"""8-bit activation checkpoints against float64.
+
+Saving and loading are exact: bytes and values are compared for equality.  Tolerances of the
+rest, derived before the first run:
+  gated activation   expf is within 2 units of 2^-23, then 1 + e, its reciprocal and two or three products
+                     at 2^-24 each: GATED = 7e-7 of the formula's terms (for dgate, whose terms
+                     may cancel, of the sum of their magnitudes); half a step, 2^-8, more in
+                     bf16.  Below gate = -128 ln 2 = -88.7228 e^-gate is infinite and the
+                     sigmoid, 2^-128 and less, 0; as |gate| e^gate falls there, FLOOR is 88.7228
+                     2^-128 = 2.6073e-37 of the other factors, and TINY a subnormal's step
+  weight gradient    products are exact in fp32; an accumulation of 16 of them rounds by 2^-23 of the
+                     sum of magnitudes at most: (T / 16 + 4) 2^-23 sum |dy| |x|, three times
+                     as many for fp32 gradients, which go through as three bf16 parts, and
+                     2^-24 sum |dy| |x| for what the parts leave; half a step, 2^-8, in bf16
+"""
+import numpy as np
+import pytest
+
+from gpu_util import nsm
+from oracle import checkpoint
+
+pytestmark = pytest.mark.gpu
+GATED, FLOOR, TINY = 7e-7, 2.61e-37, 2.0 ** -149
+HALF = {"float32": 2.0 ** -24, "bfloat16": 2.0 ** -8}
+
+
+@pytest.fixture(scope="module")
+def m():
+    return nsm()
+
+
+def _f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _matrix(rng, rows, cols, dtype="float32", pad=0, lead=0, scale=1.0, wide=True):
+    """(matrix on the device inside memory that holds 300, its float64 values)"""
+    import torch
+    x = rng.normal(0, scale, (rows, cols))
+    if wide:
+        x *= np.exp(rng.normal(0, 1.5, (1, cols)))
+    buffer = torch.full((lead + rows * (cols + pad) + 8,), 300.0, device="cuda").to(getattr(torch, dtype))
+    t = buffer[lead:lead + rows * (cols + pad)].view(rows, cols + pad)[:, :cols]
+    t.copy_(torch.from_numpy(x.astype(np.float32)).cuda())
+    return t, _f64(t)
+
+
+def _encoded(ck):
+    """(q, b) as the device holds them."""
+    data = ck.data.cpu().numpy()
+    blocks = -(-ck.cols // 32)
+    q = data[:ck.rows * blocks * 32].view(np.int8).reshape(ck.rows, -1)
+    return q, data[ck.rows * blocks * 32:].reshape(ck.rows, blocks)
+
+
+SHAPES = [(1, 1, 0, 0), (3, 31, 0, 1), (5, 32, 0, 0), (7, 33, 3, 0), (131, 1000, 0, 0), (64, 1003, 5, 3), (2, 40000, 0, 0),
+          (1025, 96, 8, 0), (4099, 17, 0, 0), (333, 9728, 64, 8)]
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("rows,cols,pad,lead", SHAPES)
+def test_save_and_load(m, rows, cols, pad, lead, dtype):
+    import torch
+    rng = np.random.default_rng([rows, cols])
+    x, v = _matrix(rng, rows, cols, dtype, pad, lead)
+    ck = m.muon_checkpoint_save(x)
+    q, b = checkpoint.encode(v)
+    got_q, got_b = _encoded(ck)
+    assert (got_b == b).all() and (got_q == q).all()
+    want = checkpoint.decode(q, b, cols)
+    for out in ("bfloat16", "float32"):
+        y, _ = _matrix(rng, rows, cols, out, pad, lead)
+        assert m.muon_checkpoint_load(ck, out=y) is y
+        assert (_f64(y) == want).all()
+        base = y._base if y._base is not None else y
+        if pad or lead:  # the memory around the rows is as it was
+            flat = base.reshape(-1)
+            keep = torch.ones(flat.numel(), dtype=torch.bool, device="cuda")
+            idx = lead + torch.arange(rows, device="cuda")[:, None] * (cols + pad) + torch.arange(cols, device="cuda")
+            keep[idx.reshape(-1)] = False
+            assert (flat[keep] == 300).all()
+    assert torch.equal(m.muon_checkpoint_load(ck), m.muon_checkpoint_load(ck, dtype=torch.float32).bfloat16())
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_special_values(m, dtype):
+    import torch
+    rng = np.random.default_rng(1)
+    x, _ = _matrix(rng, 12, 64, dtype)
+    t = x.dtype
+    x[0] = 0
+    x[1, 5] = float("nan")
+    x[2, 63] = float("inf")
+    x[3, 0] = -float("inf")
+    x[4, 7] = torch.finfo(t).max
+    x[5, 7] = -torch.finfo(t).max
+    x[6] = torch.finfo(t).tiny
+    x[7] = 0
+    x[7, 3] = torch.finfo(t).tiny / 2   # a subnormal
+    x[8, :32] = 0
+    x[8, 0] = 127.5
+    x[9, :32] = torch.arange(32, device="cuda", dtype=t) * 0.5
+    x[9, 0] = 127.0
+    x[10] = -0.0
+    x[11, :32] = 2.0 ** 127
+    v = _f64(x)
+    got = _f64(m.muon_checkpoint_load(m.muon_checkpoint_save(x)))
+    want = checkpoint.values(v)
+    assert np.array_equal(got, want, equal_nan=True)
+    assert np.isnan(got[1, :32]).all() and not np.isnan(got[1, 32:]).any() and np.isnan(got[2, 32:]).all()
+
+
+def test_past_2_31_elements(m):
+    import torch
+    rows, cols = 70001, 32768
+    x = torch.zeros(rows, cols, device="cuda", dtype=torch.bfloat16)
+    at = torch.arange(rows, device="cuda") * 7919 % cols
+    x.scatter_(1, at[:, None], 3.0)
+    ck = m.muon_checkpoint_save(x)
+    x.fill_(5.0)
+    m.muon_checkpoint_load(ck, out=x)
+    assert (x.gather(1, at[:, None]) == 3).all() and x[-100:].float().sum() == 300 and x[:100].float().sum() == 300
+    assert (x.float().sum(1) == 3).all()
+
+
+def test_nothing(m):
+    import torch
+    x = torch.zeros(0, 40, device="cuda")
+    ck = m.muon_checkpoint_save(x)
+    assert m.muon_checkpoint_load(ck).shape == (0, 40)
+    h, g, u = m.muon_swiglu_forward(x, x)
+    dg, du, again = m.muon_swiglu_backward(x, g, u, with_h=True)
+    assert h.shape == dg.shape == du.shape == again.shape == (0, 40)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("rows,cols,pad,lead", SHAPES)
+def test_gated(m, rows, cols, pad, lead, dtype):
+    rng = np.random.default_rng([rows, cols, 1])
+    gate, vg = _matrix(rng, rows, cols, dtype, pad, lead, 2.0)
+    up, vu = _matrix(rng, rows, cols, dtype, 0, lead)
+    h, cg, cu = m.muon_swiglu_forward(gate, up)
+    for ck, v in ((cg, vg), (cu, vu)):
+        q, b = _encoded(ck)
+        wq, wb = checkpoint.encode(v)
+        assert (q == wq).all() and (b == wb).all()
+    tol = GATED + (HALF[dtype] if dtype == "bfloat16" else 0)
+    want = checkpoint.swiglu(vg, vu)
+    assert (np.abs(_f64(h) - want) <= tol * np.abs(want) + FLOOR * np.abs(vu) + TINY).all()
+    dh, vd = _matrix(rng, rows, cols, dtype, pad, 0, 0.1, False)
+    g, u = checkpoint.values(vg), checkpoint.values(vu)
+    dgate, dup, again = m.muon_swiglu_backward(dh, cg, cu, with_h=True)
+    wg, wu = checkpoint.swiglu_backward(vd, g, u)
+    s = checkpoint.sigmoid(g)
+    terms = np.abs(vd * u) * s * (1 + np.abs(g) * (1 - s))
+    half = HALF[dtype] if dtype == "bfloat16" else 0
+    assert (np.abs(_f64(dgate) - wg) <= 2 * GATED * terms + half * np.abs(wg) + 2 * FLOOR * np.abs(vd * u) + TINY).all()
+    assert (np.abs(_f64(dup) - wu) <= tol * np.abs(wu) + FLOOR * np.abs(vd) + TINY).all()
+    want = checkpoint.swiglu(g, u)
+    assert (np.abs(_f64(again) - want) <= tol * np.abs(want) + FLOOR * np.abs(u) + TINY).all()
+    dgate2, dup2, none = m.muon_swiglu_backward(dh, cg, cu)
+    assert none is None and (dgate2 == dgate).all() and (dup2 == dup).all()
+
+
+def test_gated_extremes(m):
+    """Gates at which the exponential leaves fp32's range, and what is not finite."""
+    import torch
+    gate = torch.tensor([[-200.0, 200.0, -90.0, 90.0, 0.0, -1.2784645] + [1.0] * 26, [float("nan")] + [1.0] * 31],
+                        device="cuda")
+    up = torch.full_like(gate, 2.0)
+    h, cg, cu = m.muon_swiglu_forward(gate, up)
+    assert h[0, :5].tolist()[1] == 400 and abs(h[0, 0]) < 1e-30 and h[0, 4] == 0 and h[1, 0].isnan()
+    assert not h[1, 1:].isnan().any()
+    dg, du, _ = m.muon_swiglu_backward(torch.ones_like(gate), cg, cu)
+    assert not dg[0].isnan().any() and not du[0].isnan().any() and dg[0, 1] == 2 and abs(dg[0, 0]) < 1e-30
+    assert dg[1].isnan().all() and du[1].isnan().all()   # the block is not a number
+
+
+def test_gated_halves_in_place_and_graph(m):
+    import torch
+    rng = np.random.default_rng(4)
+    both, v = _matrix(rng, 50, 208, "bfloat16")
+    gate, up = both[:, :104], both[:, 104:]
+    h, cg, cu = m.muon_swiglu_forward(gate, up)
+    alone = m.muon_swiglu_forward(gate.contiguous(), up.contiguous())
+    assert torch.equal(h, alone[0]) and torch.equal(cg.data, alone[1].data) and torch.equal(cu.data, alone[2].data)
+    over = both.clone()
+    m.muon_swiglu_forward(over[:, :104], over[:, 104:], h=over[:, :104])
+    assert torch.equal(over[:, :104], h) and torch.equal(over[:, 104:], up)
+    dh = torch.randn(50, 104, device="cuda").bfloat16()
+    grads = torch.empty_like(both)
+    dg, du, again = m.muon_swiglu_backward(dh, cg, cu, dgate=grads[:, :104], dup=grads[:, 104:], with_h=True)
+    for k in range(3):   # each output in the place of dh
+        mine = dh.clone()
+        out = [None, None, torch.empty_like(dh)]
+        out[k] = mine
+        got = m.muon_swiglu_backward(mine, cg, cu, dgate=out[0], dup=out[1], h=out[2])
+        assert torch.equal(got[0], dg) and torch.equal(got[1], du) and torch.equal(got[2], again)
+    graph = torch.cuda.CUDAGraph()
+    held = dh.clone()
+    with torch.cuda.graph(graph):
+        hh, g2, u2 = m.muon_swiglu_forward(gate, up)
+        got = m.muon_swiglu_backward(held, g2, u2, with_h=True)
+    graph.replay()
+    assert torch.equal(hh, h) and all(torch.equal(a, b) for a, b in zip(got, (dg, du, again)))
+    both.mul_(0.5)
+    graph.replay()
+    fresh = m.muon_swiglu_forward(gate, up)
+    assert torch.equal(hh, fresh[0])
+
+
+def test_streams(m):
+    import torch
+    x = torch.randn(1000, 1000, device="cuda")
+    want = m.muon_checkpoint_load(m.muon_checkpoint_save(x))
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    ck = m.muon_checkpoint_save(x, stream=stream)
+    got = m.muon_checkpoint_load(ck, stream=stream.cuda_stream)
+    stream.synchronize()
+    assert torch.equal(got, want)
