@@ -600,6 +600,25 @@ muon_status muon_checkpoint_save(const void* x, int64_t x_stride, int32_t dtype,
 muon_status muon_checkpoint_load(const muon_checkpoint* checkpoint, void* x, int64_t x_stride,
                                  int32_t dtype, void* stream);
 
+/* Workspace of muon_checkpoint_weight_grad for these operands (bytes; may be 0).  Host work. */
+muon_status muon_weight_grad_workspace_bytes(const muon_checkpoint* checkpoint, const void* dy,
+                                             int64_t dy_stride, int32_t dy_dtype, int64_t outs,
+                                             size_t* bytes);
+
+/* The weight gradient of y = x W^T from x's checkpoint, as muon_clip_grad_norm and muon_step
+ * read it:
+ *   dw[o][i] = sum_t dy[t][o] x[t][i], added to dw's values where accumulate is 1.
+ * dy: [rows][outs], rows dy_stride elements apart (0 means outs); dw: [outs][cols], rows
+ * dw_stride apart (0 means cols); both MUON_DTYPE_*.  Products are exact and sums fp32, rounded
+ * once to dw's type.  bf16 gradients on 16-byte boundaries (base and row stride) are read as
+ * they lie; others pass through the workspace, fp32 ones as three bf16 parts that add up to
+ * them.  No tokens give 0.  NaN in a block of the checkpoint, or in dy, reaches every sum it
+ * takes part in. */
+muon_status muon_checkpoint_weight_grad(const muon_checkpoint* checkpoint, const void* dy,
+                                        int64_t dy_stride, int32_t dy_dtype, int64_t outs, void* dw,
+                                        int64_t dw_stride, int32_t dw_dtype, int32_t accumulate,
+                                        void* workspace, size_t workspace_bytes, void* stream);
+
 /* A gated activation and the checkpoints of its inputs, in one pass over them:
  *   h = gate s up, s = 1 / (1 + exp(-gate)).
  * gate, up and h have the checkpoints' shape and one dtype, each its own row stride (0 means

@@ -156,6 +156,10 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
         "muon_checkpoint_bytes": (c_int32, [c_int64, c_int64, POINTER(c_size_t)]),
         "muon_checkpoint_save": (c_int32, [P, c_int64, c_int32, POINTER(muon_checkpoint), P]),
         "muon_checkpoint_load": (c_int32, [POINTER(muon_checkpoint), P, c_int64, c_int32, P]),
+        "muon_weight_grad_workspace_bytes": (c_int32, [POINTER(muon_checkpoint), P, c_int64, c_int32, c_int64,
+                                                       POINTER(c_size_t)]),
+        "muon_checkpoint_weight_grad": (c_int32, [POINTER(muon_checkpoint), P, c_int64, c_int32, c_int64, P, c_int64,
+                                                  c_int32, c_int32, P, c_size_t, P]),
         "muon_swiglu_forward": (c_int32, [P, c_int64, P, c_int64, c_int32, P, c_int64, POINTER(muon_checkpoint),
                                           POINTER(muon_checkpoint), P]),
         "muon_swiglu_backward": (c_int32, [P, c_int64, c_int32, POINTER(muon_checkpoint), POINTER(muon_checkpoint), P,
@@ -927,6 +931,48 @@ def muon_checkpoint_load(checkpoint, out=None, dtype=None, stream=None):
         code = _dtype_code(out.dtype)
         _check(_lib().muon_checkpoint_load(byref(checkpoint.struct), *_matrix(out, rows, cols, out.dtype, device, "out"),
                                            code, handle), "muon_checkpoint_load")
+    return out
+
+
+def muon_weight_grad_workspace_bytes(checkpoint, dy) -> int:
+    outs, stride = _gradient_rows(checkpoint, dy)
+    v = c_size_t()
+    _check(_lib().muon_weight_grad_workspace_bytes(byref(checkpoint.struct), dy.data_ptr(), stride, _dtype_code(dy.dtype),
+                                                   outs, byref(v)), "muon_weight_grad_workspace_bytes")
+    return v.value
+
+
+def _gradient_rows(checkpoint, dy):
+    """(outs, row stride) of the gradient of a linear layer's output."""
+    rows, outs, stride = _rows(dy, "dy")
+    if rows != checkpoint.rows or dy.get_device() != checkpoint.device:
+        raise ValueError(f"dy: expected {checkpoint.rows} rows on cuda:{checkpoint.device}, got shape {tuple(dy.shape)} on "
+                         f"{dy.device}")
+    return outs, stride
+
+
+def muon_checkpoint_weight_grad(checkpoint, dy, out=None, accumulate: bool = False, dtype=None, workspace=None,
+                                stream=None):
+    """The weight gradient dy^T x [outs, cols] of y = x W^T from the checkpoint of x [rows, cols]
+    and dy [rows, outs] (bf16 or fp32), written to `out` or a new matrix of `dtype` (dy's by
+    default), or added to `out` with accumulate=True."""
+    import torch
+    outs, stride = _gradient_rows(checkpoint, dy)
+    cols, device = checkpoint.cols, checkpoint.device
+    if out is None and accumulate:
+        raise ValueError("accumulate=True needs out")
+    if out is not None and dtype is not None and out.dtype is not dtype:
+        raise ValueError(f"out: expected {dtype}, got {out.dtype}")
+    nbytes = muon_weight_grad_workspace_bytes(checkpoint, dy)
+    context, handle = _on_stream(stream, device)
+    with context:
+        _keep, ws, nbytes = _space(workspace, nbytes, device, handle) if nbytes else (None, None, 0)
+        if out is None:
+            out = torch.empty(outs, cols, dtype=dtype or dy.dtype, device=device)
+        ptr, out_stride = _matrix(out, outs, cols, out.dtype, device, "out")
+        _check(_lib().muon_checkpoint_weight_grad(byref(checkpoint.struct), dy.data_ptr(), stride, _dtype_code(dy.dtype),
+                                                  outs, ptr, out_stride, _dtype_code(out.dtype), int(bool(accumulate)),
+                                                  ws, nbytes, handle), "muon_checkpoint_weight_grad")
     return out
 
 

@@ -25,7 +25,8 @@ LIBMUON_DEBUG = os.path.join(PKG, "libmuon_debug.so")
 LIBSYNTH = os.path.join(ROOT, "synth", "libmuonsynth.so")
 
 MUON_SOURCES = ["runtime.cu", "elementwise.cu", "ns_gemm.cu", "ns_small.cu", "ns_gram.cu", "noalloc.cu",
-                "schedule.cu", "grad_clip.cu", "token_loss.cu", "token_sample.cu", "checkpoint.cu"]
+                "schedule.cu", "grad_clip.cu", "token_loss.cu", "token_sample.cu", "checkpoint.cu",
+                "checkpoint_grad.cu"]
 
 
 def _nvcc() -> str:

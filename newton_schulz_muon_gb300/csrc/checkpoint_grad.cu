@@ -1,0 +1,645 @@
+// The weight gradient of a linear layer from the 8-bit checkpoint of its input:
+//
+//   dW[o][i] = sum_t dy[t][o] x[t][i]     (+ dW)
+//
+// on the tcgen05 tensor cores.  A checkpoint's values are bf16 numbers, so the conversion
+// before the product loses nothing; products are exact in fp32 and sums are fp32.  Both
+// operands have the sum's index t outside (their rows are tokens) and are read MN-major as
+// they lie.
+//
+// A pair of CTAs on two SMs computes a 256 x 256 tile of dW with one
+// tcgen05.mma.cta_group::2 (M = N = 256); each CTA holds 128 rows of the tile (dy's columns)
+// and one 128-wide half of x.  A stage is 64 tokens.  Warps of a CTA:
+//   0      TMA producer of dy's stages (bf16, 128-byte swizzle), onto the leader's barrier
+//   1      tcgen05.mma issuer (the leader's)
+//   2      producer of the raw ring: x's bytes by TMA, the blocks' exponents by cp.async
+//   4-7    epilogue: TMEM to registers to dW, while the next tile is summed into the other
+//          accumulator
+//   8-15   converters: raw bytes and exponents to bf16 in the swizzled operand stage
+// A value q 2^(b - 133) is made by bit operations on pairs: with the byte q beside 0x43, the
+// two bf16 numbers 128 + (q mod 128) and 128 or 256 by q's sign differ by q; one product with the step follows.
+// All three are exact.
+//
+// fp32 gradients are split into three bf16 parts that add up to them exactly (8 bits of the
+// significand each) by a pass of its own, and the sum runs over the parts.  The same pass
+// copies bf16 gradients whose rows a TMA cannot read (16-byte boundaries).
+//
+// Where a matrix has too few tiles for the SMs, the tokens are divided among several pairs,
+// whose fp32 sums are added in a fixed order by a last pass.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "checkpoint.cuh"
+#include "device.cuh"
+#include "kernels.h"
+#include "launch.cuh"
+#include "muon.h"
+#include "rows.cuh"
+
+namespace muon {
+namespace {
+
+constexpr int kTile = 256;          // rows and columns of a tile of dW
+constexpr int kTokens = 64;         // tokens of a stage
+constexpr int kGradThreads = 512;
+constexpr int kGradStages = 6, kRawStages = 3;
+constexpr uint32_t kChunk = kTokens * 128;          // 64 tokens of 64 bf16 columns
+constexpr uint32_t kOperand = 2 * kChunk;           // a CTA's half of an operand
+constexpr uint32_t kRawBytes = kTokens * 128, kRawExps = kTokens * 8;
+constexpr uint32_t kRaw = kRawBytes + kRawExps;
+constexpr size_t kGradSmem = kGradStages * 2 * kOperand + kRawStages * kRaw + 1024;
+static_assert(kGradSmem <= 232448 - 1024, "shared memory of one CTA");
+constexpr int kConverters = 8, kEpilogue = 4;       // warps
+constexpr uint32_t kGradTmem = 512;
+
+struct GradArgs {
+  CUtensorMap dy;         // [parts][tokens][outs] bf16, box 64 x 64
+  CUtensorMap q;          // [tokens][P] bytes, box 128 x 64
+  const uint8_t* b;       // [tokens][blocks]
+  const uint8_t* b_end;
+  int64_t tokens;
+  int32_t blocks, cols, outs;
+  int32_t parts, steps;   // bf16 parts of dy, 64-token steps of one
+  int32_t tiles_n, tiles, splits, split_steps;
+  void* out;              // dW, or the splits' sums [splits][outs][stride] fp32
+  int64_t stride, split_stride;
+  int32_t bf16, accumulate;
+};
+
+// 4 bytes global -> shared, of which `bytes` are read and the others are 0.
+__device__ __forceinline__ void cp_async_4_part(void* dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+}
+// An arrival on `bar` once this thread's cp.async so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// An arrival on a barrier of either CTA that orders this thread's writes before it.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// mbar_wait for arrivals of both CTAs.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (mbar_try_wait_cluster(bar, parity)) return true;
+  const unsigned long long t0 = globaltimer_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    if ((i & 63u) == 0) {
+      if (*abort) return false;
+      if (globaltimer_ns() - t0 > kWaitLimitNs) {
+        *abort = 1;
+        return false;
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t x, uint32_t y) {
+  const __nv_bfloat162 r =
+      __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t y) {
+  const __nv_bfloat162 r =
+      __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// Two signed bytes, each beside 0x43, times the step.
+__device__ __forceinline__ uint32_t convert2(uint32_t w, uint32_t step) {
+  return mul_bf16x2(sub_bf16x2(w & 0xFF7FFF7Fu, w & 0xFF80FF80u), step);
+}
+
+struct Unit {
+  int m0, n0, split, kb0, kb1;
+};
+__device__ __forceinline__ Unit unit_of(const GradArgs& a, int u) {
+  Unit r;
+  r.split = u / a.tiles;
+  const int t = u - r.split * a.tiles;
+  r.m0 = t / a.tiles_n * kTile;
+  r.n0 = t % a.tiles_n * kTile;
+  r.kb0 = r.split * a.split_steps;
+  r.kb1 = min(r.kb0 + a.split_steps, a.parts * a.steps);
+  return r;
+}
+
+// 32 consecutive columns of a row of dW.
+__device__ __forceinline__ void store_row(const GradArgs& a, int split, int64_t row, int col, const float (&v)[32]) {
+  const int n = min(32, a.cols - col);
+  const int64_t at = split * a.split_stride + row * a.stride + col;
+  if (a.bf16) {
+    __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(a.out) + at;
+    if (n == 32 && (reinterpret_cast<uint64_t>(p) & 15) == 0) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float x[8];
+        if (a.accumulate) Vec<__nv_bfloat16>::unpack(reinterpret_cast<const uint4*>(p)[k], x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = a.accumulate ? x[i] + v[8 * k + i] : v[8 * k + i];
+        reinterpret_cast<uint4*>(p)[k] = Vec<__nv_bfloat16>::pack(x);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (i < n) p[i] = __float2bfloat16_rn(a.accumulate ? __bfloat162float(p[i]) + v[i] : v[i]);
+    }
+    return;
+  }
+  float* p = reinterpret_cast<float*>(a.out) + at;
+  if (n == 32 && (reinterpret_cast<uint64_t>(p) & 15) == 0) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float4 x = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+      if (a.accumulate) {
+        const float4 y = reinterpret_cast<const float4*>(p)[k];
+        x = make_float4(y.x + x.x, y.y + x.y, y.z + x.z, y.w + x.w);
+      }
+      reinterpret_cast<float4*>(p)[k] = x;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i < n) p[i] = a.accumulate ? p[i] + v[i] : v[i];
+  }
+}
+
+__global__ void __launch_bounds__(kGradThreads, 1) weight_grad_kernel(const __grid_constant__ GradArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* raw = smem + kGradStages * 2 * kOperand;
+  __shared__ __align__(8) uint64_t full_bar[kGradStages], empty_bar[kGradStages];
+  __shared__ __align__(8) uint64_t raw_full[kRawStages], raw_empty[kRawStages];
+  __shared__ __align__(8) uint64_t tfull_bar[2], tempty_bar[2], drain_bar;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_ctarank();
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, units = a.tiles * a.splits;
+  volatile int* abort_p = &abort_flag;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kGradStages; ++s) {
+      mbar_init(&full_bar[s], 1 + 2 * kConverters);  // dy's bytes of both CTAs; the converter warps of both
+      mbar_init(&empty_bar[s], 1);
+    }
+    for (int s = 0; s < kRawStages; ++s) {
+      mbar_init(&raw_full[s], 1 + 32);  // x's bytes; the exponents of each lane
+      mbar_init(&raw_empty[s], kConverters);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tfull_bar[i], 1);
+      mbar_init(&tempty_bar[i], 2 * kEpilogue);
+    }
+    mbar_init(&drain_bar, 1);
+    abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 0 && lane == 0) tma_prefetch_desc(&a.dy);
+  if (warp == 2 && lane == 0) tma_prefetch_desc(&a.q);
+  if (warp == 1) {
+    tmem_alloc<2>(&tmem_slot, kGradTmem);
+    tmem_relinquish<2>();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // barriers of both CTAs exist before any remote signal
+  tc_fence_after();
+  griddep_launch_dependents();
+  griddep_wait();
+  const uint32_t tmem = tmem_slot;
+
+  if (warp == 0) {
+    // ---- dy ----
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int u = pair; u < units && ok; u += pairs) {
+      const Unit t = unit_of(a, u);
+      for (int kb = t.kb0; kb < t.kb1; ++kb) {
+        const bool got = mbar_wait(&empty_bar[stage], phase ^ 1u, abort_p, nullptr);
+        if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+        if (lane == 0) {
+          uint8_t* sa = smem + (size_t)stage * 2 * kOperand;
+          if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2 * kOperand);
+          const uint32_t bar = mapa_shared(&full_bar[stage], 0);
+          const int part = kb / a.steps, t0 = (kb - part * a.steps) * kTokens;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            tma_load_3d_pair(sa + h * kChunk, &a.dy, bar, t.m0 + rank * 128 + h * 64, t0, part);
+        }
+        __syncwarp();
+        if (++stage == kGradStages) { stage = 0; phase ^= 1u; }
+      }
+    }
+    if (*abort_p && leader && lane == 0) {
+      // loads already issued land before the CTA exits (bounded)
+      for (int s = 0; s < kGradStages; ++s)
+        (void)mbar_wait(&full_bar[s], phase ^ (s < stage ? 0u : 1u), nullptr, nullptr, 100000000ull);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (leader) {
+      // ---- tensor cores ----
+      const uint32_t idesc = make_idesc(1u, kTile, kTile, 1u, 1u);
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (int u = pair; u < units && ok; u += pairs) {
+        const Unit t = unit_of(a, u);
+        const bool free_acc = mbar_wait(&tempty_bar[acc], acc_phase ^ 1u, abort_p, nullptr);
+        if (!__all_sync(0xffffffffu, free_acc)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + (uint32_t)(acc * kTile);
+        for (int kb = t.kb0; kb < t.kb1; ++kb) {
+          const bool got = mbar_wait_cluster(&full_bar[stage], phase, abort_p);
+          if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+          tc_fence_after();
+          if (lane == 0) {
+            const uint32_t sa = smem_u32(smem + (size_t)stage * 2 * kOperand), sb = sa + kOperand;
+#pragma unroll
+            for (int kk = 0; kk < kTokens / 16; ++kk)
+              mma<false, 2>(d, smem_desc_sw128(sa + kk * 16 * 128, kChunk, 1024),
+                            smem_desc_sw128(sb + kk * 16 * 128, kChunk, 1024), idesc, (kb > t.kb0 || kk > 0) ? 1u : 0u);
+            mma_commit_multicast<2>(&empty_bar[stage], 3);
+          }
+          __syncwarp();
+          if (++stage == kGradStages) { stage = 0; phase ^= 1u; }
+        }
+        if (!ok) break;
+        if (lane == 0) mma_commit_multicast<2>(&tfull_bar[acc], 3);
+        __syncwarp();
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+      if (lane == 0) {  // every MMA has completed before TMEM is freed
+        mma_commit<2>(&drain_bar);
+        (void)mbar_wait(&drain_bar, 0u, nullptr, nullptr);
+      }
+      __syncwarp();
+    }
+  } else if (warp == 2) {
+    // ---- x as it lies ----
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int u = pair; u < units && ok; u += pairs) {
+      const Unit t = unit_of(a, u);
+      const int col0 = t.n0 + rank * 128, block0 = col0 / kBlockCols;
+      for (int kb = t.kb0; kb < t.kb1; ++kb) {
+        const bool got = mbar_wait(&raw_empty[stage], phase ^ 1u, abort_p, nullptr);
+        if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+        uint8_t* r = raw + (size_t)stage * kRaw;
+        const int t0 = kb % a.steps * kTokens;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&raw_full[stage], kRawBytes);
+          tma_load_3d(r, &a.q, &raw_full[stage], col0, t0, 0);
+        }
+        // the 4 exponents of each token, within the 8 bytes of two 4-byte words; zeros past
+        // the last token
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int i = h * 32 + lane;
+          const uint8_t* p = a.b + (int64_t)(t0 + i) * a.blocks + block0;
+          p -= reinterpret_cast<uint64_t>(p) & 3;
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            const int64_t left = t0 + i < a.tokens ? a.b_end - (p + 4 * w) : 0;
+            cp_async_4_part(r + kRawBytes + i * 8 + 4 * w, left > 0 ? p + 4 * w : a.b, (int)max((int64_t)0, min((int64_t)4, left)));
+          }
+        }
+        cp_async_arrive(&raw_full[stage]);
+        if (++stage == kRawStages) { stage = 0; phase ^= 1u; }
+      }
+    }
+    cp_async_wait<0>();
+    if (*abort_p && lane == 0) {
+      for (int s = 0; s < kRawStages; ++s)
+        (void)mbar_wait(&raw_full[s], phase ^ (s < stage ? 0u : 1u), nullptr, nullptr, 100000000ull);
+    }
+    __syncwarp();
+  } else if (warp >= 8) {
+    // ---- bytes to bf16 ----
+    const int i = threadIdx.x - 256, unit = i & 15;  // 8 columns of tokens i / 16 + 16 k
+    int stage = 0, rs = 0;
+    uint32_t phase = 0, rphase = 0;
+    bool ok = true;
+    const uint32_t lead = mapa_shared(&full_bar[0], 0);
+    for (int u = pair; u < units && ok; u += pairs) {
+      const Unit t = unit_of(a, u);
+      for (int kb = t.kb0; kb < t.kb1; ++kb) {
+        const bool got = mbar_wait(&raw_full[rs], rphase, abort_p, nullptr) &&
+                         mbar_wait(&empty_bar[stage], phase ^ 1u, abort_p, nullptr);
+        if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+        const uint8_t* r = raw + (size_t)rs * kRaw;
+        uint8_t* sb = smem + (size_t)stage * 2 * kOperand + kOperand + (unit >> 3) * kChunk;
+        const int t0 = kb % a.steps * kTokens;
+#pragma unroll
+        for (int k = 0; k < kTokens / 16; ++k) {
+          const int tok = (i >> 4) + 16 * k;
+          const uint2 q = *reinterpret_cast<const uint2*>(r + tok * 128 + unit * 8);
+          const int b = r[kRawBytes + tok * 8 + (int)(((uint32_t)(t0 + tok) * (uint32_t)a.blocks) & 3u) + (unit >> 2)];
+          const uint32_t bits = b == 255 ? 0x7FC0u : (uint32_t)max(b - 6, 0) << 7;
+          const uint32_t step = bits | bits << 16;
+          uint4 o;
+          o.x = convert2(__byte_perm(q.x, 0x43u, 0x4140), step);
+          o.y = convert2(__byte_perm(q.x, 0x43u, 0x4342), step);
+          o.z = convert2(__byte_perm(q.y, 0x43u, 0x4140), step);
+          o.w = convert2(__byte_perm(q.y, 0x43u, 0x4342), step);
+          *reinterpret_cast<uint4*>(sb + tok * 128 + (((unit & 7) ^ (tok & 7)) << 4)) = o;
+        }
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive_cluster(lead + stage * 8);
+          mbar_arrive(&raw_empty[rs]);
+        }
+        if (++stage == kGradStages) { stage = 0; phase ^= 1u; }
+        if (++rs == kRawStages) { rs = 0; rphase ^= 1u; }
+      }
+    }
+  } else if (warp >= 4) {
+    // ---- epilogue ----
+    const int quad = warp & 3;
+    const uint32_t lead[2] = {mapa_shared(&tempty_bar[0], 0), mapa_shared(&tempty_bar[1], 0)};
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int u = pair; u < units; u += pairs) {
+      const Unit t = unit_of(a, u);
+      const bool got = mbar_wait(&tfull_bar[acc], acc_phase, abort_p, nullptr);
+      const bool ok = __all_sync(0xffffffffu, got);
+      tc_fence_after();
+      const int64_t row = (int64_t)t.m0 + rank * 128 + quad * 32 + lane;
+#pragma unroll 1
+      for (int c = 0; c < kTile / 32; ++c) {
+        if (t.n0 + c * 32 >= a.cols) break;
+        float v[32];
+        if (ok) {
+          tmem_ld_32x32b_x32(tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(acc * kTile + c * 32), v);
+        } else {  // a wait ran out: no stale values pass for a gradient
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = NAN;
+        }
+        if (row < a.outs) store_row(a, t.split, row, t.n0 + c * 32, v);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster_relaxed(lead[acc]);
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1u;
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // neither CTA frees Tensor Memory or exits while the pair's signals may still reach it
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc<2>(tmem, kGradTmem);
+  }
+}
+
+// dy as `parts` bf16 matrices [parts][tokens][ld]: a copy, or the three parts of fp32 values,
+// each cut off at 8 bits of what the ones before it leave (cutting cannot overflow).
+constexpr int kPartThreads = 256;
+template <typename T>
+__global__ void __launch_bounds__(kPartThreads) parts_kernel(const T* dy, int64_t stride, int64_t tokens, int64_t outs,
+                                                             int64_t ld, __nv_bfloat16* out) {
+  griddep_launch_dependents();
+  const int64_t per = ld / 8, items = tokens * per;
+  for (int64_t i = (int64_t)blockIdx.x * kPartThreads + threadIdx.x; i < items; i += (int64_t)gridDim.x * kPartThreads) {
+    const int64_t t = i / per, c = (i - t * per) * 8;
+    const T* p = dy + t * stride + c;
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = c + k < outs ? Vec<T>::load(p + k) : 0.f;
+    uint4* to = reinterpret_cast<uint4*>(out + t * ld + c);
+    if constexpr (sizeof(T) == 2) {
+      *to = Vec<__nv_bfloat16>::pack(v);
+    } else {
+      uint32_t h[3][8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        float rest = v[k];
+        const bool finite = fabsf(rest) < INFINITY;
+#pragma unroll
+        for (int part = 0; part < 3; ++part) {
+          const uint32_t bits = __float_as_uint(rest) & 0xFFFF0000u;
+          h[part][k] = finite ? bits >> 16 : part ? 0u : rest != rest ? 0x7FC0u : bits >> 16;
+          rest -= __uint_as_float(bits);
+        }
+      }
+#pragma unroll
+      for (int part = 0; part < 3; ++part)
+        to[part * (tokens * ld / 8)] =
+            make_uint4(h[part][0] | h[part][1] << 16, h[part][2] | h[part][3] << 16, h[part][4] | h[part][5] << 16,
+                       h[part][6] | h[part][7] << 16);
+    }
+  }
+}
+
+// dW (+)= the splits' sums, in their order.
+constexpr int kJoinThreads = 256;
+template <typename T>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const float* sums, int64_t ld, int64_t split_stride, int splits,
+                                                            T* out, int64_t stride, int64_t outs, int64_t cols,
+                                                            int accumulate) {
+  griddep_wait();
+  const int64_t per = ld / 4, items = outs * per;
+  for (int64_t i = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x; i < items; i += (int64_t)gridDim.x * kJoinThreads) {
+    const int64_t r = i / per, c = (i - r * per) * 4;
+    const float4* p = reinterpret_cast<const float4*>(sums + r * ld + c);
+    float4 s = __ldcg(p);
+    for (int k = 1; k < splits; ++k) {
+      const float4 x = __ldcg(p + k * (split_stride / 4));
+      s = make_float4(s.x + x.x, s.y + x.y, s.z + x.z, s.w + x.w);
+    }
+    const float v[4] = {s.x, s.y, s.z, s.w};
+    T* q = out + r * stride + c;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (c + k < cols) Vec<T>::store(q + k, accumulate ? Vec<T>::load(q + k) + v[k] : v[k]);
+  }
+}
+
+// dW of no tokens.
+template <typename T>
+__global__ void __launch_bounds__(kJoinThreads) zero_kernel(T* out, int64_t stride, int64_t outs, int64_t cols) {
+  const int64_t items = outs * cols;
+  for (int64_t i = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x; i < items; i += (int64_t)gridDim.x * kJoinThreads)
+    Vec<T>::store(out + i / cols * stride + i % cols, 0.f);
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+constexpr int kPairs = 76;  // of SMs on the device this is built for: the division of the tokens goes by it
+
+struct GradPlan {
+  int64_t tiles_m, tiles_n, steps, splits, split_steps;
+  int parts;        // of dy; 0: read as it lies
+  int64_t ld;       // of the parts
+  int64_t sum_ld;   // of the splits' sums
+  size_t parts_bytes, bytes;
+};
+
+GradPlan plan_of(int64_t tokens, int64_t cols, int64_t outs, const void* dy, int64_t dy_stride, int32_t dtype) {
+  GradPlan p = {};
+  p.tiles_m = (outs + kTile - 1) / kTile;
+  p.tiles_n = (cols + kTile - 1) / kTile;
+  if (dtype == MUON_DTYPE_F32) p.parts = 3;
+  else p.parts = aligned(dy, 16) && dy_stride % 8 == 0 ? 0 : 1;
+  const int64_t passes = p.parts > 1 ? p.parts : 1;
+  p.steps = (tokens + kTokens - 1) / kTokens;
+  p.ld = (outs + 7) / 8 * 8;
+  if (p.parts) p.parts_bytes = ((size_t)p.parts * tokens * p.ld * 2 + 255) / 256 * 256;
+  const int64_t all = passes * p.steps, tiles = p.tiles_m * p.tiles_n;
+  int64_t splits = tiles < kPairs ? kPairs / tiles : 1;
+  if (splits > all / 4) splits = all / 4;  // four steps a split at least
+  if (splits < 1) splits = 1;
+  p.split_steps = (all + splits - 1) / splits;
+  p.splits = all ? (all + p.split_steps - 1) / p.split_steps : 1;
+  p.sum_ld = (cols + 3) / 4 * 4;
+  p.bytes = p.parts_bytes + (p.splits > 1 ? (size_t)p.splits * outs * p.sum_ld * 4 : 0);
+  return p;
+}
+
+int32_t check_grad_args(const muon_checkpoint* c, const void* dy, int64_t dy_stride, int32_t dy_dtype, int64_t outs) {
+  if (!c) return invalid("checkpoint is NULL");
+  if (c->rows < 0 || c->rows > (1ll << 31) - 1 - kTokens) return invalid("rows must be in [0, 2^31 - 64)");
+  if (c->cols < 1 || c->cols > (1ll << 30)) return invalid("cols must be in [1, 2^30]");
+  if (outs < 1 || outs > (1ll << 30)) return invalid("outs must be in [1, 2^30]");
+  if (dy_dtype != MUON_DTYPE_F32 && dy_dtype != MUON_DTYPE_BF16) return invalid("unknown dtype of dy");
+  if (dy_stride != 0 && (dy_stride < outs || dy_stride > (1ll << 36))) return invalid("dy_stride must be 0 or at least outs");
+  if (!aligned(dy, dy_dtype == MUON_DTYPE_BF16 ? 2 : 4)) return invalid("dy is not aligned to its type");
+  return MUON_OK;
+}
+
+int grid_of(int64_t items, int threads, int sms) {
+  const int64_t want = (items + threads - 1) / threads, most = 8ll * sms;
+  return (int)(want < 1 ? 1 : want < most ? want : most);
+}
+
+template <typename T>
+cudaError_t launch_join(const GradPlan& p, const float* sums, void* dw, int64_t stride, int64_t outs, int64_t cols,
+                        int accumulate, int sms, cudaStream_t s) {
+  return launch(join_kernel<T>, grid_of(outs * (p.sum_ld / 4), kJoinThreads, sms), kJoinThreads, 0, s, 1, true, sums,
+                p.sum_ld, outs * p.sum_ld, (int)p.splits, static_cast<T*>(dw), stride, outs, cols, accumulate);
+}
+
+}  // namespace
+}  // namespace muon
+
+using namespace muon;
+
+extern "C" {
+
+muon_status muon_weight_grad_workspace_bytes(const muon_checkpoint* checkpoint, const void* dy, int64_t dy_stride,
+                                             int32_t dy_dtype, int64_t outs, size_t* bytes) {
+  if (!bytes) return invalid("bytes is NULL");
+  const int32_t st = check_grad_args(checkpoint, dy, dy_stride, dy_dtype, outs);
+  if (st != MUON_OK) return st;
+  *bytes = plan_of(checkpoint->rows, checkpoint->cols, outs, dy, dy_stride ? dy_stride : outs, dy_dtype).bytes;
+  return MUON_OK;
+}
+
+muon_status muon_checkpoint_weight_grad(const muon_checkpoint* checkpoint, const void* dy, int64_t dy_stride,
+                                        int32_t dy_dtype, int64_t outs, void* dw, int64_t dw_stride, int32_t dw_dtype,
+                                        int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream) {
+  int32_t st = check_grad_args(checkpoint, dy, dy_stride, dy_dtype, outs);
+  if (st != MUON_OK) return st;
+  const int64_t rows = checkpoint->rows, cols = checkpoint->cols;
+  if (rows > 0 && (!checkpoint->data || !aligned(checkpoint->data, 16)))
+    return invalid("checkpoint data is NULL or not 16-byte aligned");
+  if (rows > 0 && !dy) return invalid("dy is NULL");
+  if (dw_dtype != MUON_DTYPE_F32 && dw_dtype != MUON_DTYPE_BF16) return invalid("unknown dtype of dw");
+  if (!dw || !aligned(dw, dw_dtype == MUON_DTYPE_BF16 ? 2 : 4)) return invalid("dw is NULL or not aligned to its type");
+  if (dw_stride != 0 && (dw_stride < cols || dw_stride > (1ll << 36))) return invalid("dw_stride must be 0 or at least cols");
+  if (accumulate != 0 && accumulate != 1) return invalid("accumulate must be 0 or 1");
+  const int64_t stride = dy_stride ? dy_stride : outs;
+  const GradPlan p = plan_of(rows, cols, outs, dy, stride, dy_dtype);
+  if (p.tiles_m * p.tiles_n * p.splits > (1ll << 31) - 1) return set_error(MUON_ERR_UNSUPPORTED, "more than 2^31 tiles");
+  if ((int64_t)(p.parts > 1 ? p.parts : 1) * p.steps > (1ll << 31) - 1) return set_error(MUON_ERR_UNSUPPORTED, "too many tokens");
+  if (p.bytes > 0 && (st = check_workspace(workspace, workspace_bytes, p.bytes)) != MUON_OK) return st;
+  int sms;
+  if ((st = find_device(&sms)) != MUON_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  const bool bf16_out = dw_dtype == MUON_DTYPE_BF16;
+  const int64_t out_stride = dw_stride ? dw_stride : cols;
+  if (rows == 0) {
+    if (accumulate) return MUON_OK;
+    const int grid = grid_of(outs * cols, kJoinThreads, sms);
+    e = bf16_out ? launch(zero_kernel<__nv_bfloat16>, grid, kJoinThreads, 0, s, 1, false, static_cast<__nv_bfloat16*>(dw), out_stride, outs, cols)
+                 : launch(zero_kernel<float>, grid, kJoinThreads, 0, s, 1, false, static_cast<float*>(dw), out_stride, outs, cols);
+    return e == cudaSuccess ? MUON_OK : cuda_error(e);
+  }
+  GradArgs a = {};
+  const void* operand = dy;
+  int64_t ld = stride, count = 1;
+  if (p.parts) {
+    __nv_bfloat16* parts = static_cast<__nv_bfloat16*>(workspace);
+    const int grid = grid_of(rows * (p.ld / 8), kPartThreads, sms);
+    e = dy_dtype == MUON_DTYPE_BF16
+            ? launch(parts_kernel<__nv_bfloat16>, grid, kPartThreads, 0, s, 1, false, static_cast<const __nv_bfloat16*>(dy), stride, rows, outs, p.ld, parts)
+            : launch(parts_kernel<float>, grid, kPartThreads, 0, s, 1, false, static_cast<const float*>(dy), stride, rows, outs, p.ld, parts);
+    if (e != cudaSuccess) return cuda_error(e);
+    operand = parts;
+    ld = p.ld;
+    count = p.parts;
+  }
+  const int64_t blocks = (cols + kBlockCols - 1) / kBlockCols;
+  if (!encode_tensor_map(&a.dy, const_cast<void*>(operand), 2, outs, rows, count, ld, 64, kTokens, true) ||
+      !encode_tensor_map(&a.q, checkpoint->data, 1, blocks * kBlockCols, rows, 1, blocks * kBlockCols, 128, kTokens, false))
+    return set_error(MUON_ERR_CUDA, "cuTensorMapEncodeTiled rejected a tensor map");
+  a.b = static_cast<const uint8_t*>(checkpoint->data) + rows * blocks * kBlockCols;
+  a.b_end = a.b + rows * blocks;
+  a.tokens = rows;
+  a.blocks = (int32_t)blocks;
+  a.cols = (int32_t)cols;
+  a.outs = (int32_t)outs;
+  a.parts = (int32_t)count;
+  a.steps = (int32_t)p.steps;
+  a.tiles_n = (int32_t)p.tiles_n;
+  a.tiles = (int32_t)(p.tiles_m * p.tiles_n);
+  a.splits = (int32_t)p.splits;
+  a.split_steps = (int32_t)p.split_steps;
+  float* sums = nullptr;
+  if (p.splits > 1) {
+    sums = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + p.parts_bytes);
+    a.out = sums;
+    a.stride = p.sum_ld;
+    a.split_stride = outs * p.sum_ld;
+  } else {
+    a.out = dw;
+    a.stride = out_stride;
+    a.bf16 = bf16_out;
+    a.accumulate = accumulate;
+  }
+  if ((e = cudaFuncSetAttribute(weight_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGradSmem)) != cudaSuccess)
+    return cuda_error(e);
+  const int64_t units = (int64_t)a.tiles * a.splits, pairs = sms / 2;
+  e = launch(weight_grad_kernel, (int)(2 * (units < pairs ? units : pairs)), kGradThreads, kGradSmem, s, 2, p.parts > 0, a);
+  if (e != cudaSuccess) return cuda_error(e);
+  if (p.splits > 1) {
+    e = bf16_out ? launch_join<__nv_bfloat16>(p, sums, dw, out_stride, outs, cols, accumulate, sms, s)
+                 : launch_join<float>(p, sums, dw, out_stride, outs, cols, accumulate, sms, s);
+    if (e != cudaSuccess) return cuda_error(e);
+  }
+  return MUON_OK;
+}
+
+}  // extern "C"

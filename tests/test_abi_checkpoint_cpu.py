@@ -77,3 +77,45 @@ def test_binding_refuses(nsm):
         nsm.Checkpoint(3, 5, torch.zeros(3 * 33, dtype=torch.uint8))
     with pytest.raises(ValueError, match="uint8"):
         nsm.Checkpoint(3, 5, torch.zeros(3 * 33))
+
+
+def _wg(nsm, ck=None, dy=A, dy_stride=0, dy_dtype=1, outs=64, dw=2 * A, dw_stride=0, dw_dtype=0, accumulate=0, ws=3 * A,
+        nbytes=1 << 40):
+    return nsm.lib.muon_checkpoint_weight_grad(ctypes.byref(ck or _ck(nsm)), dy, dy_stride, dy_dtype, outs, dw, dw_stride,
+                                               dw_dtype, accumulate, ws, nbytes, None)
+
+
+@pytest.mark.parametrize("over", [
+    dict(dy=None), dict(dy=A + 1), dict(dy=A + 2, dy_dtype=0), dict(dy_stride=63), dict(dy_stride=-1), dict(dy_dtype=2),
+    dict(outs=0), dict(outs=(1 << 30) + 1), dict(dw=None), dict(dw=A + 2), dict(dw=A + 1, dw_dtype=1), dict(dw_stride=99),
+    dict(dw_dtype=3), dict(accumulate=2)])
+def test_weight_grad_refuses(nsm, over):
+    assert _wg(nsm, **over) == nsm.MUON_ERR_INVALID
+
+
+@pytest.mark.parametrize("over", BAD)
+def test_weight_grad_refuses_bad_checkpoints(nsm, over):
+    assert _wg(nsm, _ck(nsm, **over)) == nsm.MUON_ERR_INVALID
+
+
+def test_weight_grad_workspace(nsm):
+    def need(rows, cols, outs, dtype, dy=A, stride=0):
+        v = ctypes.c_size_t()
+        st = nsm.lib.muon_weight_grad_workspace_bytes(ctypes.byref(_ck(nsm, A, rows, cols)), dy, stride, dtype, outs,
+                                                      ctypes.byref(v))
+        assert st == nsm.MUON_OK
+        return v.value
+
+    assert need(8192, 2560, 9728, 1) == 0                      # read as it lies, a tile a pair
+    assert need(8192, 2560, 9728, 1, dy=A + 2) >= 8192 * 9728 * 2
+    assert need(8192, 2560, 9728, 1, stride=9729) >= 8192 * 9728 * 2
+    assert need(8192, 2560, 9728, 0) >= 3 * 8192 * 9728 * 2
+    assert need(100000, 40, 40, 1) > 0                         # the sums of the parts
+    assert need(0, 40, 40, 1) == 0
+    short = _wg(nsm, dy_dtype=0, nbytes=10)
+    assert short == nsm.MUON_ERR_NO_WORKSPACE
+    assert _wg(nsm, dy_dtype=0, ws=None) == nsm.MUON_ERR_NO_WORKSPACE
+    assert _wg(nsm, dy_dtype=0, ws=A + 8) == nsm.MUON_ERR_INVALID
+    v = ctypes.c_size_t()
+    assert nsm.lib.muon_weight_grad_workspace_bytes(None, A, 0, 1, 64, ctypes.byref(v)) == nsm.MUON_ERR_INVALID
+    assert nsm.lib.muon_weight_grad_workspace_bytes(ctypes.byref(_ck(nsm)), A, 0, 1, 64, None) == nsm.MUON_ERR_INVALID

@@ -219,3 +219,165 @@ def test_streams(m):
     got = m.muon_checkpoint_load(ck, stream=stream.cuda_stream)
     stream.synchronize()
     assert torch.equal(got, want)
+
+
+def _check_weight(got, dy, x, steps, parts, dtype, base=None):
+    """|error| <= (steps + 4) 2^-23 sum |dy| |x| (parts times), the type's rounding, and the sum with dw's values."""
+    want = dy.T @ x
+    terms = np.abs(dy).T @ np.abs(x)
+    if base is not None:
+        want = want + base
+        terms = terms + np.abs(base)
+    tol = (parts * steps + 4) * 2.0 ** -23 * terms + HALF[dtype] * np.abs(want) + TINY
+    err = np.abs(_f64(got) - want)
+    assert (err <= tol).all(), (err - tol).max()
+
+
+GRADS = [(1, 1, 1, 0, 0), (1, 300, 40, 0, 0), (5, 40, 300, 0, 0), (63, 129, 65, 0, 0), (64, 256, 256, 0, 0), (65, 257, 255, 3, 1),
+         (200, 8, 1000, 8, 8), (1000, 512, 128, 0, 0), (1024, 8, 8, 0, 0), (777, 300, 700, 5, 0), (300, 2000, 1537, 0, 2),
+         (4099, 264, 33, 0, 0), (130, 5000, 4999, 0, 0)]
+
+
+@pytest.mark.parametrize("dtype,out", [("bfloat16", "float32"), ("bfloat16", "bfloat16"), ("float32", "float32")])
+@pytest.mark.parametrize("rows,outs,cols,pad,lead", GRADS)
+def test_weight_grad(m, rows, outs, cols, pad, lead, dtype, out):
+    import torch
+    rng = np.random.default_rng([rows, outs, cols])
+    x, v = _matrix(rng, rows, cols)
+    dy, vd = _matrix(rng, rows, outs, dtype, pad, lead, 0.1)
+    ck = m.muon_checkpoint_save(x)
+    saved = checkpoint.values(v)
+    steps, parts = -(-rows // 16), 3 if dtype == "float32" else 1
+    dw, base = _matrix(rng, outs, cols, out, pad, lead)
+    got = m.muon_checkpoint_weight_grad(ck, dy, out=dw)
+    assert got is dw
+    _check_weight(dw, vd, saved, steps, parts, out)
+    flat = (dw._base if dw._base is not None else dw).reshape(-1)   # the memory around the rows is as it was
+    assert (flat[:lead] == 300).all() and (flat[lead + outs * (cols + pad):] == 300).all()
+    if pad:
+        assert (flat[lead:lead + outs * (cols + pad)].view(outs, cols + pad)[:, cols:] == 300).all()
+    dw2, base = _matrix(rng, outs, cols, out, pad, lead)
+    m.muon_checkpoint_weight_grad(ck, dy, out=dw2, accumulate=True)
+    _check_weight(dw2, vd, saved, steps, parts, out, base)
+    again = m.muon_checkpoint_weight_grad(ck, dy, dtype=getattr(torch, out))
+    assert torch.equal(again, dw)
+
+
+def test_weight_grad_every_tile(m):
+    """More tiles than pairs of SMs, and sums divided among pairs."""
+    for rows, outs, cols in ((40, 2600, 5200), (5000, 600, 600)):
+        rng = np.random.default_rng(rows)
+        x, v = _matrix(rng, rows, cols, "bfloat16")
+        dy, vd = _matrix(rng, rows, outs, "bfloat16")
+        ck = m.muon_checkpoint_save(x)
+        import torch
+        got = m.muon_checkpoint_weight_grad(ck, dy, dtype=torch.float32)
+        _check_weight(got, vd, checkpoint.values(v), -(-rows // 16), 1, "float32")
+
+
+def test_weight_grad_fp32_keeps_all_bits(m):
+    """One token: each element is a product of an fp32 and a bf16 number, whose sum of three parts rounds twice."""
+    import torch
+    rng = np.random.default_rng(6)
+    x, v = _matrix(rng, 1, 64)
+    dy, vd = _matrix(rng, 1, 100, scale=1e3)
+    dy[0, 0] = torch.finfo(torch.float32).max
+    dy[0, 1] = -torch.finfo(torch.float32).max
+    x[0, :32] = 0.5
+    vd, v = _f64(dy), _f64(x)
+    got = _f64(m.muon_checkpoint_weight_grad(m.muon_checkpoint_save(x), dy))
+    want = vd.T @ checkpoint.values(v)
+    fits = np.abs(want) < 3e38
+    assert (np.abs(got - want)[fits] <= 3 * 2.0 ** -24 * np.abs(want)[fits]).all()
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_weight_grad_not_finite(m, dtype):
+    import torch
+    rng = np.random.default_rng(7)
+    x, v = _matrix(rng, 100, 96, dtype)
+    dy, vd = _matrix(rng, 100, 40, dtype)
+    x[70, 40] = float("inf")
+    dy[99, 3] = float("nan")
+    dy[98, 5] = float("inf")
+    got = m.muon_checkpoint_weight_grad(m.muon_checkpoint_save(x), dy, dtype=torch.float32)
+    assert got[:, 32:64].isnan().all() and got[3].isnan().all()
+    assert not got[5, :32].isfinite().any()
+    keep = [i for i in range(40) if i not in (3, 5)]
+    assert got[keep][:, :32].isfinite().all() and got[keep][:, 64:].isfinite().all()
+
+
+def test_weight_grad_of_no_tokens(m):
+    import torch
+    ck = m.muon_checkpoint_save(torch.zeros(0, 37, device="cuda"))
+    dy = torch.zeros(0, 11, device="cuda", dtype=torch.bfloat16)
+    assert (m.muon_checkpoint_weight_grad(ck, dy, dtype=torch.float32) == 0).all()
+    dw = torch.full((11, 37), 5.0, device="cuda")
+    m.muon_checkpoint_weight_grad(ck, dy, out=dw, accumulate=True)
+    assert (dw == 5).all()
+
+
+def test_weight_grad_graph_and_streams(m):
+    """Two captured graphs, an eager call and another stream, none of which share a workspace."""
+    import torch
+    rng = np.random.default_rng(8)
+    sets = []
+    for k in range(2):
+        x, _ = _matrix(rng, 900, 300)
+        dy, _ = _matrix(rng, 900, 200)
+        sets.append((m.muon_checkpoint_save(x), dy))
+    want = [m.muon_checkpoint_weight_grad(*s) for s in sets]
+    graphs, outs = [], []
+    for s in sets:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(m.muon_checkpoint_weight_grad(*s))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        eager = m.muon_checkpoint_weight_grad(*sets[0])
+        side = m.muon_checkpoint_weight_grad(*sets[1], stream=streams[0])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs + [eager, side], want + want))
+
+
+def test_layer_backward_matches_autograd(m):
+    """A gated layer's weight gradients through the checkpoints, clipped and stepped on, against
+    float64 gradients of the same layer on the saved values."""
+    import torch
+    gen = torch.Generator("cuda").manual_seed(9)
+    T, inputs, hidden = 500, 96, 160
+    x = torch.randn(T, inputs, generator=gen, device="cuda").bfloat16()
+    weights = [torch.randn(hidden, inputs, generator=gen, device="cuda") * 0.1 for _ in range(2)]
+    weights.append(torch.randn(inputs, hidden, generator=gen, device="cuda") * 0.1)
+    gate, up = (x @ w.bfloat16().t() for w in weights[:2])
+    saved_x = m.muon_checkpoint_save(x)
+    h, cg, cu = m.muon_swiglu_forward(gate, up)
+    dy = torch.randn(T, inputs, generator=gen, device="cuda").bfloat16()
+    dh = dy @ weights[2].bfloat16()
+    dgate, dup, again = m.muon_swiglu_backward(dh, cg, cu, with_h=True)
+    saved_h = m.muon_checkpoint_save(again)
+    grads = [m.muon_checkpoint_weight_grad(saved_x, dgate, dtype=torch.float32),
+             m.muon_checkpoint_weight_grad(saved_x, dup, dtype=torch.float32),
+             m.muon_checkpoint_weight_grad(saved_h, dy, dtype=torch.float32)]
+    # in 64 bits: autograd through the activation on the loaded values, products by torch
+    lx, lh = m.muon_checkpoint_load(saved_x).double(), m.muon_checkpoint_load(saved_h).double()
+    g, u = (m.muon_checkpoint_load(c).double().requires_grad_() for c in (cg, cu))
+    (torch.nn.functional.silu(g) * u).backward(dh.double())
+    for got, d, v, exact in zip(grads, (dgate, dup, dy), (lx, lx, lh), (g.grad, u.grad, dy.double())):
+        assert (d.double() - exact).abs().max() <= 2.0 ** -7 * exact.abs().max()
+        _check_weight(got, _f64(d), v.detach().cpu().numpy(), -(-T // 16), 1, "float32")
+    norm = m.muon_clip_grad_norm(grads, 1.0)
+    total = sum((t.double() ** 2).sum() for t in grads).sqrt()
+    assert abs(total.item() - 1) < 1e-4 and norm[0] > 1
+    plan = m.muon_plan([tuple(w.shape) for w in weights], config=m.muon_config_default(grad_dtype=m.MUON_DTYPE_F32))
+    m.allocate_workspace(plan)
+    before = [w.clone() for w in weights]
+    m.muon_step(plan, weights, grads, [torch.zeros_like(w) for w in weights], 0.02, 0.9, True, 0.0)
+    status, nonfinite = m.muon_sync(plan)
+    assert status == m.MUON_OK and nonfinite == 0
+    assert all((a - b).abs().max() > 0 for a, b in zip(before, weights))
