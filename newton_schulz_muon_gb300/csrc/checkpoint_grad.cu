@@ -37,6 +37,7 @@
 #include "launch.cuh"
 #include "muon.h"
 #include "rows.cuh"
+#include "tensor_map.h"
 
 namespace muon {
 namespace {

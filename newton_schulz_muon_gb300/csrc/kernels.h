@@ -219,11 +219,6 @@ cudaError_t launch_ns_small(const SmallArgs& a, int num_sms, cudaStream_t s);
 cudaError_t launch_ns_gram(const SmallArgs& a, int num_sms, cudaStream_t s);
 constexpr int kSmallMaxRows = 128;
 
-// Tensor map of a [count][rows][ld] array of `esize`-byte elements (1: bytes, 2: bf16, 4: fp32),
-// logical (cols, rows, count), box_x x box_y x 1, with the 128-byte swizzle or none.
-bool encode_tensor_map(CUtensorMap* map, void* base, size_t esize, int64_t cols, int64_t rows, int64_t count, int64_t ld,
-                       uint32_t box_x, uint32_t box_y, bool swizzle);
-
 // Records `msg` as the calling thread's muon_last_error text and returns `s`.
 int32_t set_error(int32_t s, const char* msg);
 

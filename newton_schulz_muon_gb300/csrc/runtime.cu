@@ -38,6 +38,7 @@
 
 #include "kernels.h"
 #include "muon.h"
+#include "tensor_map.h"
 
 using namespace muon;
 
