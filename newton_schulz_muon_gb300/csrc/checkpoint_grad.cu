@@ -13,9 +13,13 @@
 //   0      TMA producer of dy's stages (bf16, 128-byte swizzle), onto the leader's barrier
 //   1      tcgen05.mma issuer (the leader's)
 //   2      producer of the raw ring: x's bytes by TMA, the blocks' exponents by cp.async
-//   4-7    epilogue: TMEM to registers to dW, while the next tile is summed into the other
-//          accumulator
-//   8-15   converters: raw bytes and exponents to bf16 in the swizzled operand stage
+//   4-11   sums: TMEM to fp32 registers and, after a tile's last stage, to dW
+//   12-19  converters, in two groups that take stages in turn: raw bytes and exponents to
+//          bf16 in the swizzled operand stage
+// The tensor cores cut off what an accumulation cannot hold, always towards zero: 512 of them
+// (8192 tokens) leave dW 5e-6 off in the mean.  So an accumulator takes kChunkSteps stages only
+// (64 accumulations), and is then added to registers, rounding to nearest, while the next
+// stages are summed into the other accumulator: 5e-7.
 // A value q 2^(b - 133) is made by bit operations on pairs: with the byte q beside 0x43, the
 // two bf16 numbers 128 + (q mod 128) and 128 or 256 by q's sign differ by q; one product with the step follows.
 // All three are exact.
@@ -44,15 +48,20 @@ namespace {
 
 constexpr int kTile = 256;          // rows and columns of a tile of dW
 constexpr int kTokens = 64;         // tokens of a stage
-constexpr int kGradThreads = 512;
-constexpr int kGradStages = 6, kRawStages = 3;
+constexpr int kGradThreads = 640;
+constexpr int kGradStages = 5, kRawStages = 6;
+constexpr int kChunkSteps = 16;     // stages that one accumulator takes
 constexpr uint32_t kChunk = kTokens * 128;          // 64 tokens of 64 bf16 columns
 constexpr uint32_t kOperand = 2 * kChunk;           // a CTA's half of an operand
 constexpr uint32_t kRawBytes = kTokens * 128, kRawExps = kTokens * 8;
 constexpr uint32_t kRaw = kRawBytes + kRawExps;
 constexpr size_t kGradSmem = kGradStages * 2 * kOperand + kRawStages * kRaw + 1024;
 static_assert(kGradSmem <= 232448 - 1024, "shared memory of one CTA");
-constexpr int kConverters = 8, kEpilogue = 4;       // warps
+constexpr int kGroups = 2, kConverters = 4;         // groups of converter warps, warps of one
+constexpr int kSummers = 8;                         // warps
+// Registers of a thread: the launch's, and what setmaxnreg makes of them.
+constexpr int kGradRegs = 96, kSummerRegs = 176, kOtherRegs = 40;
+static_assert(2 * kSummerRegs + 3 * kOtherRegs <= 5 * kGradRegs, "the launch's registers");
 constexpr uint32_t kGradTmem = 512;
 
 struct GradArgs {
@@ -123,6 +132,31 @@ __device__ __forceinline__ uint32_t convert2(uint32_t w, uint32_t step) {
   return mul_bf16x2(sub_bf16x2(w & 0xFF7FFF7Fu, w & 0xFF80FF80u), step);
 }
 
+// The calling warpgroup's registers a thread.  The increases draw on what the decreases of
+// this CTA's other warpgroups give back.
+template <int kRegs>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+// Adds 32 lanes x 16 consecutive columns of Tensor Memory to the lanes' registers.
+__device__ __forceinline__ void tmem_add16(uint32_t taddr, float (&v)[128], int at) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int j = 0; j < 16; ++j) v[at + j] += __uint_as_float(r[j]);
+}
+
 struct Unit {
   int m0, n0, split, kb0, kb1;
 };
@@ -137,43 +171,43 @@ __device__ __forceinline__ Unit unit_of(const GradArgs& a, int u) {
   return r;
 }
 
-// 32 consecutive columns of a row of dW.
-__device__ __forceinline__ void store_row(const GradArgs& a, int split, int64_t row, int col, const float (&v)[32]) {
-  const int n = min(32, a.cols - col);
-  const int64_t at = split * a.split_stride + row * a.stride + col;
+// 16 consecutive columns of a row of dW, s[at ..]; poison, 0 or NaN, is added.
+__device__ __forceinline__ void store_row(const GradArgs& a, int split, int64_t row, int col, const float (&s)[128], int at,
+                                          float poison) {
+  const int n = min(16, a.cols - col);
+  const int64_t e = split * a.split_stride + row * a.stride + col;
   if (a.bf16) {
-    __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(a.out) + at;
-    if (n == 32 && (reinterpret_cast<uint64_t>(p) & 15) == 0) {
+    __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(a.out) + e;
+    if (n == 16 && (reinterpret_cast<uint64_t>(p) & 15) == 0) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float x[8];
+      for (int k = 0; k < 2; ++k) {
+        float x[8] = {};
         if (a.accumulate) Vec<__nv_bfloat16>::unpack(reinterpret_cast<const uint4*>(p)[k], x);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = a.accumulate ? x[i] + v[8 * k + i] : v[8 * k + i];
+        for (int i = 0; i < 8; ++i) x[i] += s[at + 8 * k + i] + poison;
         reinterpret_cast<uint4*>(p)[k] = Vec<__nv_bfloat16>::pack(x);
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (i < n) p[i] = __float2bfloat16_rn(a.accumulate ? __bfloat162float(p[i]) + v[i] : v[i]);
+      for (int i = 0; i < 16; ++i)
+        if (i < n) p[i] = __float2bfloat16_rn((a.accumulate ? __bfloat162float(p[i]) : 0.f) + (s[at + i] + poison));
     }
     return;
   }
-  float* p = reinterpret_cast<float*>(a.out) + at;
-  if (n == 32 && (reinterpret_cast<uint64_t>(p) & 15) == 0) {
+  float* p = reinterpret_cast<float*>(a.out) + e;
+  if (n == 16 && (reinterpret_cast<uint64_t>(p) & 15) == 0) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      float4 x = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-      if (a.accumulate) {
-        const float4 y = reinterpret_cast<const float4*>(p)[k];
-        x = make_float4(y.x + x.x, y.y + x.y, y.z + x.z, y.w + x.w);
-      }
-      reinterpret_cast<float4*>(p)[k] = x;
+    for (int k = 0; k < 4; ++k) {
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (a.accumulate) x = reinterpret_cast<const float4*>(p)[k];
+      const float* v = s + at + 4 * k;
+      reinterpret_cast<float4*>(p)[k] =
+          make_float4(x.x + (v[0] + poison), x.y + (v[1] + poison), x.z + (v[2] + poison), x.w + (v[3] + poison));
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (i < n) p[i] = a.accumulate ? p[i] + v[i] : v[i];
+    for (int i = 0; i < 16; ++i)
+      if (i < n) p[i] = (a.accumulate ? p[i] : 0.f) + (s[at + i] + poison);
   }
 }
 
@@ -194,16 +228,16 @@ __global__ void __launch_bounds__(kGradThreads, 1) weight_grad_kernel(const __gr
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kGradStages; ++s) {
-      mbar_init(&full_bar[s], 1 + 2 * kConverters);  // dy's bytes of both CTAs; the converter warps of both
+      mbar_init(&full_bar[s], 1 + 2 * kConverters);  // dy's bytes of both CTAs; a group's warps of both
       mbar_init(&empty_bar[s], 1);
     }
     for (int s = 0; s < kRawStages; ++s) {
       mbar_init(&raw_full[s], 1 + 32);  // x's bytes; the exponents of each lane
-      mbar_init(&raw_empty[s], kConverters);
+      mbar_init(&raw_empty[s], kConverters);  // of one group
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull_bar[i], 1);
-      mbar_init(&tempty_bar[i], 2 * kEpilogue);
+      mbar_init(&tempty_bar[i], 2 * kSummers);
     }
     mbar_init(&drain_bar, 1);
     abort_flag = 0;
@@ -223,6 +257,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) weight_grad_kernel(const __gr
   griddep_wait();
   const uint32_t tmem = tmem_slot;
 
+  if (warp < 4) {
+  reg_dec<kOtherRegs>();
   if (warp == 0) {
     // ---- dy ----
     int stage = 0;
@@ -237,7 +273,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) weight_grad_kernel(const __gr
           uint8_t* sa = smem + (size_t)stage * 2 * kOperand;
           if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2 * kOperand);
           const uint32_t bar = mapa_shared(&full_bar[stage], 0);
-          const int part = kb / a.steps, t0 = (kb - part * a.steps) * kTokens;
+          const int pass = kb / a.steps, t0 = (kb - pass * a.steps) * kTokens;
+          const int part = a.parts - 1 - pass;  // the smallest first
 #pragma unroll
           for (int h = 0; h < 2; ++h)
             tma_load_3d_pair(sa + h * kChunk, &a.dy, bar, t.m0 + rank * 128 + h * 64, t0, part);
@@ -261,30 +298,33 @@ __global__ void __launch_bounds__(kGradThreads, 1) weight_grad_kernel(const __gr
       bool ok = true;
       for (int u = pair; u < units && ok; u += pairs) {
         const Unit t = unit_of(a, u);
-        const bool free_acc = mbar_wait(&tempty_bar[acc], acc_phase ^ 1u, abort_p, nullptr);
-        if (!__all_sync(0xffffffffu, free_acc)) break;
-        tc_fence_after();
-        const uint32_t d = tmem + (uint32_t)(acc * kTile);
-        for (int kb = t.kb0; kb < t.kb1; ++kb) {
-          const bool got = mbar_wait_cluster(&full_bar[stage], phase, abort_p);
-          if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+        for (int c0 = t.kb0; c0 < t.kb1; c0 += kChunkSteps) {
+          const int c1 = min(c0 + kChunkSteps, t.kb1);
+          const bool free_acc = mbar_wait(&tempty_bar[acc], acc_phase ^ 1u, abort_p, nullptr);
+          if (!__all_sync(0xffffffffu, free_acc)) { ok = false; break; }
           tc_fence_after();
-          if (lane == 0) {
-            const uint32_t sa = smem_u32(smem + (size_t)stage * 2 * kOperand), sb = sa + kOperand;
+          const uint32_t d = tmem + (uint32_t)(acc * kTile);
+          for (int kb = c0; kb < c1; ++kb) {
+            const bool got = mbar_wait_cluster(&full_bar[stage], phase, abort_p);
+            if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+            tc_fence_after();
+            if (lane == 0) {
+              const uint32_t sa = smem_u32(smem + (size_t)stage * 2 * kOperand), sb = sa + kOperand;
 #pragma unroll
-            for (int kk = 0; kk < kTokens / 16; ++kk)
-              mma<false, 2>(d, smem_desc_sw128(sa + kk * 16 * 128, kChunk, 1024),
-                            smem_desc_sw128(sb + kk * 16 * 128, kChunk, 1024), idesc, (kb > t.kb0 || kk > 0) ? 1u : 0u);
-            mma_commit_multicast<2>(&empty_bar[stage], 3);
+              for (int kk = 0; kk < kTokens / 16; ++kk)
+                mma<false, 2>(d, smem_desc_sw128(sa + kk * 16 * 128, kChunk, 1024),
+                              smem_desc_sw128(sb + kk * 16 * 128, kChunk, 1024), idesc, (kb > c0 || kk > 0) ? 1u : 0u);
+              mma_commit_multicast<2>(&empty_bar[stage], 3);
+            }
+            __syncwarp();
+            if (++stage == kGradStages) { stage = 0; phase ^= 1u; }
           }
+          if (!ok) break;
+          if (lane == 0) mma_commit_multicast<2>(&tfull_bar[acc], 3);
           __syncwarp();
-          if (++stage == kGradStages) { stage = 0; phase ^= 1u; }
+          acc ^= 1;
+          if (acc == 0) acc_phase ^= 1u;
         }
-        if (!ok) break;
-        if (lane == 0) mma_commit_multicast<2>(&tfull_bar[acc], 3);
-        __syncwarp();
-        acc ^= 1;
-        if (acc == 0) acc_phase ^= 1u;
       }
       if (lane == 0) {  // every MMA has completed before TMEM is freed
         mma_commit<2>(&drain_bar);
@@ -332,25 +372,29 @@ __global__ void __launch_bounds__(kGradThreads, 1) weight_grad_kernel(const __gr
         (void)mbar_wait(&raw_full[s], phase ^ (s < stage ? 0u : 1u), nullptr, nullptr, 100000000ull);
     }
     __syncwarp();
-  } else if (warp >= 8) {
+  }
+  } else if (warp >= 12) {
+    reg_dec<kOtherRegs>();
     // ---- bytes to bf16 ----
-    const int i = threadIdx.x - 256, unit = i & 15;  // 8 columns of tokens i / 16 + 16 k
-    int stage = 0, rs = 0;
-    uint32_t phase = 0, rphase = 0;
+    const int group = (warp - 12) / kConverters;
+    const int i = threadIdx.x - (12 + group * kConverters) * 32, unit = i & 15;  // 8 columns of tokens i / 16 + 8 k
+    int count = 0;  // stages so far, of both groups
     bool ok = true;
     const uint32_t lead = mapa_shared(&full_bar[0], 0);
     for (int u = pair; u < units && ok; u += pairs) {
       const Unit t = unit_of(a, u);
-      for (int kb = t.kb0; kb < t.kb1; ++kb) {
-        const bool got = mbar_wait(&raw_full[rs], rphase, abort_p, nullptr) &&
-                         mbar_wait(&empty_bar[stage], phase ^ 1u, abort_p, nullptr);
+      for (int kb = t.kb0; kb < t.kb1; ++kb, ++count) {
+        if (count % kGroups != group) continue;
+        const int stage = count % kGradStages, rs = count % kRawStages;
+        const bool got = mbar_wait(&raw_full[rs], (uint32_t)(count / kRawStages) & 1u, abort_p, nullptr) &&
+                         mbar_wait(&empty_bar[stage], ((uint32_t)(count / kGradStages) & 1u) ^ 1u, abort_p, nullptr);
         if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
         const uint8_t* r = raw + (size_t)rs * kRaw;
         uint8_t* sb = smem + (size_t)stage * 2 * kOperand + kOperand + (unit >> 3) * kChunk;
         const int t0 = kb % a.steps * kTokens;
-#pragma unroll
-        for (int k = 0; k < kTokens / 16; ++k) {
-          const int tok = (i >> 4) + 16 * k;
+#pragma unroll 4
+        for (int k = 0; k < kTokens / 8; ++k) {
+          const int tok = (i >> 4) + 8 * k;
           const uint2 q = *reinterpret_cast<const uint2*>(r + tok * 128 + unit * 8);
           const int b = r[kRawBytes + tok * 8 + (int)(((uint32_t)(t0 + tok) * (uint32_t)a.blocks) & 3u) + (unit >> 2)];
           const uint32_t bits = b == 255 ? 0x7FC0u : (uint32_t)max(b - 6, 0) << 7;
@@ -368,39 +412,43 @@ __global__ void __launch_bounds__(kGradThreads, 1) weight_grad_kernel(const __gr
           mbar_arrive_cluster(lead + stage * 8);
           mbar_arrive(&raw_empty[rs]);
         }
-        if (++stage == kGradStages) { stage = 0; phase ^= 1u; }
-        if (++rs == kRawStages) { rs = 0; rphase ^= 1u; }
       }
     }
-  } else if (warp >= 4) {
-    // ---- epilogue ----
-    const int quad = warp & 3;
-    const uint32_t lead[2] = {mapa_shared(&tempty_bar[0], 0), mapa_shared(&tempty_bar[1], 0)};
+  } else {
+    reg_inc<kSummerRegs>();
+    // ---- sums ----
+    const int quad = warp & 3, half = (warp - 4) >> 2;
+    const uint32_t lead = mapa_shared(&tempty_bar[0], 0);
+    const uint32_t from = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(half * (kTile / 2));
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int u = pair; u < units; u += pairs) {
       const Unit t = unit_of(a, u);
-      const bool got = mbar_wait(&tfull_bar[acc], acc_phase, abort_p, nullptr);
-      const bool ok = __all_sync(0xffffffffu, got);
-      tc_fence_after();
-      const int64_t row = (int64_t)t.m0 + rank * 128 + quad * 32 + lane;
-#pragma unroll 1
-      for (int c = 0; c < kTile / 32; ++c) {
-        if (t.n0 + c * 32 >= a.cols) break;
-        float v[32];
-        if (ok) {
-          tmem_ld_32x32b_x32(tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(acc * kTile + c * 32), v);
-        } else {  // a wait ran out: no stale values pass for a gradient
+      float sum[128];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = NAN;
-        }
-        if (row < a.outs) store_row(a, t.split, row, t.n0 + c * 32, v);
+      for (int j = 0; j < 128; ++j) sum[j] = 0.f;
+      bool ok = true;
+      for (int c0 = t.kb0; c0 < t.kb1; c0 += kChunkSteps) {
+        const bool got = mbar_wait(&tfull_bar[acc], acc_phase, abort_p, nullptr);
+        ok = __all_sync(0xffffffffu, got) && ok;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 8; ++c) tmem_add16(from + (uint32_t)(acc * kTile + c * 16), sum, c * 16);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_relaxed(lead + acc * 8);
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster_relaxed(lead[acc]);
-      acc ^= 1;
-      if (acc == 0) acc_phase ^= 1u;
+      // where a wait ran out, no stale values pass for a gradient
+      const float poison = ok ? 0.f : NAN;
+      const int64_t row = (int64_t)t.m0 + rank * 128 + quad * 32 + lane;
+      const int col = t.n0 + half * (kTile / 2);
+      if (row < a.outs) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          if (col + 16 * c < a.cols) store_row(a, t.split, row, col + 16 * c, sum, 16 * c, poison);
+      }
     }
   }
   __syncwarp();
@@ -630,6 +678,9 @@ muon_status muon_checkpoint_weight_grad(const muon_checkpoint* checkpoint, const
     a.bf16 = bf16_out;
     a.accumulate = accumulate;
   }
+  cudaFuncAttributes attr;  // setmaxnreg would wait for ever for registers that the launch does not have
+  if ((e = cudaFuncGetAttributes(&attr, weight_grad_kernel)) != cudaSuccess) return cuda_error(e);
+  if (attr.numRegs < kGradRegs) return set_error(MUON_ERR_UNSUPPORTED, "the kernel was compiled for too few registers");
   if ((e = cudaFuncSetAttribute(weight_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGradSmem)) != cudaSuccess)
     return cuda_error(e);
   const int64_t units = (int64_t)a.tiles * a.splits, pairs = sms / 2;
