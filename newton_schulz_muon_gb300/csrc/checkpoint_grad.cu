@@ -12,7 +12,7 @@
 // and one 128-wide half of x.  A stage is 64 tokens.  Warps of a CTA:
 //   0      TMA producer of dy's stages (bf16, 128-byte swizzle), onto the leader's barrier
 //   1      tcgen05.mma issuer (the leader's)
-//   2      producer of the raw ring: x's bytes by TMA, the blocks' exponents by cp.async
+//   2, 3   producers of the raw ring: x's bytes by TMA, the blocks' exponents by cp.async
 //   4-11   sums: TMEM to fp32 registers and, after a tile's last stage, to dW
 //   12-19  converters, in two groups that take stages in turn: raw bytes and exponents to
 //          bf16 in the swizzled operand stage
@@ -60,8 +60,8 @@ static_assert(kGradSmem <= 232448 - 1024, "shared memory of one CTA");
 constexpr int kGroups = 2, kConverters = 4;         // groups of converter warps, warps of one
 constexpr int kSummers = 8;                         // warps
 // Registers of a thread: the launch's, and what setmaxnreg makes of them.
-constexpr int kGradRegs = 96, kSummerRegs = 176, kOtherRegs = 40;
-static_assert(2 * kSummerRegs + 3 * kOtherRegs <= 5 * kGradRegs, "the launch's registers");
+constexpr int kGradRegs = 96, kSummerRegs = 160, kOtherRegs = 48;
+static_assert(2 * kSummerRegs + (1 + kGroups) * kOtherRegs <= kGradThreads / 128 * kGradRegs, "the launch's registers");
 constexpr uint32_t kGradTmem = 512;
 
 struct GradArgs {
@@ -86,35 +86,12 @@ __device__ __forceinline__ void cp_async_4_part(void* dst, const void* src, int 
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-// An arrival on a barrier of either CTA that orders this thread's writes before it.
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-// mbar_wait for arrivals of both CTAs.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  if (mbar_try_wait_cluster(bar, parity)) return true;
-  const unsigned long long t0 = globaltimer_ns();
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    if ((i & 63u) == 0) {
-      if (*abort) return false;
-      if (globaltimer_ns() - t0 > kWaitLimitNs) {
-        *abort = 1;
-        return false;
-      }
-    }
-  }
+// An arrival on a barrier of either CTA, after this warp's writes to its own shared memory,
+// which fence.proxy.async has made visible to the tensor core that reads them, that of the
+// same SM.  (An arrival with release at cluster scope waits for more than those writes: 8192 x
+// 9728 x 2560 587 us with it, SCOPE_US without.)
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t x, uint32_t y) {
@@ -132,6 +109,15 @@ __device__ __forceinline__ uint32_t convert2(uint32_t w, uint32_t step) {
   return mul_bf16x2(sub_bf16x2(w & 0xFF7FFF7Fu, w & 0xFF80FF80u), step);
 }
 
+__device__ __forceinline__ uint4 convert8(uint2 q, uint32_t step) {
+  return make_uint4(convert2(__byte_perm(q.x, 0x43u, 0x4140), step), convert2(__byte_perm(q.x, 0x43u, 0x4342), step),
+                    convert2(__byte_perm(q.y, 0x43u, 0x4140), step), convert2(__byte_perm(q.y, 0x43u, 0x4342), step));
+}
+// 2^(b - 133) twice, NaN for 255.  (b = 0, past the last token, gives some number, for zeros.)
+__device__ __forceinline__ uint32_t step2(uint32_t b) {
+  return b == 255u ? 0x7FC07FC0u : b * 0x00800080u - 0x03000300u;
+}
+
 // The calling warpgroup's registers a thread.  The increases draw on what the decreases of
 // this CTA's other warpgroups give back.
 template <int kRegs>
@@ -143,18 +129,17 @@ __device__ __forceinline__ void reg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
-// Adds 32 lanes x 16 consecutive columns of Tensor Memory to the lanes' registers.
-__device__ __forceinline__ void tmem_add16(uint32_t taddr, float (&v)[128], int at) {
-  uint32_t r[16];
+// Adds 32 lanes x 8 consecutive columns of Tensor Memory to the lanes' registers.
+__device__ __forceinline__ void tmem_add8(uint32_t taddr, float (&v)[128], int at) {
+  uint32_t r[8];
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
       : "r"(taddr)
       : "memory");
 #pragma unroll
-  for (int j = 0; j < 16; ++j) v[at + j] += __uint_as_float(r[j]);
+  for (int j = 0; j < 8; ++j) v[at + j] += __uint_as_float(r[j]);
 }
 
 struct Unit {
@@ -305,7 +290,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) weight_grad_kernel(const __gr
           tc_fence_after();
           const uint32_t d = tmem + (uint32_t)(acc * kTile);
           for (int kb = c0; kb < c1; ++kb) {
-            const bool got = mbar_wait_cluster(&full_bar[stage], phase, abort_p);
+            const bool got = mbar_wait(&full_bar[stage], phase, abort_p, nullptr);
             if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
             tc_fence_after();
             if (lane == 0) {
@@ -333,51 +318,87 @@ __global__ void __launch_bounds__(kGradThreads, 1) weight_grad_kernel(const __gr
       __syncwarp();
     }
   } else if (warp == 2) {
-    // ---- x as it lies ----
+    // ---- x's bytes ----
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
     for (int u = pair; u < units && ok; u += pairs) {
       const Unit t = unit_of(a, u);
-      const int col0 = t.n0 + rank * 128, block0 = col0 / kBlockCols;
+      int step = t.kb0 % a.steps;
       for (int kb = t.kb0; kb < t.kb1; ++kb) {
         const bool got = mbar_wait(&raw_empty[stage], phase ^ 1u, abort_p, nullptr);
         if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
-        uint8_t* r = raw + (size_t)stage * kRaw;
-        const int t0 = kb % a.steps * kTokens;
         if (lane == 0) {
           mbar_arrive_expect_tx(&raw_full[stage], kRawBytes);
-          tma_load_3d(r, &a.q, &raw_full[stage], col0, t0, 0);
+          tma_load_3d(raw + (size_t)stage * kRaw, &a.q, &raw_full[stage], t.n0 + rank * 128, step * kTokens, 0);
         }
-        // the 4 exponents of each token, within the 8 bytes of two 4-byte words; zeros past
-        // the last token
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int i = h * 32 + lane;
-          const uint8_t* p = a.b + (int64_t)(t0 + i) * a.blocks + block0;
-          p -= reinterpret_cast<uint64_t>(p) & 3;
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            const int64_t left = t0 + i < a.tokens ? a.b_end - (p + 4 * w) : 0;
-            cp_async_4_part(r + kRawBytes + i * 8 + 4 * w, left > 0 ? p + 4 * w : a.b, (int)max((int64_t)0, min((int64_t)4, left)));
-          }
-        }
-        cp_async_arrive(&raw_full[stage]);
+        __syncwarp();
+        if (++step == a.steps) step = 0;
         if (++stage == kRawStages) { stage = 0; phase ^= 1u; }
       }
     }
-    cp_async_wait<0>();
     if (*abort_p && lane == 0) {
       for (int s = 0; s < kRawStages; ++s)
         (void)mbar_wait(&raw_full[s], phase ^ (s < stage ? 0u : 1u), nullptr, nullptr, 100000000ull);
     }
+    __syncwarp();
+  } else {
+    // ---- x's exponents: the 4 of each token, within the 8 bytes of two 4-byte words ----
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    const int64_t next = (int64_t)kTokens * a.blocks;  // a multiple of 4 bytes
+    for (int u = pair; u < units && ok; u += pairs) {
+      const Unit t = unit_of(a, u);
+      const int block0 = (t.n0 + rank * 128) / kBlockCols;
+      int step = t.kb0 % a.steps;
+      const uint8_t* p[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        p[h] = a.b + (int64_t)(step * kTokens + h * 32 + lane) * a.blocks + block0;
+        p[h] -= reinterpret_cast<uint64_t>(p[h]) & 3;
+      }
+      for (int kb = t.kb0; kb < t.kb1; ++kb) {
+        const bool got = mbar_wait(&raw_empty[stage], phase ^ 1u, abort_p, nullptr);
+        if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+        uint8_t* r = raw + (size_t)stage * kRaw + kRawBytes + lane * 8;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          // nothing past the last token's; zeros there
+          const int64_t left = step * kTokens + h * 32 + lane < a.tokens ? a.b_end - p[h] : 0;
+          if (left >= 8) {
+            cp_async_4(r + h * 256, p[h]);
+            cp_async_4(r + h * 256 + 4, p[h] + 4);
+          } else {
+            cp_async_4_part(r + h * 256, left > 0 ? p[h] : a.b, max((int)left, 0) < 4 ? max((int)left, 0) : 4);
+            cp_async_4_part(r + h * 256 + 4, left > 4 ? p[h] + 4 : a.b, max((int)left - 4, 0));
+          }
+          p[h] += next;
+        }
+        cp_async_arrive(&raw_full[stage]);
+        if (++step == a.steps) {
+          step = 0;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) p[h] -= a.steps * next;
+        }
+        if (++stage == kRawStages) { stage = 0; phase ^= 1u; }
+      }
+    }
+    cp_async_wait<0>();
     __syncwarp();
   }
   } else if (warp >= 12) {
     reg_dec<kOtherRegs>();
     // ---- bytes to bf16 ----
     const int group = (warp - 12) / kConverters;
-    const int i = threadIdx.x - (12 + group * kConverters) * 32, unit = i & 15;  // 8 columns of tokens i / 16 + 8 k
+    // A thread takes 8 columns in each half of tokens i / 8 + 16 k; odd tokens begin with the
+    // second half, so that 16 lanes read different banks.
+    const int i = threadIdx.x - (12 + group * kConverters) * 32, unit = i & 7, tok0 = i >> 3, odd = tok0 & 1;
+    const uint32_t q_at = tok0 * 128 + unit * 8 + odd * 64;
+    // the token's exponents begin (t blocks) mod 4 bytes into its 8; stages are multiples of 4 tokens
+    const uint32_t b_at = kRawBytes + tok0 * 8 + (((uint32_t)tok0 * (uint32_t)a.blocks) & 3u) + (unit >> 2) + odd * 2;
+    const uint32_t o_at = kOperand + tok0 * 128 + ((unit ^ (tok0 & 7)) << 4) + odd * kChunk;
+    const int q_other = 64 - 128 * odd, b_other = 2 - 4 * odd, o_other = (int)kChunk * (1 - 2 * odd);
     int count = 0;  // stages so far, of both groups
     bool ok = true;
     const uint32_t lead = mapa_shared(&full_bar[0], 0);
@@ -390,26 +411,19 @@ __global__ void __launch_bounds__(kGradThreads, 1) weight_grad_kernel(const __gr
                          mbar_wait(&empty_bar[stage], ((uint32_t)(count / kGradStages) & 1u) ^ 1u, abort_p, nullptr);
         if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
         const uint8_t* r = raw + (size_t)rs * kRaw;
-        uint8_t* sb = smem + (size_t)stage * 2 * kOperand + kOperand + (unit >> 3) * kChunk;
-        const int t0 = kb % a.steps * kTokens;
-#pragma unroll 4
-        for (int k = 0; k < kTokens / 8; ++k) {
-          const int tok = (i >> 4) + 8 * k;
-          const uint2 q = *reinterpret_cast<const uint2*>(r + tok * 128 + unit * 8);
-          const int b = r[kRawBytes + tok * 8 + (int)(((uint32_t)(t0 + tok) * (uint32_t)a.blocks) & 3u) + (unit >> 2)];
-          const uint32_t bits = b == 255 ? 0x7FC0u : (uint32_t)max(b - 6, 0) << 7;
-          const uint32_t step = bits | bits << 16;
-          uint4 o;
-          o.x = convert2(__byte_perm(q.x, 0x43u, 0x4140), step);
-          o.y = convert2(__byte_perm(q.x, 0x43u, 0x4342), step);
-          o.z = convert2(__byte_perm(q.y, 0x43u, 0x4140), step);
-          o.w = convert2(__byte_perm(q.y, 0x43u, 0x4342), step);
-          *reinterpret_cast<uint4*>(sb + tok * 128 + (((unit & 7) ^ (tok & 7)) << 4)) = o;
+        uint8_t* to = smem + (size_t)stage * 2 * kOperand + o_at;
+#pragma unroll
+        for (int k = 0; k < kTokens / 16; ++k) {
+          const uint8_t *q = r + q_at + k * 16 * 128, *b = r + b_at + k * 16 * 8;
+          const uint2 q0 = *reinterpret_cast<const uint2*>(q), q1 = *reinterpret_cast<const uint2*>(q + q_other);
+          const uint32_t s0 = step2(b[0]), s1 = step2(b[b_other]);
+          *reinterpret_cast<uint4*>(to + k * 16 * 128) = convert8(q0, s0);
+          *reinterpret_cast<uint4*>(to + k * 16 * 128 + o_other) = convert8(q1, s1);
         }
         fence_proxy_async_shared();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive_cluster(lead + stage * 8);
+          mbar_arrive_pair(lead + stage * 8);
           mbar_arrive(&raw_empty[rs]);
         }
       }
@@ -433,7 +447,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) weight_grad_kernel(const __gr
         ok = __all_sync(0xffffffffu, got) && ok;
         tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < 8; ++c) tmem_add16(from + (uint32_t)(acc * kTile + c * 16), sum, c * 16);
+        for (int c = 0; c < 16; ++c) tmem_add8(from + (uint32_t)(acc * kTile + c * 8), sum, c * 8);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster_relaxed(lead + acc * 8);
