@@ -15,6 +15,8 @@
 #include <stdint.h>
 
 #include "checkpoint.cuh"
+#include "checkpoint.h"
+#include "device.cuh"
 #include "kernels.h"
 #include "launch.cuh"
 #include "muon.h"
@@ -134,6 +136,7 @@ enum Pass { kSave, kLoad, kGatedForward, kGatedBackward };
 template <typename T, int kPass>
 __global__ void __launch_bounds__(kCheckpointThreads) checkpoint_kernel(const __grid_constant__ CheckpointArgs a) {
   constexpr int N = Vec<T>::N;
+  griddep_launch_dependents();
   const int64_t first = (int64_t)blockIdx.x * (kCheckpointThreads * kItems) + threadIdx.x;
   int64_t row;
   int unit;
@@ -252,27 +255,43 @@ CheckpointView view_of(const muon_checkpoint* c) {
   return v;
 }
 
+// The pass over a.a's rows; false: too many of them for a grid.
+template <int kPass>
+bool launch_pass(CheckpointArgs& a, int32_t dtype, cudaStream_t s, cudaError_t* e) {
+  const int n = dtype == MUON_DTYPE_BF16 ? 8 : 4;
+  a.per_row = a.a.blocks * (kBlockCols / n);
+  a.items = a.a.rows * a.per_row;
+  const int64_t per_cta = kCheckpointThreads * kItems, grid = (a.items + per_cta - 1) / per_cta;
+  if (grid > (1ll << 31) - 1) return false;
+  *e = dtype == MUON_DTYPE_BF16
+           ? launch(checkpoint_kernel<__nv_bfloat16, kPass>, (int)grid, kCheckpointThreads, 0, s, 1, false, a)
+           : launch(checkpoint_kernel<float, kPass>, (int)grid, kCheckpointThreads, 0, s, 1, false, a);
+  return true;
+}
+
 template <int kPass>
 int32_t run_checkpoint(CheckpointArgs& a, int32_t dtype, void* stream) {
   int sms;
   const int32_t st = find_device(&sms);
   if (st != MUON_OK) return st;
-  const int n = dtype == MUON_DTYPE_BF16 ? 8 : 4;
-  a.per_row = a.a.blocks * (kBlockCols / n);
-  a.items = a.a.rows * a.per_row;
-  const int64_t per_cta = kCheckpointThreads * kItems, grid = (a.items + per_cta - 1) / per_cta;
-  if (grid > (1ll << 31) - 1) return set_error(MUON_ERR_UNSUPPORTED, "more than 2^31 pieces of a checkpoint");
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e =
-      dtype == MUON_DTYPE_BF16
-          ? launch(checkpoint_kernel<__nv_bfloat16, kPass>, (int)grid, kCheckpointThreads, 0, s, 1, false, a)
-          : launch(checkpoint_kernel<float, kPass>, (int)grid, kCheckpointThreads, 0, s, 1, false, a);
+  cudaError_t e;
+  if (!launch_pass<kPass>(a, dtype, static_cast<cudaStream_t>(stream), &e))
+    return set_error(MUON_ERR_UNSUPPORTED, "more than 2^31 pieces of a checkpoint");
   return e == cudaSuccess ? MUON_OK : cuda_error(e);
 }
 
 bool known(int32_t dtype) { return dtype == MUON_DTYPE_F32 || dtype == MUON_DTYPE_BF16; }
 
 }  // namespace
+
+cudaError_t launch_checkpoint_load(const muon_checkpoint* checkpoint, void* x, int64_t ld, cudaStream_t stream) {
+  CheckpointArgs a = {};
+  a.a = view_of(checkpoint);
+  a.u = Matrix{x, ld};
+  cudaError_t e;
+  return launch_pass<kLoad>(a, MUON_DTYPE_BF16, stream, &e) ? e : cudaErrorInvalidConfiguration;
+}
+
 }  // namespace muon
 
 using namespace muon;

@@ -2,31 +2,29 @@
 //
 //   dW[o][i] = sum_t dy[t][o] x[t][i]     (+ dW)
 //
-// on the tcgen05 tensor cores.  A checkpoint's values are bf16 numbers, so the conversion
-// before the product loses nothing; products are exact in fp32 and sums are fp32.  Both
-// operands have the sum's index t outside (their rows are tokens) and are read MN-major as
-// they lie.
+// on the tcgen05 tensor cores.  A checkpoint's values are bf16 numbers, so that the tensor
+// cores take them as they are; products are exact in fp32 and sums are fp32.
 //
+// x is first loaded into the workspace in bf16, where L2 mostly keeps it.  (Converting it in the
+// product's own pipeline reads fewer bytes, but every 256 columns of dy convert all of x
+// again: 8192 x 9728 x 2560 took 327 us so, with 8 converter warps a CTA that its SM's issue
+// slots could not hold beside the rest; NOW_US as it is, of which the load is LOAD_US.)
+//
+// Both operands have the sum's index t outside (their rows are tokens) and are read MN-major.
 // A pair of CTAs on two SMs computes a 256 x 256 tile of dW with one
 // tcgen05.mma.cta_group::2 (M = N = 256); each CTA holds 128 rows of the tile (dy's columns)
 // and one 128-wide half of x.  A stage is 64 tokens.  Warps of a CTA:
-//   0      TMA producer of dy's stages (bf16, 128-byte swizzle), onto the leader's barrier
+//   0      TMA producer, onto the leader's barrier
 //   1      tcgen05.mma issuer (the leader's)
-//   2, 3   producers of the raw ring: x's bytes by TMA, the blocks' exponents by cp.async
 //   4-11   sums: TMEM to fp32 registers and, after a tile's last stage, to dW
-//   12-19  converters, in two groups that take stages in turn: raw bytes and exponents to
-//          bf16 in the swizzled operand stage
 // The tensor cores cut off what an accumulation cannot hold, always towards zero: 512 of them
 // (8192 tokens) leave dW 5e-6 off in the mean.  So an accumulator takes kChunkSteps stages only
 // (64 accumulations), and is then added to registers, rounding to nearest, while the next
-// stages are summed into the other accumulator: 5e-7.
-// A value q 2^(b - 133) is made by bit operations on pairs: with the byte q beside 0x43, the
-// two bf16 numbers 128 + (q mod 128) and 128 or 256 by q's sign differ by q; one product with the step follows.
-// All three are exact.
+// stages are summed into the other accumulator: 5.5e-7.
 //
 // fp32 gradients are split into three bf16 parts that add up to them exactly (8 bits of the
-// significand each) by a pass of its own, and the sum runs over the parts.  The same pass
-// copies bf16 gradients whose rows a TMA cannot read (16-byte boundaries).
+// significand each) by a pass of its own, and the sum runs over the parts, the smallest first.
+// The same pass copies bf16 gradients whose rows a TMA cannot read (16-byte boundaries).
 //
 // Where a matrix has too few tiles for the SMs, the tokens are divided among several pairs,
 // whose fp32 sums are added in a fixed order by a last pass.
@@ -35,7 +33,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include "checkpoint.cuh"
+#include "checkpoint.h"
 #include "device.cuh"
 #include "kernels.h"
 #include "launch.cuh"
@@ -48,86 +46,26 @@ namespace {
 
 constexpr int kTile = 256;          // rows and columns of a tile of dW
 constexpr int kTokens = 64;         // tokens of a stage
-constexpr int kGradThreads = 640;
-constexpr int kGradStages = 5, kRawStages = 6;
+constexpr int kGradThreads = 384;
+constexpr int kGradStages = 7;
 constexpr int kChunkSteps = 16;     // stages that one accumulator takes
 constexpr uint32_t kChunk = kTokens * 128;          // 64 tokens of 64 bf16 columns
 constexpr uint32_t kOperand = 2 * kChunk;           // a CTA's half of an operand
-constexpr uint32_t kRawBytes = kTokens * 128, kRawExps = kTokens * 8;
-constexpr uint32_t kRaw = kRawBytes + kRawExps;
-constexpr size_t kGradSmem = kGradStages * 2 * kOperand + kRawStages * kRaw + 1024;
+constexpr size_t kGradSmem = kGradStages * 2 * kOperand + 1024;
 static_assert(kGradSmem <= 232448 - 1024, "shared memory of one CTA");
-constexpr int kGroups = 2, kConverters = 4;         // groups of converter warps, warps of one
 constexpr int kSummers = 8;                         // warps
-// Registers of a thread: the launch's, and what setmaxnreg makes of them.
-constexpr int kGradRegs = 96, kSummerRegs = 160, kOtherRegs = 48;
-static_assert(2 * kSummerRegs + (1 + kGroups) * kOtherRegs <= kGradThreads / 128 * kGradRegs, "the launch's registers");
 constexpr uint32_t kGradTmem = 512;
 
 struct GradArgs {
   CUtensorMap dy;         // [parts][tokens][outs] bf16, box 64 x 64
-  CUtensorMap q;          // [tokens][P] bytes, box 128 x 64
-  const uint8_t* b;       // [tokens][blocks]
-  const uint8_t* b_end;
-  int64_t tokens;
-  int32_t blocks, cols, outs;
+  CUtensorMap x;          // [tokens][cols] bf16, the same box
+  int32_t cols, outs;
   int32_t parts, steps;   // bf16 parts of dy, 64-token steps of one
   int32_t tiles_n, tiles, splits, split_steps;
   void* out;              // dW, or the splits' sums [splits][outs][stride] fp32
   int64_t stride, split_stride;
   int32_t bf16, accumulate;
 };
-
-// 4 bytes global -> shared, of which `bytes` are read and the others are 0.
-__device__ __forceinline__ void cp_async_4_part(void* dst, const void* src, int bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
-}
-// An arrival on `bar` once this thread's cp.async so far have landed.
-__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-// An arrival on a barrier of either CTA, after this warp's writes to its own shared memory,
-// which fence.proxy.async has made visible to the tensor core that reads them, that of the
-// same SM.  (An arrival with release at cluster scope waits for more than those writes: 8192 x
-// 9728 x 2560 587 us with it, SCOPE_US without.)
-__device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-
-__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t x, uint32_t y) {
-  const __nv_bfloat162 r =
-      __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&y));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t y) {
-  const __nv_bfloat162 r =
-      __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&y));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-// Two signed bytes, each beside 0x43, times the step.
-__device__ __forceinline__ uint32_t convert2(uint32_t w, uint32_t step) {
-  return mul_bf16x2(sub_bf16x2(w & 0xFF7FFF7Fu, w & 0xFF80FF80u), step);
-}
-
-__device__ __forceinline__ uint4 convert8(uint2 q, uint32_t step) {
-  return make_uint4(convert2(__byte_perm(q.x, 0x43u, 0x4140), step), convert2(__byte_perm(q.x, 0x43u, 0x4342), step),
-                    convert2(__byte_perm(q.y, 0x43u, 0x4140), step), convert2(__byte_perm(q.y, 0x43u, 0x4342), step));
-}
-// 2^(b - 133) twice, NaN for 255.  (b = 0, past the last token, gives some number, for zeros.)
-__device__ __forceinline__ uint32_t step2(uint32_t b) {
-  return b == 255u ? 0x7FC07FC0u : b * 0x00800080u - 0x03000300u;
-}
-
-// The calling warpgroup's registers a thread.  The increases draw on what the decreases of
-// this CTA's other warpgroups give back.
-template <int kRegs>
-__device__ __forceinline__ void reg_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-template <int kRegs>
-__device__ __forceinline__ void reg_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
 
 // Adds 32 lanes x 8 consecutive columns of Tensor Memory to the lanes' registers.
 __device__ __forceinline__ void tmem_add8(uint32_t taddr, float (&v)[128], int at) {
@@ -199,9 +137,7 @@ __device__ __forceinline__ void store_row(const GradArgs& a, int split, int64_t 
 __global__ void __launch_bounds__(kGradThreads, 1) weight_grad_kernel(const __grid_constant__ GradArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint8_t* raw = smem + kGradStages * 2 * kOperand;
   __shared__ __align__(8) uint64_t full_bar[kGradStages], empty_bar[kGradStages];
-  __shared__ __align__(8) uint64_t raw_full[kRawStages], raw_empty[kRawStages];
   __shared__ __align__(8) uint64_t tfull_bar[2], tempty_bar[2], drain_bar;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
@@ -213,12 +149,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) weight_grad_kernel(const __gr
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kGradStages; ++s) {
-      mbar_init(&full_bar[s], 1 + 2 * kConverters);  // dy's bytes of both CTAs; a group's warps of both
+      mbar_init(&full_bar[s], 1);
       mbar_init(&empty_bar[s], 1);
-    }
-    for (int s = 0; s < kRawStages; ++s) {
-      mbar_init(&raw_full[s], 1 + 32);  // x's bytes; the exponents of each lane
-      mbar_init(&raw_empty[s], kConverters);  // of one group
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull_bar[i], 1);
@@ -228,8 +160,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) weight_grad_kernel(const __gr
     abort_flag = 0;
     fence_mbarrier_init();
   }
-  if (warp == 0 && lane == 0) tma_prefetch_desc(&a.dy);
-  if (warp == 2 && lane == 0) tma_prefetch_desc(&a.q);
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&a.dy);
+    tma_prefetch_desc(&a.x);
+  }
   if (warp == 1) {
     tmem_alloc<2>(&tmem_slot, kGradTmem);
     tmem_relinquish<2>();
@@ -242,29 +176,33 @@ __global__ void __launch_bounds__(kGradThreads, 1) weight_grad_kernel(const __gr
   griddep_wait();
   const uint32_t tmem = tmem_slot;
 
-  if (warp < 4) {
-  reg_dec<kOtherRegs>();
   if (warp == 0) {
-    // ---- dy ----
+    // ---- operands ----
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
+    const uint32_t lead = mapa_shared(&full_bar[0], 0);
     for (int u = pair; u < units && ok; u += pairs) {
       const Unit t = unit_of(a, u);
+      int part = a.parts - 1 - t.kb0 / a.steps, step = t.kb0 % a.steps;  // the smallest part first
       for (int kb = t.kb0; kb < t.kb1; ++kb) {
         const bool got = mbar_wait(&empty_bar[stage], phase ^ 1u, abort_p, nullptr);
         if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
         if (lane == 0) {
           uint8_t* sa = smem + (size_t)stage * 2 * kOperand;
-          if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2 * kOperand);
-          const uint32_t bar = mapa_shared(&full_bar[stage], 0);
-          const int pass = kb / a.steps, t0 = (kb - pass * a.steps) * kTokens;
-          const int part = a.parts - 1 - pass;  // the smallest first
+          if (leader) mbar_arrive_expect_tx(&full_bar[stage], 4 * kOperand);
+          const uint32_t bar = lead + stage * 8;
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            tma_load_3d_pair(sa + h * kChunk, &a.dy, bar, t.m0 + rank * 128 + h * 64, t0, part);
+          for (int h = 0; h < 2; ++h) {
+            tma_load_3d_pair(sa + h * kChunk, &a.dy, bar, t.m0 + rank * 128 + h * 64, step * kTokens, part);
+            tma_load_3d_pair(sa + kOperand + h * kChunk, &a.x, bar, t.n0 + rank * 128 + h * 64, step * kTokens, 0);
+          }
         }
         __syncwarp();
+        if (++step == a.steps) {
+          step = 0;
+          --part;
+        }
         if (++stage == kGradStages) { stage = 0; phase ^= 1u; }
       }
     }
@@ -278,6 +216,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) weight_grad_kernel(const __gr
     if (leader) {
       // ---- tensor cores ----
       const uint32_t idesc = make_idesc(1u, kTile, kTile, 1u, 1u);
+      // 64-column chunks kChunk bytes apart, 8-token groups 1024; the address field counts 16 bytes
+      const uint64_t operand0 = smem_desc_sw128(smem_u32(smem), kChunk, 1024);
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
@@ -292,13 +232,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) weight_grad_kernel(const __gr
           for (int kb = c0; kb < c1; ++kb) {
             const bool got = mbar_wait(&full_bar[stage], phase, abort_p, nullptr);
             if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
-            tc_fence_after();
             if (lane == 0) {
-              const uint32_t sa = smem_u32(smem + (size_t)stage * 2 * kOperand), sb = sa + kOperand;
+              const uint64_t at = operand0 + (uint32_t)stage * (2 * kOperand >> 4);
 #pragma unroll
               for (int kk = 0; kk < kTokens / 16; ++kk)
-                mma<false, 2>(d, smem_desc_sw128(sa + kk * 16 * 128, kChunk, 1024),
-                              smem_desc_sw128(sb + kk * 16 * 128, kChunk, 1024), idesc, (kb > c0 || kk > 0) ? 1u : 0u);
+                mma<false, 2>(d, at + kk * (16 * 128 >> 4), at + ((kOperand >> 4) + kk * (16 * 128 >> 4)), idesc,
+                              (kb > c0 || kk > 0) ? 1u : 0u);
               mma_commit_multicast<2>(&empty_bar[stage], 3);
             }
             __syncwarp();
@@ -317,119 +256,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) weight_grad_kernel(const __gr
       }
       __syncwarp();
     }
-  } else if (warp == 2) {
-    // ---- x's bytes ----
-    int stage = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    for (int u = pair; u < units && ok; u += pairs) {
-      const Unit t = unit_of(a, u);
-      int step = t.kb0 % a.steps;
-      for (int kb = t.kb0; kb < t.kb1; ++kb) {
-        const bool got = mbar_wait(&raw_empty[stage], phase ^ 1u, abort_p, nullptr);
-        if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&raw_full[stage], kRawBytes);
-          tma_load_3d(raw + (size_t)stage * kRaw, &a.q, &raw_full[stage], t.n0 + rank * 128, step * kTokens, 0);
-        }
-        __syncwarp();
-        if (++step == a.steps) step = 0;
-        if (++stage == kRawStages) { stage = 0; phase ^= 1u; }
-      }
-    }
-    if (*abort_p && lane == 0) {
-      for (int s = 0; s < kRawStages; ++s)
-        (void)mbar_wait(&raw_full[s], phase ^ (s < stage ? 0u : 1u), nullptr, nullptr, 100000000ull);
-    }
-    __syncwarp();
-  } else {
-    // ---- x's exponents: the 4 of each token, within the 8 bytes of two 4-byte words ----
-    int stage = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    const int64_t next = (int64_t)kTokens * a.blocks;  // a multiple of 4 bytes
-    for (int u = pair; u < units && ok; u += pairs) {
-      const Unit t = unit_of(a, u);
-      const int block0 = (t.n0 + rank * 128) / kBlockCols;
-      int step = t.kb0 % a.steps;
-      const uint8_t* p[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        p[h] = a.b + (int64_t)(step * kTokens + h * 32 + lane) * a.blocks + block0;
-        p[h] -= reinterpret_cast<uint64_t>(p[h]) & 3;
-      }
-      for (int kb = t.kb0; kb < t.kb1; ++kb) {
-        const bool got = mbar_wait(&raw_empty[stage], phase ^ 1u, abort_p, nullptr);
-        if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
-        uint8_t* r = raw + (size_t)stage * kRaw + kRawBytes + lane * 8;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          // nothing past the last token's; zeros there
-          const int64_t left = step * kTokens + h * 32 + lane < a.tokens ? a.b_end - p[h] : 0;
-          if (left >= 8) {
-            cp_async_4(r + h * 256, p[h]);
-            cp_async_4(r + h * 256 + 4, p[h] + 4);
-          } else {
-            cp_async_4_part(r + h * 256, left > 0 ? p[h] : a.b, max((int)left, 0) < 4 ? max((int)left, 0) : 4);
-            cp_async_4_part(r + h * 256 + 4, left > 4 ? p[h] + 4 : a.b, max((int)left - 4, 0));
-          }
-          p[h] += next;
-        }
-        cp_async_arrive(&raw_full[stage]);
-        if (++step == a.steps) {
-          step = 0;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) p[h] -= a.steps * next;
-        }
-        if (++stage == kRawStages) { stage = 0; phase ^= 1u; }
-      }
-    }
-    cp_async_wait<0>();
-    __syncwarp();
-  }
-  } else if (warp >= 12) {
-    reg_dec<kOtherRegs>();
-    // ---- bytes to bf16 ----
-    const int group = (warp - 12) / kConverters;
-    // A thread takes 8 columns in each half of tokens i / 8 + 16 k; odd tokens begin with the
-    // second half, so that 16 lanes read different banks.
-    const int i = threadIdx.x - (12 + group * kConverters) * 32, unit = i & 7, tok0 = i >> 3, odd = tok0 & 1;
-    const uint32_t q_at = tok0 * 128 + unit * 8 + odd * 64;
-    // the token's exponents begin (t blocks) mod 4 bytes into its 8; stages are multiples of 4 tokens
-    const uint32_t b_at = kRawBytes + tok0 * 8 + (((uint32_t)tok0 * (uint32_t)a.blocks) & 3u) + (unit >> 2) + odd * 2;
-    const uint32_t o_at = kOperand + tok0 * 128 + ((unit ^ (tok0 & 7)) << 4) + odd * kChunk;
-    const int q_other = 64 - 128 * odd, b_other = 2 - 4 * odd, o_other = (int)kChunk * (1 - 2 * odd);
-    int count = 0;  // stages so far, of both groups
-    bool ok = true;
-    const uint32_t lead = mapa_shared(&full_bar[0], 0);
-    for (int u = pair; u < units && ok; u += pairs) {
-      const Unit t = unit_of(a, u);
-      for (int kb = t.kb0; kb < t.kb1; ++kb, ++count) {
-        if (count % kGroups != group) continue;
-        const int stage = count % kGradStages, rs = count % kRawStages;
-        const bool got = mbar_wait(&raw_full[rs], (uint32_t)(count / kRawStages) & 1u, abort_p, nullptr) &&
-                         mbar_wait(&empty_bar[stage], ((uint32_t)(count / kGradStages) & 1u) ^ 1u, abort_p, nullptr);
-        if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
-        const uint8_t* r = raw + (size_t)rs * kRaw;
-        uint8_t* to = smem + (size_t)stage * 2 * kOperand + o_at;
-#pragma unroll
-        for (int k = 0; k < kTokens / 16; ++k) {
-          const uint8_t *q = r + q_at + k * 16 * 128, *b = r + b_at + k * 16 * 8;
-          const uint2 q0 = *reinterpret_cast<const uint2*>(q), q1 = *reinterpret_cast<const uint2*>(q + q_other);
-          const uint32_t s0 = step2(b[0]), s1 = step2(b[b_other]);
-          *reinterpret_cast<uint4*>(to + k * 16 * 128) = convert8(q0, s0);
-          *reinterpret_cast<uint4*>(to + k * 16 * 128 + o_other) = convert8(q1, s1);
-        }
-        fence_proxy_async_shared();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive_pair(lead + stage * 8);
-          mbar_arrive(&raw_empty[rs]);
-        }
-      }
-    }
-  } else {
-    reg_inc<kSummerRegs>();
+  } else if (warp >= 4) {
     // ---- sums ----
     const int quad = warp & 3, half = (warp - 4) >> 2;
     const uint32_t lead = mapa_shared(&tempty_bar[0], 0);
@@ -554,9 +381,9 @@ constexpr int kPairs = 76;  // of SMs on the device this is built for: the divis
 struct GradPlan {
   int64_t tiles_m, tiles_n, steps, splits, split_steps;
   int parts;        // of dy; 0: read as it lies
-  int64_t ld;       // of the parts
+  int64_t ld, x_ld; // of the parts, and of x in bf16
   int64_t sum_ld;   // of the splits' sums
-  size_t parts_bytes, bytes;
+  size_t x_bytes, parts_bytes, bytes;
 };
 
 GradPlan plan_of(int64_t tokens, int64_t cols, int64_t outs, const void* dy, int64_t dy_stride, int32_t dtype) {
@@ -568,6 +395,8 @@ GradPlan plan_of(int64_t tokens, int64_t cols, int64_t outs, const void* dy, int
   const int64_t passes = p.parts > 1 ? p.parts : 1;
   p.steps = (tokens + kTokens - 1) / kTokens;
   p.ld = (outs + 7) / 8 * 8;
+  p.x_ld = (cols + 7) / 8 * 8;
+  p.x_bytes = ((size_t)tokens * p.x_ld * 2 + 255) / 256 * 256;
   if (p.parts) p.parts_bytes = ((size_t)p.parts * tokens * p.ld * 2 + 255) / 256 * 256;
   const int64_t all = passes * p.steps, tiles = p.tiles_m * p.tiles_n;
   int64_t splits = tiles < kPairs ? kPairs / tiles : 1;
@@ -576,7 +405,7 @@ GradPlan plan_of(int64_t tokens, int64_t cols, int64_t outs, const void* dy, int
   p.split_steps = (all + splits - 1) / splits;
   p.splits = all ? (all + p.split_steps - 1) / p.split_steps : 1;
   p.sum_ld = (cols + 3) / 4 * 4;
-  p.bytes = p.parts_bytes + (p.splits > 1 ? (size_t)p.splits * outs * p.sum_ld * 4 : 0);
+  p.bytes = p.x_bytes + p.parts_bytes + (p.splits > 1 ? (size_t)p.splits * outs * p.sum_ld * 4 : 0);
   return p;
 }
 
@@ -651,10 +480,12 @@ muon_status muon_checkpoint_weight_grad(const muon_checkpoint* checkpoint, const
     return e == cudaSuccess ? MUON_OK : cuda_error(e);
   }
   GradArgs a = {};
+  uint8_t* const space = static_cast<uint8_t*>(workspace);
+  if ((e = launch_checkpoint_load(checkpoint, space, p.x_ld, s)) != cudaSuccess) return cuda_error(e);
   const void* operand = dy;
   int64_t ld = stride, count = 1;
   if (p.parts) {
-    __nv_bfloat16* parts = static_cast<__nv_bfloat16*>(workspace);
+    __nv_bfloat16* parts = reinterpret_cast<__nv_bfloat16*>(space + p.x_bytes);
     const int grid = grid_of(rows * (p.ld / 8), kPartThreads, sms);
     e = dy_dtype == MUON_DTYPE_BF16
             ? launch(parts_kernel<__nv_bfloat16>, grid, kPartThreads, 0, s, 1, false, static_cast<const __nv_bfloat16*>(dy), stride, rows, outs, p.ld, parts)
@@ -664,14 +495,9 @@ muon_status muon_checkpoint_weight_grad(const muon_checkpoint* checkpoint, const
     ld = p.ld;
     count = p.parts;
   }
-  const int64_t blocks = (cols + kBlockCols - 1) / kBlockCols;
   if (!encode_tensor_map(&a.dy, const_cast<void*>(operand), 2, outs, rows, count, ld, 64, kTokens, true) ||
-      !encode_tensor_map(&a.q, checkpoint->data, 1, blocks * kBlockCols, rows, 1, blocks * kBlockCols, 128, kTokens, false))
+      !encode_tensor_map(&a.x, space, 2, cols, rows, 1, p.x_ld, 64, kTokens, true))
     return set_error(MUON_ERR_CUDA, "cuTensorMapEncodeTiled rejected a tensor map");
-  a.b = static_cast<const uint8_t*>(checkpoint->data) + rows * blocks * kBlockCols;
-  a.b_end = a.b + rows * blocks;
-  a.tokens = rows;
-  a.blocks = (int32_t)blocks;
   a.cols = (int32_t)cols;
   a.outs = (int32_t)outs;
   a.parts = (int32_t)count;
@@ -682,7 +508,7 @@ muon_status muon_checkpoint_weight_grad(const muon_checkpoint* checkpoint, const
   a.split_steps = (int32_t)p.split_steps;
   float* sums = nullptr;
   if (p.splits > 1) {
-    sums = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + p.parts_bytes);
+    sums = reinterpret_cast<float*>(space + p.x_bytes + p.parts_bytes);
     a.out = sums;
     a.stride = p.sum_ld;
     a.split_stride = outs * p.sum_ld;
@@ -692,13 +518,10 @@ muon_status muon_checkpoint_weight_grad(const muon_checkpoint* checkpoint, const
     a.bf16 = bf16_out;
     a.accumulate = accumulate;
   }
-  cudaFuncAttributes attr;  // setmaxnreg would wait for ever for registers that the launch does not have
-  if ((e = cudaFuncGetAttributes(&attr, weight_grad_kernel)) != cudaSuccess) return cuda_error(e);
-  if (attr.numRegs < kGradRegs) return set_error(MUON_ERR_UNSUPPORTED, "the kernel was compiled for too few registers");
   if ((e = cudaFuncSetAttribute(weight_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGradSmem)) != cudaSuccess)
     return cuda_error(e);
   const int64_t units = (int64_t)a.tiles * a.splits, pairs = sms / 2;
-  e = launch(weight_grad_kernel, (int)(2 * (units < pairs ? units : pairs)), kGradThreads, kGradSmem, s, 2, p.parts > 0, a);
+  e = launch(weight_grad_kernel, (int)(2 * (units < pairs ? units : pairs)), kGradThreads, kGradSmem, s, 2, true, a);
   if (e != cudaSuccess) return cuda_error(e);
   if (p.splits > 1) {
     e = bf16_out ? launch_join<__nv_bfloat16>(p, sums, dw, out_stride, outs, cols, accumulate, sms, s)

@@ -106,11 +106,11 @@ def test_weight_grad_workspace(nsm):
         assert st == nsm.MUON_OK
         return v.value
 
-    assert need(8192, 2560, 9728, 1) == 0                      # read as it lies, a tile a pair
+    assert need(8192, 2560, 9728, 1) == 8192 * 2560 * 2        # x in bf16; dy as it lies, a tile a pair
     assert need(8192, 2560, 9728, 1, dy=A + 2) >= 8192 * 9728 * 2
     assert need(8192, 2560, 9728, 1, stride=9729) >= 8192 * 9728 * 2
     assert need(8192, 2560, 9728, 0) >= 3 * 8192 * 9728 * 2
-    assert need(100000, 40, 40, 1) > 0                         # the sums of the parts
+    assert need(100000, 40, 40, 1) > 100000 * 40 * 2           # the sums of the tokens' parts
     assert need(0, 40, 40, 1) == 0
     short = _wg(nsm, dy_dtype=0, nbytes=10)
     assert short == nsm.MUON_ERR_NO_WORKSPACE
