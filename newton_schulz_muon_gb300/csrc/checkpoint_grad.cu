@@ -118,7 +118,16 @@ __device__ __forceinline__ void store_row(const GradArgs& a, int split, int64_t 
     return;
   }
   float* p = reinterpret_cast<float*>(a.out) + e;
-  if (n == 16 && (reinterpret_cast<uint64_t>(p) & 15) == 0) {
+  if (n == 16 && (reinterpret_cast<uint64_t>(p) & 31) == 0 && !a.accumulate) {  // whole sectors
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float* v = s + at + 8 * k;
+      asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p + 8 * k), "f"(v[0] + poison),
+                   "f"(v[1] + poison), "f"(v[2] + poison), "f"(v[3] + poison), "f"(v[4] + poison), "f"(v[5] + poison),
+                   "f"(v[6] + poison), "f"(v[7] + poison)
+                   : "memory");
+    }
+  } else if (n == 16 && (reinterpret_cast<uint64_t>(p) & 15) == 0) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -220,7 +229,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) weight_grad_kernel(const __gr
       const uint64_t operand0 = smem_desc_sw128(smem_u32(smem), kChunk, 1024);
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
-      bool ok = true;
+      bool ok = true, ready = false;
       for (int u = pair; u < units && ok; u += pairs) {
         const Unit t = unit_of(a, u);
         for (int c0 = t.kb0; c0 < t.kb1; c0 += kChunkSteps) {
@@ -230,18 +239,24 @@ __global__ void __launch_bounds__(kGradThreads, 1) weight_grad_kernel(const __gr
           tc_fence_after();
           const uint32_t d = tmem + (uint32_t)(acc * kTile);
           for (int kb = c0; kb < c1; ++kb) {
-            const bool got = mbar_wait(&full_bar[stage], phase, abort_p, nullptr);
-            if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+            if (!ready) {
+              const bool got = mbar_wait(&full_bar[stage], phase, abort_p, nullptr);
+              if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+            }
+            const uint64_t at = operand0 + (uint32_t)stage * (2 * kOperand >> 4);
+            uint64_t* const empty = &empty_bar[stage];
+            if (++stage == kGradStages) { stage = 0; phase ^= 1u; }
+            // whether the next stage has landed is asked before this one's MMAs are issued: the
+            // tensor core's queue is too short to cover the answer's latency (NEXT_US without)
+            ready = __all_sync(0xffffffffu, mbar_test_wait(&full_bar[stage], phase));
             if (lane == 0) {
-              const uint64_t at = operand0 + (uint32_t)stage * (2 * kOperand >> 4);
 #pragma unroll
               for (int kk = 0; kk < kTokens / 16; ++kk)
                 mma<false, 2>(d, at + kk * (16 * 128 >> 4), at + ((kOperand >> 4) + kk * (16 * 128 >> 4)), idesc,
                               (kb > c0 || kk > 0) ? 1u : 0u);
-              mma_commit_multicast<2>(&empty_bar[stage], 3);
+              mma_commit_multicast<2>(empty, 3);
             }
             __syncwarp();
-            if (++stage == kGradStages) { stage = 0; phase ^= 1u; }
           }
           if (!ok) break;
           if (lane == 0) mma_commit_multicast<2>(&tfull_bar[acc], 3);
