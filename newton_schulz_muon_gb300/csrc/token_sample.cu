@@ -130,6 +130,30 @@ __device__ __forceinline__ uint4 load_elems(const T* z, int32_t vocab, int e) {
   return Vec<T>::pack(v);
 }
 
+// Units first, first + stride, ... of a row, kLoads of them, -inf from unit u1 on.  inside: they
+// all hold elements of the row only.
+template <typename T>
+__device__ __forceinline__ void load_units(const RowUnits<T>& row, int first, int stride, int u1, bool inside,
+                                           uint4 (&w)[kLoads]) {
+  constexpr uint32_t low = Vec<T>::kLowest;
+  if (inside) {
+    const uint4* p = reinterpret_cast<const uint4*>(row.z - row.shift) + first;
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) w[k] = __ldg(p + k * stride);
+  } else {
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) {
+      const int u = first + k * stride;
+      w[k] = u < u1 ? load_elems<T>(row.z, row.vocab, row.first(u)) : make_uint4(low, low, low, low);
+    }
+  }
+}
+// Whether the units [u, u + kStripStep) lie before u1 and hold elements of the row only.
+template <typename T>
+__device__ __forceinline__ bool step_inside(const RowUnits<T>& row, int u, int u1) {
+  return u + kStripStep <= u1 && row.first(u) >= 0 && row.first(u + kStripStep) <= row.vocab;
+}
+
 // 2^(c (z - m)) of a unit's elements.
 template <typename T>
 __device__ __forceinline__ void exps(const Scale& c, float m, const uint4& w, float (&e)[Vec<T>::N]) {
@@ -147,15 +171,10 @@ __device__ __forceinline__ void exps(const Scale& c, float m, const uint4& w, fl
 // The sum of exponentials over the units [u0, u1) of a row; the same in every lane.
 template <typename T>
 __device__ __forceinline__ StripSum strip_sum(const RowUnits<T>& row, const Scale& c, int u0, int u1, int lane) {
-  constexpr uint32_t low = Vec<T>::kLowest;
   StripSum t{-INFINITY, 0.f};
   for (int u = u0; u < u1; u += kStripStep) {
     uint4 w[kLoads];
-#pragma unroll
-    for (int k = 0; k < kLoads; ++k) {
-      const int at = u + k * 32 + lane;
-      w[k] = at < u1 ? load_elems<T>(row.z, row.vocab, row.first(at)) : make_uint4(low, low, low, low);
-    }
+    load_units<T>(row, u + lane, 32, u1, step_inside<T>(row, u, u1), w);
     const float m = fmaxf(t.m, warp_max(Vec<T>::max(w)));
     F2 s0 = make_f2(0.f, 0.f), s1 = make_f2(0.f, 0.f);
 #pragma unroll
@@ -180,55 +199,94 @@ struct Refused {
   float mp, ip, mq, iq;  // frames, and reciprocals of the sums
 };
 
-// max(p - q, 0) of unit u of the target's row; each product rounded, so that equal rows leave 0.
+// max(p - q, 0) of the units first, first + stride, ... of the target's row, 0 from u1 on; each
+// product rounded, so that equal rows leave 0.
 template <typename T>
 __device__ __forceinline__ void left_over(const SampleArgs& a, const Refused& f, const RowUnits<T>& p, const T* zq,
-                                          int u, float (&r)[Vec<T>::N]) {
-  float q[Vec<T>::N];
-  exps<T>(a.target_scale, f.mp, load_elems<T>(p.z, p.vocab, p.first(u)), r);
-  exps<T>(a.draft_scale, f.mq, load_elems<T>(zq, p.vocab, p.first(u)), q);
+                                          int first, int stride, int u1, bool inside, float (&r)[kLoads * Vec<T>::N]) {
+  constexpr int N = Vec<T>::N;
+  constexpr uint32_t low = Vec<T>::kLowest;
+  uint4 wp[kLoads], wq[kLoads];
+  load_units<T>(p, first, stride, u1, inside, wp);
 #pragma unroll
-  for (int i = 0; i < Vec<T>::N; ++i) r[i] = fmaxf(__fmul_rn(r[i], f.ip) - __fmul_rn(q[i], f.iq), 0.f);
+  for (int k = 0; k < kLoads; ++k) {
+    const int u = first + k * stride;
+    wq[k] = u < u1 ? load_elems<T>(zq, p.vocab, p.first(u)) : make_uint4(low, low, low, low);
+  }
+#pragma unroll
+  for (int k = 0; k < kLoads; ++k) {
+    float x[N], y[N];
+    exps<T>(a.target_scale, f.mp, wp[k], x);
+    exps<T>(a.draft_scale, f.mq, wq[k], y);
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[k * N + i] = fmaxf(__fmul_rn(x[i], f.ip) - __fmul_rn(y[i], f.iq), 0.f);
+  }
 }
 
 // The first element of the units [u0, u1) at which the cumulated weight exceeds t (a token
-// of weight 0 never does), or the last of positive weight, or -1.  weights(u, w): those of
-// unit u.
+// of weight 0 never does), or the last of positive weight, or -1.  weights(first, inside, w):
+// those of the units first .. first + kLoads - 1 (0 from u1 on), which a lane takes side by
+// side.  A lane's weights are summed in fp32, the lanes' in 64 bits, of which the SMs do few.
 template <typename T, typename F>
 __device__ __forceinline__ int pick_element(const RowUnits<T>& row, int u0, int u1, double t, int lane, F weights) {
   constexpr int N = Vec<T>::N;
   double before = 0.;
   int last = -1;
-  for (int u = u0; u < u1; u += 32) {
-    float w[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) w[i] = 0.f;
-    if (u + lane < u1) weights(u + lane, w);
-    double s = 0.;
+  for (int u = u0; u < u1; u += kStripStep) {
+    const int first = u + lane * kLoads;
+    float w[kLoads * N];
+    weights(first, step_inside<T>(row, u, u1), w);
+    float s = 0.f;
     int positive = -1;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      s += (double)w[i];
+    for (int i = 0; i < kLoads * N; ++i) {
+      s += w[i];
       if (w[i] > 0.f) positive = i;
     }
-    const double upto = before + warp_scan64(s, lane);
+    const double upto = before + warp_scan64((double)s, lane);
     const unsigned over = __ballot_sync(0xFFFFFFFFu, positive >= 0 && upto > t);
     const unsigned any = __ballot_sync(0xFFFFFFFFu, positive >= 0);
     if (over) {
       const int l = __ffs(over) - 1;
+      const float rest = (float)(t - (upto - (double)s));  // of the lane's weights
       int found = positive;
-      double c = upto;
+      float c = 0.f;
+      bool passed = false;
 #pragma unroll
-      for (int i = N - 1; i >= 0; --i) {  // c: the weights up to element i
-        if (w[i] > 0.f && c > t) found = i;
-        c -= (double)w[i];
+      for (int i = 0; i < kLoads * N; ++i) {
+        c += w[i];
+        if (!passed && w[i] > 0.f && c > rest) {
+          found = i;
+          passed = true;
+        }
       }
-      return __shfl_sync(0xFFFFFFFFu, row.first(u + lane) + found, l);
+      return __shfl_sync(0xFFFFFFFFu, row.first(first) + found, l);
     }
-    if (any) last = __shfl_sync(0xFFFFFFFFu, row.first(u + lane) + positive, 31 - __clz(any));
+    if (any) last = __shfl_sync(0xFFFFFFFFu, row.first(first) + positive, 31 - __clz(any));
     before = __shfl_sync(0xFFFFFFFFu, upto, 31);
   }
   return last;
+}
+
+// Each lane's part of the sum over the units [u0, u1) without one token.
+template <typename T>
+__device__ __forceinline__ float sum_without(const RowUnits<T>& row, const Scale& c, float m, int u0, int u1, int token,
+                                             int lane) {
+  constexpr int N = Vec<T>::N;
+  float s = 0.f;
+  for (int u = u0; u < u1; u += kStripStep) {
+    uint4 w[kLoads];
+    load_units<T>(row, u + lane, 32, u1, step_inside<T>(row, u, u1), w);
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) {
+      float e[N];
+      exps<T>(c, m, w[k], e);
+      const int at = token - row.first(u + k * 32 + lane);
+#pragma unroll
+      for (int i = 0; i < N; ++i) s += i == at ? 0.f : e[i];
+    }
+  }
+  return s;
 }
 
 // log p of a token of the strip [u0, u1): the strip is summed again without the token, so
@@ -237,14 +295,7 @@ __device__ __forceinline__ int pick_element(const RowUnits<T>& row, int u0, int 
 template <typename T>
 __device__ __forceinline__ float token_logp(const RowUnits<T>& row, const Scale& c, float m, double rest, int u0, int u1,
                                             int token, int lane) {
-  constexpr int N = Vec<T>::N;
-  for (int u = u0 + lane; u < u1; u += 32) {
-    float e[N];
-    exps<T>(c, m, load_elems<T>(row.z, row.vocab, row.first(u)), e);
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (row.first(u) + i != token) rest += (double)e[i];
-  }
+  rest += (double)sum_without<T>(row, c, m, u0, u1, token, lane);
   float s = (float)warp_sum64(rest);
   const float d = Vec<T>::load(row.z + token) - m;
   const float x = __fmaf_rn(d, c.inv_hi, d * c.inv_lo);
@@ -446,16 +497,9 @@ __global__ void __launch_bounds__(kMaxSampleThreads) sample_kernel(const __grid_
         if (k >= 0 && k < a.strips) {  // every warp sums the strip alike
           int u0, u1;
           units_of(row, k, u0, u1);
-          double s = 0.;
-          for (int u = u0 + lane; u < u1; u += 32) {
-            float e[N];
-            exps<T>(c, p.m, load_elems<T>(row.z, row.vocab, row.first(u)), e);
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-              if (row.first(u) + i != without) s += (double)e[i];
-          }
+          const float s = sum_without<T>(row, c, p.m, u0, u1, (int)without, lane);
           without_strip = k;
-          without_sum = (float)warp_sum64(s);
+          without_sum = warp_sum(s);
         }
       }
     } else {
@@ -487,11 +531,11 @@ __global__ void __launch_bounds__(kMaxSampleThreads) sample_kernel(const __grid_
           int u0, u1;
           units_of(row, k, u0, u1);
           float s = 0.f;
-          for (int u = u0 + lane; u < u1; u += 32) {
-            float r[N];
-            left_over<T>(a, f, row, zq, u, r);
+          for (int u = u0; u < u1; u += kStripStep) {
+            float r[kLoads * N];
+            left_over<T>(a, f, row, zq, u + lane, 32, u1, step_inside<T>(row, u, u1), r);
 #pragma unroll
-            for (int i = 0; i < N; ++i) s += r[i];
+            for (int i = 0; i < kLoads * N; ++i) s += r[i];
           }
           s = warp_sum(s);
           if (lane == 0) left[k] = StripSum{0.f, s};
@@ -558,16 +602,19 @@ __global__ void __launch_bounds__(kMaxSampleThreads) sample_kernel(const __grid_
       }
       int u0, u1;
       units_of(row, strip, u0, u1);
-      token = pick_element<T>(row, u0, u1, t - before, lane, [&](int u, float(&w)[N]) {
+      token = pick_element<T>(row, u0, u1, t - before, lane, [&](int first, bool inside, float(&w)[kLoads * N]) {
         if (kind == kLeft) {
-          left_over<T>(a, f, row, zq, u, w);
+          left_over<T>(a, f, row, zq, first, 1, u1, inside, w);
           return;
         }
-        exps<T>(c, p.m, load_elems<T>(row.z, row.vocab, row.first(u)), w);
-        if (kind == kWithout) {
+        uint4 z[kLoads];
+        load_units<T>(row, first, 1, u1, inside, z);
 #pragma unroll
-          for (int i = 0; i < N; ++i)
-            if (row.first(u) + i == without) w[i] = 0.f;
+        for (int k = 0; k < kLoads; ++k) {
+          float e[N];
+          exps<T>(c, p.m, z[k], e);
+#pragma unroll
+          for (int i = 0; i < N; ++i) w[k * N + i] = kind == kWithout && row.first(first + k) + i == without ? 0.f : e[i];
         }
       });
       if (token >= 0)
