@@ -36,7 +36,7 @@ constexpr int kStripStep = 32 * kLoads;    // units that a warp takes at a time
 constexpr int kMaxRound = 8;               // rows of a sequence in one round
 constexpr int kMaxTable = 512;             // strips of a CTA and round, of each kind
 constexpr int kMaxCluster = 8;
-constexpr int kMaxSampleThreads = 1024;
+constexpr int kMaxSampleThreads = 512;
 
 // Logits are divided by the temperature: exponents in base 2 are c = c_hi + c_lo times
 // theirs, c_lo > 0 (so that -inf stays -inf).
@@ -313,12 +313,18 @@ __device__ __forceinline__ RowSum load_peer(const RowSum* p, int rank, int own) 
   return r;
 }
 
+__device__ __forceinline__ double load_peer(const double* p, int rank) {
+  double v;
+  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(mapa_shared(p, (uint32_t)rank)) : "memory");
+  return v;
+}
+
 __device__ __forceinline__ bool usable(const RowSum& t) { return t.s > 0. && t.s < (double)INFINITY; }
 
 // A cluster of CTAs a sequence (or, without drafts, a row).  Its rows are taken `round` at a
 // time until a draft is refused.
 template <typename T, bool kDrafts>
-__global__ void __launch_bounds__(kMaxSampleThreads) sample_kernel(const __grid_constant__ SampleArgs a) {
+__global__ void __launch_bounds__(kMaxSampleThreads, 2) sample_kernel(const __grid_constant__ SampleArgs a) {
   constexpr int N = Vec<T>::N;
   extern __shared__ StripSum tables[];  // [2][target and draft][round][strips]
   __shared__ SampleShared sh;
@@ -364,7 +370,7 @@ __global__ void __launch_bounds__(kMaxSampleThreads) sample_kernel(const __grid_
     RowSum r;
     r.m = warp_max(m);
     r.s = 0.;
-    for (int k = lane; k < a.strips; k += 32) r.s += (double)table[k].s * (double)factor(c, table[k].m, r.m);
+    for (int k = lane; k < a.strips; k += 32) r.s += (double)(table[k].s * factor(c, table[k].m, r.m));
     r.s = warp_sum64(r.s);
     return r;
   };
@@ -372,7 +378,7 @@ __global__ void __launch_bounds__(kMaxSampleThreads) sample_kernel(const __grid_
   auto other_strips = [&](const StripSum* table, const RowSum* slice, int k0, float m, const Scale& c) {
     double s = 0.;
     for (int k = lane; k < a.strips; k += 32)
-      if (k != k0) s += (double)table[k].s * (double)factor(c, table[k].m, m);
+      if (k != k0) s += (double)(table[k].s * factor(c, table[k].m, m));
     if (lane < a.cluster && lane != rank) {
       const RowSum t = load_peer(slice, lane, rank);
       s += t.s * (double)factor(c, t.m, m);
@@ -545,6 +551,8 @@ __global__ void __launch_bounds__(kMaxSampleThreads) sample_kernel(const __grid_
     }
   }
 
+  if (warp != 0) return;  // the cluster's barriers wait for the warps that are left
+
   int64_t token = -1;
   bool mine = rank == 0;  // this CTA writes the token
   float lp = NAN;
@@ -552,54 +560,58 @@ __global__ void __launch_bounds__(kMaxSampleThreads) sample_kernel(const __grid_
     auto weight = [&](int k) {
       if (kind == kLeft) return (double)left[k].s;
       if (kind == kWithout && k == without_strip) return (double)without_sum;
-      return (double)own[k].s * (double)factor(c, own[k].m, p.m);
+      return (double)(own[k].s * factor(c, own[k].m, p.m));
     };
-    double v = 0., upto = 0., sum = 0.;
-    for (;;) {
-      // each CTA's share of the weights, and their running sum
-      double slice = 0.;
-      for (int k = lane; k < a.strips; k += 32) slice += weight(k);
-      slice = warp_sum64(slice);
+    // each CTA's share of the weights in its lane, and their running sum
+    double v = 0.;
+    if (kind != kPlain) {
+      for (int k = lane; k < a.strips; k += 32) v += weight(k);
+      v = warp_sum64(v);
       if (a.cluster > 1) {
-        if (threadIdx.x == 0) sh.weights = slice;
+        if (lane == 0) sh.weights = v;
         cluster_sync();
+        v = lane >= a.cluster ? 0. : lane == rank ? v : load_peer(&sh.weights, lane);
+      } else if (lane > 0) {
         v = 0.;
-        if (lane < a.cluster) {
-          if (lane == rank) v = slice;
-          else asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(mapa_shared(&sh.weights, (uint32_t)lane)) : "memory");
-        }
-        cluster_sync();  // sh.weights is free
-      } else {
-        v = lane == 0 ? slice : 0.;
       }
-      upto = warp_scan64(v, lane);
-      sum = __shfl_sync(0xFFFFFFFFu, upto, 31);
-      if (sum > 0. || kind == kPlain) break;
-      kind = kPlain;  // the two models agree: the refusal was one of rounding
+      // nothing is left over where the two models agree, and the refusal was one of rounding
+      if (!__any_sync(0xFFFFFFFFu, v > 0.)) kind = kPlain;
     }
+    if (kind == kPlain) {
+      RowSum r{0., -INFINITY};
+      if (lane < a.cluster) r = load_peer(&sh.slice[parity][at], lane, rank);
+      v = r.s * (double)factor(c, r.m, p.m);
+    }
+    const double upto = warp_scan64(v, lane), sum = __shfl_sync(0xFFFFFFFFu, upto, 31);
     const float su = fmaxf(a.sample_u[seq], 0.f);
     const double t = su < 1.f ? (double)su * sum : (double)INFINITY;  // 1 and above: the last token
     const unsigned over = __ballot_sync(0xFFFFFFFFu, v > 0. && upto > t);
     const unsigned any = __ballot_sync(0xFFFFFFFFu, v > 0.);
     const int owner = over ? __ffs(over) - 1 : 31 - __clz(any);
     mine = rank == owner;
-    if (mine && warp == 0) {
-      double before = __shfl_sync(0xFFFFFFFFu, upto - v, owner);
+    if (mine) {
+      // a lane takes consecutive strips
+      const int per = (a.strips + 31) / 32, k0 = lane * per, k1 = min(k0 + per, a.strips);
+      double w = 0.;
+      for (int k = k0; k < k1; ++k) w += weight(k);
+      const double end = __shfl_sync(0xFFFFFFFFu, upto - v, owner) + warp_scan64(w, lane);
+      const unsigned above = __ballot_sync(0xFFFFFFFFu, w > 0. && end > t);
+      const unsigned some = __ballot_sync(0xFFFFFFFFu, w > 0.);
+      const int l = above ? __ffs(above) - 1 : 31 - __clz(some);
+      double before = end - w;
       int strip = -1;
-      for (int k0 = 0; k0 < a.strips; k0 += 32) {
-        const double w = k0 + lane < a.strips ? weight(k0 + lane) : 0.;
-        const double end = before + warp_scan64(w, lane);
-        const unsigned above = __ballot_sync(0xFFFFFFFFu, w > 0. && end > t);
-        const unsigned some = __ballot_sync(0xFFFFFFFFu, w > 0.);
-        if (above) {
-          const int l = __ffs(above) - 1;
-          strip = k0 + l;
-          before = __shfl_sync(0xFFFFFFFFu, end - w, l);
-          break;
+      double begun = before;
+      for (int k = k0; k < k1; ++k) {
+        const double x = weight(k);
+        if (x > 0.) {
+          strip = k;
+          begun = before;
+          if (before + x > t) break;
         }
-        if (some) strip = k0 + 31 - __clz(some);
-        before = __shfl_sync(0xFFFFFFFFu, end, 31);
+        before += x;
       }
+      strip = __shfl_sync(0xFFFFFFFFu, strip, l);
+      before = __shfl_sync(0xFFFFFFFFu, begun, l);
       int u0, u1;
       units_of(row, strip, u0, u1);
       token = pick_element<T>(row, u0, u1, t - before, lane, [&](int first, bool inside, float(&w)[kLoads * N]) {
@@ -621,13 +633,13 @@ __global__ void __launch_bounds__(kMaxSampleThreads) sample_kernel(const __grid_
         lp = token_logp<T>(row, c, p.m, other_strips(own, &sh.slice[parity][at], strip, p.m, c), u0, u1, (int)token, lane);
     }
   }
-  if (mine && threadIdx.x == 0) {
+  if (mine && lane == 0) {
     a.tokens[row0 + taken] = token;
     a.logp[row0 + taken] = lp;
   }
   if (kDrafts && rank == 0) {
-    if (threadIdx.x == 0) a.counts[seq] = taken;
-    for (int64_t r = taken + 1 + threadIdx.x; r <= n; r += blockDim.x) {
+    if (lane == 0) a.counts[seq] = taken;
+    for (int64_t r = taken + 1 + lane; r <= n; r += 32) {
       a.tokens[row0 + r] = -1;
       a.logp[row0 + r] = 0.f;
     }
@@ -673,7 +685,7 @@ int shape_of(SampleArgs& a, int64_t n_seqs, int64_t rows, int32_t dtype, int sms
   a.strips = (int32_t)((strips + cluster - 1) / cluster);
   *smem = (size_t)4 * a.round * a.strips * sizeof(StripSum);
   const int64_t jobs = (int64_t)a.round * a.strips;
-  const int64_t most_warps = n_seqs * cluster <= sms ? 32 : 8;
+  const int64_t most_warps = n_seqs * cluster <= sms ? 16 : 8;
   return (int)(32 * (jobs < most_warps ? jobs : most_warps));
 }
 
