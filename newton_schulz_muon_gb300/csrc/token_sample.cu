@@ -7,15 +7,22 @@
 //   refused there, else from p: the first token whose cumulated weight exceeds
 //   u' (the sum of all weights).
 //
-// A row is cut into strips of consecutive 16-byte units, one warp a strip, and each strip's
-// sum of exponentials is kept (in the frame of its own largest logit).  The sums give the
-// row's normaliser, and by them the strip that holds the sampled token is found: only that
-// strip is read again, so that a row is read once.  A refused draft's row is read twice,
-// since the difference of the probabilities needs both rows' normalisers first.
+// A row is cut into strips of consecutive 16-byte units, and each strip's sum of exponentials
+// is kept (in the frame of its own largest logit).  The sums give the row's normaliser, and by
+// them the strip that holds the sampled token is found: only that strip is read again, so
+// that a row is read once.  A refused draft's row is read twice, since the difference of the
+// probabilities needs both rows' normalisers first.
+//
+// Strips of all rows are dealt out to the warps of the whole chip alike, a few strips a time,
+// and a small kernel draws the tokens afterwards, a warp a row: with a CTA a row, 2048 rows of
+// 131072 bf16 logits took 117 us (the ends of rows, and 3.03 rounds of CTAs that took 4), ROWS_US so.
+// Drafts are verified position by position: the warp that finishes a row decides on its
+// draft, and later rows of a sequence whose draft was refused are left out as far as that is
+// known when their turn comes.  (What is left out changes no result.)
 //
 // Sums over a strip are fp32 (1024 bf16 or 512 fp32 logits, 32 or 16 a lane and then the
-// lanes'), sums over strips and the search for the token are in 64 bits: a token's share of
-// [0, 1) begins within a few 1e-8 of where it should.
+// lanes'), sums over strips and the search for the token's strip are in 64 bits: a token's
+// share of [0, 1) begins within a few 1e-8 of where it should.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -33,37 +40,14 @@ namespace {
 
 constexpr int kLoads = 4;                  // 16-byte units a lane takes at a time
 constexpr int kStripStep = 32 * kLoads;    // units that a warp takes at a time
-constexpr int kMaxRound = 8;               // rows of a sequence in one round
-constexpr int kMaxTable = 512;             // strips of a CTA and round, of each kind
-constexpr int kMaxCluster = 8;
-constexpr int kMaxSampleThreads = 512;
+constexpr int kMaxStrips = 512;            // of a row; longer rows have longer strips
+constexpr int kSampleWarps = 8;            // of a CTA, at most
+constexpr int kSampleCtas = 4;             // CTAs an SM, by their registers
 
 // Logits are divided by the temperature: exponents in base 2 are c = c_hi + c_lo times
 // theirs, c_lo > 0 (so that -inf stays -inf).
 struct Scale {
   float c_hi, c_lo, inv_hi, inv_lo;
-};
-
-struct SampleArgs {
-  const void* target;
-  const void* draft;         // null: drafts that were certain
-  const uint8_t* mask;       // rows of a sampling call that take part; or null
-  const int64_t* drafts;
-  const float* draft_logp;   // or null
-  const int64_t* offsets;    // [n_seqs + 1]
-  const float* accept_u;
-  const float* sample_u;
-  int64_t* tokens;
-  int64_t* counts;
-  float* logp;
-  int64_t target_stride, draft_stride;
-  int64_t n_drafts;
-  Scale target_scale, draft_scale;
-  int32_t vocab;
-  int32_t cluster;           // CTAs a sequence
-  int32_t strip_units;       // a multiple of kStripStep
-  int32_t strips;            // of a CTA
-  int32_t round;             // rows of a sequence taken side by side
 };
 
 // A sum of exponentials in the frame of m, the largest logit (-inf: none).
@@ -75,10 +59,37 @@ struct RowSum {
   float m;
 };
 
-struct SampleShared {
-  RowSum slice[2][2 * kMaxRound];  // this CTA's part of each row, read by the cluster's other CTAs
-  RowSum total[2][2 * kMaxRound];
-  double weights;                  // this CTA's part of the weights a token is drawn from
+struct SampleArgs {
+  const void* target;
+  const void* draft;         // null: drafts that were certain
+  const uint8_t* mask;       // rows of a sampling call that take part; or null
+  const int64_t* drafts;
+  const float* draft_logp;   // or null
+  const int64_t* offsets;    // [n_seqs + 1]; null: sampling, a row a sequence
+  const float* accept_u;
+  const float* sample_u;
+  int64_t* tokens;
+  int64_t* counts;
+  float* logp;
+  int64_t target_stride, draft_stride;
+  int64_t n_drafts, n_seqs;
+  Scale target_scale, draft_scale;
+  int32_t vocab;
+  int32_t strip_units;       // a multiple of kStripStep
+  int32_t strips;            // of a row
+  int32_t each;              // strips that a warp takes at a time
+  int32_t pieces;            // of a row: strips / each, rounded up
+  int32_t both;              // the draft model's rows are read with the target's
+  // workspace
+  StripSum* p;               // [target rows][strips]
+  StripSum* q;               // of the draft model: both, [drafts][strips]; else [n_seqs][strips], where a draft was refused
+  float* left;               // [n_seqs][strips] max(p - q, 0)
+  RowSum* p_total;           // [target rows]
+  RowSum* q_total;           // [drafts] or [n_seqs]
+  uint32_t* done;            // [target rows] pieces that are done; zero at first, as the next two
+  uint32_t* q_done;          // [n_seqs]
+  uint32_t* refused;         // [n_seqs] 2^31 - 1 minus the first refused draft, 0: none
+  int64_t* longest;          // the most drafts of a sequence
 };
 
 __device__ __forceinline__ float factor(const Scale& c, float m, float to) {
@@ -304,347 +315,417 @@ __device__ __forceinline__ float token_logp(const RowUnits<T>& row, const Scale&
   return x == 0.f ? 0.f - log1pf(s) : x - logf(s + expf(x));
 }
 
-__device__ __forceinline__ RowSum load_peer(const RowSum* p, int rank, int own) {
-  if (rank == own) return *p;
-  const uint32_t at = mapa_shared(p, (uint32_t)rank);
+__device__ __forceinline__ bool usable(const RowSum& t) { return t.s > 0. && t.s < (double)INFINITY; }
+
+// The sum over a row's strips, and of the lane's share of them (consecutive strips), in the
+// frame of the largest.
+__device__ __forceinline__ RowSum row_sum(const SampleArgs& a, const StripSum* t, const Scale& c, int lane) {
+  float m = -INFINITY;
+  for (int k = lane; k < a.strips; k += 32) m = fmaxf(m, __ldcg(reinterpret_cast<const float2*>(t) + k).x);
   RowSum r;
-  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(r.s) : "r"(at) : "memory");
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(r.m) : "r"(at + 8) : "memory");
+  r.m = warp_max(m);
+  double s = 0.;
+  for (int k = lane; k < a.strips; k += 32) {
+    const float2 x = __ldcg(reinterpret_cast<const float2*>(t) + k);
+    s += (double)(x.y * factor(c, x.x, r.m));
+  }
+  r.s = warp_sum64(s);
   return r;
 }
 
-__device__ __forceinline__ double load_peer(const double* p, int rank) {
-  double v;
-  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(mapa_shared(p, (uint32_t)rank)) : "memory");
-  return v;
+__device__ __forceinline__ RowSum load_total(const RowSum* p) {
+  RowSum r;
+  r.s = __ldcg(&p->s);
+  r.m = __ldcg(&p->m);
+  return r;
 }
 
-__device__ __forceinline__ bool usable(const RowSum& t) { return t.s > 0. && t.s < (double)INFINITY; }
+// A sequence's drafts; offsets out of order or range lead to nothing outside the arrays.
+struct Sequence {
+  int64_t lo, n;
+};
+__device__ __forceinline__ Sequence sequence_of(const SampleArgs& a, int64_t s) {
+  Sequence q;
+  q.lo = min(max(a.offsets[s], (int64_t)0), a.n_drafts);
+  q.n = min(max(a.offsets[s + 1], q.lo), a.n_drafts) - q.lo;
+  return q;
+}
 
-// A cluster of CTAs a sequence (or, without drafts, a row).  Its rows are taken `round` at a
-// time until a draft is refused.
-template <typename T, bool kDrafts>
-__global__ void __launch_bounds__(kMaxSampleThreads, 2) sample_kernel(const __grid_constant__ SampleArgs a) {
-  constexpr int N = Vec<T>::N;
-  extern __shared__ StripSum tables[];  // [2][target and draft][round][strips]
-  __shared__ SampleShared sh;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  const int rank = a.cluster > 1 ? (int)cluster_ctarank() : 0;
-  const int64_t seq = blockIdx.x / a.cluster;
-  int64_t lo = 0, n = 0;
-  if (kDrafts) {
-    // offsets out of order or range: nothing outside the arrays is touched
-    lo = min(max(a.offsets[seq], (int64_t)0), a.n_drafts);
-    n = min(max(a.offsets[seq + 1], lo), a.n_drafts) - lo;
-  } else if (a.mask != nullptr && a.mask[seq] == 0) {
-    if (rank == 0 && threadIdx.x == 0) {
-      a.tokens[seq] = -1;
-      a.logp[seq] = 0.f;
-    }
-    return;
+// The sums of the strips [k0, k1) of a row.
+template <typename T>
+__device__ __forceinline__ void sum_strips(const SampleArgs& a, const RowUnits<T>& row, const Scale& c, int k0, int k1,
+                                           StripSum* to, int lane) {
+  for (int k = k0; k < k1; ++k) {
+    const int u0 = (int)min((int64_t)k * a.strip_units, (int64_t)row.units), u1 = min(u0 + a.strip_units, row.units);
+    const StripSum t = strip_sum<T>(row, c, u0, u1, lane);
+    if (lane == 0) __stcg(reinterpret_cast<float2*>(to) + k, make_float2(t.m, t.s));
   }
-  const int64_t row0 = lo + seq;  // the sequence's first row
-  const bool both = kDrafts && a.draft != nullptr && a.draft_logp == nullptr;  // rows of both models a round
-  const int set = a.round * a.strips;
-  const int strip0 = rank * a.strips;
-  auto exchange = [&] {
-    if (a.cluster > 1) cluster_sync();
-    else __syncthreads();
+}
+
+// Whether the calling warp's piece is the last of `all`; what the other warps wrote is then
+// visible to every lane.
+__device__ __forceinline__ bool last_piece(uint32_t* done, uint32_t all, int lane) {
+  uint32_t before = 0;
+  if (lane == 0) {
+    __threadfence();
+    before = atomicAdd(done, 1u);
+  }
+  const bool last = __shfl_sync(0xFFFFFFFFu, before, 0) == all - 1;
+  if (last) __threadfence();
+  return last;
+}
+
+// Clears the counters and finds the longest sequence.
+constexpr int kSetupThreads = 1024;
+__global__ void __launch_bounds__(kSetupThreads) setup_kernel(const __grid_constant__ SampleArgs a) {
+  griddep_launch_dependents();
+  __shared__ long long most[kSetupThreads / 32];
+  long long n = 0;
+  for (int64_t s = threadIdx.x; s < a.n_seqs; s += kSetupThreads) {
+    n = max(n, (long long)sequence_of(a, s).n);
+    a.q_done[s] = 0;
+    a.refused[s] = 0;
+  }
+  for (int64_t r = threadIdx.x; r < a.n_drafts + a.n_seqs; r += kSetupThreads) a.done[r] = 0;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) n = max(n, __shfl_xor_sync(0xFFFFFFFFu, n, o));
+  if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = n;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int k = 1; k < kSetupThreads / 32; ++k) n = max(n, most[k]);
+    *a.longest = n;
+  }
+}
+
+// Strip sums of sampled rows.
+template <typename T>
+__global__ void __launch_bounds__(kSampleWarps * 32, kSampleCtas) rows_kernel(const __grid_constant__ SampleArgs a) {
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5), jobs = a.n_seqs * a.pieces;
+  for (int64_t job = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); job < jobs; job += warps) {
+    const int64_t t = job / a.pieces;
+    if (a.mask != nullptr && a.mask[t] == 0) continue;
+    const int k0 = (int)(job - t * a.pieces) * a.each;
+    const RowUnits<T> row(a.target, t, a.target_stride, a.vocab);
+    sum_strips<T>(a, row, a.target_scale, k0, min(k0 + a.each, a.strips), a.p + t * a.strips, lane);
+  }
+}
+
+// Strip sums of the target's rows (and, where `both`, of the draft model's), position by
+// position over all sequences, and the verdict on each draft.
+template <typename T>
+__global__ void __launch_bounds__(kSampleWarps * 32, kSampleCtas) verify_kernel(const __grid_constant__ SampleArgs a) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5);
+  const int sets = a.both ? 2 : 1, per_row = a.pieces * sets;
+  const int64_t jobs = (__ldcg(a.longest) + 1) * a.n_seqs * per_row;
+  // a job's sequence and what is known of it are read while the job before is worked on
+  int64_t job = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  int64_t i = 0, s = 0;
+  int piece = 0;
+  Sequence q{0, -1};
+  uint32_t refused = 0;
+  auto look = [&](int64_t j) {
+    if (j >= jobs) return;
+    const int64_t r = j / per_row;
+    piece = (int)(j - r * per_row);
+    i = r / a.n_seqs;
+    s = r - i * a.n_seqs;
+    q = sequence_of(a, s);
+    refused = __ldcg(a.refused + s);
   };
-  auto units_of = [&](const RowUnits<T>& row, int k, int& u0, int& u1) {  // of this CTA's strip k
-    u0 = (int)min((int64_t)(strip0 + k) * a.strip_units, (int64_t)row.units);
+  look(job);
+  while (job < jobs) {
+    const int64_t at = i, seq = s;
+    const Sequence own = q;
+    const bool of_draft = piece >= a.pieces;
+    const int k0 = (of_draft ? piece - a.pieces : piece) * a.each;
+    const uint32_t known = refused;
+    job += warps;
+    look(job);
+    // no such row, or one behind a refused draft
+    if (at > own.n || (known != 0 && (int64_t)(0x7FFFFFFFu - known) < at)) continue;
+    const int64_t r = own.lo + seq + at, d = own.lo + at;
+    if (of_draft) {
+      if (at == own.n) continue;
+      const RowUnits<T> row(a.draft, d, a.draft_stride, a.vocab);
+      sum_strips<T>(a, row, a.draft_scale, k0, min(k0 + a.each, a.strips), a.q + d * a.strips, lane);
+    } else {
+      const RowUnits<T> row(a.target, r, a.target_stride, a.vocab);
+      sum_strips<T>(a, row, a.target_scale, k0, min(k0 + a.each, a.strips), a.p + r * a.strips, lane);
+    }
+    if (!last_piece(a.done + r, at < own.n ? per_row : a.pieces, lane)) continue;
+    const RowSum p = row_sum(a, a.p + r * a.strips, a.target_scale, lane);
+    if (lane == 0) a.p_total[r] = p;
+    if (at == own.n) continue;
+    RowSum dq{1., 0.f};
+    if (a.both) {
+      dq = row_sum(a, a.q + d * a.strips, a.draft_scale, lane);
+      if (lane == 0) a.q_total[d] = dq;
+    }
+    if (lane == 0) {
+      const int64_t y = a.drafts[d];
+      bool ok = usable(p) && usable(dq) && y >= 0 && y < a.vocab;
+      if (ok) {
+        const float x = Vec<T>::load(reinterpret_cast<const T*>(a.target) + r * a.target_stride + y) - p.m;
+        const float logp = __fmaf_rn(x, a.target_scale.inv_hi, x * a.target_scale.inv_lo) - logf((float)p.s);
+        float logq = a.draft_logp != nullptr ? a.draft_logp[d] : 0.f;
+        if (a.both) {
+          const float z = Vec<T>::load(reinterpret_cast<const T*>(a.draft) + d * a.draft_stride + y) - dq.m;
+          logq = __fmaf_rn(z, a.draft_scale.inv_hi, z * a.draft_scale.inv_lo) - logf((float)dq.s);
+        }
+        ok = a.accept_u[d] < expf(logp - logq);
+      }
+      if (!ok) atomicMax(a.refused + seq, 0x7FFFFFFFu - (uint32_t)at);
+    }
+  }
+}
+
+// Where sequence s stopped: its drafts, the number of them that were taken, whether the next
+// was refused.
+struct Stop {
+  Sequence q;
+  int64_t taken;
+  bool refused;
+};
+__device__ __forceinline__ Stop stop_of(const SampleArgs& a, int64_t s) {
+  Stop r;
+  r.q = sequence_of(a, s);
+  const uint32_t known = __ldcg(a.refused + s);
+  r.refused = known != 0;
+  r.taken = known ? (int64_t)(0x7FFFFFFFu - known) : r.q.n;
+  return r;
+}
+
+// Strip sums of the draft model's row at each refused draft.
+template <typename T>
+__global__ void __launch_bounds__(kSampleWarps * 32, kSampleCtas) refused_kernel(const __grid_constant__ SampleArgs a) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5), jobs = a.n_seqs * a.pieces;
+  for (int64_t job = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); job < jobs; job += warps) {
+    const int64_t s = job / a.pieces;
+    const Stop e = stop_of(a, s);
+    if (!e.refused) continue;
+    const int k0 = (int)(job - s * a.pieces) * a.each;
+    const RowUnits<T> row(a.draft, e.q.lo + e.taken, a.draft_stride, a.vocab);
+    sum_strips<T>(a, row, a.draft_scale, k0, min(k0 + a.each, a.strips), a.q + s * a.strips, lane);
+    if (!last_piece(a.q_done + s, a.pieces, lane)) continue;
+    const RowSum q = row_sum(a, a.q + s * a.strips, a.draft_scale, lane);
+    if (lane == 0) a.q_total[s] = q;
+  }
+}
+
+__device__ __forceinline__ Refused refused_of(const SampleArgs& a, const Stop& e, int64_t s, bool* fine) {
+  const RowSum p = load_total(a.p_total + e.q.lo + s + e.taken);
+  const RowSum q = load_total(a.q_total + (a.both ? e.q.lo + e.taken : s));
+  *fine = usable(p) && usable(q);
+  return Refused{p.m, (float)(1. / p.s), q.m, (float)(1. / q.s)};
+}
+
+// Strip sums of max(p - q, 0) at each refused draft.
+template <typename T>
+__global__ void __launch_bounds__(kSampleWarps * 32, 3) left_kernel(const __grid_constant__ SampleArgs a) {
+  constexpr int N = Vec<T>::N;
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5), jobs = a.n_seqs * a.pieces;
+  for (int64_t job = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); job < jobs; job += warps) {
+    const int64_t s = job / a.pieces;
+    const Stop e = stop_of(a, s);
+    if (!e.refused) continue;
+    bool fine;
+    const Refused f = refused_of(a, e, s, &fine);
+    if (!fine) continue;
+    const RowUnits<T> row(a.target, e.q.lo + s + e.taken, a.target_stride, a.vocab);
+    const RowUnits<T> draft(a.draft, e.q.lo + e.taken, a.draft_stride, a.vocab);
+    const int k0 = (int)(job - s * a.pieces) * a.each;
+    for (int k = k0; k < min(k0 + a.each, a.strips); ++k) {
+      const int u0 = (int)min((int64_t)k * a.strip_units, (int64_t)row.units), u1 = min(u0 + a.strip_units, row.units);
+      float sum = 0.f;
+      for (int u = u0; u < u1; u += kStripStep) {
+        float r[kLoads * N];
+        left_over<T>(a, f, row, draft.z, u + lane, 32, u1, step_inside<T>(row, u, u1), r);
+#pragma unroll
+        for (int i = 0; i < kLoads * N; ++i) sum += r[i];
+      }
+      sum = warp_sum(sum);
+      if (lane == 0) __stcg(a.left + s * a.strips + k, sum);
+    }
+  }
+}
+
+// The weights that a token is drawn from.
+enum Weights {
+  kPlain,    // p
+  kWithout,  // p without the refused draft
+  kLeft,     // max(p - q, 0)
+};
+
+// Draws the token of a row; the warp's lanes get the same token and log p.
+template <typename T>
+__device__ __forceinline__ void draw(const SampleArgs& a, int64_t r, int64_t s, int kind, int64_t without, const T* zq,
+                                     const Refused& f, float u, int64_t* token, float* logp, int lane) {
+  constexpr int N = Vec<T>::N;
+  const RowUnits<T> row(a.target, r, a.target_stride, a.vocab);
+  const Scale& c = a.target_scale;
+  const float2* strips = reinterpret_cast<const float2*>(a.p + r * a.strips);
+  *token = -1;
+  *logp = NAN;
+  // a lane's strips are consecutive ones
+  const int per = (a.strips + 31) / 32, k0 = min(lane * per, a.strips), k1 = min(k0 + per, a.strips);
+  float m = -INFINITY;
+  for (int k = k0; k < k1; ++k) m = fmaxf(m, __ldcg(strips + k).x);
+  m = warp_max(m);
+  auto plain = [&](int k) {
+    const float2 x = __ldcg(strips + k);
+    return (double)(x.y * factor(c, x.x, m));
+  };
+  auto bounds = [&](int k, int& u0, int& u1) {
+    u0 = (int)min((int64_t)k * a.strip_units, (int64_t)row.units);
     u1 = min(u0 + a.strip_units, row.units);
   };
-  // sums a row's slices: warp-wide, the same in every lane
-  auto merge = [&](const RowSum* slice, const Scale& c) {
-    RowSum t{0., -INFINITY};
-    if (lane < a.cluster) t = load_peer(slice, lane, rank);
-    RowSum r;
-    r.m = warp_max(t.m);
-    r.s = warp_sum64(t.s * (double)factor(c, t.m, r.m));
-    return r;
-  };
-  auto slice_sum = [&](const StripSum* table, const Scale& c) {
-    float m = -INFINITY;
-    for (int k = lane; k < a.strips; k += 32) m = fmaxf(m, table[k].m);
-    RowSum r;
-    r.m = warp_max(m);
-    r.s = 0.;
-    for (int k = lane; k < a.strips; k += 32) r.s += (double)(table[k].s * factor(c, table[k].m, r.m));
-    r.s = warp_sum64(r.s);
-    return r;
-  };
-  // each lane's part of a row's sum without the strip k0 of this CTA
-  auto other_strips = [&](const StripSum* table, const RowSum* slice, int k0, float m, const Scale& c) {
-    double s = 0.;
-    for (int k = lane; k < a.strips; k += 32)
-      if (k != k0) s += (double)(table[k].s * factor(c, table[k].m, m));
-    if (lane < a.cluster && lane != rank) {
-      const RowSum t = load_peer(slice, lane, rank);
-      s += t.s * (double)factor(c, t.m, m);
-    }
-    return s;
-  };
-
-  int parity = 0, at = 0;  // at: the last row's place in its round
-  int64_t base = 0, taken = 0;
-  bool refused = false;
-  StripSum* table = tables;
-  for (;; base += a.round, parity ^= 1) {
-    const int rows = (int)min((int64_t)a.round, n + 1 - base);
-    table = tables + (size_t)parity * 2 * set;
-    // the drafts' scalars are on their way while the rows are read
-    int64_t y = -1;
-    float u = 0.f, zy = -INFINITY, logq = 0.f;
-    const bool draft_lane = kDrafts && lane < rows && base + lane < n;
-    if (draft_lane) {
-      const int64_t d = lo + base + lane;
-      y = a.drafts[d];
-      u = a.accept_u[d];
-      if (y < 0 || y >= a.vocab) y = -1;
-      if (y >= 0) {
-        zy = Vec<T>::load(reinterpret_cast<const T*>(a.target) + (row0 + base + lane) * a.target_stride + y);
-        if (both) logq = Vec<T>::load(reinterpret_cast<const T*>(a.draft) + d * a.draft_stride + y);
-        else if (a.draft_logp != nullptr) logq = a.draft_logp[d];
-      }
-    }
-    const int drafted = both ? (int)min((int64_t)rows, n - base) : 0;
-    for (int job = warp; job < (rows + drafted) * a.strips; job += warps) {
-      const int r = job / a.strips, k = job - r * a.strips;
-      const bool q = r >= rows;
-      const RowUnits<T> row(q ? a.draft : a.target, q ? lo + base + r - rows : row0 + base + r,
-                            q ? a.draft_stride : a.target_stride, a.vocab);
-      int u0, u1;
-      units_of(row, k, u0, u1);
-      const StripSum t = strip_sum<T>(row, q ? a.draft_scale : a.target_scale, u0, u1, lane);
-      if (lane == 0) table[(q ? set + (r - rows) * a.strips : r * a.strips) + k] = t;
-    }
-    __syncthreads();
-    for (int r = warp; r < rows + drafted; r += warps) {
-      const bool q = r >= rows;
-      const RowSum t = slice_sum(table + (q ? set + (r - rows) * a.strips : r * a.strips),
-                                 q ? a.draft_scale : a.target_scale);
-      if (lane == 0) sh.slice[parity][q ? kMaxRound + r - rows : r] = t;
-    }
-    exchange();
-    for (int r = warp; r < rows + drafted; r += warps) {
-      const bool q = r >= rows;
-      const int slot = q ? kMaxRound + r - rows : r;
-      const RowSum t = merge(&sh.slice[parity][slot], q ? a.draft_scale : a.target_scale);
-      if (lane == 0) sh.total[parity][slot] = t;
-    }
-    __syncthreads();
-    at = rows - 1;
-    if (!kDrafts) break;
-    // every warp of every CTA decides alike
-    bool ok = true;
-    if (draft_lane) {
-      const RowSum p = sh.total[parity][lane];
-      const Scale& c = a.target_scale;
-      const float d = zy - p.m;
-      const float logp = __fmaf_rn(d, c.inv_hi, d * c.inv_lo) - logf((float)p.s);
-      bool fine = usable(p) && y >= 0;
-      if (both) {
-        const RowSum q = sh.total[parity][kMaxRound + lane];
-        const float e = logq - q.m;
-        logq = __fmaf_rn(e, a.draft_scale.inv_hi, e * a.draft_scale.inv_lo) - logf((float)q.s);
-        fine = fine && usable(q);
-      }
-      ok = fine && u < expf(logp - logq);
-    }
-    const unsigned bad = __ballot_sync(0xFFFFFFFFu, !ok);
-    refused = bad != 0;
-    if (refused) at = __ffs(bad) - 1;
-    // rows of this round whose drafts were taken
-    const int good = (int)min(refused ? (int64_t)at : (int64_t)rows, n - base);
-    for (int r = 0; r < good; ++r) {
-      const int64_t t = __shfl_sync(0xFFFFFFFFu, y, r);
-      if ((base + r) % warps != warp) continue;
-      const RowUnits<T> row(a.target, row0 + base + r, a.target_stride, a.vocab);
-      const int k = ((int)t + row.shift) / N / a.strip_units - strip0;
-      if (k < 0 || k >= a.strips) continue;  // another CTA's strip
-      int u0, u1;
-      units_of(row, k, u0, u1);
-      const float m = sh.total[parity][r].m;
-      const double rest = other_strips(table + r * a.strips, &sh.slice[parity][r], k, m, a.target_scale);
-      const float lp = token_logp<T>(row, a.target_scale, m, rest, u0, u1, (int)t, lane);
-      if (lane == 0) {
-        a.tokens[row0 + base + r] = t;
-        a.logp[row0 + base + r] = lp;
-      }
-    }
-    taken = base + good;
-    if (refused || base + rows == n + 1) break;
-  }
-
-  // the token after the drafts that were taken, from row `taken`
-  const RowUnits<T> row(a.target, row0 + taken, a.target_stride, a.vocab);
-  const RowSum p = sh.total[parity][at];
-  const StripSum* own = table + at * a.strips;
-  const Scale& c = a.target_scale;
-  bool fine = usable(p);
-  // weights of the strips: kPlain p in its frame; kWithout p without the refused draft;
-  // kLeft max(p - q, 0)
-  enum { kPlain, kWithout, kLeft };
-  int kind = kPlain;
-  int64_t without = -1;
-  Refused f{};
-  const T* zq = nullptr;
-  StripSum* left = table + set + at * a.strips;  // of the draft model's row, then of the difference
+  double own = 0.;  // of p
+  for (int k = k0; k < k1; ++k) own += plain(k);
+  const RowSum p{warp_sum64(own), m};
+  if (!usable(p)) return;
   int without_strip = -1;
   float without_sum = 0.f;
-  if (kDrafts && refused && fine) {
-    const int64_t d = lo + taken;
-    if (a.draft == nullptr) {
-      kind = kWithout;
-      without = a.drafts[d];
-      if (without >= 0 && without < a.vocab) {
-        const int k = ((int)without + row.shift) / N / a.strip_units - strip0;
-        if (k >= 0 && k < a.strips) {  // every warp sums the strip alike
-          int u0, u1;
-          units_of(row, k, u0, u1);
-          const float s = sum_without<T>(row, c, p.m, u0, u1, (int)without, lane);
-          without_strip = k;
-          without_sum = warp_sum(s);
-        }
-      }
-    } else {
-      kind = kLeft;
-      const RowUnits<T> draft(a.draft, d, a.draft_stride, a.vocab);
-      zq = draft.z;
-      RowSum q;
-      if (both) {
-        q = sh.total[parity][kMaxRound + at];
-      } else {
-        for (int k = warp; k < a.strips; k += warps) {
-          int u0, u1;
-          units_of(draft, k, u0, u1);
-          const StripSum t = strip_sum<T>(draft, a.draft_scale, u0, u1, lane);
-          if (lane == 0) left[k] = t;
-        }
-        __syncthreads();
-        if (warp == 0) {
-          const RowSum t = slice_sum(left, a.draft_scale);
-          if (lane == 0) sh.slice[parity][kMaxRound] = t;
-        }
-        exchange();
-        q = merge(&sh.slice[parity][kMaxRound], a.draft_scale);
-      }
-      fine = usable(q);
-      f = Refused{p.m, (float)(1. / p.s), q.m, (float)(1. / q.s)};
-      if (fine) {
-        for (int k = warp; k < a.strips; k += warps) {
-          int u0, u1;
-          units_of(row, k, u0, u1);
-          float s = 0.f;
-          for (int u = u0; u < u1; u += kStripStep) {
-            float r[kLoads * N];
-            left_over<T>(a, f, row, zq, u + lane, 32, u1, step_inside<T>(row, u, u1), r);
-#pragma unroll
-            for (int i = 0; i < kLoads * N; ++i) s += r[i];
-          }
-          s = warp_sum(s);
-          if (lane == 0) left[k] = StripSum{0.f, s};
-        }
-        __syncthreads();
-      }
+  if (kind == kWithout && without >= 0 && without < a.vocab) {
+    without_strip = ((int)without + row.shift) / N / a.strip_units;
+    int u0, u1;
+    bounds(without_strip, u0, u1);
+    without_sum = warp_sum(sum_without<T>(row, c, m, u0, u1, (int)without, lane));
+  }
+  auto weight = [&](int k) {
+    if (kind == kLeft) return (double)__ldcg(a.left + s * a.strips + k);
+    return kind == kWithout && k == without_strip ? (double)without_sum : plain(k);
+  };
+  double w = own;
+  if (kind != kPlain) {
+    w = 0.;
+    for (int k = k0; k < k1; ++k) w += weight(k);
+    // nothing is left over where the two models agree, and the refusal was one of rounding
+    if (!__any_sync(0xFFFFFFFFu, w > 0.)) {
+      kind = kPlain;
+      w = own;
     }
   }
+  const double end = warp_scan64(w, lane), sum = __shfl_sync(0xFFFFFFFFu, end, 31);
+  u = fmaxf(u, 0.f);
+  const double t = u < 1.f ? (double)u * sum : (double)INFINITY;  // 1 and above: the last token
+  const unsigned above = __ballot_sync(0xFFFFFFFFu, w > 0. && end > t);
+  const unsigned some = __ballot_sync(0xFFFFFFFFu, w > 0.);
+  const int l = above ? __ffs(above) - 1 : 31 - __clz(some);
+  double before = end - w, begun = before;
+  int strip = 0;
+  for (int k = k0; k < k1; ++k) {
+    const double x = weight(k);
+    if (x > 0.) {
+      strip = k;
+      begun = before;
+      if (before + x > t) break;
+    }
+    before += x;
+  }
+  strip = __shfl_sync(0xFFFFFFFFu, strip, l);
+  before = __shfl_sync(0xFFFFFFFFu, begun, l);
+  int u0, u1;
+  bounds(strip, u0, u1);
+  const int found = pick_element<T>(row, u0, u1, t - before, lane, [&](int first, bool inside, float(&w)[kLoads * N]) {
+    if (kind == kLeft) {
+      left_over<T>(a, f, row, zq, first, 1, u1, inside, w);
+      return;
+    }
+    uint4 z[kLoads];
+    load_units<T>(row, first, 1, u1, inside, z);
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) {
+      float e[N];
+      exps<T>(c, m, z[k], e);
+#pragma unroll
+      for (int i = 0; i < N; ++i) w[k * N + i] = kind == kWithout && row.first(first + k) + i == without ? 0.f : e[i];
+    }
+  });
+  if (found < 0) return;
+  // the lane's part of p without the token's strip
+  double rest = 0.;
+  for (int k = k0; k < k1; ++k)
+    if (k != strip) rest += plain(k);
+  *token = found;
+  *logp = token_logp<T>(row, c, m, rest, u0, u1, found, lane);
+}
 
-  if (warp != 0) return;  // the cluster's barriers wait for the warps that are left
-
+// Sampling: a warp draws a row's token.
+template <typename T>
+__global__ void __launch_bounds__(kSampleWarps * 32, 2) draw_kernel(const __grid_constant__ SampleArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int64_t t = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  griddep_wait();
+  if (t >= a.n_seqs) return;
   int64_t token = -1;
-  bool mine = rank == 0;  // this CTA writes the token
-  float lp = NAN;
-  if (fine) {
-    auto weight = [&](int k) {
-      if (kind == kLeft) return (double)left[k].s;
-      if (kind == kWithout && k == without_strip) return (double)without_sum;
-      return (double)(own[k].s * factor(c, own[k].m, p.m));
-    };
-    // each CTA's share of the weights in its lane, and their running sum
-    double v = 0.;
-    if (kind != kPlain) {
-      for (int k = lane; k < a.strips; k += 32) v += weight(k);
-      v = warp_sum64(v);
-      if (a.cluster > 1) {
-        if (lane == 0) sh.weights = v;
-        cluster_sync();
-        v = lane >= a.cluster ? 0. : lane == rank ? v : load_peer(&sh.weights, lane);
-      } else if (lane > 0) {
-        v = 0.;
+  float logp = 0.f;
+  if (a.mask == nullptr || a.mask[t] != 0)
+    draw<T>(a, t, t, kPlain, -1, nullptr, Refused{}, a.sample_u[t], &token, &logp, lane);
+  if (lane == 0) {
+    a.tokens[t] = token;
+    a.logp[t] = logp;
+  }
+}
+
+// Verification: a warp writes a row's token: a taken draft, the drawn one, or -1.
+template <typename T>
+__global__ void __launch_bounds__(kSampleWarps * 32, 2) emit_kernel(const __grid_constant__ SampleArgs a) {
+  constexpr int N = Vec<T>::N;
+  const int lane = threadIdx.x & 31;
+  griddep_wait();
+  const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5), jobs = (__ldcg(a.longest) + 1) * a.n_seqs;
+  for (int64_t job = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); job < jobs; job += warps) {
+    const int64_t i = job / a.n_seqs, s = job - i * a.n_seqs;
+    const Stop e = stop_of(a, s);
+    if (i > e.q.n) continue;
+    const int64_t r = e.q.lo + s + i, d = e.q.lo + i;
+    int64_t token = -1;
+    float logp = 0.f;
+    if (i < e.taken) {
+      token = a.drafts[d];
+      const RowUnits<T> row(a.target, r, a.target_stride, a.vocab);
+      const RowSum p = load_total(a.p_total + r);
+      const int strip = ((int)token + row.shift) / N / a.strip_units;
+      double rest = 0.;
+      for (int k = lane; k < a.strips; k += 32) {
+        const float2 x = __ldcg(reinterpret_cast<const float2*>(a.p + r * a.strips) + k);
+        if (k != strip) rest += (double)(x.y * factor(a.target_scale, x.x, p.m));
       }
-      // nothing is left over where the two models agree, and the refusal was one of rounding
-      if (!__any_sync(0xFFFFFFFFu, v > 0.)) kind = kPlain;
-    }
-    if (kind == kPlain) {
-      RowSum r{0., -INFINITY};
-      if (lane < a.cluster) r = load_peer(&sh.slice[parity][at], lane, rank);
-      v = r.s * (double)factor(c, r.m, p.m);
-    }
-    const double upto = warp_scan64(v, lane), sum = __shfl_sync(0xFFFFFFFFu, upto, 31);
-    const float su = fmaxf(a.sample_u[seq], 0.f);
-    const double t = su < 1.f ? (double)su * sum : (double)INFINITY;  // 1 and above: the last token
-    const unsigned over = __ballot_sync(0xFFFFFFFFu, v > 0. && upto > t);
-    const unsigned any = __ballot_sync(0xFFFFFFFFu, v > 0.);
-    const int owner = over ? __ffs(over) - 1 : 31 - __clz(any);
-    mine = rank == owner;
-    if (mine) {
-      // a lane takes consecutive strips
-      const int per = (a.strips + 31) / 32, k0 = lane * per, k1 = min(k0 + per, a.strips);
-      double w = 0.;
-      for (int k = k0; k < k1; ++k) w += weight(k);
-      const double end = __shfl_sync(0xFFFFFFFFu, upto - v, owner) + warp_scan64(w, lane);
-      const unsigned above = __ballot_sync(0xFFFFFFFFu, w > 0. && end > t);
-      const unsigned some = __ballot_sync(0xFFFFFFFFu, w > 0.);
-      const int l = above ? __ffs(above) - 1 : 31 - __clz(some);
-      double before = end - w;
-      int strip = -1;
-      double begun = before;
-      for (int k = k0; k < k1; ++k) {
-        const double x = weight(k);
-        if (x > 0.) {
-          strip = k;
-          begun = before;
-          if (before + x > t) break;
+      const int u0 = strip * a.strip_units;
+      logp = token_logp<T>(row, a.target_scale, p.m, rest, u0, min(u0 + a.strip_units, row.units), (int)token, lane);
+    } else if (i == e.taken) {
+      int kind = kPlain;
+      bool fine = true;
+      Refused f{};
+      const T* zq = nullptr;
+      if (e.refused) {
+        kind = kWithout;
+        if (a.draft != nullptr) {
+          kind = kLeft;
+          f = refused_of(a, e, s, &fine);
+          zq = reinterpret_cast<const T*>(a.draft) + d * a.draft_stride;
         }
-        before += x;
       }
-      strip = __shfl_sync(0xFFFFFFFFu, strip, l);
-      before = __shfl_sync(0xFFFFFFFFu, begun, l);
-      int u0, u1;
-      units_of(row, strip, u0, u1);
-      token = pick_element<T>(row, u0, u1, t - before, lane, [&](int first, bool inside, float(&w)[kLoads * N]) {
-        if (kind == kLeft) {
-          left_over<T>(a, f, row, zq, first, 1, u1, inside, w);
-          return;
-        }
-        uint4 z[kLoads];
-        load_units<T>(row, first, 1, u1, inside, z);
-#pragma unroll
-        for (int k = 0; k < kLoads; ++k) {
-          float e[N];
-          exps<T>(c, p.m, z[k], e);
-#pragma unroll
-          for (int i = 0; i < N; ++i) w[k * N + i] = kind == kWithout && row.first(first + k) + i == without ? 0.f : e[i];
-        }
-      });
-      if (token >= 0)
-        lp = token_logp<T>(row, c, p.m, other_strips(own, &sh.slice[parity][at], strip, p.m, c), u0, u1, (int)token, lane);
+      logp = NAN;
+      if (fine) draw<T>(a, r, s, kind, e.refused ? a.drafts[d] : -1, zq, f, a.sample_u[s], &token, &logp, lane);
+      if (lane == 0) a.counts[s] = e.taken;
+    }
+    if (lane == 0) {
+      a.tokens[r] = token;
+      a.logp[r] = logp;
     }
   }
-  if (mine && lane == 0) {
-    a.tokens[row0 + taken] = token;
-    a.logp[row0 + taken] = lp;
-  }
-  if (kDrafts && rank == 0) {
-    if (lane == 0) a.counts[seq] = taken;
-    for (int64_t r = taken + 1 + lane; r <= n; r += 32) {
-      a.tokens[row0 + r] = -1;
-      a.logp[row0 + r] = 0.f;
-    }
-  }
-  if (a.cluster > 1) cluster_sync();  // no CTA leaves while another may read its sums
 }
 
 // ---------------------------------------------------------------------------
@@ -668,43 +749,81 @@ int32_t check_rows(const muon_token_batch* b) {
   return MUON_OK;
 }
 
-// The launch's shape: CTAs a sequence, rows a round, strips and threads.
-int shape_of(SampleArgs& a, int64_t n_seqs, int64_t rows, int32_t dtype, int sms, size_t* smem) {
+// Strips of a row: their length and number.
+void strips_of(int64_t vocab, int32_t dtype, int32_t* units, int32_t* strips) {
   const int64_t per = dtype == MUON_DTYPE_BF16 ? 8 : 4;
-  const int64_t units = (2 * (per - 1) + a.vocab) / per;
-  const int64_t steps = (units + kStripStep - 1) / kStripStep;  // strips if there is room for them
-  int64_t cluster = 1;
-  while (cluster < kMaxCluster && n_seqs * cluster * 2 <= 4 * sms && steps > 2 * cluster) cluster *= 2;
-  const int64_t most = (rows + n_seqs - 1) / n_seqs;  // rows of a sequence, in the mean
-  a.cluster = (int32_t)cluster;
-  a.round = n_seqs * cluster <= sms ? (int32_t)(most < kMaxRound ? most : kMaxRound) : 1;
-  const int64_t table = kMaxTable / a.round;
-  const int64_t mult = (steps + cluster * table - 1) / (cluster * table);
-  a.strip_units = (int32_t)(mult * kStripStep);
-  const int64_t strips = (steps + mult - 1) / mult;
-  a.strips = (int32_t)((strips + cluster - 1) / cluster);
-  *smem = (size_t)4 * a.round * a.strips * sizeof(StripSum);
-  const int64_t jobs = (int64_t)a.round * a.strips;
-  const int64_t most_warps = n_seqs * cluster <= sms ? 16 : 8;
-  return (int)(32 * (jobs < most_warps ? jobs : most_warps));
+  const int64_t all = (2 * (per - 1) + vocab) / per, steps = (all + kStripStep - 1) / kStripStep;
+  const int64_t mult = (steps + kMaxStrips - 1) / kMaxStrips;
+  *units = (int32_t)(mult * kStripStep);
+  *strips = (int32_t)((steps + mult - 1) / mult);
+}
+
+// The workspace's parts, each on a 16-byte boundary; sampling needs the first alone.
+size_t sample_space(SampleArgs* a, void* base, int64_t n_drafts, int64_t n_seqs, int32_t strips, bool drafts) {
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    void* p = base ? static_cast<uint8_t*>(base) + at : nullptr;
+    at += (bytes + 15) / 16 * 16;
+    return p;
+  };
+  const size_t rows = (size_t)(n_drafts + n_seqs), q_rows = (size_t)(n_drafts > n_seqs ? n_drafts : n_seqs);
+  StripSum* p = static_cast<StripSum*>(take(rows * strips * sizeof(StripSum)));
+  if (a) a->p = p;
+  if (!drafts) return at;
+  SampleArgs none;
+  SampleArgs& o = a ? *a : none;
+  o.q = static_cast<StripSum*>(take(q_rows * strips * sizeof(StripSum)));
+  o.left = static_cast<float*>(take((size_t)n_seqs * strips * sizeof(float)));
+  o.p_total = static_cast<RowSum*>(take(rows * sizeof(RowSum)));
+  o.q_total = static_cast<RowSum*>(take(q_rows * sizeof(RowSum)));
+  o.done = static_cast<uint32_t*>(take(rows * sizeof(uint32_t)));
+  o.q_done = static_cast<uint32_t*>(take((size_t)n_seqs * sizeof(uint32_t)));
+  o.refused = static_cast<uint32_t*>(take((size_t)n_seqs * sizeof(uint32_t)));
+  o.longest = static_cast<int64_t*>(take(sizeof(int64_t)));
+  return at;
+}
+
+// Strips that a warp takes at a time: two where there are enough for every warp of the chip.
+void deal_out(SampleArgs& a, int64_t rows, int sms) {
+  const int64_t warps = (int64_t)sms * kSampleCtas * kSampleWarps;
+  a.each = rows * a.strips >= 8 * warps ? 2 : 1;
+  a.pieces = (a.strips + a.each - 1) / a.each;
+}
+
+// CTAs and warps of a CTA for `jobs` jobs of a warp: one warp an SM first.
+struct Launch {
+  int grid, block;
+};
+Launch launch_of(int64_t jobs, int sms) {
+  const int64_t per_sm = (jobs + sms - 1) / sms;
+  const int64_t warps = per_sm < 1 ? 1 : per_sm < kSampleWarps ? per_sm : kSampleWarps;
+  const int64_t ctas = (jobs + warps - 1) / warps, most = (int64_t)sms * kSampleCtas;
+  return Launch{(int)(ctas < 1 ? 1 : ctas < most ? ctas : most), (int)(32 * warps)};
 }
 
 template <typename T>
-cudaError_t launch_sample(const SampleArgs& a, bool drafts, int64_t n_seqs, int threads, size_t smem, cudaStream_t s) {
-  return launch(drafts ? sample_kernel<T, true> : sample_kernel<T, false>, (int)(n_seqs * a.cluster), threads, smem, s,
-                a.cluster, false, a);
+cudaError_t run_rows(const SampleArgs& a, int sms, cudaStream_t s) {
+  const Launch l = launch_of(a.n_seqs * a.pieces, sms);
+  cudaError_t e = launch(rows_kernel<T>, l.grid, l.block, 0, s, 1, false, a);
+  if (e != cudaSuccess) return e;
+  const int64_t warps = a.n_seqs < 4ll * sms ? 1 : 4;  // a row each
+  return launch(draw_kernel<T>, (int)((a.n_seqs + warps - 1) / warps), (int)(32 * warps), 0, s, 1, true, a);
 }
 
-int32_t run_sample(SampleArgs& a, bool drafts, int64_t n_seqs, int64_t rows, int32_t dtype, void* stream) {
-  int sms;
-  const int32_t st = find_device(&sms);
-  if (st != MUON_OK) return st;
-  size_t smem;
-  const int threads = shape_of(a, n_seqs, rows, dtype, sms, &smem);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = dtype == MUON_DTYPE_BF16 ? launch_sample<__nv_bfloat16>(a, drafts, n_seqs, threads, smem, s)
-                                                 : launch_sample<float>(a, drafts, n_seqs, threads, smem, s);
-  return e == cudaSuccess ? MUON_OK : cuda_error(e);
+template <typename T>
+cudaError_t run_verify(const SampleArgs& a, int sms, cudaStream_t s) {
+  const int64_t rows = a.n_drafts + a.n_seqs;
+  cudaError_t e = launch(setup_kernel, 1, kSetupThreads, 0, s, 1, false, a);
+  if (e != cudaSuccess) return e;
+  const Launch all = launch_of((rows + (a.both ? a.n_drafts : 0)) * a.pieces, sms);
+  if ((e = launch(verify_kernel<T>, all.grid, all.block, 0, s, 1, true, a)) != cudaSuccess) return e;
+  if (a.draft != nullptr && a.n_drafts > 0) {
+    const Launch one = launch_of(a.n_seqs * a.pieces, sms);
+    if (!a.both && (e = launch(refused_kernel<T>, one.grid, one.block, 0, s, 1, true, a)) != cudaSuccess) return e;
+    if ((e = launch(left_kernel<T>, one.grid, one.block, 0, s, 1, true, a)) != cudaSuccess) return e;
+  }
+  const Launch out = launch_of(rows, sms);
+  return launch(emit_kernel<T>, out.grid, out.block, 0, s, 1, true, a);
 }
 
 }  // namespace
@@ -714,10 +833,21 @@ using namespace muon;
 
 extern "C" {
 
+muon_status muon_sample_workspace_bytes(int64_t rows, int64_t n_seqs, int64_t vocab, int32_t dtype, size_t* bytes) {
+  if (!bytes) return invalid("bytes is NULL");
+  if (rows < 0 || rows > (1ll << 31) - 1 || n_seqs < 0 || n_seqs > rows) return invalid("rows must be in [0, 2^31), n_seqs in [0, rows]");
+  if (vocab < 1 || vocab > (1ll << 30)) return invalid("vocab must be in [1, 2^30]");
+  if (dtype != MUON_DTYPE_F32 && dtype != MUON_DTYPE_BF16) return invalid("unknown logits dtype");
+  int32_t units, strips;
+  strips_of(vocab, dtype, &units, &strips);
+  *bytes = sample_space(nullptr, nullptr, rows - n_seqs, n_seqs, strips, true);
+  return MUON_OK;
+}
+
 muon_status muon_sample_tokens(const muon_token_batch* batch, const float* uniforms, int64_t* tokens, float* logp,
-                               void* stream) {
+                               void* workspace, size_t workspace_bytes, void* stream) {
   if (!batch) return invalid("batch is NULL");
-  const int32_t st = check_rows(batch);
+  int32_t st = check_rows(batch);
   if (st != MUON_OK) return st;
   if (batch->tokens == 0) return MUON_OK;
   if (!batch->logits) return invalid("logits is NULL");
@@ -733,13 +863,22 @@ muon_status muon_sample_tokens(const muon_token_batch* batch, const float* unifo
   a.logp = logp;
   a.target_scale = a.draft_scale = scale_of(batch->temperature);
   a.vocab = (int32_t)batch->vocab;
-  return run_sample(a, false, batch->tokens, batch->tokens, batch->dtype, stream);
+  a.n_seqs = batch->tokens;
+  strips_of(a.vocab, batch->dtype, &a.strip_units, &a.strips);
+  const size_t need = sample_space(&a, workspace, 0, a.n_seqs, a.strips, false);
+  if ((st = check_workspace(workspace, workspace_bytes, need)) != MUON_OK) return st;
+  int sms;
+  if ((st = find_device(&sms)) != MUON_OK) return st;
+  deal_out(a, a.n_seqs, sms);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = batch->dtype == MUON_DTYPE_BF16 ? run_rows<__nv_bfloat16>(a, sms, s) : run_rows<float>(a, sms, s);
+  return e == cudaSuccess ? MUON_OK : cuda_error(e);
 }
 
 muon_status muon_verify_drafts(const muon_token_batch* target, const muon_token_batch* draft, const float* draft_logp,
                                const int64_t* draft_offsets, int64_t n_seqs, const float* accept_uniforms,
                                const float* sample_uniforms, int64_t* tokens, int64_t* counts, float* logp,
-                               void* stream) {
+                               void* workspace, size_t workspace_bytes, void* stream) {
   if (!target || !draft) return invalid("target or draft is NULL");
   int32_t st = check_rows(target);
   if (st == MUON_OK) st = check_rows(draft);
@@ -775,7 +914,17 @@ muon_status muon_verify_drafts(const muon_token_batch* target, const muon_token_
   a.target_scale = scale_of(target->temperature);
   a.draft_scale = scale_of(draft->temperature);
   a.vocab = (int32_t)target->vocab;
-  return run_sample(a, true, n_seqs, target->tokens, target->dtype, stream);
+  a.n_seqs = n_seqs;
+  a.both = draft->logits && !draft_logp;
+  strips_of(a.vocab, target->dtype, &a.strip_units, &a.strips);
+  const size_t need = sample_space(&a, workspace, a.n_drafts, n_seqs, a.strips, true);
+  if ((st = check_workspace(workspace, workspace_bytes, need)) != MUON_OK) return st;
+  int sms;
+  if ((st = find_device(&sms)) != MUON_OK) return st;
+  deal_out(a, target->tokens, sms);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = target->dtype == MUON_DTYPE_BF16 ? run_verify<__nv_bfloat16>(a, sms, s) : run_verify<float>(a, sms, s);
+  return e == cudaSuccess ? MUON_OK : cuda_error(e);
 }
 
 }  // extern "C"

@@ -28,25 +28,28 @@ def _batch(nsm, **over):
     dict(logits=A + 2), dict(logits=A + 1, dtype=1)])
 def test_sample_refuses_bad_batches(nsm, over):
     b = _batch(nsm, **over)
-    assert nsm.lib.muon_sample_tokens(ctypes.byref(b), A, A, A, None) == nsm.MUON_ERR_INVALID
+    assert nsm.lib.muon_sample_tokens(ctypes.byref(b), A, A, A, A, 1 << 40, None) == nsm.MUON_ERR_INVALID
 
 
 def test_sample_refuses_bad_arguments(nsm):
     call, b = nsm.lib.muon_sample_tokens, _batch(nsm)
     ref = ctypes.byref(b)
-    assert call(None, A, A, A, None) == nsm.MUON_ERR_INVALID
+    assert call(None, A, A, A, A, 1 << 40, None) == nsm.MUON_ERR_INVALID
     for args in ((None, A, A), (A, None, A), (A, A, None), (A + 2, A, A), (A, A + 4, A), (A, A, A + 1)):
-        assert call(ref, *args, None) == nsm.MUON_ERR_INVALID
+        assert call(ref, *args, A, 1 << 40, None) == nsm.MUON_ERR_INVALID
+    assert call(ref, A, A, A, None, 1 << 40, None) == nsm.MUON_ERR_NO_WORKSPACE
+    assert call(ref, A, A, A, A, 5, None) == nsm.MUON_ERR_NO_WORKSPACE
+    assert call(ref, A, A, A, A + 8, 1 << 40, None) == nsm.MUON_ERR_INVALID
     empty = _batch(nsm, tokens=0, logits=None)
-    assert call(ctypes.byref(empty), None, None, None, None) == nsm.MUON_OK
+    assert call(ctypes.byref(empty), None, None, None, None, 0, None) == nsm.MUON_OK
 
 
 def _verify(nsm, target=None, draft=None, n_seqs=2, draft_logp=None, offsets=A, accept=A, sample=A, tokens=A, counts=A,
-            logp=A):
+            logp=A, ws=A, nbytes=1 << 40):
     t = _batch(nsm, **{"targets": None, **(target or {})})
     d = _batch(nsm, **{"tokens": 4, **(draft or {})})
     return nsm.lib.muon_verify_drafts(ctypes.byref(t), ctypes.byref(d), draft_logp, offsets, n_seqs, accept, sample,
-                                      tokens, counts, logp, None)
+                                      tokens, counts, logp, ws, nbytes, None)
 
 
 @pytest.mark.parametrize("over", [
@@ -62,9 +65,27 @@ def test_verify_refuses(nsm, over):
 
 
 def test_verify_of_nothing(nsm):
-    assert nsm.lib.muon_verify_drafts(None, None, None, None, 0, None, None, None, None, None, None) == nsm.MUON_ERR_INVALID
+    assert nsm.lib.muon_verify_drafts(None, None, None, None, 0, None, None, None, None, None, None, 0, None) == nsm.MUON_ERR_INVALID
     assert _verify(nsm, dict(tokens=0, logits=None), dict(tokens=0, logits=None), 0, None, None, None, None, None, None,
                    None) == nsm.MUON_OK
+
+
+def test_workspace(nsm):
+    import torch
+    need = nsm.muon_sample_workspace_bytes
+    assert need(0, 0, 5, torch.float32) < 64
+    assert need(10, 10, 1000, torch.float32) >= 10 * 2 * 8            # two strips of 512 a row
+    assert need(1 << 20, 1 << 20, 1 << 30, torch.bfloat16) < 20 << 30   # 512 strips at most
+    assert need(10, 2, 1000, torch.bfloat16) < need(20, 4, 1000, torch.bfloat16)
+    for bad in ((-1, 0, 5), (1 << 31, 0, 5), (5, 6, 5), (5, -1, 5), (5, 5, 0), (5, 5, (1 << 30) + 1)):
+        with pytest.raises(nsm.MuonError) as e:
+            need(*bad, torch.float32)
+        assert e.value.status == nsm.MUON_ERR_INVALID
+    with pytest.raises(TypeError):
+        need(5, 5, 5, torch.float16)
+    assert _verify(nsm, ws=None) == nsm.MUON_ERR_NO_WORKSPACE
+    assert _verify(nsm, nbytes=16) == nsm.MUON_ERR_NO_WORKSPACE
+    assert _verify(nsm, ws=A + 8) == nsm.MUON_ERR_INVALID
 
 
 def test_binding_refuses_host_tensors(nsm):
