@@ -458,10 +458,8 @@ typedef struct {
  * taken. */
 muon_status muon_token_logprobs(const muon_token_batch* batch, float* logp, void* stream);
 
-/* Workspace of muon_sample_tokens (n_seqs = rows) and muon_verify_drafts (rows: the target's,
- * n_drafts + n_seqs) in bytes.  Host work. */
-muon_status muon_sample_workspace_bytes(int64_t rows, int64_t n_seqs, int64_t vocab, int32_t dtype,
-                                        size_t* bytes);
+/* Workspace of muon_sample_tokens (bytes).  Host work. */
+muon_status muon_sample_workspace_bytes(int64_t tokens, int64_t vocab, int32_t dtype, size_t* bytes);
 
 /* A token for each row of logits, drawn with a given uniform number: p = softmax(logits /
  * temperature), the first token j with sum_{i <= j} p_i > uniforms[t] sum_i p_i.
@@ -498,12 +496,11 @@ muon_status muon_sample_tokens(const muon_token_batch* batch, const float* unifo
  *   logp: [n_drafts + n_seqs] fp32, log p of the tokens, 0 where they are -1 (the old_logp
  *     of muon_policy_loss, whose mask is tokens >= 0).
  * Rows without probabilities refuse their draft, and the token drawn there is -1, its logp
- * NaN. */
+ * NaN.  No workspace. */
 muon_status muon_verify_drafts(const muon_token_batch* target, const muon_token_batch* draft,
                                const float* draft_logp, const int64_t* draft_offsets, int64_t n_seqs,
                                const float* accept_uniforms, const float* sample_uniforms,
-                               int64_t* tokens, int64_t* counts, float* logp, void* workspace,
-                               size_t workspace_bytes, void* stream);
+                               int64_t* tokens, int64_t* counts, float* logp, void* stream);
 
 /* Workspace of muon_policy_loss and muon_preference_loss (bytes).  Host work. */
 muon_status muon_loss_workspace_bytes(int64_t tokens, int64_t n_seqs, size_t* bytes);

@@ -13,12 +13,15 @@
 // that a row is read once.  A refused draft's row is read twice, since the difference of the
 // probabilities needs both rows' normalisers first.
 //
-// Strips of all rows are dealt out to the warps of the whole chip alike, a few strips a time,
-// and a small kernel draws the tokens afterwards, a warp a row: with a CTA a row, 2048 rows of
-// 131072 bf16 logits took 117 us (the ends of rows, and 3.03 rounds of CTAs that took 4), ROWS_US so.
-// Drafts are verified position by position: the warp that finishes a row decides on its
-// draft, and later rows of a sequence whose draft was refused are left out as far as that is
-// known when their turn comes.  (What is left out changes no result.)
+// Sampling: the strips of all rows are dealt out to the warps of the whole chip alike, and a
+// second kernel draws the tokens, a warp a row.  (With a CTA a row 2048 rows of 131072 bf16
+// logits took 117 us: the ends of rows, and 3.03 rounds of CTAs that took 4.  ROWS_US so.)
+//
+// Verification: a cluster of CTAs a sequence, whose rows are taken one after the other until a
+// draft is refused (side by side where there are few sequences).  (Dealing out the strips of
+// all sequences' rows too, position by position, with the verdict by the warp that finishes a
+// row, took 246 us for 512 sequences of four drafts: a warp that judges falls behind, so that
+// it is the last at the next row as well.  VERIFY_US so.)
 //
 // Sums over a strip are fp32 (1024 bf16 or 512 fp32 logits, 32 or 16 a lane and then the
 // lanes'), sums over strips and the search for the token's strip are in 64 bits: a token's
@@ -41,6 +44,8 @@ namespace {
 constexpr int kLoads = 4;                  // 16-byte units a lane takes at a time
 constexpr int kStripStep = 32 * kLoads;    // units that a warp takes at a time
 constexpr int kMaxStrips = 512;            // of a row; longer rows have longer strips
+constexpr int kMaxRound = 8;               // rows of a sequence side by side
+constexpr int kMaxCluster = 8;
 constexpr int kSampleWarps = 8;            // of a CTA, at most
 constexpr int kSampleCtas = 4;             // CTAs an SM, by their registers
 
@@ -65,31 +70,24 @@ struct SampleArgs {
   const uint8_t* mask;       // rows of a sampling call that take part; or null
   const int64_t* drafts;
   const float* draft_logp;   // or null
-  const int64_t* offsets;    // [n_seqs + 1]; null: sampling, a row a sequence
+  const int64_t* offsets;    // [n_seqs + 1]
   const float* accept_u;
   const float* sample_u;
   int64_t* tokens;
   int64_t* counts;
   float* logp;
   int64_t target_stride, draft_stride;
-  int64_t n_drafts, n_seqs;
+  int64_t n_drafts, n_seqs;  // sampling: n_seqs rows
   Scale target_scale, draft_scale;
   int32_t vocab;
   int32_t strip_units;       // a multiple of kStripStep
-  int32_t strips;            // of a row
-  int32_t each;              // strips that a warp takes at a time
-  int32_t pieces;            // of a row: strips / each, rounded up
-  int32_t both;              // the draft model's rows are read with the target's
-  // workspace
-  StripSum* p;               // [target rows][strips]
-  StripSum* q;               // of the draft model: both, [drafts][strips]; else [n_seqs][strips], where a draft was refused
-  float* left;               // [n_seqs][strips] max(p - q, 0)
-  RowSum* p_total;           // [target rows]
-  RowSum* q_total;           // [drafts] or [n_seqs]
-  uint32_t* done;            // [target rows] pieces that are done; zero at first, as the next two
-  uint32_t* q_done;          // [n_seqs]
-  uint32_t* refused;         // [n_seqs] 2^31 - 1 minus the first refused draft, 0: none
-  int64_t* longest;          // the most drafts of a sequence
+  int32_t strips;            // of a row; of a CTA's part of it in verification
+  // sampling
+  int32_t each, pieces;      // strips that a warp takes at a time; of a row: strips / each, rounded up
+  StripSum* sums;            // workspace, [rows][strips]
+  // verification
+  int32_t cluster;           // CTAs a sequence
+  int32_t round;             // rows of a sequence taken side by side
 };
 
 __device__ __forceinline__ float factor(const Scale& c, float m, float to) {
@@ -179,30 +177,53 @@ __device__ __forceinline__ void exps(const Scale& c, float m, const uint4& w, fl
   }
 }
 
-// The sum of exponentials over the units [u0, u1) of a row; the same in every lane.
+// Adds a step's units to a strip's sum; the same in every lane.
 template <typename T>
-__device__ __forceinline__ StripSum strip_sum(const RowUnits<T>& row, const Scale& c, int u0, int u1, int lane) {
-  StripSum t{-INFINITY, 0.f};
-  for (int u = u0; u < u1; u += kStripStep) {
-    uint4 w[kLoads];
-    load_units<T>(row, u + lane, 32, u1, step_inside<T>(row, u, u1), w);
-    const float m = fmaxf(t.m, warp_max(Vec<T>::max(w)));
-    F2 s0 = make_f2(0.f, 0.f), s1 = make_f2(0.f, 0.f);
+__device__ __forceinline__ void add_step(const Scale& c, const uint4 (&w)[kLoads], StripSum& t) {
+  const float m = fmaxf(t.m, warp_max(Vec<T>::max(w)));
+  F2 s0 = make_f2(0.f, 0.f), s1 = make_f2(0.f, 0.f);
 #pragma unroll
-    for (int k = 0; k < kLoads; ++k) {
-      float e[Vec<T>::N];
-      exps<T>(c, frame_of(m), w[k], e);
+  for (int k = 0; k < kLoads; ++k) {
+    float e[Vec<T>::N];
+    exps<T>(c, frame_of(m), w[k], e);
 #pragma unroll
-      for (int i = 0; i < Vec<T>::N; i += 4) {
-        s0 = add2(s0, make_f2(e[i], e[i + 1]));
-        s1 = add2(s1, make_f2(e[i + 2], e[i + 3]));
-      }
+    for (int i = 0; i < Vec<T>::N; i += 4) {
+      s0 = add2(s0, make_f2(e[i], e[i + 1]));
+      s1 = add2(s1, make_f2(e[i + 2], e[i + 3]));
     }
-    const float2 r = split(add2(s0, s1));
-    t.s = t.s * factor(c, t.m, m) + warp_sum(r.x + r.y);
-    t.m = m;
   }
-  return t;
+  const float2 r = split(add2(s0, s1));
+  t.s = t.s * factor(c, t.m, m) + warp_sum(r.x + r.y);
+  t.m = m;
+}
+
+// The sums of the strips [k0, k1) of a row, into `to`.  A step's loads are under way while the
+// step before is summed.
+template <typename T>
+__device__ __forceinline__ void sum_strips(const RowUnits<T>& row, const Scale& c, int strip_units, int k0, int k1,
+                                           StripSum* to, int lane) {
+  const int end = (int)min((int64_t)k1 * strip_units, (int64_t)row.units);
+  int u = (int)min((int64_t)k0 * strip_units, (int64_t)row.units);
+  uint4 w[kLoads];
+  load_units<T>(row, u + lane, 32, end, step_inside<T>(row, u, end), w);
+  StripSum t{-INFINITY, 0.f};
+  int left = strip_units;  // of the strip
+  for (int k = k0; k < k1;) {
+    const int next = u + kStripStep;
+    uint4 x[kLoads];
+    load_units<T>(row, next + lane, 32, end, step_inside<T>(row, next, end), x);
+    add_step<T>(c, w, t);
+    left -= kStripStep;
+    if (left == 0) {
+      if (lane == 0) to[k - k0] = t;
+      t = StripSum{-INFINITY, 0.f};
+      left = strip_units;
+      ++k;
+    }
+    u = next;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) w[i] = x[i];
+  }
 }
 
 // The probabilities of both models at a refused draft.
@@ -234,51 +255,6 @@ __device__ __forceinline__ void left_over(const SampleArgs& a, const Refused& f,
   }
 }
 
-// The first element of the units [u0, u1) at which the cumulated weight exceeds t (a token
-// of weight 0 never does), or the last of positive weight, or -1.  weights(first, inside, w):
-// those of the units first .. first + kLoads - 1 (0 from u1 on), which a lane takes side by
-// side.  A lane's weights are summed in fp32, the lanes' in 64 bits, of which the SMs do few.
-template <typename T, typename F>
-__device__ __forceinline__ int pick_element(const RowUnits<T>& row, int u0, int u1, double t, int lane, F weights) {
-  constexpr int N = Vec<T>::N;
-  double before = 0.;
-  int last = -1;
-  for (int u = u0; u < u1; u += kStripStep) {
-    const int first = u + lane * kLoads;
-    float w[kLoads * N];
-    weights(first, step_inside<T>(row, u, u1), w);
-    float s = 0.f;
-    int positive = -1;
-#pragma unroll
-    for (int i = 0; i < kLoads * N; ++i) {
-      s += w[i];
-      if (w[i] > 0.f) positive = i;
-    }
-    const double upto = before + warp_scan64((double)s, lane);
-    const unsigned over = __ballot_sync(0xFFFFFFFFu, positive >= 0 && upto > t);
-    const unsigned any = __ballot_sync(0xFFFFFFFFu, positive >= 0);
-    if (over) {
-      const int l = __ffs(over) - 1;
-      const float rest = (float)(t - (upto - (double)s));  // of the lane's weights
-      int found = positive;
-      float c = 0.f;
-      bool passed = false;
-#pragma unroll
-      for (int i = 0; i < kLoads * N; ++i) {
-        c += w[i];
-        if (!passed && w[i] > 0.f && c > rest) {
-          found = i;
-          passed = true;
-        }
-      }
-      return __shfl_sync(0xFFFFFFFFu, row.first(first) + found, l);
-    }
-    if (any) last = __shfl_sync(0xFFFFFFFFu, row.first(first) + positive, 31 - __clz(any));
-    before = __shfl_sync(0xFFFFFFFFu, upto, 31);
-  }
-  return last;
-}
-
 // Each lane's part of the sum over the units [u0, u1) without one token.
 template <typename T>
 __device__ __forceinline__ float sum_without(const RowUnits<T>& row, const Scale& c, float m, int u0, int u1, int token,
@@ -300,13 +276,10 @@ __device__ __forceinline__ float sum_without(const RowUnits<T>& row, const Scale
   return s;
 }
 
-// log p of a token of the strip [u0, u1): the strip is summed again without the token, so
-// that a nearly certain token keeps its digits.  rest: each lane's part of the sum over the
-// other strips, in the row's frame m.
+// log p of a token from the sum over the others, of which each lane has a part, in the row's
+// frame m; so a nearly certain token keeps its digits.
 template <typename T>
-__device__ __forceinline__ float token_logp(const RowUnits<T>& row, const Scale& c, float m, double rest, int u0, int u1,
-                                            int token, int lane) {
-  rest += (double)sum_without<T>(row, c, m, u0, u1, token, lane);
+__device__ __forceinline__ float token_logp(const RowUnits<T>& row, const Scale& c, float m, double rest, int token) {
   float s = (float)warp_sum64(rest);
   const float d = Vec<T>::load(row.z + token) - m;
   const float x = __fmaf_rn(d, c.inv_hi, d * c.inv_lo);
@@ -317,87 +290,124 @@ __device__ __forceinline__ float token_logp(const RowUnits<T>& row, const Scale&
 
 __device__ __forceinline__ bool usable(const RowSum& t) { return t.s > 0. && t.s < (double)INFINITY; }
 
-// The sum over a row's strips, and of the lane's share of them (consecutive strips), in the
-// frame of the largest.
-__device__ __forceinline__ RowSum row_sum(const SampleArgs& a, const StripSum* t, const Scale& c, int lane) {
-  float m = -INFINITY;
-  for (int k = lane; k < a.strips; k += 32) m = fmaxf(m, __ldcg(reinterpret_cast<const float2*>(t) + k).x);
-  RowSum r;
-  r.m = warp_max(m);
-  double s = 0.;
-  for (int k = lane; k < a.strips; k += 32) {
-    const float2 x = __ldcg(reinterpret_cast<const float2*>(t) + k);
-    s += (double)(x.y * factor(c, x.x, r.m));
-  }
-  r.s = warp_sum64(s);
-  return r;
-}
-
-__device__ __forceinline__ RowSum load_total(const RowSum* p) {
-  RowSum r;
-  r.s = __ldcg(&p->s);
-  r.m = __ldcg(&p->m);
-  return r;
-}
-
-// A sequence's drafts; offsets out of order or range lead to nothing outside the arrays.
-struct Sequence {
-  int64_t lo, n;
+// The weights that a token is drawn from.
+enum Weights {
+  kPlain,    // p
+  kWithout,  // p without the refused draft
+  kLeft,     // max(p - q, 0)
 };
-__device__ __forceinline__ Sequence sequence_of(const SampleArgs& a, int64_t s) {
-  Sequence q;
-  q.lo = min(max(a.offsets[s], (int64_t)0), a.n_drafts);
-  q.n = min(max(a.offsets[s + 1], q.lo), a.n_drafts) - q.lo;
-  return q;
-}
 
-// The sums of the strips [k0, k1) of a row.
-template <typename T>
-__device__ __forceinline__ void sum_strips(const SampleArgs& a, const RowUnits<T>& row, const Scale& c, int k0, int k1,
-                                           StripSum* to, int lane) {
+// What a warp draws with.  This code runs once a row, so that it is its instructions' and the
+// tables' way to the SM that costs: loops are not unrolled more than the loads need, and what
+// is read again is kept in shared memory.
+struct DrawSpace {
+  float weight[32][kLoads * 8 + 1];  // of a step's elements, a row a lane
+};
+
+// The strip in which the cumulated weight exceeds t (one of weight 0 never does), else the
+// last of positive weight; -1: none.  before: the weights before the first strip, and then
+// before the one that is found.  weight(k), k < strips.
+template <typename F>
+__device__ __forceinline__ int find_strip(int strips, double t, double* before, int lane, F weight) {
+  // a lane's strips are consecutive ones
+  const int per = (strips + 31) / 32, k0 = min(lane * per, strips), k1 = min(k0 + per, strips);
+  double w = 0.;
+#pragma unroll 1
+  for (int k = k0; k < k1; ++k) w += (double)weight(k);
+  const double end = *before + warp_scan64(w, lane);
+  const unsigned above = __ballot_sync(0xFFFFFFFFu, w > 0. && end > t);
+  const unsigned some = __ballot_sync(0xFFFFFFFFu, w > 0.);
+  if (some == 0) return -1;
+  const int l = above ? __ffs(above) - 1 : 31 - __clz(some);
+  double at = end - w, begun = at;
+  int strip = 0;
+#pragma unroll 1
   for (int k = k0; k < k1; ++k) {
-    const int u0 = (int)min((int64_t)k * a.strip_units, (int64_t)row.units), u1 = min(u0 + a.strip_units, row.units);
-    const StripSum t = strip_sum<T>(row, c, u0, u1, lane);
-    if (lane == 0) __stcg(reinterpret_cast<float2*>(to) + k, make_float2(t.m, t.s));
+    const double x = (double)weight(k);
+    if (x > 0.) {
+      strip = k;
+      begun = at;
+      if (at + x > t) break;
+    }
+    at += x;
   }
+  *before = __shfl_sync(0xFFFFFFFFu, begun, l);
+  return __shfl_sync(0xFFFFFFFFu, strip, l);
 }
 
-// Whether the calling warp's piece is the last of `all`; what the other warps wrote is then
-// visible to every lane.
-__device__ __forceinline__ bool last_piece(uint32_t* done, uint32_t all, int lane) {
-  uint32_t before = 0;
-  if (lane == 0) {
-    __threadfence();
-    before = atomicAdd(done, 1u);
-  }
-  const bool last = __shfl_sync(0xFFFFFFFFu, before, 0) == all - 1;
-  if (last) __threadfence();
-  return last;
-}
-
-// Clears the counters and finds the longest sequence.
-constexpr int kSetupThreads = 1024;
-__global__ void __launch_bounds__(kSetupThreads) setup_kernel(const __grid_constant__ SampleArgs a) {
-  griddep_launch_dependents();
-  __shared__ long long most[kSetupThreads / 32];
-  long long n = 0;
-  for (int64_t s = threadIdx.x; s < a.n_seqs; s += kSetupThreads) {
-    n = max(n, (long long)sequence_of(a, s).n);
-    a.q_done[s] = 0;
-    a.refused[s] = 0;
-  }
-  for (int64_t r = threadIdx.x; r < a.n_drafts + a.n_seqs; r += kSetupThreads) a.done[r] = 0;
+// The first element of the units [u0, u1) at which the cumulated weight exceeds t (one of
+// weight 0 never does), else the last of positive weight; -1: none.  A lane takes kLoads units
+// side by side and sums them in fp32; the lanes' sums are added in 64 bits, of which the SMs do
+// few.  rest: the lane's part of the sum of p over the units without that element.
+template <typename T>
+__device__ __forceinline__ int find_element(const SampleArgs& a, DrawSpace& sh, const RowUnits<T>& row, int u0, int u1,
+                                            double t, int kind, int without, const T* zq, const Refused& f, float m,
+                                            float* rest, int lane) {
+  constexpr int N = Vec<T>::N;
+  const Scale& c = a.target_scale;
+  int found = -1;
+  double before = 0.;
+#pragma unroll 1
+  for (int at = u0; at < u1; at += kStripStep) {
+    const int first = at + lane * kLoads;
+    const bool inside = step_inside<T>(row, at, u1);
+    float v = 0.f;
+    if (kind == kLeft) {
+      float x[kLoads * N];
+      left_over<T>(a, f, row, zq, first, 1, u1, inside, x);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) n = max(n, __shfl_xor_sync(0xFFFFFFFFu, n, o));
-  if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = n;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int k = 1; k < kSetupThreads / 32; ++k) n = max(n, most[k]);
-    *a.longest = n;
+      for (int i = 0; i < kLoads * N; ++i) {
+        sh.weight[lane][i] = x[i];
+        v += x[i];
+      }
+    } else {
+      uint4 z[kLoads];
+      load_units<T>(row, first, 1, u1, inside, z);
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k) {
+        float e[N];
+        exps<T>(c, m, z[k], e);
+        const int drop = kind == kWithout ? without - row.first(first + k) : -1;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const float x = i == drop ? 0.f : e[i];
+          sh.weight[lane][k * N + i] = x;
+          v += x;
+        }
+      }
+    }
+    __syncwarp();
+    const double upto = before + warp_scan64((double)v, lane);
+    const unsigned above = __ballot_sync(0xFFFFFFFFu, v > 0.f && upto > t);
+    const unsigned some = __ballot_sync(0xFFFFFFFFu, v > 0.f);
+    if (some) {
+      const int l = above ? __ffs(above) - 1 : 31 - __clz(some);
+      // each lane takes one of that lane's elements
+      const float x = lane < kLoads * N ? sh.weight[l][lane] : 0.f;
+      float s = x;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float y = __shfl_up_sync(0xFFFFFFFFu, s, o);
+        if (lane >= o) s += y;
+      }
+      const float need = (float)(t - __shfl_sync(0xFFFFFFFFu, upto - (double)v, l));
+      const unsigned over = __ballot_sync(0xFFFFFFFFu, x > 0.f && s > need);
+      const unsigned any = __ballot_sync(0xFFFFFFFFu, x > 0.f);
+      const int e = above && over ? __ffs(over) - 1 : 31 - __clz(any);
+      found = row.first(at + l * kLoads) + e;
+      *rest = (lane == l ? 0.f : v) + (lane == e ? 0.f : x);
+    }
+    if (above) break;
+    before = __shfl_sync(0xFFFFFFFFu, upto, 31);
+    __syncwarp();
   }
+  if (found >= 0 && (kind != kPlain || u1 - u0 > kStripStep)) *rest = sum_without<T>(row, c, m, u0, u1, found, lane);
+  return found;
 }
 
-// Strip sums of sampled rows.
+// ---------------------------------------------------------------------------
+// sampling
+// ---------------------------------------------------------------------------
 template <typename T>
 __global__ void __launch_bounds__(kSampleWarps * 32, kSampleCtas) rows_kernel(const __grid_constant__ SampleArgs a) {
   griddep_launch_dependents();
@@ -408,324 +418,366 @@ __global__ void __launch_bounds__(kSampleWarps * 32, kSampleCtas) rows_kernel(co
     if (a.mask != nullptr && a.mask[t] == 0) continue;
     const int k0 = (int)(job - t * a.pieces) * a.each;
     const RowUnits<T> row(a.target, t, a.target_stride, a.vocab);
-    sum_strips<T>(a, row, a.target_scale, k0, min(k0 + a.each, a.strips), a.p + t * a.strips, lane);
+    sum_strips<T>(row, a.target_scale, a.strip_units, k0, min(k0 + a.each, a.strips), a.sums + t * a.strips + k0, lane);
   }
 }
 
-// Strip sums of the target's rows (and, where `both`, of the draft model's), position by
-// position over all sequences, and the verdict on each draft.
+// A warp draws a row's token.
+constexpr int kDrawWarps = 4;
 template <typename T>
-__global__ void __launch_bounds__(kSampleWarps * 32, kSampleCtas) verify_kernel(const __grid_constant__ SampleArgs a) {
-  griddep_launch_dependents();
-  griddep_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5);
-  const int sets = a.both ? 2 : 1, per_row = a.pieces * sets;
-  const int64_t jobs = (__ldcg(a.longest) + 1) * a.n_seqs * per_row;
-  // a job's sequence and what is known of it are read while the job before is worked on
-  int64_t job = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  int64_t i = 0, s = 0;
-  int piece = 0;
-  Sequence q{0, -1};
-  uint32_t refused = 0;
-  auto look = [&](int64_t j) {
-    if (j >= jobs) return;
-    const int64_t r = j / per_row;
-    piece = (int)(j - r * per_row);
-    i = r / a.n_seqs;
-    s = r - i * a.n_seqs;
-    q = sequence_of(a, s);
-    refused = __ldcg(a.refused + s);
-  };
-  look(job);
-  while (job < jobs) {
-    const int64_t at = i, seq = s;
-    const Sequence own = q;
-    const bool of_draft = piece >= a.pieces;
-    const int k0 = (of_draft ? piece - a.pieces : piece) * a.each;
-    const uint32_t known = refused;
-    job += warps;
-    look(job);
-    // no such row, or one behind a refused draft
-    if (at > own.n || (known != 0 && (int64_t)(0x7FFFFFFFu - known) < at)) continue;
-    const int64_t r = own.lo + seq + at, d = own.lo + at;
-    if (of_draft) {
-      if (at == own.n) continue;
-      const RowUnits<T> row(a.draft, d, a.draft_stride, a.vocab);
-      sum_strips<T>(a, row, a.draft_scale, k0, min(k0 + a.each, a.strips), a.q + d * a.strips, lane);
-    } else {
-      const RowUnits<T> row(a.target, r, a.target_stride, a.vocab);
-      sum_strips<T>(a, row, a.target_scale, k0, min(k0 + a.each, a.strips), a.p + r * a.strips, lane);
-    }
-    if (!last_piece(a.done + r, at < own.n ? per_row : a.pieces, lane)) continue;
-    const RowSum p = row_sum(a, a.p + r * a.strips, a.target_scale, lane);
-    if (lane == 0) a.p_total[r] = p;
-    if (at == own.n) continue;
-    RowSum dq{1., 0.f};
-    if (a.both) {
-      dq = row_sum(a, a.q + d * a.strips, a.draft_scale, lane);
-      if (lane == 0) a.q_total[d] = dq;
-    }
-    if (lane == 0) {
-      const int64_t y = a.drafts[d];
-      bool ok = usable(p) && usable(dq) && y >= 0 && y < a.vocab;
-      if (ok) {
-        const float x = Vec<T>::load(reinterpret_cast<const T*>(a.target) + r * a.target_stride + y) - p.m;
-        const float logp = __fmaf_rn(x, a.target_scale.inv_hi, x * a.target_scale.inv_lo) - logf((float)p.s);
-        float logq = a.draft_logp != nullptr ? a.draft_logp[d] : 0.f;
-        if (a.both) {
-          const float z = Vec<T>::load(reinterpret_cast<const T*>(a.draft) + d * a.draft_stride + y) - dq.m;
-          logq = __fmaf_rn(z, a.draft_scale.inv_hi, z * a.draft_scale.inv_lo) - logf((float)dq.s);
-        }
-        ok = a.accept_u[d] < expf(logp - logq);
-      }
-      if (!ok) atomicMax(a.refused + seq, 0x7FFFFFFFu - (uint32_t)at);
-    }
-  }
-}
-
-// Where sequence s stopped: its drafts, the number of them that were taken, whether the next
-// was refused.
-struct Stop {
-  Sequence q;
-  int64_t taken;
-  bool refused;
-};
-__device__ __forceinline__ Stop stop_of(const SampleArgs& a, int64_t s) {
-  Stop r;
-  r.q = sequence_of(a, s);
-  const uint32_t known = __ldcg(a.refused + s);
-  r.refused = known != 0;
-  r.taken = known ? (int64_t)(0x7FFFFFFFu - known) : r.q.n;
-  return r;
-}
-
-// Strip sums of the draft model's row at each refused draft.
-template <typename T>
-__global__ void __launch_bounds__(kSampleWarps * 32, kSampleCtas) refused_kernel(const __grid_constant__ SampleArgs a) {
-  griddep_launch_dependents();
-  griddep_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5), jobs = a.n_seqs * a.pieces;
-  for (int64_t job = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); job < jobs; job += warps) {
-    const int64_t s = job / a.pieces;
-    const Stop e = stop_of(a, s);
-    if (!e.refused) continue;
-    const int k0 = (int)(job - s * a.pieces) * a.each;
-    const RowUnits<T> row(a.draft, e.q.lo + e.taken, a.draft_stride, a.vocab);
-    sum_strips<T>(a, row, a.draft_scale, k0, min(k0 + a.each, a.strips), a.q + s * a.strips, lane);
-    if (!last_piece(a.q_done + s, a.pieces, lane)) continue;
-    const RowSum q = row_sum(a, a.q + s * a.strips, a.draft_scale, lane);
-    if (lane == 0) a.q_total[s] = q;
-  }
-}
-
-__device__ __forceinline__ Refused refused_of(const SampleArgs& a, const Stop& e, int64_t s, bool* fine) {
-  const RowSum p = load_total(a.p_total + e.q.lo + s + e.taken);
-  const RowSum q = load_total(a.q_total + (a.both ? e.q.lo + e.taken : s));
-  *fine = usable(p) && usable(q);
-  return Refused{p.m, (float)(1. / p.s), q.m, (float)(1. / q.s)};
-}
-
-// Strip sums of max(p - q, 0) at each refused draft.
-template <typename T>
-__global__ void __launch_bounds__(kSampleWarps * 32, 3) left_kernel(const __grid_constant__ SampleArgs a) {
-  constexpr int N = Vec<T>::N;
-  griddep_launch_dependents();
-  griddep_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5), jobs = a.n_seqs * a.pieces;
-  for (int64_t job = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); job < jobs; job += warps) {
-    const int64_t s = job / a.pieces;
-    const Stop e = stop_of(a, s);
-    if (!e.refused) continue;
-    bool fine;
-    const Refused f = refused_of(a, e, s, &fine);
-    if (!fine) continue;
-    const RowUnits<T> row(a.target, e.q.lo + s + e.taken, a.target_stride, a.vocab);
-    const RowUnits<T> draft(a.draft, e.q.lo + e.taken, a.draft_stride, a.vocab);
-    const int k0 = (int)(job - s * a.pieces) * a.each;
-    for (int k = k0; k < min(k0 + a.each, a.strips); ++k) {
-      const int u0 = (int)min((int64_t)k * a.strip_units, (int64_t)row.units), u1 = min(u0 + a.strip_units, row.units);
-      float sum = 0.f;
-      for (int u = u0; u < u1; u += kStripStep) {
-        float r[kLoads * N];
-        left_over<T>(a, f, row, draft.z, u + lane, 32, u1, step_inside<T>(row, u, u1), r);
-#pragma unroll
-        for (int i = 0; i < kLoads * N; ++i) sum += r[i];
-      }
-      sum = warp_sum(sum);
-      if (lane == 0) __stcg(a.left + s * a.strips + k, sum);
-    }
-  }
-}
-
-// The weights that a token is drawn from.
-enum Weights {
-  kPlain,    // p
-  kWithout,  // p without the refused draft
-  kLeft,     // max(p - q, 0)
-};
-
-// Draws the token of a row; the warp's lanes get the same token and log p.
-template <typename T>
-__device__ __forceinline__ void draw(const SampleArgs& a, int64_t r, int64_t s, int kind, int64_t without, const T* zq,
-                                     const Refused& f, float u, int64_t* token, float* logp, int lane) {
-  constexpr int N = Vec<T>::N;
-  const RowUnits<T> row(a.target, r, a.target_stride, a.vocab);
-  const Scale& c = a.target_scale;
-  const float2* strips = reinterpret_cast<const float2*>(a.p + r * a.strips);
-  *token = -1;
-  *logp = NAN;
-  // a lane's strips are consecutive ones
-  const int per = (a.strips + 31) / 32, k0 = min(lane * per, a.strips), k1 = min(k0 + per, a.strips);
-  float m = -INFINITY;
-  for (int k = k0; k < k1; ++k) m = fmaxf(m, __ldcg(strips + k).x);
-  m = warp_max(m);
-  auto plain = [&](int k) {
-    const float2 x = __ldcg(strips + k);
-    return (double)(x.y * factor(c, x.x, m));
-  };
-  auto bounds = [&](int k, int& u0, int& u1) {
-    u0 = (int)min((int64_t)k * a.strip_units, (int64_t)row.units);
-    u1 = min(u0 + a.strip_units, row.units);
-  };
-  double own = 0.;  // of p
-  for (int k = k0; k < k1; ++k) own += plain(k);
-  const RowSum p{warp_sum64(own), m};
-  if (!usable(p)) return;
-  int without_strip = -1;
-  float without_sum = 0.f;
-  if (kind == kWithout && without >= 0 && without < a.vocab) {
-    without_strip = ((int)without + row.shift) / N / a.strip_units;
-    int u0, u1;
-    bounds(without_strip, u0, u1);
-    without_sum = warp_sum(sum_without<T>(row, c, m, u0, u1, (int)without, lane));
-  }
-  auto weight = [&](int k) {
-    if (kind == kLeft) return (double)__ldcg(a.left + s * a.strips + k);
-    return kind == kWithout && k == without_strip ? (double)without_sum : plain(k);
-  };
-  double w = own;
-  if (kind != kPlain) {
-    w = 0.;
-    for (int k = k0; k < k1; ++k) w += weight(k);
-    // nothing is left over where the two models agree, and the refusal was one of rounding
-    if (!__any_sync(0xFFFFFFFFu, w > 0.)) {
-      kind = kPlain;
-      w = own;
-    }
-  }
-  const double end = warp_scan64(w, lane), sum = __shfl_sync(0xFFFFFFFFu, end, 31);
-  u = fmaxf(u, 0.f);
-  const double t = u < 1.f ? (double)u * sum : (double)INFINITY;  // 1 and above: the last token
-  const unsigned above = __ballot_sync(0xFFFFFFFFu, w > 0. && end > t);
-  const unsigned some = __ballot_sync(0xFFFFFFFFu, w > 0.);
-  const int l = above ? __ffs(above) - 1 : 31 - __clz(some);
-  double before = end - w, begun = before;
-  int strip = 0;
-  for (int k = k0; k < k1; ++k) {
-    const double x = weight(k);
-    if (x > 0.) {
-      strip = k;
-      begun = before;
-      if (before + x > t) break;
-    }
-    before += x;
-  }
-  strip = __shfl_sync(0xFFFFFFFFu, strip, l);
-  before = __shfl_sync(0xFFFFFFFFu, begun, l);
-  int u0, u1;
-  bounds(strip, u0, u1);
-  const int found = pick_element<T>(row, u0, u1, t - before, lane, [&](int first, bool inside, float(&w)[kLoads * N]) {
-    if (kind == kLeft) {
-      left_over<T>(a, f, row, zq, first, 1, u1, inside, w);
-      return;
-    }
-    uint4 z[kLoads];
-    load_units<T>(row, first, 1, u1, inside, z);
-#pragma unroll
-    for (int k = 0; k < kLoads; ++k) {
-      float e[N];
-      exps<T>(c, m, z[k], e);
-#pragma unroll
-      for (int i = 0; i < N; ++i) w[k * N + i] = kind == kWithout && row.first(first + k) + i == without ? 0.f : e[i];
-    }
-  });
-  if (found < 0) return;
-  // the lane's part of p without the token's strip
-  double rest = 0.;
-  for (int k = k0; k < k1; ++k)
-    if (k != strip) rest += plain(k);
-  *token = found;
-  *logp = token_logp<T>(row, c, m, rest, u0, u1, found, lane);
-}
-
-// Sampling: a warp draws a row's token.
-template <typename T>
-__global__ void __launch_bounds__(kSampleWarps * 32, 2) draw_kernel(const __grid_constant__ SampleArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int64_t t = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+__global__ void __launch_bounds__(kDrawWarps * 32) draw_kernel(const __grid_constant__ SampleArgs a) {
+  __shared__ DrawSpace space[kDrawWarps];
+  __shared__ float weights[kDrawWarps][kMaxStrips];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = (int64_t)blockIdx.x * (blockDim.x >> 5) + warp;
   griddep_wait();
   if (t >= a.n_seqs) return;
   int64_t token = -1;
   float logp = 0.f;
-  if (a.mask == nullptr || a.mask[t] != 0)
-    draw<T>(a, t, t, kPlain, -1, nullptr, Refused{}, a.sample_u[t], &token, &logp, lane);
+  if (a.mask == nullptr || a.mask[t] != 0) {
+    logp = NAN;
+    const Scale& c = a.target_scale;
+    const RowUnits<T> row(a.target, t, a.target_stride, a.vocab);
+    const float2* sums = reinterpret_cast<const float2*>(a.sums + t * a.strips);
+    const float u = fmaxf(a.sample_u[t], 0.f);
+    float m = -INFINITY;
+#pragma unroll 4
+    for (int k = lane; k < a.strips; k += 32) m = fmaxf(m, __ldcg(sums + k).x);
+    m = warp_max(m);
+    double own = 0.;
+#pragma unroll 1
+    for (int k = lane; k < a.strips; k += 32) {
+      const float2 x = __ldcg(sums + k);
+      weights[warp][k] = x.y * factor(c, x.x, m);
+      own += (double)weights[warp][k];
+    }
+    __syncwarp();
+    const RowSum p{warp_sum64(own), m};
+    if (usable(p)) {
+      double before = 0.;
+      const double at = u < 1.f ? (double)u * p.s : (double)INFINITY;  // 1 and above: the last token
+      const int strip = find_strip(a.strips, at, &before, lane, [&](int k) { return weights[warp][k]; });
+      const int u0 = strip * a.strip_units, u1 = min(u0 + a.strip_units, row.units);
+      float rest;
+      const int found = find_element<T>(a, space[warp], row, u0, u1, at - before, kPlain, -1, nullptr, Refused{}, m, &rest, lane);
+      double others = (double)rest;
+#pragma unroll 1
+      for (int k = lane; k < a.strips; k += 32)
+        if (k != strip) others += (double)weights[warp][k];
+      if (found >= 0) {
+        token = found;
+        logp = token_logp<T>(row, c, m, others, found);
+      }
+    }
+  }
   if (lane == 0) {
     a.tokens[t] = token;
     a.logp[t] = logp;
   }
 }
 
-// Verification: a warp writes a row's token: a taken draft, the drawn one, or -1.
+// ---------------------------------------------------------------------------
+// verification
+// ---------------------------------------------------------------------------
+struct SampleShared {
+  RowSum slice[2][2 * kMaxRound];  // this CTA's part of each row, read by the cluster's other CTAs
+  RowSum total[2][2 * kMaxRound];
+  double weights;                  // this CTA's part of the weights a token is drawn from
+  DrawSpace draw;
+};
+
+__device__ __forceinline__ RowSum load_peer(const RowSum* p, int rank, int own) {
+  if (rank == own) return *p;
+  const uint32_t at = mapa_shared(p, (uint32_t)rank);
+  RowSum r;
+  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(r.s) : "r"(at) : "memory");
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(r.m) : "r"(at + 8) : "memory");
+  return r;
+}
+
+__device__ __forceinline__ double load_peer(const double* p, int rank) {
+  double v;
+  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(mapa_shared(p, (uint32_t)rank)) : "memory");
+  return v;
+}
+
+// A cluster of CTAs a sequence.  Its rows are taken `round` at a time until a draft is refused.
 template <typename T>
-__global__ void __launch_bounds__(kSampleWarps * 32, 2) emit_kernel(const __grid_constant__ SampleArgs a) {
+__global__ void __launch_bounds__(kSampleWarps * 32, 3) verify_kernel(const __grid_constant__ SampleArgs a) {
   constexpr int N = Vec<T>::N;
-  const int lane = threadIdx.x & 31;
-  griddep_wait();
-  const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5), jobs = (__ldcg(a.longest) + 1) * a.n_seqs;
-  for (int64_t job = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); job < jobs; job += warps) {
-    const int64_t i = job / a.n_seqs, s = job - i * a.n_seqs;
-    const Stop e = stop_of(a, s);
-    if (i > e.q.n) continue;
-    const int64_t r = e.q.lo + s + i, d = e.q.lo + i;
-    int64_t token = -1;
-    float logp = 0.f;
-    if (i < e.taken) {
-      token = a.drafts[d];
-      const RowUnits<T> row(a.target, r, a.target_stride, a.vocab);
-      const RowSum p = load_total(a.p_total + r);
-      const int strip = ((int)token + row.shift) / N / a.strip_units;
-      double rest = 0.;
-      for (int k = lane; k < a.strips; k += 32) {
-        const float2 x = __ldcg(reinterpret_cast<const float2*>(a.p + r * a.strips) + k);
-        if (k != strip) rest += (double)(x.y * factor(a.target_scale, x.x, p.m));
+  extern __shared__ StripSum tables[];  // [2][target and draft][round][strips]
+  __shared__ SampleShared sh;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int rank = a.cluster > 1 ? (int)cluster_ctarank() : 0;
+  const int64_t seq = blockIdx.x / a.cluster;
+  // offsets out of order or range: nothing outside the arrays is touched
+  const int64_t lo = min(max(a.offsets[seq], (int64_t)0), a.n_drafts);
+  const int64_t n = min(max(a.offsets[seq + 1], lo), a.n_drafts) - lo;
+  const int64_t row0 = lo + seq;  // the sequence's first row
+  const bool both = a.draft != nullptr && a.draft_logp == nullptr;  // rows of both models a round
+  const int set = a.round * a.strips;
+  const int strip0 = rank * a.strips;
+  // of the CTA's strips this warp's
+  const int per_warp = (a.strips + warps - 1) / warps, mine0 = min(warp * per_warp, a.strips), mine1 = min(mine0 + per_warp, a.strips);
+  auto exchange = [&] {
+    if (a.cluster > 1) cluster_sync();
+    else __syncthreads();
+  };
+  auto units_of = [&](const RowUnits<T>& row, int k, int& u0, int& u1) {  // of this CTA's strip k
+    u0 = (int)min((int64_t)(strip0 + k) * a.strip_units, (int64_t)row.units);
+    u1 = min(u0 + a.strip_units, row.units);
+  };
+  // sums a row's slices: warp-wide, the same in every lane
+  auto merge = [&](const RowSum* slice, const Scale& c) {
+    RowSum t{0., -INFINITY};
+    if (lane < a.cluster) t = load_peer(slice, lane, rank);
+    RowSum r;
+    r.m = warp_max(t.m);
+    r.s = warp_sum64(t.s * (double)factor(c, t.m, r.m));
+    return r;
+  };
+  auto slice_sum = [&](const StripSum* table, const Scale& c) {
+    float m = -INFINITY;
+    for (int k = lane; k < a.strips; k += 32) m = fmaxf(m, table[k].m);
+    RowSum r;
+    r.m = warp_max(m);
+    r.s = 0.;
+    for (int k = lane; k < a.strips; k += 32) r.s += (double)(table[k].s * factor(c, table[k].m, r.m));
+    r.s = warp_sum64(r.s);
+    return r;
+  };
+  // each lane's part of a row's sum without the strip k0 of this CTA
+  auto other_strips = [&](const StripSum* table, const RowSum* slice, int k0, float m, const Scale& c) {
+    double s = 0.;
+    for (int k = lane; k < a.strips; k += 32)
+      if (k != k0) s += (double)(table[k].s * factor(c, table[k].m, m));
+    if (lane < a.cluster && lane != rank) {
+      const RowSum t = load_peer(slice, lane, rank);
+      s += t.s * (double)factor(c, t.m, m);
+    }
+    return s;
+  };
+
+  int parity = 0, at = 0;  // at: the last row's place in its round
+  int64_t base = 0, taken = 0;
+  bool refused = false;
+  StripSum* table = tables;
+  for (;; base += a.round, parity ^= 1) {
+    const int rows = (int)min((int64_t)a.round, n + 1 - base);
+    table = tables + (size_t)parity * 2 * set;
+    // the drafts' scalars are on their way while the rows are read
+    int64_t y = -1;
+    float u = 0.f, zy = -INFINITY, logq = 0.f;
+    const bool draft_lane = lane < rows && base + lane < n;
+    if (draft_lane) {
+      const int64_t d = lo + base + lane;
+      y = a.drafts[d];
+      u = a.accept_u[d];
+      if (y < 0 || y >= a.vocab) y = -1;
+      if (y >= 0) {
+        zy = Vec<T>::load(reinterpret_cast<const T*>(a.target) + (row0 + base + lane) * a.target_stride + y);
+        if (both) logq = Vec<T>::load(reinterpret_cast<const T*>(a.draft) + d * a.draft_stride + y);
+        else if (a.draft_logp != nullptr) logq = a.draft_logp[d];
       }
-      const int u0 = strip * a.strip_units;
-      logp = token_logp<T>(row, a.target_scale, p.m, rest, u0, min(u0 + a.strip_units, row.units), (int)token, lane);
-    } else if (i == e.taken) {
-      int kind = kPlain;
-      bool fine = true;
-      Refused f{};
-      const T* zq = nullptr;
-      if (e.refused) {
-        kind = kWithout;
-        if (a.draft != nullptr) {
-          kind = kLeft;
-          f = refused_of(a, e, s, &fine);
-          zq = reinterpret_cast<const T*>(a.draft) + d * a.draft_stride;
+    }
+    const int drafted = both ? (int)min((int64_t)rows, n - base) : 0;
+    for (int r = 0; r < rows + drafted; ++r) {
+      const bool q = r >= rows;
+      const RowUnits<T> row(q ? a.draft : a.target, q ? lo + base + r - rows : row0 + base + r,
+                            q ? a.draft_stride : a.target_stride, a.vocab);
+      sum_strips<T>(row, q ? a.draft_scale : a.target_scale, a.strip_units, strip0 + mine0, strip0 + mine1,
+                    table + (q ? set + (r - rows) * a.strips : r * a.strips) + mine0, lane);
+    }
+    __syncthreads();
+    for (int r = warp; r < rows + drafted; r += warps) {
+      const bool q = r >= rows;
+      const RowSum t = slice_sum(table + (q ? set + (r - rows) * a.strips : r * a.strips),
+                                 q ? a.draft_scale : a.target_scale);
+      if (lane == 0) sh.slice[parity][q ? kMaxRound + r - rows : r] = t;
+    }
+    exchange();
+    if (a.cluster > 1) {
+      for (int r = warp; r < rows + drafted; r += warps) {
+        const bool q = r >= rows;
+        const int slot = q ? kMaxRound + r - rows : r;
+        const RowSum t = merge(&sh.slice[parity][slot], q ? a.draft_scale : a.target_scale);
+        if (lane == 0) sh.total[parity][slot] = t;
+      }
+      __syncthreads();
+    }
+    const RowSum* totals = a.cluster > 1 ? sh.total[parity] : sh.slice[parity];
+    at = rows - 1;
+    // every warp of every CTA decides alike
+    bool ok = true;
+    if (draft_lane) {
+      const RowSum p = totals[lane];
+      const Scale& c = a.target_scale;
+      const float d = zy - p.m;
+      const float logp = __fmaf_rn(d, c.inv_hi, d * c.inv_lo) - logf((float)p.s);
+      bool fine = usable(p) && y >= 0;
+      if (both) {
+        const RowSum q = totals[kMaxRound + lane];
+        const float e = logq - q.m;
+        logq = __fmaf_rn(e, a.draft_scale.inv_hi, e * a.draft_scale.inv_lo) - logf((float)q.s);
+        fine = fine && usable(q);
+      }
+      ok = fine && u < expf(logp - logq);
+    }
+    const unsigned bad = __ballot_sync(0xFFFFFFFFu, !ok);
+    refused = bad != 0;
+    if (refused) at = __ffs(bad) - 1;
+    // rows of this round whose drafts were taken
+    const int good = (int)min(refused ? (int64_t)at : (int64_t)rows, n - base);
+    for (int r = 0; r < good; ++r) {
+      const int64_t t = __shfl_sync(0xFFFFFFFFu, y, r);
+      if ((base + r) % warps != warp) continue;
+      const RowUnits<T> row(a.target, row0 + base + r, a.target_stride, a.vocab);
+      const int k = ((int)t + row.shift) / N / a.strip_units - strip0;
+      if (k < 0 || k >= a.strips) continue;  // another CTA's strip
+      int u0, u1;
+      units_of(row, k, u0, u1);
+      const float m = totals[r].m;
+      const double rest = other_strips(table + r * a.strips, &sh.slice[parity][r], k, m, a.target_scale) +
+                          (double)sum_without<T>(row, a.target_scale, m, u0, u1, (int)t, lane);
+      const float lp = token_logp<T>(row, a.target_scale, m, rest, (int)t);
+      if (lane == 0) {
+        a.tokens[row0 + base + r] = t;
+        a.logp[row0 + base + r] = lp;
+      }
+    }
+    taken = base + good;
+    if (refused || base + rows == n + 1) break;
+  }
+
+  // the token after the drafts that were taken, from row `taken`
+  const RowUnits<T> row(a.target, row0 + taken, a.target_stride, a.vocab);
+  const RowSum* totals = a.cluster > 1 ? sh.total[parity] : sh.slice[parity];
+  const RowSum p = totals[at];
+  const StripSum* own = table + at * a.strips;
+  const Scale& c = a.target_scale;
+  bool fine = usable(p);
+  int kind = kPlain;
+  int64_t without = -1;
+  Refused f{};
+  const T* zq = nullptr;
+  StripSum* left = table + set + at * a.strips;  // of the draft model's row, then of the difference
+  int without_strip = -1;
+  float without_sum = 0.f;
+  if (refused && fine) {
+    const int64_t d = lo + taken;
+    if (a.draft == nullptr) {
+      kind = kWithout;
+      without = a.drafts[d];
+      if (without >= 0 && without < a.vocab) {
+        const int k = ((int)without + row.shift) / N / a.strip_units - strip0;
+        if (k >= 0 && k < a.strips) {  // every warp sums the strip alike
+          int u0, u1;
+          units_of(row, k, u0, u1);
+          const float s = sum_without<T>(row, c, p.m, u0, u1, (int)without, lane);
+          without_strip = k;
+          without_sum = warp_sum(s);
         }
       }
-      logp = NAN;
-      if (fine) draw<T>(a, r, s, kind, e.refused ? a.drafts[d] : -1, zq, f, a.sample_u[s], &token, &logp, lane);
-      if (lane == 0) a.counts[s] = e.taken;
-    }
-    if (lane == 0) {
-      a.tokens[r] = token;
-      a.logp[r] = logp;
+    } else {
+      kind = kLeft;
+      const RowUnits<T> draft(a.draft, d, a.draft_stride, a.vocab);
+      zq = draft.z;
+      RowSum q;
+      if (both) {
+        q = totals[kMaxRound + at];
+      } else {
+        sum_strips<T>(draft, a.draft_scale, a.strip_units, strip0 + mine0, strip0 + mine1, left + mine0, lane);
+        __syncthreads();
+        if (warp == 0) {
+          const RowSum t = slice_sum(left, a.draft_scale);
+          if (lane == 0) sh.slice[parity][kMaxRound] = t;
+        }
+        exchange();
+        q = merge(&sh.slice[parity][kMaxRound], a.draft_scale);
+      }
+      fine = usable(q);
+      f = Refused{p.m, (float)(1. / p.s), q.m, (float)(1. / q.s)};
+      if (fine) {
+        for (int k = warp; k < a.strips; k += warps) {
+          int u0, u1;
+          units_of(row, k, u0, u1);
+          float s = 0.f;
+          for (int u = u0; u < u1; u += kStripStep) {
+            float r[kLoads * N];
+            left_over<T>(a, f, row, zq, u + lane, 32, u1, step_inside<T>(row, u, u1), r);
+#pragma unroll
+            for (int i = 0; i < kLoads * N; ++i) s += r[i];
+          }
+          s = warp_sum(s);
+          if (lane == 0) left[k] = StripSum{0.f, s};
+        }
+        __syncthreads();
+      }
     }
   }
+
+  if (warp != 0) return;  // the cluster's barriers wait for the warps that are left
+
+  int64_t token = -1;
+  bool mine = rank == 0;  // this CTA writes the token
+  float lp = NAN;
+  if (fine) {
+    auto plain = [&](int k) { return own[k].s * factor(c, own[k].m, p.m); };
+    auto weight = [&](int k) { return kind == kLeft ? left[k].s : kind == kWithout && k == without_strip ? without_sum : plain(k); };
+    // each CTA's share of the weights in its lane, and their running sum
+    double v = 0.;
+    if (kind != kPlain) {
+#pragma unroll 1
+      for (int k = lane; k < a.strips; k += 32) v += (double)weight(k);
+      v = warp_sum64(v);
+      if (a.cluster > 1) {
+        if (lane == 0) sh.weights = v;
+        cluster_sync();
+        v = lane >= a.cluster ? 0. : lane == rank ? v : load_peer(&sh.weights, lane);
+      } else if (lane > 0) {
+        v = 0.;
+      }
+      // nothing is left over where the two models agree, and the refusal was one of rounding
+      if (!__any_sync(0xFFFFFFFFu, v > 0.)) kind = kPlain;
+    }
+    if (kind == kPlain) {
+      RowSum r{0., -INFINITY};
+      if (lane < a.cluster) r = load_peer(&sh.slice[parity][at], lane, rank);
+      v = r.s * (double)factor(c, r.m, p.m);
+    }
+    const double upto = warp_scan64(v, lane), sum = __shfl_sync(0xFFFFFFFFu, upto, 31);
+    const float su = fmaxf(a.sample_u[seq], 0.f);
+    const double t = su < 1.f ? (double)su * sum : (double)INFINITY;  // 1 and above: the last token
+    const unsigned over = __ballot_sync(0xFFFFFFFFu, v > 0. && upto > t);
+    const unsigned any = __ballot_sync(0xFFFFFFFFu, v > 0.);
+    const int owner = over ? __ffs(over) - 1 : 31 - __clz(any);
+    mine = rank == owner;
+    if (mine) {
+      double before = __shfl_sync(0xFFFFFFFFu, upto - v, owner);
+      const int strip = find_strip(a.strips, t, &before, lane, weight);
+      int u0, u1;
+      units_of(row, strip, u0, u1);
+      float rest;
+      const int found = find_element<T>(a, sh.draw, row, u0, u1, t - before, kind, (int)without, zq, f, p.m, &rest, lane);
+      const double others = (double)rest + other_strips(own, &sh.slice[parity][at], strip, p.m, c);
+      if (found >= 0) {
+        token = found;
+        lp = token_logp<T>(row, c, p.m, others, found);
+      }
+    }
+  }
+  if (mine && lane == 0) {
+    a.tokens[row0 + taken] = token;
+    a.logp[row0 + taken] = lp;
+  }
+  if (rank == 0) {
+    if (lane == 0) a.counts[seq] = taken;
+    for (int64_t r = taken + 1 + lane; r <= n; r += 32) {
+      a.tokens[row0 + r] = -1;
+      a.logp[row0 + r] = 0.f;
+    }
+  }
+  if (a.cluster > 1) cluster_sync();  // no CTA leaves while another may read its sums
 }
 
 // ---------------------------------------------------------------------------
@@ -758,72 +810,39 @@ void strips_of(int64_t vocab, int32_t dtype, int32_t* units, int32_t* strips) {
   *strips = (int32_t)((steps + mult - 1) / mult);
 }
 
-// The workspace's parts, each on a 16-byte boundary; sampling needs the first alone.
-size_t sample_space(SampleArgs* a, void* base, int64_t n_drafts, int64_t n_seqs, int32_t strips, bool drafts) {
-  size_t at = 0;
-  auto take = [&](size_t bytes) {
-    void* p = base ? static_cast<uint8_t*>(base) + at : nullptr;
-    at += (bytes + 15) / 16 * 16;
-    return p;
-  };
-  const size_t rows = (size_t)(n_drafts + n_seqs), q_rows = (size_t)(n_drafts > n_seqs ? n_drafts : n_seqs);
-  StripSum* p = static_cast<StripSum*>(take(rows * strips * sizeof(StripSum)));
-  if (a) a->p = p;
-  if (!drafts) return at;
-  SampleArgs none;
-  SampleArgs& o = a ? *a : none;
-  o.q = static_cast<StripSum*>(take(q_rows * strips * sizeof(StripSum)));
-  o.left = static_cast<float*>(take((size_t)n_seqs * strips * sizeof(float)));
-  o.p_total = static_cast<RowSum*>(take(rows * sizeof(RowSum)));
-  o.q_total = static_cast<RowSum*>(take(q_rows * sizeof(RowSum)));
-  o.done = static_cast<uint32_t*>(take(rows * sizeof(uint32_t)));
-  o.q_done = static_cast<uint32_t*>(take((size_t)n_seqs * sizeof(uint32_t)));
-  o.refused = static_cast<uint32_t*>(take((size_t)n_seqs * sizeof(uint32_t)));
-  o.longest = static_cast<int64_t*>(take(sizeof(int64_t)));
-  return at;
-}
-
-// Strips that a warp takes at a time: two where there are enough for every warp of the chip.
-void deal_out(SampleArgs& a, int64_t rows, int sms) {
-  const int64_t warps = (int64_t)sms * kSampleCtas * kSampleWarps;
-  a.each = rows * a.strips >= 8 * warps ? 2 : 1;
+// Sampling: strips that a warp takes at a time, four where every warp of the chip has several
+// such pieces.
+template <typename T>
+cudaError_t run_rows(SampleArgs& a, int sms, cudaStream_t s) {
+  const int64_t chip = (int64_t)sms * kSampleCtas * kSampleWarps, all = a.n_seqs * a.strips;
+  a.each = all >= 32 * chip ? 4 : all >= 4 * chip ? 2 : 1;
   a.pieces = (a.strips + a.each - 1) / a.each;
-}
-
-// CTAs and warps of a CTA for `jobs` jobs of a warp: one warp an SM first.
-struct Launch {
-  int grid, block;
-};
-Launch launch_of(int64_t jobs, int sms) {
-  const int64_t per_sm = (jobs + sms - 1) / sms;
-  const int64_t warps = per_sm < 1 ? 1 : per_sm < kSampleWarps ? per_sm : kSampleWarps;
-  const int64_t ctas = (jobs + warps - 1) / warps, most = (int64_t)sms * kSampleCtas;
-  return Launch{(int)(ctas < 1 ? 1 : ctas < most ? ctas : most), (int)(32 * warps)};
-}
-
-template <typename T>
-cudaError_t run_rows(const SampleArgs& a, int sms, cudaStream_t s) {
-  const Launch l = launch_of(a.n_seqs * a.pieces, sms);
-  cudaError_t e = launch(rows_kernel<T>, l.grid, l.block, 0, s, 1, false, a);
+  // one warp an SM first
+  const int64_t jobs = a.n_seqs * a.pieces, per_sm = (jobs + sms - 1) / sms;
+  const int64_t warps = per_sm < kSampleWarps ? per_sm : kSampleWarps, ctas = (jobs + warps - 1) / warps, most = (int64_t)sms * kSampleCtas;
+  cudaError_t e = launch(rows_kernel<T>, (int)(ctas < most ? ctas : most), (int)(32 * warps), 0, s, 1, false, a);
   if (e != cudaSuccess) return e;
-  const int64_t warps = a.n_seqs < 4ll * sms ? 1 : 4;  // a row each
-  return launch(draw_kernel<T>, (int)((a.n_seqs + warps - 1) / warps), (int)(32 * warps), 0, s, 1, true, a);
+  const int64_t drawers = a.n_seqs < 4ll * sms ? 1 : kDrawWarps;
+  return launch(draw_kernel<T>, (int)((a.n_seqs + drawers - 1) / drawers), (int)(32 * drawers), 0, s, 1, true, a);
 }
 
+// Verification: CTAs a sequence, rows side by side.
 template <typename T>
-cudaError_t run_verify(const SampleArgs& a, int sms, cudaStream_t s) {
-  const int64_t rows = a.n_drafts + a.n_seqs;
-  cudaError_t e = launch(setup_kernel, 1, kSetupThreads, 0, s, 1, false, a);
-  if (e != cudaSuccess) return e;
-  const Launch all = launch_of((rows + (a.both ? a.n_drafts : 0)) * a.pieces, sms);
-  if ((e = launch(verify_kernel<T>, all.grid, all.block, 0, s, 1, true, a)) != cudaSuccess) return e;
-  if (a.draft != nullptr && a.n_drafts > 0) {
-    const Launch one = launch_of(a.n_seqs * a.pieces, sms);
-    if (!a.both && (e = launch(refused_kernel<T>, one.grid, one.block, 0, s, 1, true, a)) != cudaSuccess) return e;
-    if ((e = launch(left_kernel<T>, one.grid, one.block, 0, s, 1, true, a)) != cudaSuccess) return e;
+cudaError_t run_verify(SampleArgs& a, int sms, cudaStream_t s) {
+  const int64_t whole = a.strips;
+  int64_t cluster = 1;
+  while (cluster < kMaxCluster && a.n_seqs * cluster * 2 <= 3 * sms && whole > 2 * cluster) cluster *= 2;
+  const int64_t most = (a.n_drafts + 2 * a.n_seqs - 1) / a.n_seqs;  // rows of a sequence, in the mean
+  a.cluster = (int32_t)cluster;
+  a.strips = (int32_t)((whole + cluster - 1) / cluster);
+  a.round = 1;
+  if (a.n_seqs * cluster <= sms) {
+    const int64_t room = kMaxStrips / a.strips, want = most < kMaxRound ? most : kMaxRound;
+    a.round = (int32_t)(want < room ? want : room);
   }
-  const Launch out = launch_of(rows, sms);
-  return launch(emit_kernel<T>, out.grid, out.block, 0, s, 1, true, a);
+  const size_t smem = (size_t)4 * a.round * a.strips * sizeof(StripSum);
+  const int warps = a.strips < kSampleWarps ? a.strips : kSampleWarps;
+  return launch(verify_kernel<T>, (int)(a.n_seqs * cluster), 32 * warps, smem, s, (int)cluster, false, a);
 }
 
 }  // namespace
@@ -833,14 +852,14 @@ using namespace muon;
 
 extern "C" {
 
-muon_status muon_sample_workspace_bytes(int64_t rows, int64_t n_seqs, int64_t vocab, int32_t dtype, size_t* bytes) {
+muon_status muon_sample_workspace_bytes(int64_t tokens, int64_t vocab, int32_t dtype, size_t* bytes) {
   if (!bytes) return invalid("bytes is NULL");
-  if (rows < 0 || rows > (1ll << 31) - 1 || n_seqs < 0 || n_seqs > rows) return invalid("rows must be in [0, 2^31), n_seqs in [0, rows]");
+  if (tokens < 0 || tokens > (1ll << 31) - 1) return invalid("tokens must be in [0, 2^31)");
   if (vocab < 1 || vocab > (1ll << 30)) return invalid("vocab must be in [1, 2^30]");
   if (dtype != MUON_DTYPE_F32 && dtype != MUON_DTYPE_BF16) return invalid("unknown logits dtype");
   int32_t units, strips;
   strips_of(vocab, dtype, &units, &strips);
-  *bytes = sample_space(nullptr, nullptr, rows - n_seqs, n_seqs, strips, true);
+  *bytes = (size_t)tokens * strips * sizeof(StripSum);
   return MUON_OK;
 }
 
@@ -865,11 +884,10 @@ muon_status muon_sample_tokens(const muon_token_batch* batch, const float* unifo
   a.vocab = (int32_t)batch->vocab;
   a.n_seqs = batch->tokens;
   strips_of(a.vocab, batch->dtype, &a.strip_units, &a.strips);
-  const size_t need = sample_space(&a, workspace, 0, a.n_seqs, a.strips, false);
-  if ((st = check_workspace(workspace, workspace_bytes, need)) != MUON_OK) return st;
+  a.sums = static_cast<StripSum*>(workspace);
+  if ((st = check_workspace(workspace, workspace_bytes, (size_t)a.n_seqs * a.strips * sizeof(StripSum))) != MUON_OK) return st;
   int sms;
   if ((st = find_device(&sms)) != MUON_OK) return st;
-  deal_out(a, a.n_seqs, sms);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = batch->dtype == MUON_DTYPE_BF16 ? run_rows<__nv_bfloat16>(a, sms, s) : run_rows<float>(a, sms, s);
   return e == cudaSuccess ? MUON_OK : cuda_error(e);
@@ -878,7 +896,7 @@ muon_status muon_sample_tokens(const muon_token_batch* batch, const float* unifo
 muon_status muon_verify_drafts(const muon_token_batch* target, const muon_token_batch* draft, const float* draft_logp,
                                const int64_t* draft_offsets, int64_t n_seqs, const float* accept_uniforms,
                                const float* sample_uniforms, int64_t* tokens, int64_t* counts, float* logp,
-                               void* workspace, size_t workspace_bytes, void* stream) {
+                               void* stream) {
   if (!target || !draft) return invalid("target or draft is NULL");
   int32_t st = check_rows(target);
   if (st == MUON_OK) st = check_rows(draft);
@@ -915,13 +933,9 @@ muon_status muon_verify_drafts(const muon_token_batch* target, const muon_token_
   a.draft_scale = scale_of(draft->temperature);
   a.vocab = (int32_t)target->vocab;
   a.n_seqs = n_seqs;
-  a.both = draft->logits && !draft_logp;
   strips_of(a.vocab, target->dtype, &a.strip_units, &a.strips);
-  const size_t need = sample_space(&a, workspace, a.n_drafts, n_seqs, a.strips, true);
-  if ((st = check_workspace(workspace, workspace_bytes, need)) != MUON_OK) return st;
   int sms;
   if ((st = find_device(&sms)) != MUON_OK) return st;
-  deal_out(a, target->tokens, sms);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = target->dtype == MUON_DTYPE_BF16 ? run_verify<__nv_bfloat16>(a, sms, s) : run_verify<float>(a, sms, s);
   return e == cudaSuccess ? MUON_OK : cuda_error(e);

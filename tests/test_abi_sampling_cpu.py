@@ -45,11 +45,11 @@ def test_sample_refuses_bad_arguments(nsm):
 
 
 def _verify(nsm, target=None, draft=None, n_seqs=2, draft_logp=None, offsets=A, accept=A, sample=A, tokens=A, counts=A,
-            logp=A, ws=A, nbytes=1 << 40):
+            logp=A):
     t = _batch(nsm, **{"targets": None, **(target or {})})
     d = _batch(nsm, **{"tokens": 4, **(draft or {})})
     return nsm.lib.muon_verify_drafts(ctypes.byref(t), ctypes.byref(d), draft_logp, offsets, n_seqs, accept, sample,
-                                      tokens, counts, logp, ws, nbytes, None)
+                                      tokens, counts, logp, None)
 
 
 @pytest.mark.parametrize("over", [
@@ -65,7 +65,7 @@ def test_verify_refuses(nsm, over):
 
 
 def test_verify_of_nothing(nsm):
-    assert nsm.lib.muon_verify_drafts(None, None, None, None, 0, None, None, None, None, None, None, 0, None) == nsm.MUON_ERR_INVALID
+    assert nsm.lib.muon_verify_drafts(None, None, None, None, 0, None, None, None, None, None, None) == nsm.MUON_ERR_INVALID
     assert _verify(nsm, dict(tokens=0, logits=None), dict(tokens=0, logits=None), 0, None, None, None, None, None, None,
                    None) == nsm.MUON_OK
 
@@ -73,19 +73,15 @@ def test_verify_of_nothing(nsm):
 def test_workspace(nsm):
     import torch
     need = nsm.muon_sample_workspace_bytes
-    assert need(0, 0, 5, torch.float32) < 64
-    assert need(10, 10, 1000, torch.float32) >= 10 * 2 * 8            # two strips of 512 a row
-    assert need(1 << 20, 1 << 20, 1 << 30, torch.bfloat16) < 20 << 30   # 512 strips at most
-    assert need(10, 2, 1000, torch.bfloat16) < need(20, 4, 1000, torch.bfloat16)
-    for bad in ((-1, 0, 5), (1 << 31, 0, 5), (5, 6, 5), (5, -1, 5), (5, 5, 0), (5, 5, (1 << 30) + 1)):
+    assert need(0, 5, torch.float32) == 0
+    assert need(10, 1000, torch.float32) == 10 * 2 * 8                  # two strips of 512 a row
+    assert need(1 << 20, 1 << 30, torch.bfloat16) == (1 << 20) * 512 * 8   # 512 strips at most
+    for bad in ((-1, 5), (1 << 31, 5), (5, 0), (5, (1 << 30) + 1)):
         with pytest.raises(nsm.MuonError) as e:
             need(*bad, torch.float32)
         assert e.value.status == nsm.MUON_ERR_INVALID
     with pytest.raises(TypeError):
-        need(5, 5, 5, torch.float16)
-    assert _verify(nsm, ws=None) == nsm.MUON_ERR_NO_WORKSPACE
-    assert _verify(nsm, nbytes=16) == nsm.MUON_ERR_NO_WORKSPACE
-    assert _verify(nsm, ws=A + 8) == nsm.MUON_ERR_INVALID
+        need(5, 5, torch.float16)
 
 
 def test_binding_refuses_host_tensors(nsm):
