@@ -47,13 +47,14 @@ namespace {
 constexpr int kTile = 256;          // rows and columns of a tile of dW
 constexpr int kTokens = 64;         // tokens of a stage
 constexpr int kGradThreads = 384;
-constexpr int kGradStages = 7;
+constexpr int kGradStages = 6;
 constexpr int kChunkSteps = 16;     // stages that one accumulator takes
 constexpr uint32_t kChunk = kTokens * 128;          // 64 tokens of 64 bf16 columns
 constexpr uint32_t kOperand = 2 * kChunk;           // a CTA's half of an operand
-constexpr size_t kGradSmem = kGradStages * 2 * kOperand + 1024;
-static_assert(kGradSmem <= 232448 - 1024, "shared memory of one CTA");
 constexpr int kSummers = 8;                         // warps
+constexpr int kTurn = 32 * 33;                      // floats of a warp's 32 x 32 block, to be turned
+constexpr size_t kGradSmem = kGradStages * 2 * kOperand + kSummers * kTurn * 4 + 1024;
+static_assert(kGradSmem <= 232448 - 512, "shared memory of one CTA");
 constexpr uint32_t kGradTmem = 512;
 
 struct GradArgs {
@@ -94,53 +95,56 @@ __device__ __forceinline__ Unit unit_of(const GradArgs& a, int u) {
   return r;
 }
 
-// 16 consecutive columns of a row of dW, s[at ..]; poison, 0 or NaN, is added.
-__device__ __forceinline__ void store_row(const GradArgs& a, int split, int64_t row, int col, const float (&s)[128], int at,
-                                          float poison) {
-  const int n = min(16, a.cols - col);
-  const int64_t e = split * a.split_stride + row * a.stride + col;
-  if (a.bf16) {
-    __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(a.out) + e;
-    if (n == 16 && (reinterpret_cast<uint64_t>(p) & 15) == 0) {
+// A column of a turned block, `rows` elements, to dW.
+template <typename T>
+__device__ __forceinline__ void add_rows(T* p, int64_t stride, int accumulate, const float* turn, int rows) {
+#pragma unroll 1
+  for (int r = 0; r < rows; r += 8) {
+    float y[8];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float x[8] = {};
-        if (a.accumulate) Vec<__nv_bfloat16>::unpack(reinterpret_cast<const uint4*>(p)[k], x);
+    for (int i = 0; i < 8; ++i) y[i] = accumulate && r + i < rows ? Vec<T>::load(p + (r + i) * stride) : 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] += s[at + 8 * k + i] + poison;
-        reinterpret_cast<uint4*>(p)[k] = Vec<__nv_bfloat16>::pack(x);
-      }
-    } else {
+    for (int i = 0; i < 8; ++i)
+      if (r + i < rows) Vec<T>::store(p + (r + i) * stride, y[i] + turn[(r + i) * 33]);
+  }
+}
+
+// A warp's 32 rows x 128 columns of dW from (row0, col), of which lane l has row l; poison, 0 or
+// NaN, is added.
+//
+// Rows of fp32 on 32-byte boundaries that are only written go out as they are, whole sectors
+// a lane.  Others are turned in shared memory, 32 columns at a time, so that a warp's accesses
+// are to one row (2005 x 1537 fp32, added to: 91 us row by lane, TURN_US so).
+__device__ __forceinline__ void store_block(const GradArgs& a, int split, int64_t row0, int col, const float (&s)[128],
+                                            float poison, float* turn, int lane) {
+  const int64_t at = split * a.split_stride + row0 * a.stride + col;
+  float* const out = reinterpret_cast<float*>(a.out) + at;
+  if (!a.bf16 && !a.accumulate && (reinterpret_cast<uint64_t>(out) & 31) == 0 && a.stride % 8 == 0 && col + 128 <= a.cols) {
+    float* const p = out + lane * a.stride;
+    if (row0 + lane < a.outs) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (i < n) p[i] = __float2bfloat16_rn((a.accumulate ? __bfloat162float(p[i]) : 0.f) + (s[at + i] + poison));
+      for (int k = 0; k < 128; k += 8)
+        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p + k), "f"(s[k] + poison),
+                     "f"(s[k + 1] + poison), "f"(s[k + 2] + poison), "f"(s[k + 3] + poison), "f"(s[k + 4] + poison),
+                     "f"(s[k + 5] + poison), "f"(s[k + 6] + poison), "f"(s[k + 7] + poison)
+                     : "memory");
     }
     return;
   }
-  float* p = reinterpret_cast<float*>(a.out) + e;
-  if (n == 16 && (reinterpret_cast<uint64_t>(p) & 31) == 0 && !a.accumulate) {  // whole sectors
+  const int rows = (int)min((int64_t)32, a.outs - row0);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const float* v = s + at + 8 * k;
-      asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p + 8 * k), "f"(v[0] + poison),
-                   "f"(v[1] + poison), "f"(v[2] + poison), "f"(v[3] + poison), "f"(v[4] + poison), "f"(v[5] + poison),
-                   "f"(v[6] + poison), "f"(v[7] + poison)
-                   : "memory");
-    }
-  } else if (n == 16 && (reinterpret_cast<uint64_t>(p) & 15) == 0) {
+  for (int c = 0; c < 128; c += 32) {
+    if (col + c >= a.cols) break;
+    __syncwarp();
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (a.accumulate) x = reinterpret_cast<const float4*>(p)[k];
-      const float* v = s + at + 4 * k;
-      reinterpret_cast<float4*>(p)[k] =
-          make_float4(x.x + (v[0] + poison), x.y + (v[1] + poison), x.z + (v[2] + poison), x.w + (v[3] + poison));
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < n) p[i] = (a.accumulate ? p[i] : 0.f) + (s[at + i] + poison);
+    for (int j = 0; j < 32; ++j) turn[lane * 33 + j] = s[c + j] + poison;
+    __syncwarp();
+    if (col + c + lane >= a.cols) continue;
+    // eight rows' loads before their stores
+    if (a.bf16) add_rows(reinterpret_cast<__nv_bfloat16*>(a.out) + at + c + lane, a.stride, a.accumulate, turn + lane, rows);
+    else add_rows(out + c + lane, a.stride, a.accumulate, turn + lane, rows);
   }
+  __syncwarp();
 }
 
 __global__ void __launch_bounds__(kGradThreads, 1) weight_grad_kernel(const __grid_constant__ GradArgs a) {
@@ -274,6 +278,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) weight_grad_kernel(const __gr
   } else if (warp >= 4) {
     // ---- sums ----
     const int quad = warp & 3, half = (warp - 4) >> 2;
+    float* const turn = reinterpret_cast<float*>(smem + kGradStages * 2 * kOperand) + (warp - 4) * kTurn;
     const uint32_t lead = mapa_shared(&tempty_bar[0], 0);
     const uint32_t from = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(half * (kTile / 2));
     int acc = 0;
@@ -298,13 +303,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) weight_grad_kernel(const __gr
       }
       // where a wait ran out, no stale values pass for a gradient
       const float poison = ok ? 0.f : NAN;
-      const int64_t row = (int64_t)t.m0 + rank * 128 + quad * 32 + lane;
+      const int64_t row0 = (int64_t)t.m0 + rank * 128 + quad * 32;
       const int col = t.n0 + half * (kTile / 2);
-      if (row < a.outs) {
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          if (col + 16 * c < a.cols) store_row(a, t.split, row, col + 16 * c, sum, 16 * c, poison);
-      }
+      if (row0 < a.outs && col < a.cols) store_block(a, t.split, row0, col, sum, poison, turn, lane);
     }
   }
   __syncwarp();
