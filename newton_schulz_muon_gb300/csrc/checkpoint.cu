@@ -7,9 +7,13 @@
 // A thread takes one 16-byte unit of a row at a time (8 bf16 or 4 fp32 columns), so that the
 // 4 or 8 lanes of a block of 32 columns find its largest magnitude with 2 or 3 shuffles and
 // every access of a warp is to consecutive bytes.  A CTA takes kItems times as many
-// consecutive units as it has threads; the loads of all of a thread's units are issued before the first
-// is used.  Each element is read and written by one thread, which reads first: an output may
-// be an input of the same layout.
+// consecutive units as it has threads; the loads of all of a thread's units are issued before
+// the first is used.  Each element is read and written by one thread, which reads first: an
+// output may be an input of the same layout.
+//
+// Bound by HBM, next to which stands the issue of instructions: bf16 passes take magnitudes two
+// at a time and bytes to numbers by their bits, and leave out bounds and alignment where all
+// rows are whole blocks on 16-byte boundaries (SAVE_US).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -26,7 +30,8 @@ namespace muon {
 namespace {
 
 constexpr int kCheckpointThreads = 256;
-constexpr int kItems = 4;
+constexpr int kItems = 4;        // units of a thread: saved or loaded
+constexpr int kGatedItems = 2;   // and of a gated activation, which has several matrices in flight
 
 // A matrix of T, rows `stride` elements apart.
 struct Matrix {
@@ -42,41 +47,61 @@ struct CheckpointArgs {
   int32_t per_row;
 };
 
-// Unit `col / N` of a row; columns from `cols` on are 0.
-template <typename T>
+// Unit `col / N` of a row; columns from `cols` on are 0.  kWhole: every unit lies in the row and on
+// a 16-byte boundary.
+template <typename T, bool kWhole>
 __device__ __forceinline__ uint4 load_cols(const Matrix& m, int64_t row, int col, int cols) {
   constexpr int N = Vec<T>::N;
   const T* p = reinterpret_cast<const T*>(m.p) + row * m.stride + col;
-  if (col + N <= cols && (reinterpret_cast<uint64_t>(p) & 15) == 0) return *reinterpret_cast<const uint4*>(p);
-  float v[N];
+  if constexpr (kWhole) {
+    return *reinterpret_cast<const uint4*>(p);
+  } else {
+    if (col + N <= cols && (reinterpret_cast<uint64_t>(p) & 15) == 0) return *reinterpret_cast<const uint4*>(p);
+    float v[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = col + i < cols ? Vec<T>::load(p + i) : 0.f;
-  return Vec<T>::pack(v);
+    for (int i = 0; i < N; ++i) v[i] = col + i < cols ? Vec<T>::load(p + i) : 0.f;
+    return Vec<T>::pack(v);
+  }
 }
 
-template <typename T>
+template <typename T, bool kWhole>
 __device__ __forceinline__ void store_cols(const Matrix& m, int64_t row, int col, int cols, const float (&v)[Vec<T>::N]) {
   constexpr int N = Vec<T>::N;
   T* p = reinterpret_cast<T*>(m.p) + row * m.stride + col;
-  if (col + N <= cols && (reinterpret_cast<uint64_t>(p) & 15) == 0) {
+  if constexpr (kWhole) {
     *reinterpret_cast<uint4*>(p) = Vec<T>::pack(v);
-    return;
-  }
+  } else if (col + N <= cols && (reinterpret_cast<uint64_t>(p) & 15) == 0) {
+    *reinterpret_cast<uint4*>(p) = Vec<T>::pack(v);
+  } else {
 #pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (col + i < cols) Vec<T>::store(p + i, v[i]);
+    for (int i = 0; i < N; ++i)
+      if (col + i < cols) Vec<T>::store(p + i, v[i]);
+  }
 }
 
-// Quantises the unit whose values are v; the lanes of a block work together.
+// The bits of the largest magnitude of a block, of which a lane has the unit w.
 template <typename T>
-__device__ __forceinline__ void save_unit(const CheckpointView& c, int64_t row, int unit, const float (&v)[Vec<T>::N],
-                                          bool live) {
+__device__ __forceinline__ uint32_t block_most(const uint4& w) {
+  constexpr int kLanes = kBlockCols / Vec<T>::N;
+  if constexpr (sizeof(T) == 2) {  // magnitudes of bf16 compare as 16-bit integers
+    uint32_t m = __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu), __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    return max(m << 16, m & 0xFFFF0000u);
+  } else {
+    uint32_t m = max(max(w.x & 0x7FFFFFFFu, w.y & 0x7FFFFFFFu), max(w.z & 0x7FFFFFFFu, w.w & 0x7FFFFFFFu));
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    return m;
+  }
+}
+
+// Quantises the unit w, whose values are v; the lanes of a block work together.
+template <typename T>
+__device__ __forceinline__ void save_unit(const CheckpointView& c, int64_t row, int unit, const uint4& w,
+                                          const float (&v)[Vec<T>::N], bool live) {
   constexpr int N = Vec<T>::N, kLanes = kBlockCols / N;
-  uint32_t most = 0;
-#pragma unroll
-  for (int i = 0; i < N; ++i) most = max(most, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-#pragma unroll
-  for (int o = kLanes / 2; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+  const uint32_t most = block_most<T>(w);
   if (!live) return;
   const int b = block_byte(most);
   const float scale = steps_per_unit(b);
@@ -122,22 +147,36 @@ template <int N>
 __device__ __forceinline__ void values_of(const SavedUnit<N>& s, float (&v)[N]) {
   const float step = step_of(s.b);
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = (float)(int8_t)(s.q[i / 4] >> (8 * (i % 4))) * step;
+  for (int i = 0; i < N; i += 4) {
+    float x[4];
+    bytes4(s.q[i / 4], x);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[i + k] = x[k] * step;
+  }
 }
 
-// 1 / (1 + e^-g) and 1 minus that, e^-g / (1 + e^-g).
+// 1 / (1 + e^-g) and 1 minus that, which is e^-g / (1 + e^-g).  For bf16, whose results keep 8
+// bits, the approximate exponential and reciprocal, 2^-22 each, and the difference.
+template <typename T>
 __device__ __forceinline__ float2 sigmoid(float g) {
-  const float e = expf(-g), s = __frcp_rn(1.f + e);
-  return make_float2(s, e == INFINITY ? 1.f : e * s);
+  if constexpr (sizeof(T) == 2) {
+    float s;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(s) : "f"(1.f + ex2(-1.4426950408889634f * g)));
+    return make_float2(s, 1.f - s);
+  } else {
+    const float e = expf(-g), s = __frcp_rn(1.f + e);
+    return make_float2(s, e == INFINITY ? 1.f : e * s);
+  }
 }
 
 enum Pass { kSave, kLoad, kGatedForward, kGatedBackward };
 
-template <typename T, int kPass>
+template <typename T, int kPass, bool kWhole>
 __global__ void __launch_bounds__(kCheckpointThreads) checkpoint_kernel(const __grid_constant__ CheckpointArgs a) {
   constexpr int N = Vec<T>::N;
+  constexpr int kCount = kPass == kGatedForward || kPass == kGatedBackward ? kGatedItems : kItems;
   griddep_launch_dependents();
-  const int64_t first = (int64_t)blockIdx.x * (kCheckpointThreads * kItems) + threadIdx.x;
+  const int64_t first = (int64_t)blockIdx.x * (kCheckpointThreads * kCount) + threadIdx.x;
   int64_t row;
   int unit;
   if (a.items <= 0xFFFFFFFFll) {
@@ -147,11 +186,11 @@ __global__ void __launch_bounds__(kCheckpointThreads) checkpoint_kernel(const __
     row = first / a.per_row;
     unit = (int)(first % a.per_row);
   }
-  int64_t rows[kItems];
-  int units[kItems];
-  bool live[kItems];
+  int64_t rows[kCount];
+  int units[kCount];
+  bool live[kCount];
 #pragma unroll
-  for (int k = 0; k < kItems; ++k) {
+  for (int k = 0; k < kCount; ++k) {
     rows[k] = row;
     units[k] = unit;
     live[k] = first + k * kCheckpointThreads < a.items;
@@ -163,63 +202,63 @@ __global__ void __launch_bounds__(kCheckpointThreads) checkpoint_kernel(const __
   }
   const int cols = a.a.cols;
   if constexpr (kPass == kSave || kPass == kGatedForward) {
-    uint4 x[kItems], y[kItems];
+    uint4 x[kCount], y[kCount];
 #pragma unroll
-    for (int k = 0; k < kItems; ++k) {
+    for (int k = 0; k < kCount; ++k) {
       x[k] = y[k] = make_uint4(0, 0, 0, 0);
       if (!live[k]) continue;
-      x[k] = load_cols<T>(a.x, rows[k], units[k] * N, cols);
-      if (kPass == kGatedForward) y[k] = load_cols<T>(a.y, rows[k], units[k] * N, cols);
+      x[k] = load_cols<T, kWhole>(a.x, rows[k], units[k] * N, cols);
+      if (kPass == kGatedForward) y[k] = load_cols<T, kWhole>(a.y, rows[k], units[k] * N, cols);
     }
 #pragma unroll
-    for (int k = 0; k < kItems; ++k) {
+    for (int k = 0; k < kCount; ++k) {
       float g[N];
       Vec<T>::unpack(x[k], g);
-      save_unit<T>(a.a, rows[k], units[k], g, live[k]);
+      save_unit<T>(a.a, rows[k], units[k], x[k], g, live[k]);
       if constexpr (kPass == kGatedForward) {
         float up[N], h[N];
         Vec<T>::unpack(y[k], up);
-        save_unit<T>(a.b, rows[k], units[k], up, live[k]);
+        save_unit<T>(a.b, rows[k], units[k], y[k], up, live[k]);
 #pragma unroll
-        for (int i = 0; i < N; ++i) h[i] = g[i] * sigmoid(g[i]).x * up[i];
-        if (live[k]) store_cols<T>(a.u, rows[k], units[k] * N, cols, h);
+        for (int i = 0; i < N; ++i) h[i] = g[i] * sigmoid<T>(g[i]).x * up[i];
+        if (live[k]) store_cols<T, kWhole>(a.u, rows[k], units[k] * N, cols, h);
       }
     }
   } else {
-    SavedUnit<N> s[kItems], t[kItems];
-    uint4 z[kItems];
+    SavedUnit<N> s[kCount], t[kCount];
+    uint4 z[kCount];
 #pragma unroll
-    for (int k = 0; k < kItems; ++k) {
+    for (int k = 0; k < kCount; ++k) {
       if (!live[k]) continue;
       s[k] = fetch_unit<N>(a.a, rows[k], units[k]);
       if (kPass == kGatedBackward) {
         t[k] = fetch_unit<N>(a.b, rows[k], units[k]);
-        z[k] = load_cols<T>(a.z, rows[k], units[k] * N, cols);
+        z[k] = load_cols<T, kWhole>(a.z, rows[k], units[k] * N, cols);
       }
     }
 #pragma unroll
-    for (int k = 0; k < kItems; ++k) {
+    for (int k = 0; k < kCount; ++k) {
       const int col = units[k] * N;
-      if (!live[k] || col >= cols) continue;
+      if (!live[k] || (!kWhole && col >= cols)) continue;
       float g[N];
       values_of<N>(s[k], g);
       if constexpr (kPass == kLoad) {
-        store_cols<T>(a.u, rows[k], col, cols, g);
+        store_cols<T, kWhole>(a.u, rows[k], col, cols, g);
       } else {
         float up[N], dh[N], dg[N], du[N], h[N];
         values_of<N>(t[k], up);
         Vec<T>::unpack(z[k], dh);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          const float2 e = sigmoid(g[i]);
+          const float2 e = sigmoid<T>(g[i]);
           const float act = g[i] * e.x;
           dg[i] = dh[i] * up[i] * __fmaf_rn(act, e.y, e.x);
           du[i] = dh[i] * act;
           h[i] = act * up[i];
         }
-        store_cols<T>(a.u, rows[k], col, cols, dg);
-        store_cols<T>(a.v, rows[k], col, cols, du);
-        if (a.w.p != nullptr) store_cols<T>(a.w, rows[k], col, cols, h);
+        store_cols<T, kWhole>(a.u, rows[k], col, cols, dg);
+        store_cols<T, kWhole>(a.v, rows[k], col, cols, du);
+        if (a.w.p != nullptr) store_cols<T, kWhole>(a.w, rows[k], col, cols, h);
       }
     }
   }
@@ -255,17 +294,28 @@ CheckpointView view_of(const muon_checkpoint* c) {
   return v;
 }
 
+// Whether every unit of every row lies on a 16-byte boundary (where there is such a matrix).
+bool whole(const Matrix& m, int n) { return !m.p || (aligned(m.p, 16) && m.stride % n == 0); }
+
+template <typename T, int kPass>
+cudaError_t launch_as(const CheckpointArgs& a, int64_t grid, cudaStream_t s) {
+  constexpr int N = Vec<T>::N;
+  const bool all = a.a.cols % kBlockCols == 0 && whole(a.x, N) && whole(a.y, N) && whole(a.z, N) && whole(a.u, N) &&
+                   whole(a.v, N) && whole(a.w, N);
+  return launch(all ? checkpoint_kernel<T, kPass, true> : checkpoint_kernel<T, kPass, false>, (int)grid, kCheckpointThreads, 0,
+                s, 1, false, a);
+}
+
 // The pass over a.a's rows; false: too many of them for a grid.
 template <int kPass>
 bool launch_pass(CheckpointArgs& a, int32_t dtype, cudaStream_t s, cudaError_t* e) {
   const int n = dtype == MUON_DTYPE_BF16 ? 8 : 4;
   a.per_row = a.a.blocks * (kBlockCols / n);
   a.items = a.a.rows * a.per_row;
-  const int64_t per_cta = kCheckpointThreads * kItems, grid = (a.items + per_cta - 1) / per_cta;
+  const int64_t per_cta = kCheckpointThreads * (kPass == kGatedForward || kPass == kGatedBackward ? kGatedItems : kItems);
+  const int64_t grid = (a.items + per_cta - 1) / per_cta;
   if (grid > (1ll << 31) - 1) return false;
-  *e = dtype == MUON_DTYPE_BF16
-           ? launch(checkpoint_kernel<__nv_bfloat16, kPass>, (int)grid, kCheckpointThreads, 0, s, 1, false, a)
-           : launch(checkpoint_kernel<float, kPass>, (int)grid, kCheckpointThreads, 0, s, 1, false, a);
+  *e = dtype == MUON_DTYPE_BF16 ? launch_as<__nv_bfloat16, kPass>(a, grid, s) : launch_as<float, kPass>(a, grid, s);
   return true;
 }
 
