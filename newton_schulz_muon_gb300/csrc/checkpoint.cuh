@@ -46,12 +46,5 @@ __device__ __forceinline__ uint32_t quantize4(float x0, float x1, float x2, floa
   return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
-// Four signed bytes as numbers: with 128 added each is the low byte of a number above 2^23.
-__device__ __forceinline__ void bytes4(uint32_t q, float (&v)[4]) {
-  const uint32_t u = q ^ 0x80808080u, big = 0x4B000000u;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(__byte_perm(u, big, 0x7650 + i)) - 8388736.f;
-}
-
 }  // namespace
 }  // namespace muon
