@@ -62,6 +62,7 @@ struct StripSum {
 struct RowSum {
   double s;
   float m;
+  double rest;  // without the strip that holds the row's draft
 };
 
 struct SampleArgs {
@@ -452,7 +453,7 @@ __global__ void __launch_bounds__(kDrawWarps * 32) draw_kernel(const __grid_cons
       own += (double)weights[warp][k];
     }
     __syncwarp();
-    const RowSum p{warp_sum64(own), m};
+    const RowSum p{warp_sum64(own), m, 0.};
     if (usable(p)) {
       double before = 0.;
       const double at = u < 1.f ? (double)u * p.s : (double)INFINITY;  // 1 and above: the last token
@@ -479,7 +480,10 @@ __global__ void __launch_bounds__(kDrawWarps * 32) draw_kernel(const __grid_cons
 // ---------------------------------------------------------------------------
 // verification
 // ---------------------------------------------------------------------------
+constexpr int kMaxTaken = 64;
 struct SampleShared {
+  float taken_m[kMaxTaken];        // of taken drafts whose log p is not written yet: the row's
+  double taken_rest[kMaxTaken];    // frame, and its sum without the draft's strip
   RowSum slice[2][2 * kMaxRound];  // this CTA's part of each row, read by the cluster's other CTAs
   RowSum total[2][2 * kMaxRound];
   double weights;                  // this CTA's part of the weights a token is drawn from
@@ -492,6 +496,7 @@ __device__ __forceinline__ RowSum load_peer(const RowSum* p, int rank, int own) 
   RowSum r;
   asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(r.s) : "r"(at) : "memory");
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(r.m) : "r"(at + 8) : "memory");
+  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(r.rest) : "r"(at + 16) : "memory");
   return r;
 }
 
@@ -529,57 +534,95 @@ __global__ void __launch_bounds__(kSampleWarps * 32, 3) verify_kernel(const __gr
   };
   // sums a row's slices: warp-wide, the same in every lane
   auto merge = [&](const RowSum* slice, const Scale& c) {
-    RowSum t{0., -INFINITY};
+    RowSum t{0., -INFINITY, 0.};
     if (lane < a.cluster) t = load_peer(slice, lane, rank);
     RowSum r;
     r.m = warp_max(t.m);
-    r.s = warp_sum64(t.s * (double)factor(c, t.m, r.m));
+    const double f = (double)factor(c, t.m, r.m);
+    r.s = warp_sum64(t.s * f);
+    r.rest = warp_sum64(t.rest * f);
     return r;
   };
-  auto slice_sum = [&](const StripSum* table, const Scale& c) {
+  // this CTA's part of a row's sums; skip: the strip of its draft
+  auto slice_sum = [&](const StripSum* table, const Scale& c, int skip) {
     float m = -INFINITY;
     for (int k = lane; k < a.strips; k += 32) m = fmaxf(m, table[k].m);
     RowSum r;
     r.m = warp_max(m);
-    r.s = 0.;
-    for (int k = lane; k < a.strips; k += 32) r.s += (double)(table[k].s * factor(c, table[k].m, r.m));
-    r.s = warp_sum64(r.s);
+    float sum = 0.f, rest = 0.f;
+    for (int k = lane; k < a.strips; k += 32) {
+      const float x = table[k].s * factor(c, table[k].m, r.m);
+      sum += x;
+      rest += k == skip ? 0.f : x;
+    }
+    r.s = warp_sum64((double)sum);
+    r.rest = warp_sum64((double)rest);
     return r;
   };
   // each lane's part of a row's sum without the strip k0 of this CTA
   auto other_strips = [&](const StripSum* table, const RowSum* slice, int k0, float m, const Scale& c) {
-    double s = 0.;
+    float own = 0.f;
     for (int k = lane; k < a.strips; k += 32)
-      if (k != k0) s += (double)(table[k].s * factor(c, table[k].m, m));
+      if (k != k0) own += table[k].s * factor(c, table[k].m, m);
+    double s = (double)own;
     if (lane < a.cluster && lane != rank) {
       const RowSum t = load_peer(slice, lane, rank);
       s += t.s * (double)factor(c, t.m, m);
     }
     return s;
   };
+  // this CTA's strip that holds a token of the target's row, or one that is not its
+  auto strip_of = [&](const RowUnits<T>& row, int64_t token) {
+    return token < 0 ? -1 : ((int)token + row.shift) / N / a.strip_units - strip0;
+  };
+  // the drafts' scalars, of 32 positions at a time: the lane's
+  int64_t pos0 = 0, y = -1;
+  float u = 0.f, zy = -INFINITY, logq = 0.f;
+  auto look = [&] {
+    y = -1;
+    if (pos0 + lane >= n) return;
+    const int64_t d = lo + pos0 + lane;
+    y = a.drafts[d];
+    u = a.accept_u[d];
+    if (y < 0 || y >= a.vocab) y = -1;
+    if (y < 0) return;
+    zy = Vec<T>::load(reinterpret_cast<const T*>(a.target) + (row0 + pos0 + lane) * a.target_stride + y);
+    if (both) logq = Vec<T>::load(reinterpret_cast<const T*>(a.draft) + d * a.draft_stride + y);
+    else if (a.draft_logp != nullptr) logq = a.draft_logp[d];
+  };
+  // tokens and log p of the taken drafts from `from` on, by the warps from w0 on
+  auto emit = [&](int64_t from, int64_t to, int w0) {
+#pragma unroll 1
+    for (int64_t i = from + warp - w0; i < to; i += warps - w0) {
+      const int64_t t = a.drafts[lo + i];
+      const RowUnits<T> row(a.target, row0 + i, a.target_stride, a.vocab);
+      const int k = strip_of(row, t);
+      if (k < 0 || k >= a.strips) continue;  // another CTA's strip
+      int u0, u1;
+      units_of(row, k, u0, u1);
+      const float m = sh.taken_m[i % kMaxTaken];
+      const double rest = (lane == 0 ? sh.taken_rest[i % kMaxTaken] : 0.) +
+                          (double)sum_without<T>(row, a.target_scale, m, u0, u1, (int)t, lane);
+      const float lp = token_logp<T>(row, a.target_scale, m, rest, (int)t);
+      if (lane == 0) {
+        a.tokens[row0 + i] = t;
+        a.logp[row0 + i] = lp;
+      }
+    }
+  };
 
   int parity = 0, at = 0;  // at: the last row's place in its round
-  int64_t base = 0, taken = 0;
+  int64_t base = 0, taken = 0, emitted = 0;
   bool refused = false;
   StripSum* table = tables;
   for (;; base += a.round, parity ^= 1) {
     const int rows = (int)min((int64_t)a.round, n + 1 - base);
     table = tables + (size_t)parity * 2 * set;
-    // the drafts' scalars are on their way while the rows are read
-    int64_t y = -1;
-    float u = 0.f, zy = -INFINITY, logq = 0.f;
-    const bool draft_lane = lane < rows && base + lane < n;
-    if (draft_lane) {
-      const int64_t d = lo + base + lane;
-      y = a.drafts[d];
-      u = a.accept_u[d];
-      if (y < 0 || y >= a.vocab) y = -1;
-      if (y >= 0) {
-        zy = Vec<T>::load(reinterpret_cast<const T*>(a.target) + (row0 + base + lane) * a.target_stride + y);
-        if (both) logq = Vec<T>::load(reinterpret_cast<const T*>(a.draft) + d * a.draft_stride + y);
-        else if (a.draft_logp != nullptr) logq = a.draft_logp[d];
-      }
+    if (base == 0 || base + rows > pos0 + 32) {
+      pos0 = base;
+      look();
     }
+    const int off = (int)(base - pos0);  // the lane of the round's first row
     const int drafted = both ? (int)min((int64_t)rows, n - base) : 0;
     for (int r = 0; r < rows + drafted; ++r) {
       const bool q = r >= rows;
@@ -591,8 +634,13 @@ __global__ void __launch_bounds__(kSampleWarps * 32, 3) verify_kernel(const __gr
     __syncthreads();
     for (int r = warp; r < rows + drafted; r += warps) {
       const bool q = r >= rows;
+      int skip = -1;
+      if (!q) {
+        const RowUnits<T> row(a.target, row0 + base + r, a.target_stride, a.vocab);
+        skip = strip_of(row, __shfl_sync(0xFFFFFFFFu, y, off + r));
+      }
       const RowSum t = slice_sum(table + (q ? set + (r - rows) * a.strips : r * a.strips),
-                                 q ? a.draft_scale : a.target_scale);
+                                 q ? a.draft_scale : a.target_scale, skip);
       if (lane == 0) sh.slice[parity][q ? kMaxRound + r - rows : r] = t;
     }
     exchange();
@@ -609,44 +657,38 @@ __global__ void __launch_bounds__(kSampleWarps * 32, 3) verify_kernel(const __gr
     at = rows - 1;
     // every warp of every CTA decides alike
     bool ok = true;
-    if (draft_lane) {
-      const RowSum p = totals[lane];
+    if (lane >= off && lane < off + rows && pos0 + lane < n) {
+      const RowSum p = totals[lane - off];
       const Scale& c = a.target_scale;
       const float d = zy - p.m;
       const float logp = __fmaf_rn(d, c.inv_hi, d * c.inv_lo) - logf((float)p.s);
       bool fine = usable(p) && y >= 0;
+      float lq = logq;
       if (both) {
-        const RowSum q = totals[kMaxRound + lane];
+        const RowSum q = totals[kMaxRound + lane - off];
         const float e = logq - q.m;
-        logq = __fmaf_rn(e, a.draft_scale.inv_hi, e * a.draft_scale.inv_lo) - logf((float)q.s);
+        lq = __fmaf_rn(e, a.draft_scale.inv_hi, e * a.draft_scale.inv_lo) - logf((float)q.s);
         fine = fine && usable(q);
       }
-      ok = fine && u < expf(logp - logq);
+      ok = fine && u < expf(logp - lq);
     }
-    const unsigned bad = __ballot_sync(0xFFFFFFFFu, !ok);
+    const unsigned bad = __ballot_sync(0xFFFFFFFFu, !ok) >> off;
     refused = bad != 0;
     if (refused) at = __ffs(bad) - 1;
-    // rows of this round whose drafts were taken
+    // rows of this round whose drafts were taken; their log p comes later, when it delays no row
     const int good = (int)min(refused ? (int64_t)at : (int64_t)rows, n - base);
-    for (int r = 0; r < good; ++r) {
-      const int64_t t = __shfl_sync(0xFFFFFFFFu, y, r);
-      if ((base + r) % warps != warp) continue;
-      const RowUnits<T> row(a.target, row0 + base + r, a.target_stride, a.vocab);
-      const int k = ((int)t + row.shift) / N / a.strip_units - strip0;
-      if (k < 0 || k >= a.strips) continue;  // another CTA's strip
-      int u0, u1;
-      units_of(row, k, u0, u1);
-      const float m = totals[r].m;
-      const double rest = other_strips(table + r * a.strips, &sh.slice[parity][r], k, m, a.target_scale) +
-                          (double)sum_without<T>(row, a.target_scale, m, u0, u1, (int)t, lane);
-      const float lp = token_logp<T>(row, a.target_scale, m, rest, (int)t);
-      if (lane == 0) {
-        a.tokens[row0 + base + r] = t;
-        a.logp[row0 + base + r] = lp;
-      }
+    if (warp == 0 && lane < good) {
+      sh.taken_m[(base + lane) % kMaxTaken] = totals[lane].m;
+      sh.taken_rest[(base + lane) % kMaxTaken] = totals[lane].rest;
     }
     taken = base + good;
     if (refused || base + rows == n + 1) break;
+    if (taken - emitted + a.round > kMaxTaken) {
+      __syncthreads();
+      emit(emitted, taken, 0);
+      emitted = taken;
+      __syncthreads();
+    }
   }
 
   // the token after the drafts that were taken, from row `taken`
@@ -669,7 +711,7 @@ __global__ void __launch_bounds__(kSampleWarps * 32, 3) verify_kernel(const __gr
       kind = kWithout;
       without = a.drafts[d];
       if (without >= 0 && without < a.vocab) {
-        const int k = ((int)without + row.shift) / N / a.strip_units - strip0;
+        const int k = strip_of(row, without);
         if (k >= 0 && k < a.strips) {  // every warp sums the strip alike
           int u0, u1;
           units_of(row, k, u0, u1);
@@ -689,7 +731,7 @@ __global__ void __launch_bounds__(kSampleWarps * 32, 3) verify_kernel(const __gr
         sum_strips<T>(draft, a.draft_scale, a.strip_units, strip0 + mine0, strip0 + mine1, left + mine0, lane);
         __syncthreads();
         if (warp == 0) {
-          const RowSum t = slice_sum(left, a.draft_scale);
+          const RowSum t = slice_sum(left, a.draft_scale, -1);
           if (lane == 0) sh.slice[parity][kMaxRound] = t;
         }
         exchange();
@@ -716,6 +758,9 @@ __global__ void __launch_bounds__(kSampleWarps * 32, 3) verify_kernel(const __gr
     }
   }
 
+  // the first warp draws the token, the others (or it alone) write the taken drafts
+  __syncthreads();
+  if (warp != 0 || warps == 1) emit(emitted, taken, warps == 1 ? 0 : 1);
   if (warp != 0) return;  // the cluster's barriers wait for the warps that are left
 
   int64_t token = -1;
@@ -741,7 +786,7 @@ __global__ void __launch_bounds__(kSampleWarps * 32, 3) verify_kernel(const __gr
       if (!__any_sync(0xFFFFFFFFu, v > 0.)) kind = kPlain;
     }
     if (kind == kPlain) {
-      RowSum r{0., -INFINITY};
+      RowSum r{0., -INFINITY, 0.};
       if (lane < a.cluster) r = load_peer(&sh.slice[parity][at], lane, rank);
       v = r.s * (double)factor(c, r.m, p.m);
     }
