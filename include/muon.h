@@ -458,8 +458,10 @@ typedef struct {
  * taken. */
 muon_status muon_token_logprobs(const muon_token_batch* batch, float* logp, void* stream);
 
-/* Workspace of muon_sample_tokens (bytes).  Host work. */
-muon_status muon_sample_workspace_bytes(int64_t tokens, int64_t vocab, int32_t dtype, size_t* bytes);
+/* Workspace of the two calls below (bytes).  rows: the rows of logits to sample; for
+ * verification the target's, n_drafts + n_seqs, and n_drafts more where draft_logp is NULL and
+ * the draft model's logits are not.  Host work. */
+muon_status muon_sample_workspace_bytes(int64_t rows, int64_t vocab, int32_t dtype, size_t* bytes);
 
 /* A token for each row of logits, drawn with a given uniform number: p = softmax(logits /
  * temperature), the first token j with sum_{i <= j} p_i > uniforms[t] sum_i p_i.
@@ -496,11 +498,12 @@ muon_status muon_sample_tokens(const muon_token_batch* batch, const float* unifo
  *   logp: [n_drafts + n_seqs] fp32, log p of the tokens, 0 where they are -1 (the old_logp
  *     of muon_policy_loss, whose mask is tokens >= 0).
  * Rows without probabilities refuse their draft, and the token drawn there is -1, its logp
- * NaN.  No workspace. */
+ * NaN. */
 muon_status muon_verify_drafts(const muon_token_batch* target, const muon_token_batch* draft,
                                const float* draft_logp, const int64_t* draft_offsets, int64_t n_seqs,
                                const float* accept_uniforms, const float* sample_uniforms,
-                               int64_t* tokens, int64_t* counts, float* logp, void* stream);
+                               int64_t* tokens, int64_t* counts, float* logp, void* workspace,
+                               size_t workspace_bytes, void* stream);
 
 /* Workspace of muon_policy_loss and muon_preference_loss (bytes).  Host work. */
 muon_status muon_loss_workspace_bytes(int64_t tokens, int64_t n_seqs, size_t* bytes);

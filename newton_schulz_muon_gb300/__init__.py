@@ -153,7 +153,7 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
         "muon_sample_workspace_bytes": (c_int32, [c_int64, c_int64, c_int32, POINTER(c_size_t)]),
         "muon_sample_tokens": (c_int32, [POINTER(muon_token_batch), P, P, P, P, c_size_t, P]),
         "muon_verify_drafts": (c_int32, [POINTER(muon_token_batch), POINTER(muon_token_batch), P, P, c_int64, P, P,
-                                         P, P, P, P]),
+                                         P, P, P, P, c_size_t, P]),
         "muon_checkpoint_bytes": (c_int32, [c_int64, c_int64, POINTER(c_size_t)]),
         "muon_checkpoint_save": (c_int32, [P, c_int64, c_int32, POINTER(muon_checkpoint), P]),
         "muon_checkpoint_load": (c_int32, [POINTER(muon_checkpoint), P, c_int64, c_int32, P]),
@@ -725,7 +725,7 @@ def muon_sample_tokens(logits, uniforms, mask=None, temperature: float = 1.0, to
 
 def muon_verify_drafts(logits, drafts, draft_offsets, accept_uniforms, sample_uniforms, draft_logits=None,
                        draft_logp=None, temperature: float = 1.0, draft_temperature: Optional[float] = None,
-                       tokens=None, counts=None, logp=None, stream=None):
+                       tokens=None, counts=None, logp=None, workspace=None, stream=None):
     """Verifies the drafted tokens of several sequences against the target's probabilities.
 
     logits: [N + S, vocab], for each sequence a row for each of its drafts and one after them;
@@ -752,8 +752,11 @@ def muon_verify_drafts(logits, drafts, draft_offsets, accept_uniforms, sample_un
             raise ValueError(f"draft_logits: expected [{n}, {target.vocab}] {logits.dtype} values on cuda:{device}, got "
                              f"shape {tuple(draft_logits.shape)}, {draft_logits.dtype} on {draft_logits.device}")
     draft.targets = _vector(drafts, n, i64, "drafts", device)
+    both = draft_logits is not None and draft_logp is None
+    nbytes = muon_sample_workspace_bytes(rows + (n if both else 0), target.vocab, logits.dtype)
     context, handle = _on_stream(stream, device)
     with context:
+        _keep, ws, nbytes = _space(workspace, nbytes, device, handle)
         if tokens is None:
             tokens = torch.empty(rows, dtype=i64, device=device)
         if counts is None:
@@ -765,8 +768,8 @@ def muon_verify_drafts(logits, drafts, draft_offsets, accept_uniforms, sample_un
             _vector(draft_offsets, n_seqs + 1, i64, "draft_offsets", device), n_seqs,
             _vector(accept_uniforms, n, f32, "accept_uniforms", device),
             _vector(sample_uniforms, n_seqs, f32, "sample_uniforms", device), _vector(tokens, rows, i64, "tokens", device),
-            _vector(counts, n_seqs, i64, "counts", device), _vector(logp, rows, f32, "logp", device), handle),
-            "muon_verify_drafts")
+            _vector(counts, n_seqs, i64, "counts", device), _vector(logp, rows, f32, "logp", device), ws, nbytes,
+            handle), "muon_verify_drafts")
     return tokens, counts, logp
 
 

@@ -17,11 +17,12 @@
 // second kernel draws the tokens, a warp a row.  (With a CTA a row 2048 rows of 131072 bf16
 // logits took 117 us: the ends of rows, and 3.03 rounds of CTAs that took 4.  ROWS_US so.)
 //
-// Verification: a cluster of CTAs a sequence, whose rows are taken one after the other until a
-// draft is refused (side by side where there are few sequences).  (Dealing out the strips of
-// all sequences' rows too, position by position, with the verdict by the warp that finishes a
-// row, took 246 us for 512 sequences of four drafts: a warp that judges falls behind, so that
-// it is the last at the next row as well.  VERIFY_US so.)
+// Verification: a CTA a row (a cluster of them where there are few rows), position by position
+// over all sequences, judges the row's draft; rows of a sequence whose draft was refused before
+// are left out as far as that is known when their CTA starts, which changes no result.  A second
+// kernel, a CTA or cluster a sequence, draws the tokens.  (A CTA a sequence, row after row, took
+// 191 us for 512 sequences of four drafts: 456 sequences run at first and the others when the chip is
+// half empty.  VERIFY_US so.)
 //
 // Sums over a strip are fp32 (1024 bf16 or 512 fp32 logits, 32 or 16 a lane and then the
 // lanes'), sums over strips and the search for the token's strip are in 64 bits: a token's
@@ -44,7 +45,6 @@ namespace {
 constexpr int kLoads = 4;                  // 16-byte units a lane takes at a time
 constexpr int kStripStep = 32 * kLoads;    // units that a warp takes at a time
 constexpr int kMaxStrips = 512;            // of a row; longer rows have longer strips
-constexpr int kMaxRound = 8;               // rows of a sequence side by side
 constexpr int kMaxCluster = 8;
 constexpr int kSampleWarps = 8;            // of a CTA, at most
 constexpr int kSampleCtas = 4;             // CTAs an SM, by their registers
@@ -85,10 +85,12 @@ struct SampleArgs {
   int32_t strips;            // of a row; of a CTA's part of it in verification
   // sampling
   int32_t each, pieces;      // strips that a warp takes at a time; of a row: strips / each, rounded up
-  StripSum* sums;            // workspace, [rows][strips]
+  StripSum* sums;            // workspace, [rows][strips of a row]
   // verification
-  int32_t cluster;           // CTAs a sequence
-  int32_t round;             // rows of a sequence taken side by side
+  StripSum* q_sums;          // workspace, [drafts][all strips], where draft_logp is null
+  int32_t cluster;           // CTAs a row or sequence
+  int32_t all_strips;        // of a row
+  int32_t positions;         // of a sequence that have a CTA each; it takes every positions-th row
 };
 
 __device__ __forceinline__ float factor(const Scale& c, float m, float to) {
@@ -480,15 +482,17 @@ __global__ void __launch_bounds__(kDrawWarps * 32) draw_kernel(const __grid_cons
 // ---------------------------------------------------------------------------
 // verification
 // ---------------------------------------------------------------------------
-constexpr int kMaxTaken = 64;
-struct SampleShared {
-  float taken_m[kMaxTaken];        // of taken drafts whose log p is not written yet: the row's
-  double taken_rest[kMaxTaken];    // frame, and its sum without the draft's strip
-  RowSum slice[2][2 * kMaxRound];  // this CTA's part of each row, read by the cluster's other CTAs
-  RowSum total[2][2 * kMaxRound];
-  double weights;                  // this CTA's part of the weights a token is drawn from
-  DrawSpace draw;
+struct Sequence {
+  int64_t lo, n, row0;  // first draft, drafts, first row
 };
+// Offsets out of order or range lead to nothing outside the arrays.
+__device__ __forceinline__ Sequence sequence_of(const SampleArgs& a, int64_t s) {
+  Sequence q;
+  q.lo = min(max(a.offsets[s], (int64_t)0), a.n_drafts);
+  q.n = min(max(a.offsets[s + 1], q.lo), a.n_drafts) - q.lo;
+  q.row0 = q.lo + s;
+  return q;
+}
 
 __device__ __forceinline__ RowSum load_peer(const RowSum* p, int rank, int own) {
   if (rank == own) return *p;
@@ -506,261 +510,229 @@ __device__ __forceinline__ double load_peer(const double* p, int rank) {
   return v;
 }
 
-// A cluster of CTAs a sequence.  Its rows are taken `round` at a time until a draft is refused.
+// A CTA's strips [strip0, strip0 + a.strips) of a row: the units of strip k.
 template <typename T>
-__global__ void __launch_bounds__(kSampleWarps * 32, 3) verify_kernel(const __grid_constant__ SampleArgs a) {
+__device__ __forceinline__ void units_of(const SampleArgs& a, const RowUnits<T>& row, int strip, int& u0, int& u1) {
+  u0 = (int)min((int64_t)strip * a.strip_units, (int64_t)row.units);
+  u1 = min(u0 + a.strip_units, row.units);
+}
+
+// Adds up n strips (-1: no strip is left out of rest): warp-wide, the same in every lane.
+__device__ __forceinline__ RowSum sum_table(const StripSum* table, int n, const Scale& c, int skip, int lane) {
+  float m = -INFINITY;
+#pragma unroll 4
+  for (int k = lane; k < n; k += 32) m = fmaxf(m, table[k].m);
+  RowSum r;
+  r.m = warp_max(m);
+  float sum = 0.f, rest = 0.f;
+#pragma unroll 4
+  for (int k = lane; k < n; k += 32) {
+    const float x = table[k].s * factor(c, table[k].m, r.m);
+    sum += x;
+    rest += k == skip ? 0.f : x;
+  }
+  r.s = warp_sum64((double)sum);
+  r.rest = warp_sum64((double)rest);
+  return r;
+}
+
+// Adds up the CTAs' parts of a row.
+__device__ __forceinline__ RowSum merge(const RowSum* slice, const Scale& c, int cluster, int rank, int lane) {
+  if (cluster == 1) return *slice;
+  RowSum t{0., -INFINITY, 0.};
+  if (lane < cluster) t = load_peer(slice, lane, rank);
+  RowSum r;
+  r.m = warp_max(t.m);
+  const double f = (double)factor(c, t.m, r.m);
+  r.s = warp_sum64(t.s * f);
+  r.rest = warp_sum64(t.rest * f);
+  return r;
+}
+
+// Strip sums of a row of the target (and of the draft model's, where its probabilities are
+// needed), the verdict on its draft and, as if it were taken, the draft's log p.
+// counts[s], all ones at first, becomes the first refused position.
+template <typename T>
+__global__ void __launch_bounds__(kSampleWarps * 32, 3) judge_kernel(const __grid_constant__ SampleArgs a) {
   constexpr int N = Vec<T>::N;
-  extern __shared__ StripSum tables[];  // [2][target and draft][round][strips]
-  __shared__ SampleShared sh;
+  extern __shared__ StripSum tables[];  // [target and draft][strips]
+  __shared__ RowSum slice[2][2];
+  __shared__ bool stop;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int rank = a.cluster > 1 ? (int)cluster_ctarank() : 0;
-  const int64_t seq = blockIdx.x / a.cluster;
-  // offsets out of order or range: nothing outside the arrays is touched
-  const int64_t lo = min(max(a.offsets[seq], (int64_t)0), a.n_drafts);
-  const int64_t n = min(max(a.offsets[seq + 1], lo), a.n_drafts) - lo;
-  const int64_t row0 = lo + seq;  // the sequence's first row
-  const bool both = a.draft != nullptr && a.draft_logp == nullptr;  // rows of both models a round
-  const int set = a.round * a.strips;
+  const int64_t unit = blockIdx.x / a.cluster, first = unit / a.n_seqs, seq = unit - first * a.n_seqs;
+  const Sequence e = sequence_of(a, seq);
+  const bool both = a.draft != nullptr && a.draft_logp == nullptr;
   const int strip0 = rank * a.strips;
   // of the CTA's strips this warp's
   const int per_warp = (a.strips + warps - 1) / warps, mine0 = min(warp * per_warp, a.strips), mine1 = min(mine0 + per_warp, a.strips);
-  auto exchange = [&] {
-    if (a.cluster > 1) cluster_sync();
-    else __syncthreads();
-  };
-  auto units_of = [&](const RowUnits<T>& row, int k, int& u0, int& u1) {  // of this CTA's strip k
-    u0 = (int)min((int64_t)(strip0 + k) * a.strip_units, (int64_t)row.units);
-    u1 = min(u0 + a.strip_units, row.units);
-  };
-  // sums a row's slices: warp-wide, the same in every lane
-  auto merge = [&](const RowSum* slice, const Scale& c) {
-    RowSum t{0., -INFINITY, 0.};
-    if (lane < a.cluster) t = load_peer(slice, lane, rank);
-    RowSum r;
-    r.m = warp_max(t.m);
-    const double f = (double)factor(c, t.m, r.m);
-    r.s = warp_sum64(t.s * f);
-    r.rest = warp_sum64(t.rest * f);
-    return r;
-  };
-  // this CTA's part of a row's sums; skip: the strip of its draft
-  auto slice_sum = [&](const StripSum* table, const Scale& c, int skip) {
-    float m = -INFINITY;
-    for (int k = lane; k < a.strips; k += 32) m = fmaxf(m, table[k].m);
-    RowSum r;
-    r.m = warp_max(m);
-    float sum = 0.f, rest = 0.f;
-    for (int k = lane; k < a.strips; k += 32) {
-      const float x = table[k].s * factor(c, table[k].m, r.m);
-      sum += x;
-      rest += k == skip ? 0.f : x;
+  griddep_launch_dependents();
+  unsigned long long* const refused = reinterpret_cast<unsigned long long*>(a.counts) + seq;
+  int parity = 0;
+  for (int64_t i = first; i <= e.n; i += a.positions, parity ^= 1) {
+    if (a.cluster == 1) {  // CTAs of a cluster must go the same way
+      if (threadIdx.x == 0) stop = __ldcg(refused) < (unsigned long long)i;
+      __syncthreads();
+      if (stop) break;
     }
-    r.s = warp_sum64((double)sum);
-    r.rest = warp_sum64((double)rest);
-    return r;
-  };
-  // each lane's part of a row's sum without the strip k0 of this CTA
-  auto other_strips = [&](const StripSum* table, const RowSum* slice, int k0, float m, const Scale& c) {
-    float own = 0.f;
-    for (int k = lane; k < a.strips; k += 32)
-      if (k != k0) own += table[k].s * factor(c, table[k].m, m);
-    double s = (double)own;
-    if (lane < a.cluster && lane != rank) {
-      const RowSum t = load_peer(slice, lane, rank);
-      s += t.s * (double)factor(c, t.m, m);
+    const int64_t r = e.row0 + i, d = e.lo + i;
+    const bool drafted = i < e.n;
+    int64_t y = -1;
+    float u = 0.f, zy = 0.f, logq = 0.f;
+    if (warp == 0 && drafted) {  // on their way while the row is read
+      y = a.drafts[d];
+      u = a.accept_u[d];
+      if (!both && a.draft_logp != nullptr) logq = a.draft_logp[d];
     }
-    return s;
-  };
-  // this CTA's strip that holds a token of the target's row, or one that is not its
-  auto strip_of = [&](const RowUnits<T>& row, int64_t token) {
-    return token < 0 ? -1 : ((int)token + row.shift) / N / a.strip_units - strip0;
-  };
-  // the drafts' scalars, of 32 positions at a time: the lane's
-  int64_t pos0 = 0, y = -1;
-  float u = 0.f, zy = -INFINITY, logq = 0.f;
-  auto look = [&] {
-    y = -1;
-    if (pos0 + lane >= n) return;
-    const int64_t d = lo + pos0 + lane;
-    y = a.drafts[d];
-    u = a.accept_u[d];
-    if (y < 0 || y >= a.vocab) y = -1;
-    if (y < 0) return;
-    zy = Vec<T>::load(reinterpret_cast<const T*>(a.target) + (row0 + pos0 + lane) * a.target_stride + y);
-    if (both) logq = Vec<T>::load(reinterpret_cast<const T*>(a.draft) + d * a.draft_stride + y);
-    else if (a.draft_logp != nullptr) logq = a.draft_logp[d];
-  };
-  // tokens and log p of the taken drafts from `from` on, by the warps from w0 on
-  auto emit = [&](int64_t from, int64_t to, int w0) {
-#pragma unroll 1
-    for (int64_t i = from + warp - w0; i < to; i += warps - w0) {
-      const int64_t t = a.drafts[lo + i];
-      const RowUnits<T> row(a.target, row0 + i, a.target_stride, a.vocab);
-      const int k = strip_of(row, t);
-      if (k < 0 || k >= a.strips) continue;  // another CTA's strip
-      int u0, u1;
-      units_of(row, k, u0, u1);
-      const float m = sh.taken_m[i % kMaxTaken];
-      const double rest = (lane == 0 ? sh.taken_rest[i % kMaxTaken] : 0.) +
-                          (double)sum_without<T>(row, a.target_scale, m, u0, u1, (int)t, lane);
-      const float lp = token_logp<T>(row, a.target_scale, m, rest, (int)t);
-      if (lane == 0) {
-        a.tokens[row0 + i] = t;
-        a.logp[row0 + i] = lp;
+    const RowUnits<T> row(a.target, r, a.target_stride, a.vocab);
+    sum_strips<T>(row, a.target_scale, a.strip_units, strip0 + mine0, strip0 + mine1, tables + mine0, lane);
+    if (both && drafted) {
+      const RowUnits<T> draft(a.draft, d, a.draft_stride, a.vocab);
+      sum_strips<T>(draft, a.draft_scale, a.strip_units, strip0 + mine0, strip0 + mine1, tables + a.strips + mine0, lane);
+    }
+    if (warp == 0) {
+      if (y < 0 || y >= a.vocab) y = -1;
+      if (y >= 0) {
+        zy = Vec<T>::load(row.z + y);
+        if (both) logq = Vec<T>::load(reinterpret_cast<const T*>(a.draft) + d * a.draft_stride + y);
       }
-    }
-  };
-
-  int parity = 0, at = 0;  // at: the last row's place in its round
-  int64_t base = 0, taken = 0, emitted = 0;
-  bool refused = false;
-  StripSum* table = tables;
-  for (;; base += a.round, parity ^= 1) {
-    const int rows = (int)min((int64_t)a.round, n + 1 - base);
-    table = tables + (size_t)parity * 2 * set;
-    if (base == 0 || base + rows > pos0 + 32) {
-      pos0 = base;
-      look();
-    }
-    const int off = (int)(base - pos0);  // the lane of the round's first row
-    const int drafted = both ? (int)min((int64_t)rows, n - base) : 0;
-    for (int r = 0; r < rows + drafted; ++r) {
-      const bool q = r >= rows;
-      const RowUnits<T> row(q ? a.draft : a.target, q ? lo + base + r - rows : row0 + base + r,
-                            q ? a.draft_stride : a.target_stride, a.vocab);
-      sum_strips<T>(row, q ? a.draft_scale : a.target_scale, a.strip_units, strip0 + mine0, strip0 + mine1,
-                    table + (q ? set + (r - rows) * a.strips : r * a.strips) + mine0, lane);
     }
     __syncthreads();
-    for (int r = warp; r < rows + drafted; r += warps) {
-      const bool q = r >= rows;
-      int skip = -1;
-      if (!q) {
-        const RowUnits<T> row(a.target, row0 + base + r, a.target_stride, a.vocab);
-        skip = strip_of(row, __shfl_sync(0xFFFFFFFFu, y, off + r));
+    // the strips' sums, for the kernel that draws
+    for (int k = threadIdx.x; k < a.strips && strip0 + k < a.all_strips; k += blockDim.x) {
+      a.sums[r * a.all_strips + strip0 + k] = tables[k];
+      if (both && drafted) a.q_sums[d * a.all_strips + strip0 + k] = tables[a.strips + k];
+    }
+    if (drafted) {
+      const int strip = y < 0 ? -1 : ((int)y + row.shift) / N / a.strip_units - strip0;  // of the draft, in this CTA's
+      if (warp == 0) {
+        const RowSum p = sum_table(tables, a.strips, a.target_scale, strip, lane);
+        if (lane == 0) slice[parity][0] = p;
+        if (both) {
+          const RowSum q = sum_table(tables + a.strips, a.strips, a.draft_scale, -1, lane);
+          if (lane == 0) slice[parity][1] = q;
+        }
+        __syncwarp();
       }
-      const RowSum t = slice_sum(table + (q ? set + (r - rows) * a.strips : r * a.strips),
-                                 q ? a.draft_scale : a.target_scale, skip);
-      if (lane == 0) sh.slice[parity][q ? kMaxRound + r - rows : r] = t;
-    }
-    exchange();
-    if (a.cluster > 1) {
-      for (int r = warp; r < rows + drafted; r += warps) {
-        const bool q = r >= rows;
-        const int slot = q ? kMaxRound + r - rows : r;
-        const RowSum t = merge(&sh.slice[parity][slot], q ? a.draft_scale : a.target_scale);
-        if (lane == 0) sh.total[parity][slot] = t;
+      if (a.cluster > 1) cluster_sync();
+      if (warp == 0) {
+        const RowSum p = merge(&slice[parity][0], a.target_scale, a.cluster, rank, lane);
+        const float x = zy - p.m;
+        const float logp = __fmaf_rn(x, a.target_scale.inv_hi, x * a.target_scale.inv_lo) - logf((float)p.s);
+        bool ok = usable(p) && y >= 0;
+        if (both) {
+          const RowSum q = merge(&slice[parity][1], a.draft_scale, a.cluster, rank, lane);
+          const float z = logq - q.m;
+          logq = __fmaf_rn(z, a.draft_scale.inv_hi, z * a.draft_scale.inv_lo) - logf((float)q.s);
+          ok = ok && usable(q);
+        }
+        ok = ok && u < expf(logp - logq);
+        if (!ok) {
+          if (rank == 0 && lane == 0) atomicMin(refused, (unsigned long long)i);
+        } else if (strip >= 0 && strip < a.strips) {
+          int u0, u1;
+          units_of(a, row, strip0 + strip, u0, u1);
+          const double rest = (lane == 0 ? p.rest : 0.) + (double)sum_without<T>(row, a.target_scale, p.m, u0, u1, (int)y, lane);
+          const float exact = token_logp<T>(row, a.target_scale, p.m, rest, (int)y);
+          if (lane == 0) {
+            a.tokens[r] = y;
+            a.logp[r] = exact;
+          }
+        }
       }
-      __syncthreads();
     }
-    const RowSum* totals = a.cluster > 1 ? sh.total[parity] : sh.slice[parity];
-    at = rows - 1;
-    // every warp of every CTA decides alike
-    bool ok = true;
-    if (lane >= off && lane < off + rows && pos0 + lane < n) {
-      const RowSum p = totals[lane - off];
-      const Scale& c = a.target_scale;
-      const float d = zy - p.m;
-      const float logp = __fmaf_rn(d, c.inv_hi, d * c.inv_lo) - logf((float)p.s);
-      bool fine = usable(p) && y >= 0;
-      float lq = logq;
-      if (both) {
-        const RowSum q = totals[kMaxRound + lane - off];
-        const float e = logq - q.m;
-        lq = __fmaf_rn(e, a.draft_scale.inv_hi, e * a.draft_scale.inv_lo) - logf((float)q.s);
-        fine = fine && usable(q);
-      }
-      ok = fine && u < expf(logp - lq);
-    }
-    const unsigned bad = __ballot_sync(0xFFFFFFFFu, !ok) >> off;
-    refused = bad != 0;
-    if (refused) at = __ffs(bad) - 1;
-    // rows of this round whose drafts were taken; their log p comes later, when it delays no row
-    const int good = (int)min(refused ? (int64_t)at : (int64_t)rows, n - base);
-    if (warp == 0 && lane < good) {
-      sh.taken_m[(base + lane) % kMaxTaken] = totals[lane].m;
-      sh.taken_rest[(base + lane) % kMaxTaken] = totals[lane].rest;
-    }
-    taken = base + good;
-    if (refused || base + rows == n + 1) break;
-    if (taken - emitted + a.round > kMaxTaken) {
-      __syncthreads();
-      emit(emitted, taken, 0);
-      emitted = taken;
-      __syncthreads();
-    }
+    __syncthreads();  // the tables are free
   }
+  if (a.cluster > 1) cluster_sync();  // no CTA leaves while another may read its sums
+}
 
-  // the token after the drafts that were taken, from row `taken`
-  const RowUnits<T> row(a.target, row0 + taken, a.target_stride, a.vocab);
-  const RowSum* totals = a.cluster > 1 ? sh.total[parity] : sh.slice[parity];
-  const RowSum p = totals[at];
-  const StripSum* own = table + at * a.strips;
+// The token after a sequence's taken drafts, and -1 behind it.
+template <typename T>
+__global__ void __launch_bounds__(kSampleWarps * 32, 3) finish_kernel(const __grid_constant__ SampleArgs a) {
+  constexpr int N = Vec<T>::N;
+  extern __shared__ StripSum tables[];  // [2][strips]: of p; of q, then of the difference
+  __shared__ RowSum slice;
+  __shared__ double share;              // this CTA's part of the weights
+  __shared__ DrawSpace space;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int rank = a.cluster > 1 ? (int)cluster_ctarank() : 0;
+  const int64_t seq = blockIdx.x / a.cluster;
+  const Sequence e = sequence_of(a, seq);
+  const int strip0 = rank * a.strips;
+  const int per_warp = (a.strips + warps - 1) / warps, mine0 = min(warp * per_warp, a.strips), mine1 = min(mine0 + per_warp, a.strips);
   const Scale& c = a.target_scale;
+  griddep_wait();
+  const unsigned long long first_refused = __ldcg(reinterpret_cast<unsigned long long*>(a.counts) + seq);
+  const bool refused = first_refused < (unsigned long long)e.n;
+  const int64_t taken = refused ? (int64_t)first_refused : e.n, r = e.row0 + taken, d = e.lo + taken;
+  const RowUnits<T> row(a.target, r, a.target_stride, a.vocab);
+  // the row's sums, by every warp alike, and this CTA's strips of them
+  const StripSum* const all = a.sums + r * a.all_strips;
+  const RowSum p = sum_table(all, a.all_strips, c, -1, lane);
+  StripSum* const own = tables;
+  StripSum* const left = tables + a.strips;
+  for (int k = threadIdx.x; k < a.strips; k += blockDim.x)
+    own[k] = strip0 + k < a.all_strips ? all[strip0 + k] : StripSum{-INFINITY, 0.f};
   bool fine = usable(p);
   int kind = kPlain;
   int64_t without = -1;
-  Refused f{};
-  const T* zq = nullptr;
-  StripSum* left = table + set + at * a.strips;  // of the draft model's row, then of the difference
   int without_strip = -1;
   float without_sum = 0.f;
-  if (refused && fine) {
-    const int64_t d = lo + taken;
-    if (a.draft == nullptr) {
-      kind = kWithout;
-      without = a.drafts[d];
-      if (without >= 0 && without < a.vocab) {
-        const int k = strip_of(row, without);
-        if (k >= 0 && k < a.strips) {  // every warp sums the strip alike
-          int u0, u1;
-          units_of(row, k, u0, u1);
-          const float s = sum_without<T>(row, c, p.m, u0, u1, (int)without, lane);
-          without_strip = k;
-          without_sum = warp_sum(s);
-        }
-      }
-    } else {
-      kind = kLeft;
-      const RowUnits<T> draft(a.draft, d, a.draft_stride, a.vocab);
-      zq = draft.z;
-      RowSum q;
-      if (both) {
-        q = totals[kMaxRound + at];
-      } else {
-        sum_strips<T>(draft, a.draft_scale, a.strip_units, strip0 + mine0, strip0 + mine1, left + mine0, lane);
-        __syncthreads();
-        if (warp == 0) {
-          const RowSum t = slice_sum(left, a.draft_scale, -1);
-          if (lane == 0) sh.slice[parity][kMaxRound] = t;
-        }
-        exchange();
-        q = merge(&sh.slice[parity][kMaxRound], a.draft_scale);
-      }
-      fine = usable(q);
-      f = Refused{p.m, (float)(1. / p.s), q.m, (float)(1. / q.s)};
-      if (fine) {
-        for (int k = warp; k < a.strips; k += warps) {
-          int u0, u1;
-          units_of(row, k, u0, u1);
-          float s = 0.f;
-          for (int u = u0; u < u1; u += kStripStep) {
-            float r[kLoads * N];
-            left_over<T>(a, f, row, zq, u + lane, 32, u1, step_inside<T>(row, u, u1), r);
-#pragma unroll
-            for (int i = 0; i < kLoads * N; ++i) s += r[i];
-          }
-          s = warp_sum(s);
-          if (lane == 0) left[k] = StripSum{0.f, s};
-        }
-        __syncthreads();
+  Refused f{};
+  const T* zq = nullptr;
+  if (refused && fine && a.draft == nullptr) {
+    kind = kWithout;
+    without = a.drafts[d];
+    if (without >= 0 && without < a.vocab) {
+      const int k = ((int)without + row.shift) / N / a.strip_units;
+      if (warp == 0 && k >= strip0 && k < strip0 + a.strips) {
+        int u0, u1;
+        units_of(a, row, k, u0, u1);
+        without_strip = k - strip0;
+        without_sum = warp_sum(sum_without<T>(row, c, p.m, u0, u1, (int)without, lane));
       }
     }
+  } else if (refused && fine) {
+    kind = kLeft;
+    const RowUnits<T> draft(a.draft, d, a.draft_stride, a.vocab);
+    zq = draft.z;
+    RowSum q;
+    if (a.draft_logp == nullptr) {
+      q = sum_table(a.q_sums + d * a.all_strips, a.all_strips, a.draft_scale, -1, lane);
+    } else {
+      sum_strips<T>(draft, a.draft_scale, a.strip_units, strip0 + mine0, strip0 + mine1, left + mine0, lane);
+      __syncthreads();
+      if (warp == 0) {
+        const RowSum t = sum_table(left, a.strips, a.draft_scale, -1, lane);
+        if (lane == 0) slice = t;
+      }
+      if (a.cluster > 1) cluster_sync();
+      else __syncthreads();
+      q = merge(&slice, a.draft_scale, a.cluster, rank, lane);
+    }
+    fine = usable(q);
+    f = Refused{p.m, (float)(1. / p.s), q.m, (float)(1. / q.s)};
+    for (int k = mine0; fine && k < mine1; ++k) {
+      int u0, u1;
+      units_of(a, row, strip0 + k, u0, u1);
+      float s = 0.f;
+      for (int u = u0; u < u1; u += kStripStep) {
+        float x[kLoads * N];
+        left_over<T>(a, f, row, zq, u + lane, 32, u1, step_inside<T>(row, u, u1), x);
+#pragma unroll
+        for (int i = 0; i < kLoads * N; ++i) s += x[i];
+      }
+      s = warp_sum(s);
+      if (lane == 0) left[k] = StripSum{0.f, s};
+    }
   }
-
-  // the first warp draws the token, the others (or it alone) write the taken drafts
   __syncthreads();
-  if (warp != 0 || warps == 1) emit(emitted, taken, warps == 1 ? 0 : 1);
+  if (rank == 0 && (warp == 1 || warps == 1)) {
+    for (int64_t i = taken + 1 + lane; i <= e.n; i += 32) {
+      a.tokens[e.row0 + i] = -1;
+      a.logp[e.row0 + i] = 0.f;
+    }
+  }
   if (warp != 0) return;  // the cluster's barriers wait for the warps that are left
 
   int64_t token = -1;
@@ -770,25 +742,23 @@ __global__ void __launch_bounds__(kSampleWarps * 32, 3) verify_kernel(const __gr
     auto plain = [&](int k) { return own[k].s * factor(c, own[k].m, p.m); };
     auto weight = [&](int k) { return kind == kLeft ? left[k].s : kind == kWithout && k == without_strip ? without_sum : plain(k); };
     // each CTA's share of the weights in its lane, and their running sum
-    double v = 0.;
-    if (kind != kPlain) {
+    double v;
+    for (;;) {
+      float w = 0.f;
 #pragma unroll 1
-      for (int k = lane; k < a.strips; k += 32) v += (double)weight(k);
-      v = warp_sum64(v);
+      for (int k = lane; k < a.strips; k += 32) w += weight(k);
+      v = warp_sum64((double)w);
       if (a.cluster > 1) {
-        if (lane == 0) sh.weights = v;
+        if (lane == 0) share = v;
         cluster_sync();
-        v = lane >= a.cluster ? 0. : lane == rank ? v : load_peer(&sh.weights, lane);
+        v = lane >= a.cluster ? 0. : lane == rank ? v : load_peer(&share, lane);
+        cluster_sync();  // share is free
       } else if (lane > 0) {
         v = 0.;
       }
       // nothing is left over where the two models agree, and the refusal was one of rounding
-      if (!__any_sync(0xFFFFFFFFu, v > 0.)) kind = kPlain;
-    }
-    if (kind == kPlain) {
-      RowSum r{0., -INFINITY, 0.};
-      if (lane < a.cluster) r = load_peer(&sh.slice[parity][at], lane, rank);
-      v = r.s * (double)factor(c, r.m, p.m);
+      if (kind == kPlain || __any_sync(0xFFFFFFFFu, v > 0.)) break;
+      kind = kPlain;
     }
     const double upto = warp_scan64(v, lane), sum = __shfl_sync(0xFFFFFFFFu, upto, 31);
     const float su = fmaxf(a.sample_u[seq], 0.f);
@@ -801,28 +771,25 @@ __global__ void __launch_bounds__(kSampleWarps * 32, 3) verify_kernel(const __gr
       double before = __shfl_sync(0xFFFFFFFFu, upto - v, owner);
       const int strip = find_strip(a.strips, t, &before, lane, weight);
       int u0, u1;
-      units_of(row, strip, u0, u1);
+      units_of(a, row, strip0 + strip, u0, u1);
       float rest;
-      const int found = find_element<T>(a, sh.draw, row, u0, u1, t - before, kind, (int)without, zq, f, p.m, &rest, lane);
-      const double others = (double)rest + other_strips(own, &sh.slice[parity][at], strip, p.m, c);
+      const int found = find_element<T>(a, space, row, u0, u1, t - before, kind, (int)without, zq, f, p.m, &rest, lane);
+      float others = 0.f;
+#pragma unroll 4
+      for (int k = lane; k < a.all_strips; k += 32)
+        if (k != strip0 + strip) others += all[k].s * factor(c, all[k].m, p.m);
       if (found >= 0) {
         token = found;
-        lp = token_logp<T>(row, c, p.m, others, found);
+        lp = token_logp<T>(row, c, p.m, (double)rest + (double)others, found);
       }
     }
   }
   if (mine && lane == 0) {
-    a.tokens[row0 + taken] = token;
-    a.logp[row0 + taken] = lp;
+    a.tokens[r] = token;
+    a.logp[r] = lp;
   }
-  if (rank == 0) {
-    if (lane == 0) a.counts[seq] = taken;
-    for (int64_t r = taken + 1 + lane; r <= n; r += 32) {
-      a.tokens[row0 + r] = -1;
-      a.logp[row0 + r] = 0.f;
-    }
-  }
-  if (a.cluster > 1) cluster_sync();  // no CTA leaves while another may read its sums
+  if (a.cluster > 1) cluster_sync();  // every CTA has read counts, and no CTA leaves before
+  if (rank == 0 && lane == 0) a.counts[seq] = taken;
 }
 
 // ---------------------------------------------------------------------------
@@ -871,23 +838,29 @@ cudaError_t run_rows(SampleArgs& a, int sms, cudaStream_t s) {
   return launch(draw_kernel<T>, (int)((a.n_seqs + drawers - 1) / drawers), (int)(32 * drawers), 0, s, 1, true, a);
 }
 
-// Verification: CTAs a sequence, rows side by side.
+// CTAs a row: as many as keep every SM busy with three, and have two strips each.
+int cluster_of(int64_t units, int64_t strips, int sms) {
+  int cluster = 1;
+  while (cluster < kMaxCluster && units * cluster * 2 <= 3 * sms && strips > 2 * cluster) cluster *= 2;
+  return cluster;
+}
+
+cudaError_t launch_verify(void (*kernel)(SampleArgs), SampleArgs a, int64_t units, int sms, bool dependent, cudaStream_t s) {
+  a.cluster = cluster_of(units, a.all_strips, sms);
+  a.strips = (a.all_strips + a.cluster - 1) / a.cluster;
+  const int warps = a.strips < kSampleWarps ? a.strips : kSampleWarps;
+  return launch(kernel, (int)(units * a.cluster), 32 * warps, (size_t)2 * a.strips * sizeof(StripSum), s, a.cluster, dependent, a);
+}
+
 template <typename T>
 cudaError_t run_verify(SampleArgs& a, int sms, cudaStream_t s) {
-  const int64_t whole = a.strips;
-  int64_t cluster = 1;
-  while (cluster < kMaxCluster && a.n_seqs * cluster * 2 <= 3 * sms && whole > 2 * cluster) cluster *= 2;
-  const int64_t most = (a.n_drafts + 2 * a.n_seqs - 1) / a.n_seqs;  // rows of a sequence, in the mean
-  a.cluster = (int32_t)cluster;
-  a.strips = (int32_t)((whole + cluster - 1) / cluster);
-  a.round = 1;
-  if (a.n_seqs * cluster <= sms) {
-    const int64_t room = kMaxStrips / a.strips, want = most < kMaxRound ? most : kMaxRound;
-    a.round = (int32_t)(want < room ? want : room);
-  }
-  const size_t smem = (size_t)4 * a.round * a.strips * sizeof(StripSum);
-  const int warps = a.strips < kSampleWarps ? a.strips : kSampleWarps;
-  return launch(verify_kernel<T>, (int)(a.n_seqs * cluster), 32 * warps, smem, s, (int)cluster, false, a);
+  cudaError_t e = cudaMemsetAsync(a.counts, 0xFF, (size_t)a.n_seqs * sizeof(int64_t), s);
+  if (e != cudaSuccess) return e;
+  // the mean number of rows, rounded up; longer sequences' CTAs take several
+  const int64_t positions = (a.n_drafts + a.n_seqs - 1) / a.n_seqs + 1, most = 0x7FFFFFFF / kMaxCluster / a.n_seqs;
+  a.positions = (int32_t)(positions < most ? positions : most < 1 ? 1 : most);
+  e = launch_verify(judge_kernel<T>, a, a.n_seqs * a.positions, sms, false, s);
+  return e == cudaSuccess ? launch_verify(finish_kernel<T>, a, a.n_seqs, sms, true, s) : e;
 }
 
 }  // namespace
@@ -897,14 +870,14 @@ using namespace muon;
 
 extern "C" {
 
-muon_status muon_sample_workspace_bytes(int64_t tokens, int64_t vocab, int32_t dtype, size_t* bytes) {
+muon_status muon_sample_workspace_bytes(int64_t rows, int64_t vocab, int32_t dtype, size_t* bytes) {
   if (!bytes) return invalid("bytes is NULL");
-  if (tokens < 0 || tokens > (1ll << 31) - 1) return invalid("tokens must be in [0, 2^31)");
+  if (rows < 0 || rows > (1ll << 32) - 1) return invalid("rows must be in [0, 2^32)");
   if (vocab < 1 || vocab > (1ll << 30)) return invalid("vocab must be in [1, 2^30]");
   if (dtype != MUON_DTYPE_F32 && dtype != MUON_DTYPE_BF16) return invalid("unknown logits dtype");
   int32_t units, strips;
   strips_of(vocab, dtype, &units, &strips);
-  *bytes = (size_t)tokens * strips * sizeof(StripSum);
+  *bytes = (size_t)rows * strips * sizeof(StripSum);
   return MUON_OK;
 }
 
@@ -941,7 +914,7 @@ muon_status muon_sample_tokens(const muon_token_batch* batch, const float* unifo
 muon_status muon_verify_drafts(const muon_token_batch* target, const muon_token_batch* draft, const float* draft_logp,
                                const int64_t* draft_offsets, int64_t n_seqs, const float* accept_uniforms,
                                const float* sample_uniforms, int64_t* tokens, int64_t* counts, float* logp,
-                               void* stream) {
+                               void* workspace, size_t workspace_bytes, void* stream) {
   if (!target || !draft) return invalid("target or draft is NULL");
   int32_t st = check_rows(target);
   if (st == MUON_OK) st = check_rows(draft);
@@ -978,7 +951,12 @@ muon_status muon_verify_drafts(const muon_token_batch* target, const muon_token_
   a.draft_scale = scale_of(draft->temperature);
   a.vocab = (int32_t)target->vocab;
   a.n_seqs = n_seqs;
-  strips_of(a.vocab, target->dtype, &a.strip_units, &a.strips);
+  strips_of(a.vocab, target->dtype, &a.strip_units, &a.all_strips);
+  const size_t row = (size_t)a.all_strips * sizeof(StripSum), rows = (size_t)(a.n_drafts + n_seqs);
+  const bool both = draft->logits && !draft_logp;
+  if ((st = check_workspace(workspace, workspace_bytes, (rows + (both ? (size_t)a.n_drafts : 0)) * row)) != MUON_OK) return st;
+  a.sums = static_cast<StripSum*>(workspace);
+  a.q_sums = both ? a.sums + rows * a.all_strips : nullptr;
   int sms;
   if ((st = find_device(&sms)) != MUON_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

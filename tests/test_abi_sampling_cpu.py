@@ -45,11 +45,11 @@ def test_sample_refuses_bad_arguments(nsm):
 
 
 def _verify(nsm, target=None, draft=None, n_seqs=2, draft_logp=None, offsets=A, accept=A, sample=A, tokens=A, counts=A,
-            logp=A):
+            logp=A, ws=A, nbytes=1 << 40):
     t = _batch(nsm, **{"targets": None, **(target or {})})
     d = _batch(nsm, **{"tokens": 4, **(draft or {})})
     return nsm.lib.muon_verify_drafts(ctypes.byref(t), ctypes.byref(d), draft_logp, offsets, n_seqs, accept, sample,
-                                      tokens, counts, logp, None)
+                                      tokens, counts, logp, ws, nbytes, None)
 
 
 @pytest.mark.parametrize("over", [
@@ -65,7 +65,7 @@ def test_verify_refuses(nsm, over):
 
 
 def test_verify_of_nothing(nsm):
-    assert nsm.lib.muon_verify_drafts(None, None, None, None, 0, None, None, None, None, None, None) == nsm.MUON_ERR_INVALID
+    assert nsm.lib.muon_verify_drafts(None, None, None, None, 0, None, None, None, None, None, None, 0, None) == nsm.MUON_ERR_INVALID
     assert _verify(nsm, dict(tokens=0, logits=None), dict(tokens=0, logits=None), 0, None, None, None, None, None, None,
                    None) == nsm.MUON_OK
 
@@ -76,12 +76,16 @@ def test_workspace(nsm):
     assert need(0, 5, torch.float32) == 0
     assert need(10, 1000, torch.float32) == 10 * 2 * 8                  # two strips of 512 a row
     assert need(1 << 20, 1 << 30, torch.bfloat16) == (1 << 20) * 512 * 8   # 512 strips at most
-    for bad in ((-1, 5), (1 << 31, 5), (5, 0), (5, (1 << 30) + 1)):
+    for bad in ((-1, 5), (1 << 32, 5), (5, 0), (5, (1 << 30) + 1)):
         with pytest.raises(nsm.MuonError) as e:
             need(*bad, torch.float32)
         assert e.value.status == nsm.MUON_ERR_INVALID
     with pytest.raises(TypeError):
         need(5, 5, torch.float16)
+    assert _verify(nsm, ws=None) == nsm.MUON_ERR_NO_WORKSPACE
+    assert _verify(nsm, nbytes=6 * 8) == nsm.MUON_ERR_NO_WORKSPACE     # the draft model's rows too
+    assert _verify(nsm, draft_logp=A, nbytes=5 * 8) == nsm.MUON_ERR_NO_WORKSPACE
+    assert _verify(nsm, ws=A + 8) == nsm.MUON_ERR_INVALID
 
 
 def test_binding_refuses_host_tensors(nsm):
