@@ -142,19 +142,19 @@ __device__ __forceinline__ uint4 load_elems(const T* z, int32_t vocab, int e) {
   return Vec<T>::pack(v);
 }
 
-// Units first, first + stride, ... of a row, kLoads of them, -inf from unit u1 on.  inside: they
+// Units first, first + stride, ... of a row, L of them, -inf from unit u1 on.  inside: they
 // all hold elements of the row only.
-template <typename T>
+template <typename T, int L>
 __device__ __forceinline__ void load_units(const RowUnits<T>& row, int first, int stride, int u1, bool inside,
-                                           uint4 (&w)[kLoads]) {
+                                           uint4 (&w)[L]) {
   constexpr uint32_t low = Vec<T>::kLowest;
   if (inside) {
     const uint4* p = reinterpret_cast<const uint4*>(row.z - row.shift) + first;
 #pragma unroll
-    for (int k = 0; k < kLoads; ++k) w[k] = __ldg(p + k * stride);
+    for (int k = 0; k < L; ++k) w[k] = __ldg(p + k * stride);
   } else {
 #pragma unroll
-    for (int k = 0; k < kLoads; ++k) {
+    for (int k = 0; k < L; ++k) {
       const int u = first + k * stride;
       w[k] = u < u1 ? load_elems<T>(row.z, row.vocab, row.first(u)) : make_uint4(low, low, low, low);
     }
@@ -234,27 +234,68 @@ struct Refused {
   float mp, ip, mq, iq;  // frames, and reciprocals of the sums
 };
 
-// max(p - q, 0) of the units first, first + stride, ... of the target's row, 0 from u1 on; each
-// product rounded, so that equal rows leave 0.
-template <typename T>
-__device__ __forceinline__ void left_over(const SampleArgs& a, const Refused& f, const RowUnits<T>& p, const T* zq,
-                                          int first, int stride, int u1, bool inside, float (&r)[kLoads * Vec<T>::N]) {
-  constexpr int N = Vec<T>::N;
-  constexpr uint32_t low = Vec<T>::kLowest;
-  uint4 wp[kLoads], wq[kLoads];
-  load_units<T>(p, first, stride, u1, inside, wp);
+// Units of the target's row and the draft model's elements at the same places.
+template <typename T, int L>
+struct UnitPair {
+  uint4 p[L], q[L];
+  __device__ __forceinline__ void load(const RowUnits<T>& row, const T* zq, int first, int stride, int u1, bool inside) {
+    constexpr uint32_t low = Vec<T>::kLowest;
+    load_units<T>(row, first, stride, u1, inside, p);
+    if (inside && ((reinterpret_cast<uint64_t>(row.z) ^ reinterpret_cast<uint64_t>(zq)) & 15) == 0) {
+      const uint4* at = reinterpret_cast<const uint4*>(zq - row.shift) + first;
 #pragma unroll
-  for (int k = 0; k < kLoads; ++k) {
-    const int u = first + k * stride;
-    wq[k] = u < u1 ? load_elems<T>(zq, p.vocab, p.first(u)) : make_uint4(low, low, low, low);
+      for (int k = 0; k < L; ++k) q[k] = __ldg(at + k * stride);
+    } else {
+#pragma unroll
+      for (int k = 0; k < L; ++k) {
+        const int u = first + k * stride;
+        q[k] = u < u1 ? load_elems<T>(zq, row.vocab, row.first(u)) : make_uint4(low, low, low, low);
+      }
+    }
   }
+  // max(p - q, 0) of unit k; each product rounded, so that equal rows leave 0.
+  __device__ __forceinline__ void left_over(const SampleArgs& a, const Refused& f, int k, float (&r)[Vec<T>::N]) const {
+    float y[Vec<T>::N];
+    exps<T>(a.target_scale, f.mp, p[k], r);
+    exps<T>(a.draft_scale, f.mq, q[k], y);
 #pragma unroll
-  for (int k = 0; k < kLoads; ++k) {
-    float x[N], y[N];
-    exps<T>(a.target_scale, f.mp, wp[k], x);
-    exps<T>(a.draft_scale, f.mq, wq[k], y);
+    for (int i = 0; i < Vec<T>::N; ++i) r[i] = fmaxf(__fmul_rn(r[i], f.ip) - __fmul_rn(y[i], f.iq), 0.f);
+  }
+};
+
+// The sums of max(p - q, 0) over the strips [k0, k1), into `to`; half a step at a time, the
+// next half's loads under way.
+template <typename T>
+__device__ __forceinline__ void sum_left(const SampleArgs& a, const Refused& f, const RowUnits<T>& row, const T* zq, int k0,
+                                         int k1, StripSum* to, int lane) {
+  constexpr int L = kLoads / 2, kHalf = 32 * L;
+  const int end = (int)min((int64_t)k1 * a.strip_units, (int64_t)row.units);
+  int u = (int)min((int64_t)k0 * a.strip_units, (int64_t)row.units);
+  auto inside = [&](int at) { return at + kHalf <= end && row.first(at) >= 0 && row.first(at + kHalf) <= row.vocab; };
+  UnitPair<T, L> now;
+  now.load(row, zq, u + lane, 32, end, inside(u));
+  float sum = 0.f;
+  int left = a.strip_units;
+  for (int k = k0; k < k1;) {
+    UnitPair<T, L> next;
+    next.load(row, zq, u + kHalf + lane, 32, end, inside(u + kHalf));
 #pragma unroll
-    for (int i = 0; i < N; ++i) r[k * N + i] = fmaxf(__fmul_rn(x[i], f.ip) - __fmul_rn(y[i], f.iq), 0.f);
+    for (int i = 0; i < L; ++i) {
+      float r[Vec<T>::N];
+      now.left_over(a, f, i, r);
+#pragma unroll
+      for (int j = 0; j < Vec<T>::N; ++j) sum += r[j];
+    }
+    left -= kHalf;
+    if (left == 0) {
+      sum = warp_sum(sum);
+      if (lane == 0) to[k - k0] = StripSum{0.f, sum};
+      sum = 0.f;
+      left = a.strip_units;
+      ++k;
+    }
+    u += kHalf;
+    now = next;
   }
 }
 
@@ -356,12 +397,17 @@ __device__ __forceinline__ int find_element(const SampleArgs& a, DrawSpace& sh, 
     const bool inside = step_inside<T>(row, at, u1);
     float v = 0.f;
     if (kind == kLeft) {
-      float x[kLoads * N];
-      left_over<T>(a, f, row, zq, first, 1, u1, inside, x);
+      UnitPair<T, kLoads> z;
+      z.load(row, zq, first, 1, u1, inside);
 #pragma unroll
-      for (int i = 0; i < kLoads * N; ++i) {
-        sh.weight[lane][i] = x[i];
-        v += x[i];
+      for (int k = 0; k < kLoads; ++k) {
+        float x[N];
+        z.left_over(a, f, k, x);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          sh.weight[lane][k * N + i] = x[i];
+          v += x[i];
+        }
       }
     } else {
       uint4 z[kLoads];
@@ -426,7 +472,7 @@ __global__ void __launch_bounds__(kSampleWarps * 32, kSampleCtas) rows_kernel(co
 }
 
 // A warp draws a row's token.
-constexpr int kDrawWarps = 4;
+constexpr int kDrawWarps = 2;  // of a CTA: 2048 rows 112, 100 and 102 us with 4, 2 and 1
 template <typename T>
 __global__ void __launch_bounds__(kDrawWarps * 32) draw_kernel(const __grid_constant__ SampleArgs a) {
   __shared__ DrawSpace space[kDrawWarps];
@@ -646,9 +692,13 @@ __global__ void __launch_bounds__(kSampleWarps * 32, 3) judge_kernel(const __gri
   if (a.cluster > 1) cluster_sync();  // no CTA leaves while another may read its sums
 }
 
-// The token after a sequence's taken drafts, and -1 behind it.
+// The token after a sequence's taken drafts, and -1 behind it.  Only some of the CTAs have a
+// refused draft's rows to read, so that a CTA alone has more warps (512 sequences of four
+// drafts in all: 180 us with 8 warps, 172 us with 12; clusters, whose barriers wait for more warps,
+// 47 and 53 us for 37 sequences).
+constexpr int kFinishWarps = 12;
 template <typename T>
-__global__ void __launch_bounds__(kSampleWarps * 32, 3) finish_kernel(const __grid_constant__ SampleArgs a) {
+__global__ void __launch_bounds__(kFinishWarps * 32, 2) finish_kernel(const __grid_constant__ SampleArgs a) {
   constexpr int N = Vec<T>::N;
   extern __shared__ StripSum tables[];  // [2][strips]: of p; of q, then of the difference
   __shared__ RowSum slice;
@@ -712,19 +762,7 @@ __global__ void __launch_bounds__(kSampleWarps * 32, 3) finish_kernel(const __gr
     }
     fine = usable(q);
     f = Refused{p.m, (float)(1. / p.s), q.m, (float)(1. / q.s)};
-    for (int k = mine0; fine && k < mine1; ++k) {
-      int u0, u1;
-      units_of(a, row, strip0 + k, u0, u1);
-      float s = 0.f;
-      for (int u = u0; u < u1; u += kStripStep) {
-        float x[kLoads * N];
-        left_over<T>(a, f, row, zq, u + lane, 32, u1, step_inside<T>(row, u, u1), x);
-#pragma unroll
-        for (int i = 0; i < kLoads * N; ++i) s += x[i];
-      }
-      s = warp_sum(s);
-      if (lane == 0) left[k] = StripSum{0.f, s};
-    }
+    if (fine) sum_left<T>(a, f, row, zq, strip0 + mine0, strip0 + mine1, left + mine0, lane);
   }
   __syncthreads();
   if (rank == 0 && (warp == 1 || warps == 1)) {
@@ -845,10 +883,11 @@ int cluster_of(int64_t units, int64_t strips, int sms) {
   return cluster;
 }
 
-cudaError_t launch_verify(void (*kernel)(SampleArgs), SampleArgs a, int64_t units, int sms, bool dependent, cudaStream_t s) {
+cudaError_t launch_verify(void (*kernel)(SampleArgs), SampleArgs a, int64_t units, int sms, int alone, bool dependent,
+                          cudaStream_t s) {
   a.cluster = cluster_of(units, a.all_strips, sms);
   a.strips = (a.all_strips + a.cluster - 1) / a.cluster;
-  const int warps = a.strips < kSampleWarps ? a.strips : kSampleWarps;
+  const int most = a.cluster == 1 ? alone : kSampleWarps, warps = a.strips < most ? a.strips : most;
   return launch(kernel, (int)(units * a.cluster), 32 * warps, (size_t)2 * a.strips * sizeof(StripSum), s, a.cluster, dependent, a);
 }
 
@@ -859,8 +898,8 @@ cudaError_t run_verify(SampleArgs& a, int sms, cudaStream_t s) {
   // the mean number of rows, rounded up; longer sequences' CTAs take several
   const int64_t positions = (a.n_drafts + a.n_seqs - 1) / a.n_seqs + 1, most = 0x7FFFFFFF / kMaxCluster / a.n_seqs;
   a.positions = (int32_t)(positions < most ? positions : most < 1 ? 1 : most);
-  e = launch_verify(judge_kernel<T>, a, a.n_seqs * a.positions, sms, false, s);
-  return e == cudaSuccess ? launch_verify(finish_kernel<T>, a, a.n_seqs, sms, true, s) : e;
+  e = launch_verify(judge_kernel<T>, a, a.n_seqs * a.positions, sms, kSampleWarps, false, s);
+  return e == cudaSuccess ? launch_verify(finish_kernel<T>, a, a.n_seqs, sms, kFinishWarps, true, s) : e;
 }
 
 }  // namespace
