@@ -9,7 +9,13 @@ Each step: logits by torch, the loss and its gradient by muon_policy_loss or
 muon_preference_loss (in place of the logits), the weights' gradients by torch, their
 clipping by muon_clip_grad_norm, and muon_step.
 
-  python examples/finetune_step.py [policy|preference] [--steps N]
+With --drafts K the policy's tokens are drafted, K a sequence, by the initial model
+(muon_sample_tokens) and verified by the one that is trained (muon_verify_drafts).  With --gated
+the model is logits = (silu(x G^T) x U^T) W^T, its activations are kept in 8 bits until the
+backward pass (muon_swiglu_forward), and the weights' gradients come from there
+(muon_swiglu_backward, muon_checkpoint_weight_grad).
+
+  python examples/finetune_step.py [policy|preference] [--steps N] [--drafts K] [--gated]
 """
 from __future__ import annotations
 
@@ -28,8 +34,8 @@ class TokenModel:
 
     def __init__(self, inputs=128, hidden=512, vocab=2048, seed=0):
         gen = torch.Generator("cuda").manual_seed(seed)
-        self.weights = [torch.randn(hidden, inputs, generator=gen, device="cuda") * inputs ** -0.5,
-                        torch.randn(vocab, hidden, generator=gen, device="cuda") * hidden ** -0.5]
+        self.weights = [torch.randn(*shape, generator=gen, device="cuda") * shape[1] ** -0.5
+                        for shape in self.shapes(inputs, hidden, vocab)]
         self.momentum = [torch.zeros_like(w) for w in self.weights]
         config = nsm.muon_config_default(grad_dtype=nsm.MUON_DTYPE_F32)
         self.plan = nsm.muon_plan([tuple(w.shape) for w in self.weights], config=config)
@@ -39,25 +45,71 @@ class TokenModel:
         self.clipped = [torch.empty_like(w) for w in self.weights]
         self.grad_set = nsm.GradSet(self.grads, self.clipped)
 
+    @staticmethod
+    def shapes(inputs, hidden, vocab):
+        return [(hidden, inputs), (vocab, hidden)]
+
     def logits(self, x):
+        """The logits, and what the backward pass needs."""
         w1, w2 = (w.bfloat16() for w in self.weights)
         h = torch.relu(x @ w1.t())
         return h @ w2.t(), h
 
-    def step(self, x, h, dlogits, max_norm=1.0, lr=0.05, momentum=0.9):
-        """Backward from the logits' gradient, clip, update; returns the (norm, factor) tensor."""
+    def backward(self, x, h, dlogits):
+        """The weights' gradients from the logits'."""
         torch.matmul(dlogits.t(), h, out=self.grads[1])
         dh = (dlogits @ self.weights[1].bfloat16()) * (h > 0)
         torch.matmul(dh.t(), x, out=self.grads[0])
+
+    def step(self, x, h, dlogits, max_norm=1.0, lr=0.05, momentum=0.9):
+        """Backward from the logits' gradient, clip, update; returns the (norm, factor) tensor."""
+        self.backward(x, h, dlogits)
         norm = nsm.muon_clip_grad_norm(self.grad_set, max_norm)
         nsm.muon_step(self.plan, self.weights, self.clipped, self.momentum, lr, momentum, True, 0.0)
         return norm
 
 
-def train_policy(steps=30, tokens=1024, sequences=32, updates=2, seed=0):
+class GatedModel(TokenModel):
+    """The same with a gated activation, kept in 8 bits between the passes."""
+
+    @staticmethod
+    def shapes(inputs, hidden, vocab):
+        return [(hidden, inputs), (hidden, inputs), (vocab, hidden)]
+
+    def logits(self, x):
+        gate, up, out = (w.bfloat16() for w in self.weights)
+        h, *saved = nsm.muon_swiglu_forward(x @ gate.t(), x @ up.t())
+        return h @ out.t(), [nsm.muon_checkpoint_save(x), *saved]
+
+    def backward(self, x, saved, dlogits):
+        saved_x, gate, up = saved
+        dh = dlogits @ self.weights[2].bfloat16()
+        dgate, dup, h = nsm.muon_swiglu_backward(dh, gate, up, with_h=True)
+        nsm.muon_checkpoint_weight_grad(saved_x, dgate, out=self.grads[0])
+        nsm.muon_checkpoint_weight_grad(saved_x, dup, out=self.grads[1])
+        torch.matmul(dlogits.t(), h, out=self.grads[2])
+
+
+def drafted_rollout(logits, reference_logits, drafts, gen):
+    """Tokens of sequences of drafts + 1 rows: the first ones drafted from the reference's logits
+    and verified by the others, one more drawn, -1 behind it.  Returns (tokens, their
+    log-probabilities under the verifying model)."""
+    sequences = logits.shape[0] // (drafts + 1)
+    rows = torch.arange(sequences * (drafts + 1), device="cuda").view(sequences, drafts + 1)[:, :drafts].reshape(-1)
+    draft_logits = reference_logits[rows]
+    uniforms = torch.rand(3, len(rows), generator=gen, device="cuda")
+    drafted, draft_logp = nsm.muon_sample_tokens(draft_logits, uniforms[0])
+    starts = torch.arange(0, len(rows) + 1, drafts, device="cuda")
+    tokens, _, logp = nsm.muon_verify_drafts(logits, drafted, starts, uniforms[1], uniforms[2, :sequences],
+                                             draft_logits=draft_logits, draft_logp=draft_logp)
+    return tokens, logp
+
+
+def train_policy(steps=30, tokens=1024, sequences=32, updates=2, seed=0, drafts=0, model_type=TokenModel):
     """Returns the share of rewarded tokens at each step (1/2 for an untrained model)."""
     gen = torch.Generator("cuda").manual_seed(seed + 1)
-    model = TokenModel(seed=seed)
+    tokens -= tokens % (drafts + 1)
+    model = model_type(seed=seed)
     reference = [w.clone() for w in model.weights]
     offsets = torch.linspace(0, tokens, sequences + 1, device="cuda").long()
     config = nsm.muon_policy_config_default(kl_beta=0.02, clip_high=0.28, reduction=nsm.MUON_REDUCE_SEQUENCE_MEAN)
@@ -66,18 +118,23 @@ def train_policy(steps=30, tokens=1024, sequences=32, updates=2, seed=0):
         x = torch.randn(tokens, 128, generator=gen, device="cuda").bfloat16()
         # rollout: the sampled tokens' log-probabilities under this policy and the initial one
         logits, _ = model.logits(x)
-        sampled = torch.multinomial(logits.float().softmax(1), 1, generator=gen)[:, 0]
-        old = nsm.muon_token_logprobs(logits, sampled)
         now, model.weights = model.weights, reference
-        ref = nsm.muon_token_logprobs(model.logits(x)[0], sampled)
+        ref_logits = model.logits(x)[0]
         model.weights = now
+        if drafts:
+            sampled, old = drafted_rollout(logits, ref_logits, drafts, gen)
+        else:
+            sampled = torch.multinomial(logits.float().softmax(1), 1, generator=gen)[:, 0]
+            old = nsm.muon_token_logprobs(logits, sampled)
+        drawn = sampled >= 0
+        ref = nsm.muon_token_logprobs(ref_logits, sampled, mask=drawn)
         reward = (sampled % 2 == 0).float()
-        rewarded.append(reward.mean().item())
-        advantage = (reward - reward.mean()) / reward.std().clamp(min=1e-3)
+        rewarded.append(reward[drawn].mean().item())
+        advantage = (reward - reward[drawn].mean()) / reward[drawn].std().clamp(min=1e-3)
         prompt = torch.rand(tokens, generator=gen, device="cuda") < 0.1   # positions that take no part
         for _ in range(updates):
             logits, h = model.logits(x)
-            _, _, dlogits = nsm.muon_policy_loss(logits, sampled, old, advantage, mask=~prompt, ref_logp=ref,
+            _, _, dlogits = nsm.muon_policy_loss(logits, sampled, old, advantage, mask=~prompt & drawn, ref_logp=ref,
                                                  seq_offsets=offsets, config=config, grad=logits)
             model.step(x, h, dlogits)
         status, nonfinite = nsm.muon_sync(model.plan)
@@ -85,10 +142,10 @@ def train_policy(steps=30, tokens=1024, sequences=32, updates=2, seed=0):
     return rewarded
 
 
-def train_preference(steps=30, pairs=16, length=24, seed=0):
+def train_preference(steps=30, pairs=16, length=24, seed=0, model_type=TokenModel):
     """Returns the mean margin at each step (0 for an untrained model)."""
     gen = torch.Generator("cuda").manual_seed(seed + 2)
-    model = TokenModel(seed=seed)
+    model = model_type(seed=seed)
     tokens = 2 * pairs * length
     x = torch.randn(tokens, 128, generator=gen, device="cuda").bfloat16()
     answers = torch.randint(0, 2048, (tokens,), generator=gen, device="cuda")
@@ -114,10 +171,15 @@ def main():
     parser = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     parser.add_argument("loss", nargs="?", default="policy", choices=["policy", "preference"])
     parser.add_argument("--steps", type=int, default=30)
+    parser.add_argument("--drafts", type=int, default=0, help="policy: drafted tokens a sequence")
+    parser.add_argument("--gated", action="store_true", help="a gated model with activations in 8 bits")
     args = parser.parse_args()
     train, what = {"policy": (train_policy, "share of rewarded tokens"),
                    "preference": (train_preference, "mean margin")}[args.loss]
-    for step, value in enumerate(train(args.steps)):
+    options = {"model_type": GatedModel if args.gated else TokenModel}
+    if args.loss == "policy":
+        options["drafts"] = args.drafts
+    for step, value in enumerate(train(args.steps, **options)):
         print(f"step {step:3d}  {what} {value:.4f}")
 
 

@@ -386,8 +386,9 @@ muon_status muon_get_bucket_stats(const muon_plan_t* plan, int64_t b, muon_bucke
 muon_status muon_get_input_norms(const muon_plan_t* plan, float* out, int64_t n, void* stream);
 
 /* ---------------------------------------------------------------------------
- * Before the step: the loss whose gradient it takes, and the gradient's clipping.
- * These entry points have no counterpart on the pages (their only mention of a
+ * Around the step: tokens to train on (sampled, or drafted and verified), the loss whose
+ * gradient it takes, activations kept in 8 bits for the backward pass, the weight gradient
+ * from them, and the gradient's clipping.  These entry points have no counterpart on the pages (their only mention of a
  * gradient norm is "Muon Optimizer + FSDP", section 内存控制方案 item 4, among the
  * scalars kept in fp32); the formulas are stated at each of them.  They take no plan, only
  * launch kernels on `stream` (capturable in a CUDA graph; the captured pointers
@@ -470,8 +471,9 @@ muon_status muon_sample_workspace_bytes(int64_t rows, int64_t vocab, int32_t dty
  *     be taken).
  *   tokens: [tokens]; logp: [tokens] fp32, log p of the token (device).
  * A row whose mask is 0 gets token -1 and logp 0 and its logits are not read; one without
- * probabilities (a logit of NaN or +inf, or none but -inf) token -1 and logp NaN.  Sums and
- * the search for the token are in 64 bits over terms of fp32. */
+ * probabilities (a logit of NaN or +inf, or none but -inf) token -1 and logp NaN.  Terms and
+ * partial sums are fp32 and the search over them is in 64 bits: a token's share of [0, 1) begins
+ * within about 1e-7 of where it should. */
 muon_status muon_sample_tokens(const muon_token_batch* batch, const float* uniforms, int64_t* tokens,
                                float* logp, void* workspace, size_t workspace_bytes, void* stream);
 

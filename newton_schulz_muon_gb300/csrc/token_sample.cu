@@ -15,18 +15,21 @@
 //
 // Sampling: the strips of all rows are dealt out to the warps of the whole chip alike, and a
 // second kernel draws the tokens, a warp a row.  (With a CTA a row 2048 rows of 131072 bf16
-// logits took 117 us: the ends of rows, and 3.03 rounds of CTAs that took 4.  ROWS_US so.)
+// logits took 117 us: the ends of rows, and 3.03 rounds of CTAs that took 4.  100 us so, a
+// tenth of them masked: 82 us of strips, 5.9 TB/s, and the draws.)
 //
 // Verification: a CTA a row (a cluster of them where there are few rows), position by position
 // over all sequences, judges the row's draft; rows of a sequence whose draft was refused before
 // are left out as far as that is known when their CTA starts, which changes no result.  A second
 // kernel, a CTA or cluster a sequence, draws the tokens.  (A CTA a sequence, row after row, took
-// 191 us for 512 sequences of four drafts: 456 sequences run at first and the others when the chip is
-// half empty.  VERIFY_US so.)
+// 191 us for 512 sequences of four drafts, since 456 sequences run at first and the others when
+// the chip is half empty.  172 us so: 100 us of verdicts, and the draws, of which a refused draft's
+// rows take a CTA 44 us.)
 //
 // Sums over a strip are fp32 (1024 bf16 or 512 fp32 logits, 32 or 16 a lane and then the
-// lanes'), sums over strips and the search for the token's strip are in 64 bits: a token's
-// share of [0, 1) begins within a few 1e-8 of where it should.
+// lanes'), and so are a lane's up to 16 strips of a row; the lanes' sums and the search for the
+// token's strip are in 64 bits, of which the SMs do few.  A token's share of [0, 1) begins
+// within about 1e-7 of where it should.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
