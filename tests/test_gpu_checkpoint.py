@@ -381,3 +381,88 @@ def test_layer_backward_matches_autograd(m):
     status, nonfinite = m.muon_sync(plan)
     assert status == m.MUON_OK and nonfinite == 0
     assert all((a - b).abs().max() > 0 for a, b in zip(before, weights))
+
+
+def test_two_threads_on_one_stream(m):
+    """Each thread has a workspace of its own."""
+    import threading
+
+    import torch
+    rng = np.random.default_rng(21)
+    sets = []
+    for k in range(2):
+        x, _ = _matrix(rng, 700, 130)
+        dy, _ = _matrix(rng, 700, 90)
+        sets.append((m.muon_checkpoint_save(x), dy))
+    want = [m.muon_checkpoint_weight_grad(*s) for s in sets]
+    torch.cuda.synchronize()
+    got, stream = [[], []], torch.cuda.current_stream()
+
+    def work(k):
+        for _ in range(20):
+            got[k].append(m.muon_checkpoint_weight_grad(*sets[k], stream=stream))
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert all(len(g) == 20 and torch.equal(t, want[k]) for k, g in enumerate(got) for t in g)
+
+
+def test_refusals(m):
+    import torch
+    x = torch.randn(10, 70, device="cuda")
+    ck = m.muon_checkpoint_save(x)
+    other = m.muon_checkpoint_save(x[:9])
+    dy = torch.randn(10, 30, device="cuda")
+    with pytest.raises(TypeError):
+        m.muon_checkpoint_save(x.half())
+    with pytest.raises(ValueError):
+        m.muon_checkpoint_save(x, checkpoint=other)
+    with pytest.raises(ValueError):
+        m.muon_checkpoint_save(x.t())
+    with pytest.raises(ValueError):
+        m.muon_checkpoint_load(ck, out=torch.empty(10, 71, device="cuda"))
+    with pytest.raises(TypeError):
+        m.muon_checkpoint_load(ck, dtype=torch.float16)
+    with pytest.raises(ValueError):
+        m.muon_checkpoint_load(ck, out=x, dtype=torch.bfloat16)
+    with pytest.raises(m.MuonError):
+        m.muon_checkpoint_load(m.Checkpoint(1, 5, torch.zeros(41, dtype=torch.uint8, device="cuda")[8:]))   # off its boundary
+    for bad in (dict(dy=dy[:9]), dict(dy=dy.cpu()), dict(out=torch.empty(30, 71, device="cuda")),
+                dict(out=torch.empty(70, 30, device="cuda").t()), dict(accumulate=True),
+                dict(out=torch.empty(30, 70, device="cuda"), dtype=torch.bfloat16)):
+        with pytest.raises(ValueError):
+            m.muon_checkpoint_weight_grad(**{"checkpoint": ck, "dy": dy, **bad})
+    with pytest.raises(TypeError):
+        m.muon_checkpoint_weight_grad(ck, dy.half())
+    with pytest.raises(m.MuonError) as e:
+        m.muon_checkpoint_weight_grad(ck, dy, workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == m.MUON_ERR_NO_WORKSPACE
+    with pytest.raises(ValueError):
+        m.muon_swiglu_forward(x, x.bfloat16())
+    with pytest.raises(ValueError):
+        m.muon_swiglu_forward(x, x[:9])
+    with pytest.raises(m.MuonError):
+        m.muon_swiglu_forward(x, x, gate_checkpoint=ck, up_checkpoint=ck)
+    with pytest.raises(ValueError):
+        m.muon_swiglu_backward(x, ck, other)
+    out = torch.empty_like(x)
+    with pytest.raises(m.MuonError):
+        m.muon_swiglu_backward(x, ck, m.muon_checkpoint_save(x), dgate=out, dup=out)
+
+
+def test_rows_written_again(m):
+    """A checkpoint, a gradient and a workspace used again hold nothing of what was there."""
+    import torch
+    x = torch.full((64, 64), float("inf"), device="cuda")
+    ck = m.muon_checkpoint_save(x)
+    dy = torch.ones(64, 64, device="cuda")
+    space = torch.full((m.muon_weight_grad_workspace_bytes(ck, dy),), 255, dtype=torch.uint8, device="cuda")
+    dw = m.muon_checkpoint_weight_grad(ck, dy, workspace=space)
+    assert dw.isnan().all()
+    m.muon_checkpoint_save(torch.ones_like(x), checkpoint=ck)
+    m.muon_checkpoint_weight_grad(ck, dy, out=dw, workspace=space)
+    assert (dw == 64).all()

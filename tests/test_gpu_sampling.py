@@ -357,3 +357,77 @@ def test_drafted_rollout_feeds_the_policy_loss(m):
     stats, _, grad = m.muon_policy_loss(target, tokens, logp, advantages, mask=live, temperature=0.7)
     assert abs(stats[0].item() + (advantages * live).sum().item() / live.sum().item()) <= 1e-4 and stats[3] == 0
     assert (grad[~live] == 0).all() and (grad[live].abs().sum(1) > 0).all()
+
+
+@pytest.mark.parametrize("form", ["logp", "logits"])
+def test_verify_with_the_drafts_own_temperature(m, form):
+    rng = np.random.default_rng(18)
+    args, e = _drafts(rng, [3, 5, 0, 2], 2501, form=form)
+    q = sampling.probabilities(args["draft_logits"].double().cpu().numpy(), 1.7)
+    e["q"], e["qx"] = q, q[np.arange(10), e["drafts"]]
+    rows = np.arange(10) + np.repeat(np.arange(4), [3, 5, 0, 2])
+    ratio = e["p"][rows, e["drafts"]] / e["qx"]
+    u = rng.random(10)
+    e["u"] = np.where(np.abs(u - ratio) < 1e-3, u / 2, u).astype(np.float32)
+    args["accept_uniforms"] = _dev(e["u"])
+    if form == "logp":
+        args["draft_logp"] = _dev(np.log(e["qx"]).astype(np.float32))
+    _check_verify(args, e, m.muon_verify_drafts(**args, draft_temperature=1.7))
+
+
+def test_two_threads_on_one_stream(m):
+    """Each thread has a workspace of its own."""
+    import threading
+
+    import torch
+    rng = np.random.default_rng(19)
+    sets = [_drafts(rng, [4, 2, 7] * 9, 9001, "bfloat16")[0] for _ in range(2)]
+    logits = [s["logits"] for s in sets]
+    u = torch.rand(len(logits[0]), device="cuda")
+    want = [(m.muon_verify_drafts(**s), m.muon_sample_tokens(z, u)) for s, z in zip(sets, logits)]
+    torch.cuda.synchronize()
+    got, stream = [[], []], torch.cuda.current_stream()
+
+    def work(k):
+        for _ in range(20):
+            got[k].append((m.muon_verify_drafts(**sets[k], stream=stream), m.muon_sample_tokens(logits[k], u, stream=stream)))
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for k in range(2):
+        assert len(got[k]) == 20
+        for a, b in got[k]:
+            assert all(torch.equal(x, y) for x, y in zip(a + b, want[k][0] + want[k][1]))
+
+
+def test_refusals(m):
+    import torch
+    z = torch.randn(6, 50, device="cuda")
+    u = torch.rand(6, device="cuda")
+    for bad in (dict(uniforms=u[:5]), dict(uniforms=u.cpu()), dict(uniforms=u.double()), dict(mask=torch.ones(6, device="cuda")),
+                dict(tokens=torch.zeros(6, device="cuda", dtype=torch.int32)), dict(logp=torch.zeros(5, device="cuda")),
+                dict(workspace=torch.zeros(1 << 12))):
+        with pytest.raises((ValueError, TypeError)):
+            m.muon_sample_tokens(z, **{"uniforms": u, **bad})
+    with pytest.raises(m.MuonError) as e:
+        m.muon_sample_tokens(z, u, workspace=torch.zeros(8, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == m.MUON_ERR_NO_WORKSPACE
+    with pytest.raises(ValueError):
+        m.muon_sample_tokens(z.t(), torch.rand(50, device="cuda"))
+    with pytest.raises(TypeError):
+        m.muon_sample_tokens(z.half(), u)
+    args, _ = _drafts(np.random.default_rng(20), [2, 1], 50)
+    for bad in (dict(drafts=args["drafts"][:2]), dict(drafts=args["drafts"].int()), dict(draft_offsets=args["draft_offsets"][:2]),
+                dict(draft_offsets=args["draft_offsets"][:0]), dict(accept_uniforms=args["sample_uniforms"]),
+                dict(sample_uniforms=args["accept_uniforms"]), dict(draft_logits=args["draft_logits"][:2]),
+                dict(draft_logits=args["draft_logits"][:, :40]), dict(draft_logits=args["draft_logits"].bfloat16()),
+                dict(draft_logp=args["draft_logp"].double())):
+        with pytest.raises(ValueError):
+            m.muon_verify_drafts(**{**args, **bad})
+    with pytest.raises(m.MuonError) as e:
+        m.muon_verify_drafts(**{**args, "draft_logits": None})   # log-probabilities of certain drafts
+    assert e.value.status == m.MUON_ERR_INVALID
