@@ -98,16 +98,16 @@ __device__ __forceinline__ Unit unit_of(const GradArgs& a, int u) {
   return r;
 }
 
-// A column of a turned block, `rows` elements, to dW.
+// A column of a turned block, `rows` elements, to dW: 16 rows' loads before their stores.
 template <typename T>
 __device__ __forceinline__ void add_rows(T* p, int64_t stride, int accumulate, const float* turn, int rows) {
 #pragma unroll 1
-  for (int r = 0; r < rows; r += 8) {
-    float y[8];
+  for (int r = 0; r < rows; r += 16) {
+    float y[16];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = accumulate && r + i < rows ? Vec<T>::load(p + (r + i) * stride) : 0.f;
+    for (int i = 0; i < 16; ++i) y[i] = accumulate && r + i < rows ? Vec<T>::load(p + (r + i) * stride) : 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 16; ++i)
       if (r + i < rows) Vec<T>::store(p + (r + i) * stride, y[i] + turn[(r + i) * 33]);
   }
 }
@@ -143,7 +143,6 @@ __device__ __forceinline__ void store_block(const GradArgs& a, int split, int64_
     for (int j = 0; j < 32; ++j) turn[lane * 33 + j] = s[c + j] + poison;
     __syncwarp();
     if (col + c + lane >= a.cols) continue;
-    // eight rows' loads before their stores
     if (a.bf16) add_rows(reinterpret_cast<__nv_bfloat16*>(a.out) + at + c + lane, a.stride, a.accumulate, turn + lane, rows);
     else add_rows(out + c + lane, a.stride, a.accumulate, turn + lane, rows);
   }
@@ -323,7 +322,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) weight_grad_kernel(const __gr
 }
 
 // dy as `parts` bf16 matrices [parts][tokens][ld]: a copy, or the three parts of fp32 values,
-// each cut off at 8 bits of what the ones before it leave (cutting cannot overflow).
+// each cut off at 8 bits of what the ones before it leave (cutting cannot overflow).  It runs
+// beside the load of x before it, and ends after it, so that the product waits for both.
 constexpr int kPartThreads = 256;
 template <typename T>
 __global__ void __launch_bounds__(kPartThreads) parts_kernel(const T* dy, int64_t stride, int64_t tokens, int64_t outs,
@@ -359,6 +359,7 @@ __global__ void __launch_bounds__(kPartThreads) parts_kernel(const T* dy, int64_
                        h[part][6] | h[part][7] << 16);
     }
   }
+  griddep_wait();
 }
 
 // dW (+)= the splits' sums, in their order.
@@ -508,8 +509,8 @@ muon_status muon_checkpoint_weight_grad(const muon_checkpoint* checkpoint, const
     __nv_bfloat16* parts = reinterpret_cast<__nv_bfloat16*>(space + p.x_bytes);
     const int grid = grid_of(rows * (p.ld / 8), kPartThreads, sms);
     e = dy_dtype == MUON_DTYPE_BF16
-            ? launch(parts_kernel<__nv_bfloat16>, grid, kPartThreads, 0, s, 1, false, static_cast<const __nv_bfloat16*>(dy), stride, rows, outs, p.ld, parts)
-            : launch(parts_kernel<float>, grid, kPartThreads, 0, s, 1, false, static_cast<const float*>(dy), stride, rows, outs, p.ld, parts);
+            ? launch(parts_kernel<__nv_bfloat16>, grid, kPartThreads, 0, s, 1, true, static_cast<const __nv_bfloat16*>(dy), stride, rows, outs, p.ld, parts)
+            : launch(parts_kernel<float>, grid, kPartThreads, 0, s, 1, true, static_cast<const float*>(dy), stride, rows, outs, p.ld, parts);
     if (e != cudaSuccess) return cuda_error(e);
     operand = parts;
     ld = p.ld;
