@@ -232,9 +232,10 @@ __device__ __forceinline__ void sum_strips(const RowUnits<T>& row, const Scale& 
   }
 }
 
-// The probabilities of both models at a refused draft.
+// The rows of both models at a refused draft.
 struct Refused {
-  float mp, ip, mq, iq;  // frames, and reciprocals of the sums
+  float mp, mq;  // frames
+  float ratio;   // of the draft model's sum of exponentials to the target's: 1 for equal rows, which leave 0
 };
 
 // Units of the target's row and the draft model's elements at the same places.
@@ -256,13 +257,17 @@ struct UnitPair {
       }
     }
   }
-  // max(p - q, 0) of unit k; each product rounded, so that equal rows leave 0.
+  // max(p - q, 0) of unit k, times the sum of the draft model's exponentials.
   __device__ __forceinline__ void left_over(const SampleArgs& a, const Refused& f, int k, float (&r)[Vec<T>::N]) const {
     float y[Vec<T>::N];
     exps<T>(a.target_scale, f.mp, p[k], r);
     exps<T>(a.draft_scale, f.mq, q[k], y);
 #pragma unroll
-    for (int i = 0; i < Vec<T>::N; ++i) r[i] = fmaxf(__fmul_rn(r[i], f.ip) - __fmul_rn(y[i], f.iq), 0.f);
+    for (int i = 0; i < Vec<T>::N; i += 2) {
+      const float2 d = split(fma2(make_f2(r[i], r[i + 1]), make_f2(-f.ratio, -f.ratio), make_f2(y[i], y[i + 1])));
+      r[i] = fmaxf(-d.x, 0.f);
+      r[i + 1] = fmaxf(-d.y, 0.f);
+    }
   }
 };
 
@@ -277,7 +282,7 @@ __device__ __forceinline__ void sum_left(const SampleArgs& a, const Refused& f, 
   auto inside = [&](int at) { return at + kHalf <= end && row.first(at) >= 0 && row.first(at + kHalf) <= row.vocab; };
   UnitPair<T, L> now;
   now.load(row, zq, u + lane, 32, end, inside(u));
-  float sum = 0.f;
+  F2 sum = make_f2(0.f, 0.f);
   int left = a.strip_units;
   for (int k = k0; k < k1;) {
     UnitPair<T, L> next;
@@ -287,13 +292,14 @@ __device__ __forceinline__ void sum_left(const SampleArgs& a, const Refused& f, 
       float r[Vec<T>::N];
       now.left_over(a, f, i, r);
 #pragma unroll
-      for (int j = 0; j < Vec<T>::N; ++j) sum += r[j];
+      for (int j = 0; j < Vec<T>::N; j += 2) sum = add2(sum, make_f2(r[j], r[j + 1]));
     }
     left -= kHalf;
     if (left == 0) {
-      sum = warp_sum(sum);
-      if (lane == 0) to[k - k0] = StripSum{0.f, sum};
-      sum = 0.f;
+      const float2 halves = split(sum);
+      const float whole = warp_sum(halves.x + halves.y);
+      if (lane == 0) to[k - k0] = StripSum{0.f, whole};
+      sum = make_f2(0.f, 0.f);
       left = a.strip_units;
       ++k;
     }
@@ -764,7 +770,7 @@ __global__ void __launch_bounds__(kFinishWarps * 32, 2) finish_kernel(const __gr
       q = merge(&slice, a.draft_scale, a.cluster, rank, lane);
     }
     fine = usable(q);
-    f = Refused{p.m, (float)(1. / p.s), q.m, (float)(1. / q.s)};
+    f = Refused{p.m, q.m, (float)(q.s / p.s)};
     if (fine) sum_left<T>(a, f, row, zq, strip0 + mine0, strip0 + mine1, left + mine0, lane);
   }
   __syncthreads();
@@ -886,9 +892,9 @@ int cluster_of(int64_t units, int64_t strips, int sms) {
   return cluster;
 }
 
-cudaError_t launch_verify(void (*kernel)(SampleArgs), SampleArgs a, int64_t units, int sms, int alone, bool dependent,
+cudaError_t launch_verify(void (*kernel)(SampleArgs), SampleArgs a, int64_t units, int cluster, int alone, bool dependent,
                           cudaStream_t s) {
-  a.cluster = cluster_of(units, a.all_strips, sms);
+  a.cluster = cluster;
   a.strips = (a.all_strips + a.cluster - 1) / a.cluster;
   const int most = a.cluster == 1 ? alone : kSampleWarps, warps = a.strips < most ? a.strips : most;
   return launch(kernel, (int)(units * a.cluster), 32 * warps, (size_t)2 * a.strips * sizeof(StripSum), s, a.cluster, dependent, a);
@@ -898,11 +904,16 @@ template <typename T>
 cudaError_t run_verify(SampleArgs& a, int sms, cudaStream_t s) {
   cudaError_t e = cudaMemsetAsync(a.counts, 0xFF, (size_t)a.n_seqs * sizeof(int64_t), s);
   if (e != cudaSuccess) return e;
-  // the mean number of rows, rounded up; longer sequences' CTAs take several
-  const int64_t positions = (a.n_drafts + a.n_seqs - 1) / a.n_seqs + 1, most = 0x7FFFFFFF / kMaxCluster / a.n_seqs;
+  // the mean number of rows, rounded up, and twice as many where that costs no second round of
+  // CTAs; longer sequences' CTAs take several
+  const int64_t rows = a.n_drafts + a.n_seqs, most = 0x7FFFFFFF / kMaxCluster / a.n_seqs;
+  int64_t positions = (rows + a.n_seqs - 1) / a.n_seqs;
+  const int cluster = cluster_of(rows, a.all_strips, sms);
+  if (a.n_seqs * positions * cluster <= 3 * sms) positions *= 2;
   a.positions = (int32_t)(positions < most ? positions : most < 1 ? 1 : most);
-  e = launch_verify(judge_kernel<T>, a, a.n_seqs * a.positions, sms, kSampleWarps, false, s);
-  return e == cudaSuccess ? launch_verify(finish_kernel<T>, a, a.n_seqs, sms, kFinishWarps, true, s) : e;
+  e = launch_verify(judge_kernel<T>, a, a.n_seqs * a.positions, cluster, kSampleWarps, false, s);
+  if (e != cudaSuccess) return e;
+  return launch_verify(finish_kernel<T>, a, a.n_seqs, cluster_of(a.n_seqs, a.all_strips, sms), kFinishWarps, true, s);
 }
 
 }  // namespace
