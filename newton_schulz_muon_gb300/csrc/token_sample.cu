@@ -357,34 +357,52 @@ struct DrawSpace {
   float weight[32][kLoads * 8 + 1];  // of a step's elements, a row a lane
 };
 
-// The strip in which the cumulated weight exceeds t (one of weight 0 never does), else the
-// last of positive weight; -1: none.  before: the weights before the first strip, and then
-// before the one that is found.  weight(k), k < strips.
+// Strips' weights, of which a lane has some consecutive ones: its sum, and the sum up to its last.
+struct StripScan {
+  float w;
+  double end;
+};
+__device__ __forceinline__ void strips_of_lane(int strips, int lane, int& k0, int& k1) {
+  const int per = (strips + 31) / 32;
+  k0 = min(lane * per, strips);
+  k1 = min(k0 + per, strips);
+}
 template <typename F>
-__device__ __forceinline__ int find_strip(int strips, double t, double* before, int lane, F weight) {
-  // a lane's strips are consecutive ones
-  const int per = (strips + 31) / 32, k0 = min(lane * per, strips), k1 = min(k0 + per, strips);
-  double w = 0.;
+__device__ __forceinline__ StripScan scan_strips(int strips, int lane, F weight) {
+  int k0, k1;
+  strips_of_lane(strips, lane, k0, k1);
+  StripScan r{0.f, 0.};
 #pragma unroll 1
-  for (int k = k0; k < k1; ++k) w += (double)weight(k);
-  const double end = *before + warp_scan64(w, lane);
-  const unsigned above = __ballot_sync(0xFFFFFFFFu, w > 0. && end > t);
-  const unsigned some = __ballot_sync(0xFFFFFFFFu, w > 0.);
+  for (int k = k0; k < k1; ++k) r.w += weight(k);
+  r.end = warp_scan64((double)r.w, lane);
+  return r;
+}
+
+// The strip in which the cumulated weight exceeds t (one of weight 0 never does), else the
+// last of positive weight; -1: none.  before: the weights before it.  weight(k), k < strips.
+template <typename F>
+__device__ __forceinline__ int find_strip(const StripScan& scan, int strips, double t, double* before, int lane, F weight) {
+  const unsigned above = __ballot_sync(0xFFFFFFFFu, scan.w > 0.f && scan.end > t);
+  const unsigned some = __ballot_sync(0xFFFFFFFFu, scan.w > 0.f);
   if (some == 0) return -1;
   const int l = above ? __ffs(above) - 1 : 31 - __clz(some);
-  double at = end - w, begun = at;
+  const double start = scan.end - (double)scan.w;
+  const float need = (float)(t - start);
+  int k0, k1;
+  strips_of_lane(strips, lane, k0, k1);
+  float at = 0.f, begun = 0.f;
   int strip = 0;
 #pragma unroll 1
   for (int k = k0; k < k1; ++k) {
-    const double x = (double)weight(k);
-    if (x > 0.) {
+    const float x = weight(k);
+    if (x > 0.f) {
       strip = k;
       begun = at;
-      if (at + x > t) break;
+      if (at + x > need) break;
     }
     at += x;
   }
-  *before = __shfl_sync(0xFFFFFFFFu, begun, l);
+  *before = __shfl_sync(0xFFFFFFFFu, start + (double)begun, l);
   return __shfl_sync(0xFFFFFFFFu, strip, l);
 }
 
@@ -466,12 +484,20 @@ __device__ __forceinline__ int find_element(const SampleArgs& a, DrawSpace& sh, 
 // ---------------------------------------------------------------------------
 // sampling
 // ---------------------------------------------------------------------------
+// A CTA's jobs are dealt to its warps as they come, since masked rows take no time.
 template <typename T>
 __global__ void __launch_bounds__(kSampleWarps * 32, kSampleCtas) rows_kernel(const __grid_constant__ SampleArgs a) {
+  __shared__ int next;
+  if (threadIdx.x == 0) next = 0;
+  __syncthreads();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31;
-  const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5), jobs = a.n_seqs * a.pieces;
-  for (int64_t job = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); job < jobs; job += warps) {
+  const int64_t jobs = a.n_seqs * a.pieces;
+  for (;;) {
+    int n;
+    if (lane == 0) n = atomicAdd(&next, 1);
+    const int64_t job = (int64_t)blockIdx.x + (int64_t)__shfl_sync(0xFFFFFFFFu, n, 0) * gridDim.x;
+    if (job >= jobs) break;
     const int64_t t = job / a.pieces;
     if (a.mask != nullptr && a.mask[t] == 0) continue;
     const int k0 = (int)(job - t * a.pieces) * a.each;
@@ -480,51 +506,54 @@ __global__ void __launch_bounds__(kSampleWarps * 32, kSampleCtas) rows_kernel(co
   }
 }
 
-// A warp draws a row's token.
-constexpr int kDrawWarps = 2;  // of a CTA: 2048 rows 112, 100 and 102 us with 4, 2 and 1
+// A warp draws a row's token.  Its time is that of a chain of steps, in which 64-bit sums weigh
+// most (a warp's takes an SM 16 cycles).
+constexpr int kDrawWarps = 2;  // of a CTA
 template <typename T>
 __global__ void __launch_bounds__(kDrawWarps * 32) draw_kernel(const __grid_constant__ SampleArgs a) {
   __shared__ DrawSpace space[kDrawWarps];
-  __shared__ float weights[kDrawWarps][kMaxStrips];
+  __shared__ StripSum table[kDrawWarps][kMaxStrips];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = (int64_t)blockIdx.x * (blockDim.x >> 5) + warp;
+  const bool live = t < a.n_seqs && (a.mask == nullptr || a.mask[t] != 0);
+  const float u = live ? fmaxf(a.sample_u[t], 0.f) : 0.f;
   griddep_wait();
   if (t >= a.n_seqs) return;
   int64_t token = -1;
   float logp = 0.f;
-  if (a.mask == nullptr || a.mask[t] != 0) {
+  if (live) {
     logp = NAN;
     const Scale& c = a.target_scale;
     const RowUnits<T> row(a.target, t, a.target_stride, a.vocab);
     const float2* sums = reinterpret_cast<const float2*>(a.sums + t * a.strips);
-    const float u = fmaxf(a.sample_u[t], 0.f);
+    StripSum* const own = table[warp];
     float m = -INFINITY;
 #pragma unroll 4
-    for (int k = lane; k < a.strips; k += 32) m = fmaxf(m, __ldcg(sums + k).x);
-    m = warp_max(m);
-    double own = 0.;
-#pragma unroll 1
     for (int k = lane; k < a.strips; k += 32) {
       const float2 x = __ldcg(sums + k);
-      weights[warp][k] = x.y * factor(c, x.x, m);
-      own += (double)weights[warp][k];
+      own[k] = StripSum{x.x, x.y};
+      m = fmaxf(m, x.x);
     }
+    m = warp_max(m);
     __syncwarp();
-    const RowSum p{warp_sum64(own), m, 0.};
+    const StripScan scan = scan_strips(a.strips, lane, [&](int k) { return own[k].s *= factor(c, own[k].m, m); });
+    const RowSum p{__shfl_sync(0xFFFFFFFFu, scan.end, 31), m, 0.};
     if (usable(p)) {
+      auto weight = [&](int k) { return own[k].s; };
       double before = 0.;
       const double at = u < 1.f ? (double)u * p.s : (double)INFINITY;  // 1 and above: the last token
-      const int strip = find_strip(a.strips, at, &before, lane, [&](int k) { return weights[warp][k]; });
+      const int strip = find_strip(scan, a.strips, at, &before, lane, weight);
       const int u0 = strip * a.strip_units, u1 = min(u0 + a.strip_units, row.units);
       float rest;
       const int found = find_element<T>(a, space[warp], row, u0, u1, at - before, kPlain, -1, nullptr, Refused{}, m, &rest, lane);
-      double others = (double)rest;
+      int k0, k1;
+      strips_of_lane(a.strips, lane, k0, k1);
+      float others = 0.f;
 #pragma unroll 1
-      for (int k = lane; k < a.strips; k += 32)
-        if (k != strip) others += (double)weights[warp][k];
+      for (int k = k0; k < k1; ++k) others += k == strip ? 0.f : weight(k);
       if (found >= 0) {
         token = found;
-        logp = token_logp<T>(row, c, m, others, found);
+        logp = token_logp<T>(row, c, m, (double)rest + (double)others, found);
       }
     }
   }
@@ -789,12 +818,11 @@ __global__ void __launch_bounds__(kFinishWarps * 32, 2) finish_kernel(const __gr
     auto plain = [&](int k) { return own[k].s * factor(c, own[k].m, p.m); };
     auto weight = [&](int k) { return kind == kLeft ? left[k].s : kind == kWithout && k == without_strip ? without_sum : plain(k); };
     // each CTA's share of the weights in its lane, and their running sum
+    StripScan scan;
     double v;
     for (;;) {
-      float w = 0.f;
-#pragma unroll 1
-      for (int k = lane; k < a.strips; k += 32) w += weight(k);
-      v = warp_sum64((double)w);
+      scan = scan_strips(a.strips, lane, weight);
+      v = __shfl_sync(0xFFFFFFFFu, scan.end, 31);
       if (a.cluster > 1) {
         if (lane == 0) share = v;
         cluster_sync();
@@ -815,12 +843,13 @@ __global__ void __launch_bounds__(kFinishWarps * 32, 2) finish_kernel(const __gr
     const int owner = over ? __ffs(over) - 1 : 31 - __clz(any);
     mine = rank == owner;
     if (mine) {
-      double before = __shfl_sync(0xFFFFFFFFu, upto - v, owner);
-      const int strip = find_strip(a.strips, t, &before, lane, weight);
+      const double here = t - __shfl_sync(0xFFFFFFFFu, upto - v, owner);  // of this CTA's weights
+      double before = 0.;
+      const int strip = find_strip(scan, a.strips, here, &before, lane, weight);
       int u0, u1;
       units_of(a, row, strip0 + strip, u0, u1);
       float rest;
-      const int found = find_element<T>(a, space, row, u0, u1, t - before, kind, (int)without, zq, f, p.m, &rest, lane);
+      const int found = find_element<T>(a, space, row, u0, u1, here - before, kind, (int)without, zq, f, p.m, &rest, lane);
       float others = 0.f;
 #pragma unroll 4
       for (int k = lane; k < a.all_strips; k += 32)
