@@ -94,6 +94,7 @@ struct SampleArgs {
   int32_t cluster;           // CTAs a row or sequence
   int32_t all_strips;        // of a row
   int32_t positions;         // of a sequence that have a CTA each; it takes every positions-th row
+  int32_t draws;             // sequences of one of finish_kernel's last CTAs
 };
 
 __device__ __forceinline__ float factor(const Scale& c, float m, float to) {
@@ -506,8 +507,45 @@ __global__ void __launch_bounds__(kSampleWarps * 32, kSampleCtas) rows_kernel(co
   }
 }
 
-// A warp draws a row's token.  Its time is that of a chain of steps, in which 64-bit sums weigh
-// most (a warp's takes an SM 16 cycles).
+// Draws row r's token from the sums of its strips, which are kept in `own`.  A warp's time here is
+// that of a chain of steps, in which 64-bit sums weigh most (a warp's takes an SM 16 cycles).
+template <typename T>
+__device__ __forceinline__ void draw_row(const SampleArgs& a, int64_t r, const StripSum* from, int strips, float u,
+                                         StripSum* own, DrawSpace& sh, int64_t* token, float* logp, int lane) {
+  const Scale& c = a.target_scale;
+  const RowUnits<T> row(a.target, r, a.target_stride, a.vocab);
+  const float2* sums = reinterpret_cast<const float2*>(from);
+  float m = -INFINITY;
+#pragma unroll 4
+  for (int k = lane; k < strips; k += 32) {
+    const float2 x = __ldcg(sums + k);
+    own[k] = StripSum{x.x, x.y};
+    m = fmaxf(m, x.x);
+  }
+  m = warp_max(m);
+  __syncwarp();
+  const StripScan scan = scan_strips(strips, lane, [&](int k) { return own[k].s *= factor(c, own[k].m, m); });
+  const RowSum p{__shfl_sync(0xFFFFFFFFu, scan.end, 31), m, 0.};
+  *token = -1;
+  *logp = NAN;
+  if (!usable(p)) return;
+  auto weight = [&](int k) { return own[k].s; };
+  double before = 0.;
+  const double at = u < 1.f ? (double)u * p.s : (double)INFINITY;  // 1 and above: the last token
+  const int strip = find_strip(scan, strips, at, &before, lane, weight);
+  const int u0 = strip * a.strip_units, u1 = min(u0 + a.strip_units, row.units);
+  float rest;
+  const int found = find_element<T>(a, sh, row, u0, u1, at - before, kPlain, -1, nullptr, Refused{}, m, &rest, lane);
+  int k0, k1;
+  strips_of_lane(strips, lane, k0, k1);
+  float others = 0.f;
+#pragma unroll 1
+  for (int k = k0; k < k1; ++k) others += k == strip ? 0.f : weight(k);
+  if (found < 0) return;
+  *token = found;
+  *logp = token_logp<T>(row, c, m, (double)rest + (double)others, found);
+}
+
 constexpr int kDrawWarps = 2;  // of a CTA
 template <typename T>
 __global__ void __launch_bounds__(kDrawWarps * 32) draw_kernel(const __grid_constant__ SampleArgs a) {
@@ -521,42 +559,7 @@ __global__ void __launch_bounds__(kDrawWarps * 32) draw_kernel(const __grid_cons
   if (t >= a.n_seqs) return;
   int64_t token = -1;
   float logp = 0.f;
-  if (live) {
-    logp = NAN;
-    const Scale& c = a.target_scale;
-    const RowUnits<T> row(a.target, t, a.target_stride, a.vocab);
-    const float2* sums = reinterpret_cast<const float2*>(a.sums + t * a.strips);
-    StripSum* const own = table[warp];
-    float m = -INFINITY;
-#pragma unroll 4
-    for (int k = lane; k < a.strips; k += 32) {
-      const float2 x = __ldcg(sums + k);
-      own[k] = StripSum{x.x, x.y};
-      m = fmaxf(m, x.x);
-    }
-    m = warp_max(m);
-    __syncwarp();
-    const StripScan scan = scan_strips(a.strips, lane, [&](int k) { return own[k].s *= factor(c, own[k].m, m); });
-    const RowSum p{__shfl_sync(0xFFFFFFFFu, scan.end, 31), m, 0.};
-    if (usable(p)) {
-      auto weight = [&](int k) { return own[k].s; };
-      double before = 0.;
-      const double at = u < 1.f ? (double)u * p.s : (double)INFINITY;  // 1 and above: the last token
-      const int strip = find_strip(scan, a.strips, at, &before, lane, weight);
-      const int u0 = strip * a.strip_units, u1 = min(u0 + a.strip_units, row.units);
-      float rest;
-      const int found = find_element<T>(a, space[warp], row, u0, u1, at - before, kPlain, -1, nullptr, Refused{}, m, &rest, lane);
-      int k0, k1;
-      strips_of_lane(a.strips, lane, k0, k1);
-      float others = 0.f;
-#pragma unroll 1
-      for (int k = k0; k < k1; ++k) others += k == strip ? 0.f : weight(k);
-      if (found >= 0) {
-        token = found;
-        logp = token_logp<T>(row, c, m, (double)rest + (double)others, found);
-      }
-    }
-  }
+  if (live) draw_row<T>(a, t, a.sums + t * a.strips, a.strips, u, table[warp], space[warp], &token, &logp, lane);
   if (lane == 0) {
     a.tokens[t] = token;
     a.logp[t] = logp;
@@ -645,17 +648,22 @@ __global__ void __launch_bounds__(kSampleWarps * 32, 3) judge_kernel(const __gri
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int rank = a.cluster > 1 ? (int)cluster_ctarank() : 0;
   const int64_t unit = blockIdx.x / a.cluster, first = unit / a.n_seqs, seq = unit - first * a.n_seqs;
+  unsigned long long* const refused = reinterpret_cast<unsigned long long*>(a.counts) + seq;
+  unsigned long long seen = ~0ull;  // the first refused position, as far as it is known
+  if (a.cluster == 1 && threadIdx.x == 0) seen = __ldcg(refused);
   const Sequence e = sequence_of(a, seq);
   const bool both = a.draft != nullptr && a.draft_logp == nullptr;
   const int strip0 = rank * a.strips;
   // of the CTA's strips this warp's
   const int per_warp = (a.strips + warps - 1) / warps, mine0 = min(warp * per_warp, a.strips), mine1 = min(mine0 + per_warp, a.strips);
   griddep_launch_dependents();
-  unsigned long long* const refused = reinterpret_cast<unsigned long long*>(a.counts) + seq;
   int parity = 0;
   for (int64_t i = first; i <= e.n; i += a.positions, parity ^= 1) {
     if (a.cluster == 1) {  // CTAs of a cluster must go the same way
-      if (threadIdx.x == 0) stop = __ldcg(refused) < (unsigned long long)i;
+      if (threadIdx.x == 0) {
+        if (i != first) seen = __ldcg(refused);
+        stop = seen < (unsigned long long)i;
+      }
       __syncthreads();
       if (stop) break;
     }
@@ -730,19 +738,41 @@ __global__ void __launch_bounds__(kSampleWarps * 32, 3) judge_kernel(const __gri
   if (a.cluster > 1) cluster_sync();  // no CTA leaves while another may read its sums
 }
 
-// The token after a sequence's taken drafts, and -1 behind it.  Only some of the CTAs have a
-// refused draft's rows to read, so that a CTA alone has more warps (512 sequences of four
-// drafts in all: 180 us with 8 warps, 172 us with 12; clusters, whose barriers wait for more warps,
-// 47 and 53 us for 37 sequences).
+// The token after a sequence's taken drafts, and -1 behind it.  A refused draft's rows take a CTA or
+// cluster; the grid's last CTAs draw for the sequences whose drafts were all taken, a warp for
+// each (with a CTA for these too, the refused ones among 512 sequences of four drafts waited for
+// them: 166 us in all).  Not all CTAs have much to do, so that one alone has more warps (512
+// sequences: 180 us with 8 warps, 172 us with 12; clusters, whose barriers wait for more warps, 47
+// and 53 us for 37 sequences).
 constexpr int kFinishWarps = 12;
+constexpr int kDraws = 4;  // sequences of one of the last CTAs
 template <typename T>
 __global__ void __launch_bounds__(kFinishWarps * 32, 2) finish_kernel(const __grid_constant__ SampleArgs a) {
   constexpr int N = Vec<T>::N;
-  extern __shared__ StripSum tables[];  // [2][strips]: of p; of q, then of the difference
+  extern __shared__ StripSum tables[];  // [2][strips]: of p; of q, then of the difference.  [draws][all strips]
   __shared__ RowSum slice;
   __shared__ double share;              // this CTA's part of the weights
-  __shared__ DrawSpace space;
+  __shared__ DrawSpace space[kDraws];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int64_t drawers = a.n_seqs * a.cluster;  // the first of the last CTAs
+  if (blockIdx.x >= drawers) {
+    const int64_t seq = (blockIdx.x - drawers) * a.draws + warp;
+    if (warp >= a.draws || seq >= a.n_seqs) return;
+    const Sequence e = sequence_of(a, seq);
+    const float u = fmaxf(a.sample_u[seq], 0.f);
+    griddep_wait();
+    if (__ldcg(a.counts + seq) >= 0) return;  // refused
+    const int64_t r = e.row0 + e.n;
+    int64_t token;
+    float logp;
+    draw_row<T>(a, r, a.sums + r * a.all_strips, a.all_strips, u, tables + warp * a.all_strips, space[warp], &token, &logp, lane);
+    if (lane == 0) {
+      a.tokens[r] = token;
+      a.logp[r] = logp;
+      a.counts[seq] = e.n;
+    }
+    return;
+  }
   const int rank = a.cluster > 1 ? (int)cluster_ctarank() : 0;
   const int64_t seq = blockIdx.x / a.cluster;
   const Sequence e = sequence_of(a, seq);
@@ -751,8 +781,9 @@ __global__ void __launch_bounds__(kFinishWarps * 32, 2) finish_kernel(const __gr
   const Scale& c = a.target_scale;
   griddep_wait();
   const unsigned long long first_refused = __ldcg(reinterpret_cast<unsigned long long*>(a.counts) + seq);
-  const bool refused = first_refused < (unsigned long long)e.n;
-  const int64_t taken = refused ? (int64_t)first_refused : e.n, r = e.row0 + taken, d = e.lo + taken;
+  // all taken: all ones, or the number of drafts where it has been drawn for
+  if (first_refused >= (unsigned long long)e.n) return;
+  const int64_t taken = (int64_t)first_refused, r = e.row0 + taken, d = e.lo + taken;
   const RowUnits<T> row(a.target, r, a.target_stride, a.vocab);
   // the row's sums, by every warp alike, and this CTA's strips of them
   const StripSum* const all = a.sums + r * a.all_strips;
@@ -768,7 +799,7 @@ __global__ void __launch_bounds__(kFinishWarps * 32, 2) finish_kernel(const __gr
   float without_sum = 0.f;
   Refused f{};
   const T* zq = nullptr;
-  if (refused && fine && a.draft == nullptr) {
+  if (fine && a.draft == nullptr) {
     kind = kWithout;
     without = a.drafts[d];
     if (without >= 0 && without < a.vocab) {
@@ -780,7 +811,7 @@ __global__ void __launch_bounds__(kFinishWarps * 32, 2) finish_kernel(const __gr
         without_sum = warp_sum(sum_without<T>(row, c, p.m, u0, u1, (int)without, lane));
       }
     }
-  } else if (refused && fine) {
+  } else if (fine) {
     kind = kLeft;
     const RowUnits<T> draft(a.draft, d, a.draft_stride, a.vocab);
     zq = draft.z;
@@ -849,7 +880,7 @@ __global__ void __launch_bounds__(kFinishWarps * 32, 2) finish_kernel(const __gr
       int u0, u1;
       units_of(a, row, strip0 + strip, u0, u1);
       float rest;
-      const int found = find_element<T>(a, space, row, u0, u1, here - before, kind, (int)without, zq, f, p.m, &rest, lane);
+      const int found = find_element<T>(a, space[0], row, u0, u1, here - before, kind, (int)without, zq, f, p.m, &rest, lane);
       float others = 0.f;
 #pragma unroll 4
       for (int k = lane; k < a.all_strips; k += 32)
@@ -864,8 +895,7 @@ __global__ void __launch_bounds__(kFinishWarps * 32, 2) finish_kernel(const __gr
     a.tokens[r] = token;
     a.logp[r] = lp;
   }
-  if (a.cluster > 1) cluster_sync();  // every CTA has read counts, and no CTA leaves before
-  if (rank == 0 && lane == 0) a.counts[seq] = taken;
+  if (a.cluster > 1) cluster_sync();  // no CTA leaves while another may read its sums
 }
 
 // ---------------------------------------------------------------------------
@@ -921,12 +951,12 @@ int cluster_of(int64_t units, int64_t strips, int sms) {
   return cluster;
 }
 
-cudaError_t launch_verify(void (*kernel)(SampleArgs), SampleArgs a, int64_t units, int cluster, int alone, bool dependent,
-                          cudaStream_t s) {
-  a.cluster = cluster;
+// The strips of a row divided among the CTAs of a cluster, and a CTA's warps.
+int share_strips(SampleArgs& a, int64_t units, int sms, int alone) {
+  a.cluster = cluster_of(units, a.all_strips, sms);
   a.strips = (a.all_strips + a.cluster - 1) / a.cluster;
-  const int most = a.cluster == 1 ? alone : kSampleWarps, warps = a.strips < most ? a.strips : most;
-  return launch(kernel, (int)(units * a.cluster), 32 * warps, (size_t)2 * a.strips * sizeof(StripSum), s, a.cluster, dependent, a);
+  const int most = a.cluster == 1 ? alone : kSampleWarps;
+  return a.strips < most ? a.strips : most;
 }
 
 template <typename T>
@@ -937,12 +967,17 @@ cudaError_t run_verify(SampleArgs& a, int sms, cudaStream_t s) {
   // CTAs; longer sequences' CTAs take several
   const int64_t rows = a.n_drafts + a.n_seqs, most = 0x7FFFFFFF / kMaxCluster / a.n_seqs;
   int64_t positions = (rows + a.n_seqs - 1) / a.n_seqs;
-  const int cluster = cluster_of(rows, a.all_strips, sms);
-  if (a.n_seqs * positions * cluster <= 3 * sms) positions *= 2;
+  int warps = share_strips(a, rows, sms, kSampleWarps);
+  if (a.n_seqs * positions * a.cluster <= 3 * sms) positions *= 2;
   a.positions = (int32_t)(positions < most ? positions : most < 1 ? 1 : most);
-  e = launch_verify(judge_kernel<T>, a, a.n_seqs * a.positions, cluster, kSampleWarps, false, s);
+  e = launch(judge_kernel<T>, (int)(a.n_seqs * a.positions * a.cluster), 32 * warps, (size_t)2 * a.strips * sizeof(StripSum), s,
+             a.cluster, false, a);
   if (e != cudaSuccess) return e;
-  return launch_verify(finish_kernel<T>, a, a.n_seqs, cluster_of(a.n_seqs, a.all_strips, sms), kFinishWarps, true, s);
+  warps = share_strips(a, a.n_seqs, sms, kFinishWarps);
+  a.draws = a.n_seqs < 4 * sms ? 1 : warps < kDraws ? warps : kDraws;
+  const int64_t drawers = (a.n_seqs + a.draws - 1) / a.draws, ctas = (a.n_seqs + (drawers + a.cluster - 1) / a.cluster) * a.cluster;
+  const int strips = 2 * a.strips > a.draws * a.all_strips ? 2 * a.strips : a.draws * a.all_strips;
+  return launch(finish_kernel<T>, (int)ctas, 32 * warps, strips * sizeof(StripSum), s, a.cluster, true, a);
 }
 
 }  // namespace
@@ -1001,7 +1036,7 @@ muon_status muon_verify_drafts(const muon_token_batch* target, const muon_token_
   int32_t st = check_rows(target);
   if (st == MUON_OK) st = check_rows(draft);
   if (st != MUON_OK) return st;
-  if (n_seqs < 0 || n_seqs > (1ll << 31) - 1) return invalid("n_seqs must be in [0, 2^31)");
+  if (n_seqs < 0 || n_seqs > (1ll << 30) - 1) return invalid("n_seqs must be in [0, 2^30)");
   if (target->tokens != draft->tokens + n_seqs)
     return invalid("the target has a row for each draft and one more for each sequence");
   if (draft->vocab != target->vocab || draft->dtype != target->dtype)
