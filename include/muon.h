@@ -460,8 +460,8 @@ typedef struct {
 muon_status muon_token_logprobs(const muon_token_batch* batch, float* logp, void* stream);
 
 /* Workspace of the two calls below (bytes).  rows: the rows of logits to sample; for
- * verification the target's, n_drafts + n_seqs, and n_drafts more where draft_logp is NULL and
- * the draft model's logits are not.  Host work. */
+ * verification the target's, n_drafts + n_seqs, and n_drafts more where the draft model's logits
+ * are not NULL.  Host work. */
 muon_status muon_sample_workspace_bytes(int64_t rows, int64_t vocab, int32_t dtype, size_t* bytes);
 
 /* A token for each row of logits, drawn with a given uniform number: p = softmax(logits /

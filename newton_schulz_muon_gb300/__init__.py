@@ -752,8 +752,7 @@ def muon_verify_drafts(logits, drafts, draft_offsets, accept_uniforms, sample_un
             raise ValueError(f"draft_logits: expected [{n}, {target.vocab}] {logits.dtype} values on cuda:{device}, got "
                              f"shape {tuple(draft_logits.shape)}, {draft_logits.dtype} on {draft_logits.device}")
     draft.targets = _vector(drafts, n, i64, "drafts", device)
-    both = draft_logits is not None and draft_logp is None
-    nbytes = muon_sample_workspace_bytes(rows + (n if both else 0), target.vocab, logits.dtype)
+    nbytes = muon_sample_workspace_bytes(rows + (0 if draft_logits is None else n), target.vocab, logits.dtype)
     context, handle = _on_stream(stream, device)
     with context:
         _keep, ws, nbytes = _space(workspace, nbytes, device, handle)

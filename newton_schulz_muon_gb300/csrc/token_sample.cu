@@ -90,7 +90,7 @@ struct SampleArgs {
   int32_t each, pieces;      // strips that a warp takes at a time; of a row: strips / each, rounded up
   StripSum* sums;            // workspace, [rows][strips of a row]
   // verification
-  StripSum* q_sums;          // workspace, [drafts][all strips], where draft_logp is null
+  StripSum* q_sums;          // workspace, [drafts][all strips], where there is a draft model
   int32_t cluster;           // CTAs a row or sequence
   int32_t all_strips;        // of a row
   int32_t positions;         // of a sequence that have a CTA each; it takes every positions-th row
@@ -644,7 +644,7 @@ __global__ void __launch_bounds__(kSampleWarps * 32, 3) judge_kernel(const __gri
   constexpr int N = Vec<T>::N;
   extern __shared__ StripSum tables[];  // [target and draft][strips]
   __shared__ RowSum slice[2][2];
-  __shared__ bool stop;
+  __shared__ bool stop, refusing;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int rank = a.cluster > 1 ? (int)cluster_ctarank() : 0;
   const int64_t unit = blockIdx.x / a.cluster, first = unit / a.n_seqs, seq = unit - first * a.n_seqs;
@@ -708,6 +708,7 @@ __global__ void __launch_bounds__(kSampleWarps * 32, 3) judge_kernel(const __gri
       }
       if (a.cluster > 1) cluster_sync();
       if (warp == 0) {
+        if (lane == 0) refusing = false;
         const RowSum p = merge(&slice[parity][0], a.target_scale, a.cluster, rank, lane);
         const float x = zy - p.m;
         const float logp = __fmaf_rn(x, a.target_scale.inv_hi, x * a.target_scale.inv_lo) - logf((float)p.s);
@@ -720,7 +721,10 @@ __global__ void __launch_bounds__(kSampleWarps * 32, 3) judge_kernel(const __gri
         }
         ok = ok && u < expf(logp - logq);
         if (!ok) {
-          if (rank == 0 && lane == 0) atomicMin(refused, (unsigned long long)i);
+          unsigned long long before = ~0ull;
+          if (rank == 0 && lane == 0) before = atomicMin(refused, (unsigned long long)i);
+          // not where an earlier draft was refused meanwhile; CTAs of a cluster go the same way
+          if (lane == 0) refusing = a.cluster > 1 || before >= (unsigned long long)i;
         } else if (strip >= 0 && strip < a.strips) {
           int u0, u1;
           units_of(a, row, strip0 + strip, u0, u1);
@@ -734,6 +738,17 @@ __global__ void __launch_bounds__(kSampleWarps * 32, 3) judge_kernel(const __gri
       }
     }
     __syncthreads();  // the tables are free
+    // a refused draft's token needs the draft model's row, too, and no row behind it
+    if (drafted && refusing) {
+      if (a.draft != nullptr && !both) {
+        const RowUnits<T> draft(a.draft, d, a.draft_stride, a.vocab);
+        sum_strips<T>(draft, a.draft_scale, a.strip_units, strip0 + mine0, strip0 + mine1, tables + mine0, lane);
+        __syncthreads();
+        for (int k = threadIdx.x; k < a.strips && strip0 + k < a.all_strips; k += blockDim.x)
+          a.q_sums[d * a.all_strips + strip0 + k] = tables[k];
+      }
+      break;
+    }
   }
   if (a.cluster > 1) cluster_sync();  // no CTA leaves while another may read its sums
 }
@@ -749,8 +764,7 @@ constexpr int kDraws = 4;  // sequences of one of the last CTAs
 template <typename T>
 __global__ void __launch_bounds__(kFinishWarps * 32, 2) finish_kernel(const __grid_constant__ SampleArgs a) {
   constexpr int N = Vec<T>::N;
-  extern __shared__ StripSum tables[];  // [2][strips]: of p; of q, then of the difference.  [draws][all strips]
-  __shared__ RowSum slice;
+  extern __shared__ StripSum tables[];  // [2][strips]: of p, of the difference.  [draws][all strips]
   __shared__ double share;              // this CTA's part of the weights
   __shared__ DrawSpace space[kDraws];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
@@ -815,20 +829,7 @@ __global__ void __launch_bounds__(kFinishWarps * 32, 2) finish_kernel(const __gr
     kind = kLeft;
     const RowUnits<T> draft(a.draft, d, a.draft_stride, a.vocab);
     zq = draft.z;
-    RowSum q;
-    if (a.draft_logp == nullptr) {
-      q = sum_table(a.q_sums + d * a.all_strips, a.all_strips, a.draft_scale, -1, lane);
-    } else {
-      sum_strips<T>(draft, a.draft_scale, a.strip_units, strip0 + mine0, strip0 + mine1, left + mine0, lane);
-      __syncthreads();
-      if (warp == 0) {
-        const RowSum t = sum_table(left, a.strips, a.draft_scale, -1, lane);
-        if (lane == 0) slice = t;
-      }
-      if (a.cluster > 1) cluster_sync();
-      else __syncthreads();
-      q = merge(&slice, a.draft_scale, a.cluster, rank, lane);
-    }
+    const RowSum q = sum_table(a.q_sums + d * a.all_strips, a.all_strips, a.draft_scale, -1, lane);
     fine = usable(q);
     f = Refused{p.m, q.m, (float)(q.s / p.s)};
     if (fine) sum_left<T>(a, f, row, zq, strip0 + mine0, strip0 + mine1, left + mine0, lane);
@@ -895,7 +896,6 @@ __global__ void __launch_bounds__(kFinishWarps * 32, 2) finish_kernel(const __gr
     a.tokens[r] = token;
     a.logp[r] = lp;
   }
-  if (a.cluster > 1) cluster_sync();  // no CTA leaves while another may read its sums
 }
 
 // ---------------------------------------------------------------------------
@@ -1070,10 +1070,10 @@ muon_status muon_verify_drafts(const muon_token_batch* target, const muon_token_
   a.n_seqs = n_seqs;
   strips_of(a.vocab, target->dtype, &a.strip_units, &a.all_strips);
   const size_t row = (size_t)a.all_strips * sizeof(StripSum), rows = (size_t)(a.n_drafts + n_seqs);
-  const bool both = draft->logits && !draft_logp;
-  if ((st = check_workspace(workspace, workspace_bytes, (rows + (both ? (size_t)a.n_drafts : 0)) * row)) != MUON_OK) return st;
+  if ((st = check_workspace(workspace, workspace_bytes, (rows + (draft->logits ? (size_t)a.n_drafts : 0)) * row)) != MUON_OK)
+    return st;
   a.sums = static_cast<StripSum*>(workspace);
-  a.q_sums = both ? a.sums + rows * a.all_strips : nullptr;
+  a.q_sums = draft->logits ? a.sums + rows * a.all_strips : nullptr;
   int sms;
   if ((st = find_device(&sms)) != MUON_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
