@@ -13,22 +13,25 @@
 // that a row is read once.  A refused draft's row is read twice, since the difference of the
 // probabilities needs both rows' normalisers first.
 //
-// Sampling: the strips of all rows are dealt out to the warps of the whole chip alike, and a
-// second kernel draws the tokens, a warp a row.  (With a CTA a row 2048 rows of 131072 bf16
-// logits took 117 us: the ends of rows, and 3.03 rounds of CTAs that took 4.  100 us so, a
-// tenth of them masked: 82 us of strips, 5.9 TB/s, and the draws.)
+// Sampling: the strips of all rows are dealt out to the CTAs of the whole chip alike, and by each to
+// its warps as they come free; a second kernel draws the tokens, a warp a row.  2048 rows of 131072
+// bf16 logits, a tenth masked: 90 us, of which the strips are 74 (6.5 TB/s) and the draws 9.  (Strips
+// dealt to the warps beforehand: 9 us more, since masked rows leave some with less; a CTA a row: 117
+// us in all.)
 //
 // Verification: a CTA a row (a cluster of them where there are few rows), position by position
 // over all sequences, judges the row's draft; rows of a sequence whose draft was refused before
 // are left out as far as that is known when their CTA starts, which changes no result.  A second
-// kernel, a CTA or cluster a sequence, draws the tokens.  (A CTA a sequence, row after row, took
-// 191 us for 512 sequences of four drafts, since 456 sequences run at first and the others when
-// the chip is half empty.  172 us so: 100 us of verdicts, and the draws, of which a refused draft's
-// rows take a CTA 44 us.)
+// kernel draws the tokens, a CTA or cluster for each refused draft, a warp for each other sequence.
+// 512 sequences of four drafts, 131072 bf16 logits: 149 us, of which 98 are verdicts, 22 the
+// difference of a refused draft's rows (two exponentials an element, at most two rows an SM: 17 us
+// of the exponential unit), 10 the steps around it.  (A CTA a sequence, row after row, took 191 us,
+// since 456 sequences run at first and the others when the chip is half empty; with four CTAs an SM
+// more rows are under way that turn out not to count: 9 us more.)
 //
 // Sums over a strip are fp32 (1024 bf16 or 512 fp32 logits, 32 or 16 a lane and then the
-// lanes'), and so are a lane's up to 16 strips of a row; the lanes' sums and the search for the
-// token's strip are in 64 bits, of which the SMs do few.  A token's share of [0, 1) begins
+// lanes'), and so are a lane's up to 16 strips of a row; the lanes' sums and the search among
+// them are in 64 bits, of which the SMs do few.  A token's share of [0, 1) begins
 // within about 1e-7 of where it should.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -546,7 +549,7 @@ __device__ __forceinline__ void draw_row(const SampleArgs& a, int64_t r, const S
   *logp = token_logp<T>(row, c, m, (double)rest + (double)others, found);
 }
 
-constexpr int kDrawWarps = 2;  // of a CTA
+constexpr int kDrawWarps = 4;  // of a CTA (1, 2 and 4 alike)
 template <typename T>
 __global__ void __launch_bounds__(kDrawWarps * 32) draw_kernel(const __grid_constant__ SampleArgs a) {
   __shared__ DrawSpace space[kDrawWarps];
@@ -756,9 +759,9 @@ __global__ void __launch_bounds__(kSampleWarps * 32, 3) judge_kernel(const __gri
 // The token after a sequence's taken drafts, and -1 behind it.  A refused draft's rows take a CTA or
 // cluster; the grid's last CTAs draw for the sequences whose drafts were all taken, a warp for
 // each (with a CTA for these too, the refused ones among 512 sequences of four drafts waited for
-// them: 166 us in all).  Not all CTAs have much to do, so that one alone has more warps (512
-// sequences: 180 us with 8 warps, 172 us with 12; clusters, whose barriers wait for more warps, 47
-// and 53 us for 37 sequences).
+// them: 14 us more).  Not all CTAs have much to do, so that one alone has more warps (512
+// sequences: 152 us with 12, 170 with 8, 155 with 16, 170 with 24; clusters, whose barriers wait for
+// more warps, 47 us with 8 and 53 with 12 for 37 sequences, when a call took that).
 constexpr int kFinishWarps = 12;
 constexpr int kDraws = 4;  // sequences of one of the last CTAs
 template <typename T>
@@ -929,7 +932,7 @@ void strips_of(int64_t vocab, int32_t dtype, int32_t* units, int32_t* strips) {
 }
 
 // Sampling: strips that a warp takes at a time, four where every warp of the chip has several
-// such pieces.
+// such pieces (2048 rows of 131072 bf16 logits: 90 us, 99 with two, 89 with eight).
 template <typename T>
 cudaError_t run_rows(SampleArgs& a, int sms, cudaStream_t s) {
   const int64_t chip = (int64_t)sms * kSampleCtas * kSampleWarps, all = a.n_seqs * a.strips;
@@ -940,8 +943,7 @@ cudaError_t run_rows(SampleArgs& a, int sms, cudaStream_t s) {
   const int64_t warps = per_sm < kSampleWarps ? per_sm : kSampleWarps, ctas = (jobs + warps - 1) / warps, most = (int64_t)sms * kSampleCtas;
   cudaError_t e = launch(rows_kernel<T>, (int)(ctas < most ? ctas : most), (int)(32 * warps), 0, s, 1, false, a);
   if (e != cudaSuccess) return e;
-  const int64_t drawers = a.n_seqs < 4ll * sms ? 1 : kDrawWarps;
-  return launch(draw_kernel<T>, (int)((a.n_seqs + drawers - 1) / drawers), (int)(32 * drawers), 0, s, 1, true, a);
+  return launch(draw_kernel<T>, (int)((a.n_seqs + kDrawWarps - 1) / kDrawWarps), 32 * kDrawWarps, 0, s, 1, true, a);
 }
 
 // CTAs a row: as many as keep every SM busy with three, and have two strips each.
