@@ -23,11 +23,11 @@
 // over all sequences, judges the row's draft; rows of a sequence whose draft was refused before
 // are left out as far as that is known when their CTA starts, which changes no result.  A second
 // kernel draws the tokens, a CTA or cluster for each refused draft, a warp for each other sequence.
-// 512 sequences of four drafts, 131072 bf16 logits: 149 us, of which 98 are verdicts, 22 the
-// difference of a refused draft's rows (two exponentials an element, at most two rows an SM: 17 us
-// of the exponential unit), 10 the steps around it.  (A CTA a sequence, row after row, took 191 us,
-// since 456 sequences run at first and the others when the chip is half empty; with four CTAs an SM
-// more rows are under way that turn out not to count: 9 us more.)
+// 512 sequences of four drafts, 131072 bf16 logits: 149 us, of which 98 are verdicts, 25 the
+// difference of 236 refused drafts' rows (5 TB/s), 10 the steps around it.  (The difference formed
+// where the draft is refused: 164 us, the last of them on an empty chip; a CTA a sequence, row after
+// row: 191 us, since 456 sequences run at first and the others when the chip is half empty; with
+// four CTAs an SM more rows are under way that turn out not to count: 9 us more.)
 //
 // Sums over a strip are fp32 (1024 bf16 or 512 fp32 logits, 32 or 16 a lane and then the
 // lanes'), and so are a lane's up to 16 strips of a row; the lanes' sums and the search among

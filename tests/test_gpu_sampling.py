@@ -216,6 +216,38 @@ def test_verify(m, lengths, v, dtype, pad, lead, off, form):
 
 
 @pytest.mark.parametrize("form", ["logp", "logits", "certain"])
+@pytest.mark.parametrize("taken", [False, True])
+def test_verify_one_long_sequence_among_many(m, form, taken):
+    """Its rows take several rounds of CTAs, and more sequences than one CTA draws for."""
+    rng = np.random.default_rng(21)
+    args, e = _drafts(rng, [0, 1, 2] * 220 + [30, 1], 700, "float32", 1, 0, 1.0, 0.3, form)
+    if taken:
+        e["u"] = np.zeros(len(e["u"]), np.float32)
+        args["accept_uniforms"] = _dev(e["u"])
+    got = m.muon_verify_drafts(**args)
+    _check_verify(args, e, got)
+    again = m.muon_verify_drafts(**args)
+    assert all((x == y).all() for x, y in zip(got, again))
+
+
+def test_sample_masked_halves(m):
+    """All of some CTAs' rows are masked."""
+    rng = np.random.default_rng(22)
+    logits, z = _rows(rng, 1300, 9000, "bfloat16", 0, 0, 1.0)
+    mask = np.arange(1300) % 7 < 2
+    mask[200:900] = False
+    u = rng.random(1300).astype(np.float32)
+    tokens, logp = m.muon_sample_tokens(logits, _dev(u), mask=_dev(mask))
+    tokens, logp = tokens.cpu().numpy(), logp.cpu().numpy()
+    assert (tokens[~mask] == -1).all() and (logp[~mask] == 0).all()
+    p = sampling.probabilities(z, 1.0)
+    for t in np.flatnonzero(mask):
+        assert sampling.distance(p[t], float(u[t]), tokens[t]) <= SHARE
+    err = np.abs(logp[mask] - _logp(p[mask], tokens[mask]))
+    assert (err <= LP_ABS + LP_REL * np.abs(logp[mask])).all(), err.max()
+
+
+@pytest.mark.parametrize("form", ["logp", "logits", "certain"])
 def test_verify_all_taken_or_none(m, form):
     rng = np.random.default_rng(11)
     for share in (1, 0):
