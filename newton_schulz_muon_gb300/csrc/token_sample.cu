@@ -275,30 +275,29 @@ struct UnitPair {
   }
 };
 
-// The sums of max(p - q, 0) over the strips [k0, k1), into `to`; half a step at a time, the
-// next half's loads under way.
+// The sums of max(p - q, 0) over the strips [k0, k1), into `to`; a step's loads are under way
+// while the step before is summed (512 sequences: 149 us with 8 warps a CTA; half steps 170, and
+// 149, 155 and 170 with 12, 16 and 24 warps).
 template <typename T>
 __device__ __forceinline__ void sum_left(const SampleArgs& a, const Refused& f, const RowUnits<T>& row, const T* zq, int k0,
                                          int k1, StripSum* to, int lane) {
-  constexpr int L = kLoads / 2, kHalf = 32 * L;
   const int end = (int)min((int64_t)k1 * a.strip_units, (int64_t)row.units);
   int u = (int)min((int64_t)k0 * a.strip_units, (int64_t)row.units);
-  auto inside = [&](int at) { return at + kHalf <= end && row.first(at) >= 0 && row.first(at + kHalf) <= row.vocab; };
-  UnitPair<T, L> now;
-  now.load(row, zq, u + lane, 32, end, inside(u));
+  UnitPair<T, kLoads> now;
+  now.load(row, zq, u + lane, 32, end, step_inside<T>(row, u, end));
   F2 sum = make_f2(0.f, 0.f);
   int left = a.strip_units;
   for (int k = k0; k < k1;) {
-    UnitPair<T, L> next;
-    next.load(row, zq, u + kHalf + lane, 32, end, inside(u + kHalf));
+    UnitPair<T, kLoads> next;
+    next.load(row, zq, u + kStripStep + lane, 32, end, step_inside<T>(row, u + kStripStep, end));
 #pragma unroll
-    for (int i = 0; i < L; ++i) {
+    for (int i = 0; i < kLoads; ++i) {
       float r[Vec<T>::N];
       now.left_over(a, f, i, r);
 #pragma unroll
       for (int j = 0; j < Vec<T>::N; j += 2) sum = add2(sum, make_f2(r[j], r[j + 1]));
     }
-    left -= kHalf;
+    left -= kStripStep;
     if (left == 0) {
       const float2 halves = split(sum);
       const float whole = warp_sum(halves.x + halves.y);
@@ -307,7 +306,7 @@ __device__ __forceinline__ void sum_left(const SampleArgs& a, const Refused& f, 
       left = a.strip_units;
       ++k;
     }
-    u += kHalf;
+    u += kStripStep;
     now = next;
   }
 }
@@ -759,13 +758,10 @@ __global__ void __launch_bounds__(kSampleWarps * 32, 3) judge_kernel(const __gri
 // The token after a sequence's taken drafts, and -1 behind it.  A refused draft's rows take a CTA or
 // cluster; the grid's last CTAs draw for the sequences whose drafts were all taken, a warp for
 // each (with a CTA for these too, the refused ones among 512 sequences of four drafts waited for
-// them: 14 us more).  Not all CTAs have much to do, so that one alone has more warps (512
-// sequences: 152 us with 12, 170 with 8, 155 with 16, 170 with 24; clusters, whose barriers wait for
-// more warps, 47 us with 8 and 53 with 12 for 37 sequences, when a call took that).
-constexpr int kFinishWarps = 12;
+// them: 14 us more).
 constexpr int kDraws = 4;  // sequences of one of the last CTAs
 template <typename T>
-__global__ void __launch_bounds__(kFinishWarps * 32, 2) finish_kernel(const __grid_constant__ SampleArgs a) {
+__global__ void __launch_bounds__(kSampleWarps * 32, 2) finish_kernel(const __grid_constant__ SampleArgs a) {
   constexpr int N = Vec<T>::N;
   extern __shared__ StripSum tables[];  // [2][strips]: of p, of the difference.  [draws][all strips]
   __shared__ double share;              // this CTA's part of the weights
@@ -954,11 +950,10 @@ int cluster_of(int64_t units, int64_t strips, int sms) {
 }
 
 // The strips of a row divided among the CTAs of a cluster, and a CTA's warps.
-int share_strips(SampleArgs& a, int64_t units, int sms, int alone) {
+int share_strips(SampleArgs& a, int64_t units, int sms) {
   a.cluster = cluster_of(units, a.all_strips, sms);
   a.strips = (a.all_strips + a.cluster - 1) / a.cluster;
-  const int most = a.cluster == 1 ? alone : kSampleWarps;
-  return a.strips < most ? a.strips : most;
+  return a.strips < kSampleWarps ? a.strips : kSampleWarps;
 }
 
 template <typename T>
@@ -969,13 +964,13 @@ cudaError_t run_verify(SampleArgs& a, int sms, cudaStream_t s) {
   // CTAs; longer sequences' CTAs take several
   const int64_t rows = a.n_drafts + a.n_seqs, most = 0x7FFFFFFF / kMaxCluster / a.n_seqs;
   int64_t positions = (rows + a.n_seqs - 1) / a.n_seqs;
-  int warps = share_strips(a, rows, sms, kSampleWarps);
+  int warps = share_strips(a, rows, sms);
   if (a.n_seqs * positions * a.cluster <= 3 * sms) positions *= 2;
   a.positions = (int32_t)(positions < most ? positions : most < 1 ? 1 : most);
   e = launch(judge_kernel<T>, (int)(a.n_seqs * a.positions * a.cluster), 32 * warps, (size_t)2 * a.strips * sizeof(StripSum), s,
              a.cluster, false, a);
   if (e != cudaSuccess) return e;
-  warps = share_strips(a, a.n_seqs, sms, kFinishWarps);
+  warps = share_strips(a, a.n_seqs, sms);
   a.draws = a.n_seqs < 4 * sms ? 1 : warps < kDraws ? warps : kDraws;
   const int64_t drawers = (a.n_seqs + a.draws - 1) / a.draws, ctas = (a.n_seqs + (drawers + a.cluster - 1) / a.cluster) * a.cluster;
   const int strips = 2 * a.strips > a.draws * a.all_strips ? 2 * a.strips : a.draws * a.all_strips;
