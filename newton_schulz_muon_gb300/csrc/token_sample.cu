@@ -807,21 +807,22 @@ __global__ void __launch_bounds__(kSampleWarps * 32, 2) finish_kernel(const __gr
     own[k] = strip0 + k < a.all_strips ? all[strip0 + k] : StripSum{-INFINITY, 0.f};
   bool fine = usable(p);
   int kind = kPlain;
-  int64_t without = -1;
+  int without = -1;
   int without_strip = -1;
   float without_sum = 0.f;
   Refused f{};
   const T* zq = nullptr;
   if (fine && a.draft == nullptr) {
-    kind = kWithout;
-    without = a.drafts[d];
-    if (without >= 0 && without < a.vocab) {
-      const int k = ((int)without + row.shift) / N / a.strip_units;
+    const int64_t x = a.drafts[d];
+    if (x >= 0 && x < a.vocab) {  // any other is no token, and all of p is left
+      kind = kWithout;
+      without = (int)x;
+      const int k = (without + row.shift) / N / a.strip_units;
       if (warp == 0 && k >= strip0 && k < strip0 + a.strips) {
         int u0, u1;
         units_of(a, row, k, u0, u1);
         without_strip = k - strip0;
-        without_sum = warp_sum(sum_without<T>(row, c, p.m, u0, u1, (int)without, lane));
+        without_sum = warp_sum(sum_without<T>(row, c, p.m, u0, u1, without, lane));
       }
     }
   } else if (fine) {
@@ -880,7 +881,7 @@ __global__ void __launch_bounds__(kSampleWarps * 32, 2) finish_kernel(const __gr
       int u0, u1;
       units_of(a, row, strip0 + strip, u0, u1);
       float rest;
-      const int found = find_element<T>(a, space[0], row, u0, u1, here - before, kind, (int)without, zq, f, p.m, &rest, lane);
+      const int found = find_element<T>(a, space[0], row, u0, u1, here - before, kind, without, zq, f, p.m, &rest, lane);
       float others = 0.f;
 #pragma unroll 4
       for (int k = lane; k < a.all_strips; k += 32)

@@ -298,6 +298,33 @@ def test_verify_drafts_out_of_range_are_refused(m, form):
         assert sampling.distance(w, float(e["su"][s]), tokens[row].item()) <= 2 * SHARE / w.sum()
 
 
+@pytest.mark.parametrize("count", [5, 700])
+@pytest.mark.parametrize("v,dtype", [(1500, "float32"), (40001, "bfloat16")])
+def test_verify_certain_drafts_past_32_bits(m, v, dtype, count):
+    """A draft outside [0, vocab) is none of the tokens, whatever its low 32 bits say: the token that
+    they name is drawn with the share that p gives it."""
+    import torch
+    rng = np.random.default_rng([v, count])
+    logits, z = _rows(rng, 2 * count, v, dtype)
+    ends = np.array([0, 2 ** 32, -2 ** 32, 2 ** 40, -2 ** 63, 3 * 2 ** 32])
+    likely = rng.integers(0, v, count)
+    first = 2 * np.arange(count)
+    logits[_dev(first), _dev(likely)] = 12.0 + float(np.log(v))
+    logits[0] = -np.inf   # one token only
+    logits[0, int(likely[0])] = 3.0
+    z = logits.double().cpu().numpy()
+    p = sampling.probabilities(z[first])
+    at = np.arange(count)
+    su = (np.cumsum(p, 1) - 0.5 * p)[at, likely].astype(np.float32)   # in the middle of the token's share
+    drafts = likely + ends[1 + at % 5]
+    assert (drafts.astype(np.int32) == likely).all() and ((drafts < 0) | (drafts >= v)).all()
+    tokens, counts, logp = m.muon_verify_drafts(logits, _dev(drafts), torch.arange(count + 1, device="cuda"),
+                                                torch.zeros(count, device="cuda"), _dev(su))
+    assert (counts == 0).all() and (tokens[1::2] == -1).all() and (logp[1::2] == 0).all()
+    assert (tokens[::2].cpu().numpy() == likely).all()
+    _check_logp(logp[::2], _logp(p, likely))
+
+
 def test_verify_rows_without_probabilities(m):
     rng = np.random.default_rng(14)
     args, e = _drafts(rng, [2, 2, 2], 700)
