@@ -608,7 +608,9 @@ muon_status muon_checkpoint_save(const void* x, int64_t x_stride, int32_t dtype,
 muon_status muon_checkpoint_load(const muon_checkpoint* checkpoint, void* x, int64_t x_stride,
                                  int32_t dtype, void* stream);
 
-/* Workspace of muon_checkpoint_weight_grad for these operands (bytes; may be 0).  Host work. */
+/* Workspace of muon_checkpoint_weight_grad for these operands (bytes; may be 0): x in bf16, a bf16
+ * copy of dy where it does not start on 16-byte boundaries, or three of an fp32 one, and partial
+ * sums of dw where the tokens are divided.  Host work. */
 muon_status muon_weight_grad_workspace_bytes(const muon_checkpoint* checkpoint, const void* dy,
                                              int64_t dy_stride, int32_t dy_dtype, int64_t outs,
                                              size_t* bytes);

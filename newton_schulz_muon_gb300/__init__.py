@@ -558,18 +558,20 @@ def _vector(t, n, dtype, what, device):
 
 
 _SPACES = threading.local()  # .held: {(device, stream): workspace}
+_MOST_HELD = 1 << 25         # bytes of one
 
 
 def _space(workspace, nbytes, device: int, handle: int):
-    """(pointer, bytes) of a call's workspace: the caller's, or one that this thread holds for
-    the stream, whose calls follow one another.  A call that is being captured, whose graph
-    may run beside them, gets one of its own from the capture's memory."""
+    """(workspace, pointer, bytes) of a call: the caller's, or one that this thread holds for the
+    stream, whose calls follow one another.  One of more than _MOST_HELD bytes is the call's
+    own: the allocator has it back, in the stream's order, when the call returns.  A call that is
+    being captured, whose graph may run beside the others, gets one from the capture's memory."""
     import torch
     if workspace is not None:
         if workspace.get_device() != device or not workspace.is_contiguous():
             raise ValueError(f"workspace: expected a contiguous tensor on cuda:{device}, got {workspace.device}")
         return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    if torch.cuda.is_current_stream_capturing():
+    if nbytes > _MOST_HELD or torch.cuda.is_current_stream_capturing():
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
         return workspace, workspace.data_ptr(), nbytes
     held = _SPACES.__dict__.setdefault("held", {})
@@ -968,7 +970,8 @@ def muon_checkpoint_weight_grad(checkpoint, dy, out=None, accumulate: bool = Fal
                                 stream=None):
     """The weight gradient dy^T x [outs, cols] of y = x W^T from the checkpoint of x [rows, cols]
     and dy [rows, outs] (bf16 or fp32), written to `out` or a new matrix of `dtype` (dy's by
-    default), or added to `out` with accumulate=True."""
+    default), or added to `out` with accumulate=True.  Its workspace (muon_weight_grad_workspace_bytes)
+    holds x in bf16 and, for fp32 dy, three bf16 copies of dy."""
     import torch
     outs, stride = _gradient_rows(checkpoint, dy)
     cols, device = checkpoint.cols, checkpoint.device

@@ -119,3 +119,18 @@ def test_weight_grad_workspace(nsm):
     v = ctypes.c_size_t()
     assert nsm.lib.muon_weight_grad_workspace_bytes(None, A, 0, 1, 64, ctypes.byref(v)) == nsm.MUON_ERR_INVALID
     assert nsm.lib.muon_weight_grad_workspace_bytes(ctypes.byref(_ck(nsm)), A, 0, 1, 64, None) == nsm.MUON_ERR_INVALID
+
+
+def test_workspaces_that_are_held(nsm, monkeypatch):
+    """A thread holds a stream's small workspaces, and gives the large ones back."""
+    torch = pytest.importorskip("torch")
+    empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *size, device=None, **kw: empty(*size, **kw))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(nsm, "_SPACES", type("S", (), {})())
+    small = nsm._space(None, 1000, 0, 7)
+    assert nsm._space(None, 2000, 0, 7)[1] == small[1] and nsm._space(None, 2000, 0, 8)[1] != small[1]
+    large, at, size = nsm._space(None, 1 << 26, 0, 7)
+    assert large.numel() == size == 1 << 26 and at == large.data_ptr()
+    assert nsm._space(None, 1000, 0, 7)[1] == small[1]
+    assert sum(w.numel() for w, _, _ in nsm._SPACES.held.values()) <= 1 << 20

@@ -411,6 +411,35 @@ def test_two_threads_on_one_stream(m):
     assert all(len(g) == 20 and torch.equal(t, want[k]) for k, g in enumerate(got) for t in g)
 
 
+def test_large_workspaces_are_not_held(m):
+    """What a call over many tokens needs beside its operands is free again after it, on every stream."""
+    import threading
+
+    import torch
+    x = torch.randn(16384, 2048, device="cuda").bfloat16()
+    dy = torch.randn(16384, 64, device="cuda").bfloat16()
+    ck, out = m.muon_checkpoint_save(x), torch.empty(2, 64, 2048, device="cuda")
+    assert m.muon_weight_grad_workspace_bytes(ck, dy) >= x.numel() * 2
+    torch.cuda.synchronize()
+    grown, side = [], torch.cuda.Stream()
+
+    def work():   # a thread has its workspaces to itself
+        for k, stream in enumerate((None, side)):
+            before = torch.cuda.memory_allocated()
+            for _ in range(3):
+                m.muon_checkpoint_weight_grad(ck, dy, out=out[k], stream=stream)
+            grown.append(torch.cuda.memory_allocated() - before)
+
+    thread = threading.Thread(target=work)
+    thread.start()
+    thread.join()
+    torch.cuda.synchronize()
+    assert len(grown) == 2 and max(grown) < x.numel() * 2
+    assert torch.equal(out[0], out[1])
+    steps = 16384 // 16
+    _check_weight(out[0], _f64(dy), _f64(m.muon_checkpoint_load(ck)), steps, 1, "float32")
+
+
 def test_refusals(m):
     import torch
     x = torch.randn(10, 70, device="cuda")
