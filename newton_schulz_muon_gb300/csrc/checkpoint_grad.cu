@@ -516,8 +516,8 @@ muon_status muon_checkpoint_weight_grad(const muon_checkpoint* checkpoint, const
     ld = p.ld;
     count = p.parts;
   }
-  if (!encode_tensor_map(&a.dy, const_cast<void*>(operand), 2, outs, rows, count, ld, 64, kTokens, true) ||
-      !encode_tensor_map(&a.x, space, 2, cols, rows, 1, p.x_ld, 64, kTokens, true))
+  if (!encode_tensor_map(&a.dy, const_cast<void*>(operand), outs, rows, count, ld, 64, kTokens) ||
+      !encode_tensor_map(&a.x, space, cols, rows, 1, p.x_ld, 64, kTokens))
     return set_error(MUON_ERR_CUDA, "cuTensorMapEncodeTiled rejected a tensor map");
   a.cols = (int32_t)cols;
   a.outs = (int32_t)outs;

@@ -217,9 +217,7 @@ bool encode_map(CUtensorMap* map, void* base, size_t esize, int64_t cols, int64_
   const cuuint64_t strides[2] = {(cuuint64_t)(ld * esize), (cuuint64_t)(ld * rows * esize)};
   const cuuint32_t box[3] = {box_x, box_y, 1};
   const cuuint32_t estr[3] = {1, 1, 1};
-  const CUtensorMapDataType dt = esize == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                 : esize == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                              : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+  const CUtensorMapDataType dt = esize == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
   CUresult r = fn(map, dt, 3, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -812,10 +810,9 @@ float elapsed(cudaEvent_t a, cudaEvent_t b) {
 
 int32_t muon::set_error(int32_t s, const char* msg) { return fail(s, "%s", msg); }
 
-bool muon::encode_tensor_map(CUtensorMap* map, void* base, size_t esize, int64_t cols, int64_t rows, int64_t count,
-                             int64_t ld, uint32_t box_x, uint32_t box_y, bool swizzle) {
-  return encode_map(map, base, esize, cols, rows, count, ld, box_x, box_y,
-                    swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE);
+bool muon::encode_tensor_map(CUtensorMap* map, void* base, int64_t cols, int64_t rows, int64_t count, int64_t ld,
+                             uint32_t box_x, uint32_t box_y) {
+  return encode_map(map, base, 2, cols, rows, count, ld, box_x, box_y);
 }
 
 // ===========================================================================

@@ -2,14 +2,13 @@
 #pragma once
 
 #include <cuda.h>
-#include <stddef.h>
 #include <stdint.h>
 
 namespace muon {
 
-// Map of a [count][rows][ld] array of `esize`-byte elements (1: bytes, 2: bf16, 4: fp32),
-// logical (cols, rows, count), box box_x x box_y x 1, with the 128-byte swizzle or none.
-bool encode_tensor_map(CUtensorMap* map, void* base, size_t esize, int64_t cols, int64_t rows, int64_t count, int64_t ld,
-                       uint32_t box_x, uint32_t box_y, bool swizzle);
+// Map of a [count][rows][ld] array of bf16, logical (cols, rows, count), box box_x x box_y x 1
+// with the 128-byte swizzle.
+bool encode_tensor_map(CUtensorMap* map, void* base, int64_t cols, int64_t rows, int64_t count, int64_t ld, uint32_t box_x,
+                       uint32_t box_y);
 
 }  // namespace muon
