@@ -282,6 +282,12 @@ int32_t check_matrix(const void* p, int64_t stride, int64_t cols, int32_t dtype,
   return MUON_OK;
 }
 
+// An output in the place of an input: each element is read and written by one thread only where both
+// have one row stride.
+bool displaced(const Matrix& out, const Matrix& in, int64_t rows) {
+  return rows > 1 && out.p == in.p && out.stride != in.stride;
+}
+
 CheckpointView view_of(const muon_checkpoint* c) {
   CheckpointView v;
   v.rows = c->rows;
@@ -393,6 +399,8 @@ muon_status muon_swiglu_forward(const void* gate, int64_t gate_stride, const voi
   if ((st = check_matrix(gate, gate_stride, cols, dtype, &a.x)) != MUON_OK) return st;
   if ((st = check_matrix(up, up_stride, cols, dtype, &a.y)) != MUON_OK) return st;
   if ((st = check_matrix(h, h_stride, cols, dtype, &a.u)) != MUON_OK) return st;
+  if (displaced(a.u, a.x, rows) || displaced(a.u, a.y, rows))
+    return invalid("h in place of gate or up must have its row stride");
   a.a = view_of(gate_checkpoint);
   a.b = view_of(up_checkpoint);
   return run_checkpoint<kGatedForward>(a, dtype, stream);
@@ -414,6 +422,8 @@ muon_status muon_swiglu_backward(const void* dh, int64_t dh_stride, int32_t dtyp
   if ((st = check_matrix(dup, dup_stride, cols, dtype, &a.v)) != MUON_OK) return st;
   if (h && (st = check_matrix(h, h_stride, cols, dtype, &a.w)) != MUON_OK) return st;
   if (dgate == dup || dgate == h || dup == h) return invalid("two outputs are one");
+  if (displaced(a.u, a.z, rows) || displaced(a.v, a.z, rows) || displaced(a.w, a.z, rows))
+    return invalid("an output in place of dh must have its row stride");
   a.a = view_of(gate_checkpoint);
   a.b = view_of(up_checkpoint);
   return run_checkpoint<kGatedBackward>(a, dtype, stream);

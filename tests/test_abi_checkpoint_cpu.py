@@ -134,3 +134,17 @@ def test_workspaces_that_are_held(nsm, monkeypatch):
     assert large.numel() == size == 1 << 26 and at == large.data_ptr()
     assert nsm._space(None, 1000, 0, 7)[1] == small[1]
     assert sum(w.numel() for w, _, _ in nsm._SPACES.held.values()) <= 1 << 20
+
+
+def test_gated_outputs_in_place_of_an_input_have_its_stride(nsm):
+    """Rows of an output that lie elsewhere than the input's would be written over before they are read."""
+    lib, ck, other = nsm.lib, ctypes.byref(_ck(nsm)), ctypes.byref(_ck(nsm, 2 * A))
+    bad = nsm.MUON_ERR_INVALID
+    assert lib.muon_swiglu_forward(A, 200, 3 * A, 0, 0, A, 0, ck, other, None) == bad
+    assert lib.muon_swiglu_forward(A, 0, 3 * A, 200, 0, 3 * A, 100, ck, other, None) == bad
+    assert lib.muon_swiglu_forward(A, 0, 3 * A, 0, 0, A, 101, ck, other, None) == bad
+    for k in range(3):
+        outs = [4 * A, 0, 5 * A, 0, 6 * A, 0]
+        outs[2 * k:2 * k + 2] = A, 300
+        assert lib.muon_swiglu_backward(A, 0, 0, ck, other, *outs, None) == bad
+        assert b"stride" in lib.muon_last_error()
