@@ -291,6 +291,39 @@ def test_weight_grad_fp32_keeps_all_bits(m):
     assert (np.abs(got - want)[fits] <= 3 * 2.0 ** -24 * np.abs(want)[fits]).all()
 
 
+def test_weight_grad_sums_do_not_drift(m):
+    """The tensor cores cut off what a sum cannot hold, less than a unit, 2^-23 of the sum so far, for each
+    accumulation of 16 tokens.  An accumulator takes 64 of them, so that terms of one sign lose less
+    than sum_{k <= 64} k / 64 2^-23 = 3.9e-6 of the whole, and what adds the accumulators up rounds to
+    nearest; one accumulator over all 512 could lose eight times as much.  (80 tiles: the tokens of
+    none of them are divided.)"""
+    import torch
+    gen = torch.Generator("cuda").manual_seed(10)
+    x = torch.rand(8192, 2048, generator=gen, device="cuda") + 0.5
+    x *= (0.5 * torch.randn(8192, 1, generator=gen, device="cuda")).exp()
+    dy = torch.randn(8192, 2560, generator=gen, device="cuda").exp().bfloat16()
+    ck = m.muon_checkpoint_save(x)
+    got = m.muon_checkpoint_weight_grad(ck, dy, dtype=torch.float32).double()
+    want = dy.double().t() @ m.muon_checkpoint_load(ck).double()
+    assert ((got - want) / want).mean().abs() <= 3.9e-6
+
+
+def test_weight_grad_small_fp32_gradients(m):
+    """Below 2^-110 an fp32 number has bits under 2^-133, the smallest bf16 number: the third part is cut there."""
+    import torch
+    rng = np.random.default_rng(11)
+    x, v = _matrix(rng, 300, 64)
+    x.mul_(2.0 ** 60)
+    dy, vd = _matrix(rng, 300, 50)
+    dy.mul_(2.0 ** -112)
+    dy[:, 25:] *= 2.0 ** -12
+    vd, v = _f64(dy), checkpoint.values(_f64(x))
+    got = _f64(m.muon_checkpoint_weight_grad(m.muon_checkpoint_save(x), dy))
+    terms = np.abs(vd).T @ np.abs(v)
+    tol = (3 * -(-300 // 16) + 4) * 2.0 ** -23 * terms + 2.0 ** -133 * np.abs(v).sum(0)
+    assert (np.abs(got - vd.T @ v) <= tol).all()
+
+
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
 def test_weight_grad_not_finite(m, dtype):
     import torch
