@@ -1,5 +1,7 @@
 """The sampling and checkpoint calls on tensors of another device than the current one, and on
 streams, with fake devices (no kernel runs)."""
+import gc
+
 import pytest
 
 from test_abi_losses_cpu import _TwoDevices
@@ -15,6 +17,7 @@ def nsm():
 
 @pytest.fixture
 def fake(nsm, monkeypatch):
+    gc.collect()   # other tests' plans go through the library that they were made by
     two = _TwoDevices(nsm, pytest.importorskip("torch"), monkeypatch)
     monkeypatch.setattr(nsm, "muon_checkpoint_bytes", lambda rows, cols: 64)
     monkeypatch.setattr(nsm, "muon_sample_workspace_bytes", lambda *a: 512)
