@@ -8,7 +8,9 @@
 // x is first loaded into the workspace in bf16, where L2 mostly keeps it.  (Converting it in the
 // product's own pipeline reads fewer bytes, but every 256 columns of dy convert all of x
 // again: 8192 x 9728 x 2560 took 327 us so, of which 300 us remained without any MMA; it takes
-// 237 us as it is, 1.72 PFLOP/s, of which the load is 13 us.)
+// 236 us as it is, 1.73 PFLOP/s, of which the load is 11 us.  Called without a pause it meets the
+// power limit: 264 us at 1770 MHz instead of 2070, and a library's bf16 product 239 instead of 203.  For 2560
+// columns of dy and 9728 of x, whose 159 MB L2 does not hold, it takes 275 us, of which the load is 39.)
 //
 // Bound by the tensor cores and what feeds them: with static operands, no waits and no stores
 // the same MMAs take 171 us, the loads without MMAs 214 us (15 TB/s from L2), and both 225 us.
@@ -21,16 +23,18 @@
 //   1      tcgen05.mma issuer (the leader's)
 //   4-11   sums: TMEM to fp32 registers and, after a tile's last stage, to dW
 // The tensor cores cut off what an accumulation cannot hold, always towards zero: 512 of them
-// (8192 tokens) leave dW 5e-6 off in the mean.  So an accumulator takes kChunkSteps stages only
-// (64 accumulations), and is then added to registers, rounding to nearest, while the next
-// stages are summed into the other accumulator: 5.5e-7.
+// (8192 tokens) leave terms of one sign 2.1e-5 of their sum low in the mean, and terms of both
+// signs 4.3e-6 of the mean |dW| off.  So an accumulator takes kChunkSteps stages only (64
+// accumulations), and is then added to registers, rounding to nearest, while the next stages
+// are summed into the other accumulator: 1.06e-6 and 2.5e-7.
 //
-// fp32 gradients are split into three bf16 parts that add up to them exactly (8 bits of the
-// significand each) by a pass of its own, and the sum runs over the parts, the smallest first.
+// fp32 gradients are split into three bf16 parts (8 bits of the significand each) by a pass of
+// its own, and the sum runs over the parts, the smallest first.  The parts add up to the value,
+// but for what lies under bf16's smallest number, 2^-133: below 2^-110 the third part is cut there.
 // The same pass copies bf16 gradients whose rows a TMA cannot read (16-byte boundaries).
 //
-// Where a matrix has too few tiles for the SMs, the tokens are divided among several pairs,
-// whose fp32 sums are added in a fixed order by a last pass.
+// Where a matrix has at most half as many tiles as there are pairs, the tokens are divided among
+// several pairs, whose fp32 sums are added in a fixed order by a last pass (plan_of).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -254,7 +258,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) weight_grad_kernel(const __gr
             if (++stage == kGradStages) { stage = 0; phase ^= 1u; }
             // whether the next stage has landed is asked before this one's MMAs are issued: the
             // tensor core's queue is too short to cover the answer's latency (8192 x 9728 x 2560:
-            // 253 us without, 245 us with it)
+            // 245 us without, 237 us with it)
             ready = __all_sync(0xffffffffu, mbar_test_wait(&full_bar[stage], phase));
             if (lane == 0) {
 #pragma unroll
@@ -322,7 +326,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) weight_grad_kernel(const __gr
 }
 
 // dy as `parts` bf16 matrices [parts][tokens][ld]: a copy, or the three parts of fp32 values,
-// each cut off at 8 bits of what the ones before it leave (cutting cannot overflow).  It runs
+// each cut off at 8 bits of what the ones before it leave (cutting cannot overflow), and at
+// 2^-133.  It runs
 // beside the load of x before it, and ends after it, so that the product waits for both.
 constexpr int kPartThreads = 256;
 template <typename T>
@@ -407,6 +412,13 @@ struct GradPlan {
   size_t x_bytes, parts_bytes, bytes;
 };
 
+// The tokens are divided by as many pairs as a tile can have.  8192 tokens, bf16 to fp32, us on the
+// device with (1, 2, 4) parts: 8 tiles 54, 35, 27 (23 with the 9 that they get), 16 tiles 54, 37, 29,
+// 38 tiles 56, 42, 46.  Above half the pairs more units than pairs would start a second round: 40 tiles
+// 56, 62, 56, 48 tiles 56, 64, 58, 160 tiles 146, 149, 162; these stay whole, and 36 pairs idle
+// beside 40 tiles, 68 in the last of three rounds of 160.
+// A part is four steps at least: 1024 tokens of 2 tiles 12.9 us with one, two or four, 14.8 with
+// eight; 512 tokens of 16 tiles 16.9, 16.9, 15.6, 15.0.
 GradPlan plan_of(int64_t tokens, int64_t cols, int64_t outs, const void* dy, int64_t dy_stride, int32_t dtype) {
   GradPlan p = {};
   p.tiles_m = (outs + kTile - 1) / kTile;
@@ -421,7 +433,7 @@ GradPlan plan_of(int64_t tokens, int64_t cols, int64_t outs, const void* dy, int
   if (p.parts) p.parts_bytes = ((size_t)p.parts * tokens * p.ld * 2 + 255) / 256 * 256;
   const int64_t all = passes * p.steps, tiles = p.tiles_m * p.tiles_n;
   int64_t splits = tiles < kPairs ? kPairs / tiles : 1;
-  if (splits > all / 4) splits = all / 4;  // four steps a split at least
+  if (splits > all / 4) splits = all / 4;
   if (splits < 1) splits = 1;
   p.split_steps = (all + splits - 1) / splits;
   p.splits = all ? (all + p.split_steps - 1) / p.split_steps : 1;
