@@ -156,7 +156,7 @@ __device__ __forceinline__ void values_of(const SavedUnit<N>& s, float (&v)[N]) 
 }
 
 // 1 / (1 + e^-g) and 1 minus that, which is e^-g / (1 + e^-g).  For bf16, whose results keep 8
-// bits, the approximate exponential and reciprocal, 2^-22 each and |g| 2^-23 for the exponent's
+// bits, the approximate exponential and reciprocal, 2^-22 each and |g| 7.3e-8 for the exponent's
 // rounding (6e-6 at the largest |g| that leaves a sigmoid, 88), and the difference.
 template <typename T>
 __device__ __forceinline__ float2 sigmoid(float g) {
